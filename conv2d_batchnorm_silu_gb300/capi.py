@@ -9,6 +9,7 @@ fallback: if the library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -95,6 +96,17 @@ _plan = _declare("conv_bn_silu_plan", [_i] * 13 + [ctypes.POINTER(PlanInfo)])
 _plan_request = _declare("conv_bn_silu_plan_request", [_i] * 11 + [ctypes.POINTER(PlanRequest), _i,
                                                                      ctypes.POINTER(PlanInfo)])
 _forward_request = _declare("conv_bn_silu_forward_request", [_p] * 5 + [_i] * 11 + [ctypes.POINTER(PlanRequest), _p])
+_ll = ctypes.c_longlong
+_layer_norm = _declare("conv_bn_silu_layer_norm", [_p, _ll, _p, _p, _f, _p, _ll, _p, _ll, _i, _i, _p])
+_layer_norm_backward = _declare("conv_bn_silu_layer_norm_backward", [_p, _ll, _p, _ll, _p, _p, _p, _ll, _p, _p,
+                                                                       _ll, _i, _i, _p, _ll, _p])
+_layer_norm_backward_workspace = _declare("conv_bn_silu_layer_norm_backward_workspace", [_ll, _i], _ll)
+_quantize_rows = _declare("conv_bn_silu_quantize_rows", [_p, _ll, _p, _ll, _p, _ll, _i, _i, _p])
+_layer_norm_quantize = _declare("conv_bn_silu_layer_norm_quantize", [_p, _ll, _p, _p, _f, _p, _ll, _p, _ll, _i, _i,
+                                                                       _p])
+_linear_int8 = _declare("conv_bn_silu_linear_int8", [_p, _ll, _p, _ll, _p, _p, _p, _p, _ll, _p, _ll, _ll, _i, _i,
+                                                       _i, _i, _p, _ll, _p])
+_linear_int8_workspace = _declare("conv_bn_silu_linear_int8_workspace", [_ll, _i, _i], _ll)
 _check = _declare("conv_bn_silu_check", [_p])
 _status_string = _declare("conv_bn_silu_status_string", [_i], ctypes.c_char_p)
 _last_cuda_error = _declare("conv_bn_silu_last_cuda_error", [])
@@ -443,6 +455,217 @@ def silu_apply(t2: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> 
     st = _silu_apply(_dev_tensor(t2, torch.bfloat16, "t2"), _dev_tensor(y, torch.bfloat16, "y"),
                      t2.numel(), _stream_handle(stream))
     _raise_if(st, "conv_bn_silu_silu_apply")
+    return y
+
+
+# ---------------------------------------------------------------- token-wise operators
+# Activations are tensors [..., c] whose last dimension is dense and whose leading dimensions
+# are rows at one distance (a contiguous tensor, or a column slice of a matrix); parameters,
+# statistics and scales are dense float32.
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _rows(t: torch.Tensor, name: str, device: int) -> tuple[int, int, int, int]:
+    """(pointer, rows, columns, distance of rows in elements) of an activation tensor."""
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on the CUDA device of the call's first tensor")
+    if t.dim() != 2:
+        if t.dim() == 0:
+            raise ValueError(f"{name} must have at least one dimension")
+        c = t.shape[-1]
+        try:
+            t = t.view(t.numel() // c if c else 0, c)
+        except RuntimeError:
+            raise ValueError(f"{name}'s leading dimensions must be rows at one distance") from None
+    rows, c = t.shape
+    distance, step = t.stride()
+    if step != 1 and c > 1:
+        raise ValueError(f"{name}'s last dimension must be dense")
+    return t.data_ptr(), rows, c, distance if rows > 1 else c
+
+
+def _vector(t: torch.Tensor | None, n: int, name: str, device: int) -> int | None:
+    if t is None:
+        return None
+    if t.dtype is not torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    if t.get_device() != device or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} dense elements on the CUDA device of the call's first tensor")
+    return t.data_ptr()
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    device = t.get_device()
+    if device < 0 or device != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    return device
+
+
+def _dtype_of(t: torch.Tensor, name: str) -> int:
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be torch.float32, torch.bfloat16 or torch.float16, got {t.dtype}")
+    return code
+
+
+def _run_stream(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream_handle(stream)
+
+
+def _empty(shape, dtype: torch.dtype, device: int, stream) -> torch.Tensor:
+    """An output or workspace; on another stream than the current one, from that stream's memory."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(stream), device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _output(t: torch.Tensor | None, shape, dtype: torch.dtype, name: str, device: int, stream) -> torch.Tensor:
+    if t is None:
+        return _empty(shape, dtype, device, stream)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+               eps: float = 1e-5, return_stats: bool = False, y: torch.Tensor | None = None, stream=None):
+    """conv_bn_silu_layer_norm: y = (x - mean) * rstd * gamma + beta over the last dimension.
+
+    x: float32, bf16 or f16 [..., c]; gamma, beta: fp32 [c] or None; y like x.  With return_stats
+    also the fp32 statistics [2, rows] (mean, then 1/sqrt(var + eps)) for layer_norm_backward.
+    """
+    device = _device_of(x, "x")
+    dtype = _dtype_of(x, "x")
+    px, rows, c, sx = _rows(x, "x", device)
+    y = _output(y, x.shape, x.dtype, "y", device, stream)
+    stats = _empty((2, rows), torch.float32, device, stream) if return_stats else None
+    if rows:
+        py, _, _, sy = _rows(y, "y", device)
+        st = _layer_norm(px, sx, _vector(gamma, c, "gamma", device), _vector(beta, c, "beta", device), eps, py, sy,
+                         stats.data_ptr() if return_stats else None, rows, c, dtype, _run_stream(stream, device))
+        if st:
+            _raise_if(st, "conv_bn_silu_layer_norm")
+    return (y, stats) if return_stats else y
+
+
+def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None, stats: torch.Tensor,
+                        dx: torch.Tensor | None = None, stream=None):
+    """conv_bn_silu_layer_norm_backward: (dx, dgamma, dbeta) from dy, the forward call's x and gamma
+    (None: ones) and the statistics it returned.  dx is like x; dgamma and dbeta are fp32 [c]."""
+    device = _device_of(x, "x")
+    dtype = _dtype_of(x, "x")
+    if dy.dtype is not x.dtype:
+        raise TypeError(f"dy must be {x.dtype}, got {dy.dtype}")
+    if dy.shape != x.shape:
+        raise ValueError(f"dy has shape {tuple(dy.shape)}, expected {tuple(x.shape)}")
+    px, rows, c, sx = _rows(x, "x", device)
+    pdy, _, _, sdy = _rows(dy, "dy", device)
+    dx = _output(dx, x.shape, x.dtype, "dx", device, stream)
+    pdx, _, _, sdx = _rows(dx, "dx", device)
+    pstats = _vector(stats, 2 * rows, "stats", device)
+    need = _layer_norm_backward_workspace(rows, c)
+    if need < 0:
+        _raise_if(CBS_ERR_INVALID_ARG, "conv_bn_silu_layer_norm_backward_workspace")
+    dgamma, dbeta = _empty((c,), torch.float32, device, stream), _empty((c,), torch.float32, device, stream)
+    work = _empty((need,), torch.uint8, device, stream)
+    st = _layer_norm_backward(pdy, sdy, px, sx, _vector(gamma, c, "gamma", device), pstats, pdx, sdx,
+                              dgamma.data_ptr(), dbeta.data_ptr(), rows, c, dtype, work.data_ptr(), need,
+                              _run_stream(stream, device))
+    if st:
+        _raise_if(st, "conv_bn_silu_layer_norm_backward")
+    return dx, dgamma, dbeta
+
+
+def quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """conv_bn_silu_quantize_rows: (q, scale), q int8 like x, scale fp32 [...] with x close to q * scale."""
+    device = _device_of(x, "x")
+    dtype = _dtype_of(x, "x")
+    px, rows, c, sx = _rows(x, "x", device)
+    q = _output(q, x.shape, torch.int8, "q", device, stream)
+    scale = _empty(x.shape[:-1], torch.float32, device, stream)
+    if rows:
+        pq, _, _, sq = _rows(q, "q", device)
+        st = _quantize_rows(px, sx, pq, sq, scale.data_ptr(), rows, c, dtype, _run_stream(stream, device))
+        if st:
+            _raise_if(st, "conv_bn_silu_quantize_rows")
+    return q, scale
+
+
+def layer_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+                        eps: float = 1e-5, q: torch.Tensor | None = None,
+                        stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """conv_bn_silu_layer_norm_quantize: layer_norm, its rows quantised in the same pass; (q, scale) as
+    quantize_rows gives them."""
+    device = _device_of(x, "x")
+    dtype = _dtype_of(x, "x")
+    px, rows, c, sx = _rows(x, "x", device)
+    q = _output(q, x.shape, torch.int8, "q", device, stream)
+    scale = _empty(x.shape[:-1], torch.float32, device, stream)
+    if rows:
+        pq, _, _, sq = _rows(q, "q", device)
+        st = _layer_norm_quantize(px, sx, _vector(gamma, c, "gamma", device), _vector(beta, c, "beta", device), eps,
+                                  pq, sq, scale.data_ptr(), rows, c, dtype, _run_stream(stream, device))
+        if st:
+            _raise_if(st, "conv_bn_silu_layer_norm_quantize")
+    return q, scale
+
+
+def linear_int8(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale: torch.Tensor,
+                bias: torch.Tensor | None = None, activation: str = "identity",
+                residual: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """conv_bn_silu_linear_int8: y = act((a @ w.T) * (a_scale[:, None] * w_scale) + bias) [+ residual].
+
+    a: int8 [..., k]; w: int8 [n, k]; a_scale: fp32, one for each row of a; w_scale, bias: fp32 [n];
+    residual and y: out_dtype [..., n] (residual may be y).  activation: "silu", "identity" or "relu".
+    """
+    device = _device_of(a, "a")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    out = DTYPES.get(out_dtype)
+    if out is None:
+        raise TypeError(f"out_dtype must be torch.float32, torch.bfloat16 or torch.float16, got {out_dtype}")
+    if a.dtype is not torch.int8 or w.dtype is not torch.int8:
+        raise TypeError("a and w must be torch.int8")
+    if w.dim() != 2:
+        raise ValueError("w must be [n, k]")
+    k = a.shape[-1]
+    n = w.shape[0]
+    if w.shape[1] != k:
+        raise ValueError(f"channel mismatch: a has {k}, w has {w.shape[1]}")
+    pw, _, _, sw = _rows(w, "w", device)
+    shape = a.shape[:-1] + (n,)
+    y = _output(y, shape, out_dtype, "y", device, stream)
+    if k:
+        pa, m, _, sa = _rows(a, "a", device)
+    else:
+        pa, m, sa = a.data_ptr(), math.prod(a.shape[:-1]), 0
+    pas, pws, pb = (_vector(a_scale, m, "a_scale", device), _vector(w_scale, n, "w_scale", device),
+                    _vector(bias, n, "bias", device))
+    pr, sr = None, 0
+    if residual is not None:
+        if residual.dtype is not out_dtype:
+            raise TypeError(f"residual must be {out_dtype}, got {residual.dtype}")
+        if residual.shape != shape:
+            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(shape)}")
+        pr, _, _, sr = _rows(residual, "residual", device)
+    if m == 0 or n == 0:
+        return y
+    py, _, _, sy = _rows(y, "y", device)
+    need = _linear_int8_workspace(m, n, k)
+    if need < 0:
+        _raise_if(CBS_ERR_INVALID_ARG, "conv_bn_silu_linear_int8_workspace")
+    work = _empty((need,), torch.uint8, device, stream) if need else None
+    st = _linear_int8(pa, sa, pw, sw, pas, pws, pb, pr, sr, py, sy, m, n, k, act, out,
+                      work.data_ptr() if need else None, need, _run_stream(stream, device))
+    if st:
+        _raise_if(st, "conv_bn_silu_linear_int8")
     return y
 
 

@@ -8,6 +8,7 @@
 
 #include "conv_bn_silu.h"
 #include "cbs_internal.h"
+#include "token_ops.h"
 
 namespace {
 
@@ -172,6 +173,64 @@ int noalloc_scratch_address(void **out)
     }
     *out = addr[dev];
     return CBS_OK;
+}
+
+
+// ------------------------------------------------------------------ token-wise operators
+bool aligned_to(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; }
+
+// Keeps every byte offset of a matrix within 2^62.
+bool rows_in_range(long long rows, long long stride) { return stride <= (1LL << 40) && (rows == 0 || stride <= (1LL << 60) / rows); }
+
+// A matrix argument: pointer, alignment to the element, and a row distance an input may have
+// (any from 0) or an output (its width at least; a single row has no distance).
+int check_rows(const void *p, long long rows, long long c, long long stride, int element, bool output)
+{
+    if (stride < 0 || !rows_in_range(rows, stride)) return CBS_ERR_INVALID_ARG;
+    if (output && rows > 1 && stride < c) return CBS_ERR_INVALID_ARG;
+    if (!p) return CBS_ERR_INVALID_ARG;
+    return aligned_to(p, element) ? CBS_OK : CBS_ERR_MISALIGNED;
+}
+
+bool norm_sizes_ok(long long rows, int c, int dtype)
+{
+    return rows >= 0 && rows <= (1LL << 40) && c >= 1 && dtype >= CBS_DTYPE_F32 && dtype <= CBS_DTYPE_F16;
+}
+
+int norm_call(const void *x, long long x_stride, const float *gamma, const float *beta, float eps, void *y,
+              long long y_stride, void *q, long long q_stride, float *row_scale, float *stats, int normalise,
+              long long rows, int c, int dtype, void *stream)
+{
+    if (!norm_sizes_ok(rows, c, dtype) || !(eps >= 0.0f) || eps > 3.0e38f) return CBS_ERR_INVALID_ARG;
+    if (rows == 0) return CBS_OK;
+    const int size = cbs::dtype_size(dtype);
+    int st = check_rows(x, rows, c, x_stride, size, false);
+    if (st != CBS_OK) return st;
+    st = q ? check_rows(q, rows, c, q_stride, 1, true) : check_rows(y, rows, c, y_stride, size, true);
+    if (st != CBS_OK) return st;
+    if (q && !row_scale) return CBS_ERR_INVALID_ARG;
+    if (!aligned_to(gamma, 4) || !aligned_to(beta, 4) || !aligned_to(stats, 4) || !aligned_to(row_scale, 4))
+        return CBS_ERR_MISALIGNED;
+    cbs::NormProblem p{};
+    p.x = cbs::Rows{const_cast<void *>(x), x_stride};
+    p.y = cbs::Rows{y, y_stride};
+    p.q = cbs::Rows{q, q_stride};
+    p.row_scale = row_scale;
+    p.stats = stats;
+    p.gamma = gamma;
+    p.beta = beta;
+    p.eps = eps;
+    p.normalise = normalise;
+    p.rows = rows;
+    p.c = c;
+    p.dtype = dtype;
+    cudaError_t e = cbs::norm_launch(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+}
+
+bool linear_sizes_ok(long long m, int n, int k)
+{
+    return m >= 0 && m <= (1LL << 36) && n >= 0 && n <= (1 << 22) && k >= 0 && k <= 131071;
 }
 
 }  // namespace
@@ -518,6 +577,131 @@ int conv_bn_silu_forward_request(const void *x, const void *w, const float *scal
     p.y = y;
     p.wait_timeout_ns = req->wait_timeout_ns;
     return launch_forward(p, algo, static_cast<cudaStream_t>(stream), &rq);
+}
+
+int conv_bn_silu_layer_norm(const void *x, long long x_stride, const float *gamma, const float *beta, float eps,
+                            void *y, long long y_stride, float *stats, long long rows, int c, int dtype,
+                            void *stream)
+{
+    return norm_call(x, x_stride, gamma, beta, eps, y, y_stride, nullptr, 0, nullptr, stats, 1, rows, c, dtype, stream);
+}
+
+int conv_bn_silu_quantize_rows(const void *x, long long x_stride, void *q, long long q_stride, float *row_scale,
+                               long long rows, int c, int dtype, void *stream)
+{
+    if (!q && rows != 0) return CBS_ERR_INVALID_ARG;
+    return norm_call(x, x_stride, nullptr, nullptr, 0.0f, nullptr, 0, q, q_stride, row_scale, nullptr, 0, rows, c,
+                     dtype, stream);
+}
+
+int conv_bn_silu_layer_norm_quantize(const void *x, long long x_stride, const float *gamma, const float *beta,
+                                     float eps, void *q, long long q_stride, float *row_scale, long long rows,
+                                     int c, int dtype, void *stream)
+{
+    if (!q && rows != 0) return CBS_ERR_INVALID_ARG;
+    return norm_call(x, x_stride, gamma, beta, eps, nullptr, 0, q, q_stride, row_scale, nullptr, 1, rows, c, dtype,
+                     stream);
+}
+
+long long conv_bn_silu_layer_norm_backward_workspace(long long rows, int c)
+{
+    if (!norm_sizes_ok(rows, c, CBS_DTYPE_F32)) return -1;
+    int sms = 0;
+    if (sm_count_current_device(&sms) != CBS_OK) return -1;
+    return 8LL * c * cbs::norm_grad_partial_rows(rows, c, sms);
+}
+
+int conv_bn_silu_layer_norm_backward(const void *dy, long long dy_stride, const void *x, long long x_stride,
+                                     const float *gamma, const float *stats, void *dx, long long dx_stride,
+                                     float *dgamma, float *dbeta, long long rows, int c, int dtype,
+                                     void *workspace, long long workspace_bytes, void *stream)
+{
+    if (!norm_sizes_ok(rows, c, dtype)) return CBS_ERR_INVALID_ARG;
+    if (!dgamma || !dbeta) return CBS_ERR_INVALID_ARG;
+    if (!aligned_to(gamma, 4) || !aligned_to(stats, 4) || !aligned_to(dgamma, 4) || !aligned_to(dbeta, 4))
+        return CBS_ERR_MISALIGNED;
+    cudaStream_t strm = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        cudaError_t e = cudaMemsetAsync(dgamma, 0, 4 * (size_t)c, strm);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dbeta, 0, 4 * (size_t)c, strm);
+        return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+    }
+    const int size = cbs::dtype_size(dtype);
+    int st = check_rows(dy, rows, c, dy_stride, size, false);
+    if (st == CBS_OK) st = check_rows(x, rows, c, x_stride, size, false);
+    if (st == CBS_OK) st = check_rows(dx, rows, c, dx_stride, size, true);
+    if (st != CBS_OK) return st;
+    if (!stats || !workspace) return CBS_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return CBS_ERR_MISALIGNED;
+    int sms = 0;
+    st = sm_count_current_device(&sms);
+    if (st != CBS_OK) return st;
+    cbs::NormGradProblem p{};
+    p.partial_rows = cbs::norm_grad_partial_rows(rows, c, sms);
+    if (workspace_bytes < 8LL * c * p.partial_rows) return CBS_ERR_INVALID_ARG;
+    p.dy = cbs::Rows{const_cast<void *>(dy), dy_stride};
+    p.x = cbs::Rows{const_cast<void *>(x), x_stride};
+    p.dx = cbs::Rows{dx, dx_stride};
+    p.gamma = gamma;
+    p.stats = stats;
+    p.dgamma = dgamma;
+    p.dbeta = dbeta;
+    p.partial = static_cast<float *>(workspace);
+    p.rows = rows;
+    p.c = c;
+    p.dtype = dtype;
+    cudaError_t e = cbs::norm_grad_launch(p, sms, strm);
+    return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+}
+
+long long conv_bn_silu_linear_int8_workspace(long long m, int n, int k)
+{
+    if (!linear_sizes_ok(m, n, k)) return -1;
+    int sms = 0;
+    if (sm_count_current_device(&sms) != CBS_OK) return -1;
+    return cbs::linear_workspace_bytes(m, n, k, sms);
+}
+
+int conv_bn_silu_linear_int8(const void *a, long long a_stride, const void *w, long long w_stride,
+                             const float *a_scale, const float *w_scale, const float *bias, const void *residual,
+                             long long residual_stride, void *y, long long y_stride, long long m, int n, int k,
+                             int activation, int out_dtype, void *workspace, long long workspace_bytes,
+                             void *stream)
+{
+    if (!linear_sizes_ok(m, n, k)) return CBS_ERR_INVALID_ARG;
+    if (activation < CBS_ACT_SILU || activation > CBS_ACT_RELU) return CBS_ERR_INVALID_ARG;
+    if (out_dtype < CBS_DTYPE_F32 || out_dtype > CBS_DTYPE_F16) return CBS_ERR_INVALID_ARG;
+    if (m == 0 || n == 0) return CBS_OK;
+    const int size = cbs::dtype_size(out_dtype);
+    int st = check_rows(y, m, n, y_stride, size, true);
+    if (st == CBS_OK && k > 0) st = check_rows(a, m, k, a_stride, 1, false);
+    if (st == CBS_OK && k > 0) st = check_rows(w, n, k, w_stride, 1, false);
+    if (st == CBS_OK && residual) st = check_rows(residual, m, n, residual_stride, size, false);
+    if (st != CBS_OK) return st;
+    if (!a_scale || !w_scale) return CBS_ERR_INVALID_ARG;
+    if (!aligned_to(a_scale, 4) || !aligned_to(w_scale, 4) || !aligned_to(bias, 4) || !aligned16(workspace))
+        return CBS_ERR_MISALIGNED;
+    int sms = 0;
+    st = sm_count_current_device(&sms);
+    if (st != CBS_OK) return st;
+    if (workspace_bytes < cbs::linear_workspace_bytes(m, n, k, sms)) return CBS_ERR_INVALID_ARG;
+    if (!workspace && workspace_bytes > 0) return CBS_ERR_INVALID_ARG;
+    cbs::LinearProblem p{};
+    p.a = cbs::Rows{const_cast<void *>(a), a_stride};
+    p.w = cbs::Rows{const_cast<void *>(w), w_stride};
+    p.residual = cbs::Rows{const_cast<void *>(residual), residual_stride};
+    p.y = cbs::Rows{y, y_stride};
+    p.a_scale = a_scale;
+    p.w_scale = w_scale;
+    p.bias = bias;
+    p.m = m;
+    p.n = n;
+    p.k = k;
+    p.out_dtype = out_dtype;
+    p.activation = activation;
+    p.workspace = workspace;
+    cudaError_t e = cbs::linear_launch(p, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CBS_OK : cuda_fail(e);
 }
 
 int conv_bn_silu_check(void *stream)

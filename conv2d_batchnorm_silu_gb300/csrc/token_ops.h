@@ -1,0 +1,72 @@
+// token_ops.h -- host-side types of the token-wise operators, shared by the C
+// ABI (capi.cu) and their translation units.  Not part of the public interface.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace cbs {
+
+// Element types of activations (the values of cbs_dtype).
+enum DType : int { kF32 = 0, kBf16 = 1, kF16 = 2 };
+
+inline int dtype_size(int t) { return t == kF32 ? 4 : 2; }
+
+// Rows of one matrix: element (r, c) is at data[r * stride + c].
+struct Rows {
+    void *data;
+    long long stride;  // in elements
+};
+
+struct NormProblem {
+    Rows x;              // input, `dtype`
+    Rows y;              // normalised output, `dtype` (q_out.data == nullptr)
+    Rows q;              // int8 output instead of y, with row_scale
+    float *row_scale;    // [rows], with q only
+    float *stats;        // nullable [2][rows]: mean, then 1/sqrt(var + eps)
+    const float *gamma;  // nullable [c]
+    const float *beta;   // nullable [c]
+    float eps;
+    int normalise;       // 0: quantise x itself (q only)
+    long long rows;
+    int c;
+    int dtype;
+};
+
+struct NormGradProblem {
+    Rows dy, x, dx;      // `dtype`
+    const float *gamma;  // nullable [c]
+    const float *stats;  // [2][rows]
+    float *dgamma;       // [c]
+    float *dbeta;        // [c]
+    float *partial;      // workspace: [partial_rows][2][c]
+    int partial_rows;    // from norm_grad_partial_rows
+    long long rows;
+    int c;
+    int dtype;
+};
+
+struct LinearProblem {
+    Rows a;                // int8 [m][k]
+    Rows w;                // int8 [n][k]
+    Rows residual;         // nullable `out_dtype` [m][n]
+    Rows y;                // `out_dtype` [m][n]
+    const float *a_scale;  // [m]
+    const float *w_scale;  // [n]
+    const float *bias;     // nullable [n]
+    long long m;
+    int n, k;
+    int out_dtype;
+    int activation;        // cbs_activation
+    void *workspace;       // linear_workspace_bytes
+};
+
+cudaError_t norm_launch(const NormProblem &p, cudaStream_t stream);
+int norm_grad_partial_rows(long long rows, int c, int sm_count);
+cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_t stream);
+
+// Bytes linear_launch may need for these sizes, whatever the pointers and strides.
+long long linear_workspace_bytes(long long m, int n, int k, int sm_count);
+cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
+
+}  // namespace cbs

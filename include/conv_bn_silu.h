@@ -318,6 +318,118 @@ int conv_bn_silu_forward_request(const void *x, const void *w, const float *scal
                                  int stride_h, int stride_w, int pad_h, int pad_w, const cbs_plan_request *req,
                                  void *stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Token-wise operators: layer norm with its gradient, rows quantised to 8-bit
+ * integers, and the linear layer over such rows.  A pixel of an NHWC tensor is
+ * a row of its channels, so they run on the same activations as the layers
+ * above ([n*h*w][c]), and on tokens [tokens][c].
+ *
+ * Conventions, besides those at the top:
+ *   - A matrix is given by a pointer, its number of rows, and the distance of
+ *     its rows in elements; elements of one row are adjacent.  Inputs may have
+ *     any distance >= 0 (0: every row the same memory), outputs at least
+ *     their width.  Pointers need only be aligned to their element; rows that
+ *     are 16-byte aligned throughout run on wider loads and stores.
+ *   - dtype is a cbs_dtype and goes for every activation of the call; parameters,
+ *     statistics and scales are float32, as the folded scale and bias are.
+ *   - Outputs must not overlap inputs, workspaces or each other.
+ *   - No call allocates.  Where a workspace is asked for, its size comes from
+ *     the call's *_workspace function; it needs no initialisation, holds nothing
+ *     between calls, and belongs to one call at a time.
+ *   - Results are deterministic: no atomics, every sum in a fixed order for one
+ *     GPU model and one set of arguments.
+ */
+
+/* Element type of activations. */
+typedef enum cbs_dtype {
+    CBS_DTYPE_F32 = 0,
+    CBS_DTYPE_BF16 = 1,
+    CBS_DTYPE_F16 = 2
+} cbs_dtype;
+
+/*
+ * Layer norm of each row over its c channels:
+ *   mean = sum x / c,  var = sum (x - mean)^2 / c,  rstd = 1 / sqrt(var + eps)
+ *   y = (x - mean) * rstd * gamma + beta
+ *   x, y  : device, dtype [rows][c], row distances x_stride and y_stride
+ *   gamma : device, float32 [c], or NULL for 1;  beta : likewise, or NULL for 0
+ *   eps   : >= 0 and finite (a constant row with eps == 0 gives NaN)
+ *   stats : device, float32 [2][rows], written with mean, then rstd (what
+ *           conv_bn_silu_layer_norm_backward needs), or NULL
+ * Computed in fp32 with the variance summed around the mean; y rounded once.
+ * rows == 0 is a no-op; c >= 1.
+ */
+int conv_bn_silu_layer_norm(const void *x, long long x_stride, const float *gamma, const float *beta, float eps,
+                            void *y, long long y_stride, float *stats, long long rows, int c, int dtype,
+                            void *stream);
+
+/*
+ * Gradient of conv_bn_silu_layer_norm.  With h = (x - mean) * rstd and g = dy * gamma,
+ *   dx = rstd * (g - sum_c(g)/c - h * sum_c(g*h)/c)
+ *   dgamma = sum over rows of dy * h,  dbeta = sum over rows of dy
+ *   dy, x, dx     : device, dtype [rows][c], row distances *_stride
+ *   gamma         : as in the forward call, or NULL for 1
+ *   stats         : device, float32 [2][rows], written by the forward call
+ *   dgamma, dbeta : device, float32 [c], written (not added to)
+ *   workspace     : device, 16-byte aligned, at least
+ *                   conv_bn_silu_layer_norm_backward_workspace(rows, c) bytes
+ * rows == 0 leaves dgamma and dbeta zero.
+ */
+int conv_bn_silu_layer_norm_backward(const void *dy, long long dy_stride, const void *x, long long x_stride,
+                                     const float *gamma, const float *stats, void *dx, long long dx_stride,
+                                     float *dgamma, float *dbeta, long long rows, int c, int dtype,
+                                     void *workspace, long long workspace_bytes, void *stream);
+
+/* Workspace of conv_bn_silu_layer_norm_backward on the current device in bytes;
+ * -1 for arguments out of range or when no device answers. */
+long long conv_bn_silu_layer_norm_backward_workspace(long long rows, int c);
+
+/*
+ * Rows quantised to 8-bit integers with one scale each:
+ *   most = max(max_c |x|, 2^-100),  scale = most / 127,  q = round(x * (127 / most))
+ * rounded to nearest even, so q * scale is x within half a step and q is in
+ * [-127, 127].  A row holding a NaN or an infinity gets q = 0 and a scale that is
+ * not finite, so that whatever is computed from it is NaN.
+ *   x         : device, dtype [rows][c];  q : device, int8 [rows][c], written
+ *   row_scale : device, float32 [rows], written
+ */
+int conv_bn_silu_quantize_rows(const void *x, long long x_stride, void *q, long long q_stride, float *row_scale,
+                               long long rows, int c, int dtype, void *stream);
+
+/* conv_bn_silu_layer_norm and conv_bn_silu_quantize_rows in one pass: the
+ * normalised values are quantised in fp32, without being rounded to dtype first. */
+int conv_bn_silu_layer_norm_quantize(const void *x, long long x_stride, const float *gamma, const float *beta,
+                                     float eps, void *q, long long q_stride, float *row_scale, long long rows,
+                                     int c, int dtype, void *stream);
+
+/*
+ * Linear layer over 8-bit integers, scales for each row (token) and output channel:
+ *   y[m][n] = act( (sum_k a[m][k] * w[n][k]) * (a_scale[m] * w_scale[n]) + bias[n] ) [+ residual[m][n]]
+ *   a        : device, int8 [m][k];  w : device, int8 [n][k] (a 1x1 filter's KRSC)
+ *   a_scale  : device, float32 [m];  w_scale : device, float32 [n]
+ *   bias     : device, float32 [n], or NULL
+ *   residual : device, out_dtype [m][n], or NULL; added after the activation, in
+ *              fp32, before the one rounding.  It may be y itself.
+ *   y        : device, out_dtype [m][n], written
+ *   activation : a cbs_activation;  out_dtype : a cbs_dtype
+ *   workspace  : device, 16-byte aligned, at least
+ *                conv_bn_silu_linear_int8_workspace(...) bytes; NULL when that is 0
+ * Sums are of integers: in 32-bit integers, or in fp32 on the tensor cores, which is
+ * exact while partial sums stay below 2^24 and rounds beyond.  k <= 131071, n <= 2^22.
+ * m == 0 or n == 0 is a no-op; k == 0 gives act(bias) + residual.
+ * A pipeline wait that runs out is reported by conv_bn_silu_check.
+ */
+int conv_bn_silu_linear_int8(const void *a, long long a_stride, const void *w, long long w_stride,
+                             const float *a_scale, const float *w_scale, const float *bias, const void *residual,
+                             long long residual_stride, void *y, long long y_stride, long long m, int n, int k,
+                             int activation, int out_dtype, void *workspace, long long workspace_bytes,
+                             void *stream);
+
+/* Workspace of conv_bn_silu_linear_int8 on the current device in bytes for these sizes, whatever
+ * the pointers and row distances; -1 for sizes out of range or when no device answers. */
+long long conv_bn_silu_linear_int8_workspace(long long m, int n, int k);
+
 /* Synchronises `stream`, then reads and clears the library's device error word.
  * Returns CBS_ERR_TIMEOUT if any kernel since the last check gave up on a
  * pipeline wait, CBS_ERR_CUDA if the synchronisation failed, else CBS_OK. */
