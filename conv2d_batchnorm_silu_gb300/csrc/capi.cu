@@ -224,7 +224,10 @@ int norm_call(const void *x, long long x_stride, const float *gamma, const float
     p.rows = rows;
     p.c = c;
     p.dtype = dtype;
-    cudaError_t e = cbs::norm_launch(p, static_cast<cudaStream_t>(stream));
+    int sms = 0;
+    st = sm_count_current_device(&sms);
+    if (st != CBS_OK) return st;
+    cudaError_t e = cbs::norm_launch(p, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CBS_OK : cuda_fail(e);
 }
 

@@ -226,6 +226,10 @@ __global__ void __launch_bounds__(32 * kJoinRuns) norm_grad_join_kernel(const Gr
 // V = 16 bytes' worth where every pointer, row distance and the width allow it, else 1.
 template <typename T, int V>
 struct Vec;
+template <int V>
+struct ParamOf { using type = __half; };  // any type whose vector has V elements
+template <>
+struct ParamOf<4> { using type = float; };
 template <typename T>
 struct Vec<T, 1> {
     T raw;
@@ -239,6 +243,10 @@ template <>
 struct Vec<float, 4> {
     float4 raw;
     __device__ __forceinline__ void load(const float *p) { raw = __ldcs(reinterpret_cast<const float4 *>(p)); }
+    __device__ __forceinline__ void from(const uint4 &w)
+    {
+        raw = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+    }
     __device__ __forceinline__ void get(float *v) const
     {
         v[0] = raw.x;
@@ -252,7 +260,8 @@ struct Vec<float, 4> {
     }
     static __device__ __forceinline__ void store_q(int8_t *p, const int *q)
     {
-        *reinterpret_cast<char4 *>(p) = make_char4((char)q[0], (char)q[1], (char)q[2], (char)q[3]);
+        const uint32_t lo = __byte_perm(q[0], q[1], 0x0040), hi = __byte_perm(q[2], q[3], 0x0040);
+        *reinterpret_cast<uint32_t *>(p) = __byte_perm(lo, hi, 0x5410);
     }
     static __device__ __forceinline__ void load_param(const float *p, float *v)
     {
@@ -285,6 +294,7 @@ template <typename T>
 struct Vec<T, 8> {
     uint4 raw;
     __device__ __forceinline__ void load(const T *p) { raw = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void from(const uint4 &w) { raw = w; }
     __device__ __forceinline__ void get(float *v) const
     {
         const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -302,8 +312,8 @@ struct Vec<T, 8> {
     static __device__ __forceinline__ void store_q(int8_t *p, const int *q)
     {
         auto four = [&](int i) {
-            return (uint32_t)(q[i] & 255) | (uint32_t)(q[i + 1] & 255) << 8 | (uint32_t)(q[i + 2] & 255) << 16 |
-                   (uint32_t)q[i + 3] << 24;
+            const uint32_t lo = __byte_perm(q[i], q[i + 1], 0x0040), hi = __byte_perm(q[i + 2], q[i + 3], 0x0040);
+            return __byte_perm(lo, hi, 0x5410);
         };
         *reinterpret_cast<uint2 *>(p) = make_uint2(four(0), four(4));
     }
@@ -313,6 +323,18 @@ struct Vec<T, 8> {
         Vec<float, 4>::load_param(p + 4, v + 4);
     }
 };
+
+// Two fp32 operations per instruction; each rounds like the scalar one.
+__device__ __forceinline__ float2 pair(float a, float b) { return make_float2(a, b); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// max(|a|, |b|, |c|); a NaN among them is the result.
+__device__ __forceinline__ float most_of(float a, float b, float c)
+{
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
 
 // Sum over the TPR threads of a row; `scratch` is this sum's own TPR / 32 floats, so that one
 // barrier does.
@@ -329,21 +351,123 @@ __device__ __forceinline__ float row_sum(float v, float *scratch)
     return v;
 }
 
+// Largest of non-negative values over the TPR threads, as bits: ordered like the values, NaN on top.
 template <int TPR>
-__device__ __forceinline__ unsigned row_max(unsigned v, float *scratch)
+__device__ __forceinline__ float row_most(float v, float *scratch)
 {
-    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    unsigned m = __float_as_uint(v);
+    if (TPR < 32)
+        for (int o = TPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    else
+        m = __reduce_max_sync(0xffffffffu, m);
     if (TPR > 32) {
-        if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = __uint_as_float(v);
+        if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = __uint_as_float(m);
         __syncthreads();
-        v = 0;
-        for (int i = 0; i < TPR / 32; ++i) v = max(v, __float_as_uint(scratch[i]));
+        m = 0;
+        for (int i = 0; i < TPR / 32; ++i) m = max(m, __float_as_uint(scratch[i]));
     }
-    return v;
+    return __uint_as_float(m);
 }
 
-constexpr int norm_block(int tpr) { return tpr < 128 ? 128 : tpr; }
+// Threads of a block in which TPR threads hold a row: one row, or as many as 128 threads hold
+// while a row stays within a warp.
+constexpr int norm_block(int tpr) { return tpr <= 32 ? 128 : tpr; }
 
+// What becomes of row r once thread `lane` of its TPR threads has its part in v (zeros beyond the
+// row): NI runs of V elements, run i at column (i * TPR + lane) * V.  params(i, g, b) gives run i's
+// gamma and beta.  All threads of a block call this together; rows past the end store nothing.
+template <typename T, int V, int NI, int TPR, bool QUANT, typename Params>
+__device__ __forceinline__ void finish_row(const NormArgs &a, long long r, int lane, float (&v)[NI * V],
+                                           float (*scratch)[TPR > 32 ? TPR / 32 : 1], const Params &params)
+{
+    static_assert(NI * V % 2 == 0, "elements are handled in pairs");
+    const bool live = r < a.rows;
+    auto inside = [&](int i) { return (i * TPR + lane) * V < a.c; };
+    if (!QUANT || a.normalise) {
+        float2 s = both(0.0f);
+        for (int e = 0; e < NI * V; e += 2) s = __fadd2_rn(s, pair(v[e], v[e + 1]));
+        const float mean = row_sum<TPR>(s.x + s.y, scratch[0]) / (float)a.c;
+        s = both(0.0f);
+        if (V == 1) {
+            for (int i = 0; i < NI; ++i)
+                if (inside(i)) {
+                    v[i] -= mean;
+                    s.x = fmaf(v[i], v[i], s.x);
+                }
+        } else {
+            for (int i = 0; i < NI; ++i)
+                if (inside(i))
+                    for (int e = i * V; e < (i + 1) * V; e += 2) {
+                        const float2 d = __fadd2_rn(pair(v[e], v[e + 1]), both(-mean));
+                        s = __ffma2_rn(d, d, s);
+                        v[e] = d.x;
+                        v[e + 1] = d.y;
+                    }
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<TPR>(s.x + s.y, scratch[1]) / (float)a.c + a.eps);
+        if (a.stats && lane == 0 && live) {
+            a.stats[r] = mean;
+            a.stats[a.rows + r] = rstd;
+        }
+        for (int i = 0; i < NI; ++i)
+            if (inside(i)) {
+                float g[V], b[V];
+                params(i, g, b);
+                if (V == 1) {
+                    v[i] = fmaf(v[i] * rstd, g[0], b[0]);
+                } else {
+                    for (int j = 0; j < V; j += 2) {
+                        const int e = i * V + j;
+                        const float2 h = __fmul2_rn(pair(v[e], v[e + 1]), both(rstd));
+                        const float2 y = __ffma2_rn(h, pair(g[j], g[j + 1]), pair(b[j], b[j + 1]));
+                        v[e] = y.x;
+                        v[e + 1] = y.y;
+                    }
+                }
+            }
+    }
+    if (QUANT) {
+        float most = 0.0f;
+        for (int e = 0; e < NI * V; e += 2) most = most_of(most, v[e], v[e + 1]);
+        most = row_most<TPR>(most, scratch[2]);
+        float inv;
+        const float scale = row_scale_of(__float_as_uint(most), &inv);
+        if (lane == 0 && live) a.row_scale[r] = scale;
+        // Adding 1.5 * 2^23 leaves a whole number, rounded to nearest even, in the low bits.  The products
+        // are scalar: a packed one is joined with the addition into one that rounds once, which tips values
+        // next to a half to the other side (seen against the definition's own arithmetic).
+        if (scale < __int_as_float(0x7f800000)) {
+            for (int e = 0; e < NI * V; e += 2) {
+                const float2 q = __fadd2_rn(pair(__fmul_rn(v[e], inv), __fmul_rn(v[e + 1], inv)), both(12582912.0f));
+                v[e] = q.x;
+                v[e + 1] = q.y;
+            }
+        } else {
+            for (int e = 0; e < NI * V; ++e) v[e] = 0.0f;
+        }
+        for (int i = 0; i < NI; ++i)
+            if (live && inside(i)) {
+                int q[V];
+                for (int j = 0; j < V; ++j) q[j] = __float_as_int(v[i * V + j]);
+                Vec<T, V>::store_q(a.q + r * a.q_stride + (i * TPR + lane) * V, q);
+            }
+    } else {
+        for (int i = 0; i < NI; ++i)
+            if (live && inside(i))
+                Vec<T, V>::store(static_cast<T *>(a.y) + r * a.y_stride + (i * TPR + lane) * V, v + i * V);
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void load_params(const NormArgs &a, int c, float *g, float *b)
+{
+    using P = Vec<typename ParamOf<V>::type, V>;
+    for (int j = 0; j < V; ++j) g[j] = 1.0f, b[j] = 0.0f;
+    if (a.gamma) P::load_param(a.gamma + c, g);
+    if (a.beta) P::load_param(a.beta + c, b);
+}
+
+// One row for each TPR threads.
 template <typename T, int V, int NI, int TPR, bool QUANT>
 __global__ void __launch_bounds__(norm_block(TPR)) norm_rows_kernel(const NormArgs a)
 {
@@ -352,72 +476,90 @@ __global__ void __launch_bounds__(norm_block(TPR)) norm_rows_kernel(const NormAr
     dev::grid_dependents_launch();
     const int lane = threadIdx.x % TPR;
     const long long r = (long long)blockIdx.x * (norm_block(TPR) / TPR) + threadIdx.x / TPR;
-    const bool live = r < a.rows;  // the same for all threads of a block of one row
-    const T *x = static_cast<const T *>(a.x) + (live ? r * a.x_stride : 0);
+    const T *x = static_cast<const T *>(a.x) + r * a.x_stride;
     Vec<T, V> raw[NI];
+    float v[NI * V];
     for (int i = 0; i < NI; ++i) {
         const int c = (i * TPR + lane) * V;
-        if (live && c < a.c) raw[i].load(x + c);
+        if (r < a.rows && c < a.c) raw[i].load(x + c);
     }
-    float v[NI][V];
     for (int i = 0; i < NI; ++i) {
-        if (live && (i * TPR + lane) * V < a.c)
-            raw[i].get(v[i]);
+        if (r < a.rows && (i * TPR + lane) * V < a.c)
+            raw[i].get(v + i * V);
         else
-            for (int j = 0; j < V; ++j) v[i][j] = 0.0f;
+            for (int j = 0; j < V; ++j) v[i * V + j] = 0.0f;
     }
-    if (!QUANT || a.normalise) {
-        float s = 0.0f;
-        for (int i = 0; i < NI; ++i)
-            for (int j = 0; j < V; ++j) s += v[i][j];
-        const float mean = row_sum<TPR>(s, scratch[0]) / (float)a.c;
-        s = 0.0f;
-        for (int i = 0; i < NI; ++i)
-            if ((i * TPR + lane) * V < a.c)
-                for (int j = 0; j < V; ++j) {
-                    v[i][j] -= mean;
-                    s = fmaf(v[i][j], v[i][j], s);
-                }
-        const float rstd = 1.0f / sqrtf(row_sum<TPR>(s, scratch[1]) / (float)a.c + a.eps);
-        if (a.stats && live && lane == 0) {
-            a.stats[r] = mean;
-            a.stats[a.rows + r] = rstd;
-        }
-        for (int i = 0; i < NI; ++i) {
-            const int c = (i * TPR + lane) * V;
-            if (c < a.c) {
-                float g[V], b[V];
-                if (a.gamma)
-                    Vec<T, V>::load_param(a.gamma + c, g);
-                else
-                    for (int j = 0; j < V; ++j) g[j] = 1.0f;
-                if (a.beta)
-                    Vec<T, V>::load_param(a.beta + c, b);
-                else
-                    for (int j = 0; j < V; ++j) b[j] = 0.0f;
-                for (int j = 0; j < V; ++j) v[i][j] = fmaf(v[i][j] * rstd, g[j], b[j]);
+    finish_row<T, V, NI, TPR, QUANT>(a, r, lane, v, scratch, [&](int i, float *g, float *b) {
+        load_params<V>(a, (i * TPR + lane) * V, g, b);
+    });
+}
+
+// ------------------------------------------------------------------ many rows: parameters held, rows streamed
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Blocks that stay for many rows: each thread keeps the gamma and beta of its columns in registers and
+// copies its own part of the coming STAGES - 1 rows to shared memory with cp.async (no barrier: nobody
+// else reads it), so that memory stays busy while a row is summed.
+constexpr int kNormVecs = 4;  // vectors of a row per thread
+constexpr int kNormStages = 3;
+constexpr int norm_stream_blocks(int tpr) { return 512 / norm_block(tpr); }  // per SM: 128 registers a thread
+template <typename T, int TPR, bool QUANT>
+__global__ void __launch_bounds__(norm_block(TPR), norm_stream_blocks(TPR)) norm_stream_kernel(const NormArgs a)
+{
+    constexpr int V = 16 / sizeof(T), NI = kNormVecs;
+    constexpr int kBlock = norm_block(TPR), kGroups = kBlock / TPR;
+    __shared__ uint4 ring[kNormStages][NI][kBlock];
+    // Two sets: a row's first sum may be written while a slow warp still reads the last row's.
+    __shared__ float scratch[2][3][TPR > 32 ? TPR / 32 : 1];
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+    const int lane = threadIdx.x % TPR;
+    const long long step = (long long)gridDim.x * kGroups;
+    auto fetch = [&](long long r, int stage) {
+        if (r < a.rows) {
+            const T *x = static_cast<const T *>(a.x) + r * a.x_stride;
+            for (int i = 0; i < NI; ++i) {
+                const int c = (i * TPR + lane) * V;
+                if (c < a.c) copy_async(dev::smem_u32(&ring[stage][i][threadIdx.x]), x + c);
             }
         }
-    }
-    if (QUANT) {
-        unsigned most = 0;
-        for (int i = 0; i < NI; ++i)
-            for (int j = 0; j < V; ++j) most = max(most, magnitude_bits(v[i][j]));
-        float inv;
-        const float scale = row_scale_of(row_max<TPR>(most, scratch[2]), &inv);
-        if (live && lane == 0) a.row_scale[r] = scale;
+        copy_commit();
+    };
+    long long r = (long long)blockIdx.x * kGroups + threadIdx.x / TPR;
+    for (int s = 0; s < kNormStages - 1; ++s) fetch(r + s * step, s);
+    float g[NI][V], b[NI][V];
+    for (int i = 0; i < NI; ++i)
+        if ((i * TPR + lane) * V < a.c) load_params<V>(a, (i * TPR + lane) * V, g[i], b[i]);
+    int stage = 0, parity = 0;
+    for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += step, r += step) {
+        fetch(r + (kNormStages - 1) * step, stage == 0 ? kNormStages - 1 : stage - 1);
+        copy_wait<kNormStages - 1>();
+        float v[NI * V];
         for (int i = 0; i < NI; ++i) {
-            const int c = (i * TPR + lane) * V;
-            int q[V];
-            for (int j = 0; j < V; ++j) q[j] = __float2int_rn(v[i][j] * inv);
-            if (live && c < a.c) Vec<T, V>::store_q(a.q + r * a.q_stride + c, q);
+            if (r < a.rows && (i * TPR + lane) * V < a.c) {
+                Vec<T, V> raw;
+                raw.from(ring[stage][i][threadIdx.x]);
+                raw.get(v + i * V);
+            } else {
+                for (int j = 0; j < V; ++j) v[i * V + j] = 0.0f;
+            }
         }
-    } else {
-        for (int i = 0; i < NI; ++i) {
-            const int c = (i * TPR + lane) * V;
-            if (live && c < a.c) Vec<T, V>::store(static_cast<T *>(a.y) + r * a.y_stride + c, v[i]);
-        }
+        finish_row<T, V, NI, TPR, QUANT>(a, r, lane, v, scratch[parity], [&](int i, float *pg, float *pb) {
+            for (int j = 0; j < V; ++j) pg[j] = g[i][j], pb[j] = b[i][j];
+        });
+        stage = stage + 1 == kNormStages ? 0 : stage + 1;
+        parity ^= 1;
     }
+    copy_wait<0>();
 }
 
 unsigned blocks_for_rows(long long rows) { return (unsigned)(rows < (1LL << 20) ? rows : (1LL << 20)); }
@@ -426,9 +568,19 @@ template <typename T, int V, int NI, int TPR>
 cudaError_t norm_rows_launch(const NormArgs &a, cudaStream_t stream)
 {
     constexpr int kRows = norm_block(TPR) / TPR;
-    const dim3 grid((unsigned)((a.rows + kRows - 1) / kRows));
-    return a.q ? launch_overlapped(norm_rows_kernel<T, V, NI, TPR, true>, grid, dim3(norm_block(TPR)), 0, stream, 1, a)
-               : launch_overlapped(norm_rows_kernel<T, V, NI, TPR, false>, grid, dim3(norm_block(TPR)), 0, stream, 1, a);
+    const dim3 grid((unsigned)((a.rows + kRows - 1) / kRows)), block(norm_block(TPR));
+    return a.q ? launch_overlapped(norm_rows_kernel<T, V, NI, TPR, true>, grid, block, 0, stream, 1, a)
+               : launch_overlapped(norm_rows_kernel<T, V, NI, TPR, false>, grid, block, 0, stream, 1, a);
+}
+
+template <typename T, int TPR>
+cudaError_t norm_stream_launch(const NormArgs &a, int sm_count, cudaStream_t stream)
+{
+    constexpr int kRows = norm_block(TPR) / TPR;
+    const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sm_count * norm_stream_blocks(TPR);
+    const dim3 grid((unsigned)(need < room ? need : room)), block(norm_block(TPR));
+    return a.q ? launch_overlapped(norm_stream_kernel<T, TPR, true>, grid, block, 0, stream, 1, a)
+               : launch_overlapped(norm_stream_kernel<T, TPR, false>, grid, block, 0, stream, 1, a);
 }
 
 bool aligned_for(const void *p, long long stride, int element, int bytes)
@@ -437,25 +589,27 @@ bool aligned_for(const void *p, long long stride, int element, int bytes)
 }
 
 template <typename T>
-cudaError_t norm_launch_t(const NormArgs &a, cudaStream_t stream)
+cudaError_t norm_launch_t(const NormArgs &a, int sm_count, cudaStream_t stream)
 {
     constexpr int V = 16 / sizeof(T);
     if (a.rows < (1LL << 31)) {
         const bool wide_loads = a.c % V == 0 && aligned_for(a.x, a.x_stride, sizeof(T), 16) &&
                                 (a.q ? aligned_for(a.q, a.q_stride, 1, V) : aligned_for(a.y, a.y_stride, sizeof(T), 16)) &&
                                 aligned_for(a.gamma, 0, 4, 16) && aligned_for(a.beta, 0, 4, 16);
-        // The fewest threads that hold the row, so that its sums cross as few lanes as possible, with at
-        // most 32 elements each (registers), from four vectors a thread on more threads instead.
+        const int nv = a.c / V;
+        // Held parameters and streamed rows are the faster from few rows on: bf16, us with one row for
+        // each TPR threads against this, 8x4096 3.2 / 2.5, 600x1024 2.9 / 2.8, 2048x2048 7.1 / 6.5,
+        // 32768x4096 110 / 84 (6.4 TB/s), 32768x256 10.0 / 9.2.  TPR is the fewest threads that hold the
+        // row in four vectors each: more threads sum over more lanes (8192x4096 on 256: 37 us).
         if (wide_loads) {
-            const int nv = a.c / V;
             if (nv <= 4) return norm_rows_launch<T, V, 1, 4>(a, stream);
-            if (nv <= 16) return norm_rows_launch<T, V, 1, 16>(a, stream);
-            if (nv <= 32) return norm_rows_launch<T, V, 1, 32>(a, stream);
-            if (nv <= 64) return norm_rows_launch<T, V, 2, 32>(a, stream);
-            if (nv <= 128) return norm_rows_launch<T, V, 4, 32>(a, stream);
-            if (nv <= 256) return norm_rows_launch<T, V, 2, 128>(a, stream);
-            if (nv <= 512) return norm_rows_launch<T, V, 4, 128>(a, stream);
-            if (nv <= 1024) return norm_rows_launch<T, V, 4, 256>(a, stream);
+            if (nv <= 16) return norm_stream_launch<T, 4>(a, sm_count, stream);
+            if (nv <= 32) return norm_stream_launch<T, 8>(a, sm_count, stream);
+            if (nv <= 64) return norm_stream_launch<T, 16>(a, sm_count, stream);
+            if (nv <= 128) return norm_stream_launch<T, 32>(a, sm_count, stream);
+            if (nv <= 256) return norm_stream_launch<T, 64>(a, sm_count, stream);
+            if (nv <= 512) return norm_stream_launch<T, 128>(a, sm_count, stream);
+            if (nv <= 1024) return norm_stream_launch<T, 256>(a, sm_count, stream);
             if (nv <= 2048) return norm_rows_launch<T, V, 4, 512>(a, stream);
         } else {
             if (a.c <= 32) return norm_rows_launch<T, 1, 4, 8>(a, stream);
@@ -485,7 +639,7 @@ cudaError_t norm_grad_launch_t(const GradArgs &a, cudaStream_t stream)
 
 }  // namespace
 
-cudaError_t norm_launch(const NormProblem &p, cudaStream_t stream)
+cudaError_t norm_launch(const NormProblem &p, int sm_count, cudaStream_t stream)
 {
     NormArgs a{};
     a.x = p.x.data;
@@ -503,9 +657,9 @@ cudaError_t norm_launch(const NormProblem &p, cudaStream_t stream)
     a.eps = p.eps;
     a.normalise = p.normalise;
     switch (p.dtype) {
-    case kF32: return norm_launch_t<float>(a, stream);
-    case kBf16: return norm_launch_t<__nv_bfloat16>(a, stream);
-    default: return norm_launch_t<__half>(a, stream);
+    case kF32: return norm_launch_t<float>(a, sm_count, stream);
+    case kBf16: return norm_launch_t<__nv_bfloat16>(a, sm_count, stream);
+    default: return norm_launch_t<__half>(a, sm_count, stream);
     }
 }
 

@@ -61,7 +61,7 @@ struct LinearProblem {
     void *workspace;       // linear_workspace_bytes
 };
 
-cudaError_t norm_launch(const NormProblem &p, cudaStream_t stream);
+cudaError_t norm_launch(const NormProblem &p, int sm_count, cudaStream_t stream);
 int norm_grad_partial_rows(long long rows, int c, int sm_count);
 cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_t stream);
 
