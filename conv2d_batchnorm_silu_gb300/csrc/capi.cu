@@ -175,7 +175,6 @@ int noalloc_scratch_address(void **out)
     return CBS_OK;
 }
 
-
 // ------------------------------------------------------------------ token-wise operators
 bool aligned_to(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0; }
 
@@ -718,7 +717,10 @@ int conv_bn_silu_check(void *stream)
     unsigned int wword = 0;
     e = cbs::cmajor_read_and_clear_error(static_cast<cudaStream_t>(stream), &wword);
     if (e != cudaSuccess) return cuda_fail(e);
-    if ((gword != 0 || wword != 0) && word == 0) return CBS_ERR_TIMEOUT;
+    unsigned int lword = 0;
+    e = cbs::linear_read_and_clear_error(static_cast<cudaStream_t>(stream), &lword);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if ((gword != 0 || wword != 0 || lword != 0) && word == 0) return CBS_ERR_TIMEOUT;
     if (word == 0) return CBS_OK;
     // A kernel gave up mid-way: stream-K ready flags may be left raised.
     e = cbs::tc_reset_workspaces();

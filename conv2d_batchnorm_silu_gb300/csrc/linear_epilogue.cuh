@@ -1,0 +1,200 @@
+// linear_epilogue.cuh -- what the int8 linear layer's kernels do to a sum:
+//   y = act(sum * (a_scale[m] * w_scale[n]) + bias[n]) [+ residual[m][n]], rounded once.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "conv_bn_silu.h"
+#include "ptx.cuh"
+#include "token_ops.h"
+
+namespace cbs {
+
+struct LinearEpilogue {
+    const float *a_scale, *w_scale, *bias;
+    const void *residual;
+    void *y;
+    long long residual_stride, y_stride;
+    long long m;
+    int n;
+    int activation;
+    int vec_params;    // w_scale and bias 16-byte aligned
+    int vec_y;         // rows of y 16-byte aligned
+    int vec_residual;  // rows of the residual 16-byte aligned
+};
+
+inline LinearEpilogue linear_epilogue_of(const LinearProblem &p)
+{
+    const int size = dtype_size(p.out_dtype);
+    auto rows16 = [&](const Rows &r) {
+        return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && r.stride * size % 16 == 0;
+    };
+    LinearEpilogue e{};
+    e.a_scale = p.a_scale;
+    e.w_scale = p.w_scale;
+    e.bias = p.bias;
+    e.residual = p.residual.data;
+    e.residual_stride = p.residual.stride;
+    e.y = p.y.data;
+    e.y_stride = p.y.stride;
+    e.m = p.m;
+    e.n = p.n;
+    e.activation = p.activation;
+    e.vec_params = reinterpret_cast<uintptr_t>(p.w_scale) % 16 == 0 && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
+    e.vec_y = rows16(p.y);
+    e.vec_residual = rows16(p.residual);
+    return e;
+}
+
+#ifdef __CUDACC__
+namespace {
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
+__device__ __forceinline__ void from_float(float v, float *out) { *out = v; }
+__device__ __forceinline__ void from_float(float v, __nv_bfloat16 *out) { *out = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void from_float(float v, __half *out) { *out = __float2half_rn(v); }
+
+// SiLU to fp32 accuracy, because the output may be fp32; z of -100 and below gives -0.
+__device__ __forceinline__ float activated(float z, int activation)
+{
+    if (activation == CBS_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
+    if (activation == CBS_ACT_RELU) return z < 0.0f ? 0.0f : z;  // keeps NaN
+    return z;
+}
+
+// One output: the general form.
+template <typename T>
+__device__ __forceinline__ void finish_one(const LinearEpilogue &e, float sum, long long m, int n)
+{
+    float z = sum * (__ldg(e.a_scale + m) * __ldg(e.w_scale + n));
+    if (e.bias) z += __ldg(e.bias + n);
+    z = activated(z, e.activation);
+    if (e.residual) z += to_float(static_cast<const T *>(e.residual)[m * e.residual_stride + n]);
+    from_float(z, static_cast<T *>(e.y) + m * e.y_stride + n);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half)
+{
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16)
+{
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// A warp's block of 32 rows x 32 columns from (row0, col0): lane l holds row row0 + l, its 32 sums in
+// v.  Rows and columns past the end are computed and not stored.  `stg` is the warp's own 32 x 32
+// elements of shared memory, through which lanes exchange rows for columns, so that each store covers
+// whole runs of a row; 16-byte pieces are swizzled so that neither direction meets a bank twice.
+template <typename T>
+__device__ __forceinline__ void finish_block(const LinearEpilogue &e, float *v, float row_scale, long long row0,
+                                             int col0, uint32_t stg, int lane)
+{
+    constexpr int kPieces = 32 * sizeof(T) / 16;      // 16-byte pieces of a row
+    constexpr int kPer = 16 / sizeof(T);              // elements of a piece
+    const bool whole = col0 + 32 <= e.n;
+    const long long row = row0 + lane;
+    if (whole && e.vec_params) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float4 s = __ldg(reinterpret_cast<const float4 *>(e.w_scale + col0 + i));
+            float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (e.bias) b = __ldg(reinterpret_cast<const float4 *>(e.bias + col0 + i));
+            v[i] = fmaf(v[i], row_scale * s.x, b.x);
+            v[i + 1] = fmaf(v[i + 1], row_scale * s.y, b.y);
+            v[i + 2] = fmaf(v[i + 2], row_scale * s.z, b.z);
+            v[i + 3] = fmaf(v[i + 3], row_scale * s.w, b.w);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const int c = col0 + i < e.n ? col0 + i : e.n - 1;
+            v[i] = fmaf(v[i], row_scale * __ldg(e.w_scale + c), e.bias ? __ldg(e.bias + c) : 0.0f);
+        }
+    }
+    if (e.activation == CBS_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = activated(v[i], CBS_ACT_SILU);
+    } else if (e.activation == CBS_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = activated(v[i], CBS_ACT_RELU);
+    }
+    if (e.residual && row < e.m) {
+        const T *res = static_cast<const T *>(e.residual) + row * e.residual_stride + col0;
+        if (whole && e.vec_residual) {
+#pragma unroll
+            for (int q = 0; q < kPieces; ++q) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(res + q * kPer);
+                if constexpr (sizeof(T) == 4) {
+                    v[4 * q] += __uint_as_float(w.x);
+                    v[4 * q + 1] += __uint_as_float(w.y);
+                    v[4 * q + 2] += __uint_as_float(w.z);
+                    v[4 * q + 3] += __uint_as_float(w.w);
+                } else {
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = unpack2(u[k], T());
+                        v[8 * q + 2 * k] += f.x;
+                        v[8 * q + 2 * k + 1] += f.y;
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (col0 + i < e.n) v[i] += to_float(res[i]);
+        }
+    }
+    auto at = [&](int r, int q) {
+        const int turn = kPieces == 8 ? (r & 7) : ((r >> 1) & 3);
+        return stg + (uint32_t)(r * (32 * (int)sizeof(T)) + ((q ^ turn) * 16));
+    };
+    __syncwarp();  // the block before has been read
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+        if constexpr (sizeof(T) == 4)
+            dev::sts_v4(at(lane, q), __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+        else
+            dev::sts_v4(at(lane, q), pack2(v[8 * q], v[8 * q + 1], T()), pack2(v[8 * q + 2], v[8 * q + 3], T()),
+                        pack2(v[8 * q + 4], v[8 * q + 5], T()), pack2(v[8 * q + 6], v[8 * q + 7], T()));
+    }
+    __syncwarp();
+    T *y = static_cast<T *>(e.y) + row0 * e.y_stride + col0;
+    if (whole && e.vec_y) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const int r = i * (32 / kPieces) + lane / kPieces, q = lane % kPieces;
+            const uint4 w = dev::lds_v4(at(r, q));
+            if (row0 + r < e.m) *reinterpret_cast<uint4 *>(y + r * e.y_stride + q * kPer) = w;
+        }
+    } else if (col0 + lane < e.n) {
+        for (int r = 0; r < 32 && row0 + r < e.m; ++r) {
+            const uint32_t addr = at(r, lane / kPer) + (uint32_t)(lane % kPer * (int)sizeof(T));
+            if constexpr (sizeof(T) == 4)
+                reinterpret_cast<uint32_t *>(y + r * e.y_stride)[lane] = dev::lds_u32(addr);
+            else
+                reinterpret_cast<unsigned short *>(y + r * e.y_stride)[lane] = (unsigned short)dev::lds_u16(addr);
+        }
+    }
+}
+
+}  // namespace
+#endif
+
+}  // namespace cbs

@@ -11,7 +11,7 @@
 #include <stdint.h>
 
 #include "cbs_internal.h"
-#include "conv_bn_silu.h"
+#include "linear_epilogue.cuh"
 #include "ptx.cuh"
 #include "token_ops.h"
 
@@ -19,30 +19,11 @@ namespace cbs {
 namespace {
 
 struct LinearArgs {
+    LinearEpilogue e;
     const int8_t *a, *w;
-    const void *residual;
-    void *y;
-    const float *a_scale, *w_scale, *bias;
-    long long a_stride, w_stride, residual_stride, y_stride;
-    long long m;
-    int n, k;
-    int activation;
+    long long a_stride, w_stride;
+    int k;
 };
-
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
-__device__ __forceinline__ void from_float(float v, float *out) { *out = v; }
-__device__ __forceinline__ void from_float(float v, __nv_bfloat16 *out) { *out = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void from_float(float v, __half *out) { *out = __float2half_rn(v); }
-
-// SiLU to fp32 accuracy: the output may be fp32, and a NaN stays one.
-__device__ __forceinline__ float activated(float z, int activation)
-{
-    if (activation == CBS_ACT_SILU) return z / (1.0f + __expf(-z));
-    if (activation == CBS_ACT_RELU) return z < 0.0f ? 0.0f : z;
-    return z;
-}
 
 // 64 x 64 outputs per block of 256 threads (4 x 4 each), K in steps of 64 through shared
 // memory, four products per __dp4a: any size, alignment and stride.
@@ -62,8 +43,8 @@ __global__ void __launch_bounds__(256) linear_tile_kernel(const LinearArgs a)
         for (int i = threadIdx.x; i < kTile * kStepK; i += 256) {
             const int r = i / kStepK, c = i % kStepK, k = k0 + c;
             int8_t va = 0, vw = 0;
-            if (k < a.k && m0 + r < a.m) va = a.a[(m0 + r) * a.a_stride + k];
-            if (k < a.k && n0 + r < a.n) vw = a.w[(long long)(n0 + r) * a.w_stride + k];
+            if (k < a.k && m0 + r < a.e.m) va = a.a[(m0 + r) * a.a_stride + k];
+            if (k < a.k && n0 + r < a.e.n) vw = a.w[(long long)(n0 + r) * a.w_stride + k];
             reinterpret_cast<int8_t *>(sa[r])[c] = va;
             reinterpret_cast<int8_t *>(sw[r])[c] = vw;
         }
@@ -77,52 +58,37 @@ __global__ void __launch_bounds__(256) linear_tile_kernel(const LinearArgs a)
         for (int j = 0; j < 4; ++j) {
             const long long m = m0 + ty + 16 * i;
             const int n = n0 + tx + 16 * j;
-            if (m >= a.m || n >= a.n) continue;
-            float z = (float)acc[i][j] * (a.a_scale[m] * a.w_scale[n]);
-            if (a.bias) z += a.bias[n];
-            z = activated(z, a.activation);
-            if (a.residual) z += to_float(static_cast<const T *>(a.residual)[m * a.residual_stride + n]);
-            from_float(z, static_cast<T *>(a.y) + m * a.y_stride + n);
+            if (m < a.e.m && n < a.e.n) finish_one<T>(a.e, (float)acc[i][j], m, n);
         }
 }
 
 template <typename T>
 cudaError_t linear_launch_t(const LinearArgs &a, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)((a.m + kTile - 1) / kTile), (unsigned)((a.n + kTile - 1) / kTile));
+    const dim3 grid((unsigned)((a.e.m + kTile - 1) / kTile), (unsigned)((a.e.n + kTile - 1) / kTile));
     return launch_overlapped(linear_tile_kernel<T>, grid, dim3(256), 0, stream, 1, a);
 }
 
 }  // namespace
 
+bool linear_on_tensor_cores(long long m, int n, int k) { return m > 16 && k > 0 && tc_linear_supported(m, n, k); }
+
 long long linear_workspace_bytes(long long m, int n, int k, int sm_count)
 {
-    (void)m;
-    (void)n;
-    (void)k;
     (void)sm_count;
-    return 0;
+    return m > 0 && n > 0 && linear_on_tensor_cores(m, n, k) ? tc_linear_workspace_bytes(m, n, k) : 0;
 }
 
 cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream)
 {
-    (void)sm_count;
+    if (linear_on_tensor_cores(p.m, p.n, p.k)) return tc_linear_launch(p, sm_count, stream);
     LinearArgs a{};
+    a.e = linear_epilogue_of(p);
     a.a = static_cast<const int8_t *>(p.a.data);
     a.a_stride = p.a.stride;
     a.w = static_cast<const int8_t *>(p.w.data);
     a.w_stride = p.w.stride;
-    a.residual = p.residual.data;
-    a.residual_stride = p.residual.stride;
-    a.y = p.y.data;
-    a.y_stride = p.y.stride;
-    a.a_scale = p.a_scale;
-    a.w_scale = p.w_scale;
-    a.bias = p.bias;
-    a.m = p.m;
-    a.n = p.n;
     a.k = p.k;
-    a.activation = p.activation;
     switch (p.out_dtype) {
     case kF32: return linear_launch_t<float>(a, stream);
     case kBf16: return linear_launch_t<__nv_bfloat16>(a, stream);
