@@ -232,7 +232,9 @@ int norm_call(const void *x, long long x_stride, const float *gamma, const float
 
 bool linear_sizes_ok(long long m, int n, int k)
 {
-    return m >= 0 && m <= (1LL << 36) && n >= 0 && n <= (1 << 22) && k >= 0 && k <= 131071;
+    // Sums of k products of -128 * -128 fit 32-bit integers; tile counts fit 32 bits.
+    return m >= 0 && m < (1LL << 31) && n >= 0 && n <= (1 << 22) && k >= 0 && k <= 131071 &&
+           ((m + 127) / 128) * ((n + 63LL) / 64) < (1LL << 30);
 }
 
 }  // namespace

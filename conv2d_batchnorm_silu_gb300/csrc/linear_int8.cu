@@ -25,63 +25,120 @@ struct LinearArgs {
     int k;
 };
 
-// 64 x 64 outputs per block of 256 threads (4 x 4 each), K in steps of 64 through shared
-// memory, four products per __dp4a: any size, alignment and stride.
-constexpr int kTile = 64;
-constexpr int kStepK = 64;
-template <typename T>
-__global__ void __launch_bounds__(256) linear_tile_kernel(const LinearArgs a)
+// ------------------------------------------------------------------ few rows
+// Up to eight rows of a: the weights are read once, at memory speed, and four products at a time go
+// into 32-bit integers with __dp4a.  A warp (or, where there are few channels, two to eight warps that
+// split K) takes kFewChannels channels; a lane holds 16 bytes of each of their weights and goes through
+// the rows of a with them, so a's bytes, which stay in L1, are read once for all the channels.
+constexpr int kFewChannels = 4;
+constexpr int kFewWarps = 8;
+
+// 16 values from k0 on, zeros past k.
+__device__ __forceinline__ uint4 load16(const int8_t *row, int k0, int k, bool aligned)
 {
-    __shared__ int sa[kTile][kStepK / 4 + 1], sw[kTile][kStepK / 4 + 1];
+    if (aligned && k0 + 16 <= k) return __ldg(reinterpret_cast<const uint4 *>(row + k0));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (k0 + e < k) w[e / 4] |= (uint32_t)(uint8_t)__ldg(row + k0 + e) << (8 * (e % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ int dot16(const uint4 &a, const uint4 &b, int acc)
+{
+    acc = __dp4a((int)a.x, (int)b.x, acc);
+    acc = __dp4a((int)a.y, (int)b.y, acc);
+    acc = __dp4a((int)a.z, (int)b.z, acc);
+    return __dp4a((int)a.w, (int)b.w, acc);
+}
+
+template <typename T, int ROWS, bool ALIGNED>
+__global__ void __launch_bounds__(32 * kFewWarps) linear_few_kernel(const LinearArgs a, int split_log2)
+{
+    constexpr int R = kFewChannels;
+    __shared__ int part[kFewWarps][R * ROWS];
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
-    const long long m0 = (long long)blockIdx.x * kTile;
-    const int n0 = blockIdx.y * kTile;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    int acc[4][4] = {};
-    for (int k0 = 0; k0 < a.k; k0 += kStepK) {
-        for (int i = threadIdx.x; i < kTile * kStepK; i += 256) {
-            const int r = i / kStepK, c = i % kStepK, k = k0 + c;
-            int8_t va = 0, vw = 0;
-            if (k < a.k && m0 + r < a.e.m) va = a.a[(m0 + r) * a.a_stride + k];
-            if (k < a.k && n0 + r < a.e.n) vw = a.w[(long long)(n0 + r) * a.w_stride + k];
-            reinterpret_cast<int8_t *>(sa[r])[c] = va;
-            reinterpret_cast<int8_t *>(sw[r])[c] = vw;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = 1 << split_log2, groups = kFewWarps >> split_log2;
+    const int n0 = (blockIdx.x * groups + (warp >> split_log2)) * R;
+    const int m = (int)a.e.m;
+    const int8_t *w[R], *x[ROWS];
+#pragma unroll
+    for (int r = 0; r < R; ++r) w[r] = a.w + (long long)min(n0 + r, a.e.n - 1) * a.w_stride;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) x[i] = a.a + min(i, m - 1) * a.a_stride;
+    int acc[R][ROWS] = {};
+    const int step = split * 512;
+#pragma unroll 2
+    for (int k0 = ((warp & (split - 1)) * 32 + lane) * 16; k0 < a.k; k0 += step) {
+        uint4 wv[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) wv[r] = load16(w[r], k0, a.k, ALIGNED);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const uint4 xv = load16(x[i], k0, a.k, ALIGNED);
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[r][i] = dot16(wv[r], xv, acc[r][i]);
         }
-        __syncthreads();
-        for (int c = 0; c < kStepK / 4; ++c)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(sa[ty + 16 * i][c], sw[tx + 16 * j][c], acc[i][j]);
-        __syncthreads();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const long long m = m0 + ty + 16 * i;
-            const int n = n0 + tx + 16 * j;
-            if (m < a.e.m && n < a.e.n) finish_one<T>(a.e, (float)acc[i][j], m, n);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int s = __reduce_add_sync(0xffffffffu, acc[r][i]);
+            if (lane == 0) part[warp][i * R + r] = s;
         }
+    __syncthreads();
+    for (int o = threadIdx.x; o < groups * R * ROWS; o += 32 * kFewWarps) {
+        const int g = o / (R * ROWS), e = o % (R * ROWS), i = e / R;
+        const int n = (blockIdx.x * groups + g) * R + e % R;
+        int s = 0;
+        for (int t = 0; t < split; ++t) s += part[g * split + t][e];
+        if (i < m && n < a.e.n) finish_one<T>(a.e, (float)s, i, n);
+    }
+}
+
+template <typename T, bool ALIGNED>
+cudaError_t linear_few_launch(const LinearArgs &a, int sm_count, cudaStream_t stream)
+{
+    // K is split among warps until an SM has 16 of them or a warp less than one whole pass of K.
+    int split_log2 = 0;
+    while (split_log2 < 3 && (long long)(a.e.n + kFewChannels - 1) / kFewChannels << split_log2 < 16LL * sm_count &&
+           a.k > 512 << split_log2)
+        ++split_log2;
+    const int per_block = kFewChannels * (kFewWarps >> split_log2);
+    const dim3 grid((unsigned)((a.e.n + per_block - 1) / per_block)), block(32 * kFewWarps);
+    if (a.e.m == 1) return launch_overlapped(linear_few_kernel<T, 1, ALIGNED>, grid, block, 0, stream, 1, a, split_log2);
+    if (a.e.m == 2) return launch_overlapped(linear_few_kernel<T, 2, ALIGNED>, grid, block, 0, stream, 1, a, split_log2);
+    if (a.e.m <= 4) return launch_overlapped(linear_few_kernel<T, 4, ALIGNED>, grid, block, 0, stream, 1, a, split_log2);
+    return launch_overlapped(linear_few_kernel<T, 8, ALIGNED>, grid, block, 0, stream, 1, a, split_log2);
 }
 
 template <typename T>
-cudaError_t linear_launch_t(const LinearArgs &a, cudaStream_t stream)
+cudaError_t linear_few_launch_t(const LinearArgs &a, int sm_count, cudaStream_t stream)
 {
-    const dim3 grid((unsigned)((a.e.m + kTile - 1) / kTile), (unsigned)((a.e.n + kTile - 1) / kTile));
-    return launch_overlapped(linear_tile_kernel<T>, grid, dim3(256), 0, stream, 1, a);
+    auto rows16 = [](const int8_t *p, long long stride) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 16 == 0;
+    };
+    return rows16(a.a, a.a_stride) && rows16(a.w, a.w_stride) ? linear_few_launch<T, true>(a, sm_count, stream)
+                                                              : linear_few_launch<T, false>(a, sm_count, stream);
 }
 
 }  // namespace
 
-bool linear_on_tensor_cores(long long m, int n, int k) { return m > 16 && k > 0 && tc_linear_supported(m, n, k); }
+// Rows up to which linear_few_kernel is the faster.
+constexpr int kFewRows = 8;
 
 long long linear_workspace_bytes(long long m, int n, int k, int sm_count)
 {
     (void)sm_count;
-    return m > 0 && n > 0 && linear_on_tensor_cores(m, n, k) ? tc_linear_workspace_bytes(m, n, k) : 0;
+    return m > kFewRows && n > 0 ? tc_linear_workspace_bytes(m, n, k) : 0;
 }
 
 cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream)
 {
-    if (linear_on_tensor_cores(p.m, p.n, p.k)) return tc_linear_launch(p, sm_count, stream);
+    if (p.m > kFewRows) return tc_linear_launch(p, sm_count, stream);
     LinearArgs a{};
     a.e = linear_epilogue_of(p);
     a.a = static_cast<const int8_t *>(p.a.data);
@@ -90,9 +147,9 @@ cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t str
     a.w_stride = p.w.stride;
     a.k = p.k;
     switch (p.out_dtype) {
-    case kF32: return linear_launch_t<float>(a, stream);
-    case kBf16: return linear_launch_t<__nv_bfloat16>(a, stream);
-    default: return linear_launch_t<__half>(a, stream);
+    case kF32: return linear_few_launch_t<float>(a, sm_count, stream);
+    case kBf16: return linear_few_launch_t<__nv_bfloat16>(a, sm_count, stream);
+    default: return linear_few_launch_t<__half>(a, sm_count, stream);
     }
 }
 

@@ -426,13 +426,6 @@ cudaError_t gemm_launch_t(const LinearProblem &p, const __half *a16, const __hal
 
 }  // namespace
 
-bool tc_linear_supported(long long m, int n, int k)
-{
-    // Tile counts and tensor-map extents within 32 bits.
-    (void)k;
-    return m < (1LL << 31) && ((m + 127) / 128) * (((long long)n + 63) / 64) < (1LL << 31) - 1024;
-}
-
 long long tc_linear_workspace_bytes(long long m, int n, int k)
 {
     const long long kp = padded_k(k);

@@ -69,8 +69,7 @@ cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_
 long long linear_workspace_bytes(long long m, int n, int k, int sm_count);
 cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
 
-// The linear layer on the tensor cores (tc_linear.cu).
-bool tc_linear_supported(long long m, int n, int k);
+// The linear layer on the tensor cores (tc_linear.cu); k == 0 counts as a step of zeros.
 long long tc_linear_workspace_bytes(long long m, int n, int k);
 cudaError_t tc_linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
 cudaError_t linear_read_and_clear_error(cudaStream_t stream, unsigned int *out);

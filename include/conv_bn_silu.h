@@ -416,7 +416,8 @@ int conv_bn_silu_layer_norm_quantize(const void *x, long long x_stride, const fl
  *   workspace  : device, 16-byte aligned, at least
  *                conv_bn_silu_linear_int8_workspace(...) bytes; NULL when that is 0
  * Sums are of integers: in 32-bit integers, or in fp32 on the tensor cores, which is
- * exact while partial sums stay below 2^24 and rounds beyond.  k <= 131071, n <= 2^22.
+ * exact while partial sums stay below 2^24 and rounds beyond.  k <= 131071, n <= 2^22,
+ * m < 2^31, and y of at most 2^43 elements.
  * m == 0 or n == 0 is a no-op; k == 0 gives act(bias) + residual.
  * A pipeline wait that runs out is reported by conv_bn_silu_check.
  */
