@@ -461,23 +461,33 @@ def silu_apply(t2: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> 
 # ---------------------------------------------------------------- token-wise operators
 # Activations are tensors [..., c] whose last dimension is dense and whose leading dimensions
 # are rows at one distance (a contiguous tensor, or a column slice of a matrix); parameters,
-# statistics and scales are dense float32.
+# statistics and scales are dense float32.  Small calls are bound by the host: an operator looks
+# at each tensor once and allocates through the entry that generated code uses (0.9 us a tensor on
+# the GB300's host, against 1.6 us and a launch slower by 2 us after torch.empty).
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    def _empty_strided_cuda(shape, stride, dtype):
+        return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
 
 
 def _rows(t: torch.Tensor, name: str, device: int) -> tuple[int, int, int, int]:
     """(pointer, rows, columns, distance of rows in elements) of an activation tensor."""
     if t.get_device() != device:
         raise ValueError(f"{name} must be on the CUDA device of the call's first tensor")
-    if t.dim() != 2:
-        if t.dim() == 0:
+    shape = t.shape
+    if len(shape) != 2:
+        if not shape:
             raise ValueError(f"{name} must have at least one dimension")
-        c = t.shape[-1]
+        c = shape[-1]
         try:
-            t = t.view(t.numel() // c if c else 0, c)
+            t = t.view(math.prod(shape[:-1]), c)
         except RuntimeError:
             raise ValueError(f"{name}'s leading dimensions must be rows at one distance") from None
-    rows, c = t.shape
+        shape = t.shape
+    rows, c = shape
     distance, step = t.stride()
     if step != 1 and c > 1:
         raise ValueError(f"{name}'s last dimension must be dense")
@@ -494,42 +504,54 @@ def _vector(t: torch.Tensor | None, n: int, name: str, device: int) -> int | Non
     return t.data_ptr()
 
 
-def _device_of(t: torch.Tensor, name: str) -> int:
+def _first(t: torch.Tensor, name: str) -> int:
+    """The device of the call's first tensor, which has to be the current one."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     device = t.get_device()
-    if device < 0 or device != torch.cuda.current_device():
+    if device < 0 or device != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current CUDA device")
     return device
 
 
-def _dtype_of(t: torch.Tensor, name: str) -> int:
-    code = DTYPES.get(t.dtype)
+def _dtype_code(dtype: torch.dtype, name: str) -> int:
+    code = DTYPES.get(dtype)
     if code is None:
-        raise TypeError(f"{name} must be torch.float32, torch.bfloat16 or torch.float16, got {t.dtype}")
+        raise TypeError(f"{name} must be torch.float32, torch.bfloat16 or torch.float16, got {dtype}")
     return code
-
-
-def _run_stream(stream, device: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream_handle(stream)
 
 
 def _empty(shape, dtype: torch.dtype, device: int, stream) -> torch.Tensor:
     """An output or workspace; on another stream than the current one, from that stream's memory."""
+    shape = tuple(shape)
+    n = len(shape)
+    if n == 1:
+        stride = (1,)
+    elif n == 2:
+        stride = (shape[1], 1)
+    else:
+        stride = tuple(math.prod(shape[i + 1:]) for i in range(n))
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty_strided_cuda(shape, stride, dtype)
     with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(stream), device=device)):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty_strided_cuda(shape, stride, dtype)
 
 
-def _output(t: torch.Tensor | None, shape, dtype: torch.dtype, name: str, device: int, stream) -> torch.Tensor:
+def _output(t: torch.Tensor | None, shape, dtype: torch.dtype, name: str, device: int, stream):
+    """(tensor, pointer, distance of rows) of an output that is given or made here."""
     if t is None:
-        return _empty(shape, dtype, device, stream)
+        t = _empty(shape, dtype, device, stream)
+        return t, t.data_ptr(), shape[-1]
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t
+    pointer, _, _, distance = _rows(t, name, device)
+    return t, pointer, distance
+
+
+def _run_stream(stream, device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream_handle(stream)
 
 
 def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
@@ -539,15 +561,18 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
     x: float32, bf16 or f16 [..., c]; gamma, beta: fp32 [c] or None; y like x.  With return_stats
     also the fp32 statistics [2, rows] (mean, then 1/sqrt(var + eps)) for layer_norm_backward.
     """
-    device = _device_of(x, "x")
-    dtype = _dtype_of(x, "x")
+    device = _first(x, "x")
+    dtype = x.dtype
+    code = _dtype_code(dtype, "x")
     px, rows, c, sx = _rows(x, "x", device)
-    y = _output(y, x.shape, x.dtype, "y", device, stream)
-    stats = _empty((2, rows), torch.float32, device, stream) if return_stats else None
+    pg, pb = _vector(gamma, c, "gamma", device), _vector(beta, c, "beta", device)
+    y, py, sy = _output(y, x.shape, dtype, "y", device, stream)
+    stats = pstats = None
+    if return_stats:
+        stats = _empty((2, rows), torch.float32, device, stream)
+        pstats = stats.data_ptr()
     if rows:
-        py, _, _, sy = _rows(y, "y", device)
-        st = _layer_norm(px, sx, _vector(gamma, c, "gamma", device), _vector(beta, c, "beta", device), eps, py, sy,
-                         stats.data_ptr() if return_stats else None, rows, c, dtype, _run_stream(stream, device))
+        st = _layer_norm(px, sx, pg, pb, eps, py, sy, pstats, rows, c, code, _run_stream(stream, device))
         if st:
             _raise_if(st, "conv_bn_silu_layer_norm")
     return (y, stats) if return_stats else y
@@ -557,25 +582,24 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor |
                         dx: torch.Tensor | None = None, stream=None):
     """conv_bn_silu_layer_norm_backward: (dx, dgamma, dbeta) from dy, the forward call's x and gamma
     (None: ones) and the statistics it returned.  dx is like x; dgamma and dbeta are fp32 [c]."""
-    device = _device_of(x, "x")
-    dtype = _dtype_of(x, "x")
-    if dy.dtype is not x.dtype:
-        raise TypeError(f"dy must be {x.dtype}, got {dy.dtype}")
+    device = _first(x, "x")
+    dtype = x.dtype
+    code = _dtype_code(dtype, "x")
+    if dy.dtype is not dtype:
+        raise TypeError(f"dy must be {dtype}, got {dy.dtype}")
     if dy.shape != x.shape:
         raise ValueError(f"dy has shape {tuple(dy.shape)}, expected {tuple(x.shape)}")
     px, rows, c, sx = _rows(x, "x", device)
     pdy, _, _, sdy = _rows(dy, "dy", device)
-    dx = _output(dx, x.shape, x.dtype, "dx", device, stream)
-    pdx, _, _, sdx = _rows(dx, "dx", device)
-    pstats = _vector(stats, 2 * rows, "stats", device)
+    pg, pstats = _vector(gamma, c, "gamma", device), _vector(stats, 2 * rows, "stats", device)
     need = _layer_norm_backward_workspace(rows, c)
     if need < 0:
         _raise_if(CBS_ERR_INVALID_ARG, "conv_bn_silu_layer_norm_backward_workspace")
+    dx, pdx, sdx = _output(dx, x.shape, dtype, "dx", device, stream)
     dgamma, dbeta = _empty((c,), torch.float32, device, stream), _empty((c,), torch.float32, device, stream)
     work = _empty((need,), torch.uint8, device, stream)
-    st = _layer_norm_backward(pdy, sdy, px, sx, _vector(gamma, c, "gamma", device), pstats, pdx, sdx,
-                              dgamma.data_ptr(), dbeta.data_ptr(), rows, c, dtype, work.data_ptr(), need,
-                              _run_stream(stream, device))
+    st = _layer_norm_backward(pdy, sdy, px, sx, pg, pstats, pdx, sdx, dgamma.data_ptr(), dbeta.data_ptr(), rows, c,
+                              code, work.data_ptr(), need, _run_stream(stream, device))
     if st:
         _raise_if(st, "conv_bn_silu_layer_norm_backward")
     return dx, dgamma, dbeta
@@ -583,14 +607,14 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor |
 
 def quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """conv_bn_silu_quantize_rows: (q, scale), q int8 like x, scale fp32 [...] with x close to q * scale."""
-    device = _device_of(x, "x")
-    dtype = _dtype_of(x, "x")
+    device = _first(x, "x")
+    code = _dtype_code(x.dtype, "x")
     px, rows, c, sx = _rows(x, "x", device)
-    q = _output(q, x.shape, torch.int8, "q", device, stream)
-    scale = _empty(x.shape[:-1], torch.float32, device, stream)
+    shape = x.shape
+    q, pq, sq = _output(q, shape, torch.int8, "q", device, stream)
+    scale = _empty(shape[:-1], torch.float32, device, stream)
     if rows:
-        pq, _, _, sq = _rows(q, "q", device)
-        st = _quantize_rows(px, sx, pq, sq, scale.data_ptr(), rows, c, dtype, _run_stream(stream, device))
+        st = _quantize_rows(px, sx, pq, sq, scale.data_ptr(), rows, c, code, _run_stream(stream, device))
         if st:
             _raise_if(st, "conv_bn_silu_quantize_rows")
     return q, scale
@@ -601,15 +625,16 @@ def layer_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, beta
                         stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """conv_bn_silu_layer_norm_quantize: layer_norm, its rows quantised in the same pass; (q, scale) as
     quantize_rows gives them."""
-    device = _device_of(x, "x")
-    dtype = _dtype_of(x, "x")
+    device = _first(x, "x")
+    code = _dtype_code(x.dtype, "x")
     px, rows, c, sx = _rows(x, "x", device)
-    q = _output(q, x.shape, torch.int8, "q", device, stream)
-    scale = _empty(x.shape[:-1], torch.float32, device, stream)
+    pg, pb = _vector(gamma, c, "gamma", device), _vector(beta, c, "beta", device)
+    shape = x.shape
+    q, pq, sq = _output(q, shape, torch.int8, "q", device, stream)
+    scale = _empty(shape[:-1], torch.float32, device, stream)
     if rows:
-        pq, _, _, sq = _rows(q, "q", device)
-        st = _layer_norm_quantize(px, sx, _vector(gamma, c, "gamma", device), _vector(beta, c, "beta", device), eps,
-                                  pq, sq, scale.data_ptr(), rows, c, dtype, _run_stream(stream, device))
+        st = _layer_norm_quantize(px, sx, pg, pb, eps, pq, sq, scale.data_ptr(), rows, c, code,
+                                  _run_stream(stream, device))
         if st:
             _raise_if(st, "conv_bn_silu_layer_norm_quantize")
     return q, scale
@@ -624,30 +649,22 @@ def linear_int8(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale
     a: int8 [..., k]; w: int8 [n, k]; a_scale: fp32, one for each row of a; w_scale, bias: fp32 [n];
     residual and y: out_dtype [..., n] (residual may be y).  activation: "silu", "identity" or "relu".
     """
-    device = _device_of(a, "a")
+    device = _first(a, "a")
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
-    out = DTYPES.get(out_dtype)
-    if out is None:
-        raise TypeError(f"out_dtype must be torch.float32, torch.bfloat16 or torch.float16, got {out_dtype}")
+    code = _dtype_code(out_dtype, "out_dtype")
     if a.dtype is not torch.int8 or w.dtype is not torch.int8:
         raise TypeError("a and w must be torch.int8")
     if w.dim() != 2:
         raise ValueError("w must be [n, k]")
-    k = a.shape[-1]
-    n = w.shape[0]
-    if w.shape[1] != k:
-        raise ValueError(f"channel mismatch: a has {k}, w has {w.shape[1]}")
-    pw, _, _, sw = _rows(w, "w", device)
-    shape = a.shape[:-1] + (n,)
-    y = _output(y, shape, out_dtype, "y", device, stream)
-    if k:
-        pa, m, _, sa = _rows(a, "a", device)
-    else:
-        pa, m, sa = a.data_ptr(), math.prod(a.shape[:-1]), 0
-    pas, pws, pb = (_vector(a_scale, m, "a_scale", device), _vector(w_scale, n, "w_scale", device),
-                    _vector(bias, n, "bias", device))
+    pw, n, k, sw = _rows(w, "w", device)
+    pa, m, ka, sa = _rows(a, "a", device)
+    if ka != k:
+        raise ValueError(f"channel mismatch: a has {ka}, w has {k}")
+    pas, pws = _vector(a_scale, m, "a_scale", device), _vector(w_scale, n, "w_scale", device)
+    pb = _vector(bias, n, "bias", device)
+    shape = (m, n) if a.dim() == 2 else (*a.shape[:-1], n)
     pr, sr = None, 0
     if residual is not None:
         if residual.dtype is not out_dtype:
@@ -655,15 +672,18 @@ def linear_int8(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale
         if residual.shape != shape:
             raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(shape)}")
         pr, _, _, sr = _rows(residual, "residual", device)
+    y, py, sy = _output(y, shape, out_dtype, "y", device, stream)
     if m == 0 or n == 0:
         return y
-    py, _, _, sy = _rows(y, "y", device)
     need = _linear_int8_workspace(m, n, k)
-    if need < 0:
+    work = pwork = None
+    if need > 0:
+        work = _empty((need,), torch.uint8, device, stream)
+        pwork = work.data_ptr()
+    elif need < 0:
         _raise_if(CBS_ERR_INVALID_ARG, "conv_bn_silu_linear_int8_workspace")
-    work = _empty((need,), torch.uint8, device, stream) if need else None
-    st = _linear_int8(pa, sa, pw, sw, pas, pws, pb, pr, sr, py, sy, m, n, k, act, out,
-                      work.data_ptr() if need else None, need, _run_stream(stream, device))
+    st = _linear_int8(pa, sa, pw, sw, pas, pws, pb, pr, sr, py, sy, m, n, k, act, code, pwork, need,
+                      _run_stream(stream, device))
     if st:
         _raise_if(st, "conv_bn_silu_linear_int8")
     return y
