@@ -623,18 +623,232 @@ cudaError_t norm_launch_t(const NormArgs &a, int sm_count, cudaStream_t stream)
     return launch_overlapped(norm_wide_kernel<T>, dim3(blocks_for_rows(a.rows)), dim3(kWideThreads), 0, stream, 1, a);
 }
 
-template <typename T>
-cudaError_t norm_grad_launch_t(const GradArgs &a, cudaStream_t stream)
+// ------------------------------------------------------------------ gradient, rows in registers
+// As norm_stream_kernel: blocks stay for many rows, TPR threads hold a row of x and dy (NI runs of V
+// elements each), and each thread keeps gamma and the running sums of dy * h and dy for its own columns
+// in registers, so that x and dy are read once for all three gradients.  The two sums over a row share
+// one barrier.  At the end the rows of a block are joined in shared memory, and each block writes one
+// row of partial sums, which norm_grad_join_kernel adds up in order.
+constexpr int kGradElements = 16;  // of a row per thread: sums, gamma, h and g of more would not fit 128 registers
+constexpr int kGradStages = 3;
+constexpr int grad_block(int tpr) { return tpr < 256 ? 256 : tpr; }
+constexpr int grad_blocks_per_sm(int tpr) { return 512 / grad_block(tpr); }
+
+// Sums of two values over the TPR threads of a row; scratch: 2 * TPR / 32 floats for each row of the block.
+template <int TPR>
+__device__ __forceinline__ float2 row_sum2(float2 v, float2 *scratch)
 {
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    if constexpr (TPR > 32) {
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) == 0) scratch[warp] = v;
+        __syncthreads();
+        v = both(0.0f);
+        for (int i = 0; i < TPR / 32; ++i) v = __fadd2_rn(v, scratch[warp / (TPR / 32) * (TPR / 32) + i]);
+    }
+    return v;
+}
+
+template <typename T, int V, int TPR>
+__global__ void __launch_bounds__(grad_block(TPR), grad_blocks_per_sm(TPR)) norm_grad_stream_kernel(const GradArgs a)
+{
+    constexpr int E = kGradElements, NI = E / V, kBlock = grad_block(TPR), kGroups = kBlock / TPR;
+    constexpr bool kRing = V > 1;  // single elements are loaded without one
+    extern __shared__ uint4 grad_ring[];  // [stage][x, dy][NI][kBlock]; afterwards the join of the block's rows
+    __shared__ float2 scratch[2][kBlock / 32];
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+    const int lane = threadIdx.x % TPR;
+    const long long step = (long long)gridDim.x * kGroups;
+    auto column = [&](int i) { return (i * TPR + lane) * V; };
+    auto slot = [&](int stage, int which, int i) {
+        return grad_ring + ((stage * 2 + which) * NI + i) * kBlock + threadIdx.x;
+    };
+    auto fetch = [&](long long r, int stage) {
+        if constexpr (kRing) {
+            if (r < a.rows) {
+                const T *x = static_cast<const T *>(a.x) + r * a.x_stride;
+                const T *dy = static_cast<const T *>(a.dy) + r * a.dy_stride;
+                for (int i = 0; i < NI; ++i)
+                    if (column(i) < a.c) {
+                        copy_async(dev::smem_u32(slot(stage, 0, i)), x + column(i));
+                        copy_async(dev::smem_u32(slot(stage, 1, i)), dy + column(i));
+                    }
+            }
+            copy_commit();
+        }
+    };
+    auto moments = [&](long long r) {
+        return r < a.rows ? make_float2(__ldg(a.stats + r), __ldg(a.stats + a.rows + r)) : both(0.0f);
+    };
+    long long r = (long long)blockIdx.x * kGroups + threadIdx.x / TPR;
+    for (int s = 0; s < kGradStages - 1; ++s) fetch(r + s * step, s);
+    float2 next = moments(r);
+    float gamma[E], dg[E], db[E];
+    for (int i = 0; i < NI; ++i) {
+        for (int j = 0; j < V; ++j) gamma[i * V + j] = 1.0f;
+        if (a.gamma && column(i) < a.c) Vec<typename ParamOf<V>::type, V>::load_param(a.gamma + column(i), gamma + i * V);
+    }
+    for (int e = 0; e < E; ++e) dg[e] = db[e] = 0.0f;
+    const float per_c = 1.0f / (float)a.c;
+    int stage = 0, parity = 0;
+    for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += step, r += step) {
+        fetch(r + (kGradStages - 1) * step, stage == 0 ? kGradStages - 1 : stage - 1);
+        const float2 moment = next;
+        next = moments(r + step);
+        if (kRing) copy_wait<kGradStages - 1>();
+        const float mean = moment.x, rstd = moment.y;
+        float h[E], g[E];
+        Vec<T, V> xs[NI], dys[NI];
+        for (int i = 0; i < NI; ++i)
+            if (r < a.rows && column(i) < a.c) {
+                if constexpr (kRing) {
+                    xs[i].from(*slot(stage, 0, i));
+                    dys[i].from(*slot(stage, 1, i));
+                } else {
+                    xs[i].load(static_cast<const T *>(a.x) + r * a.x_stride + column(i));
+                    dys[i].load(static_cast<const T *>(a.dy) + r * a.dy_stride + column(i));
+                }
+            }
+        float2 s1 = both(0.0f), s2 = both(0.0f);
+        for (int i = 0; i < NI; ++i) {
+            if (r < a.rows && column(i) < a.c) {
+                xs[i].get(h + i * V);
+                dys[i].get(g + i * V);
+            } else {  // adds nothing anywhere: h and dy are both 0
+                for (int j = 0; j < V; ++j) h[i * V + j] = mean, g[i * V + j] = 0.0f;
+            }
+        }
+        for (int e = 0; e < E; e += 2) {
+            const float2 d = pair(g[e], g[e + 1]);
+            const float2 hh = __fmul2_rn(__fadd2_rn(pair(h[e], h[e + 1]), both(-mean)), both(rstd));
+            const float2 sum_g = __ffma2_rn(d, hh, pair(dg[e], dg[e + 1]));
+            const float2 sum_b = __fadd2_rn(d, pair(db[e], db[e + 1]));
+            const float2 gg = __fmul2_rn(d, pair(gamma[e], gamma[e + 1]));
+            s1 = __fadd2_rn(s1, gg);
+            s2 = __ffma2_rn(gg, hh, s2);
+            dg[e] = sum_g.x, dg[e + 1] = sum_g.y;
+            db[e] = sum_b.x, db[e + 1] = sum_b.y;
+            h[e] = hh.x, h[e + 1] = hh.y;
+            g[e] = gg.x, g[e + 1] = gg.y;
+        }
+        const float2 sums = row_sum2<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), scratch[parity]);
+        const float m1 = sums.x * per_c, m2 = sums.y * per_c;
+        for (int e = 0; e < E; e += 2) {
+            const float2 t = __fadd2_rn(__ffma2_rn(pair(h[e], h[e + 1]), both(-m2), pair(g[e], g[e + 1])), both(-m1));
+            const float2 d = __fmul2_rn(t, both(rstd));
+            h[e] = d.x, h[e + 1] = d.y;
+        }
+        if (r < a.rows)
+            for (int i = 0; i < NI; ++i)
+                if (column(i) < a.c)
+                    Vec<T, V>::store(static_cast<T *>(a.dx) + r * a.dx_stride + column(i), h + i * V);
+        stage = stage + 1 == kGradStages ? 0 : stage + 1;
+        parity ^= 1;
+    }
+    if (kRing) copy_wait<0>();
+    float *out = a.partial + (long long)blockIdx.x * 2 * a.c;
+    if constexpr (kGroups == 1) {
+        for (int i = 0; i < NI; ++i)
+            if (column(i) < a.c) {
+                if constexpr (V == 1) {
+                    out[column(i)] = dg[i];
+                    out[a.c + column(i)] = db[i];
+                } else {
+                    for (int j = 0; j < V; j += 4) {
+                        const int e = i * V + j;
+                        *reinterpret_cast<float4 *>(out + column(i) + j) = make_float4(dg[e], dg[e + 1], dg[e + 2], dg[e + 3]);
+                        *reinterpret_cast<float4 *>(out + a.c + column(i) + j) =
+                            make_float4(db[e], db[e + 1], db[e + 2], db[e + 3]);
+                    }
+                }
+            }
+    } else {
+        // The block's rows side by side in shared memory, [row][dgamma, dbeta][element][thread]; those of one
+        // warp are joined by shuffles before.
+        constexpr int kSide = TPR < 32 ? kBlock / 32 : kGroups;
+        for (int o = TPR; o < 32; o <<= 1)
+            for (int e = 0; e < E; ++e) {
+                dg[e] += __shfl_xor_sync(0xffffffffu, dg[e], o);
+                db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+            }
+        float *join = reinterpret_cast<float *>(grad_ring);
+        __syncthreads();  // the ring is no longer read
+        if (TPR >= 32 || (threadIdx.x & 31) < TPR) {
+            float *mine = join + (TPR < 32 ? threadIdx.x / 32 : threadIdx.x / TPR) * (2 * E * TPR) + lane;
+            for (int e = 0; e < E; ++e) {
+                mine[e * TPR] = dg[e];
+                mine[(E + e) * TPR] = db[e];
+            }
+        }
+        __syncthreads();
+        for (int col = threadIdx.x; col < 2 * a.c; col += kBlock) {
+            const int c = col < a.c ? col : col - a.c;
+            const int e = c / (TPR * V) * V + c % V + (col < a.c ? 0 : E);
+            const float *at = join + e * TPR + c / V % TPR;
+            float sum = at[0];
+            for (int t = 1; t < kSide; ++t) sum += at[t * (2 * E * TPR)];
+            out[col] = sum;
+        }
+    }
+}
+
+cudaError_t norm_grad_join(const GradArgs &a, cudaStream_t stream)
+{
+    return launch_overlapped(norm_grad_join_kernel, dim3((unsigned)((2LL * a.c + 31) / 32)), dim3(32, kJoinRuns), 0,
+                             stream, 1, a);
+}
+
+template <typename T, int V, int TPR>
+cudaError_t norm_grad_stream_launch(GradArgs a, int sm_count, cudaStream_t stream)
+{
+    constexpr int kRows = grad_block(TPR) / TPR;
+    constexpr int kRing = V > 1 ? kGradStages * 2 * (kGradElements / V) * grad_block(TPR) * 16 : 0;
+    constexpr int kJoin = kRows > 1 ? (TPR < 32 ? 8 : kRows) * 2 * kGradElements * TPR * 4 : 0;
+    constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
+    static bool allowed[kMaxDevices] = {};
+    if (kSmem > 46 * 1024) {  // the sums of a block take some of the first 48 KB
+        cudaError_t e = allow_dynamic_smem(norm_grad_stream_kernel<T, V, TPR>, kSmem, allowed);
+        if (e != cudaSuccess) return e;
+    }
+    const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sm_count * grad_blocks_per_sm(TPR);
+    a.partial_rows = (int)(need < room ? need : room);
+    cudaError_t e = launch_overlapped(norm_grad_stream_kernel<T, V, TPR>, dim3((unsigned)a.partial_rows),
+                                      dim3(grad_block(TPR)), kSmem, stream, 1, a);
+    return e == cudaSuccess ? norm_grad_join(a, stream) : e;
+}
+
+template <typename T>
+cudaError_t norm_grad_launch_t(const GradArgs &a, int sm_count, cudaStream_t stream)
+{
+    constexpr int V = 16 / sizeof(T);
+    const bool wide_loads = a.c % V == 0 && aligned_for(a.x, a.x_stride, sizeof(T), 16) &&
+                            aligned_for(a.dy, a.dy_stride, sizeof(T), 16) &&
+                            aligned_for(a.dx, a.dx_stride, sizeof(T), 16) && aligned_for(a.gamma, 0, 4, 16);
+    if (wide_loads) {
+        if (a.c <= 8 * kGradElements) return norm_grad_stream_launch<T, V, 8>(a, sm_count, stream);
+        if (a.c <= 16 * kGradElements) return norm_grad_stream_launch<T, V, 16>(a, sm_count, stream);
+        if (a.c <= 32 * kGradElements) return norm_grad_stream_launch<T, V, 32>(a, sm_count, stream);
+        if (a.c <= 64 * kGradElements) return norm_grad_stream_launch<T, V, 64>(a, sm_count, stream);
+        if (a.c <= 128 * kGradElements) return norm_grad_stream_launch<T, V, 128>(a, sm_count, stream);
+        if (a.c <= 256 * kGradElements) return norm_grad_stream_launch<T, V, 256>(a, sm_count, stream);
+        if (a.c <= 512 * kGradElements) return norm_grad_stream_launch<T, V, 512>(a, sm_count, stream);
+    } else {
+        if (a.c <= 8 * kGradElements) return norm_grad_stream_launch<T, 1, 8>(a, sm_count, stream);
+        if (a.c <= 32 * kGradElements) return norm_grad_stream_launch<T, 1, 32>(a, sm_count, stream);
+        if (a.c <= 128 * kGradElements) return norm_grad_stream_launch<T, 1, 128>(a, sm_count, stream);
+        if (a.c <= 512 * kGradElements) return norm_grad_stream_launch<T, 1, 512>(a, sm_count, stream);
+    }
     cudaError_t e = launch_overlapped(norm_grad_wide_kernel<T>, dim3(blocks_for_rows(a.rows)), dim3(kWideThreads), 0,
                                       stream, 1, a);
     if (e != cudaSuccess) return e;
     e = launch_overlapped(norm_grad_columns_kernel<T>,
                           dim3((unsigned)((a.c + kWideThreads - 1) / kWideThreads), (unsigned)a.partial_rows),
                           dim3(kWideThreads), 0, stream, 1, a);
-    if (e != cudaSuccess) return e;
-    return launch_overlapped(norm_grad_join_kernel, dim3((unsigned)((2LL * a.c + 31) / 32)), dim3(32, kJoinRuns), 0,
-                             stream, 1, a);
+    return e == cudaSuccess ? norm_grad_join(a, stream) : e;
 }
 
 }  // namespace
@@ -666,13 +880,12 @@ cudaError_t norm_launch(const NormProblem &p, int sm_count, cudaStream_t stream)
 int norm_grad_partial_rows(long long rows, int c, int sm_count)
 {
     (void)c;
-    const long long most = 4LL * sm_count;
+    const long long most = 2LL * sm_count;  // norm_grad_stream_kernel's blocks at most
     return (int)(rows < most ? rows : most);
 }
 
 cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_t stream)
 {
-    (void)sm_count;
     GradArgs a{};
     a.dy = p.dy.data;
     a.dy_stride = p.dy.stride;
@@ -689,9 +902,9 @@ cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_
     a.c = p.c;
     a.partial_rows = p.partial_rows;
     switch (p.dtype) {
-    case kF32: return norm_grad_launch_t<float>(a, stream);
-    case kBf16: return norm_grad_launch_t<__nv_bfloat16>(a, stream);
-    default: return norm_grad_launch_t<__half>(a, stream);
+    case kF32: return norm_grad_launch_t<float>(a, sm_count, stream);
+    case kBf16: return norm_grad_launch_t<__nv_bfloat16>(a, sm_count, stream);
+    default: return norm_grad_launch_t<__half>(a, sm_count, stream);
     }
 }
 

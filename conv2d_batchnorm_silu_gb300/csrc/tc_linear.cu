@@ -379,26 +379,13 @@ cudaError_t encode_f16(const void *base, long long rows, int kp, int box_rows, C
 
 int padded_k(int k) { return k > 0 ? (k + kBlockK - 1) / kBlockK * kBlockK : kBlockK; }
 
-// Shared memory above 48 KB is allowed once per kernel and device.
-template <typename Kernel>
-cudaError_t allow_smem(Kernel kern, int bytes, bool (&done)[64])
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 64 && __atomic_load_n(&done[dev], __ATOMIC_ACQUIRE)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev < 64) __atomic_store_n(&done[dev], true, __ATOMIC_RELEASE);
-    return e;
-}
-
 template <typename T, int BN, bool PAIR>
 cudaError_t gemm_launch(const LinearProblem &p, const __half *a16, const __half *w16, int kp, int sm_count,
                         cudaStream_t stream)
 {
     using C = GemmCfg<BN, PAIR>;
-    static bool allowed[64] = {};
-    cudaError_t e = allow_smem(linear_gemm_kernel<T, BN, PAIR>, C::SMEM, allowed);
+    static bool allowed[kMaxDevices] = {};
+    cudaError_t e = allow_dynamic_smem(linear_gemm_kernel<T, BN, PAIR>, C::SMEM, allowed);
     if (e != cudaSuccess) return e;
     CUtensorMap ta, tw;
     e = encode_f16(a16, p.m, kp, kBlockM, &ta);

@@ -61,6 +61,20 @@ struct LinearProblem {
     void *workspace;       // linear_workspace_bytes
 };
 
+// Shared memory above 48 KB, allowed once per kernel and device; `done` is the kernel's own record.
+constexpr int kMaxDevices = 64;
+template <typename Kernel>
+cudaError_t allow_dynamic_smem(Kernel kernel, int bytes, bool (&done)[kMaxDevices])
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kMaxDevices && __atomic_load_n(&done[dev], __ATOMIC_ACQUIRE)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < kMaxDevices) __atomic_store_n(&done[dev], true, __ATOMIC_RELEASE);
+    return e;
+}
+
 cudaError_t norm_launch(const NormProblem &p, int sm_count, cudaStream_t stream);
 int norm_grad_partial_rows(long long rows, int c, int sm_count);
 cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_t stream);
