@@ -1,4 +1,5 @@
-// linear_epilogue.cuh -- what the int8 linear layer's kernels do to a sum:
+// linear_device.cuh -- shared by the int8 linear layer's kernels: loads of int8, their widening to
+// f16, and what becomes of a sum:
 //   y = act(sum * (a_scale[m] * w_scale[n]) + bias[n]) [+ residual[m][n]], rounded once.
 #pragma once
 
@@ -57,6 +58,34 @@ __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ void from_float(float v, float *out) { *out = v; }
 __device__ __forceinline__ void from_float(float v, __nv_bfloat16 *out) { *out = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void from_float(float v, __half *out) { *out = __float2half_rn(v); }
+
+// 16 values from k0 on, zeros past k.
+__device__ __forceinline__ uint4 load16(const int8_t *row, int k0, int k, bool aligned)
+{
+    if (aligned && k0 + 16 <= k) return __ldg(reinterpret_cast<const uint4 *>(row + k0));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        if (k0 + e < k) w[e / 4] |= (uint32_t)(uint8_t)__ldg(row + k0 + e) << (8 * (e % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Four int8 of a word -> two words of f16 pairs: biased to 0..255, a byte below 0x64 is the f16
+// 1024 + byte, and subtracting 1152 leaves the value.
+__device__ __forceinline__ uint2 widen4(uint32_t w)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
+    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), bias), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), bias);
+    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+}
+
+// Instruction descriptor of kind::f16 with f16 A and B (format 0), both K-major, fp32 D.
+__host__ __device__ constexpr uint32_t idesc_f16(int m, int n)
+{
+    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
 
 // SiLU to fp32 accuracy, because the output may be fp32; z of -100 and below gives -0.
 __device__ __forceinline__ float activated(float z, int activation)

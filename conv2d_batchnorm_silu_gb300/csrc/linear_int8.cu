@@ -11,7 +11,7 @@
 #include <stdint.h>
 
 #include "cbs_internal.h"
-#include "linear_epilogue.cuh"
+#include "linear_device.cuh"
 #include "ptx.cuh"
 #include "token_ops.h"
 
@@ -33,23 +33,20 @@ struct LinearArgs {
 constexpr int kFewChannels = 4;
 constexpr int kFewWarps = 8;
 
-// 16 values from k0 on, zeros past k.
-__device__ __forceinline__ uint4 load16(const int8_t *row, int k0, int k, bool aligned)
-{
-    if (aligned && k0 + 16 <= k) return __ldg(reinterpret_cast<const uint4 *>(row + k0));
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-        if (k0 + e < k) w[e / 4] |= (uint32_t)(uint8_t)__ldg(row + k0 + e) << (8 * (e % 4));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 __device__ __forceinline__ int dot16(const uint4 &a, const uint4 &b, int acc)
 {
     acc = __dp4a((int)a.x, (int)b.x, acc);
     acc = __dp4a((int)a.y, (int)b.y, acc);
     acc = __dp4a((int)a.z, (int)b.z, acc);
     return __dp4a((int)a.w, (int)b.w, acc);
+}
+
+// ALIGNED: rows on 16-byte boundaries and k a multiple of 16, so that a piece is one load without a branch.
+template <bool ALIGNED>
+__device__ __forceinline__ uint4 piece(const int8_t *row, int k0, int k)
+{
+    if constexpr (ALIGNED) return __ldg(reinterpret_cast<const uint4 *>(row + k0));
+    return load16(row, k0, k, false);
 }
 
 template <typename T, int ROWS, bool ALIGNED>
@@ -74,10 +71,10 @@ __global__ void __launch_bounds__(32 * kFewWarps) linear_few_kernel(const Linear
     for (int k0 = ((warp & (split - 1)) * 32 + lane) * 16; k0 < a.k; k0 += step) {
         uint4 wv[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) wv[r] = load16(w[r], k0, a.k, ALIGNED);
+        for (int r = 0; r < R; ++r) wv[r] = piece<ALIGNED>(w[r], k0, a.k);
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            const uint4 xv = load16(x[i], k0, a.k, ALIGNED);
+            const uint4 xv = piece<ALIGNED>(x[i], k0, a.k);
 #pragma unroll
             for (int r = 0; r < R; ++r) acc[r][i] = dot16(wv[r], xv, acc[r][i]);
         }
@@ -121,7 +118,7 @@ cudaError_t linear_few_launch_t(const LinearArgs &a, int sm_count, cudaStream_t 
     auto rows16 = [](const int8_t *p, long long stride) {
         return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 16 == 0;
     };
-    return rows16(a.a, a.a_stride) && rows16(a.w, a.w_stride) ? linear_few_launch<T, true>(a, sm_count, stream)
+    return a.k % 16 == 0 && rows16(a.a, a.a_stride) && rows16(a.w, a.w_stride) ? linear_few_launch<T, true>(a, sm_count, stream)
                                                               : linear_few_launch<T, false>(a, sm_count, stream);
 }
 
@@ -129,16 +126,22 @@ cudaError_t linear_few_launch_t(const LinearArgs &a, int sm_count, cudaStream_t 
 
 // Rows up to which linear_few_kernel is the faster.
 constexpr int kFewRows = 8;
+// Rows up to which the weights are widened on their way, where the alignment allows it.
+constexpr int kStreamRows = 512;
 
 long long linear_workspace_bytes(long long m, int n, int k, int sm_count)
 {
-    (void)sm_count;
-    return m > kFewRows && n > 0 ? tc_linear_workspace_bytes(m, n, k) : 0;
+    if (m <= kFewRows || n <= 0) return 0;
+    const long long wide = tc_linear_workspace_bytes(m, n, k);
+    const long long streamed = m <= kStreamRows ? tc_stream_workspace_bytes(m, n, k, sm_count) : 0;
+    return wide > streamed ? wide : streamed;
 }
 
 cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream)
 {
-    if (p.m > kFewRows) return tc_linear_launch(p, sm_count, stream);
+    if (p.m > kFewRows)
+        return p.m <= kStreamRows && tc_stream_supported(p) ? tc_stream_launch(p, sm_count, stream)
+                                                            : tc_linear_launch(p, sm_count, stream);
     LinearArgs a{};
     a.e = linear_epilogue_of(p);
     a.a = static_cast<const int8_t *>(p.a.data);
@@ -151,6 +154,15 @@ cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t str
     case kBf16: return linear_few_launch_t<__nv_bfloat16>(a, sm_count, stream);
     default: return linear_few_launch_t<__half>(a, sm_count, stream);
     }
+}
+
+cudaError_t linear_read_and_clear_error(cudaStream_t stream, unsigned int *out)
+{
+    unsigned int a = 0, b = 0;
+    cudaError_t e = tc_linear_read_and_clear_error(stream, &a);
+    if (e == cudaSuccess) e = tc_stream_read_and_clear_error(stream, &b);
+    *out = a | b;
+    return e;
 }
 
 }  // namespace cbs

@@ -16,7 +16,7 @@
 #include <mutex>
 
 #include "cbs_internal.h"
-#include "linear_epilogue.cuh"
+#include "linear_device.cuh"
 #include "ptx.cuh"
 #include "token_ops.h"
 
@@ -27,17 +27,6 @@ __device__ unsigned int g_linear_error = 0;
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far beyond any legitimate wait
 
 // ------------------------------------------------------------------ widening to f16
-// Four int8 of a word -> two words of f16 pairs: biased to 0..255, a byte below 0x64 is the f16
-// 1024 + byte, and subtracting 1152 leaves the value.
-__device__ __forceinline__ uint2 widen4(uint32_t w)
-{
-    const uint32_t u = w ^ 0x80808080u;
-    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
-    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), bias), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), bias);
-    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
-}
-
 struct WidenMatrix {
     const int8_t *src;
     __half *dst;
@@ -64,16 +53,8 @@ __global__ void __launch_bounds__(256) widen_kernel(const WidenArgs args)
         __half *dst = (first ? args.a.dst : args.w.dst) + row * args.kp;
         const int aligned = first ? args.a.aligned : args.w.aligned;
         for (int k0 = (threadIdx.x & (lanes - 1)) * 16; k0 < args.kp; k0 += lanes * 16) {
-            uint32_t w[4] = {0, 0, 0, 0};
-            if (aligned && k0 + 16 <= args.k) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src + k0));
-                w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (k0 + e < args.k) w[e / 4] |= (uint32_t)(uint8_t)src[k0 + e] << (8 * (e % 4));
-            }
-            const uint2 p0 = widen4(w[0]), p1 = widen4(w[1]), p2 = widen4(w[2]), p3 = widen4(w[3]);
+            const uint4 v = load16(src, k0, args.k, aligned);
+            const uint2 p0 = widen4(v.x), p1 = widen4(v.y), p2 = widen4(v.z), p3 = widen4(v.w);
             uint4 *out = reinterpret_cast<uint4 *>(dst + k0);
             out[0] = make_uint4(p0.x, p0.y, p1.x, p1.y);
             out[1] = make_uint4(p2.x, p2.y, p3.x, p3.y);
@@ -119,12 +100,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap
         " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar_cluster), "r"(c0), "r"(c1)
         : "memory");
-}
-
-// Instruction descriptor of kind::f16 with f16 A and B (format 0), both K-major, fp32 D.
-__host__ __device__ constexpr uint32_t idesc_f16(int m, int n)
-{
-    return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
 __device__ __forceinline__ void give_up(unsigned int bit, volatile int *abort_flag)
@@ -443,19 +418,9 @@ cudaError_t tc_linear_launch(const LinearProblem &p, int sm_count, cudaStream_t 
     }
 }
 
-cudaError_t linear_read_and_clear_error(cudaStream_t stream, unsigned int *out)
+cudaError_t tc_linear_read_and_clear_error(cudaStream_t stream, unsigned int *out)
 {
-    unsigned int host = 0;
-    cudaError_t st = cudaMemcpyFromSymbolAsync(&host, g_linear_error, sizeof host, 0, cudaMemcpyDeviceToHost, stream);
-    if (st == cudaSuccess) st = cudaStreamSynchronize(stream);
-    if (st != cudaSuccess) return st;
-    if (host != 0) {
-        const unsigned int zero = 0;
-        st = cudaMemcpyToSymbolAsync(g_linear_error, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, stream);
-        if (st == cudaSuccess) st = cudaStreamSynchronize(stream);
-    }
-    *out = host;
-    return st;
+    return read_and_clear_word(g_linear_error, stream, out);
 }
 
 }  // namespace cbs

@@ -75,6 +75,22 @@ cudaError_t allow_dynamic_smem(Kernel kernel, int bytes, bool (&done)[kMaxDevice
     return e;
 }
 
+// A kernel translation unit's error word: read and cleared in stream order.
+template <typename Symbol>
+cudaError_t read_and_clear_word(const Symbol &word, cudaStream_t stream, unsigned int *out)
+{
+    unsigned int host = 0;
+    cudaError_t st = cudaMemcpyFromSymbolAsync(&host, word, sizeof host, 0, cudaMemcpyDeviceToHost, stream);
+    if (st == cudaSuccess) st = cudaStreamSynchronize(stream);
+    if (st == cudaSuccess && host != 0) {
+        const unsigned int zero = 0;
+        st = cudaMemcpyToSymbolAsync(word, &zero, sizeof zero, 0, cudaMemcpyHostToDevice, stream);
+        if (st == cudaSuccess) st = cudaStreamSynchronize(stream);
+    }
+    *out = host;
+    return st;
+}
+
 cudaError_t norm_launch(const NormProblem &p, int sm_count, cudaStream_t stream);
 int norm_grad_partial_rows(long long rows, int c, int sm_count);
 cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_t stream);
@@ -86,6 +102,15 @@ cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t str
 // The linear layer on the tensor cores (tc_linear.cu); k == 0 counts as a step of zeros.
 long long tc_linear_workspace_bytes(long long m, int n, int k);
 cudaError_t tc_linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
+cudaError_t tc_linear_read_and_clear_error(cudaStream_t stream, unsigned int *out);
+
+// The linear layer with the weights widened on their way to the tensor cores (tc_linear_stream.cu).
+bool tc_stream_supported(const LinearProblem &p);
+long long tc_stream_workspace_bytes(long long m, int n, int k, int sm_count);
+cudaError_t tc_stream_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
+cudaError_t tc_stream_read_and_clear_error(cudaStream_t stream, unsigned int *out);
+
+// What any of the linear layer's kernels recorded.
 cudaError_t linear_read_and_clear_error(cudaStream_t stream, unsigned int *out);
 
 }  // namespace cbs
