@@ -70,15 +70,16 @@ __device__ __forceinline__ uint4 load16(const int8_t *row, int k0, int k, bool a
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Four int8 of a word -> two words of f16 pairs: biased to 0..255, a byte below 0x64 is the f16
-// 1024 + byte, and subtracting 1152 leaves the value.
+// Four int8 of a word -> two words of f16 pairs, bytes 0 and 2, then 1 and 3 (an order of K that both
+// operands share).  Biased to 0..255, a byte below 0x64 is the f16 1024 + byte, and subtracting 1152
+// leaves the value; the masking, the bias and the 0x64 are one three-input operation.
 __device__ __forceinline__ uint2 widen4(uint32_t w)
 {
-    const uint32_t u = w ^ 0x80808080u;
-    uint32_t lo = __byte_perm(u, 0x64646464u, 0x4140), hi = __byte_perm(u, 0x64646464u, 0x4342);
+    const uint32_t lo = (w & 0x00ff00ffu) ^ 0x64806480u, hi = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
     const __half2 bias = __half2half2(__ushort_as_half((unsigned short)0x6480));
-    __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&lo), bias), b = __hsub2(*reinterpret_cast<__half2 *>(&hi), bias);
-    return make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), bias);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2 *>(&hi), bias);
+    return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
 // Instruction descriptor of kind::f16 with f16 A and B (format 0), both K-major, fp32 D.

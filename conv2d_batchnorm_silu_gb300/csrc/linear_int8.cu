@@ -50,7 +50,7 @@ __device__ __forceinline__ uint4 piece(const int8_t *row, int k0, int k)
 }
 
 template <typename T, int ROWS, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kFewWarps) linear_few_kernel(const LinearArgs a, int split_log2)
+__global__ void __launch_bounds__(32 * kFewWarps, ROWS <= 2 ? 4 : (ROWS <= 4 ? 3 : 2)) linear_few_kernel(const LinearArgs a, int split_log2)
 {
     constexpr int R = kFewChannels;
     __shared__ int part[kFewWarps][R * ROWS];
@@ -67,7 +67,8 @@ __global__ void __launch_bounds__(32 * kFewWarps) linear_few_kernel(const Linear
     for (int i = 0; i < ROWS; ++i) x[i] = a.a + min(i, m - 1) * a.a_stride;
     int acc[R][ROWS] = {};
     const int step = split * 512;
-#pragma unroll 2
+    constexpr int kUnroll = ROWS <= 4 ? 2 : 1;
+#pragma unroll kUnroll
     for (int k0 = ((warp & (split - 1)) * 32 + lane) * 16; k0 < a.k; k0 += step) {
         uint4 wv[R];
 #pragma unroll
@@ -99,11 +100,11 @@ __global__ void __launch_bounds__(32 * kFewWarps) linear_few_kernel(const Linear
 template <typename T, bool ALIGNED>
 cudaError_t linear_few_launch(const LinearArgs &a, int sm_count, cudaStream_t stream)
 {
-    // K is split among warps until an SM has 16 of them or a warp less than one whole pass of K.
+    // K is split among the warps of a block while each has two passes (1 KB) of it: many short blocks
+    // fill the SMs evenly.
+    (void)sm_count;
     int split_log2 = 0;
-    while (split_log2 < 3 && (long long)(a.e.n + kFewChannels - 1) / kFewChannels << split_log2 < 16LL * sm_count &&
-           a.k > 512 << split_log2)
-        ++split_log2;
+    while (split_log2 < 3 && a.k >= 2048 << split_log2) ++split_log2;
     const int per_block = kFewChannels * (kFewWarps >> split_log2);
     const dim3 grid((unsigned)((a.e.n + per_block - 1) / per_block)), block(32 * kFewWarps);
     if (a.e.m == 1) return launch_overlapped(linear_few_kernel<T, 1, ALIGNED>, grid, block, 0, stream, 1, a, split_log2);

@@ -2,7 +2,7 @@
 // count: they are read once as int8 and widened to f16 between global and shared memory.
 //
 // D[channel][row] = W * A^T with 128 channels on the tensor core's M side and NT rows on its N side.
-// Eight warps hold the int8 of the coming steps in registers (kAhead steps of 128 K elements, 48 KB of
+// Sixteen warps hold the int8 of the coming steps in registers (kAhead steps of 128 K elements, 48 KB of
 // weights per SM in flight, whole 128-byte lines of each row), widen a step of weights and rows at a time into swizzled f16 tiles, and hand them
 // to the issuing warp.  Every CTA takes an equal run of the (channel tile, row tile, K step) sequence,
 // so that all SMs read the same share of the weights; a tile whose K steps fall to several CTAs is
@@ -25,7 +25,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far beyond any legitimate w
 
 constexpr int kChannels = 128;  // of a tile
 constexpr int kStep = 128;      // K elements per step: two swizzle spans of f16
-constexpr int kWidenWarps = 8;
+constexpr int kWidenWarps = 16;
 constexpr int kEpiWarps = 4;
 constexpr int kThreads = 32 * (kWidenWarps + kEpiWarps + 1);
 
@@ -36,8 +36,8 @@ struct StreamCfg {
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int STAGES = NT <= 64 ? 4 : (NT <= 128 ? 3 : 2);
     static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
-    static constexpr int ROW_LOADS = NT / 32;  // 16-byte pieces of rows per thread and step
-    static constexpr int kAhead = NT <= 128 ? 3 : 2;  // steps held in registers
+    static constexpr int ROW_LOADS = (NT + 63) / 64;  // 16-byte pieces of rows per thread and step
+    static constexpr int kAhead = NT <= 64 ? 3 : 2;  // steps held in registers
     static constexpr int TMEM_COLS = 2 * NT;
 };
 
@@ -47,8 +47,9 @@ struct StreamArgs {
     long long a_stride, w_stride;
     int k, k_steps;
     int row_tiles, tiles;      // tile = channel tile * row_tiles + row tile
-    long long steps;           // tiles * k_steps
-    int workers;               // CTAs that share them
+    int steps;                 // tiles * k_steps
+    int workers;               // CTAs that share them: run_base steps each, and one more for the first run_extra
+    int run_base, run_extra;
     float *partial;            // [workers + tiles][NT][kChannels]
 };
 
@@ -56,6 +57,24 @@ __device__ __forceinline__ void give_up(unsigned int bit, volatile int *abort_fl
 {
     atomicOr(&g_stream_error, bit);
     *abort_flag = 1;
+}
+
+// One column of the warp's 32 TMEM lanes.
+__device__ __forceinline__ float tmem_ld_one(uint32_t taddr)
+{
+    uint32_t v;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(v)
+                 : "r"(taddr)
+                 : "memory");
+    return __uint_as_float(v);
+}
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // As mbar_wait_bounded; waits here are often a little early, and reading the clock at the first
@@ -68,31 +87,49 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, cons
     return dev::mbar_wait_bounded(bar, parity, abort_flag, timeout_ns);
 }
 
-// One predicated load straight into its registers: behind a branch the value would be moved, and the
-// warp wait for it, where the branches meet.
-__device__ __forceinline__ void load_or_zero(uint4 &v, const int8_t *p, bool exists)
+// What rows of a hold past k.
+__device__ const uint4 g_zeros = {0, 0, 0, 0};
+
+// A predicated load straight into its registers, which otherwise keep what they hold.
+__device__ __forceinline__ void load_unless(uint4 &v, const int8_t *p, bool skip)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "setp.eq.b32 p, %5, 0;\n\t"
         "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-        : "l"(p), "r"((int)exists));
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "l"(p), "r"((int)skip));
+}
+
+// As sts_v4, at a constant distance from a base.
+template <int OFFSET>
+__device__ __forceinline__ void sts_v4_at(uint32_t base, const uint2 &lo, const uint2 &hi)
+{
+    asm volatile("st.shared.v4.b32 [%0+%5], {%1, %2, %3, %4};" ::"r"(base), "r"(lo.x), "r"(lo.y), "r"(hi.x), "r"(hi.y),
+                 "n"(OFFSET)
+                 : "memory");
+}
+
+template <int OFFSET>
+__device__ __forceinline__ void widen_to(uint32_t at0, uint32_t at1, const uint4 &v)
+{
+    sts_v4_at<OFFSET>(at0, widen4(v.x), widen4(v.y));
+    sts_v4_at<OFFSET>(at1, widen4(v.z), widen4(v.w));
 }
 
 // First step of worker b's run, and the worker that has step g.
-__device__ __forceinline__ long long run_start(const StreamArgs &a, int b) { return a.steps * b / a.workers; }
-__device__ __forceinline__ int worker_of(const StreamArgs &a, long long g)
+__device__ __forceinline__ int run_start(const StreamArgs &a, int b) { return b * a.run_base + min(b, a.run_extra); }
+__device__ __forceinline__ int worker_of(const StreamArgs &a, int g)
 {
-    return (int)(((g + 1) * a.workers - 1) / a.steps);
+    const int longer = a.run_extra * (a.run_base + 1);  // steps of the longer runs
+    return g < longer ? g / (a.run_base + 1) : a.run_extra + (g - longer) / a.run_base;
 }
 
 template <typename T, int NT>
 __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const StreamArgs a)
 {
     using C = StreamCfg<NT>;
-    constexpr int STAGES = C::STAGES, AHEAD = C::kAhead, LOADS = 4 + C::ROW_LOADS;
+    constexpr int STAGES = C::STAGES, AHEAD = C::kAhead, LOADS = 2 + C::ROW_LOADS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -125,80 +162,90 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     __syncthreads();
     dev::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
-    const long long g0 = run_start(a, blockIdx.x), g1 = run_start(a, blockIdx.x + 1);
+    const int g0 = run_start(a, blockIdx.x), steps = run_start(a, blockIdx.x + 1) - g0;
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
 
     if (warp < kWidenWarps) {
         // ---------------------------------------------------------- loads and widening
-        // Piece j of this thread: 16 bytes of K from 16 * (tid % 8) of weights rows tid / 8 + 32 j for
-        // j < 4, then of rows of a.
+        // Piece j of this thread: 16 bytes of K from 16 * (tid % 8) of weights rows tid / 8 + 64 j for
+        // j < 2, then of rows of a.  Rows past the end read the last one: nothing stores what they give.
+        // Past k (a multiple of 16) rows of a are zeros and the weights any values; past the run, too.
         const int tid = threadIdx.x, q = tid & 7, r8 = tid >> 3;
-        int tile = (int)(g0 / a.k_steps), ks = (int)(g0 - (long long)tile * a.k_steps);  // of the next load
-        const int8_t *w0 = nullptr, *a0 = nullptr;  // of piece 0 of either
-        int w_count = 0, a_count = 0;               // pieces whose row exists; the others read as zeros
+        int tile = g0 / a.k_steps, ks = g0 - tile * a.k_steps, unloaded = steps;  // of the next load
+        const bool has_row = NT >= 64 || r8 < NT;
+        const bool cut = (a.k_steps - 1) * kStep + q * 16 >= a.k;  // this thread's part of a last step is past k
+        const int8_t *src[LOADS];
         auto rows_of_tile = [&]() {
-            const int ct = tile / a.row_tiles, rt = tile - ct * a.row_tiles;
-            const int n = ct * kChannels + r8;
-            const long long m = (long long)rt * NT + r8;
-            w0 = a.w + n * a.w_stride;
-            a0 = a.a + m * a.a_stride;
-            w_count = n < a.e.n ? (a.e.n - n + 31) / 32 : 0;
-            a_count = m < a.e.m ? (int)((a.e.m - m + 31) / 32) : 0;
+            const int ct = tile / a.row_tiles, rt = tile - ct * a.row_tiles, k0 = ks * kStep + q * 16;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                src[j] = a.w + (long long)min(ct * kChannels + j * 64 + r8, a.e.n - 1) * a.w_stride + k0;
+#pragma unroll
+            for (int j = 0; j < C::ROW_LOADS; ++j)
+                src[2 + j] = a.a + (long long)min(rt * NT + j * 64 + r8, (int)a.e.m - 1) * a.a_stride + k0;
         };
         rows_of_tile();
         uint4 held[AHEAD][LOADS];
-        long long loaded = g0;
         auto load = [&](uint4 (&to)[LOADS]) {
-            const int k0 = ks * kStep + q * 16;
-            const bool any = loaded < g1 && k0 < a.k;  // k is a multiple of 16
+            if (unloaded <= 0) return;  // what is held is not used again
+            --unloaded;
+            const bool past = cut && ks == a.k_steps - 1;
 #pragma unroll
-            for (int j = 0; j < LOADS; ++j) {
-                const bool exists = any && (j < 4 ? j < w_count : j - 4 < a_count);
-                const int8_t *src = j < 4 ? w0 + j * 32 * a.w_stride : a0 + (j - 4) * 32 * a.a_stride;
-                load_or_zero(to[j], src + k0, exists);
+            for (int j = 0; j < 2; ++j) {
+                load_unless(to[j], src[j], past);
+                src[j] += kStep;
             }
-            ++loaded;
-            if (++ks == a.k_steps && loaded < g1) {
+            if (has_row)
+#pragma unroll
+                for (int j = 0; j < C::ROW_LOADS; ++j) {
+                    load_unless(to[2 + j], past ? reinterpret_cast<const int8_t *>(&g_zeros) : src[2 + j], false);
+                    src[2 + j] += kStep;
+                }
+            if (++ks == a.k_steps) {
                 ks = 0;
                 ++tile;
                 rows_of_tile();
             }
         };
 #pragma unroll
-        for (int d = 0; d < AHEAD; ++d) load(held[d]);
+        for (int d = 0; d < AHEAD; ++d) {
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) held[d][j] = make_uint4(0, 0, 0, 0);
+            load(held[d]);
+        }
+        // Bytes 16 q .. 16 q + 15 become two f16 pieces of the row's 256 bytes, in the first span (q < 4) or
+        // the second.  The second span holds each two pieces in the other order, for weights and rows alike:
+        // the sum is the same, and eight lanes of a row meet eight different banks.
+        const uint32_t span = (uint32_t)q >> 2, pair = ((uint32_t)q & 3u) * 2, turn = (uint32_t)r8 & 7u;
+        const uint32_t o0 = (uint32_t)r8 * 128 + (((pair + span) ^ turn) << 4);
+        const uint32_t o1 = (uint32_t)r8 * 128 + (((pair + (span ^ 1u)) ^ turn) << 4);
+        const uint32_t ta0 = dev::smem_u32(sm_a) + span * (C::A_BYTES / 2), tb0 = dev::smem_u32(sm_b) + span * (C::B_BYTES / 2);
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (long long g = g0; g < g1 && ok; g += AHEAD) {
+        for (int left = steps; left > 0 && ok; left -= AHEAD) {
 #pragma unroll
             for (int d = 0; d < AHEAD; ++d) {
-                if (g + d >= g1 || !ok) break;
+                if (d >= left) break;
                 ok = __all_sync(0xffffffffu, wait_bounded(dev::smem_u32(&empty[stage]), phase ^ 1u,
                                                                     abort_flag, kWaitNs));
                 if (!ok) {
                     if (lane == 0 && !*abort_flag) give_up(kErrTimeoutProducer, abort_flag);
                     break;
                 }
-                const uint32_t ta = dev::smem_u32(sm_a + stage * C::A_BYTES);
-                const uint32_t tb = dev::smem_u32(sm_b + stage * C::B_BYTES);
-                // Bytes 16 q .. 16 q + 15 become the f16 pieces 2 q and 2 q + 1 of the row's 256 bytes, in the
-                // first span (q < 4) or the second; the two spans take them in the other order, so that eight
-                // lanes of a row meet eight different banks.
-                const uint32_t swap = (uint32_t)q >> 2, piece = ((uint32_t)q & 3u) * 2, turn = (uint32_t)r8 & 7u;
-                const uint32_t o0 = ((piece + swap) ^ turn) << 4, o1 = ((piece + (swap ^ 1u)) ^ turn) << 4;
-#pragma unroll
-                for (int j = 0; j < LOADS; ++j) {
-                    const uint32_t row = (uint32_t)((j < 4 ? j : j - 4) * 32 + r8);
-                    const uint4 v = held[d][j];
-                    const uint2 p0 = widen4(v.x), p1 = widen4(v.y), p2 = widen4(v.z), p3 = widen4(v.w);
-                    const uint4 lo = make_uint4(p0.x, p0.y, p1.x, p1.y), hi = make_uint4(p2.x, p2.y, p3.x, p3.y);
-                    const uint4 first = swap ? hi : lo, second = swap ? lo : hi;
-                    const uint32_t at = (j < 4 ? ta + swap * (C::A_BYTES / 2) : tb + swap * (C::B_BYTES / 2)) + row * 128;
-                    dev::sts_v4(at + o0, first.x, first.y, first.z, first.w);
-                    dev::sts_v4(at + o1, second.x, second.y, second.z, second.w);
+                const uint32_t ta = ta0 + (uint32_t)(stage * C::A_BYTES), tb = tb0 + (uint32_t)(stage * C::B_BYTES);
+                widen_to<0>(ta + o0, ta + o1, held[d][0]);
+                widen_to<64 * 128>(ta + o0, ta + o1, held[d][1]);
+                if (has_row) {
+                    widen_to<0>(tb + o0, tb + o1, held[d][2]);
+                    if constexpr (C::ROW_LOADS > 1) widen_to<64 * 128>(tb + o0, tb + o1, held[d][3]);
+                    if constexpr (C::ROW_LOADS > 2) {
+                        widen_to<128 * 128>(tb + o0, tb + o1, held[d][4]);
+                        widen_to<192 * 128>(tb + o0, tb + o1, held[d][5]);
+                    }
                 }
-                dev::fence_proxy_async_shared();
+                dev::fence_proxy_async_shared();  // the tensor core reads through the async proxy
                 __syncwarp();
                 if (lane == 0) dev::mbar_arrive(dev::smem_u32(&full[stage]));
                 load(held[d]);
@@ -207,64 +254,65 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------- MMAs
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_f16(kChannels, NT);
-            const uint64_t desc_a = dev::smem_desc_kmajor(dev::smem_u32(sm_a), 128);
-            const uint64_t desc_b = dev::smem_desc_kmajor(dev::smem_u32(sm_b), 128);
-            int stage = 0, piece = 0;
-            uint32_t phase = 0;
+        // The whole warp runs the loop and one elected lane issues: with the control flow uniform, descriptors
+        // are computed and held in uniform registers, which an MMA takes as they are (49 clocks an MMA among
+        // busy warps, against 71 issued behind `lane == 0`).
+        const bool issuer = elect_one();
+        constexpr uint32_t idesc = idesc_f16(kChannels, NT);
+        const uint64_t desc_a = dev::smem_desc_kmajor(dev::smem_u32(sm_a), 128);
+        const uint64_t desc_b = dev::smem_desc_kmajor(dev::smem_u32(sm_b), 128);
+        int stage = 0, piece = 0, ks = g0 % a.k_steps;
+        uint32_t phase = 0, accumulate = 0;
+        for (int g = 0; g < steps; ++g) {
+            const int buf = piece & 1;
             bool ok = true;
-            int ks = (int)(g0 % a.k_steps);
-            bool start = true;
-            for (long long g = g0; g < g1; ++g) {
-                const int buf = piece & 1;
-                if (start) {
-                    if (!wait_bounded(dev::smem_u32(&tempty[buf]), ((uint32_t)(piece >> 1) & 1u) ^ 1u,
-                                                abort_flag, kWaitNs)) {
-                        if (!*abort_flag) give_up(kErrTimeoutMma, abort_flag);
-                        break;
-                    }
-                }
-                ok = wait_bounded(dev::smem_u32(&full[stage]), phase, abort_flag, kWaitNs);
-                if (!ok) {
-                    if (!*abort_flag) give_up(kErrTimeoutMma, abort_flag);
-                    break;
-                }
-                dev::tc_fence_after_sync();
-                const uint64_t da = desc_a + (uint64_t)(stage * (C::A_BYTES >> 4));
-                const uint64_t db = desc_b + (uint64_t)(stage * (C::B_BYTES >> 4));
-                const uint32_t d = tmem + (uint32_t)(buf * NT);
+            if (accumulate == 0)
+                ok = wait_bounded(dev::smem_u32(&tempty[buf]), ((uint32_t)(piece >> 1) & 1u) ^ 1u, abort_flag, kWaitNs);
+            ok = ok && wait_bounded(dev::smem_u32(&full[stage]), phase, abort_flag, kWaitNs);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (issuer && !*abort_flag) give_up(kErrTimeoutMma, abort_flag);
+                break;
+            }
+            dev::tc_fence_after_sync();
+            const uint64_t da = desc_a + (uint64_t)(stage * (C::A_BYTES >> 4));
+            const uint64_t db = desc_b + (uint64_t)(stage * (C::B_BYTES >> 4));
+            const uint32_t d = tmem + (uint32_t)(buf * NT);
+            const bool last = ++ks == a.k_steps || g + 1 == steps;
+            if (issuer) {
 #pragma unroll
                 for (int kk = 0; kk < kStep / 16; ++kk) {
                     const uint64_t span = (uint64_t)(kk / 4), in = (uint64_t)(2 * (kk % 4));
                     dev::tc_mma_bf16<1>(d, da + span * (C::A_BYTES / 2 >> 4) + in, db + span * (C::B_BYTES / 2 >> 4) + in,
-                                        idesc, !start || kk > 0 ? 1u : 0u);
+                                        idesc, kk > 0 ? 1u : accumulate);
                 }
                 dev::tc_commit<1>(dev::smem_u32(&empty[stage]));
-                if (++stage == STAGES) stage = 0, phase ^= 1u;
-                start = false;
-                if (++ks == a.k_steps || g + 1 == g1) {
-                    dev::tc_commit<1>(dev::smem_u32(&tfull[buf]));
-                    ks = 0;
-                    ++piece;
-                    start = true;
-                }
+                if (last) dev::tc_commit<1>(dev::smem_u32(&tfull[buf]));
             }
-            // Every MMA must have finished before tensor memory is freed.
+            __syncwarp();
+            if (++stage == STAGES) stage = 0, phase ^= 1u;
+            accumulate = 1;
+            if (last) {
+                ks = 0;
+                ++piece;
+                accumulate = 0;
+            }
+        }
+        // Every MMA must have finished before tensor memory is freed.
+        if (issuer) {
             dev::tc_commit<1>(dev::smem_u32(drain));
-            if (!wait_bounded(dev::smem_u32(drain), 0, nullptr, kWaitNs)) give_up(kErrTimeoutDrain, abort_flag);
+            if (!dev::mbar_wait_bounded(dev::smem_u32(drain), 0, nullptr, kWaitNs)) give_up(kErrTimeoutDrain, abort_flag);
         }
         __syncwarp();
     } else {
         // ---------------------------------------------------------- epilogue: lane = channel, column = row of a
+        // This code runs once or twice a launch, so it is kept short: fetching it is what would take time.
         const int quarter = warp & 3;
-        int piece = 0;
-        for (long long g = g0; g < g1; ++piece) {
-            const int tile = (int)(g / a.k_steps), ks = (int)(g - (long long)tile * a.k_steps);
-            const long long end = g + (a.k_steps - ks) < g1 ? g + (a.k_steps - ks) : g1;
-            const bool whole = ks == 0 && end - g == a.k_steps;
+        int tile = g0 / a.k_steps, ks = g0 - tile * a.k_steps;
+        for (int piece = 0, left = steps; left > 0; ++piece, ++tile, ks = 0) {
+            const int take = min(left, a.k_steps - ks), buf = piece & 1;
+            left -= take;
             const int ct = tile / a.row_tiles, rt = tile - ct * a.row_tiles;
-            const int buf = piece & 1;
+            const int rows = min(NT, (int)a.e.m - rt * NT), n = ct * kChannels + quarter * 32 + lane;
             int ok = 1;
             if (lane == 0)
                 ok = wait_bounded(dev::smem_u32(&tfull[buf]), (uint32_t)(piece >> 1) & 1u, abort_flag, kWaitNs);
@@ -275,27 +323,27 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
             }
             dev::tc_fence_after_sync();
             const uint32_t taddr = tmem + (uint32_t)(buf * NT) + ((uint32_t)(quarter * 32) << 16);
-            const long long m0 = (long long)rt * NT;
-            const int n = ct * kChannels + quarter * 32 + lane;
-            float *out = a.partial + ((long long)(blockIdx.x + tile) * NT) * kChannels + quarter * 32 + lane;
-            for (int c = 0; c < NT && m0 + c < a.e.m; c += 16) {
-                uint32_t v[16];
-                dev::tmem_ld_32x32b_x16(taddr + (uint32_t)c, v);
-                dev::tmem_ld_wait();
-                dev::reg_fence16(v);
+            if (take < a.k_steps) {
+                float *out = a.partial + ((long long)(blockIdx.x + tile) * NT) * kChannels + quarter * 32 + lane;
+#pragma unroll 1
+                for (int c = 0; c < rows; c += 16) {
+                    uint32_t v[16];
+                    dev::tmem_ld_32x32b_x16(taddr + (uint32_t)c, v);
+                    dev::tmem_ld_wait();
+                    dev::reg_fence16(v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (m0 + c + i >= a.e.m) continue;
-                    if (!whole)
-                        out[(c + i) * kChannels] = __uint_as_float(v[i]);
-                    else if (n < a.e.n)
-                        finish_one<T>(a.e, __uint_as_float(v[i]), m0 + c + i, n);
+                    for (int i = 0; i < 16; ++i) out[(c + i) * kChannels] = __uint_as_float(v[i]);  // within NT rows
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < rows; ++c) {
+                    const float sum = tmem_ld_one(taddr + (uint32_t)c);
+                    if (n < a.e.n) finish_one<T>(a.e, sum, (long long)rt * NT + c, n);
                 }
             }
             dev::tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) dev::mbar_arrive(dev::smem_u32(&tempty[buf]));
-            g = end;
         }
     }
     dev::tc_fence_before_sync();
@@ -315,7 +363,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) linear_join_kernel(const Strea
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
     const int tile = blockIdx.x;
-    const long long g = (long long)tile * a.k_steps;
+    const int g = tile * a.k_steps;
     const int b0 = worker_of(a, g), b1 = worker_of(a, g + a.k_steps - 1);
     if (b0 == b1) return;  // finished by the worker itself
     const int ct = tile / a.row_tiles, rt = tile - ct * a.row_tiles;
@@ -345,7 +393,7 @@ int row_tile_of(long long m) { return m <= 32 ? 32 : (m <= 64 ? 64 : (m <= 128 ?
 
 struct StreamPlan {
     int nt, k_steps, row_tiles, tiles, workers;
-    long long steps;
+    int steps;
 };
 
 StreamPlan plan_of(long long m, int n, int k, int sm_count)
@@ -355,10 +403,10 @@ StreamPlan plan_of(long long m, int n, int k, int sm_count)
     p.k_steps = k > 0 ? (k + kStep - 1) / kStep : 1;
     p.row_tiles = (int)((m + p.nt - 1) / p.nt);
     p.tiles = (n + kChannels - 1) / kChannels * p.row_tiles;
-    p.steps = (long long)p.tiles * p.k_steps;
+    p.steps = p.tiles * p.k_steps;
     const int fewest = p.k_steps > 32 ? (p.k_steps + 15) / 16 : 2;
-    const long long most = p.steps / fewest > 0 ? p.steps / fewest : 1;
-    p.workers = (int)(most < sm_count ? most : sm_count);
+    const int most = p.steps / fewest > 0 ? p.steps / fewest : 1;
+    p.workers = most < sm_count ? most : sm_count;
     return p;
 }
 
@@ -372,7 +420,7 @@ cudaError_t stream_launch(const StreamArgs &a, cudaStream_t stream)
     e = launch_overlapped(linear_stream_kernel<T, NT>, dim3((unsigned)a.workers), dim3(kThreads), (size_t)C::SMEM, stream,
                           1, a);
     // Equal runs that are whole tiles leave nothing to join.
-    if (e != cudaSuccess || (a.steps % a.workers == 0 && a.steps / a.workers % a.k_steps == 0)) return e;
+    if (e != cudaSuccess || (a.run_extra == 0 && a.run_base % a.k_steps == 0)) return e;
     const int rows = (int)(a.e.m < NT ? a.e.m : NT);
     return launch_overlapped(linear_join_kernel<T, NT>, dim3((unsigned)a.tiles, (unsigned)((rows + kJoinRows - 1) / kJoinRows)),
                              dim3(32, kJoinRows), 0, stream, 1, a);
@@ -418,6 +466,8 @@ cudaError_t tc_stream_launch(const LinearProblem &p, int sm_count, cudaStream_t 
     a.tiles = plan.tiles;
     a.steps = plan.steps;
     a.workers = plan.workers;
+    a.run_base = plan.steps / plan.workers;
+    a.run_extra = plan.steps % plan.workers;
     a.partial = static_cast<float *>(p.workspace);
     switch (p.out_dtype) {
     case kF32: return stream_launch_t<float>(a, plan.nt, stream);
