@@ -21,7 +21,6 @@ struct LinearEpilogue {
     long long m;
     int n;
     int activation;
-    int vec_params;    // w_scale and bias 16-byte aligned
     int vec_y;         // rows of y 16-byte aligned
     int vec_residual;  // rows of the residual 16-byte aligned
 };
@@ -43,7 +42,6 @@ inline LinearEpilogue linear_epilogue_of(const LinearProblem &p)
     e.m = p.m;
     e.n = p.n;
     e.activation = p.activation;
-    e.vec_params = reinterpret_cast<uintptr_t>(p.w_scale) % 16 == 0 && reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
     e.vec_y = rows16(p.y);
     e.vec_residual = rows16(p.residual);
     return e;
@@ -82,6 +80,23 @@ __device__ __forceinline__ uint2 widen4(uint32_t w)
     return make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
 }
 
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// As mbar_wait_bounded; waits here are often a little early, and reading the clock at the first
+// unsuccessful poll would cost more than most of them last.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, const volatile int *abort_flag,
+                                             uint64_t timeout_ns)
+{
+    for (int i = 0; i < 64; ++i)
+        if (dev::mbar_try_wait(bar, parity)) return true;
+    return dev::mbar_wait_bounded(bar, parity, abort_flag, timeout_ns);
+}
+
 // Instruction descriptor of kind::f16 with f16 A and B (format 0), both K-major, fp32 D.
 __host__ __device__ constexpr uint32_t idesc_f16(int m, int n)
 {
@@ -94,6 +109,13 @@ __device__ __forceinline__ float activated(float z, int activation)
     if (activation == CBS_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
     if (activation == CBS_ACT_RELU) return z < 0.0f ? 0.0f : z;  // keeps NaN
     return z;
+}
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // One output: the general form.
@@ -126,39 +148,84 @@ __device__ __forceinline__ float2 unpack2(uint32_t w, __half)
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
+// min(a, b, c); a NaN among them is the result.
+__device__ __forceinline__ float least_of(float a, float b, float c)
+{
+    float m;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
+
+// SiLU of 32 values, two at a time with one reciprocal between them, 1/a = b * (1 / (a b)): three
+// special-function operations a pair instead of four, which set the pace.  Values of -43 and below, for
+// which a b could leave the range, and NaN, which would spread to its neighbour, take the single form.
+__device__ __forceinline__ void silu32(float *v)
+{
+    float least = v[0];
+#pragma unroll
+    for (int i = 1; i < 31; i += 2) least = least_of(least, v[i], v[i + 1]);
+    least = least_of(least, v[31], v[31]);
+    if (__all_sync(0xffffffffu, least > -43.0f)) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float2 z = make_float2(v[i], v[i + 1]);
+            const float2 t = __fmul2_rn(z, make_float2(-1.44269504f, -1.44269504f));
+            const float2 s = __fadd2_rn(make_float2(exp2_approx(t.x), exp2_approx(t.y)), make_float2(1.0f, 1.0f));
+            const float r = __fdividef(1.0f, s.x * s.y);
+            const float2 y = __fmul2_rn(z, __fmul2_rn(make_float2(s.y, s.x), make_float2(r, r)));
+            v[i] = y.x;
+            v[i + 1] = y.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = activated(v[i], CBS_ACT_SILU);
+    }
+}
+
+// Scales, then biases, of `count` columns from col0 into `dst` in shared memory, by one warp; zeros past
+// the end.
+__device__ __forceinline__ void stage_params(const LinearEpilogue &e, int col0, int count, uint32_t dst, int lane)
+{
+    for (int i = lane; i < count; i += 32) {
+        const bool in = col0 + i < e.n;
+        const float s = in ? __ldg(e.w_scale + col0 + i) : 0.0f, b = in && e.bias ? __ldg(e.bias + col0 + i) : 0.0f;
+        dev::sts_u32(dst + 4 * i, __float_as_uint(s));
+        dev::sts_u32(dst + 4 * (count + i), __float_as_uint(b));
+    }
+    __syncwarp();
+}
+
 // A warp's block of 32 rows x 32 columns from (row0, col0): lane l holds row row0 + l, its 32 sums in
 // v.  Rows and columns past the end are computed and not stored.  `stg` is the warp's own 32 x 32
 // elements of shared memory, through which lanes exchange rows for columns, so that each store covers
-// whole runs of a row; 16-byte pieces are swizzled so that neither direction meets a bank twice.
+// whole runs of a row; 16-byte pieces are swizzled so that neither direction meets a bank twice.  The
+// block's scales are in shared memory at `scales`, its biases at `biases`.
 template <typename T>
-__device__ __forceinline__ void finish_block(const LinearEpilogue &e, float *v, float row_scale, long long row0,
-                                             int col0, uint32_t stg, int lane)
+__device__ __forceinline__ void finish_block(const LinearEpilogue &e, const uint32_t *sums, uint32_t scales,
+                                             uint32_t biases, float row_scale, long long row0, int col0, uint32_t stg, int lane)
 {
     constexpr int kPieces = 32 * sizeof(T) / 16;      // 16-byte pieces of a row
     constexpr int kPer = 16 / sizeof(T);              // elements of a piece
     const bool whole = col0 + 32 <= e.n;
     const long long row = row0 + lane;
-    if (whole && e.vec_params) {
+    float v[32];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-            const float4 s = __ldg(reinterpret_cast<const float4 *>(e.w_scale + col0 + i));
-            float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (e.bias) b = __ldg(reinterpret_cast<const float4 *>(e.bias + col0 + i));
-            v[i] = fmaf(v[i], row_scale * s.x, b.x);
-            v[i + 1] = fmaf(v[i + 1], row_scale * s.y, b.y);
-            v[i + 2] = fmaf(v[i + 2], row_scale * s.z, b.z);
-            v[i + 3] = fmaf(v[i + 3], row_scale * s.w, b.w);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const int c = col0 + i < e.n ? col0 + i : e.n - 1;
-            v[i] = fmaf(v[i], row_scale * __ldg(e.w_scale + c), e.bias ? __ldg(e.bias + c) : 0.0f);
-        }
+    for (int i = 0; i < 8; ++i) {
+        const uint4 s = dev::lds_v4(scales + 16 * i), b = dev::lds_v4(biases + 16 * i);
+        const float2 r = make_float2(row_scale, row_scale);
+        const float2 lo = __ffma2_rn(make_float2(__uint_as_float(sums[4 * i]), __uint_as_float(sums[4 * i + 1])),
+                                     __fmul2_rn(r, make_float2(__uint_as_float(s.x), __uint_as_float(s.y))),
+                                     make_float2(__uint_as_float(b.x), __uint_as_float(b.y)));
+        const float2 hi = __ffma2_rn(make_float2(__uint_as_float(sums[4 * i + 2]), __uint_as_float(sums[4 * i + 3])),
+                                     __fmul2_rn(r, make_float2(__uint_as_float(s.z), __uint_as_float(s.w))),
+                                     make_float2(__uint_as_float(b.z), __uint_as_float(b.w)));
+        v[4 * i] = lo.x;
+        v[4 * i + 1] = lo.y;
+        v[4 * i + 2] = hi.x;
+        v[4 * i + 3] = hi.y;
     }
     if (e.activation == CBS_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = activated(v[i], CBS_ACT_SILU);
+        silu32(v);
     } else if (e.activation == CBS_ACT_RELU) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = activated(v[i], CBS_ACT_RELU);
@@ -207,12 +274,15 @@ __device__ __forceinline__ void finish_block(const LinearEpilogue &e, float *v, 
     __syncwarp();
     T *y = static_cast<T *>(e.y) + row0 * e.y_stride + col0;
     if (whole && e.vec_y) {
+        uint4 w[kPieces];  // all loaded before the first is stored
+        const int q = lane % kPieces, r0 = lane / kPieces, rows = e.m - row0 < 32 ? (int)(e.m - row0) : 32;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-            const int r = i * (32 / kPieces) + lane / kPieces, q = lane % kPieces;
-            const uint4 w = dev::lds_v4(at(r, q));
-            if (row0 + r < e.m) *reinterpret_cast<uint4 *>(y + r * e.y_stride + q * kPer) = w;
-        }
+        for (int i = 0; i < kPieces; ++i) w[i] = dev::lds_v4(at(i * (32 / kPieces) + r0, q));
+        T *to = y + r0 * e.y_stride + q * kPer;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            if (i * (32 / kPieces) + r0 < rows)
+                *reinterpret_cast<uint4 *>(to + i * (32 / kPieces) * e.y_stride) = w[i];
     } else if (col0 + lane < e.n) {
         for (int r = 0; r < 32 && row0 + r < e.m; ++r) {
             const uint32_t addr = at(r, lane / kPer) + (uint32_t)(lane % kPer * (int)sizeof(T));

@@ -70,13 +70,15 @@ constexpr int kThreads = 128 + 32 * kEpiWarps;
 
 // BN output channels per tile.  PAIR: two CTAs of a cluster work as one on 256 rows, each
 // holding its 128 rows and half of the weight tile.
-template <int BN, bool PAIR>
+// SIZE: bytes of an output element.
+template <int BN, bool PAIR, int SIZE>
 struct GemmCfg {
     static constexpr int B_ROWS = PAIR ? BN / 2 : BN;
     static constexpr int A_BYTES = kBlockM * kBlockK * 2;
     static constexpr int B_BYTES = B_ROWS * kBlockK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int STG_WARP = 32 * 32 * 4;  // 32 rows x 32 columns, fp32 at most
+    static constexpr int STG_BLOCK = 32 * 32 * SIZE;              // an epilogue warp's block on its way out
+    static constexpr int STG_WARP = STG_BLOCK + 2 * (BN / 2) * 4;  // and the scales and biases of its columns
     static constexpr int STG = kEpiWarps * STG_WARP;
     static constexpr int FIT = (232448 - 1024 - 512 - STG) / STAGE;
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
@@ -108,6 +110,13 @@ __device__ __forceinline__ void give_up(unsigned int bit, volatile int *abort_fl
     *abort_flag = 1;
 }
 
+// Arrival on a barrier of the pair, which only orders the tensor memory reads fenced before it: without
+// cluster scope, which would wait for the warp's earlier stores to global memory.
+__device__ __forceinline__ void arrive_remote(uint32_t bar_cluster)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // Tile t in bands of eight row tiles, channel tiles within a band, row tiles fastest: the tiles in
 // flight at one time share both operands in L2.
 __device__ __forceinline__ void tile_at(const GemmArgs &a, int t, int &mt, int &nt)
@@ -123,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_w,
                        const GemmArgs a)
 {
-    using C = GemmCfg<BN, PAIR>;
+    using C = GemmCfg<BN, PAIR, sizeof(T)>;
     constexpr int CG = PAIR ? 2 : 1, STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -217,7 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMAs
-        if (lane == 0 && rank == 0) {
+        // The whole warp runs the loop and one elected lane issues: with the control flow uniform, descriptors
+        // are computed and held in uniform registers, which an MMA takes as they are.
+        if (rank == 0) {
+            const bool issuer = elect_one();
             constexpr uint32_t idesc = idesc_f16(CG * kBlockM, BN);
             const uint64_t desc_a = dev::smem_desc_kmajor(dev::smem_u32(sm_a), 128);
             const uint64_t desc_b = dev::smem_desc_kmajor(dev::smem_u32(sm_b), 128);
@@ -226,47 +238,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = vb; t < a.tiles && ok; t += vg, ++lt) {
                 const int buf = lt & 1;
-                if (!dev::mbar_wait_bounded(dev::smem_u32(&tempty[buf]), ((uint32_t)(lt >> 1) & 1u) ^ 1u, abort_flag,
-                                            kWaitNs)) {
-                    if (!*abort_flag) give_up(kErrTimeoutMma, abort_flag);
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, wait_bounded(dev::smem_u32(&tempty[buf]), ((uint32_t)(lt >> 1) & 1u) ^ 1u,
+                                                          abort_flag, kWaitNs));
                 dev::tc_fence_after_sync();
                 const uint32_t d = tmem + (uint32_t)(buf * BN);
-                for (int it = 0; it < a.k_iters; ++it) {
-                    if (!dev::mbar_wait_bounded(dev::smem_u32(&full[stage]), phase, abort_flag, kWaitNs)) {
-                        if (!*abort_flag) give_up(kErrTimeoutMma, abort_flag);
-                        ok = false;
-                        break;
-                    }
+                for (int it = 0; it < a.k_iters && ok; ++it) {
+                    ok = __all_sync(0xffffffffu, wait_bounded(dev::smem_u32(&full[stage]), phase, abort_flag, kWaitNs));
+                    if (!ok) break;
                     dev::tc_fence_after_sync();
                     const uint64_t da = desc_a + (uint64_t)(stage * (C::A_BYTES >> 4));
                     const uint64_t db = desc_b + (uint64_t)(stage * (C::B_BYTES >> 4));
+                    if (issuer) {
 #pragma unroll
-                    for (int kk = 0; kk < kBlockK / 16; ++kk)
-                        dev::tc_mma_bf16<CG>(d, da + (uint64_t)(2 * kk), db + (uint64_t)(2 * kk), idesc,
-                                             it > 0 || kk > 0 ? 1u : 0u);
-                    if constexpr (PAIR)
-                        dev::tc_commit_multicast<CG>(dev::smem_u32(&empty[stage]), (uint16_t)0x3);
-                    else
-                        dev::tc_commit<CG>(dev::smem_u32(&empty[stage]));
+                        for (int kk = 0; kk < kBlockK / 16; ++kk)
+                            dev::tc_mma_bf16<CG>(d, da + (uint64_t)(2 * kk), db + (uint64_t)(2 * kk), idesc,
+                                                 it > 0 || kk > 0 ? 1u : 0u);
+                        if constexpr (PAIR)
+                            dev::tc_commit_multicast<CG>(dev::smem_u32(&empty[stage]), (uint16_t)0x3);
+                        else
+                            dev::tc_commit<CG>(dev::smem_u32(&empty[stage]));
+                        if (it + 1 == a.k_iters) {
+                            if constexpr (PAIR)
+                                dev::tc_commit_multicast<CG>(dev::smem_u32(&tfull[buf]), (uint16_t)0x3);
+                            else
+                                dev::tc_commit<CG>(dev::smem_u32(&tfull[buf]));
+                        }
+                    }
+                    __syncwarp();
                     if (++stage == STAGES) stage = 0, phase ^= 1u;
                 }
-                if (!ok) break;
-                if constexpr (PAIR)
-                    dev::tc_commit_multicast<CG>(dev::smem_u32(&tfull[buf]), (uint16_t)0x3);
-                else
-                    dev::tc_commit<CG>(dev::smem_u32(&tfull[buf]));
+                if (!ok && issuer && !*abort_flag) give_up(kErrTimeoutMma, abort_flag);
             }
             // Every MMA must have finished before tensor memory is freed.
-            dev::tc_commit<CG>(dev::smem_u32(drain));
-            if (!dev::mbar_wait_bounded(dev::smem_u32(drain), 0, nullptr, kWaitNs)) give_up(kErrTimeoutDrain, abort_flag);
+            if (issuer) {
+                dev::tc_commit<CG>(dev::smem_u32(drain));
+                if (!dev::mbar_wait_bounded(dev::smem_u32(drain), 0, nullptr, kWaitNs))
+                    give_up(kErrTimeoutDrain, abort_flag);
+            }
         }
         __syncwarp();
     } else if (warp >= 4) {
         // ---------------------------------------------------------- epilogue
         const int quarter = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t stg = dev::smem_u32(sm_stg + (warp - 4) * C::STG_WARP);
+        const uint32_t stg = dev::smem_u32(sm_stg + (warp - 4) * C::STG_WARP), params = stg + C::STG_BLOCK;
         int lt = 0;
         for (int t = vb; t < a.tiles; t += vg, ++lt) {
             int mt, nt;
@@ -274,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int buf = lt & 1;
             const long long row0 = (long long)(mt * CG + rank) * kBlockM + quarter * 32;
             const float row_scale = row0 + lane < a.e.m ? __ldg(a.e.a_scale + row0 + lane) : 0.0f;
+            stage_params(a.e, nt * BN + half * (BN / 2), BN / 2, params, lane);
             int ok = 1;
             if (lane == 0)
                 ok = dev::mbar_wait_bounded(dev::smem_u32(&tfull[buf]), (uint32_t)(lt >> 1) & 1u, abort_flag, kWaitNs);
@@ -286,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t taddr = tmem + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll 1
             for (int j = 0; j < BN / 2; j += 32) {
-                const int cj = half * (BN / 2) + j;
+                const int cj = half * (BN / 2) + j, col0 = nt * BN + cj;
                 uint32_t v[32];
                 dev::tmem_ld_32x32b_x16(taddr + (uint32_t)cj, v);
                 dev::tmem_ld_32x32b_x16(taddr + (uint32_t)(cj + 16), v + 16);
@@ -299,14 +314,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) {
                         if constexpr (PAIR)
-                            dev::mbar_arrive_cluster(tempty0 + (uint32_t)(buf * 8));
+                            arrive_remote(tempty0 + (uint32_t)(buf * 8));
                         else
                             dev::mbar_arrive(dev::smem_u32(&tempty[buf]));
                     }
                 }
-                const int col0 = nt * BN + cj;
                 if (col0 < a.e.n && row0 < a.e.m)
-                    finish_block<T>(a.e, reinterpret_cast<float *>(v), row_scale, row0, col0, stg, lane);
+                    finish_block<T>(a.e, v, params + 4 * j, params + 4 * (BN / 2 + j), row_scale, row0, col0, stg, lane);
             }
         }
     }
@@ -358,7 +372,7 @@ template <typename T, int BN, bool PAIR>
 cudaError_t gemm_launch(const LinearProblem &p, const __half *a16, const __half *w16, int kp, int sm_count,
                         cudaStream_t stream)
 {
-    using C = GemmCfg<BN, PAIR>;
+    using C = GemmCfg<BN, PAIR, sizeof(T)>;
     static bool allowed[kMaxDevices] = {};
     cudaError_t e = allow_dynamic_smem(linear_gemm_kernel<T, BN, PAIR>, C::SMEM, allowed);
     if (e != cudaSuccess) return e;

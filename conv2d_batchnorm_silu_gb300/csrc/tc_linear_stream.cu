@@ -59,23 +59,6 @@ __device__ __forceinline__ void give_up(unsigned int bit, volatile int *abort_fl
     *abort_flag = 1;
 }
 
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-// As mbar_wait_bounded; waits here are often a little early, and reading the clock at the first
-// unsuccessful poll would cost more than most of them last.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, const volatile int *abort_flag,
-                                             uint64_t timeout_ns)
-{
-    for (int i = 0; i < 64; ++i)
-        if (dev::mbar_try_wait(bar, parity)) return true;
-    return dev::mbar_wait_bounded(bar, parity, abort_flag, timeout_ns);
-}
-
 // What rows of a hold past k.
 __device__ const uint4 g_zeros = {0, 0, 0, 0};
 
