@@ -182,27 +182,24 @@ __device__ __forceinline__ void silu32(float *v)
     }
 }
 
-// Scales, then biases, of `count` columns from col0 into `dst` in shared memory, by one warp; zeros past
+// Scales, then biases, of the 32 columns from col0 into `dst` in shared memory, one lane each; zeros past
 // the end.
-__device__ __forceinline__ void stage_params(const LinearEpilogue &e, int col0, int count, uint32_t dst, int lane)
+__device__ __forceinline__ void stage_params(const LinearEpilogue &e, int col0, uint32_t dst, int lane)
 {
-    for (int i = lane; i < count; i += 32) {
-        const bool in = col0 + i < e.n;
-        const float s = in ? __ldg(e.w_scale + col0 + i) : 0.0f, b = in && e.bias ? __ldg(e.bias + col0 + i) : 0.0f;
-        dev::sts_u32(dst + 4 * i, __float_as_uint(s));
-        dev::sts_u32(dst + 4 * (count + i), __float_as_uint(b));
-    }
-    __syncwarp();
+    const bool in = col0 + lane < e.n;
+    const float s = in ? __ldg(e.w_scale + col0 + lane) : 0.0f, b = in && e.bias ? __ldg(e.bias + col0 + lane) : 0.0f;
+    dev::sts_u32(dst + 4 * lane, __float_as_uint(s));
+    dev::sts_u32(dst + 128 + 4 * lane, __float_as_uint(b));
 }
 
 // A warp's block of 32 rows x 32 columns from (row0, col0): lane l holds row row0 + l, its 32 sums in
 // v.  Rows and columns past the end are computed and not stored.  `stg` is the warp's own 32 x 32
 // elements of shared memory, through which lanes exchange rows for columns, so that each store covers
 // whole runs of a row; 16-byte pieces are swizzled so that neither direction meets a bank twice.  The
-// block's scales are in shared memory at `scales`, its biases at `biases`.
+// block's scales and biases are in shared memory at `params` (stage_params).
 template <typename T>
-__device__ __forceinline__ void finish_block(const LinearEpilogue &e, const uint32_t *sums, uint32_t scales,
-                                             uint32_t biases, float row_scale, long long row0, int col0, uint32_t stg, int lane)
+__device__ __forceinline__ void finish_block(const LinearEpilogue &e, const uint32_t *sums, uint32_t params,
+                                             float row_scale, long long row0, int col0, uint32_t stg, int lane)
 {
     constexpr int kPieces = 32 * sizeof(T) / 16;      // 16-byte pieces of a row
     constexpr int kPer = 16 / sizeof(T);              // elements of a piece
@@ -211,7 +208,7 @@ __device__ __forceinline__ void finish_block(const LinearEpilogue &e, const uint
     float v[32];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint4 s = dev::lds_v4(scales + 16 * i), b = dev::lds_v4(biases + 16 * i);
+        const uint4 s = dev::lds_v4(params + 16 * i), b = dev::lds_v4(params + 128 + 16 * i);
         const float2 r = make_float2(row_scale, row_scale);
         const float2 lo = __ffma2_rn(make_float2(__uint_as_float(sums[4 * i]), __uint_as_float(sums[4 * i + 1])),
                                      __fmul2_rn(r, make_float2(__uint_as_float(s.x), __uint_as_float(s.y))),

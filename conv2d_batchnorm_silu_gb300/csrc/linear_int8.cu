@@ -127,21 +127,31 @@ cudaError_t linear_few_launch_t(const LinearArgs &a, int sm_count, cudaStream_t 
 
 // Rows up to which linear_few_kernel is the faster.
 constexpr int kFewRows = 8;
-// Rows up to which the weights are widened on their way, where the alignment allows it.
-constexpr int kStreamRows = 512;
+// More rows than this always multiply weights that were widened before: sixteen row tiles would each widen
+// them again.
+constexpr int kStreamRows = 4096;
+
+// Whether the weights are widened on their way to the tensor cores (tc_linear_stream.cu) rather than before
+// (tc_linear.cu): where reading them, not multiplying, takes the time.  8192 x 8192 weights, us, on their way
+// against before: 64 rows 23 / 86, 256 rows 45 / 88, 512 rows 81 / 90, 1024 rows 152 / 129.
+bool streamed(long long m, int n, int k, int sm_count)
+{
+    return m <= kStreamRows && tc_stream_time(m, n, k, sm_count) < tc_linear_time(m, n, k, sm_count);
+}
 
 long long linear_workspace_bytes(long long m, int n, int k, int sm_count)
 {
     if (m <= kFewRows || n <= 0) return 0;
-    const long long wide = tc_linear_workspace_bytes(m, n, k);
-    const long long streamed = m <= kStreamRows ? tc_stream_workspace_bytes(m, n, k, sm_count) : 0;
-    return wide > streamed ? wide : streamed;
+    // Which of the two runs also depends on the alignment of the call's matrices.
+    const long long before = tc_linear_workspace_bytes(m, n, k);
+    const long long on_the_way = streamed(m, n, k, sm_count) ? tc_stream_workspace_bytes(m, n, k, sm_count) : 0;
+    return before > on_the_way ? before : on_the_way;
 }
 
 cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream)
 {
     if (p.m > kFewRows)
-        return p.m <= kStreamRows && tc_stream_supported(p) ? tc_stream_launch(p, sm_count, stream)
+        return tc_stream_supported(p) && streamed(p.m, p.n, p.k, sm_count) ? tc_stream_launch(p, sm_count, stream)
                                                             : tc_linear_launch(p, sm_count, stream);
     LinearArgs a{};
     a.e = linear_epilogue_of(p);

@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(256) widen_kernel(const WidenArgs args)
 // ------------------------------------------------------------------ GEMM
 constexpr int kBlockK = 64;  // f16 elements per step: one 128-byte swizzle span
 constexpr int kBlockM = 128; // rows per CTA
-constexpr int kEpiWarps = 8; // two per TMEM lane quarter
+constexpr int kEpiPerQuarter = 3;  // epilogue warps per TMEM lane quarter; they take its 32-column blocks in turn
+constexpr int kEpiWarps = 4 * kEpiPerQuarter;
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 
 // BN output channels per tile.  PAIR: two CTAs of a cluster work as one on 256 rows, each
@@ -78,7 +79,8 @@ struct GemmCfg {
     static constexpr int B_BYTES = B_ROWS * kBlockK * 2;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int STG_BLOCK = 32 * 32 * SIZE;              // an epilogue warp's block on its way out
-    static constexpr int STG_WARP = STG_BLOCK + 2 * (BN / 2) * 4;  // and the scales and biases of its columns
+    static constexpr int BLOCKS = BN / 32, MOST = (BLOCKS + kEpiPerQuarter - 1) / kEpiPerQuarter;  // per warp
+    static constexpr int STG_WARP = STG_BLOCK + MOST * 256;  // and the scales and biases of its columns
     static constexpr int STG = kEpiWarps * STG_WARP;
     static constexpr int FIT = (232448 - 1024 - 512 - STG) / STAGE;
     static constexpr int STAGES = FIT < 8 ? FIT : 8;
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= 4) {
         // ---------------------------------------------------------- epilogue
-        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        const int quarter = warp & 3, turn = (warp - 4) >> 2;
         const uint32_t stg = dev::smem_u32(sm_stg + (warp - 4) * C::STG_WARP), params = stg + C::STG_BLOCK;
         int lt = 0;
         for (int t = vb; t < a.tiles; t += vg, ++lt) {
@@ -288,7 +290,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int buf = lt & 1;
             const long long row0 = (long long)(mt * CG + rank) * kBlockM + quarter * 32;
             const float row_scale = row0 + lane < a.e.m ? __ldg(a.e.a_scale + row0 + lane) : 0.0f;
-            stage_params(a.e, nt * BN + half * (BN / 2), BN / 2, params, lane);
+            for (int j = turn, i = 0; j < C::BLOCKS; j += kEpiPerQuarter, ++i)
+                stage_params(a.e, nt * BN + j * 32, params + 256 * i, lane);
+            __syncwarp();
             int ok = 1;
             if (lane == 0)
                 ok = dev::mbar_wait_bounded(dev::smem_u32(&tfull[buf]), (uint32_t)(lt >> 1) & 1u, abort_flag, kWaitNs);
@@ -298,29 +302,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             dev::tc_fence_after_sync();
+            auto hand_back = [&]() {
+                dev::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR)
+                        arrive_remote(tempty0 + (uint32_t)(buf * 8));
+                    else
+                        dev::mbar_arrive(dev::smem_u32(&tempty[buf]));
+                }
+            };
+            if (turn >= C::BLOCKS) hand_back();  // a warp without a block
             const uint32_t taddr = tmem + (uint32_t)(buf * BN) + ((uint32_t)(quarter * 32) << 16);
 #pragma unroll 1
-            for (int j = 0; j < BN / 2; j += 32) {
-                const int cj = half * (BN / 2) + j, col0 = nt * BN + cj;
+            for (int j = turn, i = 0; j < C::BLOCKS; j += kEpiPerQuarter, ++i) {
+                const int cj = j * 32, col0 = nt * BN + cj;
                 uint32_t v[32];
                 dev::tmem_ld_32x32b_x16(taddr + (uint32_t)cj, v);
                 dev::tmem_ld_32x32b_x16(taddr + (uint32_t)(cj + 16), v + 16);
                 dev::tmem_ld_wait();
                 dev::reg_fence16(v);
                 dev::reg_fence16(v + 16);
-                if (j + 32 == BN / 2) {
-                    // The warp's last read of this accumulator: hand it back before the stores.
-                    dev::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (PAIR)
-                            arrive_remote(tempty0 + (uint32_t)(buf * 8));
-                        else
-                            dev::mbar_arrive(dev::smem_u32(&tempty[buf]));
-                    }
-                }
+                if (j + kEpiPerQuarter >= C::BLOCKS) hand_back();  // the warp's last read, before its stores
                 if (col0 < a.e.n && row0 < a.e.m)
-                    finish_block<T>(a.e, v, params + 4 * j, params + 4 * (BN / 2 + j), row_scale, row0, col0, stg, lane);
+                    finish_block<T>(a.e, v, params + 256 * i, row_scale, row0, col0, stg, lane);
             }
         }
     }
@@ -393,14 +398,51 @@ cudaError_t gemm_launch(const LinearProblem &p, const __half *a16, const __half 
                              stream, PAIR ? 2 : 1, ta, tw, a);
 }
 
+// The three tiles: 256 x 256 and 256 x 128 by CTA pairs, 128 x 64 by single CTAs.  Their time is modelled by
+// what they measured (us): a step of 64 K elements, the least time of a tile, which its epilogue sets, and
+// what a launch takes besides.  Small tiles pay where the large ones would leave SMs idle:
+// 1024x1024x4096 22.6 / 16.0 / 18.3, 512x512x512 8.0 / 6.1 / 5.2, 4096x4096x4096 74 / 86 / 213.
+struct TileCost {
+    int rows, channels, ctas;
+    float step, least, launch;
+};
+constexpr TileCost kTiles[3] = {{256, 256, 2, 0.30f, 3.4f, 4.8f}, {256, 128, 2, 0.205f, 2.1f, 4.0f}, {128, 64, 1, 0.24f, 1.2f, 3.2f}};
+
+float tile_time(const TileCost &c, long long m, int n, int kp, int sm_count)
+{
+    const long long tiles = ((m + c.rows - 1) / c.rows) * ((n + c.channels - 1) / c.channels);
+    const int workers = sm_count / c.ctas;
+    const float steps = c.step * (float)(kp / kBlockK);
+    return (float)((tiles + workers - 1) / workers) * (steps > c.least ? steps : c.least) + c.launch;
+}
+
+int best_tile(long long m, int n, int kp, int sm_count)
+{
+    int best = 0;
+    for (int i = 1; i < 3; ++i)
+        if (tile_time(kTiles[i], m, n, kp, sm_count) < tile_time(kTiles[best], m, n, kp, sm_count)) best = i;
+    return best;
+}
+
 template <typename T>
 cudaError_t gemm_launch_t(const LinearProblem &p, const __half *a16, const __half *w16, int kp, int sm_count,
                           cudaStream_t stream)
 {
-    return gemm_launch<T, 256, true>(p, a16, w16, kp, sm_count, stream);
+    switch (best_tile(p.m, p.n, kp, sm_count)) {
+    case 0: return gemm_launch<T, 256, true>(p, a16, w16, kp, sm_count, stream);
+    case 1: return gemm_launch<T, 128, true>(p, a16, w16, kp, sm_count, stream);
+    default: return gemm_launch<T, 64, false>(p, a16, w16, kp, sm_count, stream);
+    }
 }
 
 }  // namespace
+
+float tc_linear_time(long long m, int n, int k, int sm_count)
+{
+    // Widening reads a byte and writes two for each element, at 5 TB/s.
+    const int kp = padded_k(k);
+    return 2.5f + 3.0f * (float)(m + n) * (float)kp / 5.0e6f + tile_time(kTiles[best_tile(m, n, kp, sm_count)], m, n, kp, sm_count);
+}
 
 long long tc_linear_workspace_bytes(long long m, int n, int k)
 {

@@ -418,6 +418,15 @@ cudaError_t stream_launch_t(const StreamArgs &a, int nt, cudaStream_t stream)
 
 }  // namespace
 
+float tc_stream_time(long long m, int n, int k, int sm_count)
+{
+    // A step of 128 K elements as measured for each row tile, both launches, and the sums' way through L2.
+    const StreamPlan p = plan_of(m, n, k, sm_count);
+    const float step = p.nt == 32 ? 0.60f : (p.nt == 64 ? 0.67f : (p.nt == 128 ? 0.91f : 1.50f));
+    return 5.0f + step * (float)((p.steps + p.workers - 1) / p.workers) +
+           (float)(p.workers + p.tiles) * (float)p.nt * kChannels * 8.0f / 8.0e6f;
+}
+
 bool tc_stream_supported(const LinearProblem &p)
 {
     auto rows16 = [](const Rows &r) { return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && r.stride % 16 == 0; };

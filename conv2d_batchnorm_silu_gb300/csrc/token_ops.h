@@ -101,12 +101,14 @@ cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t str
 
 // The linear layer on the tensor cores (tc_linear.cu); k == 0 counts as a step of zeros.
 long long tc_linear_workspace_bytes(long long m, int n, int k);
+float tc_linear_time(long long m, int n, int k, int sm_count);  // modelled, us
 cudaError_t tc_linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
 cudaError_t tc_linear_read_and_clear_error(cudaStream_t stream, unsigned int *out);
 
 // The linear layer with the weights widened on their way to the tensor cores (tc_linear_stream.cu).
 bool tc_stream_supported(const LinearProblem &p);
 long long tc_stream_workspace_bytes(long long m, int n, int k, int sm_count);
+float tc_stream_time(long long m, int n, int k, int sm_count);  // modelled, us
 cudaError_t tc_stream_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
 cudaError_t tc_stream_read_and_clear_error(cudaStream_t stream, unsigned int *out);
 
