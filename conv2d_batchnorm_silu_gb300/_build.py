@@ -1,15 +1,18 @@
 """Builds the in-tree CUDA library ``libconvbnsilu.so`` for sm_103a with nvcc.
 
 One object per translation unit, compiled in parallel, then linked into a
-shared library with the CUDA runtime linked statically.  The library is
-rebuilt only when a source or header is newer than it.
+shared library with the CUDA runtime linked statically; beside it, with g++,
+``_token_ops.so``, the Python calls of the token-wise operators over PyTorch's
+C++ tensors.  Both are rebuilt only when a source or header is newer than they.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +20,8 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libconvbnsilu.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
+BINDING_PATH = os.path.join(PKG_DIR, "_token_ops.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -35,18 +40,51 @@ def sources() -> list[str]:
 
 def _inputs() -> list[str]:
     return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
+            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [BINDING_SOURCE, os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found: its headers are required to build the binding")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _compile_binding() -> str:
+    """The binding's object file."""
+    torch_include = os.path.join(_torch_dir(), "include")
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD_DIR, "binding.o")
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-I", sysconfig.get_paths()["include"],
+           "-I", torch_include, "-I", os.path.join(torch_include, "torch", "csrc", "api", "include"),
+           "-I", cuda_include, "-I", os.path.join(ROOT, "include"), "-c", BINDING_SOURCE, "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SOURCE}:\n{res.stdout}\n{res.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    tmp = BINDING_PATH + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-shared", "-o", tmp, obj, "-L", PKG_DIR, "-lconvbnsilu",
+           "-Wl,-rpath,$ORIGIN", "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+           "-lc10_cuda", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING_PATH)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Compile every ``csrc/*.cu`` for sm_103a and link ``libconvbnsilu.so``; returns its path."""
+    """Compile every ``csrc/*.cu`` for sm_103a and link ``libconvbnsilu.so``, and the binding beside it;
+    returns the library's path."""
     if not force and up_to_date():
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -63,12 +101,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(compile_one, srcs))
+        binding_obj = binding.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_binding(binding_obj)
     return LIB_PATH

@@ -9,7 +9,6 @@ fallback: if the library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 
 import torch
@@ -23,6 +22,8 @@ if not os.path.exists(LIB_PATH):
         "or conv2d_batchnorm_silu_gb300._build.build()); there is no non-CUDA fallback")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+from . import _token_ops  # noqa: E402  (compiled beside the library, which it links)
 
 CBS_OK = 0
 CBS_ERR_INVALID_ARG = 1
@@ -96,17 +97,15 @@ _plan = _declare("conv_bn_silu_plan", [_i] * 13 + [ctypes.POINTER(PlanInfo)])
 _plan_request = _declare("conv_bn_silu_plan_request", [_i] * 11 + [ctypes.POINTER(PlanRequest), _i,
                                                                      ctypes.POINTER(PlanInfo)])
 _forward_request = _declare("conv_bn_silu_forward_request", [_p] * 5 + [_i] * 11 + [ctypes.POINTER(PlanRequest), _p])
+# The token-wise operators: called through _token_ops, declared here for raw_status.
 _ll = ctypes.c_longlong
-_layer_norm = _declare("conv_bn_silu_layer_norm", [_p, _ll, _p, _p, _f, _p, _ll, _p, _ll, _i, _i, _p])
-_layer_norm_backward = _declare("conv_bn_silu_layer_norm_backward", [_p, _ll, _p, _ll, _p, _p, _p, _ll, _p, _p,
-                                                                       _ll, _i, _i, _p, _ll, _p])
-_layer_norm_backward_workspace = _declare("conv_bn_silu_layer_norm_backward_workspace", [_ll, _i], _ll)
-_quantize_rows = _declare("conv_bn_silu_quantize_rows", [_p, _ll, _p, _ll, _p, _ll, _i, _i, _p])
-_layer_norm_quantize = _declare("conv_bn_silu_layer_norm_quantize", [_p, _ll, _p, _p, _f, _p, _ll, _p, _ll, _i, _i,
-                                                                       _p])
-_linear_int8 = _declare("conv_bn_silu_linear_int8", [_p, _ll, _p, _ll, _p, _p, _p, _p, _ll, _p, _ll, _ll, _i, _i,
-                                                       _i, _i, _p, _ll, _p])
-_linear_int8_workspace = _declare("conv_bn_silu_linear_int8_workspace", [_ll, _i, _i], _ll)
+_declare("conv_bn_silu_layer_norm", [_p, _ll, _p, _p, _f, _p, _ll, _p, _ll, _i, _i, _p])
+_declare("conv_bn_silu_layer_norm_backward", [_p, _ll, _p, _ll, _p, _p, _p, _ll, _p, _p, _ll, _i, _i, _p, _ll, _p])
+_declare("conv_bn_silu_layer_norm_backward_workspace", [_ll, _i], _ll)
+_declare("conv_bn_silu_quantize_rows", [_p, _ll, _p, _ll, _p, _ll, _i, _i, _p])
+_declare("conv_bn_silu_layer_norm_quantize", [_p, _ll, _p, _p, _f, _p, _ll, _p, _ll, _i, _i, _p])
+_declare("conv_bn_silu_linear_int8", [_p, _ll, _p, _ll, _p, _p, _p, _p, _ll, _p, _ll, _ll, _i, _i, _i, _i, _p, _ll, _p])
+_declare("conv_bn_silu_linear_int8_workspace", [_ll, _i, _i], _ll)
 _check = _declare("conv_bn_silu_check", [_p])
 _status_string = _declare("conv_bn_silu_status_string", [_i], ctypes.c_char_p)
 _last_cuda_error = _declare("conv_bn_silu_last_cuda_error", [])
@@ -461,97 +460,10 @@ def silu_apply(t2: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> 
 # ---------------------------------------------------------------- token-wise operators
 # Activations are tensors [..., c] whose last dimension is dense and whose leading dimensions
 # are rows at one distance (a contiguous tensor, or a column slice of a matrix); parameters,
-# statistics and scales are dense float32.  Small calls are bound by the host: an operator looks
-# at each tensor once and allocates through the entry that generated code uses (0.9 us a tensor on
-# the GB300's host, against 1.6 us and a launch slower by 2 us after torch.empty).
+# statistics and scales are dense float32.  Arguments are checked, and outputs and workspaces
+# made, in the compiled module _token_ops (csrc/binding.cpp), which returns a status that is
+# not CBS_OK as an int.
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-
-try:
-    from torch._C._dynamo.guards import _empty_strided_cuda
-except ImportError:
-    def _empty_strided_cuda(shape, stride, dtype):
-        return torch.empty_strided(shape, stride, dtype=dtype, device="cuda")
-
-
-def _rows(t: torch.Tensor, name: str, device: int) -> tuple[int, int, int, int]:
-    """(pointer, rows, columns, distance of rows in elements) of an activation tensor."""
-    if t.get_device() != device:
-        raise ValueError(f"{name} must be on the CUDA device of the call's first tensor")
-    shape = t.shape
-    if len(shape) != 2:
-        if not shape:
-            raise ValueError(f"{name} must have at least one dimension")
-        c = shape[-1]
-        try:
-            t = t.view(math.prod(shape[:-1]), c)
-        except RuntimeError:
-            raise ValueError(f"{name}'s leading dimensions must be rows at one distance") from None
-        shape = t.shape
-    rows, c = shape
-    distance, step = t.stride()
-    if step != 1 and c > 1:
-        raise ValueError(f"{name}'s last dimension must be dense")
-    return t.data_ptr(), rows, c, distance if rows > 1 else c
-
-
-def _vector(t: torch.Tensor | None, n: int, name: str, device: int) -> int | None:
-    if t is None:
-        return None
-    if t.dtype is not torch.float32:
-        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
-    if t.get_device() != device or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must hold {n} dense elements on the CUDA device of the call's first tensor")
-    return t.data_ptr()
-
-
-def _first(t: torch.Tensor, name: str) -> int:
-    """The device of the call's first tensor, which has to be the current one."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    device = t.get_device()
-    if device < 0 or device != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} must be on the current CUDA device")
-    return device
-
-
-def _dtype_code(dtype: torch.dtype, name: str) -> int:
-    code = DTYPES.get(dtype)
-    if code is None:
-        raise TypeError(f"{name} must be torch.float32, torch.bfloat16 or torch.float16, got {dtype}")
-    return code
-
-
-def _empty(shape, dtype: torch.dtype, device: int, stream) -> torch.Tensor:
-    """An output or workspace; on another stream than the current one, from that stream's memory."""
-    shape = tuple(shape)
-    n = len(shape)
-    if n == 1:
-        stride = (1,)
-    elif n == 2:
-        stride = (shape[1], 1)
-    else:
-        stride = tuple(math.prod(shape[i + 1:]) for i in range(n))
-    if stream is None:
-        return _empty_strided_cuda(shape, stride, dtype)
-    with torch.cuda.stream(torch.cuda.ExternalStream(_stream_handle(stream), device=device)):
-        return _empty_strided_cuda(shape, stride, dtype)
-
-
-def _output(t: torch.Tensor | None, shape, dtype: torch.dtype, name: str, device: int, stream):
-    """(tensor, pointer, distance of rows) of an output that is given or made here."""
-    if t is None:
-        t = _empty(shape, dtype, device, stream)
-        return t, t.data_ptr(), shape[-1]
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    pointer, _, _, distance = _rows(t, name, device)
-    return t, pointer, distance
-
-
-def _run_stream(stream, device: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream_handle(stream)
 
 
 def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
@@ -561,63 +473,29 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
     x: float32, bf16 or f16 [..., c]; gamma, beta: fp32 [c] or None; y like x.  With return_stats
     also the fp32 statistics [2, rows] (mean, then 1/sqrt(var + eps)) for layer_norm_backward.
     """
-    device = _first(x, "x")
-    dtype = x.dtype
-    code = _dtype_code(dtype, "x")
-    px, rows, c, sx = _rows(x, "x", device)
-    pg, pb = _vector(gamma, c, "gamma", device), _vector(beta, c, "beta", device)
-    y, py, sy = _output(y, x.shape, dtype, "y", device, stream)
-    stats = pstats = None
-    if return_stats:
-        stats = _empty((2, rows), torch.float32, device, stream)
-        pstats = stats.data_ptr()
-    if rows:
-        st = _layer_norm(px, sx, pg, pb, eps, py, sy, pstats, rows, c, code, _run_stream(stream, device))
-        if st:
-            _raise_if(st, "conv_bn_silu_layer_norm")
-    return (y, stats) if return_stats else y
+    out = _token_ops.layer_norm(x, gamma, beta, eps, return_stats, y,
+                                None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_layer_norm")
+    return out
 
 
 def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None, stats: torch.Tensor,
                         dx: torch.Tensor | None = None, stream=None):
     """conv_bn_silu_layer_norm_backward: (dx, dgamma, dbeta) from dy, the forward call's x and gamma
     (None: ones) and the statistics it returned.  dx is like x; dgamma and dbeta are fp32 [c]."""
-    device = _first(x, "x")
-    dtype = x.dtype
-    code = _dtype_code(dtype, "x")
-    if dy.dtype is not dtype:
-        raise TypeError(f"dy must be {dtype}, got {dy.dtype}")
-    if dy.shape != x.shape:
-        raise ValueError(f"dy has shape {tuple(dy.shape)}, expected {tuple(x.shape)}")
-    px, rows, c, sx = _rows(x, "x", device)
-    pdy, _, _, sdy = _rows(dy, "dy", device)
-    pg, pstats = _vector(gamma, c, "gamma", device), _vector(stats, 2 * rows, "stats", device)
-    need = _layer_norm_backward_workspace(rows, c)
-    if need < 0:
-        _raise_if(CBS_ERR_INVALID_ARG, "conv_bn_silu_layer_norm_backward_workspace")
-    dx, pdx, sdx = _output(dx, x.shape, dtype, "dx", device, stream)
-    dgamma, dbeta = _empty((c,), torch.float32, device, stream), _empty((c,), torch.float32, device, stream)
-    work = _empty((need,), torch.uint8, device, stream)
-    st = _layer_norm_backward(pdy, sdy, px, sx, pg, pstats, pdx, sdx, dgamma.data_ptr(), dbeta.data_ptr(), rows, c,
-                              code, work.data_ptr(), need, _run_stream(stream, device))
-    if st:
-        _raise_if(st, "conv_bn_silu_layer_norm_backward")
-    return dx, dgamma, dbeta
+    out = _token_ops.layer_norm_backward(dy, x, gamma, stats, dx, None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_layer_norm_backward")
+    return out
 
 
 def quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """conv_bn_silu_quantize_rows: (q, scale), q int8 like x, scale fp32 [...] with x close to q * scale."""
-    device = _first(x, "x")
-    code = _dtype_code(x.dtype, "x")
-    px, rows, c, sx = _rows(x, "x", device)
-    shape = x.shape
-    q, pq, sq = _output(q, shape, torch.int8, "q", device, stream)
-    scale = _empty(shape[:-1], torch.float32, device, stream)
-    if rows:
-        st = _quantize_rows(px, sx, pq, sq, scale.data_ptr(), rows, c, code, _run_stream(stream, device))
-        if st:
-            _raise_if(st, "conv_bn_silu_quantize_rows")
-    return q, scale
+    out = _token_ops.quantize_rows(x, q, None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_quantize_rows")
+    return out
 
 
 def layer_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
@@ -625,19 +503,10 @@ def layer_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, beta
                         stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """conv_bn_silu_layer_norm_quantize: layer_norm, its rows quantised in the same pass; (q, scale) as
     quantize_rows gives them."""
-    device = _first(x, "x")
-    code = _dtype_code(x.dtype, "x")
-    px, rows, c, sx = _rows(x, "x", device)
-    pg, pb = _vector(gamma, c, "gamma", device), _vector(beta, c, "beta", device)
-    shape = x.shape
-    q, pq, sq = _output(q, shape, torch.int8, "q", device, stream)
-    scale = _empty(shape[:-1], torch.float32, device, stream)
-    if rows:
-        st = _layer_norm_quantize(px, sx, pg, pb, eps, pq, sq, scale.data_ptr(), rows, c, code,
-                                  _run_stream(stream, device))
-        if st:
-            _raise_if(st, "conv_bn_silu_layer_norm_quantize")
-    return q, scale
+    out = _token_ops.layer_norm_quantize(x, gamma, beta, eps, q, None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_layer_norm_quantize")
+    return out
 
 
 def linear_int8(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale: torch.Tensor,
@@ -649,44 +518,17 @@ def linear_int8(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale
     a: int8 [..., k]; w: int8 [n, k]; a_scale: fp32, one for each row of a; w_scale, bias: fp32 [n];
     residual and y: out_dtype [..., n] (residual may be y).  activation: "silu", "identity" or "relu".
     """
-    device = _first(a, "a")
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
-    code = _dtype_code(out_dtype, "out_dtype")
-    if a.dtype is not torch.int8 or w.dtype is not torch.int8:
-        raise TypeError("a and w must be torch.int8")
-    if w.dim() != 2:
-        raise ValueError("w must be [n, k]")
-    pw, n, k, sw = _rows(w, "w", device)
-    pa, m, ka, sa = _rows(a, "a", device)
-    if ka != k:
-        raise ValueError(f"channel mismatch: a has {ka}, w has {k}")
-    pas, pws = _vector(a_scale, m, "a_scale", device), _vector(w_scale, n, "w_scale", device)
-    pb = _vector(bias, n, "bias", device)
-    shape = (m, n) if a.dim() == 2 else (*a.shape[:-1], n)
-    pr, sr = None, 0
-    if residual is not None:
-        if residual.dtype is not out_dtype:
-            raise TypeError(f"residual must be {out_dtype}, got {residual.dtype}")
-        if residual.shape != shape:
-            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(shape)}")
-        pr, _, _, sr = _rows(residual, "residual", device)
-    y, py, sy = _output(y, shape, out_dtype, "y", device, stream)
-    if m == 0 or n == 0:
-        return y
-    need = _linear_int8_workspace(m, n, k)
-    work = pwork = None
-    if need > 0:
-        work = _empty((need,), torch.uint8, device, stream)
-        pwork = work.data_ptr()
-    elif need < 0:
-        _raise_if(CBS_ERR_INVALID_ARG, "conv_bn_silu_linear_int8_workspace")
-    st = _linear_int8(pa, sa, pw, sw, pas, pws, pb, pr, sr, py, sy, m, n, k, act, code, pwork, need,
-                      _run_stream(stream, device))
-    if st:
-        _raise_if(st, "conv_bn_silu_linear_int8")
-    return y
+    code = DTYPES.get(out_dtype)
+    if code is None:
+        raise TypeError(f"out_dtype must be torch.float32, torch.bfloat16 or torch.float16, got {out_dtype}")
+    out = _token_ops.linear_int8(a, w, a_scale, w_scale, bias, act, residual, code, y,
+                                 None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_linear_int8")
+    return out
 
 
 def forward_ptr(x_ptr: int, w_ptr: int, scale_ptr: int, bias_ptr: int, y_ptr: int,
