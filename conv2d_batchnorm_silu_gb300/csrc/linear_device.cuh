@@ -57,15 +57,55 @@ __device__ __forceinline__ void from_float(float v, float *out) { *out = v; }
 __device__ __forceinline__ void from_float(float v, __nv_bfloat16 *out) { *out = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void from_float(float v, __half *out) { *out = __float2half_rn(v); }
 
-// 16 values from k0 on, zeros past k.
-__device__ __forceinline__ uint4 load16(const int8_t *row, int k0, int k, bool aligned)
+// A predicated 16-byte load straight into its registers, zeros without it: behind a branch the value would
+// be moved, and the warp wait for it, where the branches meet.
+__device__ __forceinline__ uint4 load_or_zero(const void *p, bool exists)
 {
-    if (aligned && k0 + 16 <= k) return __ldg(reinterpret_cast<const uint4 *>(row + k0));
-    uint32_t w[4] = {0, 0, 0, 0};
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((int)exists));
+    return v;
+}
+
+// 16 values of a row from k0 on, at any alignment: the two aligned 16-byte pieces of memory that hold them,
+// shifted together.  A piece is read only if it holds a byte of the row, so it may reach up to 15 bytes past
+// either end of it, within the 16-byte unit, and so the page and the allocation, of that byte.
+struct RawPiece {
+    uint4 lo, hi;
+};
+__device__ __forceinline__ RawPiece load_raw(const int8_t *row, int k0, int k)
+{
+    const uintptr_t p = reinterpret_cast<uintptr_t>(row) + k0, end = reinterpret_cast<uintptr_t>(row) + k;
+    const uintptr_t base = p & ~static_cast<uintptr_t>(15);
+    return RawPiece{load_or_zero(reinterpret_cast<const void *>(base), k0 < k && base < end),
+                    load_or_zero(reinterpret_cast<const void *>(base + 16), base != p && base + 16 < end)};
+}
+// The values of a piece; what it holds past k is left as it is.
+__device__ __forceinline__ uint4 shifted(const RawPiece &r, const int8_t *row, int k0)
+{
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) + k0) & 15u;
+    uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
 #pragma unroll
-    for (int e = 0; e < 16; ++e)
-        if (k0 + e < k) w[e / 4] |= (uint32_t)(uint8_t)__ldg(row + k0 + e) << (8 * (e % 4));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 6; ++i) w[i] = off & 8u ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = off & 4u ? w[i + 1] : w[i];
+    const uint32_t bits = 8 * (off & 3u);
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+// Zeros for the values past k.
+__device__ __forceinline__ uint4 within(uint4 v, int k0, int k)
+{
+    auto keep = [&](uint32_t w, int first) {
+        const int n = k - k0 - first;  // bytes of the word that stay
+        return n >= 4 ? w : (n <= 0 ? 0u : w & (0xffffffffu >> (8 * (4 - n))));
+    };
+    return make_uint4(keep(v.x, 0), keep(v.y, 4), keep(v.z, 8), keep(v.w, 12));
 }
 
 // Four int8 of a word -> two words of f16 pairs, bytes 0 and 2, then 1 and 3 (an order of K that both

@@ -41,16 +41,22 @@ __device__ __forceinline__ int dot16(const uint4 &a, const uint4 &b, int acc)
     return __dp4a((int)a.w, (int)b.w, acc);
 }
 
-// ALIGNED: rows on 16-byte boundaries and k a multiple of 16, so that a piece is one load without a branch.
+// 16 values from k0 < k.  ALIGNED: rows on 16-byte boundaries and k a multiple of 16.
 template <bool ALIGNED>
-__device__ __forceinline__ uint4 piece(const int8_t *row, int k0, int k)
-{
-    if constexpr (ALIGNED) return __ldg(reinterpret_cast<const uint4 *>(row + k0));
-    return load16(row, k0, k, false);
-}
+struct Piece {
+    uint4 v;
+    __device__ __forceinline__ void load(const int8_t *row, int k0, int) { v = __ldg(reinterpret_cast<const uint4 *>(row + k0)); }
+    __device__ __forceinline__ uint4 get(const int8_t *, int, int) const { return v; }
+};
+template <>
+struct Piece<false> {
+    RawPiece raw;
+    __device__ __forceinline__ void load(const int8_t *row, int k0, int k) { raw = load_raw(row, k0, k); }
+    __device__ __forceinline__ uint4 get(const int8_t *row, int k0, int) const { return shifted(raw, row, k0); }
+};
 
 template <typename T, int ROWS, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kFewWarps, ROWS <= 2 ? 4 : (ROWS <= 4 ? 3 : 2)) linear_few_kernel(const LinearArgs a, int split_log2)
+__global__ void __launch_bounds__(32 * kFewWarps, ALIGNED && ROWS <= 2 ? 4 : (ROWS <= 2 || (ALIGNED && ROWS <= 4) ? 3 : 2)) linear_few_kernel(const LinearArgs a, int split_log2)
 {
     constexpr int R = kFewChannels;
     __shared__ int part[kFewWarps][R * ROWS];
@@ -67,15 +73,21 @@ __global__ void __launch_bounds__(32 * kFewWarps, ROWS <= 2 ? 4 : (ROWS <= 4 ? 3
     for (int i = 0; i < ROWS; ++i) x[i] = a.a + min(i, m - 1) * a.a_stride;
     int acc[R][ROWS] = {};
     const int step = split * 512;
-    constexpr int kUnroll = ROWS <= 4 ? 2 : 1;
+    constexpr int kUnroll = ALIGNED && ROWS <= 4 ? 2 : 1;
 #pragma unroll kUnroll
     for (int k0 = ((warp & (split - 1)) * 32 + lane) * 16; k0 < a.k; k0 += step) {
+        Piece<ALIGNED> raw[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) raw[r].load(w[r], k0, a.k);
         uint4 wv[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) wv[r] = piece<ALIGNED>(w[r], k0, a.k);
+        for (int r = 0; r < R; ++r) wv[r] = raw[r].get(w[r], k0, a.k);
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            const uint4 xv = piece<ALIGNED>(x[i], k0, a.k);
+            Piece<ALIGNED> rx;
+            rx.load(x[i], k0, a.k);
+            uint4 xv = rx.get(x[i], k0, a.k);
+            if constexpr (!ALIGNED) xv = within(xv, k0, a.k);  // zeros here make what wv holds past k harmless
 #pragma unroll
             for (int r = 0; r < R; ++r) acc[r][i] = dot16(wv[r], xv, acc[r][i]);
         }
@@ -127,32 +139,53 @@ cudaError_t linear_few_launch_t(const LinearArgs &a, int sm_count, cudaStream_t 
 
 // Rows up to which linear_few_kernel is the faster.
 constexpr int kFewRows = 8;
-// More rows than this always multiply weights that were widened before: sixteen row tiles would each widen
-// them again.
-constexpr int kStreamRows = 4096;
+// The kernels for more rows, chosen by what they are modelled to take: linear_tile.cu's one launch, weights
+// widened on their way to the tensor cores (tc_linear_stream.cu), or both widened before (tc_linear.cu).
+enum Path { kTile, kStreamed, kWidened };
 
-// Whether the weights are widened on their way to the tensor cores (tc_linear_stream.cu) rather than before
-// (tc_linear.cu): where reading them, not multiplying, takes the time.  8192 x 8192 weights, us, on their way
-// against before: 64 rows 23 / 86, 256 rows 45 / 88, 512 rows 81 / 90, 1024 rows 152 / 129.
-bool streamed(long long m, int n, int k, int sm_count)
+// Measured, us, tile / streamed / widened before: 24x614x243 5.2 / - / 6.0 (8.6 from the host), 64x1024x1024
+// 11.2 / 5.9 / 8.9, 64 rows of 8192x8192 - / 23 / 74, 512 rows - / 81 / 87, 1024 rows - / 152 / 121.
+// A call takes the longer of its kernels and what its launches cost the host.
+Path best_path(long long m, int n, int k, int sm_count, bool aligned)
 {
-    return m <= kStreamRows && tc_stream_time(m, n, k, sm_count) < tc_linear_time(m, n, k, sm_count);
+    const float tile = linear_tile_supported(m, n) ? linear_tile_time(m, n, k, sm_count) : 1e30f;
+    const float before = tc_linear_time(m, n, k, sm_count);
+    // Beyond 4096 rows sixteen row tiles would each widen the weights again.
+    const float on_the_way = aligned && m <= 4096 ? tc_stream_time(m, n, k, sm_count) : 1e30f;
+    const float times[3] = {fmaxf(tile, 4.6f), fmaxf(on_the_way, 7.4f), fmaxf(before, 8.6f)};
+    int best = kWidened;
+    for (int i = 0; i < 2; ++i)
+        if (times[i] < times[best]) best = i;
+    return (Path)best;
+}
+
+long long path_workspace(Path path, long long m, int n, int k, int sm_count)
+{
+    switch (path) {
+    case kTile: return 0;
+    case kStreamed: return tc_stream_workspace_bytes(m, n, k, sm_count);
+    default: return tc_linear_workspace_bytes(m, n, k);
+    }
 }
 
 long long linear_workspace_bytes(long long m, int n, int k, int sm_count)
 {
     if (m <= kFewRows || n <= 0) return 0;
-    // Which of the two runs also depends on the alignment of the call's matrices.
-    const long long before = tc_linear_workspace_bytes(m, n, k);
-    const long long on_the_way = streamed(m, n, k, sm_count) ? tc_stream_workspace_bytes(m, n, k, sm_count) : 0;
-    return before > on_the_way ? before : on_the_way;
+    // For either alignment that the call's matrices may have.
+    const long long a = path_workspace(best_path(m, n, k, sm_count, true), m, n, k, sm_count);
+    const long long b = path_workspace(best_path(m, n, k, sm_count, false), m, n, k, sm_count);
+    return a > b ? a : b;
 }
 
 cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream)
 {
-    if (p.m > kFewRows)
-        return tc_stream_supported(p) && streamed(p.m, p.n, p.k, sm_count) ? tc_stream_launch(p, sm_count, stream)
-                                                            : tc_linear_launch(p, sm_count, stream);
+    if (p.m > kFewRows) {
+        switch (best_path(p.m, p.n, p.k, sm_count, tc_stream_supported(p))) {
+        case kTile: return linear_tile_launch(p, stream);
+        case kStreamed: return tc_stream_launch(p, sm_count, stream);
+        default: return tc_linear_launch(p, sm_count, stream);
+        }
+    }
     LinearArgs a{};
     a.e = linear_epilogue_of(p);
     a.a = static_cast<const int8_t *>(p.a.data);

@@ -53,7 +53,13 @@ __global__ void __launch_bounds__(256) widen_kernel(const WidenArgs args)
         __half *dst = (first ? args.a.dst : args.w.dst) + row * args.kp;
         const int aligned = first ? args.a.aligned : args.w.aligned;
         for (int k0 = (threadIdx.x & (lanes - 1)) * 16; k0 < args.kp; k0 += lanes * 16) {
-            const uint4 v = load16(src, k0, args.k, aligned);
+            uint4 v;
+            if (aligned) {
+                v = load_or_zero(src + k0, k0 < args.k);
+            } else {
+                v = shifted(load_raw(src, k0, args.k), src, k0);
+            }
+            if (k0 + 16 > args.k) v = within(v, k0, args.k);
             const uint2 p0 = widen4(v.x), p1 = widen4(v.y), p2 = widen4(v.z), p3 = widen4(v.w);
             uint4 *out = reinterpret_cast<uint4 *>(dst + k0);
             out[0] = make_uint4(p0.x, p0.y, p1.x, p1.y);

@@ -112,6 +112,11 @@ float tc_stream_time(long long m, int n, int k, int sm_count);  // modelled, us
 cudaError_t tc_stream_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
 cudaError_t tc_stream_read_and_clear_error(cudaStream_t stream, unsigned int *out);
 
+// The linear layer in one launch, for small products (linear_tile.cu).
+float linear_tile_time(long long m, int n, int k, int sm_count);  // modelled, us
+bool linear_tile_supported(long long m, int n);
+cudaError_t linear_tile_launch(const LinearProblem &p, cudaStream_t stream);
+
 // What any of the linear layer's kernels recorded.
 cudaError_t linear_read_and_clear_error(cudaStream_t stream, unsigned int *out);
 
