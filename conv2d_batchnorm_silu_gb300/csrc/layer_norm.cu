@@ -221,57 +221,11 @@ __global__ void __launch_bounds__(32 * kJoinRuns) norm_grad_join_kernel(const Gr
 }
 
 // ------------------------------------------------------------------ rows held in registers
-// A row stays in the registers of TPR threads, NI vectors of V elements each, from its one
-// load to its one store; sums go through warp shuffles and, above a warp, shared memory.
-// V = 16 bytes' worth where every pointer, row distance and the width allow it, else 1.
-template <typename T, int V>
-struct Vec;
-template <int V>
-struct ParamOf { using type = __half; };  // any type whose vector has V elements
-template <>
-struct ParamOf<4> { using type = float; };
-template <typename T>
-struct Vec<T, 1> {
-    T raw;
-    __device__ __forceinline__ void load(const T *p) { raw = __ldcs(p); }
-    __device__ __forceinline__ void get(float *v) const { v[0] = to_float(raw); }
-    static __device__ __forceinline__ void store(T *p, const float *v) { from_float(v[0], p); }
-    static __device__ __forceinline__ void store_q(int8_t *p, const int *q) { *p = (int8_t)q[0]; }
-    static __device__ __forceinline__ void load_param(const float *p, float *v) { v[0] = __ldg(p); }
-};
-template <>
-struct Vec<float, 4> {
-    float4 raw;
-    __device__ __forceinline__ void load(const float *p) { raw = __ldcs(reinterpret_cast<const float4 *>(p)); }
-    __device__ __forceinline__ void from(const uint4 &w)
-    {
-        raw = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-    }
-    __device__ __forceinline__ void get(float *v) const
-    {
-        v[0] = raw.x;
-        v[1] = raw.y;
-        v[2] = raw.z;
-        v[3] = raw.w;
-    }
-    static __device__ __forceinline__ void store(float *p, const float *v)
-    {
-        *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-    static __device__ __forceinline__ void store_q(int8_t *p, const int *q)
-    {
-        const uint32_t lo = __byte_perm(q[0], q[1], 0x0040), hi = __byte_perm(q[2], q[3], 0x0040);
-        *reinterpret_cast<uint32_t *>(p) = __byte_perm(lo, hi, 0x5410);
-    }
-    static __device__ __forceinline__ void load_param(const float *p, float *v)
-    {
-        const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
-        v[0] = f.x;
-        v[1] = f.y;
-        v[2] = f.z;
-        v[3] = f.w;
-    }
-};
+// A row stays in the registers of TPR threads from its one load to its one store; sums go through warp
+// shuffles and, above a warp, shared memory.  A thread holds NI runs of V elements, run i at column
+// (i * TPR + lane) * V.  W is the bytes of a run: 16 where every pointer, row distance and the width allow
+// it, else 4 (a pair of 16-bit elements, or one fp32), which any element alignment allows: a pair that
+// lies across two aligned words is put together from both.
 __device__ __forceinline__ float2 unpack(uint32_t w, __nv_bfloat16)
 {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -280,53 +234,148 @@ __device__ __forceinline__ float2 unpack(uint32_t w, __half)
 {
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
-__device__ __forceinline__ uint32_t pack(float lo, float hi, __nv_bfloat16)
+__device__ __forceinline__ uint32_t pack(float2 v, __nv_bfloat16)
 {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&b);
 }
-__device__ __forceinline__ uint32_t pack(float lo, float hi, __half)
+__device__ __forceinline__ uint32_t pack(float2 v, __half)
 {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&v);
+    const __half2 b = __floats2half2_rn(v.x, v.y);
+    return *reinterpret_cast<const uint32_t *>(&b);
 }
-template <typename T>
-struct Vec<T, 8> {
-    uint4 raw;
-    __device__ __forceinline__ void load(const T *p) { raw = __ldcs(reinterpret_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void from(const uint4 &w) { raw = w; }
-    __device__ __forceinline__ void get(float *v) const
+
+// Two fp32 operations per instruction; each rounds like the scalar one.
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// Asynchronous copies to shared memory; copy4 reads `bytes` (at most 4) and fills up with zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// One run: copied to its own SLOT bytes of shared memory, read from there as floats (zeros where the row
+// has no element), stored.  `n`, at least 1, is the number of elements that the row has from it on.  `odd` says that
+// the row starts in the middle of a word.
+template <typename T, int W>
+struct Run;
+
+template <>
+struct Run<float, 16> {
+    static constexpr int V = 4, SLOT = 16;
+    static __device__ __forceinline__ void copy(uint32_t dst, const float *p, int, bool) { copy16(dst, p); }
+    static __device__ __forceinline__ void get(const void *slot, bool, float2 *v)
     {
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack(w[i], T());
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+        const float4 f = *static_cast<const float4 *>(slot);
+        v[0] = make_float2(f.x, f.y);
+        v[1] = make_float2(f.z, f.w);
+    }
+    static __device__ __forceinline__ void store(float *p, const float2 *v, int)
+    {
+        *reinterpret_cast<float4 *>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    }
+};
+template <>
+struct Run<float, 4> {
+    static constexpr int V = 1, SLOT = 4;
+    static __device__ __forceinline__ void copy(uint32_t dst, const float *p, int, bool) { copy4(dst, p, 4); }
+    static __device__ __forceinline__ void get(const void *slot, bool, float *v) { *v = *static_cast<const float *>(slot); }
+    static __device__ __forceinline__ void store(float *p, const float *v, int) { *p = *v; }
+};
+template <typename T>
+struct Run<T, 16> {
+    static constexpr int V = 8, SLOT = 16;
+    static __device__ __forceinline__ void copy(uint32_t dst, const T *p, int, bool) { copy16(dst, p); }
+    static __device__ __forceinline__ void get(const void *slot, bool, float2 *v)
+    {
+        const uint4 w = *static_cast<const uint4 *>(slot);
+        v[0] = unpack(w.x, T());
+        v[1] = unpack(w.y, T());
+        v[2] = unpack(w.z, T());
+        v[3] = unpack(w.w, T());
+    }
+    static __device__ __forceinline__ void store(T *p, const float2 *v, int)
+    {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack(v[0], T()), pack(v[1], T()), pack(v[2], T()), pack(v[3], T()));
+    }
+};
+template <typename T>
+struct Run<T, 4> {
+    static constexpr int V = 2, SLOT = 8;
+    static __device__ __forceinline__ void copy(uint32_t dst, const T *p, int n, bool odd)
+    {
+        if (odd) {
+            copy4(dst, p - 1, 4);
+            copy4(dst + 4, p + 1, n > 1 ? 2 : 0);
+        } else {
+            copy4(dst, p, n > 1 ? 4 : 2);
         }
     }
-    static __device__ __forceinline__ void store(T *p, const float *v)
+    static __device__ __forceinline__ void get(const void *slot, bool odd, float2 *v)
     {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack(v[0], v[1], T()), pack(v[2], v[3], T()),
-                                                   pack(v[4], v[5], T()), pack(v[6], v[7], T()));
+        const uint2 w = *static_cast<const uint2 *>(slot);
+        v[0] = unpack(odd ? __byte_perm(w.x, w.y, 0x5432) : w.x, T());
     }
-    static __device__ __forceinline__ void store_q(int8_t *p, const int *q)
+    static __device__ __forceinline__ void store(T *p, const float2 *v, int n)
     {
-        auto four = [&](int i) {
-            const uint32_t lo = __byte_perm(q[i], q[i + 1], 0x0040), hi = __byte_perm(q[i + 2], q[i + 3], 0x0040);
-            return __byte_perm(lo, hi, 0x5410);
-        };
-        *reinterpret_cast<uint2 *>(p) = make_uint2(four(0), four(4));
-    }
-    static __device__ __forceinline__ void load_param(const float *p, float *v)
-    {
-        Vec<float, 4>::load_param(p, v);
-        Vec<float, 4>::load_param(p + 4, v + 4);
+        const uint32_t w = pack(v[0], T());
+        if (n > 1 && reinterpret_cast<uintptr_t>(p) % 4 == 0) {
+            *reinterpret_cast<uint32_t *>(p) = w;
+        } else {
+            unsigned short *h = reinterpret_cast<unsigned short *>(p);
+            h[0] = (unsigned short)w;
+            if (n > 1) h[1] = (unsigned short)(w >> 16);
+        }
     }
 };
 
-// Two fp32 operations per instruction; each rounds like the scalar one.
-__device__ __forceinline__ float2 pair(float a, float b) { return make_float2(a, b); }
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+// V quantised values (in the low bytes of q) to memory.
+template <int V>
+__device__ __forceinline__ void store_q(int8_t *p, const int *q, int n)
+{
+    auto four = [&](int i) {
+        const uint32_t lo = __byte_perm(q[i], q[i + 1], 0x0040), hi = __byte_perm(q[i + 2], q[i + 3], 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    };
+    if constexpr (V == 8)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(four(0), four(4));
+    else if constexpr (V == 4)
+        *reinterpret_cast<uint32_t *>(p) = four(0);
+    else
+        for (int i = 0; i < V; ++i)
+            if (i < n) p[i] = (int8_t)q[i];
+}
+
+// Parameters of n columns from column 0 of p, `otherwise` where there is no array and 0 where the row has
+// no column.
+template <int V>
+__device__ __forceinline__ void load_params(const float *p, float otherwise, int n, float *v)
+{
+    for (int j = 0; j < V; ++j) v[j] = j < n ? otherwise : 0.0f;
+    if (!p || n <= 0) return;
+    if constexpr (V >= 4) {
+        for (int j = 0; j < V; j += 4) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(p + j));
+            v[j] = f.x;
+            v[j + 1] = f.y;
+            v[j + 2] = f.z;
+            v[j + 3] = f.w;
+        }
+    } else {
+        for (int j = 0; j < V; ++j)
+            if (j < n) v[j] = __ldg(p + j);
+    }
+}
 
 // max(|a|, |b|, |c|); a NaN among them is the result.
 __device__ __forceinline__ float most_of(float a, float b, float c)
@@ -342,7 +391,7 @@ template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *scratch)
 {
     for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (TPR > 32) {
+    if constexpr (TPR > 32) {
         if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
         __syncthreads();
         v = 0.0f;
@@ -351,16 +400,16 @@ __device__ __forceinline__ float row_sum(float v, float *scratch)
     return v;
 }
 
-// Largest of non-negative values over the TPR threads, as bits: ordered like the values, NaN on top.
+// Largest of non-negative values over the TPR threads of a row, as bits: ordered like the values, NaN on top.
 template <int TPR>
 __device__ __forceinline__ float row_most(float v, float *scratch)
 {
     unsigned m = __float_as_uint(v);
-    if (TPR < 32)
-        for (int o = TPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    else
+    if constexpr (TPR >= 32)
         m = __reduce_max_sync(0xffffffffu, m);
-    if (TPR > 32) {
+    else
+        for (int o = TPR / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if constexpr (TPR > 32) {
         if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = __uint_as_float(m);
         __syncthreads();
         m = 0;
@@ -369,193 +418,118 @@ __device__ __forceinline__ float row_most(float v, float *scratch)
     return __uint_as_float(m);
 }
 
-// Threads of a block in which TPR threads hold a row: one row, or as many as 128 threads hold
-// while a row stays within a warp.
-constexpr int norm_block(int tpr) { return tpr <= 32 ? 128 : tpr; }
-
-// What becomes of row r once thread `lane` of its TPR threads has its part in v (zeros beyond the
-// row): NI runs of V elements, run i at column (i * TPR + lane) * V.  params(i, g, b) gives run i's
-// gamma and beta.  All threads of a block call this together; rows past the end store nothing.
-template <typename T, int V, int NI, int TPR, bool QUANT, typename Params>
-__device__ __forceinline__ void finish_row(const NormArgs &a, long long r, int lane, float (&v)[NI * V],
-                                           float (*scratch)[TPR > 32 ? TPR / 32 : 1], const Params &params)
-{
-    static_assert(NI * V % 2 == 0, "elements are handled in pairs");
-    const bool live = r < a.rows;
-    auto inside = [&](int i) { return (i * TPR + lane) * V < a.c; };
-    if (!QUANT || a.normalise) {
-        float2 s = both(0.0f);
-        for (int e = 0; e < NI * V; e += 2) s = __fadd2_rn(s, pair(v[e], v[e + 1]));
-        const float mean = row_sum<TPR>(s.x + s.y, scratch[0]) / (float)a.c;
-        s = both(0.0f);
-        if (V == 1) {
-            for (int i = 0; i < NI; ++i)
-                if (inside(i)) {
-                    v[i] -= mean;
-                    s.x = fmaf(v[i], v[i], s.x);
-                }
-        } else {
-            for (int i = 0; i < NI; ++i)
-                if (inside(i))
-                    for (int e = i * V; e < (i + 1) * V; e += 2) {
-                        const float2 d = __fadd2_rn(pair(v[e], v[e + 1]), both(-mean));
-                        s = __ffma2_rn(d, d, s);
-                        v[e] = d.x;
-                        v[e + 1] = d.y;
-                    }
-        }
-        const float rstd = 1.0f / sqrtf(row_sum<TPR>(s.x + s.y, scratch[1]) / (float)a.c + a.eps);
-        if (a.stats && lane == 0 && live) {
-            a.stats[r] = mean;
-            a.stats[a.rows + r] = rstd;
-        }
-        for (int i = 0; i < NI; ++i)
-            if (inside(i)) {
-                float g[V], b[V];
-                params(i, g, b);
-                if (V == 1) {
-                    v[i] = fmaf(v[i] * rstd, g[0], b[0]);
-                } else {
-                    for (int j = 0; j < V; j += 2) {
-                        const int e = i * V + j;
-                        const float2 h = __fmul2_rn(pair(v[e], v[e + 1]), both(rstd));
-                        const float2 y = __ffma2_rn(h, pair(g[j], g[j + 1]), pair(b[j], b[j + 1]));
-                        v[e] = y.x;
-                        v[e + 1] = y.y;
-                    }
-                }
-            }
-    }
-    if (QUANT) {
-        float most = 0.0f;
-        for (int e = 0; e < NI * V; e += 2) most = most_of(most, v[e], v[e + 1]);
-        most = row_most<TPR>(most, scratch[2]);
-        float inv;
-        const float scale = row_scale_of(__float_as_uint(most), &inv);
-        if (lane == 0 && live) a.row_scale[r] = scale;
-        // Adding 1.5 * 2^23 leaves a whole number, rounded to nearest even, in the low bits.  The products
-        // are scalar: a packed one is joined with the addition into one that rounds once, which tips values
-        // next to a half to the other side (seen against the definition's own arithmetic).
-        if (scale < __int_as_float(0x7f800000)) {
-            for (int e = 0; e < NI * V; e += 2) {
-                const float2 q = __fadd2_rn(pair(__fmul_rn(v[e], inv), __fmul_rn(v[e + 1], inv)), both(12582912.0f));
-                v[e] = q.x;
-                v[e + 1] = q.y;
-            }
-        } else {
-            for (int e = 0; e < NI * V; ++e) v[e] = 0.0f;
-        }
-        for (int i = 0; i < NI; ++i)
-            if (live && inside(i)) {
-                int q[V];
-                for (int j = 0; j < V; ++j) q[j] = __float_as_int(v[i * V + j]);
-                Vec<T, V>::store_q(a.q + r * a.q_stride + (i * TPR + lane) * V, q);
-            }
-    } else {
-        for (int i = 0; i < NI; ++i)
-            if (live && inside(i))
-                Vec<T, V>::store(static_cast<T *>(a.y) + r * a.y_stride + (i * TPR + lane) * V, v + i * V);
-    }
-}
-
-template <int V>
-__device__ __forceinline__ void load_params(const NormArgs &a, int c, float *g, float *b)
-{
-    using P = Vec<typename ParamOf<V>::type, V>;
-    for (int j = 0; j < V; ++j) g[j] = 1.0f, b[j] = 0.0f;
-    if (a.gamma) P::load_param(a.gamma + c, g);
-    if (a.beta) P::load_param(a.beta + c, b);
-}
-
-// One row for each TPR threads.
-template <typename T, int V, int NI, int TPR, bool QUANT>
-__global__ void __launch_bounds__(norm_block(TPR)) norm_rows_kernel(const NormArgs a)
-{
-    __shared__ float scratch[3][TPR > 32 ? TPR / 32 : 1];
-    dev::grid_dependency_wait();
-    dev::grid_dependents_launch();
-    const int lane = threadIdx.x % TPR;
-    const long long r = (long long)blockIdx.x * (norm_block(TPR) / TPR) + threadIdx.x / TPR;
-    const T *x = static_cast<const T *>(a.x) + r * a.x_stride;
-    Vec<T, V> raw[NI];
-    float v[NI * V];
-    for (int i = 0; i < NI; ++i) {
-        const int c = (i * TPR + lane) * V;
-        if (r < a.rows && c < a.c) raw[i].load(x + c);
-    }
-    for (int i = 0; i < NI; ++i) {
-        if (r < a.rows && (i * TPR + lane) * V < a.c)
-            raw[i].get(v + i * V);
-        else
-            for (int j = 0; j < V; ++j) v[i * V + j] = 0.0f;
-    }
-    finish_row<T, V, NI, TPR, QUANT>(a, r, lane, v, scratch, [&](int i, float *g, float *b) {
-        load_params<V>(a, (i * TPR + lane) * V, g, b);
-    });
-}
-
-// ------------------------------------------------------------------ many rows: parameters held, rows streamed
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Blocks that stay for many rows: each thread keeps the gamma and beta of its columns in registers and
-// copies its own part of the coming STAGES - 1 rows to shared memory with cp.async (no barrier: nobody
-// else reads it), so that memory stays busy while a row is summed.
-constexpr int kNormVecs = 4;  // vectors of a row per thread
+// Blocks stay for many rows.  Each thread keeps the gamma and beta of its columns in registers and copies
+// its own part of the coming kNormStages - 1 rows to shared memory with cp.async (no barrier: nobody else
+// reads it), so that memory stays busy while a row is summed.
 constexpr int kNormStages = 3;
-constexpr int norm_stream_blocks(int tpr) { return 512 / norm_block(tpr); }  // per SM: 128 registers a thread
-template <typename T, int TPR, bool QUANT>
-__global__ void __launch_bounds__(norm_block(TPR), norm_stream_blocks(TPR)) norm_stream_kernel(const NormArgs a)
+constexpr int norm_runs(int w) { return w == 16 ? 4 : 16; }  // of a row per thread
+// Threads of a block: one row, or as many as 128 threads hold while a row stays within a warp.
+constexpr int norm_block(int tpr) { return tpr <= 32 ? 128 : tpr; }
+constexpr int kSmThreads = 512;  // on an SM: 128 registers a thread
+
+template <typename T, int W, int TPR, bool QUANT>
+__global__ void __launch_bounds__(norm_block(TPR), kSmThreads / norm_block(TPR)) norm_stream_kernel(const NormArgs a)
 {
-    constexpr int V = 16 / sizeof(T), NI = kNormVecs;
-    constexpr int kBlock = norm_block(TPR), kGroups = kBlock / TPR;
-    __shared__ uint4 ring[kNormStages][NI][kBlock];
+    using R = Run<T, W>;
+    constexpr int V = R::V, NI = norm_runs(W), E = NI * V, kBlock = norm_block(TPR), kGroups = kBlock / TPR;
+    extern __shared__ __align__(16) unsigned char norm_ring[];  // [stage][run][thread] slots
     // Two sets: a row's first sum may be written while a slow warp still reads the last row's.
     __shared__ float scratch[2][3][TPR > 32 ? TPR / 32 : 1];
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
     const int lane = threadIdx.x % TPR;
     const long long step = (long long)gridDim.x * kGroups;
+    auto column = [&](int i) { return (i * TPR + lane) * V; };
+    auto slot = [&](int stage, int i) { return norm_ring + ((stage * NI + i) * kBlock + threadIdx.x) * R::SLOT; };
+    auto row_at = [&](long long r) { return static_cast<const T *>(a.x) + r * a.x_stride; };
+    auto odd = [&](long long r) { return sizeof(T) == 2 && W == 4 && reinterpret_cast<uintptr_t>(row_at(r)) % 4 != 0; };
     auto fetch = [&](long long r, int stage) {
         if (r < a.rows) {
-            const T *x = static_cast<const T *>(a.x) + r * a.x_stride;
-            for (int i = 0; i < NI; ++i) {
-                const int c = (i * TPR + lane) * V;
-                if (c < a.c) copy_async(dev::smem_u32(&ring[stage][i][threadIdx.x]), x + c);
-            }
+            const T *x = row_at(r);
+            const bool o = odd(r);
+            for (int i = 0; i < NI; ++i)
+                if (column(i) < a.c) R::copy(dev::smem_u32(slot(stage, i)), x + column(i), a.c - column(i), o);
         }
         copy_commit();
     };
     long long r = (long long)blockIdx.x * kGroups + threadIdx.x / TPR;
     for (int s = 0; s < kNormStages - 1; ++s) fetch(r + s * step, s);
-    float g[NI][V], b[NI][V];
-    for (int i = 0; i < NI; ++i)
-        if ((i * TPR + lane) * V < a.c) load_params<V>(a, (i * TPR + lane) * V, g[i], b[i]);
+    float2 g[(E + 1) / 2], b[(E + 1) / 2];
+    for (int i = 0; i < NI; ++i) {
+        load_params<V>(a.gamma ? a.gamma + column(i) : nullptr, 1.0f, a.c - column(i), reinterpret_cast<float *>(g) + i * V);
+        load_params<V>(a.beta ? a.beta + column(i) : nullptr, 0.0f, a.c - column(i), reinterpret_cast<float *>(b) + i * V);
+    }
+    const float per_c = 1.0f / (float)a.c;
     int stage = 0, parity = 0;
+    // All groups of a block go round together; rows past the end are zeros and store nothing.
     for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += step, r += step) {
         fetch(r + (kNormStages - 1) * step, stage == 0 ? kNormStages - 1 : stage - 1);
         copy_wait<kNormStages - 1>();
-        float v[NI * V];
+        const bool live = r < a.rows, o = odd(r);
+        float2 v[E / 2];
+        float *vs = reinterpret_cast<float *>(v);
         for (int i = 0; i < NI; ++i) {
-            if (r < a.rows && (i * TPR + lane) * V < a.c) {
-                Vec<T, V> raw;
-                raw.from(ring[stage][i][threadIdx.x]);
-                raw.get(v + i * V);
+            if (live && column(i) < a.c) {
+                if constexpr (V == 1)
+                    R::get(slot(stage, i), o, vs + i);
+                else
+                    R::get(slot(stage, i), o, v + i * (V / 2));
             } else {
-                for (int j = 0; j < V; ++j) v[i * V + j] = 0.0f;
+                for (int j = 0; j < V; ++j) vs[i * V + j] = 0.0f;
             }
         }
-        finish_row<T, V, NI, TPR, QUANT>(a, r, lane, v, scratch[parity], [&](int i, float *pg, float *pb) {
-            for (int j = 0; j < V; ++j) pg[j] = g[i][j], pb[j] = b[i][j];
-        });
+        if (!QUANT || a.normalise) {
+            float2 s = both(0.0f);
+            for (int e = 0; e < E / 2; ++e) s = __fadd2_rn(s, v[e]);
+            const float mean = row_sum<TPR>(s.x + s.y, scratch[parity][0]) * per_c;
+            // Around the mean, and 0 again where the row has no element.
+            for (int e = 0; e < E / 2; ++e) v[e] = __fadd2_rn(v[e], both(-mean));
+            for (int i = 0; i < NI; ++i)
+                if (column(i) + V > a.c)
+                    for (int j = 0; j < V; ++j)
+                        if (column(i) + j >= a.c) vs[i * V + j] = 0.0f;
+            s = both(0.0f);
+            for (int e = 0; e < E / 2; ++e) s = __ffma2_rn(v[e], v[e], s);
+            const float rstd = rsqrtf(row_sum<TPR>(s.x + s.y, scratch[parity][1]) * per_c + a.eps);
+            if (a.stats && lane == 0 && live) {
+                a.stats[r] = mean;
+                a.stats[a.rows + r] = rstd;
+            }
+            for (int e = 0; e < E / 2; ++e) v[e] = __ffma2_rn(__fmul2_rn(v[e], both(rstd)), g[e], b[e]);
+        }
+        if (QUANT) {
+            float most = 0.0f;
+            for (int e = 0; e < E / 2; ++e) most = most_of(most, v[e].x, v[e].y);
+            most = row_most<TPR>(most, scratch[parity][2]);
+            float inv;
+            const float scale = row_scale_of(__float_as_uint(most), &inv);
+            if (lane == 0 && live) a.row_scale[r] = scale;
+            // Adding 1.5 * 2^23 leaves a whole number, rounded to nearest even, in the low bits.  The products
+            // are scalar: a packed one is joined with the addition into one that rounds once, which tips values
+            // next to a half to the other side (seen against the definition's own arithmetic).
+            if (scale < __int_as_float(0x7f800000)) {
+                for (int e = 0; e < E / 2; ++e)
+                    v[e] = __fadd2_rn(make_float2(__fmul_rn(v[e].x, inv), __fmul_rn(v[e].y, inv)), both(12582912.0f));
+            } else {
+                for (int e = 0; e < E / 2; ++e) v[e] = both(0.0f);
+            }
+            if (live)
+                for (int i = 0; i < NI; ++i)
+                    if (column(i) < a.c) {
+                        int q[V];
+                        for (int j = 0; j < V; ++j) q[j] = __float_as_int(vs[i * V + j]);
+                        store_q<V>(a.q + r * a.q_stride + column(i), q, a.c - column(i));
+                    }
+        } else if (live) {
+            T *y = static_cast<T *>(a.y) + r * a.y_stride;
+            for (int i = 0; i < NI; ++i)
+                if (column(i) < a.c) {
+                    if constexpr (V == 1)
+                        R::store(y + column(i), vs + i, 1);
+                    else
+                        R::store(y + column(i), v + i * (V / 2), a.c - column(i));
+                }
+        }
         stage = stage + 1 == kNormStages ? 0 : stage + 1;
         parity ^= 1;
     }
@@ -564,23 +538,21 @@ __global__ void __launch_bounds__(norm_block(TPR), norm_stream_blocks(TPR)) norm
 
 unsigned blocks_for_rows(long long rows) { return (unsigned)(rows < (1LL << 20) ? rows : (1LL << 20)); }
 
-template <typename T, int V, int NI, int TPR>
-cudaError_t norm_rows_launch(const NormArgs &a, cudaStream_t stream)
-{
-    constexpr int kRows = norm_block(TPR) / TPR;
-    const dim3 grid((unsigned)((a.rows + kRows - 1) / kRows)), block(norm_block(TPR));
-    return a.q ? launch_overlapped(norm_rows_kernel<T, V, NI, TPR, true>, grid, block, 0, stream, 1, a)
-               : launch_overlapped(norm_rows_kernel<T, V, NI, TPR, false>, grid, block, 0, stream, 1, a);
-}
-
-template <typename T, int TPR>
+template <typename T, int W, int TPR>
 cudaError_t norm_stream_launch(const NormArgs &a, int sm_count, cudaStream_t stream)
 {
-    constexpr int kRows = norm_block(TPR) / TPR;
-    const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sm_count * norm_stream_blocks(TPR);
-    const dim3 grid((unsigned)(need < room ? need : room)), block(norm_block(TPR));
-    return a.q ? launch_overlapped(norm_stream_kernel<T, TPR, true>, grid, block, 0, stream, 1, a)
-               : launch_overlapped(norm_stream_kernel<T, TPR, false>, grid, block, 0, stream, 1, a);
+    constexpr int kBlock = norm_block(TPR), kRows = kBlock / TPR;
+    constexpr int kSmem = kNormStages * norm_runs(W) * kBlock * Run<T, W>::SLOT;
+    const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sm_count * (kSmThreads / kBlock);
+    const dim3 grid((unsigned)(need < room ? need : room)), block(kBlock);
+    static bool allowed[2][kMaxDevices] = {};
+    if (kSmem > 46 * 1024) {  // the sums take some of the first 48 KB
+        const cudaError_t e = a.q ? allow_dynamic_smem(norm_stream_kernel<T, W, TPR, true>, kSmem, allowed[1])
+                                  : allow_dynamic_smem(norm_stream_kernel<T, W, TPR, false>, kSmem, allowed[0]);
+        if (e != cudaSuccess) return e;
+    }
+    return a.q ? launch_overlapped(norm_stream_kernel<T, W, TPR, true>, grid, block, kSmem, stream, 1, a)
+               : launch_overlapped(norm_stream_kernel<T, W, TPR, false>, grid, block, kSmem, stream, 1, a);
 }
 
 bool aligned_for(const void *p, long long stride, int element, int bytes)
@@ -588,53 +560,50 @@ bool aligned_for(const void *p, long long stride, int element, int bytes)
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * element % bytes == 0;
 }
 
+// A row gets the fewest threads, a power of two of them, that hold it: more sum over more lanes (bf16,
+// 8192x4096 on 256 threads of two vectors each 37 us, on 128 of four 25 us), and a number of warps that only
+// the launch knows costs more than it saves (16384x4096 quantised 65 us against 47 us).
+template <typename T, int W>
+cudaError_t norm_stream_pick(const NormArgs &a, int sm_count, cudaStream_t stream, bool *done)
+{
+    constexpr int kHeld = norm_runs(W) * Run<T, W>::V;
+    *done = true;
+    if (a.c <= 4 * kHeld) return norm_stream_launch<T, W, 4>(a, sm_count, stream);
+    if (a.c <= 8 * kHeld) return norm_stream_launch<T, W, 8>(a, sm_count, stream);
+    if (a.c <= 16 * kHeld) return norm_stream_launch<T, W, 16>(a, sm_count, stream);
+    if (a.c <= 32 * kHeld) return norm_stream_launch<T, W, 32>(a, sm_count, stream);
+    if (a.c <= 64 * kHeld) return norm_stream_launch<T, W, 64>(a, sm_count, stream);
+    if (a.c <= 128 * kHeld) return norm_stream_launch<T, W, 128>(a, sm_count, stream);
+    if (a.c <= 256 * kHeld) return norm_stream_launch<T, W, 256>(a, sm_count, stream);
+    if (a.c <= 512 * kHeld) return norm_stream_launch<T, W, 512>(a, sm_count, stream);
+    *done = false;
+    return cudaSuccess;
+}
+
 template <typename T>
 cudaError_t norm_launch_t(const NormArgs &a, int sm_count, cudaStream_t stream)
 {
     constexpr int V = 16 / sizeof(T);
-    if (a.rows < (1LL << 31)) {
-        const bool wide_loads = a.c % V == 0 && aligned_for(a.x, a.x_stride, sizeof(T), 16) &&
-                                (a.q ? aligned_for(a.q, a.q_stride, 1, V) : aligned_for(a.y, a.y_stride, sizeof(T), 16)) &&
-                                aligned_for(a.gamma, 0, 4, 16) && aligned_for(a.beta, 0, 4, 16);
-        const int nv = a.c / V;
-        // Held parameters and streamed rows are the faster from few rows on: bf16, us with one row for
-        // each TPR threads against this, 8x4096 3.2 / 2.5, 600x1024 2.9 / 2.8, 2048x2048 7.1 / 6.5,
-        // 32768x4096 110 / 84 (6.4 TB/s), 32768x256 10.0 / 9.2.  TPR is the fewest threads that hold the
-        // row in four vectors each: more threads sum over more lanes (8192x4096 on 256: 37 us).
-        if (wide_loads) {
-            if (nv <= 4) return norm_rows_launch<T, V, 1, 4>(a, stream);
-            if (nv <= 16) return norm_stream_launch<T, 4>(a, sm_count, stream);
-            if (nv <= 32) return norm_stream_launch<T, 8>(a, sm_count, stream);
-            if (nv <= 64) return norm_stream_launch<T, 16>(a, sm_count, stream);
-            if (nv <= 128) return norm_stream_launch<T, 32>(a, sm_count, stream);
-            if (nv <= 256) return norm_stream_launch<T, 64>(a, sm_count, stream);
-            if (nv <= 512) return norm_stream_launch<T, 128>(a, sm_count, stream);
-            if (nv <= 1024) return norm_stream_launch<T, 256>(a, sm_count, stream);
-            if (nv <= 2048) return norm_rows_launch<T, V, 4, 512>(a, stream);
-        } else {
-            if (a.c <= 32) return norm_rows_launch<T, 1, 4, 8>(a, stream);
-            if (a.c <= 128) return norm_rows_launch<T, 1, 4, 32>(a, stream);
-            if (a.c <= 512) return norm_rows_launch<T, 1, 16, 32>(a, stream);
-            if (a.c <= 1024) return norm_rows_launch<T, 1, 8, 128>(a, stream);
-            if (a.c <= 2048) return norm_rows_launch<T, 1, 16, 128>(a, stream);
-            if (a.c <= 8192) return norm_rows_launch<T, 1, 32, 256>(a, stream);
-        }
-    }
+    const bool wide_loads = a.c % V == 0 && aligned_for(a.x, a.x_stride, sizeof(T), 16) &&
+                            (a.q ? aligned_for(a.q, a.q_stride, 1, V) : aligned_for(a.y, a.y_stride, sizeof(T), 16)) &&
+                            aligned_for(a.gamma, 0, 4, 16) && aligned_for(a.beta, 0, 4, 16);
+    bool done = false;
+    const cudaError_t e = wide_loads ? norm_stream_pick<T, 16>(a, sm_count, stream, &done)
+                                     : norm_stream_pick<T, 4>(a, sm_count, stream, &done);
+    if (done) return e;
     return launch_overlapped(norm_wide_kernel<T>, dim3(blocks_for_rows(a.rows)), dim3(kWideThreads), 0, stream, 1, a);
 }
 
 // ------------------------------------------------------------------ gradient, rows in registers
-// As norm_stream_kernel: blocks stay for many rows, TPR threads hold a row of x and dy (NI runs of V
-// elements each), and each thread keeps gamma and the running sums of dy * h and dy for its own columns
-// in registers, so that x and dy are read once for all three gradients.  The two sums over a row share
-// one barrier.  At the end the rows of a block are joined in shared memory, and each block writes one
+// As norm_stream_kernel, for x and dy: each thread keeps gamma and the running sums of dy * h and dy for its
+// own columns in registers, so that x and dy are read once for all three gradients.  The two sums over a row
+// share one barrier.  At the end the rows of a block are joined in shared memory, and each block writes one
 // row of partial sums, which norm_grad_join_kernel adds up in order.
 constexpr int kGradElements = 16;  // of a row per thread: sums, gamma, h and g of more would not fit 128 registers
 constexpr int kGradStages = 3;
 constexpr int grad_block(int tpr) { return tpr < 256 ? 256 : tpr; }
-constexpr int grad_blocks_per_sm(int tpr) { return 512 / grad_block(tpr); }
 
-// Sums of two values over the TPR threads of a row; scratch: 2 * TPR / 32 floats for each row of the block.
+// Sums of two values over the TPR threads of a row; scratch: a float2 for each warp of the block.
 template <int TPR>
 __device__ __forceinline__ float2 row_sum2(float2 v, float2 *scratch)
 {
@@ -643,21 +612,22 @@ __device__ __forceinline__ float2 row_sum2(float2 v, float2 *scratch)
         v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
     if constexpr (TPR > 32) {
+        constexpr int warps = TPR / 32;
         const int warp = threadIdx.x >> 5;
         if ((threadIdx.x & 31) == 0) scratch[warp] = v;
         __syncthreads();
         v = both(0.0f);
-        for (int i = 0; i < TPR / 32; ++i) v = __fadd2_rn(v, scratch[warp / (TPR / 32) * (TPR / 32) + i]);
+        for (int i = 0; i < warps; ++i) v = __fadd2_rn(v, scratch[warp / warps * warps + i]);
     }
     return v;
 }
 
-template <typename T, int V, int TPR>
-__global__ void __launch_bounds__(grad_block(TPR), grad_blocks_per_sm(TPR)) norm_grad_stream_kernel(const GradArgs a)
+template <typename T, int W, int TPR>
+__global__ void __launch_bounds__(grad_block(TPR), kSmThreads / grad_block(TPR)) norm_grad_stream_kernel(const GradArgs a)
 {
-    constexpr int E = kGradElements, NI = E / V, kBlock = grad_block(TPR), kGroups = kBlock / TPR;
-    constexpr bool kRing = V > 1;  // single elements are loaded without one
-    extern __shared__ uint4 grad_ring[];  // [stage][x, dy][NI][kBlock]; afterwards the join of the block's rows
+    using R = Run<T, W>;
+    constexpr int V = R::V, E = kGradElements, NI = E / V, kBlock = grad_block(TPR), kGroups = kBlock / TPR;
+    extern __shared__ __align__(16) unsigned char grad_ring[];  // [stage][x, dy][run][thread] slots; then the join
     __shared__ float2 scratch[2][kBlock / 32];
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
@@ -665,21 +635,22 @@ __global__ void __launch_bounds__(grad_block(TPR), grad_blocks_per_sm(TPR)) norm
     const long long step = (long long)gridDim.x * kGroups;
     auto column = [&](int i) { return (i * TPR + lane) * V; };
     auto slot = [&](int stage, int which, int i) {
-        return grad_ring + ((stage * 2 + which) * NI + i) * kBlock + threadIdx.x;
+        return grad_ring + (((stage * 2 + which) * NI + i) * kBlock + threadIdx.x) * R::SLOT;
     };
+    auto x_at = [&](long long r) { return static_cast<const T *>(a.x) + r * a.x_stride; };
+    auto dy_at = [&](long long r) { return static_cast<const T *>(a.dy) + r * a.dy_stride; };
+    auto odd = [&](const T *p) { return sizeof(T) == 2 && W == 4 && reinterpret_cast<uintptr_t>(p) % 4 != 0; };
     auto fetch = [&](long long r, int stage) {
-        if constexpr (kRing) {
-            if (r < a.rows) {
-                const T *x = static_cast<const T *>(a.x) + r * a.x_stride;
-                const T *dy = static_cast<const T *>(a.dy) + r * a.dy_stride;
-                for (int i = 0; i < NI; ++i)
-                    if (column(i) < a.c) {
-                        copy_async(dev::smem_u32(slot(stage, 0, i)), x + column(i));
-                        copy_async(dev::smem_u32(slot(stage, 1, i)), dy + column(i));
-                    }
-            }
-            copy_commit();
+        if (r < a.rows) {
+            const T *x = x_at(r), *dy = dy_at(r);
+            const bool ox = odd(x), ody = odd(dy);
+            for (int i = 0; i < NI; ++i)
+                if (column(i) < a.c) {
+                    R::copy(dev::smem_u32(slot(stage, 0, i)), x + column(i), a.c - column(i), ox);
+                    R::copy(dev::smem_u32(slot(stage, 1, i)), dy + column(i), a.c - column(i), ody);
+                }
         }
+        copy_commit();
     };
     auto moments = [&](long long r) {
         return r < a.rows ? make_float2(__ldg(a.stats + r), __ldg(a.stats + a.rows + r)) : both(0.0f);
@@ -687,101 +658,97 @@ __global__ void __launch_bounds__(grad_block(TPR), grad_blocks_per_sm(TPR)) norm
     long long r = (long long)blockIdx.x * kGroups + threadIdx.x / TPR;
     for (int s = 0; s < kGradStages - 1; ++s) fetch(r + s * step, s);
     float2 next = moments(r);
-    float gamma[E], dg[E], db[E];
-    for (int i = 0; i < NI; ++i) {
-        for (int j = 0; j < V; ++j) gamma[i * V + j] = 1.0f;
-        if (a.gamma && column(i) < a.c) Vec<typename ParamOf<V>::type, V>::load_param(a.gamma + column(i), gamma + i * V);
-    }
-    for (int e = 0; e < E; ++e) dg[e] = db[e] = 0.0f;
+    float2 gamma[E / 2], dg[E / 2], db[E / 2];
+    for (int i = 0; i < NI; ++i)
+        load_params<V>(a.gamma ? a.gamma + column(i) : nullptr, 1.0f, a.c - column(i),
+                       reinterpret_cast<float *>(gamma) + i * V);
+    for (int e = 0; e < E / 2; ++e) dg[e] = db[e] = both(0.0f);
     const float per_c = 1.0f / (float)a.c;
     int stage = 0, parity = 0;
     for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += step, r += step) {
         fetch(r + (kGradStages - 1) * step, stage == 0 ? kGradStages - 1 : stage - 1);
-        const float2 moment = next;
+        const float mean = next.x, rstd = next.y;
         next = moments(r + step);
-        if (kRing) copy_wait<kGradStages - 1>();
-        const float mean = moment.x, rstd = moment.y;
-        float h[E], g[E];
-        Vec<T, V> xs[NI], dys[NI];
-        for (int i = 0; i < NI; ++i)
-            if (r < a.rows && column(i) < a.c) {
-                if constexpr (kRing) {
-                    xs[i].from(*slot(stage, 0, i));
-                    dys[i].from(*slot(stage, 1, i));
-                } else {
-                    xs[i].load(static_cast<const T *>(a.x) + r * a.x_stride + column(i));
-                    dys[i].load(static_cast<const T *>(a.dy) + r * a.dy_stride + column(i));
-                }
-            }
-        float2 s1 = both(0.0f), s2 = both(0.0f);
+        copy_wait<kGradStages - 1>();
+        const bool live = r < a.rows, ox = odd(x_at(r)), ody = odd(dy_at(r));
+        float2 h[E / 2], g[E / 2];
+        float *hs = reinterpret_cast<float *>(h), *gs = reinterpret_cast<float *>(g);
         for (int i = 0; i < NI; ++i) {
-            if (r < a.rows && column(i) < a.c) {
-                xs[i].get(h + i * V);
-                dys[i].get(g + i * V);
+            if (live && column(i) < a.c) {
+                if constexpr (V == 1) {
+                    R::get(slot(stage, 0, i), ox, hs + i);
+                    R::get(slot(stage, 1, i), ody, gs + i);
+                } else {
+                    R::get(slot(stage, 0, i), ox, h + i * (V / 2));
+                    R::get(slot(stage, 1, i), ody, g + i * (V / 2));
+                }
             } else {  // adds nothing anywhere: h and dy are both 0
-                for (int j = 0; j < V; ++j) h[i * V + j] = mean, g[i * V + j] = 0.0f;
+                for (int j = 0; j < V; ++j) hs[i * V + j] = mean, gs[i * V + j] = 0.0f;
             }
         }
-        for (int e = 0; e < E; e += 2) {
-            const float2 d = pair(g[e], g[e + 1]);
-            const float2 hh = __fmul2_rn(__fadd2_rn(pair(h[e], h[e + 1]), both(-mean)), both(rstd));
-            const float2 sum_g = __ffma2_rn(d, hh, pair(dg[e], dg[e + 1]));
-            const float2 sum_b = __fadd2_rn(d, pair(db[e], db[e + 1]));
-            const float2 gg = __fmul2_rn(d, pair(gamma[e], gamma[e + 1]));
-            s1 = __fadd2_rn(s1, gg);
-            s2 = __ffma2_rn(gg, hh, s2);
-            dg[e] = sum_g.x, dg[e + 1] = sum_g.y;
-            db[e] = sum_b.x, db[e + 1] = sum_b.y;
-            h[e] = hh.x, h[e + 1] = hh.y;
-            g[e] = gg.x, g[e + 1] = gg.y;
+        float2 s1 = both(0.0f), s2 = both(0.0f);
+        for (int e = 0; e < E / 2; ++e) {
+            const float2 d = g[e];
+            h[e] = __fmul2_rn(__fadd2_rn(h[e], both(-mean)), both(rstd));
+            dg[e] = __ffma2_rn(d, h[e], dg[e]);
+            db[e] = __fadd2_rn(d, db[e]);
+            g[e] = __fmul2_rn(d, gamma[e]);
+            s1 = __fadd2_rn(s1, g[e]);
+            s2 = __ffma2_rn(g[e], h[e], s2);
         }
         const float2 sums = row_sum2<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), scratch[parity]);
         const float m1 = sums.x * per_c, m2 = sums.y * per_c;
-        for (int e = 0; e < E; e += 2) {
-            const float2 t = __fadd2_rn(__ffma2_rn(pair(h[e], h[e + 1]), both(-m2), pair(g[e], g[e + 1])), both(-m1));
-            const float2 d = __fmul2_rn(t, both(rstd));
-            h[e] = d.x, h[e + 1] = d.y;
-        }
-        if (r < a.rows)
+        for (int e = 0; e < E / 2; ++e)
+            h[e] = __fmul2_rn(__fadd2_rn(__ffma2_rn(h[e], both(-m2), g[e]), both(-m1)), both(rstd));
+        if (live) {
+            T *dx = static_cast<T *>(a.dx) + r * a.dx_stride;
             for (int i = 0; i < NI; ++i)
-                if (column(i) < a.c)
-                    Vec<T, V>::store(static_cast<T *>(a.dx) + r * a.dx_stride + column(i), h + i * V);
+                if (column(i) < a.c) {
+                    if constexpr (V == 1)
+                        R::store(dx + column(i), hs + i, 1);
+                    else
+                        R::store(dx + column(i), h + i * (V / 2), a.c - column(i));
+                }
+        }
         stage = stage + 1 == kGradStages ? 0 : stage + 1;
         parity ^= 1;
     }
-    if (kRing) copy_wait<0>();
+    copy_wait<0>();
     float *out = a.partial + (long long)blockIdx.x * 2 * a.c;
+    float *dgs = reinterpret_cast<float *>(dg), *dbs = reinterpret_cast<float *>(db);
     if constexpr (kGroups == 1) {
         for (int i = 0; i < NI; ++i)
-            if (column(i) < a.c) {
-                if constexpr (V == 1) {
-                    out[column(i)] = dg[i];
-                    out[a.c + column(i)] = db[i];
-                } else {
-                    for (int j = 0; j < V; j += 4) {
-                        const int e = i * V + j;
-                        *reinterpret_cast<float4 *>(out + column(i) + j) = make_float4(dg[e], dg[e + 1], dg[e + 2], dg[e + 3]);
-                        *reinterpret_cast<float4 *>(out + a.c + column(i) + j) =
-                            make_float4(db[e], db[e + 1], db[e + 2], db[e + 3]);
+            for (int j = 0; j < V; ++j)
+                if (column(i) + j < a.c) {
+                    if constexpr (V >= 4) {
+                        if (j % 4 == 0) {
+                            const int e = i * V + j;
+                            *reinterpret_cast<float4 *>(out + column(i) + j) =
+                                make_float4(dgs[e], dgs[e + 1], dgs[e + 2], dgs[e + 3]);
+                            *reinterpret_cast<float4 *>(out + a.c + column(i) + j) =
+                                make_float4(dbs[e], dbs[e + 1], dbs[e + 2], dbs[e + 3]);
+                        }
+                    } else {
+                        out[column(i) + j] = dgs[i * V + j];
+                        out[a.c + column(i) + j] = dbs[i * V + j];
                     }
                 }
-            }
     } else {
         // The block's rows side by side in shared memory, [row][dgamma, dbeta][element][thread]; those of one
         // warp are joined by shuffles before.
         constexpr int kSide = TPR < 32 ? kBlock / 32 : kGroups;
         for (int o = TPR; o < 32; o <<= 1)
             for (int e = 0; e < E; ++e) {
-                dg[e] += __shfl_xor_sync(0xffffffffu, dg[e], o);
-                db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+                dgs[e] += __shfl_xor_sync(0xffffffffu, dgs[e], o);
+                dbs[e] += __shfl_xor_sync(0xffffffffu, dbs[e], o);
             }
         float *join = reinterpret_cast<float *>(grad_ring);
         __syncthreads();  // the ring is no longer read
         if (TPR >= 32 || (threadIdx.x & 31) < TPR) {
             float *mine = join + (TPR < 32 ? threadIdx.x / 32 : threadIdx.x / TPR) * (2 * E * TPR) + lane;
             for (int e = 0; e < E; ++e) {
-                mine[e * TPR] = dg[e];
-                mine[(E + e) * TPR] = db[e];
+                mine[e * TPR] = dgs[e];
+                mine[(E + e) * TPR] = dbs[e];
             }
         }
         __syncthreads();
@@ -802,45 +769,46 @@ cudaError_t norm_grad_join(const GradArgs &a, cudaStream_t stream)
                              stream, 1, a);
 }
 
-template <typename T, int V, int TPR>
+template <typename T, int W, int TPR>
 cudaError_t norm_grad_stream_launch(GradArgs a, int sm_count, cudaStream_t stream)
 {
-    constexpr int kRows = grad_block(TPR) / TPR;
-    constexpr int kRing = V > 1 ? kGradStages * 2 * (kGradElements / V) * grad_block(TPR) * 16 : 0;
-    constexpr int kJoin = kRows > 1 ? (TPR < 32 ? 8 : kRows) * 2 * kGradElements * TPR * 4 : 0;
+    constexpr int kBlock = grad_block(TPR), kRows = kBlock / TPR;
+    constexpr int kRing = kGradStages * 2 * (kGradElements / Run<T, W>::V) * kBlock * Run<T, W>::SLOT;
+    constexpr int kJoin = kRows > 1 ? (TPR < 32 ? kBlock / 32 : kRows) * 2 * kGradElements * TPR * 4 : 0;
     constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
     static bool allowed[kMaxDevices] = {};
     if (kSmem > 46 * 1024) {  // the sums of a block take some of the first 48 KB
-        cudaError_t e = allow_dynamic_smem(norm_grad_stream_kernel<T, V, TPR>, kSmem, allowed);
+        cudaError_t e = allow_dynamic_smem(norm_grad_stream_kernel<T, W, TPR>, kSmem, allowed);
         if (e != cudaSuccess) return e;
     }
-    const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sm_count * grad_blocks_per_sm(TPR);
+    const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sm_count * (kSmThreads / kBlock);
     a.partial_rows = (int)(need < room ? need : room);
-    cudaError_t e = launch_overlapped(norm_grad_stream_kernel<T, V, TPR>, dim3((unsigned)a.partial_rows),
-                                      dim3(grad_block(TPR)), kSmem, stream, 1, a);
+    cudaError_t e = launch_overlapped(norm_grad_stream_kernel<T, W, TPR>, dim3((unsigned)a.partial_rows), dim3(kBlock),
+                                      kSmem, stream, 1, a);
     return e == cudaSuccess ? norm_grad_join(a, stream) : e;
+}
+
+template <typename T, int W>
+cudaError_t norm_grad_stream_pick(const GradArgs &a, int sm_count, cudaStream_t stream)
+{
+    if (a.c <= 8 * kGradElements) return norm_grad_stream_launch<T, W, 8>(a, sm_count, stream);
+    if (a.c <= 16 * kGradElements) return norm_grad_stream_launch<T, W, 16>(a, sm_count, stream);
+    if (a.c <= 32 * kGradElements) return norm_grad_stream_launch<T, W, 32>(a, sm_count, stream);
+    if (a.c <= 64 * kGradElements) return norm_grad_stream_launch<T, W, 64>(a, sm_count, stream);
+    if (a.c <= 128 * kGradElements) return norm_grad_stream_launch<T, W, 128>(a, sm_count, stream);
+    if (a.c <= 256 * kGradElements) return norm_grad_stream_launch<T, W, 256>(a, sm_count, stream);
+    return norm_grad_stream_launch<T, W, 512>(a, sm_count, stream);
 }
 
 template <typename T>
 cudaError_t norm_grad_launch_t(const GradArgs &a, int sm_count, cudaStream_t stream)
 {
     constexpr int V = 16 / sizeof(T);
-    const bool wide_loads = a.c % V == 0 && aligned_for(a.x, a.x_stride, sizeof(T), 16) &&
-                            aligned_for(a.dy, a.dy_stride, sizeof(T), 16) &&
-                            aligned_for(a.dx, a.dx_stride, sizeof(T), 16) && aligned_for(a.gamma, 0, 4, 16);
-    if (wide_loads) {
-        if (a.c <= 8 * kGradElements) return norm_grad_stream_launch<T, V, 8>(a, sm_count, stream);
-        if (a.c <= 16 * kGradElements) return norm_grad_stream_launch<T, V, 16>(a, sm_count, stream);
-        if (a.c <= 32 * kGradElements) return norm_grad_stream_launch<T, V, 32>(a, sm_count, stream);
-        if (a.c <= 64 * kGradElements) return norm_grad_stream_launch<T, V, 64>(a, sm_count, stream);
-        if (a.c <= 128 * kGradElements) return norm_grad_stream_launch<T, V, 128>(a, sm_count, stream);
-        if (a.c <= 256 * kGradElements) return norm_grad_stream_launch<T, V, 256>(a, sm_count, stream);
-        if (a.c <= 512 * kGradElements) return norm_grad_stream_launch<T, V, 512>(a, sm_count, stream);
-    } else {
-        if (a.c <= 8 * kGradElements) return norm_grad_stream_launch<T, 1, 8>(a, sm_count, stream);
-        if (a.c <= 32 * kGradElements) return norm_grad_stream_launch<T, 1, 32>(a, sm_count, stream);
-        if (a.c <= 128 * kGradElements) return norm_grad_stream_launch<T, 1, 128>(a, sm_count, stream);
-        if (a.c <= 512 * kGradElements) return norm_grad_stream_launch<T, 1, 512>(a, sm_count, stream);
+    if (a.c <= 512 * kGradElements) {
+        const bool wide_loads = a.c % V == 0 && aligned_for(a.x, a.x_stride, sizeof(T), 16) &&
+                                aligned_for(a.dy, a.dy_stride, sizeof(T), 16) &&
+                                aligned_for(a.dx, a.dx_stride, sizeof(T), 16) && aligned_for(a.gamma, 0, 4, 16);
+        return wide_loads ? norm_grad_stream_pick<T, 16>(a, sm_count, stream) : norm_grad_stream_pick<T, 4>(a, sm_count, stream);
     }
     cudaError_t e = launch_overlapped(norm_grad_wide_kernel<T>, dim3(blocks_for_rows(a.rows)), dim3(kWideThreads), 0,
                                       stream, 1, a);
