@@ -57,6 +57,13 @@ __device__ __forceinline__ void from_float(float v, float *out) { *out = v; }
 __device__ __forceinline__ void from_float(float v, __nv_bfloat16 *out) { *out = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void from_float(float v, __half *out) { *out = __float2half_rn(v); }
 
+// Brings `bytes` bytes (a multiple of 16, from a 16-byte boundary) into L2.  Only a hint, so it may run
+// before grid_dependency_wait(): weights are on their way while the kernel before still quantises the rows.
+__device__ __forceinline__ void prefetch_l2(const void *p, uint32_t bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // A predicated 16-byte load straight into its registers, zeros without it: behind a branch the value would
 // be moved, and the warp wait for it, where the branches meet.
 __device__ __forceinline__ uint4 load_or_zero(const void *p, bool exists)

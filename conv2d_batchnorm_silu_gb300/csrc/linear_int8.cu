@@ -60,12 +60,26 @@ __global__ void __launch_bounds__(32 * kFewWarps, ALIGNED && ROWS <= 2 ? 4 : (RO
 {
     constexpr int R = kFewChannels;
     __shared__ int part[kFewWarps][R * ROWS];
-    dev::grid_dependency_wait();
-    dev::grid_dependents_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = 1 << split_log2, groups = kFewWarps >> split_log2;
     const int n0 = (blockIdx.x * groups + (warp >> split_log2)) * R;
     const int m = (int)a.e.m;
+    if constexpr (ALIGNED) {
+        const int n = blockIdx.x * groups * R + threadIdx.x;
+        if (threadIdx.x < groups * R && n < a.e.n && a.k > 0) prefetch_l2(a.w + n * a.w_stride, (uint32_t)a.k);
+    }
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+    // This thread's output, whose scales load along with the weights.
+    const int out_e = threadIdx.x % (R * ROWS), out_i = out_e / R;
+    const int out_n = (blockIdx.x * groups + threadIdx.x / (R * ROWS)) * R + out_e % R;
+    const bool has_out = threadIdx.x < groups * R * ROWS && out_i < m && out_n < a.e.n;
+    float scale = 0.0f, bias = 0.0f, residual = 0.0f;
+    if (has_out) {
+        scale = __ldg(a.e.a_scale + out_i) * __ldg(a.e.w_scale + out_n);
+        if (a.e.bias) bias = __ldg(a.e.bias + out_n);
+        if (a.e.residual) residual = to_float(static_cast<const T *>(a.e.residual)[out_i * a.e.residual_stride + out_n]);
+    }
     const int8_t *w[R], *x[ROWS];
 #pragma unroll
     for (int r = 0; r < R; ++r) w[r] = a.w + (long long)min(n0 + r, a.e.n - 1) * a.w_stride;
@@ -100,12 +114,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, ALIGNED && ROWS <= 2 ? 4 : (RO
             if (lane == 0) part[warp][i * R + r] = s;
         }
     __syncthreads();
-    for (int o = threadIdx.x; o < groups * R * ROWS; o += 32 * kFewWarps) {
-        const int g = o / (R * ROWS), e = o % (R * ROWS), i = e / R;
-        const int n = (blockIdx.x * groups + g) * R + e % R;
+    static_assert(R * ROWS * kFewWarps <= 32 * kFewWarps, "one output a thread");
+    if (has_out) {
+        const int g = threadIdx.x / (R * ROWS);
         int s = 0;
-        for (int t = 0; t < split; ++t) s += part[g * split + t][e];
-        if (i < m && n < a.e.n) finish_one<T>(a.e, (float)s, i, n);
+        for (int t = 0; t < split; ++t) s += part[g * split + t][out_e];
+        const float z = activated(fmaf((float)s, scale, bias), a.e.activation) + residual;
+        from_float(z, static_cast<T *>(a.e.y) + out_i * a.e.y_stride + out_n);
     }
 }
 

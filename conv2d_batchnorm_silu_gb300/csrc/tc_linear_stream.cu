@@ -25,6 +25,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far beyond any legitimate w
 
 constexpr int kChannels = 128;  // of a tile
 constexpr int kStep = 128;      // K elements per step: two swizzle spans of f16
+constexpr int kPrefetch = 1024;  // bytes of each weights row that the start of a run brings into L2
 constexpr int kWidenWarps = 16;
 constexpr int kEpiWarps = 4;
 constexpr int kThreads = 32 * (kWidenWarps + kEpiWarps + 1);
@@ -135,6 +136,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     dev::tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     const int g0 = run_start(a, blockIdx.x), steps = run_start(a, blockIdx.x + 1) - g0;
+    if (threadIdx.x < kChannels) {
+        // The weights of the run's first steps.
+        const int tile = g0 / a.k_steps, k0 = (g0 - tile * a.k_steps) * kStep;
+        const int n = min(tile / a.row_tiles * kChannels + (int)threadIdx.x, a.e.n - 1);
+        prefetch_l2(a.w + n * a.w_stride + k0, (uint32_t)min(a.k - k0, kPrefetch));
+    }
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
 
