@@ -134,14 +134,30 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// As mbar_wait_bounded; waits here are often a little early, and reading the clock at the first
-// unsuccessful poll would cost more than most of them last.
+// Waits for a barrier's phase while the hardware holds the thread back, up to 20 us at a time, so that
+// waiting warps leave the issue slots to the working ones.  False if the abort flag is raised or timeout_ns
+// pass.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, const volatile int *abort_flag,
                                              uint64_t timeout_ns)
 {
-    for (int i = 0; i < 64; ++i)
-        if (dev::mbar_try_wait(bar, parity)) return true;
-    return dev::mbar_wait_bounded(bar, parity, abort_flag, timeout_ns);
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((i & 7u) == 7) {
+            if (abort_flag != nullptr && *abort_flag) return false;
+            const uint64_t now = dev::globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > timeout_ns) return false;
+        }
+    }
 }
 
 // Instruction descriptor of kind::f16 with f16 A and B (format 0), both K-major, fp32 D.
@@ -163,6 +179,17 @@ __device__ __forceinline__ float exp2_approx(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float2 lds_pair(uint32_t addr)
+{
+    float2 v;
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_pair(uint32_t addr, float2 v)
+{
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
 
 // One output: the general form.
@@ -239,97 +266,128 @@ __device__ __forceinline__ void stage_params(const LinearEpilogue &e, int col0, 
     dev::sts_u32(dst + 128 + 4 * lane, __float_as_uint(b));
 }
 
-// A warp's block of 32 rows x 32 columns from (row0, col0): lane l holds row row0 + l, its 32 sums in
-// v.  Rows and columns past the end are computed and not stored.  `stg` is the warp's own 32 x 32
-// elements of shared memory, through which lanes exchange rows for columns, so that each store covers
-// whole runs of a row; 16-byte pieces are swizzled so that neither direction meets a bank twice.  The
-// block's scales and biases are in shared memory at `params` (stage_params).
+// A warp's 32 rows x 32 columns of a TMEM accumulator from column `col` on, in the layout of a matrix
+// instruction's result: with g = lane / 4 and t = lane % 4, v[16 h + 4 j + 2 i + e] is row 16 h + 8 i + g,
+// column 8 j + 2 t + e.  A lane so holds 8 columns of 4 rows and needs the scales of those only.
+__device__ __forceinline__ void load_block(uint32_t taddr, uint32_t col, uint32_t *v)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t *r = v + 16 * h;
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x4.b32"
+            " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+              "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr + ((uint32_t)(16 * h) << 16) + col));
+    }
+}
+
+// What becomes of such a block, from row row0 and column col0 of the output: sums in v, row_scale[i] the
+// scale of row 8 i + g, scales and biases of the columns in shared memory at `params` (stage_params).  Rows and
+// columns past the end are computed and not stored.  `stg` is the warp's own 32 x 32 elements of shared
+// memory, through which lanes exchange pairs for runs of a row, so that each store covers whole sectors; its
+// 16-byte pieces are swizzled so that neither direction meets a bank twice.  (Each lane with a row of its own,
+// as TMEM gives it by default, took 64 of a block's 112 shared-memory cycles for the columns' scales alone:
+// 25600x256x1024 with SiLU 27 us, this layout %s.)
 template <typename T>
 __device__ __forceinline__ void finish_block(const LinearEpilogue &e, const uint32_t *sums, uint32_t params,
-                                             float row_scale, long long row0, int col0, uint32_t stg, int lane)
+                                             const float *row_scale, long long row0, int col0, uint32_t stg, int lane)
 {
-    constexpr int kPieces = 32 * sizeof(T) / 16;      // 16-byte pieces of a row
-    constexpr int kPer = 16 / sizeof(T);              // elements of a piece
+    constexpr int kPieces = 32 * sizeof(T) / 16;  // 16-byte pieces of a row
+    constexpr int kPer = 16 / sizeof(T);          // elements of a piece
+    const int g = lane >> 2, t = lane & 3;
     const bool whole = col0 + 32 <= e.n;
-    const long long row = row0 + lane;
-    float v[32];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint4 s = dev::lds_v4(params + 16 * i), b = dev::lds_v4(params + 128 + 16 * i);
-        const float2 r = make_float2(row_scale, row_scale);
-        const float2 lo = __ffma2_rn(make_float2(__uint_as_float(sums[4 * i]), __uint_as_float(sums[4 * i + 1])),
-                                     __fmul2_rn(r, make_float2(__uint_as_float(s.x), __uint_as_float(s.y))),
-                                     make_float2(__uint_as_float(b.x), __uint_as_float(b.y)));
-        const float2 hi = __ffma2_rn(make_float2(__uint_as_float(sums[4 * i + 2]), __uint_as_float(sums[4 * i + 3])),
-                                     __fmul2_rn(r, make_float2(__uint_as_float(s.z), __uint_as_float(s.w))),
-                                     make_float2(__uint_as_float(b.z), __uint_as_float(b.w)));
-        v[4 * i] = lo.x;
-        v[4 * i + 1] = lo.y;
-        v[4 * i + 2] = hi.x;
-        v[4 * i + 3] = hi.y;
-    }
-    if (e.activation == CBS_ACT_SILU) {
-        silu32(v);
-    } else if (e.activation == CBS_ACT_RELU) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = activated(v[i], CBS_ACT_RELU);
-    }
-    if (e.residual && row < e.m) {
-        const T *res = static_cast<const T *>(e.residual) + row * e.residual_stride + col0;
-        if (whole && e.vec_residual) {
-#pragma unroll
-            for (int q = 0; q < kPieces; ++q) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(res + q * kPer);
-                if constexpr (sizeof(T) == 4) {
-                    v[4 * q] += __uint_as_float(w.x);
-                    v[4 * q + 1] += __uint_as_float(w.y);
-                    v[4 * q + 2] += __uint_as_float(w.z);
-                    v[4 * q + 3] += __uint_as_float(w.w);
-                } else {
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 f = unpack2(u[k], T());
-                        v[8 * q + 2 * k] += f.x;
-                        v[8 * q + 2 * k + 1] += f.y;
-                    }
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (col0 + i < e.n) v[i] += to_float(res[i]);
-        }
-    }
-    auto at = [&](int r, int q) {
-        const int turn = kPieces == 8 ? (r & 7) : ((r >> 1) & 3);
+    const int rows = e.m - row0 < 32 ? (int)(e.m - row0) : 32;
+    // Where piece q of row r lies, and this lane's pair j of row r.
+    auto piece_at = [&](int r, int q) {
+        const int turn = kPieces == 8 ? 2 * (r & 3) : (r >> 1) & 3;
         return stg + (uint32_t)(r * (32 * (int)sizeof(T)) + ((q ^ turn) * 16));
     };
-    __syncwarp();  // the block before has been read
+    auto pair_at = [&](int r, int j) {
+        return sizeof(T) == 4 ? piece_at(r, 2 * j + (t >> 1)) + (uint32_t)(t & 1) * 8 : piece_at(r, j) + (uint32_t)t * 4;
+    };
+    auto row_of = [&](int i) { return 8 * i + g; };  // rows 0 to 3 of this lane
+    const int q = lane % kPieces, r0 = lane / kPieces;  // this lane's piece on the way to or from memory
+    constexpr int kRowsAtOnce = 32 / kPieces;
+    float2 v[16];  // [row of this lane][j]
+    {
+        float2 scale[4], bias[4];
 #pragma unroll
-    for (int q = 0; q < kPieces; ++q) {
-        if constexpr (sizeof(T) == 4)
-            dev::sts_v4(at(lane, q), __float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
-                        __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-        else
-            dev::sts_v4(at(lane, q), pack2(v[8 * q], v[8 * q + 1], T()), pack2(v[8 * q + 2], v[8 * q + 3], T()),
-                        pack2(v[8 * q + 4], v[8 * q + 5], T()), pack2(v[8 * q + 6], v[8 * q + 7], T()));
+        for (int j = 0; j < 4; ++j) {
+            scale[j] = lds_pair(params + 4 * (8 * j + 2 * t));
+            bias[j] = lds_pair(params + 128 + 4 * (8 * j + 2 * t));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t *s = sums + 16 * (i >> 1) + 4 * j + 2 * (i & 1);
+                v[4 * i + j] = __ffma2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])),
+                                          __fmul2_rn(scale[j], make_float2(row_scale[i], row_scale[i])), bias[j]);
+            }
     }
+    if (e.activation == CBS_ACT_SILU) {
+        silu32(reinterpret_cast<float *>(v));
+    } else if (e.activation == CBS_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = make_float2(activated(v[i].x, CBS_ACT_RELU), activated(v[i].y, CBS_ACT_RELU));
+    }
+    __syncwarp();  // the block before has been read
+    if (e.residual) {
+        const T *res = static_cast<const T *>(e.residual) + row0 * e.residual_stride + col0;
+        if (whole && e.vec_residual) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int r = i * kRowsAtOnce + r0;
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (r < rows) w = *reinterpret_cast<const uint4 *>(res + r * e.residual_stride + q * kPer);
+                dev::sts_v4(piece_at(r, q), w.x, w.y, w.z, w.w);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (sizeof(T) == 4)
+                        v[4 * i + j] = __fadd2_rn(v[4 * i + j], lds_pair(pair_at(row_of(i), j)));
+                    else
+                        v[4 * i + j] = __fadd2_rn(v[4 * i + j], unpack2(dev::lds_u32(pair_at(row_of(i), j)), T()));
+                }
+            __syncwarp();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const T *p = res + row_of(i) * e.residual_stride + 8 * j + 2 * t;
+                    if (row_of(i) < rows && col0 + 8 * j + 2 * t < e.n) v[4 * i + j].x += to_float(p[0]);
+                    if (row_of(i) < rows && col0 + 8 * j + 2 * t + 1 < e.n) v[4 * i + j].y += to_float(p[1]);
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (sizeof(T) == 4)
+                sts_pair(pair_at(row_of(i), j), v[4 * i + j]);
+            else
+                dev::sts_u32(pair_at(row_of(i), j), pack2(v[4 * i + j].x, v[4 * i + j].y, T()));
+        }
     __syncwarp();
     T *y = static_cast<T *>(e.y) + row0 * e.y_stride + col0;
     if (whole && e.vec_y) {
         uint4 w[kPieces];  // all loaded before the first is stored
-        const int q = lane % kPieces, r0 = lane / kPieces, rows = e.m - row0 < 32 ? (int)(e.m - row0) : 32;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) w[i] = dev::lds_v4(at(i * (32 / kPieces) + r0, q));
+        for (int i = 0; i < kPieces; ++i) w[i] = dev::lds_v4(piece_at(i * kRowsAtOnce + r0, q));
         T *to = y + r0 * e.y_stride + q * kPer;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-            if (i * (32 / kPieces) + r0 < rows)
-                *reinterpret_cast<uint4 *>(to + i * (32 / kPieces) * e.y_stride) = w[i];
+            if (i * kRowsAtOnce + r0 < rows) *reinterpret_cast<uint4 *>(to + i * kRowsAtOnce * e.y_stride) = w[i];
     } else if (col0 + lane < e.n) {
-        for (int r = 0; r < 32 && row0 + r < e.m; ++r) {
-            const uint32_t addr = at(r, lane / kPer) + (uint32_t)(lane % kPer * (int)sizeof(T));
+        for (int r = 0; r < rows; ++r) {
+            const uint32_t addr = piece_at(r, lane / kPer) + (uint32_t)(lane % kPer * (int)sizeof(T));
             if constexpr (sizeof(T) == 4)
                 reinterpret_cast<uint32_t *>(y + r * e.y_stride)[lane] = dev::lds_u32(addr);
             else

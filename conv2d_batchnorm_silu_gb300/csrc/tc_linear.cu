@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tile_at(a, t, mt, nt);
                 const int row = weights ? nt * BN + rank * C::B_ROWS : (mt * CG + rank) * kBlockM;
                 for (int it = 0; it < a.k_iters; ++it) {
-                    if (!dev::mbar_wait_bounded(dev::smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kWaitNs)) {
+                    if (!wait_bounded(dev::smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kWaitNs)) {
                         if (!*abort_flag) give_up(kErrTimeoutProducer, abort_flag);
                         ok = false;
                         break;
@@ -295,13 +295,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             tile_at(a, t, mt, nt);
             const int buf = lt & 1;
             const long long row0 = (long long)(mt * CG + rank) * kBlockM + quarter * 32;
-            const float row_scale = row0 + lane < a.e.m ? __ldg(a.e.a_scale + row0 + lane) : 0.0f;
+            float row_scale[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const long long row = row0 + 8 * i + (lane >> 2);
+                row_scale[i] = row < a.e.m ? __ldg(a.e.a_scale + row) : 0.0f;
+            }
             for (int j = turn, i = 0; j < C::BLOCKS; j += kEpiPerQuarter, ++i)
                 stage_params(a.e, nt * BN + j * 32, params + 256 * i, lane);
             __syncwarp();
             int ok = 1;
             if (lane == 0)
-                ok = dev::mbar_wait_bounded(dev::smem_u32(&tfull[buf]), (uint32_t)(lt >> 1) & 1u, abort_flag, kWaitNs);
+                ok = wait_bounded(dev::smem_u32(&tfull[buf]), (uint32_t)(lt >> 1) & 1u, abort_flag, kWaitNs);
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) {
                 if (lane == 0 && !*abort_flag) give_up(kErrTimeoutEpilogue, abort_flag);
@@ -324,8 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = turn, i = 0; j < C::BLOCKS; j += kEpiPerQuarter, ++i) {
                 const int cj = j * 32, col0 = nt * BN + cj;
                 uint32_t v[32];
-                dev::tmem_ld_32x32b_x16(taddr + (uint32_t)cj, v);
-                dev::tmem_ld_32x32b_x16(taddr + (uint32_t)(cj + 16), v + 16);
+                load_block(taddr, (uint32_t)cj, v);
                 dev::tmem_ld_wait();
                 dev::reg_fence16(v);
                 dev::reg_fence16(v + 16);
