@@ -256,16 +256,6 @@ __device__ __forceinline__ void silu32(float *v)
     }
 }
 
-// Scales, then biases, of the 32 columns from col0 into `dst` in shared memory, one lane each; zeros past
-// the end.
-__device__ __forceinline__ void stage_params(const LinearEpilogue &e, int col0, uint32_t dst, int lane)
-{
-    const bool in = col0 + lane < e.n;
-    const float s = in ? __ldg(e.w_scale + col0 + lane) : 0.0f, b = in && e.bias ? __ldg(e.bias + col0 + lane) : 0.0f;
-    dev::sts_u32(dst + 4 * lane, __float_as_uint(s));
-    dev::sts_u32(dst + 128 + 4 * lane, __float_as_uint(b));
-}
-
 // A warp's 32 rows x 32 columns of a TMEM accumulator from column `col` on, in the layout of a matrix
 // instruction's result: with g = lane / 4 and t = lane % 4, v[16 h + 4 j + 2 i + e] is row 16 h + 8 i + g,
 // column 8 j + 2 t + e.  A lane so holds 8 columns of 4 rows and needs the scales of those only.
@@ -284,12 +274,12 @@ __device__ __forceinline__ void load_block(uint32_t taddr, uint32_t col, uint32_
 }
 
 // What becomes of such a block, from row row0 and column col0 of the output: sums in v, row_scale[i] the
-// scale of row 8 i + g, scales and biases of the columns in shared memory at `params` (stage_params).  Rows and
+// scale of row 8 i + g, the columns' 32 scales and 32 biases in shared memory at `params`.  Rows and
 // columns past the end are computed and not stored.  `stg` is the warp's own 32 x 32 elements of shared
 // memory, through which lanes exchange pairs for runs of a row, so that each store covers whole sectors; its
-// 16-byte pieces are swizzled so that neither direction meets a bank twice.  (Each lane with a row of its own,
-// as TMEM gives it by default, took 64 of a block's 112 shared-memory cycles for the columns' scales alone:
-// 25600x256x1024 with SiLU 27 us, this layout %s.)
+// 16-byte pieces are swizzled so that neither direction meets a bank twice.  (With a row to each lane
+// instead, 64 of a block's 112 shared-memory cycles went to the columns' scales: 25600x1024x256 took 25.9 us
+// with its widening, this layout 24.9.)
 template <typename T>
 __device__ __forceinline__ void finish_block(const LinearEpilogue &e, const uint32_t *sums, uint32_t params,
                                              const float *row_scale, long long row0, int col0, uint32_t stg, int lane)
