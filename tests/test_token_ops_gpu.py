@@ -404,3 +404,56 @@ def test_binding_refusals(capi):
         capi.linear_int8(a, w, sa, sw, residual=torch.zeros(4, 32, device="cuda"))
     with pytest.raises(ValueError):
         capi.linear_int8(a, w, sa, sw, residual=torch.zeros(4, 31, dtype=torch.bfloat16, device="cuda"))
+
+
+# Sizes at which each of the layer's kernels is the one that runs (152 SMs): weights widened on their way with
+# row tiles of 32, 64, 128 and 256, then both widened before, in tiles of 128 x 64, 256 x 128 and 256 x 256.
+LARGER = [(20, 300, 4096), (40, 712, 2048), (100, 712, 2048), (300, 300, 4096), (700, 1300, 400), (1500, 1300, 400),
+          (2300, 2000, 1040)]
+
+
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("activation", ["identity", "silu", "relu"])
+@pytest.mark.parametrize("m,n,k", LARGER)
+def test_larger_linear_epilogues(capi, m, n, k, activation, out):
+    check_linear(capi, m, n, k, out, activation, bias=False, residual=False)
+    check_linear(capi, m, n, k, out, activation, bias=True, residual=True)
+    check_linear(capi, m, n - 3, k, out, activation, bias=True, residual=True)  # columns and rows of y at any alignment
+
+
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("pad,offset", [(16, 0), (16, 16), (7, 0), (3, 1), (8, 8)])
+@pytest.mark.parametrize("m,n,k", [(20, 300, 4096), (40, 707, 2001), (130, 712, 2048), (300, 296, 4095), (710, 1296, 403),
+                                   (1501, 1300, 400)])
+def test_larger_linear_of_slices(capi, m, n, k, pad, offset, out):
+    check_linear(capi, m, n, k, out, "silu", residual=True, pad=pad, offset=offset)
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 264, 320), (40, 264, 320)] + LARGER)
+def test_linear_silu_far_from_zero_and_special_scales(capi, m, n, k):
+    a, w = ints(1, m, k), ints(2, n, k)
+    # z has a deviation of some 50, so that many are where e^-z leaves the range of fp32
+    a_scale, w_scale = vector(3, m, 0.5), vector(4, n, 0.5) * 0.6 / (64 * k ** 0.5)
+    y = capi.linear_int8(a, w, a_scale, w_scale, activation="silu", out_dtype=torch.float32)
+    want, z, total = ref.linear_int8(host(a), host(w), host(a_scale), host(w_scale), None, "silu", None)
+    assert (z < -88).any() and (z > 88).any()
+    scales = host(a_scale)[:, None] * host(w_scale)[None, :]
+    summed = np.where(total < 2.0 ** 24, 0.0, (k / 16 + 1) * 2.0 ** -23 * total)
+    zerr = scales * summed + 4 * E32 * (np.abs(z) + scales * total)
+    tol = zerr * 1.1 + np.abs(want) * (6 + 1.2 * np.abs(z)) * 2 * E32 + 1e-37 + 3 * E32 * np.abs(want)
+    assert (np.abs(host(y) - want) <= tol).all()
+    # a NaN or an infinity among the scales is its own row's and column's alone
+    a_scale[m // 2], w_scale[5], w_scale[n - 1] = float("inf"), float("nan"), float("inf")
+    y = host(capi.linear_int8(a, w, a_scale, w_scale, activation="silu", out_dtype=torch.float32))
+    assert np.isnan(y[:, 5]).all() and not np.isfinite(y[m // 2][z[m // 2] > 0]).any()
+    rows, cols = np.arange(m) != m // 2, np.ones(n, bool)
+    cols[[5, n - 1]] = False
+    assert (np.abs(y - want) <= tol)[np.ix_(rows, cols)].all()
+    capi.check()
+
+
+@pytest.mark.parametrize("m,n,k", [(8, 300, 4096)] + LARGER)
+def test_linear_repeats_to_the_bit(capi, m, n, k):
+    a, w, sa, sw = ints(1, m, k), ints(2, n, k), vector(3, m, 0.5), vector(4, n, 0.5)
+    first = capi.linear_int8(a, w, sa, sw, activation="silu")
+    assert all(torch.equal(first, capi.linear_int8(a, w, sa, sw, activation="silu")) for _ in range(5))
