@@ -442,13 +442,11 @@ __global__ void __launch_bounds__(norm_block(TPR), kSmThreads / norm_block(TPR))
     auto column = [&](int i) { return (i * TPR + lane) * V; };
     auto slot = [&](int stage, int i) { return norm_ring + ((stage * NI + i) * kBlock + threadIdx.x) * R::SLOT; };
     auto row_at = [&](long long r) { return static_cast<const T *>(a.x) + r * a.x_stride; };
-    auto odd = [&](long long r) { return sizeof(T) == 2 && W == 4 && reinterpret_cast<uintptr_t>(row_at(r)) % 4 != 0; };
     auto fetch = [&](long long r, int stage) {
         if (r < a.rows) {
             const T *x = row_at(r);
-            const bool o = odd(r);
             for (int i = 0; i < NI; ++i)
-                if (column(i) < a.c) R::copy(dev::smem_u32(slot(stage, i)), x + column(i), a.c - column(i), o);
+                if (column(i) < a.c) R::copy(dev::smem_u32(slot(stage, i)), x + column(i), a.c - column(i), false);
         }
         copy_commit();
     };
@@ -465,15 +463,15 @@ __global__ void __launch_bounds__(norm_block(TPR), kSmThreads / norm_block(TPR))
     for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += step, r += step) {
         fetch(r + (kNormStages - 1) * step, stage == 0 ? kNormStages - 1 : stage - 1);
         copy_wait<kNormStages - 1>();
-        const bool live = r < a.rows, o = odd(r);
+        const bool live = r < a.rows;
         float2 v[E / 2];
         float *vs = reinterpret_cast<float *>(v);
         for (int i = 0; i < NI; ++i) {
             if (live && column(i) < a.c) {
                 if constexpr (V == 1)
-                    R::get(slot(stage, i), o, vs + i);
+                    R::get(slot(stage, i), false, vs + i);
                 else
-                    R::get(slot(stage, i), o, v + i * (V / 2));
+                    R::get(slot(stage, i), false, v + i * (V / 2));
             } else {
                 for (int j = 0; j < V; ++j) vs[i * V + j] = 0.0f;
             }
@@ -555,6 +553,98 @@ cudaError_t norm_stream_launch(const NormArgs &a, int sm_count, cudaStream_t str
                : launch_overlapped(norm_stream_kernel<T, W, TPR, false>, grid, block, kSmem, stream, 1, a);
 }
 
+// ------------------------------------------------------------------ 16-bit rows at any alignment
+// A row's elements one by one past the lanes that hold them: their places in memory words change from row to row,
+// and putting words together again costs more than it saves.  Nothing is copied ahead; many small blocks keep
+// memory busy instead.  f16, us, against the streamed kernel in 4-byte runs: 3001x777 7.0 / 8.6, 1500x1023 4.6 / 7.0,
+// 25000x257 17.5 / 19.5, 25000x1537 63 / 71 (2.4 TB/s; bound by its 2-byte loads and stores), and 2.2 / 3.7 where a
+// row of 33 leaves only latency.
+template <typename T, int NI, int TPR, bool QUANT>
+__global__ void __launch_bounds__(norm_block(TPR)) norm_row_kernel(const NormArgs a)
+{
+    constexpr int kGroups = norm_block(TPR) / TPR;
+    __shared__ float scratch[3][TPR / 32];
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    auto column = [&](int i) { return i * TPR + lane; };
+    const float per_c = 1.0f / (float)a.c;
+    for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += (long long)gridDim.x * kGroups) {
+        const long long r = base + group;
+        const bool live = r < a.rows;
+        const T *x = static_cast<const T *>(a.x) + r * a.x_stride;
+        float v[NI];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) v[i] = live && column(i) < a.c ? to_float(x[column(i)]) : 0.0f;
+        if (!QUANT || a.normalise) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) s += v[i];
+            const float mean = row_sum<TPR>(s, scratch[0]) * per_c;
+            s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                v[i] = column(i) < a.c ? v[i] - mean : 0.0f;
+                s = fmaf(v[i], v[i], s);
+            }
+            const float rstd = rsqrtf(row_sum<TPR>(s, scratch[1]) * per_c + a.eps);
+            if (a.stats && lane == 0 && live) {
+                a.stats[r] = mean;
+                a.stats[a.rows + r] = rstd;
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (column(i) < a.c)
+                    v[i] = fmaf(v[i] * rstd, a.gamma ? __ldg(a.gamma + column(i)) : 1.0f,
+                                a.beta ? __ldg(a.beta + column(i)) : 0.0f);
+        }
+        if (QUANT) {
+            float most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) most = most_of(most, v[i], v[i]);
+            most = row_most<TPR>(most, scratch[2]);
+            float inv;
+            const float scale = row_scale_of(__float_as_uint(most), &inv);
+            if (lane == 0 && live) a.row_scale[r] = scale;
+            const bool finite = scale < __int_as_float(0x7f800000);
+#pragma unroll
+            for (int i = 0; i < NI; ++i)  // rounded to nearest even by the addition, as above
+                if (live && column(i) < a.c)
+                    a.q[r * a.q_stride + column(i)] =
+                        (int8_t)(finite ? __float_as_int(__fadd_rn(__fmul_rn(v[i], inv), 12582912.0f)) : 0);
+        } else if (live) {
+            T *y = static_cast<T *>(a.y) + r * a.y_stride;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (column(i) < a.c) from_float(v[i], y + column(i));
+        }
+        if (TPR > 32) __syncthreads();  // before the scratch's next use
+    }
+}
+
+template <typename T, int NI, int TPR>
+cudaError_t norm_row_launch(const NormArgs &a, cudaStream_t stream)
+{
+    constexpr int kRows = norm_block(TPR) / TPR;
+    const dim3 grid(blocks_for_rows((a.rows + kRows - 1) / kRows)), block(norm_block(TPR));
+    return a.q ? launch_overlapped(norm_row_kernel<T, NI, TPR, true>, grid, block, 0, stream, 1, a)
+               : launch_overlapped(norm_row_kernel<T, NI, TPR, false>, grid, block, 0, stream, 1, a);
+}
+
+// Wider rows go to norm_wide_kernel: 25000x4099 143 us, where the streamed kernel in 4-byte runs took 239 and
+// this one 282, half of its threads having nothing.
+template <typename T>
+cudaError_t norm_row_pick(const NormArgs &a, cudaStream_t stream, bool *done)
+{
+    *done = true;
+    if (a.c <= 8 * 32) return norm_row_launch<T, 8, 32>(a, stream);
+    if (a.c <= 8 * 64) return norm_row_launch<T, 8, 64>(a, stream);
+    if (a.c <= 8 * 128) return norm_row_launch<T, 8, 128>(a, stream);
+    if (a.c <= 16 * 128) return norm_row_launch<T, 16, 128>(a, stream);
+    *done = false;
+    return cudaSuccess;
+}
+
 bool aligned_for(const void *p, long long stride, int element, int bytes)
 {
     return reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride * element % bytes == 0;
@@ -588,8 +678,13 @@ cudaError_t norm_launch_t(const NormArgs &a, int sm_count, cudaStream_t stream)
                             (a.q ? aligned_for(a.q, a.q_stride, 1, V) : aligned_for(a.y, a.y_stride, sizeof(T), 16)) &&
                             aligned_for(a.gamma, 0, 4, 16) && aligned_for(a.beta, 0, 4, 16);
     bool done = false;
-    const cudaError_t e = wide_loads ? norm_stream_pick<T, 16>(a, sm_count, stream, &done)
-                                     : norm_stream_pick<T, 4>(a, sm_count, stream, &done);
+    cudaError_t e;
+    if (wide_loads)
+        e = norm_stream_pick<T, 16>(a, sm_count, stream, &done);
+    else if constexpr (sizeof(T) == 4)
+        e = norm_stream_pick<T, 4>(a, sm_count, stream, &done);
+    else
+        e = norm_row_pick<T>(a, stream, &done);
     if (done) return e;
     return launch_overlapped(norm_wide_kernel<T>, dim3(blocks_for_rows(a.rows)), dim3(kWideThreads), 0, stream, 1, a);
 }
