@@ -155,21 +155,26 @@ cudaError_t linear_few_launch_t(const LinearArgs &a, int sm_count, cudaStream_t 
 // Rows up to which linear_few_kernel is the faster.
 constexpr int kFewRows = 8;
 // The kernels for more rows, chosen by what they are modelled to take: linear_tile.cu's one launch, weights
-// widened on their way to the tensor cores (tc_linear_stream.cu), or both widened before (tc_linear.cu).
-enum Path { kTile, kStreamed, kWidened };
+// widened on their way to the tensor cores (tc_linear_stream.cu), rows on theirs (the same kernel with the operands'
+// sides changed), or both widened before (tc_linear.cu).
+enum Path { kTile, kStreamed, kTurned, kWidened };
 
 // Measured, us, tile / streamed / widened before: 24x614x243 5.2 / - / 6.0 (8.6 from the host), 64x1024x1024
-// 11.2 / 5.9 / 8.9, 64 rows of 8192x8192 - / 23 / 74, 512 rows - / 81 / 87, 1024 rows - / 152 / 121.
+// 11.2 / 5.9 / 8.9, 64 rows of 8192x8192 - / 23 / 74, 512 rows - / 81 / 87, 1024 rows - / 152 / 121.  Streamed with
+// the sides changed / widened before: 25984x40x4800 41 / 132, 11609x128x4512 27 / 58, 100000x16x256 16 / 28,
+// 25600x256x1024 39 / 31, 16384x512x512 36 / 17.
 // A call takes the longer of its kernels and what its launches cost the host.
 Path best_path(long long m, int n, int k, int sm_count, bool aligned)
 {
     const float tile = linear_tile_supported(m, n) ? linear_tile_time(m, n, k, sm_count) : 1e30f;
     const float before = tc_linear_time(m, n, k, sm_count);
     // Beyond 4096 rows sixteen row tiles would each widen the weights again.
-    const float on_the_way = aligned && m <= 4096 ? tc_stream_time(m, n, k, sm_count) : 1e30f;
-    const float times[3] = {fmaxf(tile, 4.6f), fmaxf(on_the_way, 7.4f), fmaxf(before, 8.6f)};
+    const float on_the_way = aligned && m <= 4096 ? tc_stream_time(m, n, k, false, sm_count) : 1e30f;
+    const bool few_channels = n <= 1024 && m <= (1 << 30) && m * k < (1LL << 42);  // its steps fit an int
+    const float turned = aligned && few_channels ? tc_stream_time(n, (int)m, k, true, sm_count) : 1e30f;
+    const float times[4] = {fmaxf(tile, 4.6f), fmaxf(on_the_way, 7.4f), fmaxf(turned, 7.4f), fmaxf(before, 8.6f)};
     int best = kWidened;
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 3; ++i)
         if (times[i] < times[best]) best = i;
     return (Path)best;
 }
@@ -179,6 +184,7 @@ long long path_workspace(Path path, long long m, int n, int k, int sm_count)
     switch (path) {
     case kTile: return 0;
     case kStreamed: return tc_stream_workspace_bytes(m, n, k, sm_count);
+    case kTurned: return tc_stream_workspace_bytes(n, (int)m, k, sm_count);
     default: return tc_linear_workspace_bytes(m, n, k);
     }
 }
@@ -197,7 +203,8 @@ cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t str
     if (p.m > kFewRows) {
         switch (best_path(p.m, p.n, p.k, sm_count, tc_stream_supported(p))) {
         case kTile: return linear_tile_launch(p, stream);
-        case kStreamed: return tc_stream_launch(p, sm_count, stream);
+        case kStreamed: return tc_stream_launch(p, false, sm_count, stream);
+        case kTurned: return tc_stream_launch(p, true, sm_count, stream);
         default: return tc_linear_launch(p, sm_count, stream);
         }
     }

@@ -44,8 +44,11 @@ struct StreamCfg {
 
 struct StreamArgs {
     LinearEpilogue e;
+    // The operands, channels on the tensor core's M side and rows on its N side: the weights and the rows of the
+    // layer or, where its weights are few, the other way round (its rows streamed as channels).
     const int8_t *a, *w;
     long long a_stride, w_stride;
+    int rows, channels;
     int k, k_steps;
     int row_tiles, tiles;      // tile = channel tile * row_tiles + row tile
     int steps;                 // tiles * k_steps
@@ -139,8 +142,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     if (threadIdx.x < kChannels) {
         // The weights of the run's first steps.
         const int tile = g0 / a.k_steps, k0 = (g0 - tile * a.k_steps) * kStep;
-        const int n = min(tile / a.row_tiles * kChannels + (int)threadIdx.x, a.e.n - 1);
-        prefetch_l2(a.w + n * a.w_stride + k0, (uint32_t)min(a.k - k0, kPrefetch));
+        const int n = min(tile / a.row_tiles * kChannels + (int)threadIdx.x, a.channels - 1);
+        prefetch_l2(a.w + (long long)n * a.w_stride + k0, (uint32_t)min(a.k - k0, kPrefetch));
     }
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
@@ -159,10 +162,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
             const int ct = tile / a.row_tiles, rt = tile - ct * a.row_tiles, k0 = ks * kStep + q * 16;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                src[j] = a.w + (long long)min(ct * kChannels + j * 64 + r8, a.e.n - 1) * a.w_stride + k0;
+                src[j] = a.w + (long long)min(ct * kChannels + j * 64 + r8, a.channels - 1) * a.w_stride + k0;
 #pragma unroll
             for (int j = 0; j < C::ROW_LOADS; ++j)
-                src[2 + j] = a.a + (long long)min(rt * NT + j * 64 + r8, (int)a.e.m - 1) * a.a_stride + k0;
+                src[2 + j] = a.a + (long long)min(rt * NT + j * 64 + r8, a.rows - 1) * a.a_stride + k0;
         };
         rows_of_tile();
         uint4 held[AHEAD][LOADS];
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         for (int piece = 0, left = steps; left > 0; ++piece, ++tile, ks = 0) {
             const int take = min(left, a.k_steps - ks), buf = piece & 1;
             left -= take;
-            const int rows = min(NT, (int)a.e.m - tile % a.row_tiles * NT);
+            const int rows = min(NT, a.rows - tile % a.row_tiles * NT);
             int ok = 1;
             if (lane == 0)
                 ok = wait_bounded(dev::smem_u32(&tfull[buf]), (uint32_t)(piece >> 1) & 1u, abort_flag, kWaitNs);
@@ -325,8 +328,24 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
     }
 }
 
-// The workers' partial sums of a tile added in K order, and finished.  A thread takes four channels of a
-// row; eight workers' sums load at a time.
+// The partial sums of four channels of a tile's row from workers b0 to b1, added in K order; eight load at a time.
+template <int NT>
+__device__ __forceinline__ void add_partial(const StreamArgs &a, int tile, int b0, int b1, int row, int channel, float *s)
+{
+    const float *from = a.partial + ((long long)(b0 + tile) * NT + row) * kChannels + channel;
+    s[0] = s[1] = s[2] = s[3] = 0.0f;
+    for (int b = b0; b <= b1; b += 8) {
+        float4 v[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            if (b + t <= b1) v[t] = *reinterpret_cast<const float4 *>(from + (long long)(b - b0 + t) * NT * kChannels);
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+            if (b + t <= b1) s[0] += v[t].x, s[1] += v[t].y, s[2] += v[t].z, s[3] += v[t].w;
+    }
+}
+
+// The workers' partial sums of a tile joined and finished.  A thread takes four channels of a row.
 constexpr int kJoinRows = 4;
 template <typename T, int NT>
 __global__ void __launch_bounds__(32 * kJoinRows) linear_join_kernel(const StreamArgs a)
@@ -352,17 +371,8 @@ __global__ void __launch_bounds__(32 * kJoinRows) linear_join_kernel(const Strea
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
     if (!mine) return;
-    const float *from = a.partial + ((long long)(b0 + tile) * NT + i) * kChannels + threadIdx.x * 4;
-    float s[4] = {};
-    for (int b = b0; b <= b1; b += 8) {
-        float4 v[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-            if (b + t <= b1) v[t] = *reinterpret_cast<const float4 *>(from + (long long)(b - b0 + t) * NT * kChannels);
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-            if (b + t <= b1) s[0] += v[t].x, s[1] += v[t].y, s[2] += v[t].z, s[3] += v[t].w;
-    }
+    float s[4];
+    add_partial<NT>(a, tile, b0, b1, i, threadIdx.x * 4, s);
     const T *res = a.e.residual ? static_cast<const T *>(a.e.residual) + m * a.e.residual_stride + n : nullptr;
     T *y = static_cast<T *>(a.e.y) + m * a.e.y_stride + n;
 #pragma unroll
@@ -372,6 +382,49 @@ __global__ void __launch_bounds__(32 * kJoinRows) linear_join_kernel(const Strea
             if (res) z += to_float(res[j]);
             from_float(z, y + j);
         }
+}
+
+// The same where the channels are the layer's rows: 32 columns of 128 rows turned round in shared memory, so that
+// each warp finishes 32 columns of a row of y at a time.
+constexpr int kTurnWarps = 8;
+template <typename T, int NT>
+__global__ void __launch_bounds__(32 * kTurnWarps) linear_join_turned_kernel(const StreamArgs a)
+{
+    __shared__ float turned[32][kChannels + 1];
+    const int tile = blockIdx.x, g = tile * a.k_steps, lane = threadIdx.x, warp = threadIdx.y;
+    const int b0 = worker_of(a, g), b1 = worker_of(a, g + a.k_steps - 1);
+    const int ct = tile / a.row_tiles, c0 = blockIdx.y * 32, n0 = (tile - ct * a.row_tiles) * NT + c0;
+    const long long m0 = (long long)ct * kChannels;
+    // Scales and biases before the wait, as in linear_join_kernel.
+    const int n = n0 + lane;
+    float scale = 0.0f, bias = 0.0f, row_scale[kChannels / kTurnWarps];
+    if (n < a.e.n) {
+        scale = __ldg(a.e.w_scale + n);
+        if (a.e.bias) bias = __ldg(a.e.bias + n);
+    }
+#pragma unroll
+    for (int j = 0; j < kChannels / kTurnWarps; ++j)
+        row_scale[j] = m0 + j * kTurnWarps + warp < a.e.m ? __ldg(a.e.a_scale + m0 + j * kTurnWarps + warp) : 0.0f;
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+#pragma unroll
+    for (int j = 0; j < 32 / kTurnWarps; ++j) {
+        const int c = j * kTurnWarps + warp;
+        if (n0 + c >= a.e.n) continue;
+        float s[4];
+        add_partial<NT>(a, tile, b0, b1, c0 + c, lane * 4, s);
+        for (int t = 0; t < 4; ++t) turned[c][lane * 4 + t] = s[t];
+    }
+    __syncthreads();
+    if (n >= a.e.n) return;
+#pragma unroll
+    for (int j = 0; j < kChannels / kTurnWarps; ++j) {
+        const long long m = m0 + j * kTurnWarps + warp;
+        if (m >= a.e.m) break;
+        float z = activated(fmaf(turned[lane][j * kTurnWarps + warp], row_scale[j] * scale, bias), a.e.activation);
+        if (a.e.residual) z += to_float(static_cast<const T *>(a.e.residual)[m * a.e.residual_stride + n]);
+        from_float(z, static_cast<T *>(a.e.y) + m * a.e.y_stride + n);
+    }
 }
 
 // Row tile for m rows: the smallest that holds them.
@@ -398,7 +451,7 @@ StreamPlan plan_of(long long m, int n, int k, int sm_count)
 }
 
 template <typename T, int NT>
-cudaError_t stream_launch(const StreamArgs &a, cudaStream_t stream)
+cudaError_t stream_launch(const StreamArgs &a, bool turned, cudaStream_t stream)
 {
     using C = StreamCfg<NT>;
     static bool allowed[kMaxDevices] = {};
@@ -407,31 +460,35 @@ cudaError_t stream_launch(const StreamArgs &a, cudaStream_t stream)
     e = launch_overlapped(linear_stream_kernel<NT>, dim3((unsigned)a.workers), dim3(kThreads), (size_t)C::SMEM, stream,
                           1, a);
     if (e != cudaSuccess) return e;
-    const int rows = (int)(a.e.m < NT ? a.e.m : NT);
+    const int rows = a.rows < NT ? a.rows : NT;
+    if (turned)
+        return launch_overlapped(linear_join_turned_kernel<T, NT>, dim3((unsigned)a.tiles, (unsigned)((rows + 31) / 32)),
+                                 dim3(32, kTurnWarps), 0, stream, 1, a);
     return launch_overlapped(linear_join_kernel<T, NT>, dim3((unsigned)a.tiles, (unsigned)((rows + kJoinRows - 1) / kJoinRows)),
                              dim3(32, kJoinRows), 0, stream, 1, a);
 }
 
 template <typename T>
-cudaError_t stream_launch_t(const StreamArgs &a, int nt, cudaStream_t stream)
+cudaError_t stream_launch_t(const StreamArgs &a, int nt, bool turned, cudaStream_t stream)
 {
     switch (nt) {
-    case 32: return stream_launch<T, 32>(a, stream);
-    case 64: return stream_launch<T, 64>(a, stream);
-    case 128: return stream_launch<T, 128>(a, stream);
-    default: return stream_launch<T, 256>(a, stream);
+    case 32: return stream_launch<T, 32>(a, turned, stream);
+    case 64: return stream_launch<T, 64>(a, turned, stream);
+    case 128: return stream_launch<T, 128>(a, turned, stream);
+    default: return stream_launch<T, 256>(a, turned, stream);
     }
 }
 
 }  // namespace
 
-float tc_stream_time(long long m, int n, int k, int sm_count)
+float tc_stream_time(long long rows, int channels, int k, bool turned, int sm_count)
 {
-    // A step of 128 K elements as measured for each row tile, both launches, and the sums' way through L2.
-    const StreamPlan p = plan_of(m, n, k, sm_count);
+    // A step of 128 K elements as measured for each row tile, both launches, and the sums' way through L2 (at
+    // 5.5 TB/s, with a slower second launch, where they are turned round).
+    const StreamPlan p = plan_of(rows, channels, k, sm_count);
     const float step = p.nt == 32 ? 0.60f : (p.nt == 64 ? 0.67f : (p.nt == 128 ? 0.91f : 1.50f));
-    return 5.0f + step * (float)((p.steps + p.workers - 1) / p.workers) +
-           (float)(p.workers + p.tiles) * (float)p.nt * kChannels * 8.0f / 8.0e6f;
+    return (turned ? 6.5f : 5.0f) + step * (float)((p.steps + p.workers - 1) / p.workers) +
+           (float)(p.workers + p.tiles) * (float)p.nt * kChannels * 8.0f / (turned ? 5.5e6f : 8.0e6f);
 }
 
 bool tc_stream_supported(const LinearProblem &p)
@@ -440,21 +497,24 @@ bool tc_stream_supported(const LinearProblem &p)
     return p.k > 0 && p.k % 16 == 0 && rows16(p.a) && rows16(p.w);
 }
 
-long long tc_stream_workspace_bytes(long long m, int n, int k, int sm_count)
+long long tc_stream_workspace_bytes(long long rows, int channels, int k, int sm_count)
 {
-    const StreamPlan p = plan_of(m, n, k, sm_count);
+    const StreamPlan p = plan_of(rows, channels, k, sm_count);
     return ((long long)p.workers + p.tiles) * p.nt * kChannels * 4;
 }
 
-cudaError_t tc_stream_launch(const LinearProblem &p, int sm_count, cudaStream_t stream)
+cudaError_t tc_stream_launch(const LinearProblem &p, bool turned, int sm_count, cudaStream_t stream)
 {
-    const StreamPlan plan = plan_of(p.m, p.n, p.k, sm_count);
     StreamArgs a{};
     a.e = linear_epilogue_of(p);
-    a.a = static_cast<const int8_t *>(p.a.data);
-    a.a_stride = p.a.stride;
-    a.w = static_cast<const int8_t *>(p.w.data);
-    a.w_stride = p.w.stride;
+    a.rows = turned ? p.n : (int)p.m;
+    a.channels = turned ? (int)p.m : p.n;
+    const Rows &rows = turned ? p.w : p.a, &channels = turned ? p.a : p.w;
+    a.a = static_cast<const int8_t *>(rows.data);
+    a.a_stride = rows.stride;
+    a.w = static_cast<const int8_t *>(channels.data);
+    a.w_stride = channels.stride;
+    const StreamPlan plan = plan_of(a.rows, a.channels, p.k, sm_count);
     a.k = p.k;
     a.k_steps = plan.k_steps;
     a.row_tiles = plan.row_tiles;
@@ -465,9 +525,9 @@ cudaError_t tc_stream_launch(const LinearProblem &p, int sm_count, cudaStream_t 
     a.run_extra = plan.steps % plan.workers;
     a.partial = static_cast<float *>(p.workspace);
     switch (p.out_dtype) {
-    case kF32: return stream_launch_t<float>(a, plan.nt, stream);
-    case kBf16: return stream_launch_t<__nv_bfloat16>(a, plan.nt, stream);
-    default: return stream_launch_t<__half>(a, plan.nt, stream);
+    case kF32: return stream_launch_t<float>(a, plan.nt, turned, stream);
+    case kBf16: return stream_launch_t<__nv_bfloat16>(a, plan.nt, turned, stream);
+    default: return stream_launch_t<__half>(a, plan.nt, turned, stream);
     }
 }
 

@@ -457,3 +457,28 @@ def test_linear_repeats_to_the_bit(capi, m, n, k):
     a, w, sa, sw = ints(1, m, k), ints(2, n, k), vector(3, m, 0.5), vector(4, n, 0.5)
     first = capi.linear_int8(a, w, sa, sw, activation="silu")
     assert all(torch.equal(first, capi.linear_int8(a, w, sa, sw, activation="silu")) for _ in range(5))
+
+
+# Few channels for many rows: the rows are widened on their way.
+TURNED = [(700, 40, 4096), (1500, 9, 4096), (5000, 33, 1040), (9000, 100, 2048), (9000, 200, 4096), (6000, 300, 8192)]
+
+
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("activation", ["identity", "silu", "relu"])
+@pytest.mark.parametrize("m,n,k", TURNED)
+def test_linear_of_few_channels(capi, m, n, k, activation, out):
+    check_linear(capi, m, n, k, out, activation, bias=False, residual=False)
+    check_linear(capi, m - 1, n, k, out, activation, bias=True, residual=True)
+    check_linear(capi, m, n, k, out, activation, bias=True, residual=True, pad=16, offset=16)
+
+
+@pytest.mark.parametrize("m,n,k", TURNED)
+def test_linear_of_few_channels_repeats_to_the_bit(capi, m, n, k):
+    a, w, sa, sw = ints(1, m, k), ints(2, n, k), vector(3, m, 0.5), vector(4, n, 0.5)
+    first = capi.linear_int8(a, w, sa, sw, activation="silu")
+    assert all(torch.equal(first, capi.linear_int8(a, w, sa, sw, activation="silu")) for _ in range(5))
+    sa[m // 2] = float("nan")
+    y = capi.linear_int8(a, w, sa, sw, activation="silu")
+    assert y[m // 2].isnan().all()
+    rest = torch.arange(m, device="cuda") != m // 2
+    assert torch.equal(y[rest], first[rest])
