@@ -164,14 +164,14 @@ enum Path { kTile, kStreamed, kTurned, kWidened };
 // the sides changed / widened before: 25984x40x4800 41 / 132, 11609x128x4512 27 / 58, 100000x16x256 16 / 28,
 // 25600x256x1024 39 / 31, 16384x512x512 36 / 17.
 // A call takes the longer of its kernels and what its launches cost the host.
-Path best_path(long long m, int n, int k, int sm_count, bool aligned)
+Path best_path(long long m, int n, int k, int sm_count, int align)
 {
     const float tile = linear_tile_supported(m, n) ? linear_tile_time(m, n, k, sm_count) : 1e30f;
     const float before = tc_linear_time(m, n, k, sm_count);
     // Beyond 4096 rows sixteen row tiles would each widen the weights again.
-    const float on_the_way = aligned && m <= 4096 ? tc_stream_time(m, n, k, false, sm_count) : 1e30f;
+    const float on_the_way = align > 0 && m <= 4096 ? tc_stream_time(m, n, k, align, false, sm_count) : 1e30f;
     const bool few_channels = n <= 1024 && m <= (1 << 30) && m * k < (1LL << 42);  // its steps fit an int
-    const float turned = aligned && few_channels ? tc_stream_time(n, (int)m, k, true, sm_count) : 1e30f;
+    const float turned = align > 0 && few_channels ? tc_stream_time(n, (int)m, k, align, true, sm_count) : 1e30f;
     const float times[4] = {fmaxf(tile, 4.6f), fmaxf(on_the_way, 7.4f), fmaxf(turned, 7.4f), fmaxf(before, 8.6f)};
     int best = kWidened;
     for (int i = 0; i < 3; ++i)
@@ -192,16 +192,19 @@ long long path_workspace(Path path, long long m, int n, int k, int sm_count)
 long long linear_workspace_bytes(long long m, int n, int k, int sm_count)
 {
     if (m <= kFewRows || n <= 0) return 0;
-    // For either alignment that the call's matrices may have.
-    const long long a = path_workspace(best_path(m, n, k, sm_count, true), m, n, k, sm_count);
-    const long long b = path_workspace(best_path(m, n, k, sm_count, false), m, n, k, sm_count);
-    return a > b ? a : b;
+    // For any alignment that the call's matrices may have.
+    long long most = 0;
+    for (int align : {16, 4, 0}) {
+        const long long bytes = path_workspace(best_path(m, n, k, sm_count, align), m, n, k, sm_count);
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream)
 {
     if (p.m > kFewRows) {
-        switch (best_path(p.m, p.n, p.k, sm_count, tc_stream_supported(p))) {
+        switch (best_path(p.m, p.n, p.k, sm_count, tc_stream_align(p))) {
         case kTile: return linear_tile_launch(p, stream);
         case kStreamed: return tc_stream_launch(p, false, sm_count, stream);
         case kTurned: return tc_stream_launch(p, true, sm_count, stream);

@@ -3,8 +3,9 @@
 //
 // D[channel][row] = W * A^T with 128 channels on the tensor core's M side and NT rows on its N side.
 // Sixteen warps hold the int8 of the coming steps in registers (kAhead steps of 128 K elements, 48 KB of
-// weights per SM in flight, whole 128-byte lines of each row), widen a step of weights and rows at a time into swizzled f16 tiles, and hand them
-// to the issuing warp.  Every CTA takes an equal run of the (channel tile, row tile, K step) sequence,
+// weights per SM in flight, whole 128-byte lines of each row), widen a step of weights and rows at a time into
+// swizzled f16 tiles, and hand them to the issuing warp.  Rows that start at multiples of 4 bytes only are loaded
+// in words (64x8192x8196 27 us, where 64x8192x8192 takes 23; widened before the product 76).  Every CTA takes an equal run of the (channel tile, row tile, K step) sequence,
 // so that all SMs read the same share of the weights, and leaves its tiles as fp32 partial sums in the
 // workspace, which a second kernel adds in K order and finishes.
 #include <cuda_bf16.h>
@@ -66,15 +67,51 @@ __device__ __forceinline__ void give_up(unsigned int bit, volatile int *abort_fl
 // What rows of a hold past k.
 __device__ const uint4 g_zeros = {0, 0, 0, 0};
 
-// A predicated load straight into its registers, which otherwise keep what they hold.
-__device__ __forceinline__ void load_unless(uint4 &v, const int8_t *p, bool skip)
+// Predicated loads of 16 bytes straight into their registers, which otherwise keep what they hold: in one piece,
+// or in four of the first `left` bytes where rows start at any multiple of 4.
+__device__ __forceinline__ void load_if(uint32_t &v, const int8_t *p, bool yes)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.eq.b32 p, %5, 0;\n\t"
+        "setp.ne.b32 p, %2, 0;\n\t"
+        "@p ld.global.nc.b32 %0, [%1];\n\t}"
+        : "+r"(v)
+        : "l"(p), "r"((int)yes));
+}
+__device__ __forceinline__ void load_if(uint4 &v, const int8_t *p, bool yes)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
         "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
         : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-        : "l"(p), "r"((int)skip));
+        : "l"(p), "r"((int)yes));
+}
+template <int ALIGN>
+__device__ __forceinline__ void load_weights(uint4 &v, const int8_t *p, int left)
+{
+    if constexpr (ALIGN == 16) {
+        load_if(v, p, left > 0);
+    } else {
+        load_if(v.x, p, left > 0);
+        load_if(v.y, p + 4, left > 4);
+        load_if(v.z, p + 8, left > 8);
+        load_if(v.w, p + 12, left > 12);
+    }
+}
+// Zeros for what is past.
+template <int ALIGN>
+__device__ __forceinline__ void load_row(uint4 &v, const int8_t *p, int left)
+{
+    const int8_t *zeros = reinterpret_cast<const int8_t *>(&g_zeros);
+    if constexpr (ALIGN == 16) {
+        load_if(v, left > 0 ? p : zeros, true);
+    } else {
+        load_if(v.x, left > 0 ? p : zeros, true);
+        load_if(v.y, left > 4 ? p + 4 : zeros, true);
+        load_if(v.z, left > 8 ? p + 8 : zeros, true);
+        load_if(v.w, left > 12 ? p + 12 : zeros, true);
+    }
 }
 
 // As sts_v4, at a constant distance from a base.
@@ -101,7 +138,8 @@ __device__ __forceinline__ int worker_of(const StreamArgs &a, int g)
     return g < longer ? g / (a.run_base + 1) : a.run_extra + (g - longer) / a.run_base;
 }
 
-template <int NT>
+// ALIGN: rows of both operands start at multiples of it, and k is one.
+template <int NT, int ALIGN>
 __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const StreamArgs a)
 {
     using C = StreamCfg<NT>;
@@ -143,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         // The weights of the run's first steps.
         const int tile = g0 / a.k_steps, k0 = (g0 - tile * a.k_steps) * kStep;
         const int n = min(tile / a.row_tiles * kChannels + (int)threadIdx.x, a.channels - 1);
-        prefetch_l2(a.w + (long long)n * a.w_stride + k0, (uint32_t)min(a.k - k0, kPrefetch));
+        if constexpr (ALIGN == 16) prefetch_l2(a.w + (long long)n * a.w_stride + k0, (uint32_t)min(a.k - k0, kPrefetch));
     }
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
@@ -152,11 +190,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         // ---------------------------------------------------------- loads and widening
         // Piece j of this thread: 16 bytes of K from 16 * (tid % 8) of weights rows tid / 8 + 64 j for
         // j < 2, then of rows of a.  Rows past the end read the last one: nothing stores what they give.
-        // Past k (a multiple of 16) rows of a are zeros and the weights any values; past the run, too.
+        // Past k rows of a are zeros and the weights any values; past the run, too.
         const int tid = threadIdx.x, q = tid & 7, r8 = tid >> 3;
         int tile = g0 / a.k_steps, ks = g0 - tile * a.k_steps, unloaded = steps;  // of the next load
         const bool has_row = NT >= 64 || r8 < NT;
-        const bool cut = (a.k_steps - 1) * kStep + q * 16 >= a.k;  // this thread's part of a last step is past k
+        const int last_left = a.k - (a.k_steps - 1) * kStep - q * 16;  // of a last step, from this thread's part on
         const int8_t *src[LOADS];
         auto rows_of_tile = [&]() {
             const int ct = tile / a.row_tiles, rt = tile - ct * a.row_tiles, k0 = ks * kStep + q * 16;
@@ -172,16 +210,16 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         auto load = [&](uint4 (&to)[LOADS]) {
             if (unloaded <= 0) return;  // what is held is not used again
             --unloaded;
-            const bool past = cut && ks == a.k_steps - 1;
+            const int left = ks == a.k_steps - 1 ? last_left : 16;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                load_unless(to[j], src[j], past);
+                load_weights<ALIGN>(to[j], src[j], left);
                 src[j] += kStep;
             }
             if (has_row)
 #pragma unroll
                 for (int j = 0; j < C::ROW_LOADS; ++j) {
-                    load_unless(to[2 + j], past ? reinterpret_cast<const int8_t *>(&g_zeros) : src[2 + j], false);
+                    load_row<ALIGN>(to[2 + j], src[2 + j], left);
                     src[2 + j] += kStep;
                 }
             if (++ks == a.k_steps) {
@@ -450,15 +488,21 @@ StreamPlan plan_of(long long m, int n, int k, int sm_count)
     return p;
 }
 
-template <typename T, int NT>
-cudaError_t stream_launch(const StreamArgs &a, bool turned, cudaStream_t stream)
+template <int NT, int ALIGN>
+cudaError_t sums_launch(const StreamArgs &a, cudaStream_t stream)
 {
     using C = StreamCfg<NT>;
     static bool allowed[kMaxDevices] = {};
-    cudaError_t e = allow_dynamic_smem(linear_stream_kernel<NT>, C::SMEM, allowed);
-    if (e != cudaSuccess) return e;
-    e = launch_overlapped(linear_stream_kernel<NT>, dim3((unsigned)a.workers), dim3(kThreads), (size_t)C::SMEM, stream,
-                          1, a);
+    cudaError_t e = allow_dynamic_smem(linear_stream_kernel<NT, ALIGN>, C::SMEM, allowed);
+    return e != cudaSuccess ? e
+                            : launch_overlapped(linear_stream_kernel<NT, ALIGN>, dim3((unsigned)a.workers), dim3(kThreads),
+                                                (size_t)C::SMEM, stream, 1, a);
+}
+
+template <typename T, int NT>
+cudaError_t stream_launch(const StreamArgs &a, int align, bool turned, cudaStream_t stream)
+{
+    cudaError_t e = align == 16 ? sums_launch<NT, 16>(a, stream) : sums_launch<NT, 4>(a, stream);
     if (e != cudaSuccess) return e;
     const int rows = a.rows < NT ? a.rows : NT;
     if (turned)
@@ -469,32 +513,36 @@ cudaError_t stream_launch(const StreamArgs &a, bool turned, cudaStream_t stream)
 }
 
 template <typename T>
-cudaError_t stream_launch_t(const StreamArgs &a, int nt, bool turned, cudaStream_t stream)
+cudaError_t stream_launch_t(const StreamArgs &a, int nt, int align, bool turned, cudaStream_t stream)
 {
     switch (nt) {
-    case 32: return stream_launch<T, 32>(a, turned, stream);
-    case 64: return stream_launch<T, 64>(a, turned, stream);
-    case 128: return stream_launch<T, 128>(a, turned, stream);
-    default: return stream_launch<T, 256>(a, turned, stream);
+    case 32: return stream_launch<T, 32>(a, align, turned, stream);
+    case 64: return stream_launch<T, 64>(a, align, turned, stream);
+    case 128: return stream_launch<T, 128>(a, align, turned, stream);
+    default: return stream_launch<T, 256>(a, align, turned, stream);
     }
 }
 
 }  // namespace
 
-float tc_stream_time(long long rows, int channels, int k, bool turned, int sm_count)
+float tc_stream_time(long long rows, int channels, int k, int align, bool turned, int sm_count)
 {
     // A step of 128 K elements as measured for each row tile, both launches, and the sums' way through L2 (at
     // 5.5 TB/s, with a slower second launch, where they are turned round).
     const StreamPlan p = plan_of(rows, channels, k, sm_count);
-    const float step = p.nt == 32 ? 0.60f : (p.nt == 64 ? 0.67f : (p.nt == 128 ? 0.91f : 1.50f));
+    const float whole = p.nt == 32 ? 0.60f : (p.nt == 64 ? 0.67f : (p.nt == 128 ? 0.91f : 1.50f));
+    const float step = align == 16 ? whole : whole * (p.nt <= 128 ? 1.2f : 1.4f);  // rows loaded in words of 4 bytes
     return (turned ? 6.5f : 5.0f) + step * (float)((p.steps + p.workers - 1) / p.workers) +
            (float)(p.workers + p.tiles) * (float)p.nt * kChannels * 8.0f / (turned ? 5.5e6f : 8.0e6f);
 }
 
-bool tc_stream_supported(const LinearProblem &p)
+int tc_stream_align(const LinearProblem &p)
 {
-    auto rows16 = [](const Rows &r) { return reinterpret_cast<uintptr_t>(r.data) % 16 == 0 && r.stride % 16 == 0; };
-    return p.k > 0 && p.k % 16 == 0 && rows16(p.a) && rows16(p.w);
+    auto rows_at = [&](const Rows &r, int bytes) {
+        return reinterpret_cast<uintptr_t>(r.data) % bytes == 0 && r.stride % bytes == 0 && p.k % bytes == 0;
+    };
+    auto both_at = [&](int bytes) { return p.k > 0 && rows_at(p.a, bytes) && rows_at(p.w, bytes); };
+    return both_at(16) ? 16 : (both_at(4) ? 4 : 0);
 }
 
 long long tc_stream_workspace_bytes(long long rows, int channels, int k, int sm_count)
@@ -505,6 +553,8 @@ long long tc_stream_workspace_bytes(long long rows, int channels, int k, int sm_
 
 cudaError_t tc_stream_launch(const LinearProblem &p, bool turned, int sm_count, cudaStream_t stream)
 {
+    const int align = tc_stream_align(p);
+    if (align == 0) return cudaErrorInvalidValue;
     StreamArgs a{};
     a.e = linear_epilogue_of(p);
     a.rows = turned ? p.n : (int)p.m;
@@ -525,9 +575,9 @@ cudaError_t tc_stream_launch(const LinearProblem &p, bool turned, int sm_count, 
     a.run_extra = plan.steps % plan.workers;
     a.partial = static_cast<float *>(p.workspace);
     switch (p.out_dtype) {
-    case kF32: return stream_launch_t<float>(a, plan.nt, turned, stream);
-    case kBf16: return stream_launch_t<__nv_bfloat16>(a, plan.nt, turned, stream);
-    default: return stream_launch_t<__half>(a, plan.nt, turned, stream);
+    case kF32: return stream_launch_t<float>(a, plan.nt, align, turned, stream);
+    case kBf16: return stream_launch_t<__nv_bfloat16>(a, plan.nt, align, turned, stream);
+    default: return stream_launch_t<__half>(a, plan.nt, align, turned, stream);
     }
 }
 

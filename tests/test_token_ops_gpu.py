@@ -482,3 +482,12 @@ def test_linear_of_few_channels_repeats_to_the_bit(capi, m, n, k):
     assert y[m // 2].isnan().all()
     rest = torch.arange(m, device="cuda") != m // 2
     assert torch.equal(y[rest], first[rest])
+
+
+# Rows that start at multiples of 4 bytes, and one size of more channels than a tile of the turned product.
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("m,n,k,pad", [(904, 64, 12644, 0), (64, 3265, 2004, 0), (2368, 40, 4996, 0), (300, 296, 4092, 0),
+                                       (100, 712, 2052, 4), (20, 300, 4100, 8), (700, 40, 4096, 4), (64, 300, 4096, 12),
+                                       (5467, 386, 9264, 0)])
+def test_linear_of_rows_at_words(capi, m, n, k, pad, out):
+    check_linear(capi, m, n, k, out, "silu", residual=True, pad=pad, offset=pad)
