@@ -4,6 +4,8 @@
 // widen it for the fast tensor cores first.  32 x 64 outputs per block of four warps; K in steps of 128
 // through shared memory, the next step's bytes loading meanwhile; products by the 8-bit integer matrix
 // instruction (150 TOP/s on this part, like __dp4a: the reason for the other kernels), exact in 32 bits.
+// Bound by its launch and the latency of its steps: 64x256x256 5.5 us a call, 512x512x256 5.7 (the widened
+// product 7.4, two launches).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

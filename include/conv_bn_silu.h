@@ -330,7 +330,10 @@ int conv_bn_silu_forward_request(const void *x, const void *w, const float *scal
  *     its rows in elements; elements of one row are adjacent.  Inputs may have
  *     any distance >= 0 (0: every row the same memory), outputs at least
  *     their width.  Pointers need only be aligned to their element; rows that
- *     are 16-byte aligned throughout run on wider loads and stores.
+ *     are 16-byte aligned throughout run on wider loads and stores (8-bit rows
+ *     on 4-byte boundaries nearly as fast).  Input rows off those boundaries
+ *     are read in whole aligned words of up to 16 bytes, of which each holds
+ *     at least a byte of the row.
  *   - dtype is a cbs_dtype and goes for every activation of the call; parameters,
  *     statistics and scales are float32, as the folded scale and bias are.
  *   - Outputs must not overlap inputs, workspaces or each other.
