@@ -92,8 +92,8 @@ struct NormArgs {
 };
 
 // One row per block at a time, read once for each sum it needs: any width, alignment and stride.  What the
-// kernels below do not hold comes here: rows of more than 16384 (f32 8192) elements and 16-bit rows of more than
-// 2048 off 16-byte boundaries.  Bound by its element-wise loads: bf16, 14592x4099 86 us (2.8 TB/s).
+// kernels below do not hold comes here: rows of more than 16384 elements, or 8192 in f32 or off 16-byte boundaries.
+// Bound by its element-wise loads: bf16, 14592x9001 209 us (2.5 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormArgs a)
 {
@@ -250,14 +250,14 @@ __device__ __forceinline__ uint32_t pack(float2 v, __half)
 // Two fp32 operations per instruction; each rounds like the scalar one.
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
-// Asynchronous copies to shared memory; copy4 reads `bytes` (at most 4) and fills up with zeros.
+// Asynchronous copies to shared memory.
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes)
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -266,23 +266,22 @@ __device__ __forceinline__ void copy_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One run: copied to its own SLOT bytes of shared memory, read from there as floats (zeros where the row
-// has no element), stored.  `n`, at least 1, is the number of elements that the row has from it on.  `odd` says that
-// the row starts in the middle of a word.
+// One run of a row: copied to its thread's own SLOT bytes of shared memory, read from there as floats, stored.
+// Only runs within the row are.
 template <typename T, int W>
 struct Run;
 
 template <>
 struct Run<float, 16> {
     static constexpr int V = 4, SLOT = 16;
-    static __device__ __forceinline__ void copy(uint32_t dst, const float *p, int, bool) { copy16(dst, p); }
-    static __device__ __forceinline__ void get(const void *slot, bool, float2 *v)
+    static __device__ __forceinline__ void copy(uint32_t dst, const float *p) { copy16(dst, p); }
+    static __device__ __forceinline__ void get(const void *slot, float2 *v)
     {
         const float4 f = *static_cast<const float4 *>(slot);
         v[0] = make_float2(f.x, f.y);
         v[1] = make_float2(f.z, f.w);
     }
-    static __device__ __forceinline__ void store(float *p, const float2 *v, int)
+    static __device__ __forceinline__ void store(float *p, const float2 *v)
     {
         *reinterpret_cast<float4 *>(p) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
     }
@@ -290,15 +289,15 @@ struct Run<float, 16> {
 template <>
 struct Run<float, 4> {
     static constexpr int V = 1, SLOT = 4;
-    static __device__ __forceinline__ void copy(uint32_t dst, const float *p, int, bool) { copy4(dst, p, 4); }
-    static __device__ __forceinline__ void get(const void *slot, bool, float *v) { *v = *static_cast<const float *>(slot); }
-    static __device__ __forceinline__ void store(float *p, const float *v, int) { *p = *v; }
+    static __device__ __forceinline__ void copy(uint32_t dst, const float *p) { copy4(dst, p); }
+    static __device__ __forceinline__ void get(const void *slot, float *v) { *v = *static_cast<const float *>(slot); }
+    static __device__ __forceinline__ void store(float *p, const float *v) { *p = *v; }
 };
 template <typename T>
 struct Run<T, 16> {
     static constexpr int V = 8, SLOT = 16;
-    static __device__ __forceinline__ void copy(uint32_t dst, const T *p, int, bool) { copy16(dst, p); }
-    static __device__ __forceinline__ void get(const void *slot, bool, float2 *v)
+    static __device__ __forceinline__ void copy(uint32_t dst, const T *p) { copy16(dst, p); }
+    static __device__ __forceinline__ void get(const void *slot, float2 *v)
     {
         const uint4 w = *static_cast<const uint4 *>(slot);
         v[0] = unpack(w.x, T());
@@ -306,40 +305,33 @@ struct Run<T, 16> {
         v[2] = unpack(w.z, T());
         v[3] = unpack(w.w, T());
     }
-    static __device__ __forceinline__ void store(T *p, const float2 *v, int)
+    static __device__ __forceinline__ void store(T *p, const float2 *v)
     {
         *reinterpret_cast<uint4 *>(p) = make_uint4(pack(v[0], T()), pack(v[1], T()), pack(v[2], T()), pack(v[3], T()));
     }
 };
+// Elements one by one, of a row that its threads copied together (fetch_row).
 template <typename T>
-struct Run<T, 4> {
-    static constexpr int V = 2, SLOT = 8;
-    static __device__ __forceinline__ void copy(uint32_t dst, const T *p, int n, bool odd)
-    {
-        if (odd) {
-            copy4(dst, p - 1, 4);
-            copy4(dst + 4, p + 1, n > 1 ? 2 : 0);
-        } else {
-            copy4(dst, p, n > 1 ? 4 : 2);
-        }
-    }
-    static __device__ __forceinline__ void get(const void *slot, bool odd, float2 *v)
-    {
-        const uint2 w = *static_cast<const uint2 *>(slot);
-        v[0] = unpack(odd ? __byte_perm(w.x, w.y, 0x5432) : w.x, T());
-    }
-    static __device__ __forceinline__ void store(T *p, const float2 *v, int n)
-    {
-        const uint32_t w = pack(v[0], T());
-        if (n > 1 && reinterpret_cast<uintptr_t>(p) % 4 == 0) {
-            *reinterpret_cast<uint32_t *>(p) = w;
-        } else {
-            unsigned short *h = reinterpret_cast<unsigned short *>(p);
-            h[0] = (unsigned short)w;
-            if (n > 1) h[1] = (unsigned short)(w >> 16);
-        }
-    }
+struct Run<T, 2> {
+    static constexpr int V = 1, SLOT = 2;
+    static __device__ __forceinline__ void copy(uint32_t, const T *) {}
+    static __device__ __forceinline__ void get(const void *slot, float *v) { *v = to_float(*static_cast<const T *>(slot)); }
+    static __device__ __forceinline__ void store(T *p, const float *v) { from_float(*v, p); }
 };
+
+// A row at any alignment copied by its TPR threads in the aligned 16-byte pieces that hold it: row_bytes() of
+// shared memory, in which the row starts where it does in its first piece.  (Every thread its own runs, as where
+// rows are aligned, takes two 4-byte copies for a pair of elements: 3001x777 8.6 us against 5.9.)
+constexpr int row_bytes(int elements) { return elements * 2 + 32; }
+template <int TPR, typename T>
+__device__ __forceinline__ void fetch_row(uint32_t dst, const T *row, int c, int lane)
+{
+    const uintptr_t from = reinterpret_cast<uintptr_t>(row) & ~(uintptr_t)15;
+    const int pieces = (int)((reinterpret_cast<uintptr_t>(row + c) - from + 15) >> 4);
+    for (int i = lane; i < pieces; i += TPR) copy16(dst + 16 * i, reinterpret_cast<const void *>(from + 16 * (uintptr_t)i));
+}
+template <typename T>
+__device__ __forceinline__ int start_of(const T *row) { return (int)(reinterpret_cast<uintptr_t>(row) & 15); }
 
 // V quantised values (in the low bytes of q) to memory.
 template <int V>
@@ -421,87 +413,113 @@ __device__ __forceinline__ float row_most(float v, float *scratch)
 }
 
 // Blocks stay for many rows.  Each thread keeps the gamma and beta of its columns in registers and copies
-// its own part of the coming kNormStages - 1 rows to shared memory with cp.async (no barrier: nobody else
+// its own part of the coming rows to shared memory with cp.async (no barrier: nobody else
 // reads it), so that memory stays busy while a row is summed.  Short rows share a warp.
 // Bound by memory: bf16, 16384x4096 45 us and 14592x8192 72 us (5.9 and 6.6 TB/s of 6.8 for a copy).  With
-// quantisation by its instructions, whatever part of the held row is used: 14592x4096 42 us, x5120 82, x8192 88.
-constexpr int kNormStages = 3;
-constexpr int norm_runs(int w) { return w == 16 ? 4 : 16; }  // of a row per thread
+// quantisation by its instructions: 14592x4096 39 us, x8192 81 (4.6 and 4.4 TB/s).
+constexpr int norm_stages(int w) { return w == 2 ? 4 : 3; }
 // Threads of a block: one row, or as many as 128 threads hold while a row stays within a warp.
 constexpr int norm_block(int tpr) { return tpr <= 32 ? 128 : tpr; }
 constexpr int kSmThreads = 512;  // on an SM: 128 registers a thread
 
-template <typename T, int W, int TPR, bool QUANT>
+template <typename T, int W, int NI, int TPR, bool QUANT>
 __global__ void __launch_bounds__(norm_block(TPR), kSmThreads / norm_block(TPR)) norm_stream_kernel(const NormArgs a)
 {
     using R = Run<T, W>;
-    constexpr int V = R::V, NI = norm_runs(W), E = NI * V, kBlock = norm_block(TPR), kGroups = kBlock / TPR;
-    extern __shared__ __align__(16) unsigned char norm_ring[];  // [stage][run][thread] slots
+    constexpr int V = R::V, E = NI * V, kBlock = norm_block(TPR), kGroups = kBlock / TPR;
+    constexpr int kStages = norm_stages(W);
+    constexpr bool kTogether = W == 2;  // a row's threads copy it together: what one reads, others have copied
+    extern __shared__ __align__(16) unsigned char norm_ring[];  // [stage][run][thread] slots, or [stage][group] rows
     // Two sets: a row's first sum may be written while a slow warp still reads the last row's.
     __shared__ float scratch[2][3][TPR > 32 ? TPR / 32 : 1];
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
     const int lane = threadIdx.x % TPR;
     const long long step = (long long)gridDim.x * kGroups;
+    // Of what a thread may hold, nothing lies in the row from past(i)'s run or unused(e)'s pair on.  Looked at where
+    // instructions set the pace: 14592x5120 quantised 82 -> 72 us, but 14592x16384 151 -> 162.
+    constexpr bool kSkips = W == 4 || (W == 16 && QUANT);
+    auto past = [&](int i) { return kSkips && i > 0 && i * V % (V < 4 ? 4 : V) == 0 && i * TPR * V >= a.c; };
+    auto unused = [&](int e) { return kSkips && e > 0 && 2 * e % (V < 4 ? 4 : V) == 0 && 2 * e / V * TPR * V >= a.c; };
     auto column = [&](int i) { return (i * TPR + lane) * V; };
-    auto slot = [&](int stage, int i) { return norm_ring + ((stage * NI + i) * kBlock + threadIdx.x) * R::SLOT; };
     auto row_at = [&](long long r) { return static_cast<const T *>(a.x) + r * a.x_stride; };
+    auto row_ring = [&](int stage) { return norm_ring + (stage * kGroups + threadIdx.x / TPR) * row_bytes(E * TPR); };
+    auto slot = [&](int stage, int i) { return norm_ring + ((stage * NI + i) * kBlock + threadIdx.x) * R::SLOT; };
     auto fetch = [&](long long r, int stage) {
         if (r < a.rows) {
             const T *x = row_at(r);
-            for (int i = 0; i < NI; ++i)
-                if (column(i) < a.c) R::copy(dev::smem_u32(slot(stage, i)), x + column(i), a.c - column(i), false);
+            if constexpr (kTogether) {
+                fetch_row<TPR>(dev::smem_u32(row_ring(stage)), x, a.c, lane);
+            } else {
+                for (int i = 0; i < NI; ++i)
+                    if (column(i) < a.c) R::copy(dev::smem_u32(slot(stage, i)), x + column(i));
+            }
         }
         copy_commit();
     };
     long long r = (long long)blockIdx.x * kGroups + threadIdx.x / TPR;
-    for (int s = 0; s < kNormStages - 1; ++s) fetch(r + s * step, s);
+    for (int s = 0; s < kStages - 1; ++s) fetch(r + s * step, s);
     float2 g[(E + 1) / 2], b[(E + 1) / 2];
     for (int i = 0; i < NI; ++i) {
         load_params<V>(a.gamma ? a.gamma + column(i) : nullptr, 1.0f, a.c - column(i), reinterpret_cast<float *>(g) + i * V);
         load_params<V>(a.beta ? a.beta + column(i) : nullptr, 0.0f, a.c - column(i), reinterpret_cast<float *>(b) + i * V);
     }
+    if constexpr (kTogether) {
+        copy_wait<kStages - 2>();
+        __syncthreads();
+    }
     const float per_c = 1.0f / (float)a.c;
     int stage = 0, parity = 0;
     // All groups of a block go round together; rows past the end are zeros and store nothing.
     for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += step, r += step) {
-        fetch(r + (kNormStages - 1) * step, stage == 0 ? kNormStages - 1 : stage - 1);
-        copy_wait<kNormStages - 1>();
+        fetch(r + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+        // Rows copied together are waited for one round ahead: the barrier of this row's sums is also theirs.
+        copy_wait<kTogether ? kStages - 2 : kStages - 1>();
         const bool live = r < a.rows;
+        const unsigned char *mine = row_ring(stage) + start_of(row_at(r));
         float2 v[E / 2];
         float *vs = reinterpret_cast<float *>(v);
-        for (int i = 0; i < NI; ++i) {
+#pragma unroll
+        for (int i = 0; i < NI && !past(i); ++i) {
             if (live && column(i) < a.c) {
-                if constexpr (V == 1)
-                    R::get(slot(stage, i), false, vs + i);
+                if constexpr (kTogether)
+                    R::get(mine + column(i) * sizeof(T), vs + i);
+                else if constexpr (V == 1)
+                    R::get(slot(stage, i), vs + i);
                 else
-                    R::get(slot(stage, i), false, v + i * (V / 2));
+                    R::get(slot(stage, i), v + i * (V / 2));
             } else {
                 for (int j = 0; j < V; ++j) vs[i * V + j] = 0.0f;
             }
         }
         if (!QUANT || a.normalise) {
             float2 s = both(0.0f);
-            for (int e = 0; e < E / 2; ++e) s = __fadd2_rn(s, v[e]);
+#pragma unroll
+            for (int e = 0; e < E / 2 && !unused(e); ++e) s = __fadd2_rn(s, v[e]);
             const float mean = row_sum<TPR>(s.x + s.y, scratch[parity][0]) * per_c;
             // Around the mean, and 0 again where the row has no element.
-            for (int e = 0; e < E / 2; ++e) v[e] = __fadd2_rn(v[e], both(-mean));
-            for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int e = 0; e < E / 2 && !unused(e); ++e) v[e] = __fadd2_rn(v[e], both(-mean));
+#pragma unroll
+            for (int i = 0; i < NI && !past(i); ++i)
                 if (column(i) + V > a.c)
                     for (int j = 0; j < V; ++j)
                         if (column(i) + j >= a.c) vs[i * V + j] = 0.0f;
             s = both(0.0f);
-            for (int e = 0; e < E / 2; ++e) s = __ffma2_rn(v[e], v[e], s);
+#pragma unroll
+            for (int e = 0; e < E / 2 && !unused(e); ++e) s = __ffma2_rn(v[e], v[e], s);
             const float rstd = rsqrtf(row_sum<TPR>(s.x + s.y, scratch[parity][1]) * per_c + a.eps);
             if (a.stats && lane == 0 && live) {
                 a.stats[r] = mean;
                 a.stats[a.rows + r] = rstd;
             }
-            for (int e = 0; e < E / 2; ++e) v[e] = __ffma2_rn(__fmul2_rn(v[e], both(rstd)), g[e], b[e]);
+#pragma unroll
+            for (int e = 0; e < E / 2 && !unused(e); ++e) v[e] = __ffma2_rn(__fmul2_rn(v[e], both(rstd)), g[e], b[e]);
         }
         if (QUANT) {
             float most = 0.0f;
-            for (int e = 0; e < E / 2; ++e) most = most_of(most, v[e].x, v[e].y);
+#pragma unroll
+            for (int e = 0; e < E / 2 && !unused(e); ++e) most = most_of(most, v[e].x, v[e].y);
             most = row_most<TPR>(most, scratch[parity][2]);
             float inv;
             const float scale = row_scale_of(__float_as_uint(most), &inv);
@@ -510,13 +528,16 @@ __global__ void __launch_bounds__(norm_block(TPR), kSmThreads / norm_block(TPR))
             // are scalar: a packed one is joined with the addition into one that rounds once, which tips values
             // next to a half to the other side (seen against the definition's own arithmetic).
             if (scale < __int_as_float(0x7f800000)) {
-                for (int e = 0; e < E / 2; ++e)
+#pragma unroll
+                for (int e = 0; e < E / 2 && !unused(e); ++e)
                     v[e] = __fadd2_rn(make_float2(__fmul_rn(v[e].x, inv), __fmul_rn(v[e].y, inv)), both(12582912.0f));
             } else {
-                for (int e = 0; e < E / 2; ++e) v[e] = both(0.0f);
+#pragma unroll
+                for (int e = 0; e < E / 2 && !unused(e); ++e) v[e] = both(0.0f);
             }
             if (live)
-                for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int i = 0; i < NI && !past(i); ++i)
                     if (column(i) < a.c) {
                         int q[V];
                         for (int j = 0; j < V; ++j) q[j] = __float_as_int(vs[i * V + j]);
@@ -524,15 +545,17 @@ __global__ void __launch_bounds__(norm_block(TPR), kSmThreads / norm_block(TPR))
                     }
         } else if (live) {
             T *y = static_cast<T *>(a.y) + r * a.y_stride;
-            for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int i = 0; i < NI && !past(i); ++i)
                 if (column(i) < a.c) {
                     if constexpr (V == 1)
-                        R::store(y + column(i), vs + i, 1);
+                        R::store(y + column(i), vs + i);
                     else
-                        R::store(y + column(i), v + i * (V / 2), a.c - column(i));
+                        R::store(y + column(i), v + i * (V / 2));
                 }
         }
-        stage = stage + 1 == kNormStages ? 0 : stage + 1;
+        if (kTogether && TPR <= 32) __syncwarp();
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         parity ^= 1;
     }
     copy_wait<0>();
@@ -540,113 +563,22 @@ __global__ void __launch_bounds__(norm_block(TPR), kSmThreads / norm_block(TPR))
 
 unsigned blocks_for_rows(long long rows) { return (unsigned)(rows < (1LL << 20) ? rows : (1LL << 20)); }
 
-template <typename T, int W, int TPR>
+template <typename T, int W, int NI, int TPR>
 cudaError_t norm_stream_launch(const NormArgs &a, int sm_count, cudaStream_t stream)
 {
     constexpr int kBlock = norm_block(TPR), kRows = kBlock / TPR;
-    constexpr int kSmem = kNormStages * norm_runs(W) * kBlock * Run<T, W>::SLOT;
+    constexpr int kSmem = norm_stages(W) * (W == 2 ? kRows * row_bytes(NI * TPR)
+                                                   : NI * kBlock * Run<T, W>::SLOT);
     const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sm_count * (kSmThreads / kBlock);
     const dim3 grid((unsigned)(need < room ? need : room)), block(kBlock);
     static bool allowed[2][kMaxDevices] = {};
     if (kSmem > 46 * 1024) {  // the sums take some of the first 48 KB
-        const cudaError_t e = a.q ? allow_dynamic_smem(norm_stream_kernel<T, W, TPR, true>, kSmem, allowed[1])
-                                  : allow_dynamic_smem(norm_stream_kernel<T, W, TPR, false>, kSmem, allowed[0]);
+        const cudaError_t e = a.q ? allow_dynamic_smem(norm_stream_kernel<T, W, NI, TPR, true>, kSmem, allowed[1])
+                                  : allow_dynamic_smem(norm_stream_kernel<T, W, NI, TPR, false>, kSmem, allowed[0]);
         if (e != cudaSuccess) return e;
     }
-    return a.q ? launch_overlapped(norm_stream_kernel<T, W, TPR, true>, grid, block, kSmem, stream, 1, a)
-               : launch_overlapped(norm_stream_kernel<T, W, TPR, false>, grid, block, kSmem, stream, 1, a);
-}
-
-// ------------------------------------------------------------------ 16-bit rows at any alignment
-// A row's elements one by one past the lanes that hold them: their places in memory words change from row to row,
-// and putting words together again costs more than it saves.  Nothing is copied ahead; many small blocks keep
-// memory busy instead.  f16, us, against the streamed kernel in 4-byte runs: 3001x777 7.0 / 8.6, 1500x1023 4.6 / 7.0,
-// 25000x257 17.5 / 19.5, 25000x1537 63 / 71 (2.4 TB/s; bound by its 2-byte loads and stores), and 2.2 / 3.7 where a
-// row of 33 leaves only latency.
-template <typename T, int NI, int TPR, bool QUANT>
-__global__ void __launch_bounds__(norm_block(TPR)) norm_row_kernel(const NormArgs a)
-{
-    constexpr int kGroups = norm_block(TPR) / TPR;
-    __shared__ float scratch[3][TPR / 32];
-    dev::grid_dependency_wait();
-    dev::grid_dependents_launch();
-    const int lane = threadIdx.x % TPR, group = threadIdx.x / TPR;
-    auto column = [&](int i) { return i * TPR + lane; };
-    const float per_c = 1.0f / (float)a.c;
-    for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += (long long)gridDim.x * kGroups) {
-        const long long r = base + group;
-        const bool live = r < a.rows;
-        const T *x = static_cast<const T *>(a.x) + r * a.x_stride;
-        float v[NI];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) v[i] = live && column(i) < a.c ? to_float(x[column(i)]) : 0.0f;
-        if (!QUANT || a.normalise) {
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) s += v[i];
-            const float mean = row_sum<TPR>(s, scratch[0]) * per_c;
-            s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                v[i] = column(i) < a.c ? v[i] - mean : 0.0f;
-                s = fmaf(v[i], v[i], s);
-            }
-            const float rstd = rsqrtf(row_sum<TPR>(s, scratch[1]) * per_c + a.eps);
-            if (a.stats && lane == 0 && live) {
-                a.stats[r] = mean;
-                a.stats[a.rows + r] = rstd;
-            }
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (column(i) < a.c)
-                    v[i] = fmaf(v[i] * rstd, a.gamma ? __ldg(a.gamma + column(i)) : 1.0f,
-                                a.beta ? __ldg(a.beta + column(i)) : 0.0f);
-        }
-        if (QUANT) {
-            float most = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) most = most_of(most, v[i], v[i]);
-            most = row_most<TPR>(most, scratch[2]);
-            float inv;
-            const float scale = row_scale_of(__float_as_uint(most), &inv);
-            if (lane == 0 && live) a.row_scale[r] = scale;
-            const bool finite = scale < __int_as_float(0x7f800000);
-#pragma unroll
-            for (int i = 0; i < NI; ++i)  // rounded to nearest even by the addition, as above
-                if (live && column(i) < a.c)
-                    a.q[r * a.q_stride + column(i)] =
-                        (int8_t)(finite ? __float_as_int(__fadd_rn(__fmul_rn(v[i], inv), 12582912.0f)) : 0);
-        } else if (live) {
-            T *y = static_cast<T *>(a.y) + r * a.y_stride;
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (column(i) < a.c) from_float(v[i], y + column(i));
-        }
-        if (TPR > 32) __syncthreads();  // before the scratch's next use
-    }
-}
-
-template <typename T, int NI, int TPR>
-cudaError_t norm_row_launch(const NormArgs &a, cudaStream_t stream)
-{
-    constexpr int kRows = norm_block(TPR) / TPR;
-    const dim3 grid(blocks_for_rows((a.rows + kRows - 1) / kRows)), block(norm_block(TPR));
-    return a.q ? launch_overlapped(norm_row_kernel<T, NI, TPR, true>, grid, block, 0, stream, 1, a)
-               : launch_overlapped(norm_row_kernel<T, NI, TPR, false>, grid, block, 0, stream, 1, a);
-}
-
-// Wider rows go to norm_wide_kernel: 25000x4099 143 us, where the streamed kernel in 4-byte runs took 239 and
-// this one 282, half of its threads having nothing.
-template <typename T>
-cudaError_t norm_row_pick(const NormArgs &a, cudaStream_t stream, bool *done)
-{
-    *done = true;
-    if (a.c <= 8 * 32) return norm_row_launch<T, 8, 32>(a, stream);
-    if (a.c <= 8 * 64) return norm_row_launch<T, 8, 64>(a, stream);
-    if (a.c <= 8 * 128) return norm_row_launch<T, 8, 128>(a, stream);
-    if (a.c <= 16 * 128) return norm_row_launch<T, 16, 128>(a, stream);
-    *done = false;
-    return cudaSuccess;
+    return a.q ? launch_overlapped(norm_stream_kernel<T, W, NI, TPR, true>, grid, block, kSmem, stream, 1, a)
+               : launch_overlapped(norm_stream_kernel<T, W, NI, TPR, false>, grid, block, kSmem, stream, 1, a);
 }
 
 bool aligned_for(const void *p, long long stride, int element, int bytes)
@@ -657,19 +589,37 @@ bool aligned_for(const void *p, long long stride, int element, int bytes)
 // A row gets the fewest threads, a power of two of them, that hold it: more sum over more lanes (bf16,
 // 8192x4096 on 256 threads of two vectors each 37 us, on 128 of four 25 us), and a number of warps that only
 // the launch knows costs more than it saves (16384x4096 quantised 65 us against 47 us).
-template <typename T, int W>
+template <typename T, int W, int NI>
 cudaError_t norm_stream_pick(const NormArgs &a, int sm_count, cudaStream_t stream, bool *done)
 {
-    constexpr int kHeld = norm_runs(W) * Run<T, W>::V;
+    constexpr int kHeld = NI * Run<T, W>::V;
     *done = true;
-    if (a.c <= 4 * kHeld) return norm_stream_launch<T, W, 4>(a, sm_count, stream);
-    if (a.c <= 8 * kHeld) return norm_stream_launch<T, W, 8>(a, sm_count, stream);
-    if (a.c <= 16 * kHeld) return norm_stream_launch<T, W, 16>(a, sm_count, stream);
-    if (a.c <= 32 * kHeld) return norm_stream_launch<T, W, 32>(a, sm_count, stream);
-    if (a.c <= 64 * kHeld) return norm_stream_launch<T, W, 64>(a, sm_count, stream);
-    if (a.c <= 128 * kHeld) return norm_stream_launch<T, W, 128>(a, sm_count, stream);
-    if (a.c <= 256 * kHeld) return norm_stream_launch<T, W, 256>(a, sm_count, stream);
-    if (a.c <= 512 * kHeld) return norm_stream_launch<T, W, 512>(a, sm_count, stream);
+    if (a.c <= 4 * kHeld) return norm_stream_launch<T, W, NI, 4>(a, sm_count, stream);
+    if (a.c <= 8 * kHeld) return norm_stream_launch<T, W, NI, 8>(a, sm_count, stream);
+    if (a.c <= 16 * kHeld) return norm_stream_launch<T, W, NI, 16>(a, sm_count, stream);
+    if (a.c <= 32 * kHeld) return norm_stream_launch<T, W, NI, 32>(a, sm_count, stream);
+    if (a.c <= 64 * kHeld) return norm_stream_launch<T, W, NI, 64>(a, sm_count, stream);
+    if (a.c <= 128 * kHeld) return norm_stream_launch<T, W, NI, 128>(a, sm_count, stream);
+    if (a.c <= 256 * kHeld) return norm_stream_launch<T, W, NI, 256>(a, sm_count, stream);
+    if (a.c <= 512 * kHeld) return norm_stream_launch<T, W, NI, 512>(a, sm_count, stream);
+    *done = false;
+    return cudaSuccess;
+}
+
+// 16-bit rows off 16-byte boundaries: 16 elements a thread, or 32 where 128 threads would not hold the row (the
+// least that fits is the fastest: f16, 14592x1537 29 / 28, 3001x777 5.8 / 6.2 us with 16 / 32; x2051 58 / 49).
+template <typename T>
+cudaError_t norm_together_pick(const NormArgs &a, int sm_count, cudaStream_t stream, bool *done)
+{
+    *done = true;
+    if (a.c <= 16 * 4) return norm_stream_launch<T, 2, 16, 4>(a, sm_count, stream);
+    if (a.c <= 16 * 8) return norm_stream_launch<T, 2, 16, 8>(a, sm_count, stream);
+    if (a.c <= 16 * 16) return norm_stream_launch<T, 2, 16, 16>(a, sm_count, stream);
+    if (a.c <= 16 * 32) return norm_stream_launch<T, 2, 16, 32>(a, sm_count, stream);
+    if (a.c <= 16 * 64) return norm_stream_launch<T, 2, 16, 64>(a, sm_count, stream);
+    if (a.c <= 16 * 128) return norm_stream_launch<T, 2, 16, 128>(a, sm_count, stream);
+    if (a.c <= 32 * 128) return norm_stream_launch<T, 2, 32, 128>(a, sm_count, stream);
+    if (a.c <= 32 * 256) return norm_stream_launch<T, 2, 32, 256>(a, sm_count, stream);
     *done = false;
     return cudaSuccess;
 }
@@ -684,11 +634,11 @@ cudaError_t norm_launch_t(const NormArgs &a, int sm_count, cudaStream_t stream)
     bool done = false;
     cudaError_t e;
     if (wide_loads)
-        e = norm_stream_pick<T, 16>(a, sm_count, stream, &done);
+        e = norm_stream_pick<T, 16, 4>(a, sm_count, stream, &done);
     else if constexpr (sizeof(T) == 4)
-        e = norm_stream_pick<T, 4>(a, sm_count, stream, &done);
+        e = norm_stream_pick<T, 4, 16>(a, sm_count, stream, &done);
     else
-        e = norm_row_pick<T>(a, stream, &done);
+        e = norm_together_pick<T>(a, sm_count, stream, &done);
     if (done) return e;
     return launch_overlapped(norm_wide_kernel<T>, dim3(blocks_for_rows(a.rows)), dim3(kWideThreads), 0, stream, 1, a);
 }
@@ -699,9 +649,10 @@ cudaError_t norm_launch_t(const NormArgs &a, int sm_count, cudaStream_t stream)
 // share one barrier.  At the end the rows of a block are joined in shared memory, and each block writes one
 // row of partial sums, which norm_grad_join_kernel adds up in order.  bf16 with the join: 16384x4096 72 us
 // (5.6 TB/s), 25600x256 12 us, of which the join and the two launches' ends are a third.  Rows off 16-byte
-// boundaries go through 4-byte runs: f32, 16384x1537 65 us (4.6 TB/s); bf16 68 us, bound by the runs' count.
+// boundaries: f32 in 4-byte runs, 14592x1536 58 us (4.6 TB/s); bf16 copied together, 14592x1537 43 us (3.1 TB/s),
+// bound by its element-wise reads and stores (61 us in 4-byte runs, two of them to a pair).
 constexpr int kGradElements = 16;  // of a row per thread: sums, gamma, h and g of more would not fit 128 registers
-constexpr int kGradStages = 3;
+constexpr int grad_stages(int w) { return w == 2 ? 4 : 3; }
 constexpr int grad_block(int tpr) { return tpr < 256 ? 256 : tpr; }
 
 // Sums of two values over the TPR threads of a row; scratch: a float2 for each warp of the block.
@@ -728,28 +679,40 @@ __global__ void __launch_bounds__(grad_block(TPR), kSmThreads / grad_block(TPR))
 {
     using R = Run<T, W>;
     constexpr int V = R::V, E = kGradElements, NI = E / V, kBlock = grad_block(TPR), kGroups = kBlock / TPR;
-    extern __shared__ __align__(16) unsigned char grad_ring[];  // [stage][x, dy][run][thread] slots; then the join
+    constexpr int kStages = grad_stages(W);
+    constexpr bool kTogether = W == 2;  // as in norm_stream_kernel
+    extern __shared__ __align__(16) unsigned char grad_ring[];  // [stage][x, dy][run][thread] slots or [group] rows; then the join
     __shared__ float2 scratch[2][kBlock / 32];
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
     const int lane = threadIdx.x % TPR;
     const long long step = (long long)gridDim.x * kGroups;
+    // As in norm_stream_kernel: f32, 14592x5121 245 -> 210 us.
+    constexpr bool kSkips = W != 2;
+    auto past = [&](int i) { return kSkips && i > 0 && i * V % (V < 4 ? 4 : V) == 0 && i * TPR * V >= a.c; };
+    auto unused = [&](int e) { return kSkips && e > 0 && 2 * e % (V < 4 ? 4 : V) == 0 && 2 * e / V * TPR * V >= a.c; };
     auto column = [&](int i) { return (i * TPR + lane) * V; };
     auto slot = [&](int stage, int which, int i) {
         return grad_ring + (((stage * 2 + which) * NI + i) * kBlock + threadIdx.x) * R::SLOT;
     };
+    auto row_ring = [&](int stage, int which) {
+        return grad_ring + ((stage * 2 + which) * kGroups + threadIdx.x / TPR) * row_bytes(E * TPR);
+    };
     auto x_at = [&](long long r) { return static_cast<const T *>(a.x) + r * a.x_stride; };
     auto dy_at = [&](long long r) { return static_cast<const T *>(a.dy) + r * a.dy_stride; };
-    auto odd = [&](const T *p) { return sizeof(T) == 2 && W == 4 && reinterpret_cast<uintptr_t>(p) % 4 != 0; };
     auto fetch = [&](long long r, int stage) {
         if (r < a.rows) {
             const T *x = x_at(r), *dy = dy_at(r);
-            const bool ox = odd(x), ody = odd(dy);
-            for (int i = 0; i < NI; ++i)
-                if (column(i) < a.c) {
-                    R::copy(dev::smem_u32(slot(stage, 0, i)), x + column(i), a.c - column(i), ox);
-                    R::copy(dev::smem_u32(slot(stage, 1, i)), dy + column(i), a.c - column(i), ody);
-                }
+            if constexpr (kTogether) {
+                fetch_row<TPR>(dev::smem_u32(row_ring(stage, 0)), x, a.c, lane);
+                fetch_row<TPR>(dev::smem_u32(row_ring(stage, 1)), dy, a.c, lane);
+            } else {
+                for (int i = 0; i < NI; ++i)
+                    if (column(i) < a.c) {
+                        R::copy(dev::smem_u32(slot(stage, 0, i)), x + column(i));
+                        R::copy(dev::smem_u32(slot(stage, 1, i)), dy + column(i));
+                    }
+            }
         }
         copy_commit();
     };
@@ -757,38 +720,48 @@ __global__ void __launch_bounds__(grad_block(TPR), kSmThreads / grad_block(TPR))
         return r < a.rows ? make_float2(__ldg(a.stats + r), __ldg(a.stats + a.rows + r)) : both(0.0f);
     };
     long long r = (long long)blockIdx.x * kGroups + threadIdx.x / TPR;
-    for (int s = 0; s < kGradStages - 1; ++s) fetch(r + s * step, s);
+    for (int s = 0; s < kStages - 1; ++s) fetch(r + s * step, s);
     float2 next = moments(r);
     float2 gamma[E / 2], dg[E / 2], db[E / 2];
     for (int i = 0; i < NI; ++i)
         load_params<V>(a.gamma ? a.gamma + column(i) : nullptr, 1.0f, a.c - column(i),
                        reinterpret_cast<float *>(gamma) + i * V);
     for (int e = 0; e < E / 2; ++e) dg[e] = db[e] = both(0.0f);
+    if constexpr (kTogether) {
+        copy_wait<kStages - 2>();
+        __syncthreads();
+    }
     const float per_c = 1.0f / (float)a.c;
     int stage = 0, parity = 0;
     for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += step, r += step) {
-        fetch(r + (kGradStages - 1) * step, stage == 0 ? kGradStages - 1 : stage - 1);
+        fetch(r + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
         const float mean = next.x, rstd = next.y;
         next = moments(r + step);
-        copy_wait<kGradStages - 1>();
-        const bool live = r < a.rows, ox = odd(x_at(r)), ody = odd(dy_at(r));
+        copy_wait<kTogether ? kStages - 2 : kStages - 1>();
+        const bool live = r < a.rows;
+        const unsigned char *my_x = row_ring(stage, 0) + start_of(x_at(r)), *my_dy = row_ring(stage, 1) + start_of(dy_at(r));
         float2 h[E / 2], g[E / 2];
         float *hs = reinterpret_cast<float *>(h), *gs = reinterpret_cast<float *>(g);
-        for (int i = 0; i < NI; ++i) {
+#pragma unroll
+        for (int i = 0; i < NI && !past(i); ++i) {
             if (live && column(i) < a.c) {
-                if constexpr (V == 1) {
-                    R::get(slot(stage, 0, i), ox, hs + i);
-                    R::get(slot(stage, 1, i), ody, gs + i);
+                if constexpr (kTogether) {
+                    R::get(my_x + column(i) * sizeof(T), hs + i);
+                    R::get(my_dy + column(i) * sizeof(T), gs + i);
+                } else if constexpr (V == 1) {
+                    R::get(slot(stage, 0, i), hs + i);
+                    R::get(slot(stage, 1, i), gs + i);
                 } else {
-                    R::get(slot(stage, 0, i), ox, h + i * (V / 2));
-                    R::get(slot(stage, 1, i), ody, g + i * (V / 2));
+                    R::get(slot(stage, 0, i), h + i * (V / 2));
+                    R::get(slot(stage, 1, i), g + i * (V / 2));
                 }
             } else {  // adds nothing anywhere: h and dy are both 0
                 for (int j = 0; j < V; ++j) hs[i * V + j] = mean, gs[i * V + j] = 0.0f;
             }
         }
         float2 s1 = both(0.0f), s2 = both(0.0f);
-        for (int e = 0; e < E / 2; ++e) {
+#pragma unroll
+        for (int e = 0; e < E / 2 && !unused(e); ++e) {
             const float2 d = g[e];
             h[e] = __fmul2_rn(__fadd2_rn(h[e], both(-mean)), both(rstd));
             dg[e] = __ffma2_rn(d, h[e], dg[e]);
@@ -799,19 +772,22 @@ __global__ void __launch_bounds__(grad_block(TPR), kSmThreads / grad_block(TPR))
         }
         const float2 sums = row_sum2<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), scratch[parity]);
         const float m1 = sums.x * per_c, m2 = sums.y * per_c;
-        for (int e = 0; e < E / 2; ++e)
+#pragma unroll
+        for (int e = 0; e < E / 2 && !unused(e); ++e)
             h[e] = __fmul2_rn(__fadd2_rn(__ffma2_rn(h[e], both(-m2), g[e]), both(-m1)), both(rstd));
         if (live) {
             T *dx = static_cast<T *>(a.dx) + r * a.dx_stride;
-            for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int i = 0; i < NI && !past(i); ++i)
                 if (column(i) < a.c) {
                     if constexpr (V == 1)
-                        R::store(dx + column(i), hs + i, 1);
+                        R::store(dx + column(i), hs + i);
                     else
-                        R::store(dx + column(i), h + i * (V / 2), a.c - column(i));
+                        R::store(dx + column(i), h + i * (V / 2));
                 }
         }
-        stage = stage + 1 == kGradStages ? 0 : stage + 1;
+        if (kTogether && TPR <= 32) __syncwarp();
+        stage = stage + 1 == kStages ? 0 : stage + 1;
         parity ^= 1;
     }
     copy_wait<0>();
@@ -874,7 +850,8 @@ template <typename T, int W, int TPR>
 cudaError_t norm_grad_stream_launch(GradArgs a, int sm_count, cudaStream_t stream)
 {
     constexpr int kBlock = grad_block(TPR), kRows = kBlock / TPR;
-    constexpr int kRing = kGradStages * 2 * (kGradElements / Run<T, W>::V) * kBlock * Run<T, W>::SLOT;
+    constexpr int kRing = grad_stages(W) * 2 * (W == 2 ? kRows * row_bytes(kGradElements * TPR)
+                                                       : kGradElements / Run<T, W>::V * kBlock * Run<T, W>::SLOT);
     constexpr int kJoin = kRows > 1 ? (TPR < 32 ? kBlock / 32 : kRows) * 2 * kGradElements * TPR * 4 : 0;
     constexpr int kSmem = kRing > kJoin ? kRing : kJoin;
     static bool allowed[kMaxDevices] = {};
@@ -909,7 +886,8 @@ cudaError_t norm_grad_launch_t(const GradArgs &a, int sm_count, cudaStream_t str
         const bool wide_loads = a.c % V == 0 && aligned_for(a.x, a.x_stride, sizeof(T), 16) &&
                                 aligned_for(a.dy, a.dy_stride, sizeof(T), 16) &&
                                 aligned_for(a.dx, a.dx_stride, sizeof(T), 16) && aligned_for(a.gamma, 0, 4, 16);
-        return wide_loads ? norm_grad_stream_pick<T, 16>(a, sm_count, stream) : norm_grad_stream_pick<T, 4>(a, sm_count, stream);
+        return wide_loads ? norm_grad_stream_pick<T, 16>(a, sm_count, stream)
+                          : norm_grad_stream_pick<T, sizeof(T) == 4 ? 4 : 2>(a, sm_count, stream);
     }
     cudaError_t e = launch_overlapped(norm_grad_wide_kernel<T>, dim3(blocks_for_rows(a.rows)), dim3(kWideThreads), 0,
                                       stream, 1, a);
