@@ -196,7 +196,7 @@ long long linear_workspace_bytes(long long m, int n, int k, int sm_count)
     if (m <= kFewRows || n <= 0) return 0;
     // For any alignment that the call's matrices may have.
     long long most = 0;
-    for (int align : {16, 4, 0}) {
+    for (int align : {16, 4, 1, 0}) {
         const long long bytes = path_workspace(best_path(m, n, k, sm_count, align), m, n, k, sm_count);
         if (bytes > most) most = bytes;
     }

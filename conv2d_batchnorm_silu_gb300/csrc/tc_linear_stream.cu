@@ -5,8 +5,8 @@
 // Sixteen warps hold the int8 of the coming steps in registers (kAhead steps of 128 K elements, 48 KB of
 // weights per SM in flight, whole 128-byte lines of each row), widen a step of weights and rows at a time into
 // swizzled f16 tiles, and hand them to the issuing warp.  Rows that start at multiples of 4 bytes only are loaded
-// in words (64x8192x8196 27 us, where 64x8192x8192 takes 23; widened before the product 76).  Every CTA takes an
-// equal run of the (channel tile, row tile, K step) sequence, so that all SMs read the same share of the weights,
+// in words, and rows that start anywhere in one word more (64x8192x8192 23 us, x8196 26, x8193 43; widened before
+// the product 75).  Every CTA takes an equal run of the (channel tile, row tile, K step) sequence, so that all SMs read the same share of the weights,
 // and leaves its tiles as fp32 partial sums in the workspace, which a second kernel adds in K order and finishes.
 //
 // Bound by the widening: a step of 128 K elements takes 1,200 clocks with 64 rows, of which its loads need some
@@ -71,8 +71,7 @@ __device__ __forceinline__ void give_up(unsigned int bit, volatile int *abort_fl
 // What rows of a hold past k.
 __device__ const uint4 g_zeros = {0, 0, 0, 0};
 
-// Predicated loads of 16 bytes straight into their registers, which otherwise keep what they hold: in one piece,
-// or in four of the first `left` bytes where rows start at any multiple of 4.
+// Predicated loads straight into their registers, which otherwise keep what they hold.
 __device__ __forceinline__ void load_if(uint32_t &v, const int8_t *p, bool yes)
 {
     asm volatile(
@@ -91,32 +90,48 @@ __device__ __forceinline__ void load_if(uint4 &v, const int8_t *p, bool yes)
         : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
         : "l"(p), "r"((int)yes));
 }
+// 16 bytes of a row, of which the row has `left`: in one load, in four words, or in the five words that hold them
+// where rows start anywhere, which are put in place when they are used.  Of weights what is past the row may be
+// anything; of rows it has to be zeros, and is but for the bytes of a last word (get_row).
 template <int ALIGN>
-__device__ __forceinline__ void load_weights(uint4 &v, const int8_t *p, int left)
-{
-    if constexpr (ALIGN == 16) {
-        load_if(v, p, left > 0);
-    } else {
-        load_if(v.x, p, left > 0);
-        load_if(v.y, p + 4, left > 4);
-        load_if(v.z, p + 8, left > 8);
-        load_if(v.w, p + 12, left > 12);
+struct Held {
+    uint4 v;
+    uint32_t more;
+    __device__ __forceinline__ void load_weights(const int8_t *p, int left)
+    {
+        if constexpr (ALIGN == 16) {
+            load_if(v, p, left > 0);
+        } else {
+            const int off = ALIGN == 1 ? (int)(reinterpret_cast<uintptr_t>(p) & 3) : 0;
+            load_if(v.x, p - off, left > 0);
+            load_if(v.y, p - off + 4, left > 4 - off);
+            load_if(v.z, p - off + 8, left > 8 - off);
+            load_if(v.w, p - off + 12, left > 12 - off);
+            if constexpr (ALIGN == 1) load_if(more, p - off + 16, off > 0 && left > 16 - off);
+        }
     }
-}
-// Zeros for what is past.
-template <int ALIGN>
-__device__ __forceinline__ void load_row(uint4 &v, const int8_t *p, int left)
-{
-    const int8_t *zeros = reinterpret_cast<const int8_t *>(&g_zeros);
-    if constexpr (ALIGN == 16) {
-        load_if(v, left > 0 ? p : zeros, true);
-    } else {
-        load_if(v.x, left > 0 ? p : zeros, true);
-        load_if(v.y, left > 4 ? p + 4 : zeros, true);
-        load_if(v.z, left > 8 ? p + 8 : zeros, true);
-        load_if(v.w, left > 12 ? p + 12 : zeros, true);
+    __device__ __forceinline__ void load_row(const int8_t *p, int left)
+    {
+        const int8_t *zeros = reinterpret_cast<const int8_t *>(&g_zeros);
+        if constexpr (ALIGN == 16) {
+            load_if(v, left > 0 ? p : zeros, true);
+        } else {
+            const int off = ALIGN == 1 ? (int)(reinterpret_cast<uintptr_t>(p) & 3) : 0;
+            load_if(v.x, left > 0 ? p - off : zeros, true);
+            load_if(v.y, left > 4 - off ? p - off + 4 : zeros, true);
+            load_if(v.z, left > 8 - off ? p - off + 8 : zeros, true);
+            load_if(v.w, left > 12 - off ? p - off + 12 : zeros, true);
+            if constexpr (ALIGN == 1) load_if(more, off > 0 && left > 16 - off ? p - off + 16 : zeros, true);
+        }
     }
-}
+    __device__ __forceinline__ uint4 get(uint32_t off) const
+    {
+        if constexpr (ALIGN != 1) return v;
+        const uint32_t bits = off * 8;
+        return make_uint4(__funnelshift_r(v.x, v.y, bits), __funnelshift_r(v.y, v.z, bits), __funnelshift_r(v.z, v.w, bits),
+                          __funnelshift_r(v.w, more, bits));
+    }
+};
 
 // As sts_v4, at a constant distance from a base.
 template <int OFFSET>
@@ -210,20 +225,26 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
                 src[2 + j] = a.a + (long long)min(rt * NT + j * 64 + r8, a.rows - 1) * a.a_stride + k0;
         };
         rows_of_tile();
-        uint4 held[AHEAD][LOADS];
-        auto load = [&](uint4 (&to)[LOADS]) {
+        Held<ALIGN> held[AHEAD][LOADS];
+        uint32_t offs[AHEAD];  // where the pieces of each start in a word, two bits for each; bit 31: a last step
+        auto load = [&](Held<ALIGN> (&to)[LOADS], uint32_t &off) {
             if (unloaded <= 0) return;  // what is held is not used again
             --unloaded;
             const int left = ks == a.k_steps - 1 ? last_left : 16;
+            if constexpr (ALIGN == 1) {
+                off = ks == a.k_steps - 1 ? 1u << 31 : 0u;
+#pragma unroll
+                for (int j = 0; j < LOADS; ++j) off |= ((uint32_t)reinterpret_cast<uintptr_t>(src[j]) & 3u) << (2 * j);
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                load_weights<ALIGN>(to[j], src[j], left);
+                to[j].load_weights(src[j], left);
                 src[j] += kStep;
             }
             if (has_row)
 #pragma unroll
                 for (int j = 0; j < C::ROW_LOADS; ++j) {
-                    load_row<ALIGN>(to[2 + j], src[2 + j], left);
+                    to[2 + j].load_row(src[2 + j], left);
                     src[2 + j] += kStep;
                 }
             if (++ks == a.k_steps) {
@@ -235,8 +256,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
 #pragma unroll
         for (int d = 0; d < AHEAD; ++d) {
 #pragma unroll
-            for (int j = 0; j < LOADS; ++j) held[d][j] = make_uint4(0, 0, 0, 0);
-            load(held[d]);
+            for (int j = 0; j < LOADS; ++j) held[d][j].v = make_uint4(0, 0, 0, 0), held[d][j].more = 0;
+            offs[d] = 0;
+            load(held[d], offs[d]);
         }
         // Bytes 16 q .. 16 q + 15 become two f16 pieces of the row's 256 bytes, in the first span (q < 4) or
         // the second.  The second span holds each two pieces in the other order, for weights and rows alike:
@@ -259,20 +281,25 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
                     break;
                 }
                 const uint32_t ta = ta0 + (uint32_t)(stage * C::A_BYTES), tb = tb0 + (uint32_t)(stage * C::B_BYTES);
-                widen_to<0>(ta + o0, ta + o1, held[d][0]);
-                widen_to<64 * 128>(ta + o0, ta + o1, held[d][1]);
+                auto weights = [&](int j) { return held[d][j].get(offs[d] >> (2 * j) & 3u); };
+                auto row = [&](int j) {
+                    const uint4 v = held[d][2 + j].get(offs[d] >> (2 * j + 4) & 3u);
+                    return ALIGN == 1 && (int)offs[d] < 0 ? within(v, 0, max(last_left, 0)) : v;
+                };
+                widen_to<0>(ta + o0, ta + o1, weights(0));
+                widen_to<64 * 128>(ta + o0, ta + o1, weights(1));
                 if (has_row) {
-                    widen_to<0>(tb + o0, tb + o1, held[d][2]);
-                    if constexpr (C::ROW_LOADS > 1) widen_to<64 * 128>(tb + o0, tb + o1, held[d][3]);
+                    widen_to<0>(tb + o0, tb + o1, row(0));
+                    if constexpr (C::ROW_LOADS > 1) widen_to<64 * 128>(tb + o0, tb + o1, row(1));
                     if constexpr (C::ROW_LOADS > 2) {
-                        widen_to<128 * 128>(tb + o0, tb + o1, held[d][4]);
-                        widen_to<192 * 128>(tb + o0, tb + o1, held[d][5]);
+                        widen_to<128 * 128>(tb + o0, tb + o1, row(2));
+                        widen_to<192 * 128>(tb + o0, tb + o1, row(3));
                     }
                 }
                 dev::fence_proxy_async_shared();  // the tensor core reads through the async proxy
                 __syncwarp();
                 if (lane == 0) dev::mbar_arrive(dev::smem_u32(&full[stage]));
-                load(held[d]);
+                load(held[d], offs[d]);
                 if (++stage == STAGES) stage = 0, phase ^= 1u;
             }
         }
@@ -506,7 +533,9 @@ cudaError_t sums_launch(const StreamArgs &a, cudaStream_t stream)
 template <typename T, int NT>
 cudaError_t stream_launch(const StreamArgs &a, int align, bool turned, cudaStream_t stream)
 {
-    cudaError_t e = align == 16 ? sums_launch<NT, 16>(a, stream) : sums_launch<NT, 4>(a, stream);
+    cudaError_t e = align == 16  ? sums_launch<NT, 16>(a, stream)
+                    : align == 4 ? sums_launch<NT, 4>(a, stream)
+                                 : sums_launch<NT, 1>(a, stream);
     if (e != cudaSuccess) return e;
     const int rows = a.rows < NT ? a.rows : NT;
     if (turned)
@@ -535,7 +564,8 @@ float tc_stream_time(long long rows, int channels, int k, int align, bool turned
     // 5.5 TB/s, with a slower second launch, where they are turned round).
     const StreamPlan p = plan_of(rows, channels, k, sm_count);
     const float whole = p.nt == 32 ? 0.60f : (p.nt == 64 ? 0.67f : (p.nt == 128 ? 0.91f : 1.50f));
-    const float step = align == 16 ? whole : whole * (p.nt <= 128 ? 1.2f : 1.4f);  // rows loaded in words of 4 bytes
+    const float words = p.nt <= 128 ? 1.2f : 1.4f, anywhere = p.nt == 128 ? 1.6f : 2.0f;
+    const float step = whole * (align == 16 ? 1.0f : (align == 4 ? words : anywhere));
     return (turned ? 6.5f : 5.0f) + step * (float)((p.steps + p.workers - 1) / p.workers) +
            (float)(p.workers + p.tiles) * (float)p.nt * kChannels * 8.0f / (turned ? 5.5e6f : 8.0e6f);
 }
@@ -546,7 +576,7 @@ int tc_stream_align(const LinearProblem &p)
         return reinterpret_cast<uintptr_t>(r.data) % bytes == 0 && r.stride % bytes == 0 && p.k % bytes == 0;
     };
     auto both_at = [&](int bytes) { return p.k > 0 && rows_at(p.a, bytes) && rows_at(p.w, bytes); };
-    return both_at(16) ? 16 : (both_at(4) ? 4 : 0);
+    return both_at(16) ? 16 : (both_at(4) ? 4 : (p.k > 0 ? 1 : 0));
 }
 
 long long tc_stream_workspace_bytes(long long rows, int channels, int k, int sm_count)

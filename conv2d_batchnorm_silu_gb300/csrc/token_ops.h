@@ -107,7 +107,7 @@ cudaError_t tc_linear_read_and_clear_error(cudaStream_t stream, unsigned int *ou
 
 // The linear layer with the weights widened on their way to the tensor cores, and turned, with its rows in the
 // weights' place (tc_linear_stream.cu): rows and channels are then n and m.
-int tc_stream_align(const LinearProblem &p);  // 16 or 4: all rows start at multiples of it, and k is one; 0: neither
+int tc_stream_align(const LinearProblem &p);  // 16, 4 or 1: all rows start at multiples of it, and k is one; 0: k is 0
 long long tc_stream_workspace_bytes(long long rows, int channels, int k, int sm_count);
 float tc_stream_time(long long rows, int channels, int k, int align, bool turned, int sm_count);  // modelled, us
 cudaError_t tc_stream_launch(const LinearProblem &p, bool turned, int sm_count, cudaStream_t stream);

@@ -491,3 +491,12 @@ def test_linear_of_few_channels_repeats_to_the_bit(capi, m, n, k):
                                        (5467, 386, 9264, 0)])
 def test_linear_of_rows_at_words(capi, m, n, k, pad, out):
     check_linear(capi, m, n, k, out, "silu", residual=True, pad=pad, offset=pad)
+
+
+# Rows that start anywhere, at sizes for which they are widened on their way.
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("m,n,k,pad", [(13, 4000, 6005, 0), (20, 300, 4097, 0), (40, 712, 2050, 0), (100, 712, 2051, 0),
+                                       (300, 300, 4095, 0), (200, 1000, 2048, 7), (1024, 38, 4967, 0), (3823, 21, 2853, 0),
+                                       (5000, 100, 4018, 1), (5000, 33, 2048, 3), (6000, 250, 4101, 0), (64, 1000, 129, 2)])
+def test_linear_of_rows_anywhere(capi, m, n, k, pad, out):
+    check_linear(capi, m, n, k, out, "silu", residual=True, pad=pad, offset=pad)
