@@ -5,6 +5,8 @@
 // a row's scale and a channel's scale multiply the whole sum, so the sum itself
 // is of integers and the scales, bias, activation and residual are an epilogue
 // on it, applied before the one rounding to the output's type.
+//
+// Sizes in the linear layer's comments are rows x channels x K, times of one call without the host's part.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -161,7 +163,7 @@ constexpr int kFewRows = 8;
 // sides changed), or both widened before (tc_linear.cu).
 enum Path { kTile, kStreamed, kTurned, kWidened };
 
-// Measured, us, tile / streamed / widened before: 24x614x243 5.2 / - / 6.0 (8.6 from the host), 64x1024x1024
+// Measured, us, tile / streamed / widened before: 24x614x243 5.2 / - / 6.0 (8.6 with the host's part), 64x1024x1024
 // 11.2 / 5.9 / 8.9, 64 rows of 8192x8192 - / 23 / 74, 512 rows - / 81 / 87, 1024 rows - / 152 / 121.  Streamed with
 // the sides changed / widened before: 25984x40x4800 41 / 132, 11609x128x4512 27 / 58, 100000x16x256 16 / 28,
 // 25600x256x1024 39 / 31, 16384x512x512 36 / 17.
