@@ -199,26 +199,37 @@ __global__ void __launch_bounds__(kWideThreads) norm_grad_columns_kernel(const G
     a.partial[(long long)blockIdx.y * 2 * a.c + a.c + i] = sb;
 }
 
-// Column sums of partial[partial_rows][2c] in a fixed order: 32 columns per block, eight
-// runs of rows summed side by side and joined in shared memory.
-constexpr int kJoinRuns = 8;
+// Column sums of partial[partial_rows][2c] in a fixed order: 32 columns per block, 32 runs of rows summed side by
+// side and joined by shuffles.  A thread's loads are all in flight at once (two rows an SM are ten a thread): the
+// kernel is one trip to L2 and its launch.
+constexpr int kJoinRuns = 32, kJoinLoads = 10;
 __global__ void __launch_bounds__(32 * kJoinRuns) norm_grad_join_kernel(const GradArgs a)
 {
-    __shared__ float part[kJoinRuns][32];
+    __shared__ float part[kJoinRuns][33];
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
     const int i = blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
-    if (i < 2 * a.c)
-        for (int r = threadIdx.y; r < a.partial_rows; r += kJoinRuns) s += a.partial[(long long)r * 2 * a.c + i];
+    for (int r0 = threadIdx.y; r0 < a.partial_rows; r0 += kJoinRuns * kJoinLoads) {
+        float v[kJoinLoads];
+#pragma unroll
+        for (int j = 0; j < kJoinLoads; ++j) {
+            const int r = r0 + j * kJoinRuns;
+            v[j] = r < a.partial_rows && i < 2 * a.c ? a.partial[(long long)r * 2 * a.c + i] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinLoads; ++j) s += v[j];
+    }
     part[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && i < 2 * a.c) {
-        for (int t = 1; t < kJoinRuns; ++t) s += part[t][threadIdx.x];
-        if (i < a.c)
-            a.dgamma[i] = s;
+    s = part[threadIdx.x][threadIdx.y];
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int column = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && column < 2 * a.c) {
+        if (column < a.c)
+            a.dgamma[column] = s;
         else
-            a.dbeta[i - a.c] = s;
+            a.dbeta[column - a.c] = s;
     }
 }
 
@@ -647,10 +658,10 @@ cudaError_t norm_launch_t(const NormArgs &a, int sm_count, cudaStream_t stream)
 // As norm_stream_kernel, for x and dy: each thread keeps gamma and the running sums of dy * h and dy for its
 // own columns in registers, so that x and dy are read once for all three gradients.  The two sums over a row
 // share one barrier.  At the end the rows of a block are joined in shared memory, and each block writes one
-// row of partial sums, which norm_grad_join_kernel adds up in order.  bf16 with the join: 16384x4096 72 us
-// (5.6 TB/s), 25600x256 12 us, of which the join and the two launches' ends are a third.  Rows off 16-byte
-// boundaries: f32 in 4-byte runs, 14592x1536 58 us (4.6 TB/s); bf16 copied together, 14592x1537 43 us (3.1 TB/s),
-// bound by its element-wise reads and stores (61 us in 4-byte runs, two of them to a pair).
+// row of partial sums, which norm_grad_join_kernel adds up in order.  bf16 with the join: 14592x4096 64 us
+// (5.6 TB/s), 14592x256 9 us, of which the join and the launches' ends are a third.  Rows off 16-byte
+// boundaries: f32 in 4-byte runs, 14592x1536 56 us (4.8 TB/s); bf16 copied together, 14592x1537 41 us (3.2 TB/s),
+// bound by its element-wise reads and stores (59 us in 4-byte runs, two of them to a pair).
 constexpr int kGradElements = 16;  // of a row per thread: sums, gamma, h and g of more would not fit 128 registers
 constexpr int grad_stages(int w) { return w == 2 ? 4 : 3; }
 constexpr int grad_block(int tpr) { return tpr < 256 ? 256 : tpr; }

@@ -500,3 +500,14 @@ def test_linear_of_rows_at_words(capi, m, n, k, pad, out):
                                        (5000, 100, 4018, 1), (5000, 33, 2048, 3), (6000, 250, 4101, 0), (64, 1000, 129, 2)])
 def test_linear_of_rows_anywhere(capi, m, n, k, pad, out):
     check_linear(capi, m, n, k, out, "silu", residual=True, pad=pad, offset=pad)
+
+
+@pytest.mark.parametrize("out", list(TYPES))
+@pytest.mark.parametrize("m,n,k", LARGER + TURNED[:5])
+def test_larger_linear_adds_to_its_residual_in_place(capi, m, n, k, out):
+    a, w, sa, sw = ints(1, m, k), ints(2, n, k), vector(3, m, 0.5) / 64, vector(4, n, 0.5) / (64 * k ** 0.5)
+    res = rows_of(5, m, n, out)
+    want = capi.linear_int8(a, w, sa, sw, None, "silu", res, TYPES[out])
+    y = res.clone()
+    assert capi.linear_int8(a, w, sa, sw, None, "silu", y, TYPES[out], y=y) is not None
+    assert torch.equal(y, want)
