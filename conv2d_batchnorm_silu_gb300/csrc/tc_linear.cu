@@ -472,6 +472,21 @@ cudaError_t gemm_launch_t(const LinearProblem &p, const __half *a16, const __hal
 
 }  // namespace
 
+cudaError_t encode_bytes_map(const void *base, long long rows, int k, long long stride, int box_rows, int box_k,
+                             CUtensorMap *out)
+{
+    const cudaError_t e = load_encoder();
+    if (e != cudaSuccess) return e;
+    cuuint64_t dims[2] = {(cuuint64_t)k / 4, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)stride};
+    cuuint32_t box[2] = {(cuuint32_t)box_k / 4, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 float tc_linear_time(long long m, int n, int k, int sm_count)
 {
     // Widening reads a byte and writes two for each element, at 5 TB/s.

@@ -5,13 +5,14 @@
 // Sixteen warps hold the int8 of the coming steps in registers (kAhead steps of 128 K elements, 48 KB of
 // weights per SM in flight, whole 128-byte lines of each row), widen a step of weights and rows at a time into
 // swizzled f16 tiles, and hand them to the issuing warp.  Rows that start at multiples of 4 bytes only are loaded
-// in words, and rows that start anywhere in one word more (64x8192x8192 23 us, x8196 26, x8193 43; widened before
-// the product 75).  Every CTA takes an equal run of the (channel tile, row tile, K step) sequence, so that all SMs read the same share of the weights,
-// and leaves its tiles as fp32 partial sums in the workspace, which a second kernel adds in K order and finishes.
+// in words, and rows that start anywhere in one word more (64x8192x8192 22 us, x8196 26, x8193 43; widened before
+// the product 75).  Every CTA takes an equal run of the (channel tile, row tile, K step) sequence, so that all SMs
+// read the same share of the weights, and leaves its tiles as fp32 partial sums in the workspace, which a second
+// kernel adds in K order and finishes.
 //
-// Bound by the widening: a step of 128 K elements takes 1,200 clocks with 64 rows, of which its loads need some
-// 700 at the memory's rate and its MMAs 500; 8192x8192 weights 16 rows 21 us, 64 rows 23 us (2.9 TB/s), 128 rows
-// 30 us (570 TOP/s), each with the join of the sums.
+// Bound by the widening: with loads in words a step of 128 K elements takes 1,400 clocks with 64 rows, of which
+// its bytes need some 700 at the memory's rate and its MMAs 500.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -155,6 +156,45 @@ __device__ __forceinline__ int worker_of(const StreamArgs &a, int g)
 {
     const int longer = a.run_extra * (a.run_base + 1);  // steps of the longer runs
     return g < longer ? g / (a.run_base + 1) : a.run_extra + (g - longer) / a.run_base;
+}
+
+// The sums of a run's tiles to the workspace: lane = channel, column = row of a.  This code runs once or twice a
+// launch and is bound by fetching itself: it only stores the sums.  (With the epilogue's arithmetic here for tiles
+// of one CTA, 64x512x512 took 8.9 us against 6.0 us with the join.)
+template <int NT>
+__device__ __forceinline__ void store_sums(const StreamArgs &a, int g0, int steps, uint32_t tmem, int warp, int lane,
+                                           uint64_t *tfull, uint64_t *tempty, volatile int *abort_flag)
+{
+    const int quarter = warp & 3;
+    int tile = g0 / a.k_steps, ks = g0 - tile * a.k_steps;
+    for (int piece = 0, left = steps; left > 0; ++piece, ++tile, ks = 0) {
+        const int take = min(left, a.k_steps - ks), buf = piece & 1;
+        left -= take;
+        const int rows = min(NT, a.rows - tile % a.row_tiles * NT);
+        int ok = 1;
+        if (lane == 0)
+            ok = wait_bounded(dev::smem_u32(&tfull[buf]), (uint32_t)(piece >> 1) & 1u, abort_flag, kWaitNs);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) {
+            if (lane == 0 && !*abort_flag) give_up(kErrTimeoutEpilogue, abort_flag);
+            break;
+        }
+        dev::tc_fence_after_sync();
+        const uint32_t taddr = tmem + (uint32_t)(buf * NT) + ((uint32_t)(quarter * 32) << 16);
+        float *out = a.partial + ((long long)(blockIdx.x + tile) * NT) * kChannels + quarter * 32 + lane;
+#pragma unroll 1
+        for (int c = 0; c < rows; c += 16) {
+            uint32_t v[16];
+            dev::tmem_ld_32x32b_x16(taddr + (uint32_t)c, v);
+            dev::tmem_ld_wait();
+            dev::reg_fence16(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) out[(c + i) * kChannels] = __uint_as_float(v[i]);  // within NT rows
+        }
+        dev::tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) dev::mbar_arrive(dev::smem_u32(&tempty[buf]));
+    }
 }
 
 // ALIGN: rows of both operands start at multiples of it, and k is one.
@@ -355,45 +395,252 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
         }
         __syncwarp();
     } else {
-        // ---------------------------------------------------------- epilogue: lane = channel, column = row of a
-        // This code runs once or twice a launch and is bound by fetching itself: it only stores the sums.  (With
-        // the epilogue's arithmetic here for tiles of one CTA, 64x512x512 took 8.9 us against 6.0 us with the join.)
-        const int quarter = warp & 3;
-        int tile = g0 / a.k_steps, ks = g0 - tile * a.k_steps;
-        for (int piece = 0, left = steps; left > 0; ++piece, ++tile, ks = 0) {
-            const int take = min(left, a.k_steps - ks), buf = piece & 1;
-            left -= take;
-            const int rows = min(NT, a.rows - tile % a.row_tiles * NT);
-            int ok = 1;
-            if (lane == 0)
-                ok = wait_bounded(dev::smem_u32(&tfull[buf]), (uint32_t)(piece >> 1) & 1u, abort_flag, kWaitNs);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) {
-                if (lane == 0 && !*abort_flag) give_up(kErrTimeoutEpilogue, abort_flag);
-                break;
-            }
-            dev::tc_fence_after_sync();
-            const uint32_t taddr = tmem + (uint32_t)(buf * NT) + ((uint32_t)(quarter * 32) << 16);
-            float *out = a.partial + ((long long)(blockIdx.x + tile) * NT) * kChannels + quarter * 32 + lane;
-#pragma unroll 1
-            for (int c = 0; c < rows; c += 16) {
-                uint32_t v[16];
-                dev::tmem_ld_32x32b_x16(taddr + (uint32_t)c, v);
-                dev::tmem_ld_wait();
-                dev::reg_fence16(v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) out[(c + i) * kChannels] = __uint_as_float(v[i]);  // within NT rows
-            }
-            dev::tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) dev::mbar_arrive(dev::smem_u32(&tempty[buf]));
-        }
+        store_sums<NT>(a, g0, steps, tmem, warp, lane, tfull, tempty, abort_flag);
     }
     dev::tc_fence_before_sync();
     __syncthreads();
     if (warp == kMmaWarp) {
         dev::tc_fence_after_sync();
         dev::tmem_dealloc<1>(tmem, C::TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------------ the same with the weights in tensor memory
+// Where both operands' rows are 16-byte aligned and a tile has at most 128 rows.  In linear_stream_kernel shared
+// memory takes the widened weights and gives them to the tensor core again, four bytes for each one of memory, and
+// each of its loads costs instructions.  Here the bytes of both operands come through TMA rings (96 to 140 KB in
+// flight), two groups of eight warps widen the weights of alternate steps from there into tensor memory, where the
+// tensor core finds its first operand (lane = channel), and four more widen the rows into shared memory.
+//
+// 8192x8192 weights: 32 rows 20.0 us (21.1 in linear_stream_kernel), 64 rows 21.8 (23.2), 128 rows 27.6 (30.2);
+// 64x512x512 5.9 (7.4); turned 25984x40x4800 37 (41).  A step takes 1,000 clocks with 32 rows, hot in L2 or not: what
+// 152 SMs draw from L2, weights at 4.8 TB/s and rows beside them; the first step comes 5,000 clocks after the start.
+// Tried and slower: prefetching each row's next 1 KB into L2 (32 us), loads in bursts of three steps (23.0).
+template <int NT>
+struct RingCfg {
+    static constexpr int W_RAW = kChannels * kStep, R_RAW = NT * kStep, RAW = W_RAW + R_RAW;
+    static constexpr int RAWS = NT == 128 ? 4 : (NT == 64 ? 6 : 7);  // steps of bytes in flight
+    static constexpr int B_BYTES = NT * kStep * 2;
+    static constexpr int STAGES = NT == 128 ? 3 : 4;  // widened steps
+    static constexpr int A_COLS = kStep / 2;          // of tensor memory, for each of them
+    static constexpr int WIDEN_WARPS = 8 + 4;         // of a step, for weights and rows; two such groups take turns
+    static constexpr int WARPS = 4 + 2 * WIDEN_WARPS + 4;  // TMA, MMA, two without work, widening, epilogue
+    static constexpr int SMEM = 1024 + RAWS * RAW + STAGES * B_BYTES + 256;
+    static_assert(2 * NT + STAGES * A_COLS <= 512 && SMEM <= 232448, "fits");
+};
+
+__device__ __forceinline__ void tc_mma_tmem_a(uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 words of each lane to 32 columns of its warp's quarter of tensor memory.
+__device__ __forceinline__ void tmem_st_32(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+        " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
+        " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+template <int NT>
+__global__ void __launch_bounds__(32 * RingCfg<NT>::WARPS, 1)
+    linear_ring_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_r, const StreamArgs a)
+{
+    using C = RingCfg<NT>;
+    constexpr int STAGES = C::STAGES, RAWS = C::RAWS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    const uint32_t sm_raw = dev::smem_u32(smem), sm_b = sm_raw + RAWS * C::RAW;
+    uint64_t *rfull = reinterpret_cast<uint64_t *>(smem + RAWS * C::RAW + STAGES * C::B_BYTES);
+    uint64_t *rempty = rfull + RAWS, *full = rempty + RAWS, *empty = full + STAGES, *tfull = empty + STAGES;
+    uint64_t *tempty = tfull + 2, *drain = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < RAWS; ++i) {
+            dev::mbar_init(dev::smem_u32(&rfull[i]), 1);
+            dev::mbar_init(dev::smem_u32(&rempty[i]), C::WIDEN_WARPS);
+        }
+        for (int i = 0; i < STAGES; ++i) {
+            dev::mbar_init(dev::smem_u32(&full[i]), C::WIDEN_WARPS);
+            dev::mbar_init(dev::smem_u32(&empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            dev::mbar_init(dev::smem_u32(&tfull[i]), 1);
+            dev::mbar_init(dev::smem_u32(&tempty[i]), kEpiWarps);
+        }
+        dev::mbar_init(dev::smem_u32(drain), 1);
+        *abort_flag = 0;
+        dev::fence_mbarrier_init();
+        dev::prefetch_tensormap(&tm_w);
+        dev::prefetch_tensormap(&tm_r);
+    }
+    if (warp == 1) {
+        dev::tmem_alloc<1>(dev::smem_u32(tmem_slot), 512);
+        dev::tmem_relinquish_alloc_permit<1>();
+    }
+    dev::tc_fence_before_sync();
+    __syncthreads();
+    dev::tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot, tmem_a = tmem + 2 * NT;
+    const int g0 = run_start(a, blockIdx.x), steps = run_start(a, blockIdx.x + 1) - g0;
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- loads
+        int tile = g0 / a.k_steps, ks = g0 - tile * a.k_steps, stage = 0;
+        uint32_t phase = 0, issued = 0, issued_parity = 0;
+        for (int g = 0; g < steps; ++g) {
+            bool ok = true;
+            if (lane == 0) {
+                ok = wait_bounded(dev::smem_u32(&rempty[stage]), phase ^ 1u, abort_flag, kWaitNs);
+                if (!ok && !*abort_flag) give_up(kErrTimeoutProducer, abort_flag);
+                if (ok) {
+                    const int ct = tile / a.row_tiles, rt = tile - ct * a.row_tiles;
+                    const uint32_t bar = dev::smem_u32(&rfull[stage]), dst = sm_raw + (uint32_t)(stage * C::RAW);
+                    dev::mbar_arrive_expect_tx(bar, C::RAW);
+                    dev::tma_load_2d(dst, &tm_w, bar, ks * (kStep / 4), ct * kChannels);
+                    dev::tma_load_2d(dst + C::W_RAW, &tm_r, bar, ks * (kStep / 4), rt * NT);
+                    issued |= 1u << stage;
+                    issued_parity = (issued_parity & ~(1u << stage)) | (phase << stage);
+                }
+            }
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (++stage == RAWS) stage = 0, phase ^= 1u;
+            if (++ks == a.k_steps) ks = 0, ++tile;
+        }
+        // Every load must have landed before the CTA may leave.
+        if (lane == 0)
+            for (int i = 0; i < RAWS; ++i)
+                if ((issued >> i) & 1u)
+                    if (!dev::mbar_wait_bounded(dev::smem_u32(&rfull[i]), (issued_parity >> i) & 1u, nullptr, kWaitNs)) {
+                        give_up(kErrTimeoutDrain, abort_flag);
+                        break;
+                    }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- MMAs, as in linear_stream_kernel
+        const bool issuer = elect_one();
+        constexpr uint32_t idesc = idesc_f16(kChannels, NT);
+        const uint64_t desc_b = dev::smem_desc_kmajor(sm_b, 128);
+        int stage = 0, piece = 0, ks = g0 % a.k_steps;
+        uint32_t phase = 0, accumulate = 0;
+        for (int g = 0; g < steps; ++g) {
+            const int buf = piece & 1;
+            bool ok = true;
+            if (accumulate == 0)
+                ok = wait_bounded(dev::smem_u32(&tempty[buf]), ((uint32_t)(piece >> 1) & 1u) ^ 1u, abort_flag, kWaitNs);
+            ok = ok && wait_bounded(dev::smem_u32(&full[stage]), phase, abort_flag, kWaitNs);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (issuer && !*abort_flag) give_up(kErrTimeoutMma, abort_flag);
+                break;
+            }
+            dev::tc_fence_after_sync();
+            const uint32_t ta = tmem_a + (uint32_t)(stage * C::A_COLS), d = tmem + (uint32_t)(buf * NT);
+            const uint64_t db = desc_b + (uint64_t)(stage * (C::B_BYTES >> 4));
+            const bool last = ++ks == a.k_steps || g + 1 == steps;
+            if (issuer) {
+#pragma unroll
+                for (int kk = 0; kk < kStep / 16; ++kk)
+                    tc_mma_tmem_a(d, ta + (uint32_t)(8 * kk), db + (uint64_t)(kk / 4 * (C::B_BYTES / 2 >> 4) + 2 * (kk % 4)),
+                                  idesc, kk > 0 ? 1u : accumulate);
+                dev::tc_commit<1>(dev::smem_u32(&empty[stage]));
+                if (last) dev::tc_commit<1>(dev::smem_u32(&tfull[buf]));
+            }
+            __syncwarp();
+            if (++stage == STAGES) stage = 0, phase ^= 1u;
+            accumulate = 1;
+            if (last) {
+                ks = 0;
+                ++piece;
+                accumulate = 0;
+            }
+        }
+        // Every MMA must have finished before tensor memory is freed.
+        if (issuer) {
+            dev::tc_commit<1>(dev::smem_u32(drain));
+            if (!dev::mbar_wait_bounded(dev::smem_u32(drain), 0, nullptr, kWaitNs)) give_up(kErrTimeoutDrain, abort_flag);
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 4 + 2 * C::WIDEN_WARPS) {
+        // ---------------------------------------------------------- widening
+        // Weights: a lane has its channel's 64 bytes of a step.  Rows: pieces of 16 bytes, as linear_stream_kernel
+        // places them; the second span's pieces hold their halves in the other order, here and there.
+        const int group = warp >= 4 + C::WIDEN_WARPS, mine = warp - 4 - group * C::WIDEN_WARPS;
+        const bool weights = mine < 8;
+        const int half = mine >> 2, channel = (warp & 3) * 32 + lane;
+        const int tid = (mine - 8) * 32 + lane, q = tid & 7, r8 = tid >> 3;
+        constexpr int kRowsAtOnce = 4 * (C::WIDEN_WARPS - 8);
+        const uint32_t span = (uint32_t)q >> 2, pair = ((uint32_t)q & 3u) * 2, turn = (uint32_t)r8 & 7u;
+        const uint32_t o0 = span * (C::B_BYTES / 2) + (uint32_t)r8 * 128 + (((pair + span) ^ turn) << 4);
+        const uint32_t o1 = span * (C::B_BYTES / 2) + (uint32_t)r8 * 128 + (((pair + (span ^ 1u)) ^ turn) << 4);
+        int raw = group, stage = group;
+        uint32_t raw_phase = 0, phase = 0;
+        for (int g = group; g < steps; g += 2) {
+            bool ok = wait_bounded(dev::smem_u32(&rfull[raw]), raw_phase, abort_flag, kWaitNs) &&
+                      wait_bounded(dev::smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kWaitNs);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) {
+                if (lane == 0 && !*abort_flag) give_up(kErrTimeoutProducer, abort_flag);
+                break;
+            }
+            const uint32_t from = sm_raw + (uint32_t)(raw * C::RAW);
+            if (weights) {
+                dev::tc_fence_after_sync();
+                uint32_t v[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 b = dev::lds_v4(from + (uint32_t)channel * 128 + ((uint32_t)((4 * half + c) ^ (channel & 7)) << 4));
+                    const uint2 x = widen4(half ? b.z : b.x), y = widen4(half ? b.w : b.y);
+                    const uint2 z = widen4(half ? b.x : b.z), w = widen4(half ? b.y : b.w);
+                    v[8 * c] = x.x, v[8 * c + 1] = x.y, v[8 * c + 2] = y.x, v[8 * c + 3] = y.y;
+                    v[8 * c + 4] = z.x, v[8 * c + 5] = z.y, v[8 * c + 6] = w.x, v[8 * c + 7] = w.y;
+                }
+                tmem_st_32(tmem_a + (uint32_t)(stage * C::A_COLS + 32 * half) + ((uint32_t)((warp & 3) * 32) << 16), v);
+                dev::tc_fence_before_sync();
+            } else {
+                const uint32_t to = sm_b + (uint32_t)(stage * C::B_BYTES);
+#pragma unroll
+                for (int r = 0; r < NT; r += kRowsAtOnce) {
+                    const uint4 b = dev::lds_v4(from + C::W_RAW + (uint32_t)(r + r8) * 128 + (((uint32_t)q ^ turn) << 4));
+                    const uint2 x = widen4(b.x), y = widen4(b.y), z = widen4(b.z), w = widen4(b.w);
+                    dev::sts_v4(to + o0 + (uint32_t)r * 128, x.x, x.y, y.x, y.y);
+                    dev::sts_v4(to + o1 + (uint32_t)r * 128, z.x, z.y, w.x, w.y);
+                }
+                dev::fence_proxy_async_shared();  // the tensor core reads through the async proxy
+            }
+            __syncwarp();
+            if (lane == 0) {
+                dev::mbar_arrive(dev::smem_u32(&full[stage]));
+                dev::mbar_arrive(dev::smem_u32(&rempty[raw]));
+            }
+            if ((raw += 2) >= RAWS) raw -= RAWS, raw_phase ^= 1u;
+            if ((stage += 2) >= STAGES) stage -= STAGES, phase ^= 1u;
+        }
+    } else if (warp >= 4) {
+        store_sums<NT>(a, g0, steps, tmem, warp, lane, tfull, tempty, abort_flag);
+    }
+    dev::tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        dev::tc_fence_after_sync();
+        dev::tmem_dealloc<1>(tmem, 512);
     }
 }
 
@@ -519,15 +766,35 @@ StreamPlan plan_of(long long m, int n, int k, int sm_count)
     return p;
 }
 
+template <int NT>
+cudaError_t ring_launch(const StreamArgs &a, cudaStream_t stream)
+{
+    using C = RingCfg<NT>;
+    static bool allowed[kMaxDevices] = {};
+    cudaError_t e = allow_dynamic_smem(linear_ring_kernel<NT>, C::SMEM, allowed);
+    CUtensorMap tw, tr;
+    if (e == cudaSuccess) e = encode_bytes_map(a.w, a.channels, a.k, a.w_stride, kChannels, kStep, &tw);
+    if (e == cudaSuccess) e = encode_bytes_map(a.a, a.rows, a.k, a.a_stride, NT, kStep, &tr);
+    return e != cudaSuccess ? e
+                            : launch_overlapped(linear_ring_kernel<NT>, dim3((unsigned)a.workers), dim3(32 * C::WARPS),
+                                                (size_t)C::SMEM, stream, 1, tw, tr, a);
+}
+
 template <int NT, int ALIGN>
 cudaError_t sums_launch(const StreamArgs &a, cudaStream_t stream)
 {
-    using C = StreamCfg<NT>;
-    static bool allowed[kMaxDevices] = {};
-    cudaError_t e = allow_dynamic_smem(linear_stream_kernel<NT, ALIGN>, C::SMEM, allowed);
-    return e != cudaSuccess ? e
-                            : launch_overlapped(linear_stream_kernel<NT, ALIGN>, dim3((unsigned)a.workers), dim3(kThreads),
-                                                (size_t)C::SMEM, stream, 1, a);
+    if constexpr (ALIGN == 16 && NT <= 128) {
+        // Rows that overlap (as where all are the same) or lie 2^40 bytes apart have no tensor map.
+        auto mapped = [&](long long stride) { return stride >= a.k && stride < 1LL << 40; };
+        return mapped(a.a_stride) && mapped(a.w_stride) ? ring_launch<NT>(a, stream) : sums_launch<NT, 4>(a, stream);
+    } else {
+        using C = StreamCfg<NT>;
+        static bool allowed[kMaxDevices] = {};
+        const cudaError_t e = allow_dynamic_smem(linear_stream_kernel<NT, ALIGN>, C::SMEM, allowed);
+        return e != cudaSuccess ? e
+                                : launch_overlapped(linear_stream_kernel<NT, ALIGN>, dim3((unsigned)a.workers),
+                                                    dim3(kThreads), (size_t)C::SMEM, stream, 1, a);
+    }
 }
 
 template <typename T, int NT>
@@ -563,9 +830,10 @@ float tc_stream_time(long long rows, int channels, int k, int align, bool turned
     // A step of 128 K elements as measured for each row tile, both launches, and the sums' way through L2 (at
     // 5.5 TB/s, with a slower second launch, where they are turned round).
     const StreamPlan p = plan_of(rows, channels, k, sm_count);
-    const float whole = p.nt == 32 ? 0.60f : (p.nt == 64 ? 0.67f : (p.nt == 128 ? 0.91f : 1.50f));
+    const float loaded = p.nt == 32 ? 0.60f : (p.nt == 64 ? 0.67f : (p.nt == 128 ? 0.91f : 1.50f));
+    const float ringed = p.nt == 32 ? 0.52f : (p.nt == 64 ? 0.56f : (p.nt == 128 ? 0.71f : 1.50f));
     const float words = p.nt <= 128 ? 1.2f : 1.4f, anywhere = p.nt == 128 ? 1.6f : 2.0f;
-    const float step = whole * (align == 16 ? 1.0f : (align == 4 ? words : anywhere));
+    const float step = align == 16 ? ringed : loaded * (align == 4 ? words : anywhere);
     return (turned ? 6.5f : 5.0f) + step * (float)((p.steps + p.workers - 1) / p.workers) +
            (float)(p.workers + p.tiles) * (float)p.nt * kChannels * 8.0f / (turned ? 5.5e6f : 8.0e6f);
 }

@@ -2,6 +2,7 @@
 // ABI (capi.cu) and their translation units.  Not part of the public interface.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -104,6 +105,11 @@ long long tc_linear_workspace_bytes(long long m, int n, int k);
 float tc_linear_time(long long m, int n, int k, int sm_count);  // modelled, us
 cudaError_t tc_linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
 cudaError_t tc_linear_read_and_clear_error(cudaStream_t stream, unsigned int *out);
+
+// Bytes [rows][k] at a distance of `stride` (all multiples of 16 but k) in boxes of box_rows rows of box_k bytes,
+// 128-byte swizzled; zeros past the ends.
+cudaError_t encode_bytes_map(const void *base, long long rows, int k, long long stride, int box_rows, int box_k,
+                             CUtensorMap *out);
 
 // The linear layer with the weights widened on their way to the tensor cores, and turned, with its rows in the
 // weights' place (tc_linear_stream.cu): rows and channels are then n and m.
