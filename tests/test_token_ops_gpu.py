@@ -511,3 +511,10 @@ def test_larger_linear_adds_to_its_residual_in_place(capi, m, n, k, out):
     y = res.clone()
     assert capi.linear_int8(a, w, sa, sw, None, "silu", y, TYPES[out], y=y) is not None
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("m,n,k", [(5, 300, 4096), (20, 300, 4096), (64, 712, 2048), (300, 300, 4096), (1500, 9, 4096), (1500, 1300, 400)])
+def test_linear_of_one_row_broadcast(capi, m, n, k):
+    a = ints(1, 1, k).expand(m, k)
+    check_linear(capi, m, n, k, "f32", "silu", residual=True, a=a)
+    check_linear(capi, m, n, k, "bf16", a=a, w=ints(2, 1, k).expand(n, k))
