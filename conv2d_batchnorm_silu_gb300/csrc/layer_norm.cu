@@ -92,8 +92,8 @@ struct NormArgs {
 };
 
 // One row per block at a time, read once for each sum it needs: any width, alignment and stride.  What the
-// kernels below do not hold comes here: rows of more than 16384 elements, or 8192 in f32 or off 16-byte boundaries.
-// Bound by its element-wise loads: bf16, 14592x9001 209 us (2.5 TB/s).
+// kernels below do not hold comes here: rows of more than 16384 elements (f32 8192), and many rows of 8193 to 9500
+// off 16-byte boundaries.  Bound by its element-wise loads: bf16, 14592x9001 209 us (2.5 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormArgs a)
 {
@@ -631,6 +631,9 @@ cudaError_t norm_together_pick(const NormArgs &a, int sm_count, cudaStream_t str
     if (a.c <= 16 * 128) return norm_stream_launch<T, 2, 16, 128>(a, sm_count, stream);
     if (a.c <= 32 * 128) return norm_stream_launch<T, 2, 32, 128>(a, sm_count, stream);
     if (a.c <= 32 * 256) return norm_stream_launch<T, 2, 32, 256>(a, sm_count, stream);
+    // Half of 512 threads have nothing of a row just beyond 8192, which only counts where there are many rows:
+    // f16, this / norm_wide_kernel, 64x8193 5.5 / 9.6 us, 14592x8193 227 / 164, 14592x10001 235 / 244, x16001 272 / 362.
+    if (a.c <= 32 * 512 && (a.c > 9500 || a.rows <= 1000)) return norm_stream_launch<T, 2, 32, 512>(a, sm_count, stream);
     *done = false;
     return cudaSuccess;
 }

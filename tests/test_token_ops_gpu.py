@@ -518,3 +518,16 @@ def test_linear_of_one_row_broadcast(capi, m, n, k):
     a = ints(1, 1, k).expand(m, k)
     check_linear(capi, m, n, k, "f32", "silu", residual=True, a=a)
     check_linear(capi, m, n, k, "bf16", a=a, w=ints(2, 1, k).expand(n, k))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,c", [(3, 9501), (40, 12345), (700, 16383), (1001, 9001)])
+def test_layer_norm_of_long_rows_off_alignment(capi, rows, c, dtype):
+    x, gamma, beta = rows_of(c, rows, c, dtype, pad=1), vector(1, c, 0.5), vector(2, c)
+    y, stats = capi.layer_norm(x, gamma, beta, EPS, return_stats=True)
+    want, mean, rstd = ref.layer_norm(host(x), host(gamma), host(beta), EPS)
+    assert (np.abs(host(y) - want) <= norm_bound(x, gamma, want, mean, rstd, dtype)).all()
+    q, scale = capi.quantize_rows(x)
+    most = np.abs(host(x)).max(1)
+    assert (np.abs(host(scale) * 127 - most) <= 4 * E32 * most).all()
+    assert (np.abs(host(q) * host(scale)[:, None] - host(x)) <= host(scale)[:, None] * (0.5 + 127 * 8 * E32)).all()
