@@ -193,7 +193,8 @@ int check_rows(const void *p, long long rows, long long c, long long stride, int
 
 bool norm_sizes_ok(long long rows, int c, int dtype)
 {
-    return rows >= 0 && rows <= (1LL << 40) && c >= 1 && dtype >= CBS_DTYPE_F32 && dtype <= CBS_DTYPE_F16;
+    // The kernels count columns, up to 2 c of them and a block beyond, in 32-bit integers.
+    return rows >= 0 && rows <= (1LL << 40) && c >= 1 && c <= (1 << 29) && dtype >= CBS_DTYPE_F32 && dtype <= CBS_DTYPE_F16;
 }
 
 int norm_call(const void *x, long long x_stride, const float *gamma, const float *beta, float eps, void *y,

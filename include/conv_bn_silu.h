@@ -334,6 +334,8 @@ int conv_bn_silu_forward_request(const void *x, const void *w, const float *scal
  *     on 4-byte boundaries nearly as fast).  Input rows off those boundaries
  *     are read in whole aligned words of up to 16 bytes, of which each holds
  *     at least a byte of the row.
+ *   - The norm, its gradient and the quantisation take up to 2^40 rows of 1 to 2^29
+ *     channels; wider rows are CBS_ERR_INVALID_ARG.
  *   - dtype is a cbs_dtype and goes for every activation of the call; parameters,
  *     statistics and scales are float32, as the folded scale and bias are.
  *   - Outputs must not overlap inputs, workspaces or each other.
