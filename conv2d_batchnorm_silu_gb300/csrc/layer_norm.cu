@@ -423,6 +423,21 @@ __device__ __forceinline__ float row_most(float v, float *scratch)
     return __uint_as_float(m);
 }
 
+// Quotients by a row's width, which is known beforehand: products with its reciprocal in two parts, with one rounding
+// at the end (Brisebarre, Muller and Raina, "Accelerating correctly rounded floating-point division when the divisor
+// is known in advance", 2004).  A quotient that fp32 holds comes out exactly, so the mean of equal values is that
+// value; by the rounded reciprocal alone a row of 1000 and 7 channels ended 0.02 off beta.  (f16, 3001x777 5.1 us; with
+// ordinary divisions, which give the same, 6.4.)
+struct Width {
+    float hi, lo;
+    __device__ __forceinline__ explicit Width(int c) : hi(1.0f / (float)c), lo(fmaf(-hi, (float)c, 1.0f) * hi) {}
+    __device__ __forceinline__ float share(float sum) const
+    {
+        const float q = sum * hi;
+        return fabsf(q) < __int_as_float(0x7f800000) ? fmaf(sum, hi, sum * lo) : q;  // infinities and NaN stay
+    }
+};
+
 // Blocks stay for many rows.  Each thread keeps the gamma and beta of its columns in registers and copies
 // its own part of the coming rows to shared memory with cp.async (no barrier: nobody else
 // reads it), so that memory stays busy while a row is summed.  Short rows share a warp.
@@ -479,7 +494,7 @@ __global__ void __launch_bounds__(norm_block(TPR), kSmThreads / norm_block(TPR))
         copy_wait<kStages - 2>();
         __syncthreads();
     }
-    const float per_c = 1.0f / (float)a.c;
+    const Width width(a.c);
     int stage = 0, parity = 0;
     // All groups of a block go round together; rows past the end are zeros and store nothing.
     for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += step, r += step) {
@@ -507,7 +522,7 @@ __global__ void __launch_bounds__(norm_block(TPR), kSmThreads / norm_block(TPR))
             float2 s = both(0.0f);
 #pragma unroll
             for (int e = 0; e < E / 2 && !unused(e); ++e) s = __fadd2_rn(s, v[e]);
-            const float mean = row_sum<TPR>(s.x + s.y, scratch[parity][0]) * per_c;
+            const float mean = width.share(row_sum<TPR>(s.x + s.y, scratch[parity][0]));
             // Around the mean, and 0 again where the row has no element.
 #pragma unroll
             for (int e = 0; e < E / 2 && !unused(e); ++e) v[e] = __fadd2_rn(v[e], both(-mean));
@@ -519,7 +534,9 @@ __global__ void __launch_bounds__(norm_block(TPR), kSmThreads / norm_block(TPR))
             s = both(0.0f);
 #pragma unroll
             for (int e = 0; e < E / 2 && !unused(e); ++e) s = __ffma2_rn(v[e], v[e], s);
-            const float rstd = rsqrtf(row_sum<TPR>(s.x + s.y, scratch[parity][1]) * per_c + a.eps);
+            // One rounding of the variance more than a division, and 2 units in the last place of the root: a relative
+            // error that the sum over the row has already.
+            const float rstd = rsqrtf(row_sum<TPR>(s.x + s.y, scratch[parity][1]) * width.hi + a.eps);
             if (a.stats && lane == 0 && live) {
                 a.stats[r] = mean;
                 a.stats[a.rows + r] = rstd;

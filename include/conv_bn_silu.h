@@ -359,10 +359,11 @@ typedef enum cbs_dtype {
  *   y = (x - mean) * rstd * gamma + beta
  *   x, y  : device, dtype [rows][c], row distances x_stride and y_stride
  *   gamma : device, float32 [c], or NULL for 1;  beta : likewise, or NULL for 0
- *   eps   : >= 0 and finite (a constant row with eps == 0 gives NaN)
+ *   eps   : >= 0 and finite (with eps == 0 a row whose variance comes out 0 gives NaN)
  *   stats : device, float32 [2][rows], written with mean, then rstd (what
  *           conv_bn_silu_layer_norm_backward needs), or NULL
  * Computed in fp32 with the variance summed around the mean; y rounded once.
+ * (A constant row whose sum fp32 holds has its value as its mean, and beta as y.)
  * rows == 0 is a no-op; c >= 1.
  */
 int conv_bn_silu_layer_norm(const void *x, long long x_stride, const float *gamma, const float *beta, float eps,

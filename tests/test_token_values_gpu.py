@@ -1,0 +1,50 @@
+"""Values of the token-wise operators that their definitions give exactly."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def capi():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from conv2d_batchnorm_silu_gb300 import capi
+    return capi
+
+
+def vector(seed, c):
+    return torch.randn(c, generator=torch.Generator().manual_seed(seed)).cuda()
+
+
+def inexact_reciprocal(low, high, step=1):
+    """The first width above low, a multiple of step, whose reciprocal is rounded so that 3 c (1/c) is not 3 in fp32."""
+    f = np.float32
+    return next(c for c in range(-(-low // step) * step, high, step) if f(f(3 * c) * f(f(1) / f(c))) != f(3))
+
+
+# Aligned and other widths for each number of threads that share a row.
+WIDTHS = sorted({inexact_reciprocal(low, 9 * low, step) for low in (7, 33, 65, 129, 257, 513, 1025, 2049, 4097, 8193)
+                 for step in (1, 8)})
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("c", WIDTHS)
+def test_layer_norm_of_one_value(capi, c, pad, dtype):
+    # Sums of c equal whole numbers are exact (below 2^24), so the mean is the value and what is left is beta.
+    for value in (3.0, -7.0, 1000.0):
+        if abs(value) * c >= 2 ** 24:
+            continue
+        x = torch.full((5, c + pad), value, dtype=TYPES[dtype], device="cuda")[:, :c]
+        gamma, beta = vector(1, c), vector(2, c)
+        y, stats = capi.layer_norm(x, gamma, beta, 1e-5, return_stats=True)
+        assert torch.equal(stats[0], torch.full((5,), value, device="cuda"))
+        assert torch.equal(y, beta.to(x.dtype).expand(5, c))
+        q, scale = capi.layer_norm_quantize(x, gamma, beta, 1e-5)
+        wq, ws = capi.quantize_rows(beta[None])
+        assert torch.equal(q, wq.expand(5, c)) and torch.equal(scale, ws.expand(5))
+        assert capi.layer_norm(x, gamma, beta, 0.0).isnan().all()
