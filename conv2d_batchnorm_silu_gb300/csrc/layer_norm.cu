@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(grad_block(TPR), kSmThreads / grad_block(TPR))
         copy_wait<kStages - 2>();
         __syncthreads();
     }
-    const float per_c = 1.0f / (float)a.c;
+    const Width width(a.c);
     int stage = 0, parity = 0;
     for (long long base = (long long)blockIdx.x * kGroups; base < a.rows; base += step, r += step) {
         fetch(r + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(grad_block(TPR), kSmThreads / grad_block(TPR))
             s2 = __ffma2_rn(g[e], h[e], s2);
         }
         const float2 sums = row_sum2<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), scratch[parity]);
-        const float m1 = sums.x * per_c, m2 = sums.y * per_c;
+        const float m1 = width.share(sums.x), m2 = width.share(sums.y);
 #pragma unroll
         for (int e = 0; e < E / 2 && !unused(e); ++e)
             h[e] = __fmul2_rn(__fadd2_rn(__ffma2_rn(h[e], both(-m2), g[e]), both(-m1)), both(rstd));

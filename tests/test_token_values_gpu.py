@@ -48,3 +48,20 @@ def test_layer_norm_of_one_value(capi, c, pad, dtype):
         wq, ws = capi.quantize_rows(beta[None])
         assert torch.equal(q, wq.expand(5, c)) and torch.equal(scale, ws.expand(5))
         assert capi.layer_norm(x, gamma, beta, 0.0).isnan().all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("c", WIDTHS)
+def test_layer_norm_gradient_of_one_value(capi, c, pad, dtype):
+    # h is 1, -1, 1, ... (0 in an odd last place): its sums with a constant gradient vanish, and the mean of that
+    # gradient is its one value, so nothing is left for the input.
+    rows = 5
+    store = torch.zeros(rows, c + pad, dtype=TYPES[dtype], device="cuda")
+    x = store[:, :c]
+    x[:, : c // 2 * 2] = torch.tensor([1.0, -1.0], dtype=x.dtype, device="cuda").repeat(c // 2)
+    dy = torch.full((rows, c + pad), 3.0, dtype=x.dtype, device="cuda")[:, :c]
+    stats = torch.stack((torch.zeros(rows), torch.ones(rows))).cuda()
+    dx, dgamma, dbeta = capi.layer_norm_backward(dy, x, None, stats)
+    assert not dx.any()
+    assert torch.equal(dgamma, 3.0 * rows * x[0].float()) and torch.equal(dbeta, torch.full_like(dbeta, 3.0 * rows))
