@@ -166,10 +166,23 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n)
     return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// SiLU to fp32 accuracy, because the output may be fp32; z of -100 and below gives -0.
+constexpr float kLog2E = 1.44269504f;                                       // log2(e) rounded
+constexpr float kLog2ERest = (float)(1.4426950408889634 - (double)kLog2E);  // and what that leaves
+
+// The activation of a sum whose output is of type T.  SiLU to the type's accuracy: for fp32 the library's exponential
+// and a quotient, each within 2 units in the last place, and -0 from -88.8 on, where e^-z leaves the range; for the
+// 16-bit types the fast exponential, off by some 1.2 |z| units of fp32, and -0 from -87.4 on, where the fast quotient
+// gives 0 and SiLU is above -1.1e-36.
+template <typename T>
 __device__ __forceinline__ float activated(float z, int activation)
 {
-    if (activation == CBS_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
+    if (activation == CBS_ACT_SILU) {
+        if constexpr (sizeof(T) == 4) {
+            const float s = 1.0f + expf(-z), k = s > 8.0e37f ? 0.00390625f : 1.0f;
+            return __fdividef(z, s * k) * k;
+        }
+        return __fdividef(z, 1.0f + __expf(-z));
+    }
     if (activation == CBS_ACT_RELU) return z < 0.0f ? 0.0f : z;  // keeps NaN
     return z;
 }
@@ -198,7 +211,7 @@ __device__ __forceinline__ void finish_one(const LinearEpilogue &e, float sum, l
 {
     float z = sum * (__ldg(e.a_scale + m) * __ldg(e.w_scale + n));
     if (e.bias) z += __ldg(e.bias + n);
-    z = activated(z, e.activation);
+    z = activated<T>(z, e.activation);
     if (e.residual) z += to_float(static_cast<const T *>(e.residual)[m * e.residual_stride + n]);
     from_float(z, static_cast<T *>(e.y) + m * e.y_stride + n);
 }
@@ -230,29 +243,61 @@ __device__ __forceinline__ float least_of(float a, float b, float c)
     return m;
 }
 
+// 1 + e^-z of two values, with e^-z = 2^-u, u = z log2(e), for z from -43 to 10^30.  For fp32 with what u loses in its
+// rounding and in that of log2(e): 2^(-u + d) = 2^-u (1 + d ln 2) but for d^2, where d is below 2^-16 unless e^-z is 0.
+template <typename T>
+__device__ __forceinline__ float2 one_plus_exp_of_minus(float2 z)
+{
+    const float2 one = make_float2(1.0f, 1.0f), u = __fmul2_rn(z, make_float2(kLog2E, kLog2E));
+    const float2 e = make_float2(exp2_approx(-u.x), exp2_approx(-u.y));
+    if constexpr (sizeof(T) != 4) return __fadd2_rn(e, one);
+    float2 d = __ffma2_rn(z, make_float2(-kLog2E, -kLog2E), u);
+    d = __ffma2_rn(z, make_float2(-kLog2ERest, -kLog2ERest), d);
+    return __ffma2_rn(e, __ffma2_rn(d, make_float2(0.693147181f, 0.693147181f), one), one);
+}
+
 // SiLU of 32 values, two at a time with one reciprocal between them, 1/a = b * (1 / (a b)): three
 // special-function operations a pair instead of four, which set the pace.  Values of -43 and below, for
-// which a b could leave the range, and NaN, which would spread to its neighbour, take the single form.
-__device__ __forceinline__ void silu32(float *v)
+// which a b could leave the range, and NaN, which would spread to its neighbour, take the single form.  Accurate to
+// the type T of the output, as in activated().  `stg` is the warp's own shared memory (finish_block): the single form
+// in fp32, which is long, goes through it a value at a time, so that it stands in the code once.
+template <typename T>
+__device__ __forceinline__ void silu32(float *v, uint32_t stg, int lane)
 {
     float least = v[0];
 #pragma unroll
     for (int i = 1; i < 31; i += 2) least = least_of(least, v[i], v[i + 1]);
     least = least_of(least, v[31], v[31]);
-    if (__all_sync(0xffffffffu, least > -43.0f)) {
+    bool paired = least > -43.0f;
+    if constexpr (sizeof(T) == 4) {
+        float most = v[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) most = fmaxf(most, v[i]);
+        paired = paired && most < 1e30f;
+    }
+    if (__all_sync(0xffffffffu, paired)) {
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
-            const float2 z = make_float2(v[i], v[i + 1]);
-            const float2 t = __fmul2_rn(z, make_float2(-1.44269504f, -1.44269504f));
-            const float2 s = __fadd2_rn(make_float2(exp2_approx(t.x), exp2_approx(t.y)), make_float2(1.0f, 1.0f));
+            const float2 z = make_float2(v[i], v[i + 1]), s = one_plus_exp_of_minus<T>(z);
             const float r = __fdividef(1.0f, s.x * s.y);
             const float2 y = __fmul2_rn(z, __fmul2_rn(make_float2(s.y, s.x), make_float2(r, r)));
             v[i] = y.x;
             v[i + 1] = y.y;
         }
+    } else if constexpr (sizeof(T) == 4) {
+        __syncwarp();  // the block before has been read
+        const uint32_t mine = stg + 4 * (uint32_t)lane;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) dev::sts_u32(mine + 128 * i, __float_as_uint(v[i]));
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            dev::sts_u32(mine + 128 * i,
+                         __float_as_uint(activated<T>(__uint_as_float(dev::lds_u32(mine + 128 * i)), CBS_ACT_SILU)));
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(dev::lds_u32(mine + 128 * i));
     } else {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = activated(v[i], CBS_ACT_SILU);
+        for (int i = 0; i < 32; ++i) v[i] = activated<T>(v[i], CBS_ACT_SILU);
     }
 }
 
@@ -318,10 +363,10 @@ __device__ __forceinline__ void finish_block(const LinearEpilogue &e, const uint
             }
     }
     if (e.activation == CBS_ACT_SILU) {
-        silu32(reinterpret_cast<float *>(v));
+        silu32<T>(reinterpret_cast<float *>(v), stg, lane);
     } else if (e.activation == CBS_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = make_float2(activated(v[i].x, CBS_ACT_RELU), activated(v[i].y, CBS_ACT_RELU));
+        for (int i = 0; i < 16; ++i) v[i] = make_float2(activated<T>(v[i].x, CBS_ACT_RELU), activated<T>(v[i].y, CBS_ACT_RELU));
     }
     __syncwarp();  // the block before has been read
     if (e.residual) {

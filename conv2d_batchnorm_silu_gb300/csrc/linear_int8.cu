@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, ALIGNED && ROWS <= 2 ? 4 : (RO
         const int g = threadIdx.x / (R * ROWS);
         int s = 0;
         for (int t = 0; t < split; ++t) s += part[g * split + t][out_e];
-        const float z = activated(fmaf((float)s, scale, bias), a.e.activation) + residual;
+        const float z = activated<T>(fmaf((float)s, scale, bias), a.e.activation) + residual;
         from_float(z, static_cast<T *>(a.e.y) + out_i * a.e.y_stride + out_n);
     }
 }

@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(32 * kJoinRows) linear_join_kernel(const Strea
 #pragma unroll
     for (int j = 0; j < 4; ++j)
         if (n + j < a.e.n) {
-            float z = activated(fmaf(s[j], scale[j], bias[j]), a.e.activation);
+            float z = activated<T>(fmaf(s[j], scale[j], bias[j]), a.e.activation);
             if (res) z += to_float(res[j]);
             from_float(z, y + j);
         }
@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(32 * kTurnWarps) linear_join_turned_kernel(con
     for (int j = 0; j < kChannels / kTurnWarps; ++j) {
         const long long m = m0 + j * kTurnWarps + warp;
         if (m >= a.e.m) break;
-        float z = activated(fmaf(turned[lane][j * kTurnWarps + warp], row_scale[j] * scale, bias), a.e.activation);
+        float z = activated<T>(fmaf(turned[lane][j * kTurnWarps + warp], row_scale[j] * scale, bias), a.e.activation);
         if (a.e.residual) z += to_float(static_cast<const T *>(a.e.residual)[m * a.e.residual_stride + n]);
         from_float(z, static_cast<T *>(a.e.y) + m * a.e.y_stride + n);
     }

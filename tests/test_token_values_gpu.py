@@ -1,4 +1,4 @@
-"""Values of the token-wise operators that their definitions give exactly."""
+"""Values of the token-wise operators that their definitions give exactly, and SiLU in fp32 to the last places."""
 import numpy as np
 import pytest
 import torch
@@ -6,6 +6,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+E32 = 2.0 ** -24
 
 
 @pytest.fixture(scope="module")
@@ -65,3 +66,36 @@ def test_layer_norm_gradient_of_one_value(capi, c, pad, dtype):
     dx, dgamma, dbeta = capi.layer_norm_backward(dy, x, None, stats)
     assert not dx.any()
     assert torch.equal(dgamma, 3.0 * rows * x[0].float()) and torch.equal(dbeta, torch.full_like(dbeta, 3.0 * rows))
+
+
+# Few rows, the one-launch tile, sums joined after streamed weights at each row tile, streamed rows, and the widened
+# product in each of its tiles.
+SIZES = [(3, 300, 16), (8, 300, 1000), (24, 300, 64), (20, 300, 4096), (40, 712, 2048), (100, 712, 2048), (300, 300, 4096),
+         (700, 1300, 400), (1500, 1300, 400), (2300, 2000, 1040), (1500, 9, 4096), (9000, 100, 2048), (100, 712, 2051)]
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+def test_linear_silu_in_fp32(capi, m, n, k):
+    # One product in each sum and scales of powers of two: z is exact, from -112 to 112 in steps of 1/8.
+    a, w = torch.zeros(m, k, dtype=torch.int8, device="cuda"), torch.zeros(n, k, dtype=torch.int8, device="cuda")
+    where = k // 2
+    a[:, where] = (torch.arange(m, device="cuda") * 29 % 257 - 128).to(torch.int8)
+    w[:, where] = (torch.arange(n, device="cuda") % 7 + 1).to(torch.int8)
+    a_scale, w_scale = torch.full((m,), 0.25, device="cuda"), torch.full((n,), 0.5, device="cuda")
+    z = a[:, where].double()[:, None] * w[:, where].double() / 8
+    want = z * torch.sigmoid(z)
+    y = capi.linear_int8(a, w, a_scale, w_scale, activation="silu", out_dtype=torch.float32).double()
+    # The exponential errs by 2 units in the last place, the sum, the quotient (or a reciprocal of two sums'
+    # product and two products) by half a unit each: 5 + 5 roundings.  Beyond -88.7 the exponential leaves the range and
+    # the result is -0, at most 88.8 * 2^-128 off.
+    tol = 10 * E32 * want.abs() + torch.where(z < -88.7, 2.7e-37, 0.0)
+    assert ((y - want).abs() <= tol).all(), float(((y - want).abs() / want.abs().clamp(min=1e-37)).max())
+    # The residual is added to that, and the 16-bit types see the same value but for what their rounding hides.
+    res = torch.full((m, n), 1.0, device="cuda")
+    y = capi.linear_int8(a, w, a_scale, w_scale, None, "silu", res, torch.float32).double()
+    assert ((y - want - 1.0).abs() <= tol + E32 * 1.001 * (want + 1.0).abs()).all()
+    for out, unit in ((torch.bfloat16, 2.0 ** -8), (torch.float16, 2.0 ** -11)):
+        y = capi.linear_int8(a, w, a_scale, w_scale, activation="silu", out_dtype=out).double()
+        tiny = 1e-36 if out == torch.bfloat16 else 2.0 ** -24
+        assert ((y - want).abs() <= unit * 1.01 * want.abs() + tiny).all()
+    capi.check()
