@@ -49,9 +49,10 @@ class TokenBlock:
             y, stats = capi.layer_norm(h, self.gamma, self.beta, self.eps, return_stats=True)
             off = y.float() - target
             losses.append(float(off.square().sum() / (2 * tokens)))
-            _, dgamma, dbeta = capi.layer_norm_backward((off / tokens).to(h.dtype), h, self.gamma, stats)
-            self.gamma = self.gamma - rate * dgamma
-            self.beta = self.beta - rate * dbeta
+            # The gradient of the sum over tokens, so that 16-bit types do not lose errors divided by their number.
+            _, dgamma, dbeta = capi.layer_norm_backward(off.to(h.dtype), h, self.gamma, stats)
+            self.gamma = self.gamma - rate / tokens * dgamma
+            self.beta = self.beta - rate / tokens * dbeta
         return losses
 
 

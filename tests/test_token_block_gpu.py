@@ -73,3 +73,21 @@ def test_tuning_the_norm_follows_the_gradient():
         g, b = g - 0.2 * (off * hat).sum(0) / len(rows), b - 0.2 * off.sum(0) / len(rows)
     assert np.abs(host(block.gamma) - g).max() <= 1e-4 and np.abs(host(block.beta) - b).max() <= 1e-4
     assert losses[2] < losses[1] < losses[0]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_tuning_over_many_tokens_in_16_bits(dtype):
+    # The error of a token divided by a million of them is nothing in f16, so the gradient has to be of its sum.
+    from conv2d_batchnorm_silu_gb300.token_block import TokenBlock
+    tokens, c, steps = 1 << 20, 16, 60
+    h = torch.randn(tokens, c, generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(dtype)
+    want_gamma, want_beta = 1 + 0.1 * rand(11, c), 0.1 * rand(12, c)
+    block = TokenBlock(torch.ones(c).cuda(), torch.zeros(c).cuda(), rand(9, 32, c), rand(7, 32), rand(10, c, 32), rand(8, c))
+    target = torch.nn.functional.layer_norm(h.float(), (c,), want_gamma, want_beta, 1e-5)
+    losses = block.tune_norm(h, target, steps=steps)
+    # Each step leaves 0.8 of an error of at most 0.4, and takes 0.2 of the mean of what rounding y to the type adds
+    # (at most a unit roundoff of |y| times |h|, both of mean square 1.3 and 1), so at most one such mean remains.
+    unit = 2.0 ** -11 if dtype == torch.float16 else 2.0 ** -8
+    left = 0.4 * 0.8 ** steps + 1.3 * unit
+    assert float((block.gamma - want_gamma).abs().max()) <= left and float((block.beta - want_beta).abs().max()) <= left
+    assert losses[-1] < losses[0]
