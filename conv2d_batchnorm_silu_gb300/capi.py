@@ -4,7 +4,10 @@ Argument marshalling only: every step of the layer runs in the CUDA library
 ``libconvbnsilu.so``; this module checks tensor dtypes/layouts, passes raw
 device pointers, sizes and the current CUDA stream, and turns status codes
 into exceptions.  PyTorch supplies device memory and streams.  There is no
-fallback: if the library is missing, importing this module raises.
+fallback: if the library is missing, importing this module raises.  The
+token-wise operators' calls are compiled over PyTorch's C++ tensors in
+``_token_ops.so``, which loads on their first use and raises then if it is
+missing or was built for another PyTorch or Python.
 """
 from __future__ import annotations
 
@@ -22,8 +25,6 @@ if not os.path.exists(LIB_PATH):
         "or conv2d_batchnorm_silu_gb300._build.build()); there is no non-CUDA fallback")
 
 _lib = ctypes.CDLL(LIB_PATH)
-
-from . import _token_ops  # noqa: E402  (compiled beside the library, which it links)
 
 CBS_OK = 0
 CBS_ERR_INVALID_ARG = 1
@@ -463,6 +464,21 @@ def silu_apply(t2: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> 
 # statistics and scales are dense float32.  Arguments are checked, and outputs and workspaces
 # made, in the compiled module _token_ops (csrc/binding.cpp), which returns a status that is
 # not CBS_OK as an int.
+_token_ops = None
+
+
+def _load_token_ops():
+    global _token_ops
+    try:
+        from . import _token_ops as module
+    except ImportError as e:
+        raise ImportError(
+            f"the token-wise operators need {os.path.join(_PKG, '_token_ops.so')}, built for this PyTorch and Python: "
+            f"build it with conv2d_batchnorm_silu_gb300._build.build() ({e})") from e
+    _token_ops = module
+    return module
+
+
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -473,8 +489,9 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
     x: float32, bf16 or f16 [..., c]; gamma, beta: fp32 [c] or None; y like x.  With return_stats
     also the fp32 statistics [2, rows] (mean, then 1/sqrt(var + eps)) for layer_norm_backward.
     """
-    out = _token_ops.layer_norm(x, gamma, beta, eps, return_stats, y,
-                                None if stream is None else _stream_handle(stream))
+    ops = _token_ops or _load_token_ops()
+    out = ops.layer_norm(x, gamma, beta, eps, return_stats, y,
+                         None if stream is None else _stream_handle(stream))
     if type(out) is int:
         _raise_if(out, "conv_bn_silu_layer_norm")
     return out
@@ -484,7 +501,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor |
                         dx: torch.Tensor | None = None, stream=None):
     """conv_bn_silu_layer_norm_backward: (dx, dgamma, dbeta) from dy, the forward call's x and gamma
     (None: ones) and the statistics it returned.  dx is like x; dgamma and dbeta are fp32 [c]."""
-    out = _token_ops.layer_norm_backward(dy, x, gamma, stats, dx, None if stream is None else _stream_handle(stream))
+    ops = _token_ops or _load_token_ops()
+    out = ops.layer_norm_backward(dy, x, gamma, stats, dx, None if stream is None else _stream_handle(stream))
     if type(out) is int:
         _raise_if(out, "conv_bn_silu_layer_norm_backward")
     return out
@@ -492,7 +510,8 @@ def layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor |
 
 def quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """conv_bn_silu_quantize_rows: (q, scale), q int8 like x, scale fp32 [...] with x close to q * scale."""
-    out = _token_ops.quantize_rows(x, q, None if stream is None else _stream_handle(stream))
+    ops = _token_ops or _load_token_ops()
+    out = ops.quantize_rows(x, q, None if stream is None else _stream_handle(stream))
     if type(out) is int:
         _raise_if(out, "conv_bn_silu_quantize_rows")
     return out
@@ -503,7 +522,8 @@ def layer_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, beta
                         stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """conv_bn_silu_layer_norm_quantize: layer_norm, its rows quantised in the same pass; (q, scale) as
     quantize_rows gives them."""
-    out = _token_ops.layer_norm_quantize(x, gamma, beta, eps, q, None if stream is None else _stream_handle(stream))
+    ops = _token_ops or _load_token_ops()
+    out = ops.layer_norm_quantize(x, gamma, beta, eps, q, None if stream is None else _stream_handle(stream))
     if type(out) is int:
         _raise_if(out, "conv_bn_silu_layer_norm_quantize")
     return out
@@ -524,8 +544,9 @@ def linear_int8(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale
     code = DTYPES.get(out_dtype)
     if code is None:
         raise TypeError(f"out_dtype must be torch.float32, torch.bfloat16 or torch.float16, got {out_dtype}")
-    out = _token_ops.linear_int8(a, w, a_scale, w_scale, bias, act, residual, code, y,
-                                 None if stream is None else _stream_handle(stream))
+    ops = _token_ops or _load_token_ops()
+    out = ops.linear_int8(a, w, a_scale, w_scale, bias, act, residual, code, y,
+                          None if stream is None else _stream_handle(stream))
     if type(out) is int:
         _raise_if(out, "conv_bn_silu_linear_int8")
     return out
