@@ -3,15 +3,18 @@
 One object per translation unit, compiled in parallel, then linked into a
 shared library with the CUDA runtime linked statically; beside it, with g++,
 ``_token_ops.so``, the Python calls of the token-wise operators over PyTorch's
-C++ tensors.  Both are rebuilt only when a source or header is newer than they.
+C++ tensors, where PyTorch is installed.  Each is rebuilt only when a source or
+header of its own is newer, the second also for another PyTorch or Python.
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
@@ -38,23 +41,50 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _inputs() -> list[str]:
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [BINDING_SOURCE, os.path.abspath(__file__)])
+def _headers() -> list[str]:
+    return glob.glob(os.path.join(ROOT, "include", "*.h"))
+
+
+def _newer_than(path: str, inputs: list[str]) -> bool:
+    """Whether `path` exists and none of its inputs has changed since."""
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in inputs)
+
+
+def _library_up_to_date() -> bool:
+    return _newer_than(LIB_PATH, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+                       + _headers() + [os.path.abspath(__file__)])
+
+
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return list(spec.submodule_search_locations)[0] if spec and spec.submodule_search_locations else None
+
+
+def _built_for() -> str:
+    """The PyTorch and the Python that the binding is compiled against."""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # not installed as a package
+        torch = _torch_dir()
+    return f"torch {torch}, {sys.implementation.cache_tag}"
+
+
+def _stamp_path() -> str:
+    return os.path.join(BUILD_DIR, "binding.for")
+
+
+def _binding_up_to_date() -> bool:
+    if not _newer_than(BINDING_PATH, _headers() + [BINDING_SOURCE, os.path.abspath(__file__)]):
+        return False
+    try:
+        with open(_stamp_path()) as f:
+            return f.read() == _built_for()
+    except FileNotFoundError:
+        return False
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(BINDING_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(f) <= t for f in _inputs())
-
-
-def _torch_dir() -> str:
-    spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("PyTorch not found: its headers are required to build the binding")
-    return list(spec.submodule_search_locations)[0]
+    return _library_up_to_date() and (_torch_dir() is None or _binding_up_to_date())
 
 
 def _compile_binding() -> str:
@@ -80,12 +110,16 @@ def _link_binding(obj: str) -> None:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING_PATH)
+    with open(_stamp_path(), "w") as f:
+        f.write(_built_for())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    """Compile every ``csrc/*.cu`` for sm_103a and link ``libconvbnsilu.so``, and the binding beside it;
-    returns the library's path."""
-    if not force and up_to_date():
+    """Compile every ``csrc/*.cu`` for sm_103a and link ``libconvbnsilu.so``, and the binding beside it where PyTorch
+    is installed; returns the library's path.  The library is in place before an error of the binding's is raised."""
+    library = force or not _library_up_to_date()
+    with_binding = _torch_dir() is not None and (force or not _binding_up_to_date())
+    if not library and not with_binding:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     flags = NVCC_FLAGS + ARCH_FLAGS + (extra_flags or [])
@@ -100,16 +134,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(res.stdout + res.stderr)
         return obj
 
-    srcs = sources()
+    srcs = sources() if library else []
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = ex.submit(_compile_binding) if with_binding else None
         objs = list(ex.map(compile_one, srcs))
-        binding_obj = binding.result()
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, LIB_PATH)
-    _link_binding(binding_obj)
+    if library:
+        tmp = LIB_PATH + f".tmp{os.getpid()}"
+        cmd = [nvcc(), *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", tmp, *objs]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, LIB_PATH)
+    if binding is not None:
+        _link_binding(binding.result())
     return LIB_PATH

@@ -65,3 +65,51 @@ assert "{PACKAGE}._token_ops" in sys.modules
 """
     run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
     assert run.returncode == 0, run.stderr
+
+
+@pytest.fixture
+def small_build(built, monkeypatch, tmp_path):
+    """_build over a source of a few lines, in a folder of its own."""
+    source = tmp_path / "answer.cu"
+    source.write_text('extern "C" int answer() { return 42; }\n')
+    monkeypatch.setattr(built, "sources", lambda: [str(source)])
+    monkeypatch.setattr(built, "BUILD_DIR", str(tmp_path / "_build"))
+    monkeypatch.setattr(built, "LIB_PATH", str(tmp_path / "libconvbnsilu.so"))
+    monkeypatch.setattr(built, "BINDING_PATH", str(tmp_path / "_token_ops.so"))
+    monkeypatch.setattr(built, "PKG_DIR", str(tmp_path))
+    return built
+
+
+def answer(path):
+    code = f"import ctypes; assert ctypes.CDLL({path!r}).answer() == 42"
+    assert subprocess.run([sys.executable, "-c", code]).returncode == 0
+
+
+def test_the_library_builds_where_there_is_no_pytorch(small_build, monkeypatch):
+    import importlib.util
+    found = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else found(name, *a))
+    assert small_build.build() == small_build.LIB_PATH
+    answer(small_build.LIB_PATH)
+    assert not os.path.exists(small_build.BINDING_PATH) and small_build.up_to_date()
+
+
+def test_the_library_is_there_when_the_compiled_module_does_not_build(small_build, monkeypatch, tmp_path):
+    broken = tmp_path / "binding.cpp"
+    broken.write_text("#error headers of another PyTorch\n")
+    monkeypatch.setattr(small_build, "BINDING_SOURCE", str(broken))
+    with pytest.raises(RuntimeError, match="headers of another PyTorch"):
+        small_build.build()
+    answer(small_build.LIB_PATH)
+    before = os.path.getmtime(small_build.LIB_PATH)
+    with pytest.raises(RuntimeError, match="headers of another PyTorch"):  # and is not built again for it
+        small_build.build()
+    assert os.path.getmtime(small_build.LIB_PATH) == before
+
+
+def test_the_compiled_module_is_built_again_for_another_pytorch(built, monkeypatch):
+    import importlib.metadata
+    assert built.up_to_date()
+    version = importlib.metadata.version
+    monkeypatch.setattr(importlib.metadata, "version", lambda name: "0.1" if name == "torch" else version(name))
+    assert not built.up_to_date()
