@@ -13,6 +13,7 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
@@ -183,8 +184,8 @@ PyObject *guarded(Py_ssize_t given, Py_ssize_t wanted, F &&f)
         PyErr_SetString(r.type, r.text.c_str());
     } catch (const Status &s) {
         return PyLong_FromLong(s.code);
-    } catch (const std::exception &e) {  // PyTorch's, such as out of memory
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {  // PyTorch's, as PyTorch raises them (torch.OutOfMemoryError and the others)
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }
