@@ -200,7 +200,8 @@ PyObject *layer_norm(PyObject *, PyObject *const *arg, Py_ssize_t count)
         const float *gamma = vector_of(arg[1], r.c, "gamma", device), *beta = vector_of(arg[2], r.c, "beta", device);
         const double eps = PyFloat_AsDouble(arg[3]);
         if (eps == -1.0 && PyErr_Occurred()) return nullptr;
-        const bool with_stats = PyObject_IsTrue(arg[4]) == 1;
+        const int with_stats = PyObject_IsTrue(arg[4]);
+        if (with_stats < 0) return nullptr;
         const Stream stream(arg[6], device);
         const at::Tensor y = output(arg[5], x.sizes(), x.scalar_type(), "y", stream);
         const Rows ry = rows_of(y, "y", device);

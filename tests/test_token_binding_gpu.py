@@ -30,3 +30,12 @@ def test_out_of_memory_is_pytorchs_own_error(capi):
     finally:
         torch.cuda.set_per_process_memory_fraction(1.0)
     assert not capi.layer_norm(x[:3]).any()  # and the calls go on
+
+
+def test_an_argument_without_a_truth_value(capi):
+    class Neither:
+        def __bool__(self):
+            raise KeyError("neither")
+
+    with pytest.raises(KeyError, match="neither"):
+        capi.layer_norm(torch.zeros(2, 8, device="cuda"), return_stats=Neither())
