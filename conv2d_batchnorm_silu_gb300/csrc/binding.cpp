@@ -133,6 +133,8 @@ struct Stream {
                 PyErr_Clear();
                 wrong_type("stream must be a CUDA stream");
             }
+            // The runtime's handle for the default stream, whose number PyTorch gives a stream of its own.
+            if (p == static_cast<void *>(cudaStreamLegacy)) p = nullptr;
             guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), (c10::DeviceIndex)device));
         }
         handle = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();

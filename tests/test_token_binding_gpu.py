@@ -39,3 +39,26 @@ def test_an_argument_without_a_truth_value(capi):
 
     with pytest.raises(KeyError, match="neither"):
         capi.layer_norm(torch.zeros(2, 8, device="cuda"), return_stats=Neither())
+
+
+def test_streams_by_handle(capi):
+    # The default stream, the runtime's two names for it, and a stream of one's own, each alone and in PyTorch's class.
+    x = torch.randn(300, 64, device="cuda").bfloat16()
+    w, scale = torch.randint(-9, 9, (32, 64), dtype=torch.int8, device="cuda"), torch.rand(32, device="cuda")
+
+    def block(stream):
+        y, stats = capi.layer_norm(x, return_stats=True, stream=stream)
+        q, rows = capi.layer_norm_quantize(x, stream=stream)
+        return (y, *capi.layer_norm_backward(y, x, None, stats, stream=stream), *capi.quantize_rows(x, stream=stream),
+                capi.linear_int8(q, w, rows, scale, stream=stream))
+
+    want = block(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (0, 1, 2, side, side.cuda_stream, torch.cuda.ExternalStream(side.cuda_stream)):
+        got = block(stream)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got)), stream
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    with pytest.raises(TypeError):
+        capi.layer_norm(x, stream=object())
