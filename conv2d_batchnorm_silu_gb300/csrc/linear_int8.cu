@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "cbs_internal.h"
 #include "linear_device.cuh"
 #include "ptx.cuh"
@@ -205,11 +207,16 @@ long long linear_workspace_bytes(long long m, int n, int k, int sm_count)
     return most;
 }
 
+// Whether a kernel that may record an error was launched, or captured, since the library was loaded.
+static std::atomic<bool> g_recorders_launched{false};
+
 cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream)
 {
     if (p.m > kFewRows) {
-        switch (best_path(p.m, p.n, p.k, sm_count, tc_stream_align(p))) {
-        case kTile: return linear_tile_launch(p, stream);
+        const Path path = best_path(p.m, p.n, p.k, sm_count, tc_stream_align(p));
+        if (path == kTile) return linear_tile_launch(p, stream);
+        g_recorders_launched.store(true, std::memory_order_relaxed);
+        switch (path) {
         case kStreamed: return tc_stream_launch(p, false, sm_count, stream);
         case kTurned: return tc_stream_launch(p, true, sm_count, stream);
         default: return tc_linear_launch(p, sm_count, stream);
@@ -231,6 +238,9 @@ cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t str
 
 cudaError_t linear_read_and_clear_error(cudaStream_t stream, unsigned int *out)
 {
+    // Each word is a copy and a wait, 10 us of a check, which programs without these kernels need not pay.
+    *out = 0;
+    if (!g_recorders_launched.load(std::memory_order_relaxed)) return cudaSuccess;
     unsigned int a = 0, b = 0;
     cudaError_t e = tc_linear_read_and_clear_error(stream, &a);
     if (e == cudaSuccess) e = tc_stream_read_and_clear_error(stream, &b);
