@@ -36,6 +36,7 @@ CBS_ERR_TIMEOUT = 5
 ALGOS = {"auto": 0, "tcgen05": 1, "direct": 2}
 ACTIVATIONS = {"silu": 0, "identity": 1, "relu": 2}
 ALGO_NAMES = {v: k for k, v in ALGOS.items()}
+LINEAR_KERNELS = ("few", "tile", "ring", "stream", "gemm")
 
 _i = ctypes.c_int
 _p = ctypes.c_void_p
@@ -54,6 +55,15 @@ class PlanInfo(ctypes.Structure):
         d = {name: getattr(self, name) for name, _ in self._fields_}
         d["algo"] = ALGO_NAMES.get(d["algo"], d["algo"])
         return d
+
+
+class LinearPlan(ctypes.Structure):
+    """cbs_linear_plan."""
+    _fields_ = [(name, ctypes.c_int) for name in ("kernel", "turned", "tile_rows", "tile_channels", "align", "k_steps",
+                                                  "tiles", "workers")]
+
+    def as_dict(self) -> dict:
+        return {**{name: getattr(self, name) for name, _ in self._fields_}, "kernel": LINEAR_KERNELS[self.kernel]}
 
 
 class FoldLayer(ctypes.Structure):
@@ -107,6 +117,7 @@ _declare("conv_bn_silu_quantize_rows", [_p, _ll, _p, _ll, _p, _ll, _i, _i, _p])
 _declare("conv_bn_silu_layer_norm_quantize", [_p, _ll, _p, _p, _f, _p, _ll, _p, _ll, _i, _i, _p])
 _declare("conv_bn_silu_linear_int8", [_p, _ll, _p, _ll, _p, _p, _p, _p, _ll, _p, _ll, _ll, _i, _i, _i, _i, _p, _ll, _p])
 _declare("conv_bn_silu_linear_int8_workspace", [_ll, _i, _i], _ll)
+_linear_int8_plan = _declare("conv_bn_silu_linear_int8_plan", [_ll, _i, _i, _i, _i, ctypes.POINTER(LinearPlan)])
 _check = _declare("conv_bn_silu_check", [_p])
 _status_string = _declare("conv_bn_silu_status_string", [_i], ctypes.c_char_p)
 _last_cuda_error = _declare("conv_bn_silu_last_cuda_error", [])
@@ -550,6 +561,14 @@ def linear_int8(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale
     if type(out) is int:
         _raise_if(out, "conv_bn_silu_linear_int8")
     return out
+
+
+def linear_int8_plan(m: int, n: int, k: int, align: int = 16, sm_count: int = 152) -> dict:
+    """conv_bn_silu_linear_int8_plan: which kernel linear_int8 runs for m rows, n channels and K = k, and its tiles; align
+    is the largest of 16, 4 and 1 that the addresses and row distances of a and w are multiples of.  Host only."""
+    info = LinearPlan()
+    _raise_if(_linear_int8_plan(m, n, k, align, sm_count, ctypes.byref(info)), "conv_bn_silu_linear_int8_plan")
+    return info.as_dict()
 
 
 def forward_ptr(x_ptr: int, w_ptr: int, scale_ptr: int, bias_ptr: int, y_ptr: int,

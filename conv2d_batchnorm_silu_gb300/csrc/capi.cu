@@ -667,6 +667,15 @@ long long conv_bn_silu_linear_int8_workspace(long long m, int n, int k)
     return cbs::linear_workspace_bytes(m, n, k, sms);
 }
 
+int conv_bn_silu_linear_int8_plan(long long m, int n, int k, int align, int sm_count, cbs_linear_plan *plan)
+{
+    if (!plan || sm_count < 1 || !linear_sizes_ok(m, n, k) || (align != 16 && align != 4 && align != 1))
+        return CBS_ERR_INVALID_ARG;
+    const cbs::LinearPlan p = cbs::linear_plan(m, n, k, align, sm_count);
+    *plan = cbs_linear_plan{p.kernel, p.turned, p.tile_rows, p.tile_channels, p.align, p.k_steps, p.tiles, p.workers};
+    return CBS_OK;
+}
+
 int conv_bn_silu_linear_int8(const void *a, long long a_stride, const void *w, long long w_stride,
                              const float *a_scale, const float *w_scale, const float *bias, const void *residual,
                              long long residual_stride, void *y, long long y_stride, long long m, int n, int k,

@@ -130,15 +130,20 @@ __global__ void __launch_bounds__(32 * kFewWarps, ALIGNED && ROWS <= 2 ? 4 : (RO
     }
 }
 
-template <typename T, bool ALIGNED>
-cudaError_t linear_few_launch(const LinearArgs &a, int sm_count, cudaStream_t stream)
+// K is split among the warps of a block while each has two passes (1 KB) of it: many short blocks
+// fill the SMs evenly.
+int few_split_log2(int k)
 {
-    // K is split among the warps of a block while each has two passes (1 KB) of it: many short blocks
-    // fill the SMs evenly.
-    (void)sm_count;
     int split_log2 = 0;
-    while (split_log2 < 3 && a.k >= 2048 << split_log2) ++split_log2;
-    const int per_block = kFewChannels * (kFewWarps >> split_log2);
+    while (split_log2 < 3 && k >= 2048 << split_log2) ++split_log2;
+    return split_log2;
+}
+int few_per_block(int split_log2) { return kFewChannels * (kFewWarps >> split_log2); }  // of a block
+
+template <typename T, bool ALIGNED>
+cudaError_t linear_few_launch(const LinearArgs &a, cudaStream_t stream)
+{
+    const int split_log2 = few_split_log2(a.k), per_block = few_per_block(split_log2);
     const dim3 grid((unsigned)((a.e.n + per_block - 1) / per_block)), block(32 * kFewWarps);
     if (a.e.m == 1) return launch_overlapped(linear_few_kernel<T, 1, ALIGNED>, grid, block, 0, stream, 1, a, split_log2);
     if (a.e.m == 2) return launch_overlapped(linear_few_kernel<T, 2, ALIGNED>, grid, block, 0, stream, 1, a, split_log2);
@@ -147,13 +152,13 @@ cudaError_t linear_few_launch(const LinearArgs &a, int sm_count, cudaStream_t st
 }
 
 template <typename T>
-cudaError_t linear_few_launch_t(const LinearArgs &a, int sm_count, cudaStream_t stream)
+cudaError_t linear_few_launch_t(const LinearArgs &a, cudaStream_t stream)
 {
     auto rows16 = [](const int8_t *p, long long stride) {
         return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 16 == 0;
     };
-    return a.k % 16 == 0 && rows16(a.a, a.a_stride) && rows16(a.w, a.w_stride) ? linear_few_launch<T, true>(a, sm_count, stream)
-                                                              : linear_few_launch<T, false>(a, sm_count, stream);
+    return a.k % 16 == 0 && rows16(a.a, a.a_stride) && rows16(a.w, a.w_stride) ? linear_few_launch<T, true>(a, stream)
+                                                                                  : linear_few_launch<T, false>(a, stream);
 }
 
 }  // namespace
@@ -207,6 +212,30 @@ long long linear_workspace_bytes(long long m, int n, int k, int sm_count)
     return most;
 }
 
+LinearPlan linear_plan(long long m, int n, int k, int align, int sm_count)
+{
+    LinearPlan plan{};
+    if (m == 0 || n == 0) return plan;
+    plan.align = align == 16 ? 16 : 1;  // what the kernels but the streamed ones tell apart
+    while (align > 1 && k % align != 0) align = align == 16 ? 4 : 1;
+    if (m <= kFewRows) {
+        plan.align = align == 16 ? 16 : 1;
+        plan.kernel = CBS_LINEAR_FEW;
+        plan.tile_rows = m <= 2 ? (int)m : (m <= 4 ? 4 : kFewRows);
+        plan.tile_channels = few_per_block(few_split_log2(k));
+        plan.k_steps = (k + (512 << few_split_log2(k)) - 1) / (512 << few_split_log2(k));
+        plan.tiles = plan.workers = (n + plan.tile_channels - 1) / plan.tile_channels;
+        return plan;
+    }
+    switch (best_path(m, n, k, sm_count, k > 0 ? align : 0)) {
+    case kTile: linear_tile_plan(m, n, k, &plan); break;
+    case kStreamed: tc_stream_plan(m, n, k, align, false, sm_count, &plan); break;
+    case kTurned: tc_stream_plan(n, (int)m, k, align, true, sm_count, &plan); break;
+    default: tc_linear_plan(m, n, k, sm_count, &plan);
+    }
+    return plan;
+}
+
 // Whether a kernel that may record an error was launched, or captured, since the library was loaded.
 static std::atomic<bool> g_recorders_launched{false};
 
@@ -230,9 +259,9 @@ cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t str
     a.w_stride = p.w.stride;
     a.k = p.k;
     switch (p.out_dtype) {
-    case kF32: return linear_few_launch_t<float>(a, sm_count, stream);
-    case kBf16: return linear_few_launch_t<__nv_bfloat16>(a, sm_count, stream);
-    default: return linear_few_launch_t<__half>(a, sm_count, stream);
+    case kF32: return linear_few_launch_t<float>(a, stream);
+    case kBf16: return linear_few_launch_t<__nv_bfloat16>(a, stream);
+    default: return linear_few_launch_t<__half>(a, stream);
     }
 }
 

@@ -116,6 +116,15 @@ float linear_tile_time(long long m, int n, int k, int sm_count)
     return 3.0f + (step > all ? step : all) + 0.9f * blocks / (float)sm_count;
 }
 
+void linear_tile_plan(long long m, int n, int k, LinearPlan *plan)
+{
+    plan->kernel = CBS_LINEAR_TILE;
+    plan->tile_rows = kRows;
+    plan->tile_channels = kChannels;
+    plan->k_steps = (k + kStep - 1) / kStep;
+    plan->tiles = plan->workers = (int)((m + kRows - 1) / kRows * ((n + kChannels - 1) / kChannels));
+}
+
 bool linear_tile_supported(long long m, int n) { return (m + kRows - 1) / kRows <= 65535 && n > 0; }
 
 template <bool ALIGNED>

@@ -494,6 +494,17 @@ float tc_linear_time(long long m, int n, int k, int sm_count)
     return 2.5f + 3.0f * (float)(m + n) * (float)kp / 5.0e6f + tile_time(kTiles[best_tile(m, n, kp, sm_count)], m, n, kp, sm_count);
 }
 
+void tc_linear_plan(long long m, int n, int k, int sm_count, LinearPlan *plan)
+{
+    const TileCost &c = kTiles[best_tile(m, n, padded_k(k), sm_count)];
+    plan->kernel = CBS_LINEAR_GEMM;
+    plan->tile_rows = c.rows;
+    plan->tile_channels = c.channels;
+    plan->k_steps = padded_k(k) / kBlockK;
+    plan->tiles = (int)(((m + c.rows - 1) / c.rows) * ((n + c.channels - 1) / c.channels));
+    plan->workers = plan->tiles < sm_count / c.ctas ? plan->tiles : sm_count / c.ctas;
+}
+
 long long tc_linear_workspace_bytes(long long m, int n, int k)
 {
     const long long kp = padded_k(k);

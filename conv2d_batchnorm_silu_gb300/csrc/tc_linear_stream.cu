@@ -93,7 +93,7 @@ __device__ __forceinline__ void load_if(uint4 &v, const int8_t *p, bool yes)
 }
 // 16 bytes of a row, of which the row has `left`: in one load, in four words, or in the five words that hold them
 // where rows start anywhere, which are put in place when they are used.  Of weights what is past the row may be
-// anything; of rows it has to be zeros, and is but for the bytes of a last word (get_row).
+// anything; of rows it has to be zeros, and is but for the bytes of a last word, which are masked when it is used.
 template <int ALIGN>
 struct Held {
     uint4 v;
@@ -780,10 +780,13 @@ cudaError_t ring_launch(const StreamArgs &a, cudaStream_t stream)
                                                 (size_t)C::SMEM, stream, 1, tw, tr, a);
 }
 
+// Where linear_ring_kernel is the one that runs, but for rows without a tensor map.
+constexpr bool ring_runs(int nt, int align) { return align == 16 && nt <= 128; }
+
 template <int NT, int ALIGN>
 cudaError_t sums_launch(const StreamArgs &a, cudaStream_t stream)
 {
-    if constexpr (ALIGN == 16 && NT <= 128) {
+    if constexpr (ring_runs(NT, ALIGN)) {
         // Rows that overlap (as where all are the same) or lie 2^40 bytes apart have no tensor map.
         auto mapped = [&](long long stride) { return stride >= a.k && stride < 1LL << 40; };
         return mapped(a.a_stride) && mapped(a.w_stride) ? ring_launch<NT>(a, stream) : sums_launch<NT, 4>(a, stream);
@@ -851,6 +854,19 @@ long long tc_stream_workspace_bytes(long long rows, int channels, int k, int sm_
 {
     const StreamPlan p = plan_of(rows, channels, k, sm_count);
     return ((long long)p.workers + p.tiles) * p.nt * kChannels * 4;
+}
+
+void tc_stream_plan(long long rows, int channels, int k, int align, bool turned, int sm_count, LinearPlan *plan)
+{
+    const StreamPlan p = plan_of(rows, channels, k, sm_count);
+    plan->kernel = ring_runs(p.nt, align) ? CBS_LINEAR_RING : CBS_LINEAR_STREAM;
+    plan->turned = turned;
+    plan->tile_rows = turned ? kChannels : p.nt;
+    plan->tile_channels = turned ? p.nt : kChannels;
+    plan->align = align;
+    plan->k_steps = p.k_steps;
+    plan->tiles = p.tiles;
+    plan->workers = p.workers;
 }
 
 cudaError_t tc_stream_launch(const LinearProblem &p, bool turned, int sm_count, cudaStream_t stream)

@@ -21,7 +21,7 @@ struct Rows {
 
 struct NormProblem {
     Rows x;              // input, `dtype`
-    Rows y;              // normalised output, `dtype` (q_out.data == nullptr)
+    Rows y;              // normalised output, `dtype` (q.data == nullptr)
     Rows q;              // int8 output instead of y, with row_scale
     float *row_scale;    // [rows], with q only
     float *stats;        // nullable [2][rows]: mean, then 1/sqrt(var + eps)
@@ -96,6 +96,16 @@ cudaError_t norm_launch(const NormProblem &p, int sm_count, cudaStream_t stream)
 int norm_grad_partial_rows(long long rows, int c, int sm_count);
 cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_t stream);
 
+// What linear_launch runs (the fields of cbs_linear_plan but for the workspace).
+struct LinearPlan {
+    int kernel;  // cbs_linear_kernel
+    int turned;
+    int tile_rows, tile_channels;
+    int align;
+    int k_steps, tiles, workers;
+};
+LinearPlan linear_plan(long long m, int n, int k, int align, int sm_count);
+
 // Bytes linear_launch may need for these sizes, whatever the pointers and strides.
 long long linear_workspace_bytes(long long m, int n, int k, int sm_count);
 cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
@@ -103,6 +113,7 @@ cudaError_t linear_launch(const LinearProblem &p, int sm_count, cudaStream_t str
 // The linear layer on the tensor cores (tc_linear.cu); k == 0 counts as a step of zeros.
 long long tc_linear_workspace_bytes(long long m, int n, int k);
 float tc_linear_time(long long m, int n, int k, int sm_count);  // modelled, us
+void tc_linear_plan(long long m, int n, int k, int sm_count, LinearPlan *plan);
 cudaError_t tc_linear_launch(const LinearProblem &p, int sm_count, cudaStream_t stream);
 cudaError_t tc_linear_read_and_clear_error(cudaStream_t stream, unsigned int *out);
 
@@ -116,12 +127,14 @@ cudaError_t encode_bytes_map(const void *base, long long rows, int k, long long 
 int tc_stream_align(const LinearProblem &p);  // 16, 4 or 1: all rows start at multiples of it, and k is one; 0: k is 0
 long long tc_stream_workspace_bytes(long long rows, int channels, int k, int sm_count);
 float tc_stream_time(long long rows, int channels, int k, int align, bool turned, int sm_count);  // modelled, us
+void tc_stream_plan(long long rows, int channels, int k, int align, bool turned, int sm_count, LinearPlan *plan);
 cudaError_t tc_stream_launch(const LinearProblem &p, bool turned, int sm_count, cudaStream_t stream);
 cudaError_t tc_stream_read_and_clear_error(cudaStream_t stream, unsigned int *out);
 
 // The linear layer in one launch, for small products (linear_tile.cu).
 float linear_tile_time(long long m, int n, int k, int sm_count);  // modelled, us
 bool linear_tile_supported(long long m, int n);
+void linear_tile_plan(long long m, int n, int k, LinearPlan *plan);
 cudaError_t linear_tile_launch(const LinearProblem &p, cudaStream_t stream);
 
 // What any of the linear layer's kernels recorded.

@@ -440,6 +440,32 @@ int conv_bn_silu_linear_int8(const void *a, long long a_stride, const void *w, l
  * the pointers and row distances; -1 for sizes out of range or when no device answers. */
 long long conv_bn_silu_linear_int8_workspace(long long m, int n, int k);
 
+/* The kernels of conv_bn_silu_linear_int8. */
+typedef enum cbs_linear_kernel {
+    CBS_LINEAR_FEW = 0,    /* few rows: the weights streamed once past integer dot products */
+    CBS_LINEAR_TILE = 1,   /* small products: one launch on the integer matrix instruction */
+    CBS_LINEAR_RING = 2,   /* one operand streamed through TMA and widened into tensor memory */
+    CBS_LINEAR_STREAM = 3, /* one operand streamed through registers and widened into shared memory */
+    CBS_LINEAR_GEMM = 4    /* both operands widened first, then a tensor-core product */
+} cbs_linear_kernel;
+
+/* What conv_bn_silu_linear_int8 launches for these sizes. */
+typedef struct cbs_linear_plan {
+    int kernel;         /* cbs_linear_kernel */
+    int turned;         /* RING and STREAM: 1 when a is the streamed operand in place of w */
+    int tile_rows;      /* of an output tile */
+    int tile_channels;
+    int align;          /* bytes that the kernel takes rows of a and w to start at multiples of: 16, 4 or 1 */
+    int k_steps;        /* steps of K in a tile */
+    int tiles;
+    int workers;        /* CTAs, or CTA pairs, that share the tiles */
+} cbs_linear_plan;
+
+/* Fills `plan` for m, n and k as in conv_bn_silu_linear_int8 and the device's SM count; align is the largest of
+ * 16, 4 and 1 that the addresses and row distances of a and w are multiples of.  For rows at least k apart (RING has
+ * no form for rows that overlap, which run as STREAM); all zeros where m or n is 0.  Host only, touches no GPU. */
+int conv_bn_silu_linear_int8_plan(long long m, int n, int k, int align, int sm_count, cbs_linear_plan *plan);
+
 /* Synchronises `stream`, then reads and clears the library's device error word.
  * Returns CBS_ERR_TIMEOUT if any kernel since the last check gave up on a
  * pipeline wait, CBS_ERR_CUDA if the synchronisation failed, else CBS_OK. */
