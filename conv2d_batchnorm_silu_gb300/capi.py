@@ -472,7 +472,8 @@ def silu_apply(t2: torch.Tensor, y: torch.Tensor | None = None, stream=None) -> 
 # ---------------------------------------------------------------- token-wise operators
 # Activations are tensors [..., c] whose last dimension is dense and whose leading dimensions
 # are rows at one distance (a contiguous tensor, or a column slice of a matrix); parameters,
-# statistics and scales are dense float32.  Arguments are checked, and outputs and workspaces
+# statistics and scales are dense float32.  No call records a gradient for PyTorch's autograd:
+# layer_norm_backward is called by the program.  Arguments are checked, and outputs and workspaces
 # made, in the compiled module _token_ops (csrc/binding.cpp), which returns a status that is
 # not CBS_OK as an int.
 _token_ops = None
@@ -498,7 +499,8 @@ def layer_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.T
     """conv_bn_silu_layer_norm: y = (x - mean) * rstd * gamma + beta over the last dimension.
 
     x: float32, bf16 or f16 [..., c]; gamma, beta: fp32 [c] or None; y like x.  With return_stats
-    also the fp32 statistics [2, rows] (mean, then 1/sqrt(var + eps)) for layer_norm_backward.
+    also the fp32 statistics [2, rows] (mean, then 1/sqrt(var + eps)) for layer_norm_backward; autograd
+    does not see the call.
     """
     ops = _token_ops or _load_token_ops()
     out = ops.layer_norm(x, gamma, beta, eps, return_stats, y,
@@ -548,6 +550,7 @@ def linear_int8(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale
 
     a: int8 [..., k]; w: int8 [n, k]; a_scale: fp32, one for each row of a; w_scale, bias: fp32 [n];
     residual and y: out_dtype [..., n] (residual may be y).  activation: "silu", "identity" or "relu".
+    linear_int8_plan says which kernel runs.
     """
     act = ACTIVATIONS.get(activation)
     if act is None:

@@ -613,7 +613,7 @@ long long conv_bn_silu_layer_norm_backward_workspace(long long rows, int c)
     if (!norm_sizes_ok(rows, c, CBS_DTYPE_F32)) return -1;
     int sms = 0;
     if (sm_count_current_device(&sms) != CBS_OK) return -1;
-    return 8LL * c * cbs::norm_grad_partial_rows(rows, c, sms);
+    return 8LL * c * cbs::norm_grad_partial_rows(rows, sms);
 }
 
 int conv_bn_silu_layer_norm_backward(const void *dy, long long dy_stride, const void *x, long long x_stride,
@@ -642,7 +642,7 @@ int conv_bn_silu_layer_norm_backward(const void *dy, long long dy_stride, const 
     st = sm_count_current_device(&sms);
     if (st != CBS_OK) return st;
     cbs::NormGradProblem p{};
-    p.partial_rows = cbs::norm_grad_partial_rows(rows, c, sms);
+    p.partial_rows = cbs::norm_grad_partial_rows(rows, sms);
     if (workspace_bytes < 8LL * c * p.partial_rows) return CBS_ERR_INVALID_ARG;
     p.dy = cbs::Rows{const_cast<void *>(dy), dy_stride};
     p.x = cbs::Rows{const_cast<void *>(x), x_stride};

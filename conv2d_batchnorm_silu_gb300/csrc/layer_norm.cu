@@ -93,7 +93,7 @@ struct NormArgs {
 
 // One row per block at a time, read once for each sum it needs: any width, alignment and stride.  What the
 // kernels below do not hold comes here: rows of more than 16384 elements (f32 8192), and many rows of 8193 to 9500
-// off 16-byte boundaries.  Bound by its element-wise loads: bf16, 14592x9001 209 us (2.5 TB/s).
+// off 16-byte boundaries.  Bound by its element-wise loads: bf16, 14592x9001 214 us (2.5 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(kWideThreads) norm_wide_kernel(const NormArgs a)
 {
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(32 * kJoinRuns) norm_grad_join_kernel(const Gr
 // A row stays in the registers of TPR threads from its one load to its one store; sums go through warp
 // shuffles and, above a warp, shared memory.  A thread holds NI runs of V elements, run i at column
 // (i * TPR + lane) * V.  W is the bytes of a run: 16 where every pointer, row distance and the width allow
-// it, else 4 (a pair of 16-bit elements, or one fp32), which any element alignment allows: a pair that
-// lies across two aligned words is put together from both.
+// it; else 4 for f32, one element, and 2 for the 16-bit types, one element of a row that its threads copied
+// together (fetch_row).
 __device__ __forceinline__ float2 unpack(uint32_t w, __nv_bfloat16)
 {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
@@ -442,7 +442,7 @@ struct Width {
 // its own part of the coming rows to shared memory with cp.async (no barrier: nobody else
 // reads it), so that memory stays busy while a row is summed.  Short rows share a warp.
 // Bound by memory: bf16, 16384x4096 45 us and 14592x8192 72 us (5.9 and 6.6 TB/s of 6.8 for a copy).  With
-// quantisation by its instructions: 14592x4096 39 us, x8192 81 (4.6 and 4.4 TB/s).
+// quantisation 14592x4096 39 us, x8192 81 (4.6 and 4.4 TB/s), with neither memory nor any pipe full.
 constexpr int norm_stages(int w) { return w == 2 ? 4 : 3; }
 // Threads of a block: one row, or as many as 128 threads hold while a row stays within a warp.
 constexpr int norm_block(int tpr) { return tpr <= 32 ? 128 : tpr; }
@@ -955,9 +955,8 @@ cudaError_t norm_launch(const NormProblem &p, int sm_count, cudaStream_t stream)
     }
 }
 
-int norm_grad_partial_rows(long long rows, int c, int sm_count)
+int norm_grad_partial_rows(long long rows, int sm_count)
 {
-    (void)c;
     const long long most = 2LL * sm_count;  // norm_grad_stream_kernel's blocks at most
     return (int)(rows < most ? rows : most);
 }

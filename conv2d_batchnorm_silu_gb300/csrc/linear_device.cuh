@@ -116,7 +116,7 @@ __device__ __forceinline__ uint4 within(uint4 v, int k0, int k)
 }
 
 // Four int8 of a word -> two words of f16 pairs, bytes 0 and 2, then 1 and 3 (an order of K that both
-// operands share).  Biased to 0..255, a byte below 0x64 is the f16 1024 + byte, and subtracting 1152
+// operands share).  The well-known conversion through a biased mantissa.  Biased to 0..255, a byte below 0x64 is the f16 1024 + byte, and subtracting 1152
 // leaves the value; the masking, the bias and the 0x64 are one three-input operation.
 __device__ __forceinline__ uint2 widen4(uint32_t w)
 {

@@ -34,8 +34,8 @@ struct LinearArgs {
 // into 32-bit integers with __dp4a.  A warp (or, where there are few channels, two to eight warps that
 // split K) takes kFewChannels channels; a lane holds 16 bytes of each of their weights and goes through
 // the rows of a with them, so a's bytes, which stay in L1, are read once for all the channels.  8192x8192
-// weights, kernel alone: one row 12.3 us (5.5 TB/s of 6.8 for a copy; the start and the end of 2048 blocks are the
-// rest), two 13.0, four 16.8, eight 21.1, where the products' rate counts (51 of 150 TOP/s, a's bytes from L1).
+// weights, kernel alone: one row 12.1 us (5.5 TB/s of 6.8 for a copy; the start and the end of 2048 blocks are the
+// rest), two 12.6, four 16.0, eight 20.1, where the products' rate counts (53 of 150 TOP/s, a's bytes from L1).
 constexpr int kFewChannels = 4;
 constexpr int kFewWarps = 8;
 
@@ -171,8 +171,8 @@ constexpr int kFewRows = 8;
 enum Path { kTile, kStreamed, kTurned, kWidened };
 
 // Measured, us, tile / streamed / widened before: 24x614x243 5.2 / - / 6.0 (8.6 with the host's part), 64x1024x1024
-// 11.2 / 5.9 / 8.9, 64 rows of 8192x8192 - / 23 / 74, 512 rows - / 81 / 87, 1024 rows - / 152 / 121.  Streamed with
-// the sides changed / widened before: 25984x40x4800 41 / 132, 11609x128x4512 27 / 58, 100000x16x256 16 / 28,
+// 11.2 / 5.3 / 8.9, 64 rows of 8192x8192 - / 21 / 74, 512 rows - / 81 / 87, 1024 rows - / 152 / 123.  Streamed with
+// the sides changed / widened before: 25984x40x4800 37 / 132, 11609x128x4512 24 / 58, 100000x16x256 15 / 28,
 // 25600x256x1024 39 / 31, 16384x512x512 36 / 17.
 // A call takes the longer of its kernels and what its launches cost the host.
 Path best_path(long long m, int n, int k, int sm_count, int align)

@@ -7,8 +7,8 @@
 // stride and alignment of the inputs reaches the second kernel as aligned tiles), and a
 // persistent GEMM multiplies them with the scales, bias, activation and residual in its epilogue.
 //
-// Measured, both kernels: 8192x16384x4096 620 us (1,770 TOP/s; the tensor cores' rate, and 58 us of widening),
-// 4096x4096x4096 95 us, 25600x1024x256 24 us, where the epilogue sets the pace (a 256 x 256
+// Measured, both kernels: 8192x16384x4096 623 us (1,760 TOP/s; the tensor cores' rate, and 58 us of widening),
+// 4096x4096x4096 96 us, 25600x1024x256 24 us, where the epilogue sets the pace (a 256 x 256
 // tile's takes 3,600 of 5,000 clocks, its MMAs 2,048).
 #include <cuda.h>
 #include <cudaTypedefs.h>

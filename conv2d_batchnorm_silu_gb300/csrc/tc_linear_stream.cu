@@ -5,7 +5,7 @@
 // Sixteen warps hold the int8 of the coming steps in registers (kAhead steps of 128 K elements, 48 KB of
 // weights per SM in flight, whole 128-byte lines of each row), widen a step of weights and rows at a time into
 // swizzled f16 tiles, and hand them to the issuing warp.  Rows that start at multiples of 4 bytes only are loaded
-// in words, and rows that start anywhere in one word more (64x8192x8192 22 us, x8196 26, x8193 43; widened before
+// in words, and rows that start anywhere in one word more (64x8192x8192 21 us, x8196 26, x8193 43; widened before
 // the product 75).  Every CTA takes an equal run of the (channel tile, row tile, K step) sequence, so that all SMs
 // read the same share of the weights, and leaves its tiles as fp32 partial sums in the workspace, which a second
 // kernel adds in K order and finishes.
@@ -412,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
 // flight), two groups of eight warps widen the weights of alternate steps from there into tensor memory, where the
 // tensor core finds its first operand (lane = channel), and four more widen the rows into shared memory.
 //
-// 8192x8192 weights: 32 rows 20.0 us (21.1 in linear_stream_kernel), 64 rows 21.8 (23.2), 128 rows 27.6 (30.2);
-// 64x512x512 5.9 (7.4); turned 25984x40x4800 37 (41).  A step takes 1,000 clocks with 32 rows, hot in L2 or not: what
+// 8192x8192 weights: 32 rows 19.4 us (21.1 in linear_stream_kernel), 64 rows 21.3 (23.2), 128 rows 27.3 (30.2);
+// turned 25984x40x4800 37 (41).  A step takes 1,000 clocks with 32 rows, hot in L2 or not: what
 // 152 SMs draw from L2, weights at 4.8 TB/s and rows beside them; the first step comes 5,000 clocks after the start.
 // Tried and slower: prefetching each row's next 1 KB into L2 (32 us), loads in bursts of three steps (23.0).
 template <int NT>

@@ -93,7 +93,7 @@ cudaError_t read_and_clear_word(const Symbol &word, cudaStream_t stream, unsigne
 }
 
 cudaError_t norm_launch(const NormProblem &p, int sm_count, cudaStream_t stream);
-int norm_grad_partial_rows(long long rows, int c, int sm_count);
+int norm_grad_partial_rows(long long rows, int sm_count);  // of partial sums, each [2][c]
 cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_t stream);
 
 // What linear_launch runs (the fields of cbs_linear_plan but for the workspace).

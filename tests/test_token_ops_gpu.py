@@ -460,6 +460,8 @@ def test_linear_repeats_to_the_bit(capi, m, n, k):
 
 
 # Few channels for many rows: the rows are widened on their way.
+# (Of these, 6000x300x8192 is modelled faster with both widened before, and runs so; tests/linear_cases.py has sizes
+# whose kernel is asserted.)
 TURNED = [(700, 40, 4096), (1500, 9, 4096), (5000, 33, 1040), (9000, 100, 2048), (9000, 200, 4096), (6000, 300, 8192)]
 
 
@@ -494,6 +496,7 @@ def test_linear_of_rows_at_words(capi, m, n, k, pad, out):
 
 
 # Rows that start anywhere, at sizes for which they are widened on their way.
+# (Of these, 6000x250x4101 runs with both widened before, and 64x1000x129 in the one-launch tile kernel.)
 @pytest.mark.parametrize("out", list(TYPES))
 @pytest.mark.parametrize("m,n,k,pad", [(13, 4000, 6005, 0), (20, 300, 4097, 0), (40, 712, 2050, 0), (100, 712, 2051, 0),
                                        (300, 300, 4095, 0), (200, 1000, 2048, 7), (1024, 38, 4967, 0), (3823, 21, 2853, 0),
