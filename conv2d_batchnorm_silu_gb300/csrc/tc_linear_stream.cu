@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_stream_kernel(const Stream
 // flight), two groups of eight warps widen the weights of alternate steps from there into tensor memory, where the
 // tensor core finds its first operand (lane = channel), and four more widen the rows into shared memory.
 //
-// 8192x8192 weights: 32 rows 19.4 us (21.1 in linear_stream_kernel), 64 rows 21.3 (23.2), 128 rows 27.3 (30.2);
+// 8192x8192 weights: 32 rows 19.7 us (21.1 in linear_stream_kernel), 64 rows 21.5 (23.2), 128 rows 27.1 (30.2);
 // turned 25984x40x4800 37 (41).  A step takes 1,000 clocks with 32 rows, hot in L2 or not: what
 // 152 SMs draw from L2, weights at 4.8 TB/s and rows beside them; the first step comes 5,000 clocks after the start.
 // Tried and slower: prefetching each row's next 1 KB into L2 (32 us), loads in bursts of three steps (23.0).
