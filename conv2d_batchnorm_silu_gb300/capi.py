@@ -66,6 +66,18 @@ class LinearPlan(ctypes.Structure):
         return {**{name: getattr(self, name) for name, _ in self._fields_}, "kernel": LINEAR_KERNELS[self.kernel]}
 
 
+class AdamWTensor(ctypes.Structure):
+    """cbs_adamw_tensor."""
+    _fields_ = [("param", _p), ("grad", _p), ("exp_avg", _p), ("exp_avg_sq", _p), ("exp_avg_scale", _p),
+                ("exp_avg_sq_scale", _p), ("n", ctypes.c_longlong), ("param_dtype", _i), ("grad_dtype", _i)]
+
+
+class AdamWOptions(ctypes.Structure):
+    """cbs_adamw_options."""
+    _fields_ = [(name, ctypes.c_double) for name in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + [
+        ("step", ctypes.c_longlong), ("lr_device", _p), ("grad_scale_device", _p), ("step_device", _p), ("state_bits", _i)]
+
+
 class FoldLayer(ctypes.Structure):
     """cbs_fold_layer: one layer of conv_bn_silu_fold_batch."""
     _fields_ = [("gamma", _p), ("beta", _p), ("mean", _p), ("var", _p), ("eps", _f), ("c_out", _i),
@@ -115,6 +127,12 @@ _declare("conv_bn_silu_layer_norm_backward", [_p, _ll, _p, _ll, _p, _p, _p, _ll,
 _declare("conv_bn_silu_layer_norm_backward_workspace", [_ll, _i], _ll)
 _declare("conv_bn_silu_quantize_rows", [_p, _ll, _p, _ll, _p, _ll, _i, _i, _p])
 _declare("conv_bn_silu_layer_norm_quantize", [_p, _ll, _p, _p, _f, _p, _ll, _p, _ll, _i, _i, _p])
+_declare("conv_bn_silu_rms_norm", [_p, _ll, _p, _ll, _p, _f, _p, _ll, _p, _ll, _p, _ll, _i, _i, _p])
+_declare("conv_bn_silu_rms_norm_quantize", [_p, _ll, _p, _ll, _p, _f, _p, _ll, _p, _ll, _p, _ll, _p, _p, _ll, _i, _i, _p])
+_declare("conv_bn_silu_rms_norm_backward",
+         [_p, _ll, _p, _ll, _p, _p, _p, _ll, _p, _ll, _p, _ll, _i, _i, _p, _ll, _p])
+_declare("conv_bn_silu_rms_norm_backward_workspace", [_ll, _i], _ll)
+_declare("conv_bn_silu_adamw_step", [ctypes.POINTER(AdamWTensor), _i, ctypes.POINTER(AdamWOptions), _p])
 _declare("conv_bn_silu_linear_int8", [_p, _ll, _p, _ll, _p, _p, _p, _p, _ll, _p, _ll, _ll, _i, _i, _i, _i, _p, _ll, _p])
 _declare("conv_bn_silu_linear_int8_workspace", [_ll, _i, _i], _ll)
 _linear_int8_plan = _declare("conv_bn_silu_linear_int8_plan", [_ll, _i, _i, _i, _i, ctypes.POINTER(LinearPlan)])
@@ -540,6 +558,92 @@ def layer_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, beta
     if type(out) is int:
         _raise_if(out, "conv_bn_silu_layer_norm_quantize")
     return out
+
+
+def rms_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, eps: float = 1e-6,
+             residual: torch.Tensor | None = None, return_rstd: bool = False, y: torch.Tensor | None = None,
+             total: torch.Tensor | None = None, stream=None):
+    """conv_bn_silu_rms_norm: y = total * rstd * gamma over the last dimension, total = x + residual rounded to x's type
+    (x without a residual).
+
+    x, residual, y, total: float32, bf16 or f16 [..., c] (total may be residual itself); gamma: fp32 [c] or None.
+    Returns y; (y, total) with a residual; with return_rstd also the fp32 1/sqrt(mean square + eps) of each row, last,
+    for rms_norm_backward.  Autograd does not see the call.
+    """
+    ops = _token_ops or _load_token_ops()
+    out = ops.rms_norm(x, gamma, eps, residual, False, False, return_rstd, y, None, total,
+                       None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_rms_norm")
+    return out
+
+
+def rms_norm_quantize(x: torch.Tensor, gamma: torch.Tensor | None = None, eps: float = 1e-6,
+                      residual: torch.Tensor | None = None, return_y: bool = False, return_rstd: bool = False,
+                      q: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                      total: torch.Tensor | None = None, stream=None):
+    """conv_bn_silu_rms_norm_quantize: rms_norm, its rows quantised in the same pass.
+
+    Returns (q, scale) as quantize_rows gives them, then total with a residual, then y with return_y (or where y is
+    given): the rows in x's type too, for adapters beside linear_int8; then rstd with return_rstd.
+    """
+    ops = _token_ops or _load_token_ops()
+    out = ops.rms_norm(x, gamma, eps, residual, True, return_y, return_rstd, y, q, total,
+                       None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_rms_norm_quantize")
+    return out
+
+
+def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None, rstd: torch.Tensor,
+                      residual: torch.Tensor | None = None, dx: torch.Tensor | None = None,
+                      stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """conv_bn_silu_rms_norm_backward: (dx, dgamma) from dy, what the forward call normalised (its total, where it had
+    a residual), gamma (None: ones) and the rstd it returned.
+
+    residual: the gradient that arrives at the total past the norm, added to dx (it may be dx itself).  dx, like x, is
+    the gradient of the forward call's x and of its residual; dgamma is fp32 [c].
+    """
+    ops = _token_ops or _load_token_ops()
+    out = ops.rms_norm_backward(dy, x, gamma, rstd, residual, dx, None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_rms_norm_backward")
+    return out
+
+
+def adamw_state(params, bits: int = 32) -> dict:
+    """The moments of adamw_step before its first step, as its keyword arguments: exp_avg and exp_avg_sq, a tensor for
+    each parameter, fp32, or, with bits=8, float8_e4m3fn and a fp32 scale for each 256 elements of them in
+    exp_avg_scale and exp_avg_sq_scale (exp_avg_sq then holds the square root)."""
+    if bits not in (8, 32):
+        raise ValueError("bits must be 8 or 32")
+    kind = torch.float32 if bits == 32 else torch.float8_e4m3fn
+
+    def zeros():
+        return [torch.zeros(p.shape, dtype=torch.float32 if bits == 32 else torch.uint8, device=p.device).view(kind)
+                for p in params]
+
+    def scales():
+        return [torch.zeros((p.numel() + 255) // 256, dtype=torch.float32, device=p.device) for p in params]
+
+    state = {"exp_avg": zeros(), "exp_avg_sq": zeros()}
+    return state if bits == 32 else {**state, "exp_avg_scale": scales(), "exp_avg_sq_scale": scales()}
+
+
+def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, betas: tuple[float, float] = (0.9, 0.999),
+               eps: float = 1e-8, weight_decay: float = 0.01, grad_scale=1.0, exp_avg_scale=None, exp_avg_sq_scale=None,
+               stream=None) -> None:
+    """conv_bn_silu_adamw_step: one AdamW step of every parameter, in place, with the moments that adamw_state made.
+
+    params, grads: lists of dense float32, bf16 or f16 tensors of the same sizes; no parameter twice.  step counts from
+    1.  step, lr and grad_scale (which every gradient is multiplied with) may be CUDA tensors of one element (int64,
+    float32, float32): they are read when the step runs, so that a captured graph can be replayed with other values.
+    """
+    ops = _token_ops or _load_token_ops()
+    out = ops.adamw_step(params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, step, lr, betas[0], betas[1],
+                         eps, weight_decay, grad_scale, None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_adamw_step")
 
 
 def linear_int8(a: torch.Tensor, w: torch.Tensor, a_scale: torch.Tensor, w_scale: torch.Tensor,

@@ -1,0 +1,376 @@
+// adamw.cu -- the AdamW step of many tensors in one launch, with the moments in fp32 or in 8 bits.
+//
+//   g' = grad_scale * g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+//   p = p (1 - lr decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+//
+// in fp32, p rounded once to its own type.  In 8 bits m and sqrt(v) are e4m3 values with one scale for each 256 in a
+// row (their largest magnitude / 448): sqrt(v), whose range is half of v's, and a float format, so that small values
+// beside a large one keep their relative precision.  They are rounded to one of the two values around them with the
+// odds that keep the mean: to nearest, a change of less than a sixteenth a step (beta2 = 0.999 changes v by a
+// thousandth) would be lost each time.  The odds come from the place and the step alone.  sqrt(v) never becomes 0
+// where it was not: m / (0 + eps) would be a step without bounds.  This step itself uses m and v before the rounding.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "cbs_internal.h"
+#include "ptx.cuh"
+#include "token_ops.h"
+
+namespace cbs {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kBlock = 256;  // elements that share a scale; a warp's work at a time
+constexpr int kPerLane = kBlock / 32;
+constexpr int kBlocksPerWarp = 2;
+constexpr int kChunk = kBlock * kWarps * kBlocksPerWarp;  // elements of a CTA
+constexpr float kTiniest = 7.8886090522101181e-31f;       // 2^-100: as for quantised rows
+constexpr float kMost8 = 448.0f;                          // of e4m3
+
+// A tensor as the kernel sees it.
+struct Entry {
+    void *p;
+    const void *g;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    long long n;
+    unsigned end;        // chunks of this tensor and those before it
+    unsigned char p_type, g_type, wide, unused;
+};
+
+template <int N>
+struct Table {
+    Entry e[N];
+};
+
+__device__ __forceinline__ float get(const float *p) { return *p; }
+__device__ __forceinline__ float get(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float get(const __half *p) { return __half2float(*p); }
+__device__ __forceinline__ void put(float *p, float v) { *p = v; }
+__device__ __forceinline__ void put(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half *p, float v) { *p = __float2half_rn(v); }
+
+// A lane's eight neighbours at once: 32 bytes of fp32, 16 of the 16-bit types, 8 of the 8-bit one.
+__device__ __forceinline__ void get8(const float *p, float *v)
+{
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void put8(float *p, const float *v)
+{
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void get8(const T *p, float *v)
+{
+    const uint4 w = *reinterpret_cast<const uint4 *>(p);
+    const T *t = reinterpret_cast<const T *>(&w);
+    for (int j = 0; j < 8; ++j) v[j] = get(t + j);
+}
+template <typename T>
+__device__ __forceinline__ void put8(T *p, const float *v)
+{
+    uint4 w;
+    T *t = reinterpret_cast<T *>(&w);
+    for (int j = 0; j < 8; ++j) put(t + j, v[j]);
+    *reinterpret_cast<uint4 *>(p) = w;
+}
+
+__device__ __forceinline__ float from_e4m3(uint8_t b)
+{
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3)));
+}
+__device__ __forceinline__ uint8_t to_e4m3(float v)  // of a value that it holds
+{
+    return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+// The two halves of the mixed bits of a place and a step, as numbers in [0, 1): the 32-bit finaliser of Appleby's
+// MurmurHash3.
+__device__ __forceinline__ void dither(uint32_t z, float *a, float *b)
+{
+    z = (z ^ (z >> 16)) * 0x85EBCA6Bu;
+    z = (z ^ (z >> 13)) * 0xC2B2AE35u;
+    z ^= z >> 16;
+    *a = (float)(z >> 16) * 0x1p-16f;
+    *b = (float)(z & 0xFFFFu) * 0x1p-16f;
+}
+
+// x in [0, 448] to the e4m3 value below it or the one above, by u in [0, 1): every step here but the floor is exact,
+// or rounds far below u's own steps.
+__device__ __forceinline__ float eighth(float x, float u)
+{
+    int e = (int)(__float_as_uint(x) >> 23);
+    e = (e < 127 - 6 ? 127 - 6 : e) - 3;  // of the distance between values around x
+    const float v = floorf(x * __uint_as_float((unsigned)(254 - e) << 23) + u) * __uint_as_float((unsigned)e << 23);
+    return v > kMost8 ? kMost8 : v;  // a NaN stays
+}
+
+// Largest of the warp's non-negative values, NaN on top.
+__device__ __forceinline__ float warp_most(float v) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v))); }
+__device__ __forceinline__ float either_most(float a, float b)
+{
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
+struct Rates {
+    float lr, decay_factor, step_size, inv_root_c2, grad_scale;
+    uint32_t step;
+};
+
+// What a step multiplies with, from the host's numbers or the device's.
+__device__ __forceinline__ Rates rates_of(const AdamWScalars &s)
+{
+    Rates r;
+    r.lr = s.lr_at ? *s.lr_at : s.lr;
+    r.grad_scale = s.grad_scale_at ? *s.grad_scale_at : s.grad_scale;
+    float c1 = s.c1, root_c2 = s.root_c2;
+    r.step = (uint32_t)s.step;
+    if (s.step_at) {  // 1 - beta^t through the logarithm, which the host takes in 64 bits: no difference of near equals
+        const long long t = *s.step_at;
+        r.step = (uint32_t)t;
+        c1 = -expm1f((float)t * s.ln_beta1);
+        root_c2 = sqrtf(-expm1f((float)t * s.ln_beta2));
+    }
+    r.decay_factor = 1.0f - r.lr * s.decay;
+    r.step_size = r.lr / c1;
+    r.inv_root_c2 = 1.0f / root_c2;
+    return r;
+}
+
+// 256 elements from `at` on by one warp.  WIDE: all there, a lane's eight side by side; else a lane's are 32 apart.
+template <typename P, typename G, bool EIGHT, bool WIDE>
+__device__ __forceinline__ void step_block(const Entry &e, long long at, const AdamWScalars &s, const Rates &r)
+{
+    const int lane = threadIdx.x & 31;
+    const int have = WIDE ? kBlock : (int)(e.n - at < kBlock ? e.n - at : kBlock);
+    auto place = [&](int j) { return WIDE ? lane * kPerLane + j : j * 32 + lane; };
+    P *p_at = static_cast<P *>(e.p) + at;
+    const G *g_at = static_cast<const G *>(e.g) + at;
+    float p[kPerLane], g[kPerLane], m[kPerLane], v[kPerLane];
+    if constexpr (WIDE) {
+        get8(p_at + place(0), p);
+        get8(g_at + place(0), g);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+            p[j] = place(j) < have ? get(p_at + place(j)) : 0.0f;
+            g[j] = place(j) < have ? get(g_at + place(j)) : 0.0f;
+        }
+    }
+    if constexpr (EIGHT) {
+        const uint8_t *m_at = static_cast<const uint8_t *>(e.m) + at, *v_at = static_cast<const uint8_t *>(e.v) + at;
+        const float ms = e.m_scale[at / kBlock], vs = e.v_scale[at / kBlock];
+        uint8_t mb[kPerLane], vb[kPerLane];
+        if constexpr (WIDE) {
+            *reinterpret_cast<uint2 *>(mb) = *reinterpret_cast<const uint2 *>(m_at + place(0));
+            *reinterpret_cast<uint2 *>(vb) = *reinterpret_cast<const uint2 *>(v_at + place(0));
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPerLane; ++j) {
+                mb[j] = place(j) < have ? m_at[place(j)] : 0;
+                vb[j] = place(j) < have ? v_at[place(j)] : 0;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+            m[j] = from_e4m3(mb[j]) * ms;
+            const float root = from_e4m3(vb[j]) * vs;
+            v[j] = root * root;
+        }
+    } else {
+        const float *m_at = static_cast<const float *>(e.m) + at, *v_at = static_cast<const float *>(e.v) + at;
+        if constexpr (WIDE) {
+            get8(m_at + place(0), m);
+            get8(v_at + place(0), v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPerLane; ++j) {
+                m[j] = place(j) < have ? m_at[place(j)] : 0.0f;
+                v[j] = place(j) < have ? v_at[place(j)] : 0.0f;
+            }
+        }
+    }
+    float root[kPerLane];
+#pragma unroll
+    for (int j = 0; j < kPerLane; ++j) {
+        const float gj = g[j] * r.grad_scale;
+        m[j] = fmaf(s.beta1, m[j], s.rest1 * gj);
+        v[j] = fmaf(s.beta2, v[j], s.rest2 * gj * gj);
+        root[j] = sqrtf(v[j]);
+        p[j] = p[j] * r.decay_factor - r.step_size * m[j] / (root[j] * r.inv_root_c2 + s.eps);
+    }
+    if constexpr (WIDE) {
+        put8(p_at + place(0), p);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j)
+            if (place(j) < have) put(p_at + place(j), p[j]);
+    }
+    if constexpr (EIGHT) {
+        float most_m = 0.0f, most_v = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+            most_m = either_most(most_m, fabsf(m[j]));
+            most_v = either_most(most_v, root[j]);
+        }
+        most_m = warp_most(most_m);
+        most_v = warp_most(most_v);
+        if (most_m < kTiniest) most_m = kTiniest;
+        if (most_v < kTiniest) most_v = kTiniest;
+        const float inv_m = kMost8 / most_m, inv_v = kMost8 / most_v;
+        uint8_t mb[kPerLane], vb[kPerLane];
+#pragma unroll
+        for (int j = 0; j < kPerLane; ++j) {
+            float um, uv;
+            dither((uint32_t)(at + place(j)) + r.step * 0x9E3779B9u, &um, &uv);
+            mb[j] = to_e4m3(copysignf(eighth(fabsf(m[j]) * inv_m, um), m[j]));
+            float held = eighth(root[j] * inv_v, uv);
+            if (held == 0.0f && root[j] > 0.0f) held = 0x1p-9f;
+            vb[j] = to_e4m3(held);
+        }
+        uint8_t *m_at = static_cast<uint8_t *>(e.m) + at, *v_at = static_cast<uint8_t *>(e.v) + at;
+        if constexpr (WIDE) {
+            *reinterpret_cast<uint2 *>(m_at + place(0)) = *reinterpret_cast<const uint2 *>(mb);
+            *reinterpret_cast<uint2 *>(v_at + place(0)) = *reinterpret_cast<const uint2 *>(vb);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPerLane; ++j)
+                if (place(j) < have) {
+                    m_at[place(j)] = mb[j];
+                    v_at[place(j)] = vb[j];
+                }
+        }
+        if (lane == 0) {  // after every lane's reading of the old ones: the reductions above
+            e.m_scale[at / kBlock] = most_m / kMost8;
+            e.v_scale[at / kBlock] = most_v / kMost8;
+        }
+    } else {
+        float *m_at = static_cast<float *>(e.m) + at, *v_at = static_cast<float *>(e.v) + at;
+        if constexpr (WIDE) {
+            put8(m_at + place(0), m);
+            put8(v_at + place(0), v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kPerLane; ++j)
+                if (place(j) < have) {
+                    m_at[place(j)] = m[j];
+                    v_at[place(j)] = v[j];
+                }
+        }
+    }
+}
+
+template <typename P, typename G, bool EIGHT>
+__device__ __forceinline__ void step_chunk(const Entry &e, long long chunk, const AdamWScalars &s, const Rates &r)
+{
+    for (int b = 0; b < kBlocksPerWarp; ++b) {
+        const long long at = chunk * kChunk + (b * kWarps + threadIdx.x / 32) * kBlock;
+        if (at >= e.n) return;
+        if (e.wide && at + kBlock <= e.n)
+            step_block<P, G, EIGHT, true>(e, at, s, r);
+        else
+            step_block<P, G, EIGHT, false>(e, at, s, r);
+    }
+}
+
+template <bool EIGHT, int N>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<N> table, const int count,
+                                                         const __grid_constant__ AdamWScalars s)
+{
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+    int lo = 0, hi = count - 1;  // the first tensor whose chunks end behind this one
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (blockIdx.x < table.e[mid].end)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    const Entry &e = table.e[lo];
+    const long long chunk = blockIdx.x - (lo ? table.e[lo - 1].end : 0u);
+    const Rates r = rates_of(s);
+    switch (e.p_type * 3 + e.g_type) {
+    case kF32 * 3 + kF32: return step_chunk<float, float, EIGHT>(e, chunk, s, r);
+    case kF32 * 3 + kBf16: return step_chunk<float, __nv_bfloat16, EIGHT>(e, chunk, s, r);
+    case kF32 * 3 + kF16: return step_chunk<float, __half, EIGHT>(e, chunk, s, r);
+    case kBf16 * 3 + kF32: return step_chunk<__nv_bfloat16, float, EIGHT>(e, chunk, s, r);
+    case kBf16 * 3 + kBf16: return step_chunk<__nv_bfloat16, __nv_bfloat16, EIGHT>(e, chunk, s, r);
+    case kBf16 * 3 + kF16: return step_chunk<__nv_bfloat16, __half, EIGHT>(e, chunk, s, r);
+    case kF16 * 3 + kF32: return step_chunk<__half, float, EIGHT>(e, chunk, s, r);
+    case kF16 * 3 + kBf16: return step_chunk<__half, __nv_bfloat16, EIGHT>(e, chunk, s, r);
+    default: return step_chunk<__half, __half, EIGHT>(e, chunk, s, r);
+    }
+}
+
+template <int N>
+cudaError_t launch_table(const Entry *entries, int count, const AdamWScalars &s, bool eight, cudaStream_t stream)
+{
+    Table<N> table;
+    for (int i = 0; i < count; ++i) table.e[i] = entries[i];
+    const dim3 grid(entries[count - 1].end), block(kThreads);
+    return eight ? launch_overlapped(adamw_kernel<true, N>, grid, block, 0, stream, 1, table, count, s)
+                 : launch_overlapped(adamw_kernel<false, N>, grid, block, 0, stream, 1, table, count, s);
+}
+
+// As many tensors as a launch's parameters hold (32,764 bytes).
+constexpr int kMostEntries = 448;
+
+}  // namespace
+
+cudaError_t adamw_launch(const AdamWTensor *tensors, int count, const AdamWScalars &s, bool eight, cudaStream_t stream)
+{
+    Entry entries[kMostEntries];
+    int held = 0;
+    long long chunks = 0;
+    auto flush = [&]() {
+        cudaError_t e = cudaSuccess;
+        if (held) {
+            e = held <= 8     ? launch_table<8>(entries, held, s, eight, stream)
+                : held <= 64  ? launch_table<64>(entries, held, s, eight, stream)
+                              : launch_table<kMostEntries>(entries, held, s, eight, stream);
+        }
+        held = 0;
+        chunks = 0;
+        return e;
+    };
+    for (int i = 0; i < count; ++i) {
+        const AdamWTensor &t = tensors[i];
+        if (t.n == 0) continue;
+        const long long need = (t.n + kChunk - 1) / kChunk;
+        if (held == kMostEntries || chunks + need > 0x7fffffffLL) {
+            const cudaError_t e = flush();
+            if (e != cudaSuccess) return e;
+        }
+        chunks += need;
+        auto aligned = [](const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; };
+        Entry &e = entries[held++];
+        e.p = t.p;
+        e.g = t.g;
+        e.m = t.m;
+        e.v = t.v;
+        e.m_scale = t.m_scale;
+        e.v_scale = t.v_scale;
+        e.n = t.n;
+        e.end = (unsigned)chunks;
+        e.p_type = (unsigned char)t.p_type;
+        e.g_type = (unsigned char)t.g_type;
+        e.wide = aligned(t.p, 8 * dtype_size(t.p_type)) && aligned(t.g, 8 * dtype_size(t.g_type)) &&
+                 aligned(t.m, eight ? 8 : 32) && aligned(t.v, eight ? 8 : 32);
+        e.unused = 0;
+    }
+    return flush();
+}
+
+}  // namespace cbs

@@ -20,6 +20,7 @@
 #include <exception>
 #include <optional>
 #include <string>
+#include <vector>
 
 #include "conv_bn_silu.h"
 
@@ -160,6 +161,22 @@ at::Tensor output(PyObject *o, at::IntArrayRef shape, at::ScalarType type, const
     has_type(t, type, name);
     if (t.sizes() != shape)
         wrong_value(std::string(name) + " has shape " + shape_text(t.sizes()) + ", expected " + shape_text(shape));
+    return t;
+}
+
+// Tensors as a tuple.
+PyObject *tuple_of(std::initializer_list<at::Tensor> tensors)
+{
+    PyObject *t = PyTuple_New((Py_ssize_t)tensors.size());
+    Py_ssize_t i = 0;
+    for (const at::Tensor &x : tensors) {
+        PyObject *o = t ? THPVariable_Wrap(x) : nullptr;
+        if (!o) {
+            Py_XDECREF(t);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(t, i++, o);
+    }
     return t;
 }
 
@@ -334,9 +351,208 @@ PyObject *linear_int8(PyObject *, PyObject *const *arg, Py_ssize_t count)
     });
 }
 
+// An activation tensor beside x: its type and shape.
+Rows rows_like(PyObject *o, const at::Tensor &x, const char *name, int device)
+{
+    const at::Tensor &t = tensor(o, name);
+    has_type(t, x.scalar_type(), name);
+    if (t.sizes() != x.sizes())
+        wrong_value(std::string(name) + " has shape " + shape_text(t.sizes()) + ", expected " + shape_text(x.sizes()));
+    return rows_of(t, name, device);
+}
+
+// (x, gamma, eps, residual, quantise, return_y, return_rstd, y, q, total, stream) -> the outputs asked for, in the order
+// y, or q and scale; total, with a residual; y, beside q; rstd.  One alone comes as it is.
+PyObject *rms_norm(PyObject *, PyObject *const *arg, Py_ssize_t count)
+{
+    return guarded(count, 11, [&]() -> PyObject * {
+        const at::Tensor &x = tensor(arg[0], "x");
+        const int device = first_device(x, "x"), type = activation_type(x, "x");
+        const Rows r = rows_of(x, "x", device);
+        const float *gamma = vector_of(arg[1], r.c, "gamma", device);
+        const double eps = PyFloat_AsDouble(arg[2]);
+        if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+        const int quantise = PyObject_IsTrue(arg[4]), with_y = PyObject_IsTrue(arg[5]), with_rstd = PyObject_IsTrue(arg[6]);
+        if (quantise < 0 || with_y < 0 || with_rstd < 0) return nullptr;
+        const bool adds = arg[3] != Py_None, writes_y = !quantise || with_y || arg[7] != Py_None;
+        Rows res{nullptr, 0, 0, 0}, rt{nullptr, 0, 0, 0}, ry{nullptr, 0, 0, 0}, rq{nullptr, 0, 0, 0};
+        if (adds) res = rows_like(arg[3], x, "residual", device);
+        if (!adds && arg[9] != Py_None) wrong_value("total is an output of calls with a residual");
+        const Stream stream(arg[10], device);
+        at::Tensor total, y, q, scale, rstd;
+        if (adds) {
+            total = output(arg[9], x.sizes(), x.scalar_type(), "total", stream);
+            rt = rows_of(total, "total", device);
+        }
+        if (writes_y) {
+            y = output(arg[7], x.sizes(), x.scalar_type(), "y", stream);
+            ry = rows_of(y, "y", device);
+        }
+        const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
+        if (quantise) {
+            q = output(arg[8], x.sizes(), at::kChar, "q", stream);
+            rq = rows_of(q, "q", device);
+            scale = stream.empty(lead, at::kFloat);
+        }
+        if (with_rstd) rstd = stream.empty(lead, at::kFloat);
+        if (r.rows) {
+            float *rstd_at = with_rstd ? rstd.data_ptr<float>() : nullptr;
+            check(quantise ? conv_bn_silu_rms_norm_quantize(r.data, r.distance, res.data, res.distance, gamma, (float)eps,
+                                                            rt.data, rt.distance, ry.data, ry.distance, rq.data, rq.distance,
+                                                            scale.data_ptr<float>(), rstd_at, r.rows, (int)r.c, type,
+                                                            stream.handle)
+                           : conv_bn_silu_rms_norm(r.data, r.distance, res.data, res.distance, gamma, (float)eps, rt.data,
+                                                   rt.distance, ry.data, ry.distance, rstd_at, r.rows, (int)r.c, type,
+                                                   stream.handle));
+        }
+        at::Tensor out[5];
+        int n = 0;
+        if (quantise) {
+            out[n++] = q;
+            out[n++] = scale;
+        } else {
+            out[n++] = y;
+        }
+        if (adds) out[n++] = total;
+        if (quantise && writes_y) out[n++] = y;
+        if (with_rstd) out[n++] = rstd;
+        switch (n) {
+        case 1: return THPVariable_Wrap(out[0]);
+        case 2: return tuple_of({out[0], out[1]});
+        case 3: return tuple_of({out[0], out[1], out[2]});
+        case 4: return tuple_of({out[0], out[1], out[2], out[3]});
+        default: return tuple_of({out[0], out[1], out[2], out[3], out[4]});
+        }
+    });
+}
+
+// (dy, x, gamma, rstd, residual, dx, stream) -> (dx, dgamma)
+PyObject *rms_norm_backward(PyObject *, PyObject *const *arg, Py_ssize_t count)
+{
+    return guarded(count, 7, [&]() -> PyObject * {
+        const at::Tensor &x = tensor(arg[1], "x");
+        const int device = first_device(x, "x"), type = activation_type(x, "x");
+        const Rows r = rows_of(x, "x", device), rdy = rows_like(arg[0], x, "dy", device);
+        const float *gamma = vector_of(arg[2], r.c, "gamma", device);
+        const float *rstd = vector_of(arg[3], r.rows, "rstd", device);
+        if (!rstd && arg[3] == Py_None) wrong_type("rstd must be a torch.Tensor");
+        Rows res{nullptr, 0, 0, 0};
+        if (arg[4] != Py_None) res = rows_like(arg[4], x, "residual", device);
+        const long long need = conv_bn_silu_rms_norm_backward_workspace(r.rows, (int)r.c);
+        if (need < 0) throw Status{CBS_ERR_INVALID_ARG};
+        const Stream stream(arg[6], device);
+        const at::Tensor dx = output(arg[5], x.sizes(), x.scalar_type(), "dx", stream);
+        const Rows rdx = rows_of(dx, "dx", device);
+        const at::Tensor dgamma = stream.empty({r.c}, at::kFloat);
+        const at::Tensor work = stream.empty({need}, at::kByte);
+        check(conv_bn_silu_rms_norm_backward(rdy.data, rdy.distance, r.data, r.distance, gamma, rstd, res.data, res.distance,
+                                             rdx.data, rdx.distance, dgamma.data_ptr<float>(), r.rows, (int)r.c, type,
+                                             work.data_ptr(), need, stream.handle));
+        return pair(dx, dgamma);
+    });
+}
+
+// A list or tuple of tensors.
+struct Tensors {
+    PyObject *fast = nullptr;
+    const char *name;
+    Tensors(PyObject *o, const char *name) : name(name)
+    {
+        if (!PyList_Check(o) && !PyTuple_Check(o)) wrong_type(std::string(name) + " must be a list or tuple of tensors");
+        fast = o;
+    }
+    Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(fast); }
+    const at::Tensor &at(Py_ssize_t i) const { return tensor(PySequence_Fast_GET_ITEM(fast, i), name); }
+};
+
+[[noreturn]] void wrong_item(const char *name, Py_ssize_t i, const std::string &what)
+{
+    wrong_value(std::string(name) + "[" + std::to_string(i) + "] " + what);
+}
+
+// A number, or a CUDA tensor of one element of `type` that the step reads on the device: its address.
+const void *number_at(PyObject *o, at::ScalarType type, const char *name, int device)
+{
+    if (!THPVariable_Check(o)) return nullptr;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    has_type(t, type, name);
+    if (!t.is_cuda() || t.get_device() != device || t.numel() != 1)
+        wrong_value(std::string(name) + " must be a number or hold one element on the CUDA device of the call's first tensor");
+    return t.const_data_ptr();
+}
+
+// (params, grads, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, step, lr, beta1, beta2, eps, weight_decay,
+// grad_scale, stream) -> None; the scales both None for 32-bit moments
+PyObject *adamw_step(PyObject *, PyObject *const *arg, Py_ssize_t count)
+{
+    return guarded(count, 14, [&]() -> PyObject * {
+        const Tensors p(arg[0], "params"), g(arg[1], "grads"), m(arg[2], "exp_avg"), v(arg[3], "exp_avg_sq");
+        const bool eight = arg[4] != Py_None || arg[5] != Py_None;
+        const Tensors ms(eight ? arg[4] : arg[2], "exp_avg_scale"), vs(eight ? arg[5] : arg[2], "exp_avg_sq_scale");
+        const Py_ssize_t n = p.size();
+        for (const Tensors *t : {&g, &m, &v, &ms, &vs})
+            if (t->size() != n)
+                wrong_value(std::string(t->name) + " has " + std::to_string(t->size()) + " tensors, expected " + std::to_string(n));
+        if (!n) Py_RETURN_NONE;
+        const int device = first_device(p.at(0), "params[0]");
+        const at::ScalarType state = eight ? at::kFloat8_e4m3fn : at::kFloat;
+        auto dense = [&](const Tensors &t, Py_ssize_t i, int64_t elements) -> const at::Tensor & {
+            const at::Tensor &x = t.at(i);
+            if (!x.is_cuda() || x.get_device() != device) wrong_item(t.name, i, "must be on the CUDA device of the call's first tensor");
+            if (x.numel() != elements) wrong_item(t.name, i, "has " + std::to_string(x.numel()) + " elements, expected " + std::to_string(elements));
+            if (!x.is_contiguous()) wrong_item(t.name, i, "must be dense");
+            return x;
+        };
+        std::vector<cbs_adamw_tensor> all((size_t)n);
+        for (Py_ssize_t i = 0; i < n; ++i) {
+            cbs_adamw_tensor &e = all[(size_t)i];
+            const int64_t elements = p.at(i).numel();
+            const at::Tensor &tp = dense(p, i, elements), &tg = dense(g, i, elements), &tm = dense(m, i, elements),
+                             &tv = dense(v, i, elements);
+            e.param_dtype = activation_type(tp, "params");
+            e.grad_dtype = activation_type(tg, "grads");
+            has_type(tm, state, "exp_avg");
+            has_type(tv, state, "exp_avg_sq");
+            e.param = tp.data_ptr();
+            e.grad = tg.data_ptr();
+            e.exp_avg = tm.data_ptr();
+            e.exp_avg_sq = tv.data_ptr();
+            e.exp_avg_scale = e.exp_avg_sq_scale = nullptr;
+            if (eight) {
+                const at::Tensor &a = dense(ms, i, (elements + 255) / 256), &b = dense(vs, i, (elements + 255) / 256);
+                has_type(a, at::kFloat, "exp_avg_scale");
+                has_type(b, at::kFloat, "exp_avg_sq_scale");
+                e.exp_avg_scale = static_cast<float *>(a.data_ptr());
+                e.exp_avg_sq_scale = static_cast<float *>(b.data_ptr());
+            }
+            e.n = elements;
+        }
+        cbs_adamw_options o{};
+        o.step_device = static_cast<const long long *>(number_at(arg[6], at::kLong, "step", device));
+        o.lr_device = static_cast<const float *>(number_at(arg[7], at::kFloat, "lr", device));
+        o.grad_scale_device = static_cast<const float *>(number_at(arg[12], at::kFloat, "grad_scale", device));
+        if (!o.step_device) {
+            o.step = PyLong_AsLongLong(arg[6]);
+            if (o.step == -1 && PyErr_Occurred()) return nullptr;
+        }
+        double *const to[] = {&o.lr, &o.beta1, &o.beta2, &o.eps, &o.weight_decay, &o.grad_scale};
+        for (int i = 0; i < 6; ++i) {
+            PyObject *from = arg[7 + i];
+            if ((i == 0 && o.lr_device) || (i == 5 && o.grad_scale_device)) continue;
+            *to[i] = PyFloat_AsDouble(from);
+            if (*to[i] == -1.0 && PyErr_Occurred()) return nullptr;
+        }
+        o.state_bits = eight ? 8 : 32;
+        const Stream stream(arg[13], device);
+        check(conv_bn_silu_adamw_step(all.data(), (int)n, &o, stream.handle));
+        Py_RETURN_NONE;
+    });
+}
+
 #define CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {CALL(layer_norm), CALL(layer_norm_backward), CALL(quantize_rows), CALL(layer_norm_quantize),
-                           CALL(linear_int8), {nullptr, nullptr, 0, nullptr}};
+                           CALL(linear_int8), CALL(rms_norm), CALL(rms_norm_backward), CALL(adamw_step),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_token_ops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -3,7 +3,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <cmath>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include "conv_bn_silu.h"
@@ -228,6 +231,48 @@ int norm_call(const void *x, long long x_stride, const float *gamma, const float
     st = sm_count_current_device(&sms);
     if (st != CBS_OK) return st;
     cudaError_t e = cbs::norm_launch(p, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+}
+
+// An input that an output may be: the same memory row by row, or none of it.
+bool same_or_apart(const void *in, long long in_stride, const void *out, long long out_stride, long long rows)
+{
+    return in != out || rows <= 1 || in_stride == out_stride;
+}
+
+int rms_norm_call(const void *x, long long x_stride, const void *residual, long long residual_stride, const float *gamma,
+                  float eps, void *total, long long total_stride, void *y, long long y_stride, void *q,
+                  long long q_stride, float *row_scale, float *rstd, long long rows, int c, int dtype, void *stream)
+{
+    if (!norm_sizes_ok(rows, c, dtype) || !(eps >= 0.0f) || eps > 3.0e38f) return CBS_ERR_INVALID_ARG;
+    if (rows == 0) return CBS_OK;
+    const int size = cbs::dtype_size(dtype);
+    int st = check_rows(x, rows, c, x_stride, size, false);
+    if (st == CBS_OK && residual) st = check_rows(residual, rows, c, residual_stride, size, false);
+    if (st == CBS_OK && residual) st = check_rows(total, rows, c, total_stride, size, true);
+    if (st == CBS_OK && (y || !q)) st = check_rows(y, rows, c, y_stride, size, true);
+    if (st == CBS_OK && q) st = check_rows(q, rows, c, q_stride, 1, true);
+    if (st != CBS_OK) return st;
+    if ((q && !row_scale) || (residual && !same_or_apart(residual, residual_stride, total, total_stride, rows)))
+        return CBS_ERR_INVALID_ARG;
+    if (!aligned_to(gamma, 4) || !aligned_to(rstd, 4) || !aligned_to(row_scale, 4)) return CBS_ERR_MISALIGNED;
+    cbs::RmsNormProblem p{};
+    p.x = cbs::Rows{const_cast<void *>(x), x_stride};
+    p.residual = cbs::Rows{const_cast<void *>(residual), residual_stride};
+    p.total = cbs::Rows{residual ? total : nullptr, total_stride};
+    p.y = cbs::Rows{y, y_stride};
+    p.q = cbs::Rows{q, q_stride};
+    p.row_scale = row_scale;
+    p.rstd = rstd;
+    p.gamma = gamma;
+    p.eps = eps;
+    p.rows = rows;
+    p.c = c;
+    p.dtype = dtype;
+    int sms = 0;
+    st = sm_count_current_device(&sms);
+    if (st != CBS_OK) return st;
+    cudaError_t e = cbs::rms_norm_launch(p, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CBS_OK : cuda_fail(e);
 }
 
@@ -656,6 +701,138 @@ int conv_bn_silu_layer_norm_backward(const void *dy, long long dy_stride, const 
     p.c = c;
     p.dtype = dtype;
     cudaError_t e = cbs::norm_grad_launch(p, sms, strm);
+    return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+}
+
+int conv_bn_silu_rms_norm(const void *x, long long x_stride, const void *residual, long long residual_stride,
+                          const float *gamma, float eps, void *total, long long total_stride, void *y,
+                          long long y_stride, float *rstd, long long rows, int c, int dtype, void *stream)
+{
+    return rms_norm_call(x, x_stride, residual, residual_stride, gamma, eps, total, total_stride, y, y_stride, nullptr, 0,
+                         nullptr, rstd, rows, c, dtype, stream);
+}
+
+int conv_bn_silu_rms_norm_quantize(const void *x, long long x_stride, const void *residual,
+                                   long long residual_stride, const float *gamma, float eps, void *total,
+                                   long long total_stride, void *y, long long y_stride, void *q,
+                                   long long q_stride, float *row_scale, float *rstd, long long rows, int c,
+                                   int dtype, void *stream)
+{
+    if (!q && rows != 0) return CBS_ERR_INVALID_ARG;
+    return rms_norm_call(x, x_stride, residual, residual_stride, gamma, eps, total, total_stride, y, y_stride, q, q_stride,
+                         row_scale, rstd, rows, c, dtype, stream);
+}
+
+long long conv_bn_silu_rms_norm_backward_workspace(long long rows, int c)
+{
+    if (!norm_sizes_ok(rows, c, CBS_DTYPE_F32)) return -1;
+    int sms = 0;
+    if (sm_count_current_device(&sms) != CBS_OK) return -1;
+    return 4LL * c * cbs::rms_grad_partial_rows(rows, sms);
+}
+
+int conv_bn_silu_rms_norm_backward(const void *dy, long long dy_stride, const void *x, long long x_stride,
+                                   const float *gamma, const float *rstd, const void *residual,
+                                   long long residual_stride, void *dx, long long dx_stride, float *dgamma,
+                                   long long rows, int c, int dtype, void *workspace, long long workspace_bytes,
+                                   void *stream)
+{
+    if (!norm_sizes_ok(rows, c, dtype)) return CBS_ERR_INVALID_ARG;
+    if (!dgamma) return CBS_ERR_INVALID_ARG;
+    if (!aligned_to(gamma, 4) || !aligned_to(rstd, 4) || !aligned_to(dgamma, 4)) return CBS_ERR_MISALIGNED;
+    cudaStream_t strm = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        cudaError_t e = cudaMemsetAsync(dgamma, 0, 4 * (size_t)c, strm);
+        return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+    }
+    const int size = cbs::dtype_size(dtype);
+    int st = check_rows(dy, rows, c, dy_stride, size, false);
+    if (st == CBS_OK) st = check_rows(x, rows, c, x_stride, size, false);
+    if (st == CBS_OK && residual) st = check_rows(residual, rows, c, residual_stride, size, false);
+    if (st == CBS_OK) st = check_rows(dx, rows, c, dx_stride, size, true);
+    if (st != CBS_OK) return st;
+    if (!rstd || !workspace || !same_or_apart(residual, residual_stride, dx, dx_stride, rows)) return CBS_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return CBS_ERR_MISALIGNED;
+    int sms = 0;
+    st = sm_count_current_device(&sms);
+    if (st != CBS_OK) return st;
+    cbs::RmsNormGradProblem p{};
+    p.partial_rows = cbs::rms_grad_partial_rows(rows, sms);
+    if (workspace_bytes < 4LL * c * p.partial_rows) return CBS_ERR_INVALID_ARG;
+    p.dy = cbs::Rows{const_cast<void *>(dy), dy_stride};
+    p.x = cbs::Rows{const_cast<void *>(x), x_stride};
+    p.residual = cbs::Rows{const_cast<void *>(residual), residual_stride};
+    p.dx = cbs::Rows{dx, dx_stride};
+    p.gamma = gamma;
+    p.rstd = rstd;
+    p.dgamma = dgamma;
+    p.partial = static_cast<float *>(workspace);
+    p.rows = rows;
+    p.c = c;
+    p.dtype = dtype;
+    cudaError_t e = cbs::rms_norm_grad_launch(p, sms, strm);
+    return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+}
+
+int conv_bn_silu_adamw_step(const cbs_adamw_tensor *tensors, int count, const cbs_adamw_options *options,
+                            void *stream)
+{
+    if (count < 0 || (count > 0 && !tensors) || !options) return CBS_ERR_INVALID_ARG;
+    const cbs_adamw_options &o = *options;
+    const bool eight = o.state_bits == 8;
+    if (!eight && o.state_bits != 32) return CBS_ERR_INVALID_ARG;
+    if (!std::isfinite(o.lr) || !std::isfinite(o.weight_decay) || !std::isfinite(o.grad_scale)) return CBS_ERR_INVALID_ARG;
+    if (!(o.beta1 >= 0.0 && o.beta1 < 1.0) || !(o.beta2 >= 0.0 && o.beta2 < 1.0) || !(o.eps >= 0.0) || o.eps > 3.0e38)
+        return CBS_ERR_INVALID_ARG;
+    if (!o.step_device && o.step < 1) return CBS_ERR_INVALID_ARG;
+    if (!aligned_to(o.lr_device, 4) || !aligned_to(o.grad_scale_device, 4) || !aligned_to(o.step_device, 8))
+        return CBS_ERR_MISALIGNED;
+    std::vector<cbs::AdamWTensor> v;
+    std::vector<std::pair<uintptr_t, uintptr_t>> written;  // [from, to) of each parameter
+    v.reserve((size_t)count);
+    written.reserve((size_t)count);
+    for (int i = 0; i < count; ++i) {
+        const cbs_adamw_tensor &t = tensors[i];
+        if (t.n < 0 || t.n > (1LL << 40) || t.param_dtype < CBS_DTYPE_F32 || t.param_dtype > CBS_DTYPE_F16 ||
+            t.grad_dtype < CBS_DTYPE_F32 || t.grad_dtype > CBS_DTYPE_F16)
+            return CBS_ERR_INVALID_ARG;
+        if (t.n == 0) continue;
+        if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq || (eight && (!t.exp_avg_scale || !t.exp_avg_sq_scale)))
+            return CBS_ERR_INVALID_ARG;
+        if (!aligned_to(t.param, cbs::dtype_size(t.param_dtype)) || !aligned_to(t.grad, cbs::dtype_size(t.grad_dtype)) ||
+            (!eight && (!aligned_to(t.exp_avg, 4) || !aligned_to(t.exp_avg_sq, 4))) ||
+            (eight && (!aligned_to(t.exp_avg_scale, 4) || !aligned_to(t.exp_avg_sq_scale, 4))))
+            return CBS_ERR_MISALIGNED;
+        const uintptr_t from = reinterpret_cast<uintptr_t>(t.param);
+        written.emplace_back(from, from + (uintptr_t)t.n * cbs::dtype_size(t.param_dtype));
+        v.push_back(cbs::AdamWTensor{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale, t.n,
+                                     t.param_dtype, t.grad_dtype});
+    }
+    if (v.empty()) return CBS_OK;
+    // A parameter given twice would be stepped by two blocks at once.
+    std::sort(written.begin(), written.end());
+    for (size_t i = 1; i < written.size(); ++i)
+        if (written[i].first < written[i - 1].second) return CBS_ERR_INVALID_ARG;
+    cbs::AdamWScalars s{};
+    s.lr_at = o.lr_device;
+    s.grad_scale_at = o.grad_scale_device;
+    s.step_at = o.step_device;
+    s.lr = (float)o.lr;
+    s.grad_scale = (float)o.grad_scale;
+    s.beta1 = (float)o.beta1;
+    s.beta2 = (float)o.beta2;
+    s.rest1 = (float)(1.0 - o.beta1);
+    s.rest2 = (float)(1.0 - o.beta2);
+    s.ln_beta1 = (float)std::log(o.beta1);  // of 0: -infinity, and 1 - beta^t is 1
+    s.ln_beta2 = (float)std::log(o.beta2);
+    if (!o.step_device) {
+        s.step = o.step;
+        s.c1 = (float)-std::expm1((double)o.step * std::log(o.beta1));
+        s.root_c2 = (float)std::sqrt(-std::expm1((double)o.step * std::log(o.beta2)));
+    }
+    s.eps = (float)o.eps;
+    s.decay = (float)o.weight_decay;
+    cudaError_t e = cbs::adamw_launch(v.data(), (int)v.size(), s, eight, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CBS_OK : cuda_fail(e);
 }
 

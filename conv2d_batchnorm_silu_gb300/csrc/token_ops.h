@@ -47,6 +47,56 @@ struct NormGradProblem {
     int dtype;
 };
 
+struct RmsNormProblem {
+    Rows x;              // input, `dtype`
+    Rows residual;       // nullable, added to x
+    Rows total;          // their sum, with residual only; may be residual itself
+    Rows y;              // normalised output, `dtype`; nullable with q
+    Rows q;              // nullable int8 output, with row_scale
+    float *row_scale;    // [rows], with q only
+    float *rstd;         // nullable [rows]: 1/sqrt(mean square + eps)
+    const float *gamma;  // nullable [c]
+    float eps;
+    long long rows;
+    int c;
+    int dtype;
+};
+
+struct RmsNormGradProblem {
+    Rows dy, x, dx;      // `dtype`; x is what was normalised
+    Rows residual;       // nullable, added to dx; may be dx itself
+    const float *gamma;  // nullable [c]
+    const float *rstd;   // [rows]
+    float *dgamma;       // [c]
+    float *partial;      // workspace: [partial_rows][c]
+    int partial_rows;    // from rms_grad_partial_rows
+    long long rows;
+    int c;
+    int dtype;
+};
+
+// One tensor of an AdamW step: fp32 moments, or e4m3 ones (v's square root) with a scale for each 256 elements.
+struct AdamWTensor {
+    void *p;
+    const void *g;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    long long n;
+    int p_type, g_type;  // DType
+};
+
+// The step's numbers; those with an address are read there, on the device.
+struct AdamWScalars {
+    const float *lr_at, *grad_scale_at;
+    const long long *step_at;
+    float lr, grad_scale;
+    float beta1, beta2, rest1, rest2;  // rest: 1 - beta
+    float ln_beta1, ln_beta2;
+    float c1, root_c2;                 // 1 - beta1^step, sqrt(1 - beta2^step)
+    float eps, decay;
+    long long step;
+};
+
 struct LinearProblem {
     Rows a;                // int8 [m][k]
     Rows w;                // int8 [n][k]
@@ -95,6 +145,13 @@ cudaError_t read_and_clear_word(const Symbol &word, cudaStream_t stream, unsigne
 cudaError_t norm_launch(const NormProblem &p, int sm_count, cudaStream_t stream);
 int norm_grad_partial_rows(long long rows, int sm_count);  // of partial sums, each [2][c]
 cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_t stream);
+
+cudaError_t rms_norm_launch(const RmsNormProblem &p, int sm_count, cudaStream_t stream);
+int rms_grad_partial_rows(long long rows, int sm_count);  // of partial sums, each [c]
+cudaError_t rms_norm_grad_launch(const RmsNormGradProblem &p, int sm_count, cudaStream_t stream);
+
+constexpr int kAdamWBlock = 256;  // elements that share a scale
+cudaError_t adamw_launch(const AdamWTensor *tensors, int count, const AdamWScalars &s, bool eight, cudaStream_t stream);
 
 // What linear_launch runs (the fields of cbs_linear_plan but for the workspace).
 struct LinearPlan {

@@ -320,8 +320,8 @@ int conv_bn_silu_forward_request(const void *x, const void *w, const float *scal
 
 /*
  * ---------------------------------------------------------------------------
- * Token-wise operators: layer norm with its gradient, rows quantised to 8-bit
- * integers, and the linear layer over such rows.  A pixel of an NHWC tensor is
+ * Token-wise operators: layer norm and root-mean-square norm with their gradients,
+ * rows quantised to 8-bit integers, and the linear layer over such rows.  A pixel of an NHWC tensor is
  * a row of its channels, so they run on the same activations as the layers
  * above ([n*h*w][c]), and on tokens [tokens][c].
  *
@@ -334,7 +334,7 @@ int conv_bn_silu_forward_request(const void *x, const void *w, const float *scal
  *     on 4-byte boundaries nearly as fast).  Input rows off those boundaries
  *     are read in whole aligned words of up to 16 bytes, of which each holds
  *     at least a byte of the row.
- *   - The norm, its gradient and the quantisation take up to 2^40 rows of 1 to 2^29
+ *   - The norms, their gradients and the quantisation take up to 2^40 rows of 1 to 2^29
  *     channels; wider rows are CBS_ERR_INVALID_ARG.
  *   - dtype is a cbs_dtype and goes for every activation of the call; parameters,
  *     statistics and scales are float32, as the folded scale and bias are.
@@ -408,6 +408,98 @@ int conv_bn_silu_quantize_rows(const void *x, long long x_stride, void *q, long 
 int conv_bn_silu_layer_norm_quantize(const void *x, long long x_stride, const float *gamma, const float *beta,
                                      float eps, void *q, long long q_stride, float *row_scale, long long rows,
                                      int c, int dtype, void *stream);
+
+/*
+ * Root-mean-square norm of each row over its c channels, after the residual's addition:
+ *   total = x + residual, rounded to dtype (residual NULL: total is x, and nothing is written)
+ *   rstd = 1 / sqrt(sum total^2 / c + eps),  y = total * rstd * gamma
+ *   x, residual, total, y : device, dtype [rows][c], row distances *_stride; total is written
+ *           and may be residual itself (the same pointer and distance)
+ *   gamma : device, float32 [c], or NULL for 1
+ *   eps   : >= 0 and finite (with eps == 0 a row of zeros gives NaN)
+ *   rstd  : device, float32 [rows], written (what conv_bn_silu_rms_norm_backward needs), or NULL
+ * The norm is of the rounded total.  Computed in fp32, y rounded once.
+ * rows == 0 is a no-op; c >= 1.
+ */
+int conv_bn_silu_rms_norm(const void *x, long long x_stride, const void *residual, long long residual_stride,
+                          const float *gamma, float eps, void *total, long long total_stride, void *y,
+                          long long y_stride, float *rstd, long long rows, int c, int dtype, void *stream);
+
+/* conv_bn_silu_rms_norm and conv_bn_silu_quantize_rows in one pass: the normalised values are
+ * quantised in fp32, without being rounded to dtype first.  y may be NULL: it is written only
+ * for callers that need the rows in dtype as well (adapters beside the int8 linear layer). */
+int conv_bn_silu_rms_norm_quantize(const void *x, long long x_stride, const void *residual,
+                                   long long residual_stride, const float *gamma, float eps, void *total,
+                                   long long total_stride, void *y, long long y_stride, void *q,
+                                   long long q_stride, float *row_scale, float *rstd, long long rows, int c,
+                                   int dtype, void *stream);
+
+/*
+ * Gradient of conv_bn_silu_rms_norm.  With h = x * rstd and g = dy * gamma,
+ *   dx = rstd * (g - h * sum_c(g * h) / c) [+ residual]
+ *   dgamma = sum over rows of dy * h
+ *   dy, x, dx : device, dtype [rows][c], row distances *_stride; x is what the forward call
+ *               normalised (its total, where it had a residual)
+ *   gamma     : as in the forward call, or NULL for 1
+ *   rstd      : device, float32 [rows], written by the forward call
+ *   residual  : device, dtype [rows][c], or NULL: the gradient that arrives at x past the norm,
+ *               added in fp32 before the one rounding.  It may be dx itself.
+ *   dgamma    : device, float32 [c], written (not added to)
+ *   workspace : device, 16-byte aligned, at least
+ *               conv_bn_silu_rms_norm_backward_workspace(rows, c) bytes
+ * dx is the gradient of x and of the forward call's residual alike.
+ * rows == 0 leaves dgamma zero.
+ */
+int conv_bn_silu_rms_norm_backward(const void *dy, long long dy_stride, const void *x, long long x_stride,
+                                   const float *gamma, const float *rstd, const void *residual,
+                                   long long residual_stride, void *dx, long long dx_stride, float *dgamma,
+                                   long long rows, int c, int dtype, void *workspace, long long workspace_bytes,
+                                   void *stream);
+
+/* Workspace of conv_bn_silu_rms_norm_backward on the current device in bytes; -1 for arguments
+ * out of range or when no device answers. */
+long long conv_bn_silu_rms_norm_backward_workspace(long long rows, int c);
+
+/*
+ * AdamW step of `count` tensors, each in place:
+ *   g' = grad_scale * grad,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
+ *   param = param (1 - lr decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32, the parameter rounded once to its type.  Elements of a tensor are adjacent.
+ *   state_bits 32: m and v are float32 [n].
+ *   state_bits 8 : m and v hold 8-bit floats (e4m3) [n], each times the scale of its block of 256
+ *                  elements: m, and the square root of v.  A block's scale is its largest magnitude
+ *                  (2^-100 at least) / 448.  A value goes to one of the two around it: to
+ *                  floor(|value| / distance + u) * distance with u in [0, 1) from the mixed bits of
+ *                  (element + step * 0x9E3779B9) modulo 2^32, so the same step gives the same bits
+ *                  again; where v is not 0 its root is held as 2^-9 of the scale at least.  A block with a
+ *                  gradient that is not finite becomes NaN.  Zeros everywhere are the initial state.
+ * No tensor may overlap another; pointers are aligned to their element, and those aligned to 8
+ * elements (float32 to 32 bytes) run on wide loads and stores.
+ */
+typedef struct cbs_adamw_tensor {
+    void *param;             /* device, param_dtype [n] */
+    const void *grad;        /* device, grad_dtype [n] */
+    void *exp_avg;           /* m */
+    void *exp_avg_sq;        /* v, or its square root in 8 bits */
+    float *exp_avg_scale;    /* device, float32 [(n + 255) / 256]; 8 bits only */
+    float *exp_avg_sq_scale; /* likewise */
+    long long n;             /* 0 <= n <= 2^40 */
+    int param_dtype, grad_dtype; /* cbs_dtype */
+} cbs_adamw_tensor;
+
+typedef struct cbs_adamw_options {
+    double lr, beta1, beta2, eps, weight_decay; /* finite; 0 <= beta < 1, eps >= 0.  In 64 bits, so that
+                                                   1 - beta keeps its bits */
+    double grad_scale;
+    long long step;                /* >= 1: the number of this step, counted from 1 */
+    const float *lr_device;        /* not NULL: read on the device in place of lr, grad_scale, step */
+    const float *grad_scale_device;
+    const long long *step_device;
+    int state_bits;                /* 8 or 32 */
+} cbs_adamw_options;
+
+int conv_bn_silu_adamw_step(const cbs_adamw_tensor *tensors, int count, const cbs_adamw_options *options,
+                            void *stream);
 
 /*
  * Linear layer over 8-bit integers, scales for each row (token) and output channel:

@@ -1,5 +1,5 @@
-"""Token-wise operators in 64 bits (numpy), the reference the tests compare with: layer norm,
-its gradient, rows quantised to 8-bit integers, and the linear layer over them.  Inputs are
+"""Token-wise operators in 64 bits (numpy), the reference the tests compare with: the norms,
+their gradients, rows quantised to 8-bit integers, and the linear layer over them.  Inputs are
 arrays of any float type, widened to float64; nothing here is shared with the CUDA path."""
 from __future__ import annotations
 
@@ -70,3 +70,45 @@ def linear_int8(a, w, a_scale, w_scale, bias=None, activation="identity", residu
     if residual is not None:
         y = y + np.asarray(residual, np.float64)
     return y, z, np.abs(a) @ np.abs(w).T
+
+
+def rms_norm(x, gamma=None, eps=1e-6):
+    """(y, rstd)."""
+    x = np.asarray(x, np.float64)
+    rstd = 1.0 / np.sqrt((x ** 2).mean(axis=1) + eps)
+    y = x * rstd[:, None]
+    return (y if gamma is None else y * np.asarray(gamma, np.float64)), rstd
+
+
+def rms_norm_backward(dy, x, gamma, rstd, residual=None):
+    """(dx, dgamma)."""
+    dy, x, rstd = np.asarray(dy, np.float64), np.asarray(x, np.float64), np.asarray(rstd, np.float64)[:, None]
+    h = x * rstd
+    g = dy if gamma is None else dy * np.asarray(gamma, np.float64)
+    dx = rstd * (g - h * (g * h).mean(axis=1, keepdims=True))
+    return (dx if residual is None else dx + np.asarray(residual, np.float64)), (dy * h).sum(0)
+
+
+def adamw(p, g, m, v, step, lr, beta1, beta2, eps, decay, grad_scale=1.0):
+    """(p, m, v) after the step."""
+    p, g, m, v = (np.asarray(t, np.float64) for t in (p, g, m, v))
+    g = g * grad_scale
+    m, v = beta1 * m + (1 - beta1) * g, beta2 * v + (1 - beta2) * g * g
+    u = m / (1 - beta1 ** step) / (np.sqrt(v / (1 - beta2 ** step)) + eps)
+    return p * (1 - lr * decay) - lr * u, m, v
+
+
+def dither(n, step):
+    """The two numbers in [0, 1) of each place of a tensor in a step with 8-bit moments."""
+    with np.errstate(over="ignore"):
+        z = np.arange(n, dtype=np.uint32) + np.uint32(step * 0x9E3779B9 % 2 ** 32)
+        z = (z ^ (z >> np.uint32(16))) * np.uint32(0x85EBCA6B)
+        z = (z ^ (z >> np.uint32(13))) * np.uint32(0xC2B2AE35)
+        z = z ^ (z >> np.uint32(16))
+    return (z >> np.uint32(16)) / 65536.0, (z & np.uint32(0xFFFF)) / 65536.0
+
+
+def e4m3_distance(x):
+    """Between the 8-bit floats around magnitudes x."""
+    with np.errstate(divide="ignore"):
+        return 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(x, 2.0 ** -60))), -6) - 3)
