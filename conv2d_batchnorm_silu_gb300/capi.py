@@ -132,6 +132,11 @@ _declare("conv_bn_silu_rms_norm_quantize", [_p, _ll, _p, _ll, _p, _f, _p, _ll, _
 _declare("conv_bn_silu_rms_norm_backward",
          [_p, _ll, _p, _ll, _p, _p, _p, _ll, _p, _ll, _p, _ll, _i, _i, _p, _ll, _p])
 _declare("conv_bn_silu_rms_norm_backward_workspace", [_ll, _i], _ll)
+_declare("conv_bn_silu_linear_adapters", [_p, _ll, _p, _p, _p, _p, _p, _ll, _p, _ll, _p, _ll, _i, _i, _i, _i, _i, _p, _ll, _p])
+_declare("conv_bn_silu_linear_adapters_workspace", [_ll, _i, _i, _i, _i], _ll)
+_declare("conv_bn_silu_linear_adapters_backward",
+         [_p, _ll, _p, _ll, _p, _p, _p, _p, _p, _p, _ll, _p, _ll, _p, _p, _ll, _i, _i, _i, _i, _i, _p, _ll, _p])
+_declare("conv_bn_silu_linear_adapters_backward_workspace", [_ll, _i, _i, _i, _i], _ll)
 _declare("conv_bn_silu_adamw_step", [ctypes.POINTER(AdamWTensor), _i, ctypes.POINTER(AdamWOptions), _p])
 _declare("conv_bn_silu_linear_int8", [_p, _ll, _p, _ll, _p, _p, _p, _p, _ll, _p, _ll, _ll, _i, _i, _i, _i, _p, _ll, _p])
 _declare("conv_bn_silu_linear_int8_workspace", [_ll, _i, _i], _ll)
@@ -608,6 +613,39 @@ def rms_norm_backward(dy: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | N
     out = ops.rms_norm_backward(dy, x, gamma, rstd, residual, dx, None if stream is None else _stream_handle(stream))
     if type(out) is int:
         _raise_if(out, "conv_bn_silu_rms_norm_backward")
+    return out
+
+
+def linear_adapters(x: torch.Tensor, index: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                    scale: torch.Tensor | None = None, base: torch.Tensor | None = None, return_hidden: bool = False,
+                    y: torch.Tensor | None = None, stream=None):
+    """conv_bn_silu_linear_adapters: y[i] = base[i] + scale[g] * b[g] @ (a[g] @ x[i]) with g = index[i], the low-rank
+    adapters of many requests at once beside a linear layer whose output is base (None: 0).
+
+    x: float32, bf16 or f16 [..., k]; index: int32, one for each row of x, in any order, outside [0, adapters) for rows
+    without an adapter (y is base there); a [adapters, rank, k] and b [adapters, n, rank]: dense, x's type; scale: fp32
+    [adapters] or None; base and y: x's type [..., n] (base may be y).  With return_hidden also the fp32 [..., rank]
+    a[g] @ x[i] for linear_adapters_backward; autograd does not see the call.
+    """
+    ops = _token_ops or _load_token_ops()
+    out = ops.linear_adapters(x, index, a, b, scale, base, return_hidden, y,
+                              None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_linear_adapters")
+    return out
+
+
+def linear_adapters_backward(dy: torch.Tensor, x: torch.Tensor, index: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                             scale: torch.Tensor | None, hidden: torch.Tensor, base: torch.Tensor | None = None,
+                             dx: torch.Tensor | None = None, stream=None):
+    """conv_bn_silu_linear_adapters_backward: (dx, da, db) from dy, the forward call's arguments and the hidden rows it
+    returned.  base: the gradient that x has from elsewhere, added to dx (it may be dx); dx is like x; da and db are fp32
+    like a and b, zeros for adapters without rows.  The gradient of the forward call's base is dy itself."""
+    ops = _token_ops or _load_token_ops()
+    out = ops.linear_adapters_backward(dy, x, index, a, b, scale, hidden, base, dx,
+                                       None if stream is None else _stream_handle(stream))
+    if type(out) is int:
+        _raise_if(out, "conv_bn_silu_linear_adapters_backward")
     return out
 
 

@@ -1,0 +1,381 @@
+// adapters.cu -- low-rank adapters of many requests beside a linear layer, and their gradients.
+//
+// Row i has adapter g = index[i], or none where index[i] is outside [0, adapters):
+//
+//   hidden_i = A_g x_i,  y_i = base_i + s_g B_g hidden_i        (y_i = base_i without an adapter)
+//
+// and with the gradient dy of y,
+//
+//   dhidden_i = B_g^T dy_i,  dx_i = base_i + s_g A_g^T dhidden_i,
+//   dA_g = s_g sum_i dhidden_i x_i^T,  dB_g = s_g sum_i dy_i hidden_i^T  over the rows of g.
+//
+// y and dx are the same two products after one another, the second with the transposed weights.  Rows are taken by
+// adapter, in an order that this file's first kernel finds: any order of rows costs the same, and the sums of the
+// weights' gradients are over the rows as they come.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "adapters.h"
+#include "cbs_internal.h"
+#include "ptx.cuh"
+#include "token_ops.h"
+
+namespace cbs {
+namespace {
+
+// ------------------------------------------------------------------ rows by adapter
+// Each block takes a window of 1024 rows and sorts them by adapter; where an adapter's rows go in all, it finds by
+// counting the whole index itself, so that no block waits for another.  The counts are sums of integers: their order
+// does not matter.  Rows without an adapter come last, as those of an adapter more.
+constexpr int kWindow = 1024;
+
+struct OrderArgs {
+    const int *index;
+    int *order, *starts, *tile_count;
+    AdapterTile *tiles;
+    int m, adapters, tile_rows;
+};
+
+__global__ void __launch_bounds__(kWindow) adapter_order_kernel(const OrderArgs a)
+{
+    extern __shared__ int order_bins[];  // [5][bins]
+    __shared__ unsigned keys[kWindow];
+    __shared__ unsigned long long warp_sums[32];
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+    const int bins = a.adapters + 1, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    int *total = order_bins, *before = total + bins, *head = before + bins, *base = head + bins, *tile_base = base + bins;
+    for (int i = tid; i < bins; i += kWindow) total[i] = before[i] = 0;
+    __syncthreads();
+    auto of = [&](int i) {
+        const int v = a.index[i];
+        return v < 0 || v >= a.adapters ? a.adapters : v;
+    };
+    const int start = (int)blockIdx.x * kWindow;
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 < a.m; i0 += kAhead * kWindow) {
+        int v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) v[j] = i0 + j * kWindow + tid < a.m ? of(i0 + j * kWindow + tid) : -1;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const unsigned same = __match_any_sync(0xffffffffu, v[j]);
+            if (v[j] >= 0 && lane == __ffs((int)same) - 1) {
+                atomicAdd(total + v[j], __popc(same));
+                if (i0 + j * kWindow < start) atomicAdd(before + v[j], __popc(same));
+            }
+        }
+    }
+    // The window's rows by adapter, and among one adapter's in their order.
+    unsigned key = start + tid < a.m ? (unsigned)of(start + tid) << 10 | (unsigned)tid : 0xffffffffu;
+    for (int k = 2; k <= kWindow; k <<= 1)
+        for (int j = k / 2; j > 0; j >>= 1) {
+            unsigned other;
+            if (j >= 32) {
+                __syncthreads();
+                keys[tid] = key;
+                __syncthreads();
+                other = keys[tid ^ j];
+            } else {
+                other = __shfl_xor_sync(0xffffffffu, key, j);
+            }
+            const bool smaller = ((tid & j) == 0) == ((tid & k) == 0);
+            key = (key < other) == smaller ? key : other;
+        }
+    __syncthreads();
+    keys[tid] = key;
+    __syncthreads();
+    const bool here = key != 0xffffffffu;
+    const int mine = (int)(key >> 10);
+    if (here && (tid == 0 || (int)(keys[tid - 1] >> 10) != mine)) head[mine] = tid;
+    // Exclusive sums of rows and of tiles over the adapters before.
+    const int each = (bins + kWindow - 1) / kWindow;
+    auto amount = [&](int b) {
+        const unsigned rows = (unsigned)total[b];
+        return (unsigned long long)((rows + a.tile_rows - 1) / a.tile_rows) << 32 | rows;
+    };
+    unsigned long long sum = 0;
+    for (int b = tid * each; b < (tid + 1) * each && b < bins; ++b) sum += amount(b);
+    unsigned long long scan = sum;
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long v = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += v;
+    }
+    if (lane == 31) warp_sums[warp] = scan;
+    __syncthreads();
+    if (warp == 0) {
+        unsigned long long v = warp_sums[lane];
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned long long u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        warp_sums[lane] = v;
+    }
+    __syncthreads();
+    unsigned long long run = scan - sum + (warp ? warp_sums[warp - 1] : 0ull);
+    for (int b = tid * each; b < (tid + 1) * each && b < bins; ++b) {
+        base[b] = (int)(unsigned)run;
+        tile_base[b] = (int)(run >> 32);
+        if (blockIdx.x == 0) a.starts[b] = (int)(unsigned)run;
+        run += amount(b);
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        a.starts[bins] = a.m;
+        *a.tile_count = (int)(warp_sums[31] >> 32);
+    }
+    __syncthreads();
+    if (!here) return;
+    const int rank = before[mine] + tid - head[mine], at = base[mine] + rank;
+    a.order[at] = start + (int)(key & 1023u);
+    if (rank % a.tile_rows == 0) {
+        const int left = total[mine] - rank;
+        a.tiles[tile_base[mine] + rank / a.tile_rows] = AdapterTile{mine, at, left < a.tile_rows ? left : a.tile_rows, 0};
+    }
+}
+
+cudaError_t order_launch(const OrderArgs &a, cudaStream_t stream)
+{
+    const int smem = 5 * 4 * (a.adapters + 1);
+    static bool allowed[kMaxDevices] = {};
+    if (smem > 40 * 1024) {
+        const cudaError_t e = allow_dynamic_smem(adapter_order_kernel, 5 * 4 * (kMostAdapters + 1), allowed);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_overlapped(adapter_order_kernel, dim3((unsigned)((a.m + kWindow - 1) / kWindow)), dim3(kWindow), smem, stream, 1, a);
+}
+
+// ------------------------------------------------------------------ the weights' gradients, joined
+// Adapters whose rows reach over several chunks: the partial sums of the first (its second row), then of the others
+// (their first rows), in order.  Those without rows get zeros.
+__global__ void __launch_bounds__(kAdapterThreads) adapter_join_kernel(const AdapterGradArgs a)
+{
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+    const long long of_a = (long long)a.rank * a.k, all = of_a + (long long)a.rank * a.n;
+    for (int adapter = blockIdx.y; adapter < a.adapters; adapter += gridDim.y) {
+        const int first = a.starts[adapter], last = a.starts[adapter + 1];
+        const int c0 = first / a.chunk_rows, c1 = (last - 1) / a.chunk_rows;
+        if (first < last && c0 == c1) continue;
+        for (long long i = (long long)blockIdx.x * kAdapterThreads + threadIdx.x; i < all; i += (long long)gridDim.x * kAdapterThreads) {
+            float v = 0.0f;
+            if (first < last) {
+                v = a.partial[(2LL * c0 + 1) * all + i];
+                for (int c = c0 + 1; c <= c1; ++c) v += a.partial[2LL * c * all + i];
+            }
+            if (i < of_a)
+                a.da[adapter * of_a + i] = v;
+            else
+                a.db[adapter * (all - of_a) + i - of_a] = v;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ what a call launches
+struct Layout {
+    bool few;      // each cluster finds its rows itself
+    bool many;     // tiles of kAdapterManyRows
+    int tile_rows, tiles;  // tiles at most
+    int clusters, size;
+};
+
+// Rows that one call of adapter_products_kernel's clusters looks at by itself.
+constexpr int kFew = kAdapterThreads;
+
+Layout layout_of(const AdapterProblem &p, bool ordered, int k, int n, int sm_count)
+{
+    Layout l{};
+    l.few = !ordered && p.m <= kFew;
+    // Tiles of 64 rows read an adapter's weights a fourth as often; where an adapter has few rows, on average over all
+    // there are, most of such a tile's warps would have none.
+    l.many = p.m > kFew && p.m >= 24LL * p.adapters;
+    l.tile_rows = l.many ? kAdapterManyRows : kAdapterFewRows;
+    const int full = (p.m + l.tile_rows - 1) / l.tile_rows;
+    l.tiles = full + (p.adapters + 1 < p.m ? p.adapters + 1 : p.m);
+    l.clusters = l.few ? p.m : l.tiles;
+    // As many CTAs a tile as the SMs want, while each has some steps of 32 elements for its warps.
+    const int steps = ((k > n ? k : n) + 31) / 32;
+    l.size = 1;
+    while (l.size < 8 && steps >= 16 * l.size && (l.few ? 1 : full) * l.size < 3 * sm_count) l.size *= 2;
+    return l;
+}
+
+constexpr long long up16(long long v) { return (v + 15) / 16 * 16; }
+
+struct Workspace {
+    long long starts, order, tiles, dhidden, partial, bytes;
+    int chunks, chunk_rows;
+};
+
+// Chunks of rows for the weights' gradients: enough CTAs for the SMs, 128 rows each at least, and at most 2048, which
+// keeps the runs of additions in the matrix instruction's accumulators short.
+Workspace workspace_of(const AdapterProblem &p, bool gradient, int sm_count)
+{
+    Workspace w{};
+    const long long rows = p.m;
+    w.starts = 16;
+    w.order = w.starts + up16(4LL * (p.adapters + 2));
+    w.tiles = w.order + up16(4 * rows);
+    w.dhidden = w.tiles + 16LL * ((rows + kAdapterFewRows - 1) / kAdapterFewRows + p.adapters + 1);
+    w.bytes = w.dhidden;
+    if (gradient) {
+        const int columns = adapter_columns(p.rank);
+        const long long strips = (p.k + columns - 1) / columns + (p.n + columns - 1) / columns;
+        long long chunks = (4LL * sm_count + strips - 1) / strips;
+        if (chunks > (rows + 127) / 128) chunks = (rows + 127) / 128;
+        if (chunks < (rows + 2047) / 2048) chunks = (rows + 2047) / 2048;
+        if (chunks < 1) chunks = 1;
+        w.chunk_rows = (int)((rows + chunks - 1) / chunks);
+        if (w.chunk_rows < 1) w.chunk_rows = 1;
+        w.chunks = (int)((rows + w.chunk_rows - 1) / w.chunk_rows);
+        w.partial = w.dhidden + up16(4 * rows * p.rank);
+        w.bytes = w.partial + 8LL * w.chunks * p.rank * ((long long)p.k + p.n);
+    }
+    return w;
+}
+
+bool on_boundary(const void *p, long long stride, int element)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * element % 16 == 0;
+}
+
+cudaError_t products(const AdapterArgs &a, int dtype, bool transposed, const Layout &l, cudaStream_t stream)
+{
+    switch (dtype) {
+    case kF32: return adapter_products_launch<float>(a, transposed, l.many, l.clusters, l.size, stream);
+    case kBf16: return adapter_products_launch<__nv_bfloat16>(a, transposed, l.many, l.clusters, l.size, stream);
+    default: return adapter_products_launch<__half>(a, transposed, l.many, l.clusters, l.size, stream);
+    }
+}
+
+OrderArgs order_args(const AdapterProblem &p, const Workspace &w, const Layout &l, char *work)
+{
+    OrderArgs o{};
+    o.index = p.index;
+    o.tile_count = reinterpret_cast<int *>(work);
+    o.starts = reinterpret_cast<int *>(work + w.starts);
+    o.order = reinterpret_cast<int *>(work + w.order);
+    o.tiles = reinterpret_cast<AdapterTile *>(work + w.tiles);
+    o.m = p.m;
+    o.adapters = p.adapters;
+    o.tile_rows = l.tile_rows;
+    return o;
+}
+
+}  // namespace
+
+long long adapters_workspace_bytes(const AdapterProblem &p, bool gradient, int sm_count)
+{
+    if (!gradient && p.m <= kFew) return 0;
+    return workspace_of(p, gradient, sm_count).bytes;
+}
+
+cudaError_t adapters_launch(const AdapterProblem &p, int sm_count, cudaStream_t stream)
+{
+    const int size = dtype_size(p.dtype);
+    const Layout l = layout_of(p, false, p.k, p.n, sm_count);
+    AdapterArgs a{};
+    a.x = p.x.data;
+    a.x_stride = p.x.stride;
+    a.base = p.base.data;
+    a.base_stride = p.base.stride;
+    a.y = p.y.data;
+    a.y_stride = p.y.stride;
+    a.hidden = p.hidden_out;
+    a.w1 = p.a;
+    a.w2 = p.b;
+    a.scale = p.scale;
+    a.index = p.index;
+    a.m = p.m;
+    a.k = p.k;
+    a.n = p.n;
+    a.rank = p.rank;
+    a.adapters = p.adapters;
+    a.x_wide = p.k % 8 == 0 && on_boundary(p.x.data, p.x.stride, size);
+    a.w1_wide = p.k % 8 == 0 && on_boundary(p.a, 0, size);
+    a.w2_wide = p.rank % 4 == 0 && on_boundary(p.b, 0, size);
+    a.y_wide = p.n % 8 == 0 && on_boundary(p.y.data, p.y.stride, size) && on_boundary(p.base.data, p.base.stride, size);
+    if (!l.few) {
+        const Workspace w = workspace_of(p, false, sm_count);
+        const OrderArgs o = order_args(p, w, l, static_cast<char *>(p.workspace));
+        const cudaError_t e = order_launch(o, stream);
+        if (e != cudaSuccess) return e;
+        a.order = o.order;
+        a.tiles = o.tiles;
+        a.tile_count = o.tile_count;
+    }
+    return products(a, p.dtype, false, l, stream);
+}
+
+cudaError_t adapters_grad_launch(const AdapterProblem &p, int sm_count, cudaStream_t stream)
+{
+    const int size = dtype_size(p.dtype);
+    const Layout l = layout_of(p, true, p.n, p.k, sm_count);
+    const Workspace w = workspace_of(p, true, sm_count);
+    char *work = static_cast<char *>(p.workspace);
+    const OrderArgs o = order_args(p, w, l, work);
+    cudaError_t e = order_launch(o, stream);
+    if (e != cudaSuccess) return e;
+    // dhidden and dx: the two products with dy, B and A.
+    float *dhidden = reinterpret_cast<float *>(work + w.dhidden);
+    AdapterArgs a{};
+    a.x = p.dy.data;
+    a.x_stride = p.dy.stride;
+    a.base = p.base.data;
+    a.base_stride = p.base.stride;
+    a.y = p.y.data;
+    a.y_stride = p.y.stride;
+    a.hidden = dhidden;
+    a.w1 = p.b;
+    a.w2 = p.a;
+    a.scale = p.scale;
+    a.index = p.index;
+    a.order = o.order;
+    a.tiles = o.tiles;
+    a.tile_count = o.tile_count;
+    a.m = p.m;
+    a.k = p.n;
+    a.n = p.k;
+    a.rank = p.rank;
+    a.adapters = p.adapters;
+    const int near = adapter_rank_tiles(p.rank) < 4 ? 2 * adapter_rank_tiles(p.rank) : 8;  // ranks a lane loads at once
+    a.x_wide = p.n % 8 == 0 && on_boundary(p.dy.data, p.dy.stride, size);
+    a.w1_wide = p.rank % near == 0 && on_boundary(p.b, 0, size);
+    a.w2_wide = p.k % 4 == 0 && on_boundary(p.a, 0, size);
+    a.y_wide = p.k % 8 == 0 && on_boundary(p.y.data, p.y.stride, size) && on_boundary(p.base.data, p.base.stride, size);
+    e = products(a, p.dtype, true, l, stream);
+    if (e != cudaSuccess) return e;
+    AdapterGradArgs g{};
+    g.x = p.x.data;
+    g.x_stride = p.x.stride;
+    g.dy = p.dy.data;
+    g.dy_stride = p.dy.stride;
+    g.hidden = p.hidden;
+    g.dhidden = dhidden;
+    g.scale = p.scale;
+    g.order = o.order;
+    g.starts = o.starts;
+    g.da = p.da;
+    g.db = p.db;
+    g.partial = reinterpret_cast<float *>(work + w.partial);
+    g.k = p.k;
+    g.n = p.n;
+    g.rank = p.rank;
+    g.adapters = p.adapters;
+    g.chunks = w.chunks;
+    g.chunk_rows = w.chunk_rows;
+    g.x_wide = p.k % 8 == 0 && on_boundary(p.x.data, p.x.stride, size);
+    g.dy_wide = p.n % 8 == 0 && on_boundary(p.dy.data, p.dy.stride, size);
+    switch (p.dtype) {
+    case kF32: e = adapter_weights_launch<float>(g, stream); break;
+    case kBf16: e = adapter_weights_launch<__nv_bfloat16>(g, stream); break;
+    default: e = adapter_weights_launch<__half>(g, stream); break;
+    }
+    if (e != cudaSuccess) return e;
+    const long long blocks = ((long long)p.rank * ((long long)p.k + p.n) + 4 * kAdapterThreads - 1) / (4 * kAdapterThreads);
+    return launch_overlapped(adapter_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096), (unsigned)p.adapters),
+                             dim3(kAdapterThreads), 0, stream, 1, g);
+}
+
+}  // namespace cbs

@@ -1,0 +1,62 @@
+// adapters.h -- what the translation units of the low-rank adapters share (adapters.cu has the formulas).
+// Not part of the public interface.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "token_ops.h"
+
+namespace cbs {
+
+// Rows of one adapter that a group of CTAs takes: `count` positions from `first` on in the order by adapter.
+struct AdapterTile {
+    int adapter, first, count, unused;
+};
+
+// Two products after one another for each row, y = base + s (x W1) W2, W1 and W2 those of the row's adapter: forward
+// with x, A and B, and for the gradient of x with dy, B and A, whose memory is then the transposed one.
+struct AdapterArgs {
+    const void *x, *base;
+    void *y;
+    float *hidden;          // nullable [m][rank]: x W1
+    const void *w1, *w2;
+    const float *scale;     // nullable [adapters]
+    const int *index;       // [m]
+    const int *order;       // nullable: rows by adapter, with tiles and tile_count
+    const AdapterTile *tiles;
+    const int *tile_count;
+    long long x_stride, base_stride, y_stride;
+    int m, k, n, rank, adapters;
+    bool x_wide, w1_wide, w2_wide, y_wide;  // rows on the boundaries of wide loads and stores, and as long as they are
+};
+
+// Gradients of the adapters' weights: sums over the rows of each adapter.
+struct AdapterGradArgs {
+    const void *x, *dy;
+    const float *hidden, *dhidden;  // [m][rank]
+    const float *scale;             // nullable
+    const int *order, *starts;      // starts [adapters + 2]
+    float *da, *db;                 // [adapters][rank][k], [adapters][n][rank]
+    float *partial;                 // [2 * chunks][rank * (k + n)]
+    long long x_stride, dy_stride;
+    int k, n, rank, adapters;
+    int chunks, chunk_rows;
+    bool x_wide, dy_wide;
+};
+
+constexpr int kAdapterThreads = 256;
+constexpr int kAdapterFewRows = 16, kAdapterManyRows = 64;  // of a tile
+constexpr int kAdapterColumns = 64;                         // of a weight gradient's CTA, 32 for ranks above 32
+
+inline int adapter_rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
+inline int adapter_columns(int rank) { return rank <= 32 ? kAdapterColumns : kAdapterColumns / 2; }
+
+// By element type (adapters_*.cu).  `many`: tiles of 64 rows, else of 16.
+template <typename T>
+cudaError_t adapter_products_launch(const AdapterArgs &a, bool transposed, bool many, int clusters, int cluster_size,
+                                    cudaStream_t stream);
+template <typename T>
+cudaError_t adapter_weights_launch(const AdapterGradArgs &a, cudaStream_t stream);
+
+}  // namespace cbs

@@ -1,0 +1,667 @@
+// adapters_device.cuh -- kernels of the low-rank adapters, for one element type (adapters.cu has the formulas).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "adapters.h"
+#include "cbs_internal.h"
+#include "ptx.cuh"
+
+namespace cbs {
+namespace {
+
+// ------------------------------------------------------------------ matrix instructions
+// A warp's m16n8 product.  Lane l has g = l / 4 and t = l % 4; of the first operand it holds rows g and g + 8, of the
+// second column g, both at the K positions of t, and of the result rows g and g + 8 at columns 2t and 2t + 1.  Which
+// elements stand at t's positions is free as long as both operands agree: here neighbours in memory, eight of a
+// 32-element step (four of 16 for the second product), so that both operands come by wide loads from where they lie.
+__device__ __forceinline__ void mma16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                      __nv_bfloat16)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                      __half)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// fp32 as the sum of two of the instruction's 19-bit floats, to 2^-22 of it.
+struct Parts {
+    uint32_t hi, lo;
+};
+__device__ __forceinline__ Parts parts_of(float v)
+{
+    Parts p;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(p.hi) : "f"(v));
+    // Of infinities and NaN the first part alone: their difference with themselves would be NaN.
+    const float rest = fabsf(v) < __int_as_float(0x7f800000) ? v - __uint_as_float(p.hi) : 0.0f;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(p.lo) : "f"(rest));
+    return p;
+}
+// The same with both operands in two parts: three products, without that of the small parts.
+__device__ __forceinline__ void mma8_parts(float *c, Parts a0, Parts a1, Parts a2, Parts a3, Parts b0, Parts b1)
+{
+    mma8(c, a0.lo, a1.lo, a2.lo, a3.lo, b0.hi, b1.hi);
+    mma8(c, a0.hi, a1.hi, a2.hi, a3.hi, b0.lo, b1.lo);
+    mma8(c, a0.hi, a1.hi, a2.hi, a3.hi, b0.hi, b1.hi);
+}
+
+// ------------------------------------------------------------------ neighbours in memory
+__device__ __forceinline__ float widened(float v) { return v; }
+__device__ __forceinline__ float widened(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float widened(__half v) { return __half2float(v); }
+__device__ __forceinline__ void narrowed(float v, float *out) { *out = v; }
+__device__ __forceinline__ void narrowed(float v, __nv_bfloat16 *out) { *out = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void narrowed(float v, __half *out) { *out = __float2half_rn(v); }
+
+__device__ __forceinline__ uint32_t packed(float a, float b, __nv_bfloat16)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t packed(float a, float b, __half)
+{
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// N neighbours: words of two for the 16-bit types.
+template <typename T, int N>
+struct Near {
+    uint32_t w[N / 2];
+    __device__ __forceinline__ float at(int i) const { return widened(reinterpret_cast<const T *>(w)[i]); }
+};
+template <int N>
+struct Near<float, N> {
+    float w[N];
+    __device__ __forceinline__ float at(int i) const { return w[i]; }
+};
+
+// A load of what nothing writes while the kernel runs, or of what the same thread writes afterwards.
+template <bool KEPT, typename W>
+__device__ __forceinline__ W load(const W *p)
+{
+    if constexpr (KEPT) return __ldg(p);
+    else return *p;
+}
+
+// `have` of N neighbours from p on (none where it is 0 or less), zeros in the place of the others.  WIDE: N or none,
+// on a boundary of their size (16 bytes at most).
+template <bool WIDE, typename T, int N, bool KEPT = true>
+__device__ __forceinline__ Near<T, N> near(const T *p, int have)
+{
+    Near<T, N> v;
+    constexpr int kBytes = N * (int)sizeof(T);
+    if constexpr (WIDE) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(v.w);
+        if (have > 0) {
+            if constexpr (kBytes >= 16) {
+#pragma unroll
+                for (int i = 0; i < kBytes / 16; ++i) {
+                    const uint4 u = load<KEPT>(reinterpret_cast<const uint4 *>(p) + i);
+                    w[4 * i] = u.x;
+                    w[4 * i + 1] = u.y;
+                    w[4 * i + 2] = u.z;
+                    w[4 * i + 3] = u.w;
+                }
+            } else if constexpr (kBytes == 8) {
+                const uint2 u = load<KEPT>(reinterpret_cast<const uint2 *>(p));
+                w[0] = u.x;
+                w[1] = u.y;
+            } else {
+                w[0] = load<KEPT>(reinterpret_cast<const uint32_t *>(p));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kBytes / 4; ++i) w[i] = 0;
+        }
+    } else {
+        T *out = reinterpret_cast<T *>(v.w);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            T e;
+            narrowed(0.0f, &e);
+            if (i < have) e = p[i];
+            out[i] = e;
+        }
+    }
+    return v;
+}
+
+template <bool WIDE, typename T>
+__device__ __forceinline__ void store_near(T *p, const float *v, int have)
+{
+    if constexpr (WIDE) {
+        if (have <= 0) return;
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(packed(v[0], v[1], T()), packed(v[2], v[3], T()),
+                                                       packed(v[4], v[5], T()), packed(v[6], v[7], T()));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < have) narrowed(v[i], p + i);
+    }
+}
+
+// 32 elements of K: rows g (lo) and g + 8 (hi), column g, eight neighbours a lane.
+template <typename T>
+__device__ __forceinline__ void mma_eight(float *c, const Near<T, 8> &lo, const Near<T, 8> &hi, const Near<T, 8> &col)
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            mma8_parts(c, parts_of(lo.w[2 * s]), parts_of(hi.w[2 * s]), parts_of(lo.w[2 * s + 1]), parts_of(hi.w[2 * s + 1]),
+                       parts_of(col.w[2 * s]), parts_of(col.w[2 * s + 1]));
+    } else {
+        mma16(c, lo.w[0], hi.w[0], lo.w[1], hi.w[1], col.w[0], col.w[1], T());
+        mma16(c, lo.w[2], hi.w[2], lo.w[3], hi.w[3], col.w[2], col.w[3], T());
+    }
+}
+// 16 elements of K, four neighbours a lane.
+template <typename T>
+__device__ __forceinline__ void mma_four(float *c, const Near<T, 4> &lo, const Near<T, 4> &hi, const Near<T, 4> &col)
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            mma8_parts(c, parts_of(lo.w[2 * s]), parts_of(hi.w[2 * s]), parts_of(lo.w[2 * s + 1]), parts_of(hi.w[2 * s + 1]),
+                       parts_of(col.w[2 * s]), parts_of(col.w[2 * s + 1]));
+    } else {
+        mma16(c, lo.w[0], hi.w[0], lo.w[1], hi.w[1], col.w[0], col.w[1], T());
+    }
+}
+
+// N rows of N neighbours -> for each neighbour the N values of its rows, as the second operand wants them.
+template <typename T, int K, int N>
+__device__ __forceinline__ void turned(const Near<T, N> (&rows)[K], Near<T, K> (&out)[N])
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int i = 0; i < K; ++i) out[j].w[i] = rows[i].w[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int i = 0; i < K / 2; ++i)
+                out[j].w[i] = __byte_perm(rows[2 * i].w[j / 2], rows[2 * i + 1].w[j / 2], j % 2 ? 0x7632 : 0x5410);
+    }
+}
+
+// ------------------------------------------------------------------ clusters
+__device__ __forceinline__ uint32_t cluster_size()
+{
+    uint32_t v;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(v));
+    return v;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ float4 load_cluster(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// ------------------------------------------------------------------ y = base + s (x W1) W2
+// A cluster takes a tile of rows of one adapter.  Its CTAs share K for the first product and the output's columns
+// for the second; in between the partial sums [rows][rank] are added up through the cluster's shared memory, in the
+// same order by every CTA.  So x, base, y and, per tile, the weights go by once, and nothing goes through memory in
+// between.  In a CTA, WM warps share the rows, 16 each, and the others K or the columns.
+template <int RT>
+constexpr int hidden_pitch() { return RT == 1 ? 16 : 16 * RT + 16; }  // floats; 16-byte reads without bank conflicts
+template <int RT, int WM>
+constexpr int adapter_smem()
+{
+    constexpr int kRows = 16 * WM, kK = kAdapterThreads / 32 / WM;
+    return (kK + 1) * kRows * hidden_pitch<RT>() * 4;
+}
+
+template <typename T, int RT, int WM, bool TURNED, bool WIDE>
+__global__ void __launch_bounds__(kAdapterThreads, RT <= 2 ? 2 : 1) adapter_products_kernel(const AdapterArgs a)
+{
+    constexpr int kRows = 16 * WM, kWarps = kAdapterThreads / 32, kSplit = kWarps / WM, kPitch = hidden_pitch<RT>();
+    extern __shared__ __align__(16) float adapter_sums[];  // [kSplit][kRows][kPitch] partial sums, then [kRows][kPitch] whole ones
+    __shared__ int rows[kRows];
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int part = (int)dev::cluster_ctarank(), parts = (int)cluster_size();
+    const int tile = (int)blockIdx.x / parts;
+    int adapter, count;
+    if (a.tiles) {
+        if (tile >= *a.tile_count) return;
+        const AdapterTile my = a.tiles[tile];
+        adapter = my.adapter;
+        count = my.count;
+        if ((int)threadIdx.x < count) rows[threadIdx.x] = a.order[my.first + threadIdx.x];
+    } else {
+        // Few rows: a cluster for each.  Those whose row is the first, or the 17th and so on, of its adapter take it and
+        // the next ones of the adapter; the others have nothing to do.
+        __shared__ int before_warp[kWarps];
+        auto of = [&](int i) {
+            const int v = a.index[i];
+            return v < 0 || v >= a.adapters ? a.adapters : v;
+        };
+        adapter = of(tile);
+        const int i = threadIdx.x;
+        const bool same = i < a.m && of(i) == adapter;
+        const int before = __syncthreads_count(same && i < tile);
+        if (before % kRows != 0) return;
+        const unsigned mine = __ballot_sync(0xffffffffu, same && i >= tile);
+        if (lane == 0) before_warp[warp] = __popc(mine);
+        __syncthreads();
+        int rank = __popc(mine & ((1u << lane) - 1));
+        count = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) rank += before_warp[w];
+            count += before_warp[w];
+        }
+        if (same && i >= tile && rank < kRows) rows[rank] = i;
+        count = count < kRows ? count : kRows;
+    }
+    __syncthreads();
+    const bool live = adapter < a.adapters;
+    const int wm = warp % WM, ws = warp / WM;
+    const int row_lo = 16 * wm + g, row_hi = row_lo + 8;
+    const bool has_lo = row_lo < count, has_hi = row_hi < count;
+    const long long at_lo = has_lo ? rows[row_lo] : 0, at_hi = has_hi ? rows[row_hi] : 0;
+    float *whole = adapter_sums + kSplit * kRows * kPitch;
+
+    if (live) {
+        const T *x_lo = static_cast<const T *>(a.x) + at_lo * a.x_stride, *x_hi = static_cast<const T *>(a.x) + at_hi * a.x_stride;
+        const T *w1 = static_cast<const T *>(a.w1) + (long long)adapter * a.rank * a.k;
+        float acc[2 * RT][4] = {};
+        const int steps = (a.k + 31) / 32, from = (int)((long long)steps * part / parts), to = (int)((long long)steps * (part + 1) / parts);
+        // This warp's rows may all be beyond the tile's.
+        if (16 * wm < count) {
+#pragma unroll 2
+            for (int s = from + ws; s < to; s += kSplit) {
+                const int k0 = 32 * s + 8 * t, have = a.k - k0;
+                const Near<T, 8> lo = near<WIDE, T, 8>(x_lo + k0, has_lo ? have : 0);
+                const Near<T, 8> hi = near<WIDE, T, 8>(x_hi + k0, has_hi ? have : 0);
+                if constexpr (!TURNED) {
+                    // W1 is [rank][k]: column j's values are neighbours.
+#pragma unroll
+                    for (int j = 0; j < 2 * RT; ++j) {
+                        const int r = 8 * j + g;
+                        mma_eight<T>(acc[j], lo, hi, near<WIDE, T, 8>(w1 + (long long)r * a.k + k0, r < a.rank ? have : 0));
+                    }
+                } else {
+                    // W1 is [k][rank]: a lane loads its columns' neighbours in its eight rows, and turns them.
+                    constexpr int kC = 2 * RT < 8 ? 2 * RT : 8;  // columns at a time
+#pragma unroll
+                    for (int c = 0; c < 2 * RT; c += kC) {
+                        const int r = 2 * RT * g + c;
+                        Near<T, kC> in[8];
+                        Near<T, 8> col[kC];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            in[i] = near<WIDE, T, kC>(w1 + (long long)(k0 + i) * a.rank + r, i < have ? a.rank - r : 0);
+                        turned<T, 8, kC>(in, col);
+#pragma unroll
+                        for (int j = 0; j < kC; ++j) mma_eight<T>(acc[c + j], lo, hi, col[j]);
+                    }
+                }
+            }
+        }
+        float *mine = adapter_sums + (ws * kRows + 16 * wm) * kPitch;
+#pragma unroll
+        for (int j = 0; j < 2 * RT; ++j) {
+            const int r0 = TURNED ? 2 * RT * (2 * t) + j : 8 * j + 2 * t, r1 = TURNED ? 2 * RT * (2 * t + 1) + j : r0 + 1;
+            mine[g * kPitch + r0] = acc[j][0];
+            mine[g * kPitch + r1] = acc[j][1];
+            mine[(g + 8) * kPitch + r0] = acc[j][2];
+            mine[(g + 8) * kPitch + r1] = acc[j][3];
+        }
+        __syncthreads();
+        constexpr int kQuads = 4 * RT;  // of a row
+        if constexpr (kSplit > 1) {
+            for (int i = threadIdx.x; i < kRows * kQuads; i += kAdapterThreads) {
+                float4 *at = reinterpret_cast<float4 *>(adapter_sums + i / kQuads * kPitch) + i % kQuads;
+                float4 v = *at;
+                for (int s = 1; s < kSplit; ++s) {
+                    const float4 u = at[s * kRows * kPitch / 4];
+                    v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+                }
+                *at = v;
+            }
+        }
+        cluster_arrive();
+        cluster_wait();
+        const uint32_t sums = dev::smem_u32(adapter_sums);
+        for (int i = threadIdx.x; i < kRows * kQuads; i += kAdapterThreads) {
+            const int offset = i / kQuads * kPitch + i % kQuads * 4;
+            float4 v = load_cluster(dev::mapa_cluster(sums + 4 * offset, 0));
+            for (int p = 1; p < parts; ++p) {
+                const float4 u = load_cluster(dev::mapa_cluster(sums + 4 * offset, (uint32_t)p));
+                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            }
+            *reinterpret_cast<float4 *>(whole + offset) = v;
+        }
+        __syncthreads();
+        cluster_arrive();  // nobody leaves before all have read its sums: waited for at the end
+    }
+    if (a.hidden) {
+        for (int i = threadIdx.x; i < count * a.rank; i += kAdapterThreads) {
+            const int row = i / a.rank;
+            if (row % parts == part)
+                a.hidden[(long long)rows[row] * a.rank + i % a.rank] = live ? whole[row * kPitch + i % a.rank] : 0.0f;
+        }
+    }
+    if (16 * wm < count && (live || a.base != a.y)) {
+        // Rows of the first operand.  16-bit: rounded once more to the activations' type, whose rounding of y it stays
+        // below; f16, whose range the sums may leave, after division by a power of two near the row's largest.
+        Near<T, 4> h_lo[RT], h_hi[RT];
+        float s_lo = live ? (a.scale ? a.scale[adapter] : 1.0f) : 0.0f, s_hi = s_lo;
+        if (live) {
+            float4 v_lo[RT], v_hi[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                v_lo[i] = *reinterpret_cast<const float4 *>(whole + row_lo * kPitch + 16 * i + 4 * t);
+                v_hi[i] = *reinterpret_cast<const float4 *>(whole + row_hi * kPitch + 16 * i + 4 * t);
+            }
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    h_lo[i].w[0] = v_lo[i].x, h_lo[i].w[1] = v_lo[i].y, h_lo[i].w[2] = v_lo[i].z, h_lo[i].w[3] = v_lo[i].w;
+                    h_hi[i].w[0] = v_hi[i].x, h_hi[i].w[1] = v_hi[i].y, h_hi[i].w[2] = v_hi[i].z, h_hi[i].w[3] = v_hi[i].w;
+                }
+            } else {
+                auto narrow = [&](const float4 *v, Near<T, 4> *h, float *s) {
+                    float factor = 1.0f;
+                    if constexpr (sizeof(T) == 2) {
+                        T probe;
+                        narrowed(1e30f, &probe);
+                        if (isinf(widened(probe))) {  // f16, known when it is compiled
+                            float most = 0.0f;
+#pragma unroll
+                            for (int i = 0; i < RT; ++i)
+                                most = fmaxf(most, fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
+                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                            int e = (int)(__float_as_uint(most) >> 23);  // 127 + its exponent; 255 where it is infinite
+                            e = e < 2 ? 2 : e > 252 ? 252 : e;
+                            factor = __uint_as_float((unsigned)(254 - e) << 23);
+                            *s *= __uint_as_float((unsigned)e << 23);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        h[i].w[0] = packed(v[i].x * factor, v[i].y * factor, T());
+                        h[i].w[1] = packed(v[i].z * factor, v[i].w * factor, T());
+                    }
+                };
+                narrow(v_lo, h_lo, &s_lo);
+                narrow(v_hi, h_hi, &s_hi);
+            }
+        }
+        const T *w2 = static_cast<const T *>(a.w2) + (live ? (long long)adapter * a.rank * a.n : 0);
+        const T *b_lo = static_cast<const T *>(a.base) + at_lo * a.base_stride, *b_hi = static_cast<const T *>(a.base) + at_hi * a.base_stride;
+        T *y_lo = static_cast<T *>(a.y) + at_lo * a.y_stride, *y_hi = static_cast<T *>(a.y) + at_hi * a.y_stride;
+        const int steps = (a.n + 31) / 32, from = (int)((long long)steps * part / parts), to = (int)((long long)steps * (part + 1) / parts);
+#pragma unroll 2
+        for (int s = from + ws; s < to; s += kSplit) {
+            // Of 32 columns: as the second operand the lane's are 4g to 4g + 3, as the result 8t to 8t + 7.
+            const int n0 = 32 * s + 8 * t, have = a.n - n0;
+            Near<T, 8> old_lo, old_hi;
+            if (a.base) {
+                old_lo = near<WIDE, T, 8, false>(b_lo + n0, has_lo ? have : 0);
+                old_hi = near<WIDE, T, 8, false>(b_hi + n0, has_hi ? have : 0);
+            }
+            float acc[4][4] = {};
+            if (live) {
+                const int c0 = 32 * s + 4 * g;
+                if constexpr (!TURNED) {
+                    // W2 is [n][rank].
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int i = 0; i < RT; ++i)
+                            mma_four<T>(acc[q], h_lo[i], h_hi[i],
+                                        near<WIDE, T, 4>(w2 + (long long)(c0 + q) * a.rank + 16 * i + 4 * t,
+                                                         c0 + q < a.n ? a.rank - 16 * i - 4 * t : 0));
+                } else {
+                    // W2 is [rank][n].
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) {
+                        Near<T, 4> in[4], col[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int r = 16 * i + 4 * t + j;
+                            in[j] = near<WIDE, T, 4>(w2 + (long long)r * a.n + c0, r < a.rank ? a.n - c0 : 0);
+                        }
+                        turned<T, 4, 4>(in, col);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mma_four<T>(acc[q], h_lo[i], h_hi[i], col[q]);
+                    }
+                }
+            }
+            float v_lo[8], v_hi[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                v_lo[q] = acc[q][0] * s_lo;
+                v_lo[4 + q] = acc[q][1] * s_lo;
+                v_hi[q] = acc[q][2] * s_hi;
+                v_hi[4 + q] = acc[q][3] * s_hi;
+            }
+            if (a.base) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v_lo[j] = live ? old_lo.at(j) + v_lo[j] : old_lo.at(j);
+                    v_hi[j] = live ? old_hi.at(j) + v_hi[j] : old_hi.at(j);
+                }
+            }
+            if (has_lo) store_near<WIDE, T>(y_lo + n0, v_lo, have);
+            if (has_hi) store_near<WIDE, T>(y_hi + n0, v_hi, have);
+        }
+    }
+    if (live) cluster_wait();
+}
+
+// ------------------------------------------------------------------ gradients of the weights
+// Sums over an adapter's rows of outer products, [columns][rank]: a CTA takes a strip of columns of x (for dA) or dy
+// (for dB) and a chunk of the rows in the order by adapter, its warps 16 rows at a time in turn.  A lane loads eight
+// neighbouring columns (four for large ranks) of four rows, and turns them into the first operand; the second, the
+// small rows, comes as fp32 in two parts, so that the sums keep fp32's bits.  An adapter within the chunk is written
+// as it is, one that reaches beyond it into the chunk's two rows of partial sums, which adapter_join_kernel adds up
+// in order.
+template <typename T, int RT, bool WIDE>
+__global__ void __launch_bounds__(kAdapterThreads, RT <= 4 ? 2 : 1) adapter_weights_kernel(const AdapterGradArgs a)
+{
+    constexpr int kColumns = RT <= 2 ? 64 : 32, kNear = kColumns / 8, kWarps = kAdapterThreads / 32, kRank = 16 * RT;
+    __shared__ float sums[kColumns][kRank + 1];
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int x_strips = (a.k + kColumns - 1) / kColumns;
+    const bool of_x = (int)blockIdx.x < x_strips;
+    const int column0 = ((int)blockIdx.x - (of_x ? 0 : x_strips)) * kColumns, width = of_x ? a.k : a.n;
+    const T *data = static_cast<const T *>(of_x ? a.x : a.dy);
+    const long long stride = of_x ? a.x_stride : a.dy_stride;
+    const float *small = of_x ? a.dhidden : a.hidden;
+    const int chunk = blockIdx.y, valid = a.starts[a.adapters];
+    int at = chunk * a.chunk_rows;
+    const int stop = at + a.chunk_rows < valid ? at + a.chunk_rows : valid;
+    const int my_column = column0 + kNear * g, have = width - my_column;
+    while (at < stop) {
+        // The adapter of position `at`: as many as end at or before it come first.
+        int adapter = 0;
+        for (int i = 0; i < a.adapters; i += kAdapterThreads)
+            adapter += __syncthreads_count(i + (int)threadIdx.x < a.adapters && a.starts[i + threadIdx.x + 1] <= at);
+        const int first = a.starts[adapter], last = a.starts[adapter + 1], end = last < stop ? last : stop;
+        float acc[kNear / 2][2 * RT][4] = {};
+        for (int p = at + 16 * warp; p < end; p += 16 * kWarps) {
+            int row[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) row[i] = p + 4 * t + i < end ? a.order[p + 4 * t + i] : -1;
+            Near<T, kNear> in[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                in[i] = near<WIDE, T, kNear>(data + (row[i] < 0 ? 0 : row[i] * stride + my_column), row[i] < 0 ? 0 : have);
+            float h[2 * RT][4];
+#pragma unroll
+            for (int j = 0; j < 2 * RT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    h[j][i] = row[i] >= 0 && 8 * j + g < a.rank ? __ldg(small + (long long)row[i] * a.rank + 8 * j + g) : 0.0f;
+            if constexpr (sizeof(T) == 2 && __is_same(T, __nv_bfloat16)) {
+                Near<T, 4> col[kNear];
+                turned<T, 4, kNear>(in, col);
+#pragma unroll
+                for (int j = 0; j < 2 * RT; ++j) {
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float u = h[j][2 * i], v = h[j][2 * i + 1];
+                        hi[i] = packed(u, v, T());
+                        const float most = __int_as_float(0x7f800000);  // of infinities and NaN the first part alone
+                        lo[i] = packed(fabsf(u) < most ? u - __uint_as_float(hi[i] << 16) : 0.0f,
+                                       fabsf(v) < most ? v - __uint_as_float(hi[i] & 0xffff0000u) : 0.0f, T());
+                    }
+#pragma unroll
+                    for (int c = 0; c < kNear / 2; ++c) {
+                        mma16(acc[c][j], col[2 * c].w[0], col[2 * c + 1].w[0], col[2 * c].w[1], col[2 * c + 1].w[1], lo[0], lo[1], T());
+                        mma16(acc[c][j], col[2 * c].w[0], col[2 * c + 1].w[0], col[2 * c].w[1], col[2 * c + 1].w[1], hi[0], hi[1], T());
+                    }
+                }
+            } else {
+                // f16 and f32 in the 19-bit floats, which hold an f16 exactly.
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int j = 0; j < 2 * RT; ++j) {
+                        const Parts b0 = parts_of(h[j][2 * s]), b1 = parts_of(h[j][2 * s + 1]);
+#pragma unroll
+                        for (int c = 0; c < kNear / 2; ++c) {
+                            const float v0 = in[2 * s].at(2 * c), v1 = in[2 * s].at(2 * c + 1), v2 = in[2 * s + 1].at(2 * c),
+                                        v3 = in[2 * s + 1].at(2 * c + 1);
+                            if constexpr (sizeof(T) == 4) {
+                                mma8_parts(acc[c][j], parts_of(v0), parts_of(v1), parts_of(v2), parts_of(v3), b0, b1);
+                            } else {
+                                const uint32_t a0 = __float_as_uint(v0), a1 = __float_as_uint(v1), a2 = __float_as_uint(v2),
+                                               a3 = __float_as_uint(v3);
+                                mma8(acc[c][j], a0, a1, a2, a3, b0.lo, b1.lo);
+                                mma8(acc[c][j], a0, a1, a2, a3, b0.hi, b1.hi);
+                            }
+                        }
+                    }
+            }
+        }
+        // The warps' sums, in their order.
+        for (int w = 0; w < kWarps; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int c = 0; c < kNear / 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 2 * RT; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float *to = &sums[kNear * g + 2 * c + e / 2][8 * j + 2 * t + e % 2];
+                            *to = w ? *to + acc[c][j][e] : acc[c][j][e];
+                        }
+            }
+            __syncthreads();
+        }
+        const float s = a.scale ? a.scale[adapter] : 1.0f;
+        const bool whole = first >= chunk * a.chunk_rows && last <= stop;
+        float *out = of_x ? a.da + (long long)adapter * a.rank * a.k : a.db + (long long)adapter * a.rank * a.n;
+        if (!whole) {
+            out = a.partial + (2LL * chunk + (first >= chunk * a.chunk_rows)) * a.rank * ((long long)a.k + a.n);
+            if (!of_x) out += (long long)a.rank * a.k;
+        }
+        const int columns = width - column0 < kColumns ? width - column0 : kColumns;
+        if (of_x) {
+            for (int i = threadIdx.x; i < a.rank * kColumns; i += kAdapterThreads)
+                if (i % kColumns < columns) out[(long long)(i / kColumns) * a.k + column0 + i % kColumns] = s * sums[i % kColumns][i / kColumns];
+        } else {
+            for (int i = threadIdx.x; i < columns * a.rank; i += kAdapterThreads)
+                out[(long long)column0 * a.rank + i] = s * sums[i / a.rank][i % a.rank];
+        }
+        __syncthreads();
+        at = end;
+    }
+}
+
+// ------------------------------------------------------------------ launches
+template <typename T, int RT, int WM, bool TURNED, bool WIDE>
+cudaError_t products_launch(const AdapterArgs &a, int clusters, int cluster_size, cudaStream_t stream)
+{
+    constexpr int kSmem = adapter_smem<RT, WM>();
+    static bool allowed[kMaxDevices] = {};
+    if (kSmem > 46 * 1024) {
+        const cudaError_t e = allow_dynamic_smem(adapter_products_kernel<T, RT, WM, TURNED, WIDE>, kSmem, allowed);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_overlapped(adapter_products_kernel<T, RT, WM, TURNED, WIDE>, dim3((unsigned)clusters * (unsigned)cluster_size),
+                             dim3(kAdapterThreads), kSmem, stream, cluster_size, a);
+}
+
+template <typename T, int RT, int WM>
+cudaError_t products_pick(const AdapterArgs &a, bool turned, int clusters, int cluster_size, cudaStream_t stream)
+{
+    const bool wide = a.x_wide && a.w1_wide && a.w2_wide && a.y_wide;
+    if (turned)
+        return wide ? products_launch<T, RT, WM, true, true>(a, clusters, cluster_size, stream)
+                    : products_launch<T, RT, WM, true, false>(a, clusters, cluster_size, stream);
+    return wide ? products_launch<T, RT, WM, false, true>(a, clusters, cluster_size, stream)
+                : products_launch<T, RT, WM, false, false>(a, clusters, cluster_size, stream);
+}
+
+template <typename T, int RT>
+cudaError_t weights_launch(const AdapterGradArgs &a, cudaStream_t stream)
+{
+    const int columns = adapter_columns(a.rank);
+    const dim3 grid((unsigned)((a.k + columns - 1) / columns + (a.n + columns - 1) / columns), (unsigned)a.chunks);
+    return a.x_wide && a.dy_wide
+               ? launch_overlapped(adapter_weights_kernel<T, RT, true>, grid, dim3(kAdapterThreads), 0, stream, 1, a)
+               : launch_overlapped(adapter_weights_kernel<T, RT, false>, grid, dim3(kAdapterThreads), 0, stream, 1, a);
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t adapter_products_launch(const AdapterArgs &a, bool transposed, bool many, int clusters, int cluster_size,
+                                    cudaStream_t stream)
+{
+    constexpr int kMany = kAdapterManyRows / 16;
+    switch (adapter_rank_tiles(a.rank)) {
+    case 1: return many ? products_pick<T, 1, kMany>(a, transposed, clusters, cluster_size, stream) : products_pick<T, 1, 1>(a, transposed, clusters, cluster_size, stream);
+    case 2: return many ? products_pick<T, 2, kMany>(a, transposed, clusters, cluster_size, stream) : products_pick<T, 2, 1>(a, transposed, clusters, cluster_size, stream);
+    case 4: return many ? products_pick<T, 4, kMany>(a, transposed, clusters, cluster_size, stream) : products_pick<T, 4, 1>(a, transposed, clusters, cluster_size, stream);
+    default: return many ? products_pick<T, 8, kMany>(a, transposed, clusters, cluster_size, stream) : products_pick<T, 8, 1>(a, transposed, clusters, cluster_size, stream);
+    }
+}
+
+template <typename T>
+cudaError_t adapter_weights_launch(const AdapterGradArgs &a, cudaStream_t stream)
+{
+    switch (adapter_rank_tiles(a.rank)) {
+    case 1: return weights_launch<T, 1>(a, stream);
+    case 2: return weights_launch<T, 2>(a, stream);
+    case 4: return weights_launch<T, 4>(a, stream);
+    default: return weights_launch<T, 8>(a, stream);
+    }
+}
+
+}  // namespace cbs

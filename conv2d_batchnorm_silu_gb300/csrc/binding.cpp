@@ -452,6 +452,117 @@ PyObject *rms_norm_backward(PyObject *, PyObject *const *arg, Py_ssize_t count)
     });
 }
 
+// What both calls of the adapters share: x, index, a, b and scale.
+struct Adapters {
+    Rows x;
+    const int *index;
+    const void *a, *b;
+    const float *scale;
+    long long m, k, n, rank, adapters;
+    int type;
+    Adapters(PyObject *px, PyObject *pindex, PyObject *pa, PyObject *pb, PyObject *pscale, int device)
+    {
+        const at::Tensor &tx = tensor(px, "x"), &ti = tensor(pindex, "index"), &ta = tensor(pa, "a"), &tb = tensor(pb, "b");
+        type = activation_type(tx, "x");
+        x = rows_of(tx, "x", device);
+        m = x.rows;
+        k = x.c;
+        has_type(ti, at::kInt, "index");
+        if (!ti.is_cuda() || ti.get_device() != device || ti.numel() != m || !ti.is_contiguous())
+            wrong_value("index must hold " + std::to_string(m) + " dense elements on the CUDA device of the call's first tensor");
+        has_type(ta, tx.scalar_type(), "a");
+        has_type(tb, tx.scalar_type(), "b");
+        same_device(ta, "a", device);
+        same_device(tb, "b", device);
+        if (ta.dim() != 3 || ta.size(2) != k) wrong_value("a must be [adapters, rank, " + std::to_string(k) + "], got " + shape_text(ta.sizes()));
+        adapters = ta.size(0);
+        rank = ta.size(1);
+        if (tb.dim() != 3 || tb.size(0) != adapters || tb.size(2) != rank)
+            wrong_value("b must be [" + std::to_string(adapters) + ", n, " + std::to_string(rank) + "], got " + shape_text(tb.sizes()));
+        n = tb.size(1);
+        if (!ta.is_contiguous() || !tb.is_contiguous()) wrong_value("a and b must be dense");
+        if (n > INT32_MAX || rank > INT32_MAX || adapters > INT32_MAX) throw Status{CBS_ERR_INVALID_ARG};
+        index = ti.const_data_ptr<int>();
+        a = ta.const_data_ptr();
+        b = tb.const_data_ptr();
+        scale = vector_of(pscale, adapters, "scale", device);
+    }
+};
+
+// A tensor of x's type and the given shape.
+Rows rows_shaped(PyObject *o, at::ScalarType type, at::IntArrayRef shape, const char *name, int device)
+{
+    const at::Tensor &t = tensor(o, name);
+    has_type(t, type, name);
+    if (t.sizes() != shape)
+        wrong_value(std::string(name) + " has shape " + shape_text(t.sizes()) + ", expected " + shape_text(shape));
+    return rows_of(t, name, device);
+}
+
+// (x, index, a, b, scale, base, return_hidden, y, stream) -> y or (y, hidden)
+PyObject *linear_adapters(PyObject *, PyObject *const *arg, Py_ssize_t count)
+{
+    return guarded(count, 9, [&]() -> PyObject * {
+        const at::Tensor &x = tensor(arg[0], "x");
+        const int device = first_device(x, "x");
+        const Adapters p(arg[0], arg[1], arg[2], arg[3], arg[4], device);
+        const int with_hidden = PyObject_IsTrue(arg[6]);
+        if (with_hidden < 0) return nullptr;
+        c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
+        shape.back() = p.n;
+        Rows base{nullptr, 0, 0, 0};
+        if (arg[5] != Py_None) base = rows_shaped(arg[5], x.scalar_type(), shape, "base", device);
+        const long long need = conv_bn_silu_linear_adapters_workspace(p.m, (int)p.k, (int)p.n, (int)p.rank, (int)p.adapters);
+        if (need < 0) throw Status{CBS_ERR_INVALID_ARG};
+        const Stream stream(arg[8], device);
+        const at::Tensor y = output(arg[7], shape, x.scalar_type(), "y", stream);
+        const Rows ry = rows_of(y, "y", device);
+        at::Tensor hidden, work;
+        if (with_hidden) {
+            shape.back() = p.rank;
+            hidden = stream.empty(shape, at::kFloat);
+        }
+        if (need) work = stream.empty({need}, at::kByte);
+        check(conv_bn_silu_linear_adapters(p.x.data, p.x.distance, p.index, p.a, p.b, p.scale, base.data, base.distance,
+                                           ry.data, ry.distance, with_hidden ? hidden.data_ptr<float>() : nullptr, p.m,
+                                           (int)p.k, (int)p.n, (int)p.rank, (int)p.adapters, p.type,
+                                           need ? work.data_ptr() : nullptr, need, stream.handle));
+        return with_hidden ? pair(y, hidden) : THPVariable_Wrap(y);
+    });
+}
+
+// (dy, x, index, a, b, scale, hidden, base, dx, stream) -> (dx, da, db)
+PyObject *linear_adapters_backward(PyObject *, PyObject *const *arg, Py_ssize_t count)
+{
+    return guarded(count, 10, [&]() -> PyObject * {
+        const at::Tensor &x = tensor(arg[1], "x");
+        const int device = first_device(x, "x");
+        const Adapters p(arg[1], arg[2], arg[3], arg[4], arg[5], device);
+        c10::SmallVector<int64_t, 6> shape(x.sizes().begin(), x.sizes().end());
+        shape.back() = p.n;
+        const Rows dy = rows_shaped(arg[0], x.scalar_type(), shape, "dy", device);
+        const float *hidden = vector_of(arg[6], p.m * p.rank, "hidden", device);
+        if (!hidden && arg[6] == Py_None) wrong_type("hidden must be a torch.Tensor");
+        Rows base{nullptr, 0, 0, 0};
+        if (arg[7] != Py_None) base = rows_shaped(arg[7], x.scalar_type(), x.sizes(), "base", device);
+        const long long need =
+            conv_bn_silu_linear_adapters_backward_workspace(p.m, (int)p.k, (int)p.n, (int)p.rank, (int)p.adapters);
+        if (need < 0) throw Status{CBS_ERR_INVALID_ARG};
+        const Stream stream(arg[9], device);
+        const at::Tensor dx = output(arg[8], x.sizes(), x.scalar_type(), "dx", stream);
+        const Rows rdx = rows_of(dx, "dx", device);
+        const at::Tensor da = stream.empty({p.adapters, p.rank, p.k}, at::kFloat);
+        const at::Tensor db = stream.empty({p.adapters, p.n, p.rank}, at::kFloat);
+        const at::Tensor work = stream.empty({need}, at::kByte);
+        check(conv_bn_silu_linear_adapters_backward(dy.data, dy.distance, p.x.data, p.x.distance, p.index, p.a, p.b, p.scale,
+                                                    hidden, base.data, base.distance, rdx.data, rdx.distance,
+                                                    da.data_ptr<float>(), db.data_ptr<float>(), p.m, (int)p.k, (int)p.n,
+                                                    (int)p.rank, (int)p.adapters, p.type, work.data_ptr(), need,
+                                                    stream.handle));
+        return tuple_of({dx, da, db});
+    });
+}
+
 // A list or tuple of tensors.
 struct Tensors {
     PyObject *fast = nullptr;
@@ -551,7 +662,8 @@ PyObject *adamw_step(PyObject *, PyObject *const *arg, Py_ssize_t count)
 
 #define CALL(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {CALL(layer_norm), CALL(layer_norm_backward), CALL(quantize_rows), CALL(layer_norm_quantize),
-                           CALL(linear_int8), CALL(rms_norm), CALL(rms_norm_backward), CALL(adamw_step),
+                           CALL(linear_int8), CALL(rms_norm), CALL(rms_norm_backward), CALL(linear_adapters),
+                           CALL(linear_adapters_backward), CALL(adamw_step),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_token_ops", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

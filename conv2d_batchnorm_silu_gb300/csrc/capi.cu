@@ -276,6 +276,27 @@ int rms_norm_call(const void *x, long long x_stride, const void *residual, long 
     return e == cudaSuccess ? CBS_OK : cuda_fail(e);
 }
 
+bool adapter_sizes_ok(long long m, int k, int n, int rank, int adapters, int dtype)
+{
+    return m >= 0 && m <= cbs::kMostAdapterRows && k >= 1 && k <= (1 << 22) && n >= 1 && n <= (1 << 22) && rank >= 1 &&
+           rank <= cbs::kMostRank && adapters >= 1 && adapters <= cbs::kMostAdapters && dtype >= CBS_DTYPE_F32 &&
+           dtype <= CBS_DTYPE_F16;
+}
+
+long long adapter_workspace(long long m, int k, int n, int rank, int adapters, bool gradient)
+{
+    if (!adapter_sizes_ok(m, k, n, rank, adapters, CBS_DTYPE_F32)) return -1;
+    int sms = 0;
+    if (sm_count_current_device(&sms) != CBS_OK) return -1;
+    cbs::AdapterProblem p{};
+    p.m = (int)m;
+    p.k = k;
+    p.n = n;
+    p.rank = rank;
+    p.adapters = adapters;
+    return cbs::adapters_workspace_bytes(p, gradient, sms);
+}
+
 bool linear_sizes_ok(long long m, int n, int k)
 {
     // Sums of k products of -128 * -128 fit 32-bit integers; tile counts fit 32 bits.
@@ -771,6 +792,110 @@ int conv_bn_silu_rms_norm_backward(const void *dy, long long dy_stride, const vo
     p.c = c;
     p.dtype = dtype;
     cudaError_t e = cbs::rms_norm_grad_launch(p, sms, strm);
+    return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+}
+
+long long conv_bn_silu_linear_adapters_workspace(long long m, int k, int n, int rank, int adapters)
+{
+    return adapter_workspace(m, k, n, rank, adapters, false);
+}
+
+long long conv_bn_silu_linear_adapters_backward_workspace(long long m, int k, int n, int rank, int adapters)
+{
+    return adapter_workspace(m, k, n, rank, adapters, true);
+}
+
+int conv_bn_silu_linear_adapters(const void *x, long long x_stride, const int *index, const void *a, const void *b,
+                                 const float *scale, const void *base, long long base_stride, void *y,
+                                 long long y_stride, float *hidden, long long m, int k, int n, int rank,
+                                 int adapters, int dtype, void *workspace, long long workspace_bytes, void *stream)
+{
+    if (!adapter_sizes_ok(m, k, n, rank, adapters, dtype)) return CBS_ERR_INVALID_ARG;
+    if (m == 0) return CBS_OK;
+    const int size = cbs::dtype_size(dtype);
+    int st = check_rows(x, m, k, x_stride, size, false);
+    if (st == CBS_OK && base) st = check_rows(base, m, n, base_stride, size, false);
+    if (st == CBS_OK) st = check_rows(y, m, n, y_stride, size, true);
+    if (st != CBS_OK) return st;
+    if (!index || !a || !b || !same_or_apart(base, base_stride, y, y_stride, m)) return CBS_ERR_INVALID_ARG;
+    if (!aligned_to(index, 4) || !aligned_to(a, size) || !aligned_to(b, size) || !aligned_to(scale, 4) ||
+        !aligned_to(hidden, 4) || !aligned16(workspace))
+        return CBS_ERR_MISALIGNED;
+    int sms = 0;
+    st = sm_count_current_device(&sms);
+    if (st != CBS_OK) return st;
+    cbs::AdapterProblem p{};
+    p.x = cbs::Rows{const_cast<void *>(x), x_stride};
+    p.base = cbs::Rows{const_cast<void *>(base), base_stride};
+    p.y = cbs::Rows{y, y_stride};
+    p.index = index;
+    p.a = a;
+    p.b = b;
+    p.scale = scale;
+    p.hidden_out = hidden;
+    p.m = (int)m;
+    p.k = k;
+    p.n = n;
+    p.rank = rank;
+    p.adapters = adapters;
+    p.dtype = dtype;
+    p.workspace = workspace;
+    const long long need = cbs::adapters_workspace_bytes(p, false, sms);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return CBS_ERR_INVALID_ARG;
+    cudaError_t e = cbs::adapters_launch(p, sms, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+}
+
+int conv_bn_silu_linear_adapters_backward(const void *dy, long long dy_stride, const void *x, long long x_stride,
+                                          const int *index, const void *a, const void *b, const float *scale,
+                                          const float *hidden, const void *base, long long base_stride, void *dx,
+                                          long long dx_stride, float *da, float *db, long long m, int k, int n,
+                                          int rank, int adapters, int dtype, void *workspace,
+                                          long long workspace_bytes, void *stream)
+{
+    if (!adapter_sizes_ok(m, k, n, rank, adapters, dtype) || !da || !db) return CBS_ERR_INVALID_ARG;
+    if (!aligned_to(da, 4) || !aligned_to(db, 4)) return CBS_ERR_MISALIGNED;
+    cudaStream_t strm = static_cast<cudaStream_t>(stream);
+    if (m == 0) {
+        cudaError_t e = cudaMemsetAsync(da, 0, 4 * (size_t)adapters * rank * k, strm);
+        if (e == cudaSuccess) e = cudaMemsetAsync(db, 0, 4 * (size_t)adapters * rank * n, strm);
+        return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+    }
+    const int size = cbs::dtype_size(dtype);
+    int st = check_rows(dy, m, n, dy_stride, size, false);
+    if (st == CBS_OK) st = check_rows(x, m, k, x_stride, size, false);
+    if (st == CBS_OK && base) st = check_rows(base, m, k, base_stride, size, false);
+    if (st == CBS_OK) st = check_rows(dx, m, k, dx_stride, size, true);
+    if (st != CBS_OK) return st;
+    if (!index || !a || !b || !hidden || !workspace || !same_or_apart(base, base_stride, dx, dx_stride, m))
+        return CBS_ERR_INVALID_ARG;
+    if (!aligned_to(index, 4) || !aligned_to(a, size) || !aligned_to(b, size) || !aligned_to(scale, 4) ||
+        !aligned_to(hidden, 4) || !aligned16(workspace))
+        return CBS_ERR_MISALIGNED;
+    int sms = 0;
+    st = sm_count_current_device(&sms);
+    if (st != CBS_OK) return st;
+    cbs::AdapterProblem p{};
+    p.x = cbs::Rows{const_cast<void *>(x), x_stride};
+    p.base = cbs::Rows{const_cast<void *>(base), base_stride};
+    p.y = cbs::Rows{dx, dx_stride};
+    p.dy = cbs::Rows{const_cast<void *>(dy), dy_stride};
+    p.index = index;
+    p.a = a;
+    p.b = b;
+    p.scale = scale;
+    p.hidden = hidden;
+    p.da = da;
+    p.db = db;
+    p.m = (int)m;
+    p.k = k;
+    p.n = n;
+    p.rank = rank;
+    p.adapters = adapters;
+    p.dtype = dtype;
+    p.workspace = workspace;
+    if (workspace_bytes < cbs::adapters_workspace_bytes(p, true, sms)) return CBS_ERR_INVALID_ARG;
+    cudaError_t e = cbs::adapters_grad_launch(p, sms, strm);
     return e == cudaSuccess ? CBS_OK : cuda_fail(e);
 }
 

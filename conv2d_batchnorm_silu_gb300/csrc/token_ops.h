@@ -75,6 +75,24 @@ struct RmsNormGradProblem {
     int dtype;
 };
 
+// Low-rank adapters and their gradients.
+struct AdapterProblem {
+    Rows x;             // `dtype` [m][k]
+    Rows base;          // nullable [m][n], or for the gradient [m][k]; may be y itself
+    Rows y;             // [m][n]; for the gradient dx [m][k]
+    Rows dy;            // gradient only: [m][n]
+    const int *index;   // [m]
+    const void *a, *b;  // `dtype` [adapters][rank][k], [adapters][n][rank]
+    const float *scale; // nullable [adapters]
+    float *hidden_out;  // nullable [m][rank], forward only
+    const float *hidden;// gradient only
+    float *da, *db;     // gradient only: as a and b
+    int m, k, n, rank, adapters;
+    int dtype;
+    void *workspace;    // adapters_workspace_bytes
+};
+constexpr int kMostAdapters = 4096, kMostRank = 128, kMostAdapterRows = 1 << 20;
+
 // One tensor of an AdamW step: fp32 moments, or e4m3 ones (v's square root) with a scale for each 256 elements.
 struct AdamWTensor {
     void *p;
@@ -149,6 +167,10 @@ cudaError_t norm_grad_launch(const NormGradProblem &p, int sm_count, cudaStream_
 cudaError_t rms_norm_launch(const RmsNormProblem &p, int sm_count, cudaStream_t stream);
 int rms_grad_partial_rows(long long rows, int sm_count);  // of partial sums, each [c]
 cudaError_t rms_norm_grad_launch(const RmsNormGradProblem &p, int sm_count, cudaStream_t stream);
+
+long long adapters_workspace_bytes(const AdapterProblem &p, bool gradient, int sm_count);
+cudaError_t adapters_launch(const AdapterProblem &p, int sm_count, cudaStream_t stream);
+cudaError_t adapters_grad_launch(const AdapterProblem &p, int sm_count, cudaStream_t stream);
 
 constexpr int kAdamWBlock = 256;  // elements that share a scale
 cudaError_t adamw_launch(const AdamWTensor *tensors, int count, const AdamWScalars &s, bool eight, cudaStream_t stream);

@@ -461,6 +461,55 @@ int conv_bn_silu_rms_norm_backward(const void *dy, long long dy_stride, const vo
 long long conv_bn_silu_rms_norm_backward_workspace(long long rows, int c);
 
 /*
+ * Low-rank adapters of many requests beside a linear layer.  Row i has adapter g = index[i], or
+ * none where index[i] is outside [0, adapters):
+ *   hidden[i] = A_g x[i],  y[i] = base[i] + scale[g] * B_g hidden[i]      (without one: y[i] = base[i])
+ *   x      : device, dtype [m][k];  index : device, int32 [m], in any order
+ *   a, b   : device, dtype [adapters][rank][k] and [adapters][n][rank], dense
+ *   scale  : device, float32 [adapters], or NULL for 1
+ *   base   : device, dtype [m][n], or NULL for 0 (the linear layer's output).  It may be y itself,
+ *            whose rows without an adapter are then left as they are
+ *   y      : device, dtype [m][n], written
+ *   hidden : device, float32 [m][rank], written (what conv_bn_silu_linear_adapters_backward needs;
+ *            zeros without an adapter), or NULL
+ *   workspace : device, 16-byte aligned, at least conv_bn_silu_linear_adapters_workspace(...)
+ *               bytes; NULL when that is 0
+ * Sums in fp32; with 16-bit activations hidden is rounded to their type (f16 with a power of two
+ * a row) before the second product, and y once more.  float32 activations are products of
+ * two-part 19-bit floats, to some 2^-21 of their terms.
+ * m <= 2^20; 1 <= k, n <= 2^22; 1 <= rank <= 128; 1 <= adapters <= 4096.  m == 0 is a no-op.
+ * Adapters of lower rank than the others are padded with zeros.
+ */
+int conv_bn_silu_linear_adapters(const void *x, long long x_stride, const int *index, const void *a, const void *b,
+                                 const float *scale, const void *base, long long base_stride, void *y,
+                                 long long y_stride, float *hidden, long long m, int k, int n, int rank,
+                                 int adapters, int dtype, void *workspace, long long workspace_bytes, void *stream);
+
+/*
+ * Gradients of conv_bn_silu_linear_adapters:
+ *   dhidden[i] = B_g^T dy[i],  dx[i] = base[i] + scale[g] * A_g^T dhidden[i]   (without an adapter: base[i])
+ *   da_g = scale[g] * sum over the rows of g of dhidden x^T,  db_g likewise of dy hidden^T
+ *   dy, x, index, a, b, scale : of the forward call
+ *   hidden : device, float32 [m][rank], written by the forward call
+ *   base   : device, dtype [m][k], or NULL for 0: the gradient that x has from elsewhere.  It may be dx itself
+ *   dx     : device, dtype [m][k], written
+ *   da, db : device, float32 [adapters][rank][k] and [adapters][n][rank], written (zeros for adapters
+ *            without rows)
+ * The gradient of base is dy itself.  Sizes as in the forward call; m == 0 leaves da and db zero.
+ */
+int conv_bn_silu_linear_adapters_backward(const void *dy, long long dy_stride, const void *x, long long x_stride,
+                                          const int *index, const void *a, const void *b, const float *scale,
+                                          const float *hidden, const void *base, long long base_stride, void *dx,
+                                          long long dx_stride, float *da, float *db, long long m, int k, int n,
+                                          int rank, int adapters, int dtype, void *workspace,
+                                          long long workspace_bytes, void *stream);
+
+/* Workspaces of the two calls on the current device in bytes; -1 for sizes out of range or when
+ * no device answers. */
+long long conv_bn_silu_linear_adapters_workspace(long long m, int k, int n, int rank, int adapters);
+long long conv_bn_silu_linear_adapters_backward_workspace(long long m, int k, int n, int rank, int adapters);
+
+/*
  * AdamW step of `count` tensors, each in place:
  *   g' = grad_scale * grad,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
  *   param = param (1 - lr decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)

@@ -112,3 +112,37 @@ def e4m3_distance(x):
     """Between the 8-bit floats around magnitudes x."""
     with np.errstate(divide="ignore"):
         return 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(x, 2.0 ** -60))), -6) - 3)
+
+
+def linear_adapters(x, index, a, b, scale=None, base=None):
+    """(y, hidden, total): the adapters' output, their hidden rows, and sum |terms| of y for error bounds."""
+    x, a, b = (np.asarray(t, np.float64) for t in (x, a, b))
+    hidden, y = np.zeros((len(x), a.shape[1])), np.zeros((len(x), b.shape[1]))
+    total = np.zeros_like(y)
+    for i, g in enumerate(index):
+        if 0 <= g < len(a):
+            s = 1.0 if scale is None else float(scale[g])
+            hidden[i] = a[g] @ x[i]
+            y[i] = s * (b[g] @ hidden[i])
+            total[i] = abs(s) * (np.abs(b[g]) @ (np.abs(a[g]) @ np.abs(x[i])))
+    if base is not None:
+        y, total = y + np.asarray(base, np.float64), total + np.abs(np.asarray(base, np.float64))
+    return y, hidden, total
+
+
+def linear_adapters_backward(dy, x, index, a, b, scale, hidden, base=None):
+    """((dx, da, db), (sum |terms| of each))."""
+    dy, x, a, b, hidden = (np.asarray(t, np.float64) for t in (dy, x, a, b, hidden))
+    out, terms = (np.zeros_like(x), np.zeros_like(a), np.zeros_like(b)), (np.zeros_like(x), np.zeros_like(a), np.zeros_like(b))
+    for i, g in enumerate(index):
+        if 0 <= g < len(a):
+            s = 1.0 if scale is None else float(scale[g])
+            for to, f in ((out, lambda v: v), (terms, np.abs)):
+                dh = f(b[g]).T @ f(dy[i])
+                to[0][i] = f(np.float64(s)) * (f(a[g]).T @ dh)
+                to[1][g] += f(np.float64(s)) * np.outer(dh, f(x[i]))
+                to[2][g] += f(np.float64(s)) * np.outer(f(dy[i]), f(hidden[i]))
+    if base is not None:
+        out[0][:] += np.asarray(base, np.float64)
+        terms[0][:] += np.abs(np.asarray(base, np.float64))
+    return out, terms
