@@ -187,7 +187,7 @@ Layout layout_of(const AdapterProblem &p, bool ordered, int k, int n, int sm_cou
 {
     Layout l{};
     l.few = !ordered && p.m <= kFew;
-    // Tiles of 64 rows read an adapter's weights a fourth as often; where an adapter has few rows, on average over all
+    // Tiles of 128 rows read an adapter's weights an eighth as often; where an adapter has few rows, on average over all
     // there are, most of such a tile's warps would have none.
     l.many = p.m > kFew && p.m >= 24LL * p.adapters;
     l.tile_rows = l.many ? kAdapterManyRows : kAdapterFewRows;
@@ -295,6 +295,8 @@ cudaError_t adapters_launch(const AdapterProblem &p, int sm_count, cudaStream_t 
     a.x_wide = p.k % 8 == 0 && on_boundary(p.x.data, p.x.stride, size);
     a.w1_wide = p.k % 8 == 0 && on_boundary(p.a, 0, size);
     a.w2_wide = p.rank % 4 == 0 && on_boundary(p.b, 0, size);
+    a.w1_pieces = p.k * size % 16 == 0 && on_boundary(p.a, 0, size);
+    a.w2_pieces = p.rank * size % 16 == 0 && on_boundary(p.b, 0, size);
     a.y_wide = p.n % 8 == 0 && on_boundary(p.y.data, p.y.stride, size) && on_boundary(p.base.data, p.base.stride, size);
     if (!l.few) {
         const Workspace w = workspace_of(p, false, sm_count);
@@ -343,6 +345,8 @@ cudaError_t adapters_grad_launch(const AdapterProblem &p, int sm_count, cudaStre
     a.x_wide = p.n % 8 == 0 && on_boundary(p.dy.data, p.dy.stride, size);
     a.w1_wide = p.rank % near == 0 && on_boundary(p.b, 0, size);
     a.w2_wide = p.k % 4 == 0 && on_boundary(p.a, 0, size);
+    a.w1_pieces = p.rank * size % 16 == 0 && on_boundary(p.b, 0, size);
+    a.w2_pieces = p.k * size % 16 == 0 && on_boundary(p.a, 0, size);
     a.y_wide = p.k % 8 == 0 && on_boundary(p.y.data, p.y.stride, size) && on_boundary(p.base.data, p.base.stride, size);
     e = products(a, p.dtype, true, l, stream);
     if (e != cudaSuccess) return e;

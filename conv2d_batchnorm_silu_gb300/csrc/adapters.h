@@ -29,6 +29,7 @@ struct AdapterArgs {
     long long x_stride, base_stride, y_stride;
     int m, k, n, rank, adapters;
     bool x_wide, w1_wide, w2_wide, y_wide;  // rows on the boundaries of wide loads and stores, and as long as they are
+    bool w1_pieces, w2_pieces;              // the weights' rows in whole pieces of 16 bytes
 };
 
 // Gradients of the adapters' weights: sums over the rows of each adapter.
@@ -46,13 +47,13 @@ struct AdapterGradArgs {
 };
 
 constexpr int kAdapterThreads = 256;
-constexpr int kAdapterFewRows = 16, kAdapterManyRows = 64;  // of a tile
+constexpr int kAdapterFewRows = 16, kAdapterManyRows = 128;  // of a tile
 constexpr int kAdapterColumns = 64;                         // of a weight gradient's CTA, 32 for ranks above 32
 
 inline int adapter_rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 inline int adapter_columns(int rank) { return rank <= 32 ? kAdapterColumns : kAdapterColumns / 2; }
 
-// By element type (adapters_*.cu).  `many`: tiles of 64 rows, else of 16.
+// By element type (adapters_*.cu).  `many`: tiles of 128 rows, else of 16.
 template <typename T>
 cudaError_t adapter_products_launch(const AdapterArgs &a, bool transposed, bool many, int clusters, int cluster_size,
                                     cudaStream_t stream);

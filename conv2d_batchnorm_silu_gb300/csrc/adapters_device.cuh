@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "adapters.h"
 #include "cbs_internal.h"
 #include "ptx.cuh"
@@ -187,6 +189,48 @@ __device__ __forceinline__ void mma_four(float *c, const Near<T, 4> &lo, const N
     } else {
         mma16(c, lo.w[0], hi.w[0], lo.w[1], hi.w[1], col.w[0], col.w[1], T());
     }
+}
+
+template <typename T>
+__device__ __forceinline__ void mma_near(float *c, const Near<T, 8> &lo, const Near<T, 8> &hi, const Near<T, 8> &col) { mma_eight<T>(c, lo, hi, col); }
+template <typename T>
+__device__ __forceinline__ void mma_near(float *c, const Near<T, 4> &lo, const Near<T, 4> &hi, const Near<T, 4> &col) { mma_four<T>(c, lo, hi, col); }
+
+// Neighbours from shared memory, on a boundary of their size (16 bytes at most).
+template <typename T, int N>
+__device__ __forceinline__ void from_shared(const unsigned char *p, Near<T, N> *v)
+{
+    constexpr int kBytes = N * (int)sizeof(T);
+    uint32_t *w = reinterpret_cast<uint32_t *>(v->w);
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i) {
+            const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
+            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+        }
+    } else if constexpr (kBytes == 8) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(p);
+        w[0] = u.x, w[1] = u.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+// What a row's N values of this lane (a quarter of the row's) are multiplied with before they are rounded to f16, whose
+// range the sums may leave: a power of two that takes the row's largest to [1, 2).  *s takes its inverse.
+template <typename T, int N>
+__device__ __forceinline__ float narrow_factor(const float *v, float *s)
+{
+    if constexpr (!__is_same(T, __half)) return 1.0f;
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) most = fmaxf(most, fabsf(v[i]));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    int e = (int)(__float_as_uint(most) >> 23);  // 127 + its exponent; 255 where it is infinite
+    e = e < 2 ? 2 : e > 252 ? 252 : e;
+    *s *= __uint_as_float((unsigned)e << 23);
+    return __uint_as_float((unsigned)(254 - e) << 23);
 }
 
 // N rows of N neighbours -> for each neighbour the N values of its rows, as the second operand wants them.
@@ -389,23 +433,7 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 ? 2 : 1) adapter_prod
                 }
             } else {
                 auto narrow = [&](const float4 *v, Near<T, 4> *h, float *s) {
-                    float factor = 1.0f;
-                    if constexpr (sizeof(T) == 2) {
-                        T probe;
-                        narrowed(1e30f, &probe);
-                        if (isinf(widened(probe))) {  // f16, known when it is compiled
-                            float most = 0.0f;
-#pragma unroll
-                            for (int i = 0; i < RT; ++i)
-                                most = fmaxf(most, fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
-                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                            int e = (int)(__float_as_uint(most) >> 23);  // 127 + its exponent; 255 where it is infinite
-                            e = e < 2 ? 2 : e > 252 ? 252 : e;
-                            factor = __uint_as_float((unsigned)(254 - e) << 23);
-                            *s *= __uint_as_float((unsigned)e << 23);
-                        }
-                    }
+                    const float factor = narrow_factor<T, 4 * RT>(reinterpret_cast<const float *>(v), s);
 #pragma unroll
                     for (int i = 0; i < RT; ++i) {
                         h[i].w[0] = packed(v[i].x * factor, v[i].y * factor, T());
@@ -477,6 +505,366 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 ? 2 : 1) adapter_prod
         }
     }
     if (live) cluster_wait();
+}
+
+// ------------------------------------------------------------------ the same for many rows of an adapter
+// Tiles of 128 rows: a warp takes 32 of them, and what it reads of the weights serves both its halves.  Either product
+// goes in steps of 64 (of K, or of the output's columns), through a ring in shared memory that asynchronous copies
+// fill some steps ahead: the step's weights, which all warps read, and each thread's own eight elements of its four
+// rows of x or of base, which nobody else reads.  (Both loaded to registers a step ahead, with 16 warps on an SM,
+// waited for memory most of the time: 8192x4096x16384 with rank 64 263 us; weights read by every warp from where
+// they lie, 394.)
+constexpr int kManyStep = 64;
+
+// Own elements in the ring: eight on their boundary, or the aligned pieces that they lie in.
+template <typename T, bool WIDE>
+constexpr int own_pieces() { return sizeof(T) == 4 || !WIDE ? 2 : 1; }
+// A step's weights are [rank][64] ("flat") or [64][rank]: bytes of a row, with a pad that keeps readers off each
+// other's banks.
+template <typename T, int RT, bool FLAT>
+constexpr int weight_pitch() { return (FLAT ? kManyStep : 16 * RT) * (int)sizeof(T) + 16; }
+template <typename T, int RT, bool FLAT>
+constexpr int weight_rows() { return FLAT ? 16 * RT : kManyStep; }
+template <typename T, int RT>
+constexpr int weight_bytes()
+{
+    constexpr int flat = weight_rows<T, RT, true>() * weight_pitch<T, RT, true>(), tall = weight_rows<T, RT, false>() * weight_pitch<T, RT, false>();
+    return flat > tall ? flat : tall;
+}
+template <typename T, int RT, bool WIDE>
+constexpr int many_stage() { return 4 * kAdapterThreads * 16 * own_pieces<T, WIDE>() + weight_bytes<T, RT>(); }
+template <typename T, int RT, bool WIDE>
+constexpr int many_stages() { return sizeof(T) == 2 && WIDE ? 4 : 3; }
+template <typename T, int RT, bool WIDE>
+constexpr int many_smem()
+{
+    constexpr int ring = many_stages<T, RT, WIDE>() * many_stage<T, RT, WIDE>(), sums = 2 * kAdapterManyRows * hidden_pitch<RT>() * 4;
+    return ring > sums ? ring : sums;
+}
+
+// Ranks that a lane has side by side in the second product: 8 of 32 in 16 bits, as one load of 16 bytes, else 4 of 16.
+template <typename T, int RT>
+constexpr int many_near() { return sizeof(T) == 2 && RT % 2 == 0 ? 8 : 4; }
+
+__device__ __forceinline__ void copy_piece(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_word(uint32_t dst, const void *src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+
+// Eight elements from p, `have` of them there, to their thread's pieces of 16 bytes, kAdapterThreads pieces apart.
+template <bool WIDE, typename T>
+__device__ __forceinline__ void copy_own(uint32_t dst, const T *p, int have)
+{
+    constexpr int kApart = 16 * kAdapterThreads;
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < own_pieces<T, true>(); ++i) copy_piece(dst + i * kApart, reinterpret_cast<const char *>(p) + 16 * i, have > 0);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) copy_word(dst + i / 4 * kApart + i % 4 * 4, p + (i < have ? i : 0), i < have);
+    } else {
+        // The aligned pieces that hold some of them.
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p), from = at & ~(uintptr_t)15;
+        const int bytes = (int)(at - from) + 2 * (have < 8 ? have : 8);
+        copy_piece(dst, reinterpret_cast<const void *>(from), have > 0);
+        copy_piece(dst + kApart, reinterpret_cast<const void *>(bytes > 16 ? from + 16 : from), have > 0 && bytes > 16);
+    }
+}
+// They again, from the pieces at `src`, zeros beyond `have`.
+template <bool WIDE, typename T>
+__device__ __forceinline__ Near<T, 8> own_of(const unsigned char *src, const T *p, int have)
+{
+    constexpr int kApart = 16 * kAdapterThreads;
+    Near<T, 8> v;
+    uint32_t *w = reinterpret_cast<uint32_t *>(v.w);
+    const uint4 u = *reinterpret_cast<const uint4 *>(src);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    if constexpr (sizeof(T) == 4) {
+        const uint4 o = *reinterpret_cast<const uint4 *>(src + kApart);
+        w[4] = o.x, w[5] = o.y, w[6] = o.z, w[7] = o.w;
+    } else if constexpr (!WIDE) {
+        const uint4 o = *reinterpret_cast<const uint4 *>(src + kApart);
+        const unsigned off = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;
+        uint32_t all[8] = {u.x, u.y, u.z, u.w, o.x, o.y, o.z, o.w};
+        // Down by whole words, two and one at a time, then by half a word.
+#pragma unroll
+        for (int i = 0; i < 6; ++i) all[i] = off & 8 ? all[i + 2] : all[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) all[i] = off & 4 ? all[i + 1] : all[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = __funnelshift_r(all[i], all[i + 1], (off & 2) * 8);
+            const int left = have - 2 * i;
+            if (left < 2) w[i] = left < 1 ? 0u : w[i] & 0xffffu;
+        }
+    }
+    return v;
+}
+
+template <typename T, int RT, bool TURNED, bool WIDE>
+__global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2 : 1) adapter_many_kernel(const AdapterArgs a)
+{
+    constexpr int kRows = kAdapterManyRows, kPitch = hidden_pitch<RT>(), kNear = many_near<T, RT>(), kSteps = 16 * RT / (4 * kNear);
+    constexpr int kStages = many_stages<T, RT, WIDE>(), kStage = many_stage<T, RT, WIDE>();
+    constexpr int kOwn = 16 * kAdapterThreads * own_pieces<T, WIDE>();  // bytes of all threads' elements of one row
+    extern __shared__ __align__(16) float adapter_sums[];  // the ring, and between the products [2][kRows][kPitch] partial and whole sums
+    __shared__ int rows[kRows];
+    dev::grid_dependency_wait();
+    dev::grid_dependents_launch();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+    const int part = (int)dev::cluster_ctarank(), parts = (int)cluster_size();
+    const int tile = (int)blockIdx.x / parts;
+    if (tile >= *a.tile_count) return;
+    const AdapterTile my = a.tiles[tile];
+    const int adapter = my.adapter, count = my.count;
+    if ((int)threadIdx.x < count) rows[threadIdx.x] = a.order[my.first + threadIdx.x];
+    __syncthreads();
+    const bool live = adapter < a.adapters;
+    const int wm = warp % 4, ws = warp / 4;  // 32 rows of the tile; a half of each step
+    const bool busy = 32 * wm < count;
+    bool has[4];
+    int row[4];  // g, g + 8, g + 16 and g + 24 of the warp's
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        has[i] = 32 * wm + 8 * i + g < count;
+        row[i] = has[i] ? rows[32 * wm + 8 * i + g] : 0;
+    }
+    float *whole = adapter_sums + kRows * kPitch;
+    unsigned char *ring = reinterpret_cast<unsigned char *>(adapter_sums);
+
+    // Steps of a product that this CTA takes, and their copies: the weights [a step's 64 of `length`], and from `data`
+    // this thread's elements.
+    auto share = [&](int length, int *first, int *stop) {
+        const long long steps = (length + kManyStep - 1) / kManyStep;
+        *first = (int)(steps * part / parts);
+        *stop = (int)(steps * (part + 1) / parts);
+    };
+    auto own_column = [&](int step) { return step * kManyStep + 32 * ws + 8 * t; };
+    auto fetch = [&](auto flat, const T *weights, bool pieces, int length, const T *data, long long stride, int step, int first, int stop) {
+        constexpr bool kFlat = decltype(flat)::value;
+        constexpr int kWRows = weight_rows<T, RT, kFlat>(), kWPitch = weight_pitch<T, RT, kFlat>();
+        constexpr int kLong = kFlat ? kManyStep : 16 * RT, kPiece = 16 / (int)sizeof(T), kPieces = kLong / kPiece;
+        if (step < stop) {
+            unsigned char *to = ring + (step - first) % kStages * kStage;
+            if (data) {
+                const int c = own_column(step);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    copy_own<WIDE, T>(dev::smem_u32(to + i * kOwn + threadIdx.x * 16), data + row[i] * stride + (c < length ? c : 0),
+                                      has[i] ? length - c : 0);
+            }
+            to += 4 * kOwn;
+            if (live && pieces) {
+                for (int i = threadIdx.x; i < kWRows * kPieces; i += kAdapterThreads) {
+                    const int r = i / kPieces, c = i % kPieces * kPiece;
+                    const int rank = kFlat ? r : c, at = step * kManyStep + (kFlat ? c : r);
+                    const bool there = rank < a.rank && at < length;
+                    const T *from = weights + (kFlat ? (long long)rank * length + at : (long long)at * a.rank + rank);
+                    copy_piece(dev::smem_u32(to + r * kWPitch + c * (int)sizeof(T)), there ? from : weights, there);
+                }
+            } else if (live) {
+                for (int i = threadIdx.x; i < kWRows * kLong; i += kAdapterThreads) {
+                    const int r = i / kLong, c = i % kLong;
+                    const int rank = kFlat ? r : c, at = step * kManyStep + (kFlat ? c : r);
+                    T v;
+                    narrowed(0.0f, &v);
+                    if (rank < a.rank && at < length) v = weights[kFlat ? (long long)rank * length + at : (long long)at * a.rank + rank];
+                    reinterpret_cast<T *>(to + r * kWPitch)[c] = v;
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto arrived = [&]() {  // a step's copies, for all; and the step before it read by all
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncthreads();
+    };
+    auto own_at = [&](int i, const T *data, long long stride, int length, int step, int first) {
+        const int c = own_column(step);
+        return own_of<WIDE, T>(ring + (step - first) % kStages * kStage + i * kOwn + threadIdx.x * 16,
+                               data + row[i] * stride + (c < length ? c : 0), has[i] ? length - c : 0);
+    };
+    auto weights_at = [&](int step, int first) { return ring + (step - first) % kStages * kStage + 4 * kOwn; };
+
+    if (live) {
+        const std::integral_constant<bool, !TURNED> flat{};
+        constexpr int kWPitch = weight_pitch<T, RT, !TURNED>();
+        const T *w1 = static_cast<const T *>(a.w1) + (long long)adapter * a.rank * a.k, *x = static_cast<const T *>(a.x);
+        float acc[2][2 * RT][4] = {};
+        int first, stop;
+        share(a.k, &first, &stop);
+        for (int j = 0; j < kStages - 1; ++j) fetch(flat, w1, a.w1_pieces, a.k, x, a.x_stride, first + j, first, stop);
+        for (int step = first; step < stop; ++step) {
+            arrived();
+            fetch(flat, w1, a.w1_pieces, a.k, x, a.x_stride, step + kStages - 1, first, stop);
+            if (!busy) continue;
+            Near<T, 8> own[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) own[i] = own_at(i, x, a.x_stride, a.k, step, first);
+            const unsigned char *w = weights_at(step, first);
+            if constexpr (!TURNED) {
+#pragma unroll
+                for (int j = 0; j < 2 * RT; ++j) {
+                    Near<T, 8> col;
+                    from_shared(w + (8 * j + g) * kWPitch + (32 * ws + 8 * t) * (int)sizeof(T), &col);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) mma_eight<T>(acc[h][j], own[2 * h], own[2 * h + 1], col);
+                }
+            } else {
+                constexpr int kC = 2 * RT < 8 ? 2 * RT : 8;
+#pragma unroll
+                for (int c = 0; c < 2 * RT; c += kC) {
+                    Near<T, kC> in[8];
+                    Near<T, 8> col[kC];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) from_shared(w + (32 * ws + 8 * t + i) * kWPitch + (2 * RT * g + c) * (int)sizeof(T), &in[i]);
+                    turned<T, 8, kC>(in, col);
+#pragma unroll
+                    for (int j = 0; j < kC; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) mma_eight<T>(acc[h][c + j], own[2 * h], own[2 * h + 1], col[j]);
+                }
+            }
+        }
+        __syncthreads();  // the ring is read; what was copied ahead of it, nothing
+        // The two halves of the steps: the second's sums beside, where the whole ones will be.
+        float *mine = (ws ? whole : adapter_sums) + 32 * wm * kPitch;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2 * RT; ++j) {
+                const int r0 = TURNED ? 2 * RT * (2 * t) + j : 8 * j + 2 * t, r1 = TURNED ? 2 * RT * (2 * t + 1) + j : r0 + 1;
+                mine[(16 * h + g) * kPitch + r0] = acc[h][j][0];
+                mine[(16 * h + g) * kPitch + r1] = acc[h][j][1];
+                mine[(16 * h + g + 8) * kPitch + r0] = acc[h][j][2];
+                mine[(16 * h + g + 8) * kPitch + r1] = acc[h][j][3];
+            }
+        __syncthreads();
+        constexpr int kQuads = 4 * RT;  // of a row
+        for (int i = threadIdx.x; i < count * kQuads; i += kAdapterThreads) {
+            const int offset = i / kQuads * kPitch + i % kQuads * 4;
+            float4 *at = reinterpret_cast<float4 *>(adapter_sums + offset);
+            const float4 u = *reinterpret_cast<const float4 *>(whole + offset);
+            *at = make_float4(at->x + u.x, at->y + u.y, at->z + u.z, at->w + u.w);
+        }
+        cluster_arrive();
+        cluster_wait();
+        const uint32_t sums = dev::smem_u32(adapter_sums);
+        for (int i = threadIdx.x; i < kRows * kQuads; i += kAdapterThreads) {
+            const int offset = i / kQuads * kPitch + i % kQuads * 4;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < count * kQuads) {
+                v = load_cluster(dev::mapa_cluster(sums + 4 * offset, 0));
+                for (int p = 1; p < parts; ++p) {
+                    const float4 u = load_cluster(dev::mapa_cluster(sums + 4 * offset, (uint32_t)p));
+                    v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+                }
+            }
+            *reinterpret_cast<float4 *>(whole + offset) = v;
+        }
+        __syncthreads();
+        cluster_arrive();  // waited for before the ring takes the sums' place
+    }
+    if (a.hidden) {
+        for (int i = threadIdx.x; i < count * a.rank; i += kAdapterThreads) {
+            const int r = i / a.rank;
+            if (r % parts == part) a.hidden[(long long)rows[r] * a.rank + i % a.rank] = live ? whole[r * kPitch + i % a.rank] : 0.0f;
+        }
+    }
+    // The first operand's rows, as in adapter_products_kernel.
+    Near<T, kNear> h[4][kSteps];
+    float s[4] = {};
+    if (live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i] = a.scale ? a.scale[adapter] : 1.0f;
+            float v[kSteps][kNear];
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int q = 0; q < kNear; q += 4) {
+                    const float4 u = *reinterpret_cast<const float4 *>(whole + (32 * wm + 8 * i + g) * kPitch + 4 * kNear * k + kNear * t + q);
+                    v[k][q] = u.x, v[k][q + 1] = u.y, v[k][q + 2] = u.z, v[k][q + 3] = u.w;
+                }
+            const float factor = narrow_factor<T, kSteps * kNear>(&v[0][0], &s[i]);
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int q = 0; q < kNear; q += 2) {
+                    if constexpr (sizeof(T) == 4) {
+                        h[i][k].w[q] = v[k][q];
+                        h[i][k].w[q + 1] = v[k][q + 1];
+                    } else {
+                        h[i][k].w[q / 2] = packed(v[k][q] * factor, v[k][q + 1] * factor, T());
+                    }
+                }
+        }
+        cluster_wait();
+        __syncthreads();
+    }
+    if (live || a.base != a.y) {
+        const std::integral_constant<bool, TURNED> flat{};
+        constexpr int kWPitch = weight_pitch<T, RT, TURNED>();
+        const T *w2 = static_cast<const T *>(a.w2) + (live ? (long long)adapter * a.rank * a.n : 0), *base = static_cast<const T *>(a.base);
+        int first, stop;
+        share(a.n, &first, &stop);
+        for (int j = 0; j < kStages - 1; ++j) fetch(flat, w2, a.w2_pieces, a.n, base, a.base_stride, first + j, first, stop);
+        for (int step = first; step < stop; ++step) {
+            arrived();
+            fetch(flat, w2, a.w2_pieces, a.n, base, a.base_stride, step + kStages - 1, first, stop);
+            if (!busy) continue;
+            float acc[2][4][4] = {};
+            if (live) {
+                const unsigned char *w = weights_at(step, first);
+                if constexpr (!TURNED) {
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            Near<T, kNear> col;
+                            from_shared(w + (32 * ws + 4 * g + q) * kWPitch + (4 * kNear * k + kNear * t) * (int)sizeof(T), &col);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) mma_near<T>(acc[m][q], h[2 * m][k], h[2 * m + 1][k], col);
+                        }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+                        Near<T, 4> in[kNear];
+                        Near<T, kNear> col[4];
+#pragma unroll
+                        for (int r = 0; r < kNear; ++r)
+                            from_shared(w + (4 * kNear * k + kNear * t + r) * kWPitch + (32 * ws + 4 * g) * (int)sizeof(T), &in[r]);
+                        turned<T, kNear, 4>(in, col);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) mma_near<T>(acc[m][q], h[2 * m][k], h[2 * m + 1][k], col[q]);
+                    }
+                }
+            }
+            const int n0 = own_column(step), have = a.n - n0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[q] = acc[i / 2][q][i % 2 * 2] * s[i];
+                    v[4 + q] = acc[i / 2][q][i % 2 * 2 + 1] * s[i];
+                }
+                if (a.base) {
+                    const Near<T, 8> old = own_at(i, base, a.base_stride, a.n, step, first);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v[q] = live ? old.at(q) + v[q] : old.at(q);
+                }
+                if (has[i]) store_near<WIDE, T>(static_cast<T *>(a.y) + row[i] * a.y_stride + n0, v, have);
+            }
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ gradients of the weights
@@ -604,6 +992,17 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 ? 2 : 1) adapter_weig
 }
 
 // ------------------------------------------------------------------ launches
+template <typename T, int RT, bool TURNED, bool WIDE>
+cudaError_t many_launch(const AdapterArgs &a, int clusters, int cluster_size, cudaStream_t stream)
+{
+    constexpr int kSmem = many_smem<T, RT, WIDE>();
+    static bool allowed[kMaxDevices] = {};
+    const cudaError_t e = allow_dynamic_smem(adapter_many_kernel<T, RT, TURNED, WIDE>, kSmem, allowed);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(adapter_many_kernel<T, RT, TURNED, WIDE>, dim3((unsigned)clusters * (unsigned)cluster_size),
+                             dim3(kAdapterThreads), kSmem, stream, cluster_size, a);
+}
+
 template <typename T, int RT, int WM, bool TURNED, bool WIDE>
 cudaError_t products_launch(const AdapterArgs &a, int clusters, int cluster_size, cudaStream_t stream)
 {
@@ -617,15 +1016,18 @@ cudaError_t products_launch(const AdapterArgs &a, int clusters, int cluster_size
                              dim3(kAdapterThreads), kSmem, stream, cluster_size, a);
 }
 
-template <typename T, int RT, int WM>
-cudaError_t products_pick(const AdapterArgs &a, bool turned, int clusters, int cluster_size, cudaStream_t stream)
+template <typename T, int RT>
+cudaError_t products_pick(const AdapterArgs &a, bool turned, bool many, int clusters, int cluster_size, cudaStream_t stream)
 {
-    const bool wide = a.x_wide && a.w1_wide && a.w2_wide && a.y_wide;
-    if (turned)
-        return wide ? products_launch<T, RT, WM, true, true>(a, clusters, cluster_size, stream)
-                    : products_launch<T, RT, WM, true, false>(a, clusters, cluster_size, stream);
-    return wide ? products_launch<T, RT, WM, false, true>(a, clusters, cluster_size, stream)
-                : products_launch<T, RT, WM, false, false>(a, clusters, cluster_size, stream);
+    const bool wide = a.x_wide && a.y_wide && (many || (a.w1_wide && a.w2_wide));
+    auto pick = [&](auto t, auto w) {
+        constexpr bool kTurned = decltype(t)::value, kWide = decltype(w)::value;
+        return many ? many_launch<T, RT, kTurned, kWide>(a, clusters, cluster_size, stream)
+                    : products_launch<T, RT, 1, kTurned, kWide>(a, clusters, cluster_size, stream);
+    };
+    constexpr std::true_type yes;
+    constexpr std::false_type no;
+    return turned ? (wide ? pick(yes, yes) : pick(yes, no)) : (wide ? pick(no, yes) : pick(no, no));
 }
 
 template <typename T, int RT>
@@ -644,12 +1046,11 @@ template <typename T>
 cudaError_t adapter_products_launch(const AdapterArgs &a, bool transposed, bool many, int clusters, int cluster_size,
                                     cudaStream_t stream)
 {
-    constexpr int kMany = kAdapterManyRows / 16;
     switch (adapter_rank_tiles(a.rank)) {
-    case 1: return many ? products_pick<T, 1, kMany>(a, transposed, clusters, cluster_size, stream) : products_pick<T, 1, 1>(a, transposed, clusters, cluster_size, stream);
-    case 2: return many ? products_pick<T, 2, kMany>(a, transposed, clusters, cluster_size, stream) : products_pick<T, 2, 1>(a, transposed, clusters, cluster_size, stream);
-    case 4: return many ? products_pick<T, 4, kMany>(a, transposed, clusters, cluster_size, stream) : products_pick<T, 4, 1>(a, transposed, clusters, cluster_size, stream);
-    default: return many ? products_pick<T, 8, kMany>(a, transposed, clusters, cluster_size, stream) : products_pick<T, 8, 1>(a, transposed, clusters, cluster_size, stream);
+    case 1: return products_pick<T, 1>(a, transposed, many, clusters, cluster_size, stream);
+    case 2: return products_pick<T, 2>(a, transposed, many, clusters, cluster_size, stream);
+    case 4: return products_pick<T, 4>(a, transposed, many, clusters, cluster_size, stream);
+    default: return products_pick<T, 8>(a, transposed, many, clusters, cluster_size, stream);
     }
 }
 
