@@ -294,9 +294,10 @@ cudaError_t adapters_launch(const AdapterProblem &p, int sm_count, cudaStream_t 
     a.adapters = p.adapters;
     a.x_wide = p.k % 8 == 0 && on_boundary(p.x.data, p.x.stride, size);
     a.w1_wide = p.k % 8 == 0 && on_boundary(p.a, 0, size);
-    a.w2_wide = p.rank % 4 == 0 && on_boundary(p.b, 0, size);
+    // Ranks that a lane loads at once in the second product.
+    const int near = l.many && size == 2 && adapter_rank_tiles(p.rank) > 1 ? 8 : 4;
+    a.w2_wide = p.rank % near == 0 && on_boundary(p.b, 0, size);
     a.w1_pieces = p.k * size % 16 == 0 && on_boundary(p.a, 0, size);
-    a.w2_pieces = p.rank * size % 16 == 0 && on_boundary(p.b, 0, size);
     a.y_wide = p.n % 8 == 0 && on_boundary(p.y.data, p.y.stride, size) && on_boundary(p.base.data, p.base.stride, size);
     if (!l.few) {
         const Workspace w = workspace_of(p, false, sm_count);
@@ -344,9 +345,8 @@ cudaError_t adapters_grad_launch(const AdapterProblem &p, int sm_count, cudaStre
     const int near = adapter_rank_tiles(p.rank) < 4 ? 2 * adapter_rank_tiles(p.rank) : 8;  // ranks a lane loads at once
     a.x_wide = p.n % 8 == 0 && on_boundary(p.dy.data, p.dy.stride, size);
     a.w1_wide = p.rank % near == 0 && on_boundary(p.b, 0, size);
-    a.w2_wide = p.k % 4 == 0 && on_boundary(p.a, 0, size);
+    a.w2_wide = p.k % (l.many ? 8 : 4) == 0 && on_boundary(p.a, 0, size);
     a.w1_pieces = p.rank * size % 16 == 0 && on_boundary(p.b, 0, size);
-    a.w2_pieces = p.k * size % 16 == 0 && on_boundary(p.a, 0, size);
     a.y_wide = p.k % 8 == 0 && on_boundary(p.y.data, p.y.stride, size) && on_boundary(p.base.data, p.base.stride, size);
     e = products(a, p.dtype, true, l, stream);
     if (e != cudaSuccess) return e;

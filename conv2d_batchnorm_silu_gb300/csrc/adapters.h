@@ -29,7 +29,7 @@ struct AdapterArgs {
     long long x_stride, base_stride, y_stride;
     int m, k, n, rank, adapters;
     bool x_wide, w1_wide, w2_wide, y_wide;  // rows on the boundaries of wide loads and stores, and as long as they are
-    bool w1_pieces, w2_pieces;              // the weights' rows in whole pieces of 16 bytes
+    bool w1_pieces;                         // the first weights' rows in whole pieces of 16 bytes
 };
 
 // Gradients of the adapters' weights: sums over the rows of each adapter.

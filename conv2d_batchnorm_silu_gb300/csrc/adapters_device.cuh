@@ -23,22 +23,38 @@ namespace {
 __device__ __forceinline__ void mma16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
                                       __nv_bfloat16)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma16(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
                                       __half)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma8(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The first product of a sum.
+__device__ __forceinline__ void mma16_first(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                            __nv_bfloat16)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void mma16_first(float *c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                            __half)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // fp32 as the sum of two of the instruction's 19-bit floats, to 2^-22 of it.
@@ -144,17 +160,22 @@ __device__ __forceinline__ Near<T, N> near(const T *p, int have)
     return v;
 }
 
+__device__ __forceinline__ void store_piece(void *p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, bool there)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %5, 0;\n @p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n}" ::"l"(p), "r"(a), "r"(b),
+                 "r"(c), "r"(d), "r"((int)there)
+                 : "memory");
+}
+
 template <bool WIDE, typename T>
 __device__ __forceinline__ void store_near(T *p, const float *v, int have)
 {
     if constexpr (WIDE) {
-        if (have <= 0) return;
         if constexpr (sizeof(T) == 4) {
-            reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            store_piece(p, __float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]), have > 0);
+            store_piece(p + 4, __float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]), have > 0);
         } else {
-            *reinterpret_cast<uint4 *>(p) = make_uint4(packed(v[0], v[1], T()), packed(v[2], v[3], T()),
-                                                       packed(v[4], v[5], T()), packed(v[6], v[7], T()));
+            store_piece(p, packed(v[0], v[1], T()), packed(v[2], v[3], T()), packed(v[4], v[5], T()), packed(v[6], v[7], T()), have > 0);
         }
     } else {
 #pragma unroll
@@ -191,33 +212,43 @@ __device__ __forceinline__ void mma_four(float *c, const Near<T, 4> &lo, const N
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void mma_near(float *c, const Near<T, 8> &lo, const Near<T, 8> &hi, const Near<T, 8> &col) { mma_eight<T>(c, lo, hi, col); }
-template <typename T>
-__device__ __forceinline__ void mma_near(float *c, const Near<T, 4> &lo, const Near<T, 4> &hi, const Near<T, 4> &col) { mma_four<T>(c, lo, hi, col); }
+// 16 elements of K, or 8 in fp32, by the operands' registers; `first`: instead of adding to c.
+template <typename T, typename W>
+__device__ __forceinline__ void mma_quad(float *c, uint4 a, W b0, W b1, bool first)
+{
+    if constexpr (sizeof(T) == 4) {
+        if (first) c[0] = c[1] = c[2] = c[3] = 0.0f;
+        mma8_parts(c, parts_of(__uint_as_float(a.x)), parts_of(__uint_as_float(a.y)), parts_of(__uint_as_float(a.z)),
+                   parts_of(__uint_as_float(a.w)), parts_of(b0), parts_of(b1));
+    } else if (first) {
+        mma16_first(c, a.x, a.y, a.z, a.w, b0, b1, T());
+    } else {
+        mma16(c, a.x, a.y, a.z, a.w, b0, b1, T());
+    }
+}
 
 // Neighbours from shared memory, on a boundary of their size (16 bytes at most).
 template <typename T, int N>
-__device__ __forceinline__ void from_shared(const unsigned char *p, Near<T, N> *v)
+__device__ __forceinline__ void from_shared(uint32_t p, Near<T, N> *v)
 {
     constexpr int kBytes = N * (int)sizeof(T);
     uint32_t *w = reinterpret_cast<uint32_t *>(v->w);
     if constexpr (kBytes >= 16) {
 #pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i) {
-            const uint4 u = reinterpret_cast<const uint4 *>(p)[i];
-            w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
-        }
+        for (int i = 0; i < kBytes / 16; ++i)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                         : "r"(p + 16 * i));
     } else if constexpr (kBytes == 8) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        w[0] = u.x, w[1] = u.y;
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(p));
     } else {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(p));
     }
 }
 
-// What a row's N values of this lane (a quarter of the row's) are multiplied with before they are rounded to f16, whose
-// range the sums may leave: a power of two that takes the row's largest to [1, 2).  *s takes its inverse.
+// What a row's N values of this lane are multiplied with before they are rounded to f16, whose range the sums may
+// leave: a power of two that takes the row's largest, over the four lanes that share it, to [1, 2).  *s takes its
+// inverse.
 template <typename T, int N>
 __device__ __forceinline__ float narrow_factor(const float *v, float *s)
 {
@@ -508,21 +539,27 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 ? 2 : 1) adapter_prod
 }
 
 // ------------------------------------------------------------------ the same for many rows of an adapter
-// Tiles of 128 rows: a warp takes 32 of them, and what it reads of the weights serves both its halves.  Either product
-// goes in steps of 64 (of K, or of the output's columns), through a ring in shared memory that asynchronous copies
-// fill some steps ahead: the step's weights, which all warps read, and each thread's own eight elements of its four
-// rows of x or of base, which nobody else reads.  (Both loaded to registers a step ahead, with 16 warps on an SM,
-// waited for memory most of the time: 8192x4096x16384 with rank 64 263 us; weights read by every warp from where
-// they lie, 394.)
+// Tiles of 128 rows.  The first product goes in steps of 64 of K through a ring in shared memory that asynchronous
+// copies fill some steps ahead: the step's weights, which all warps read, and each thread's own eight elements of its
+// four rows of x, which nobody else reads; a warp takes 32 rows and a half of each step.  For the second, the small
+// rows wait in shared memory, and each warp goes through strips of 32 output columns: it holds the strip's weights in
+// registers and takes 32 rows of base at a time, the coming ones on their way through its threads' own places in the
+// ring, with no barrier.  The eight warps' strips lie side by side, so that 512 bytes of a row of base and y are
+// touched at about the same time: with all 128 rows of 64 columns in each step, pieces of 128 bytes
+// (8192x4096x16384 with rank 64 168 us), memory gave half of its rate to whatever number of warps.
 constexpr int kManyStep = 64;
 
 // Own elements in the ring: eight on their boundary, or the aligned pieces that they lie in.
 template <typename T, bool WIDE>
 constexpr int own_pieces() { return sizeof(T) == 4 || !WIDE ? 2 : 1; }
-// A step's weights are [rank][64] ("flat") or [64][rank]: bytes of a row, with a pad that keeps readers off each
-// other's banks.
+// A step's weights are [rank][64] ("flat") or [64][rank]: bytes of a row, an odd number of 64 where they are read 64
+// from two rows at a time, which keeps those off each other's banks.
 template <typename T, int RT, bool FLAT>
-constexpr int weight_pitch() { return (FLAT ? kManyStep : 16 * RT) * (int)sizeof(T) + 16; }
+constexpr int weight_pitch()
+{
+    constexpr int bytes = (FLAT ? kManyStep : 16 * RT) * (int)sizeof(T);
+    return FLAT ? bytes + 16 : bytes % 128 == 0 ? bytes + 64 : bytes;
+}
 template <typename T, int RT, bool FLAT>
 constexpr int weight_rows() { return FLAT ? 16 * RT : kManyStep; }
 template <typename T, int RT>
@@ -533,13 +570,24 @@ constexpr int weight_bytes()
 }
 template <typename T, int RT, bool WIDE>
 constexpr int many_stage() { return 4 * kAdapterThreads * 16 * own_pieces<T, WIDE>() + weight_bytes<T, RT>(); }
-template <typename T, int RT, bool WIDE>
-constexpr int many_stages() { return sizeof(T) == 2 && WIDE ? 4 : 3; }
+constexpr int kManyStages = 3, kManyAhead = 4;  // of the first and the second product
+// Bytes of the second product's small rows, in the activations' type, in their places in memory, and what they are
+// multiplied with.
+template <typename T, int RT>
+constexpr int small_rows() { return kAdapterManyRows * (16 * RT * (int)sizeof(T) + 8 + 8 + 4); }
+// The whole sums, behind the partial ones, which other CTAs read, and behind where the small rows go from them.
+template <typename T, int RT>
+constexpr int whole_sums()
+{
+    constexpr int partial = kAdapterManyRows * hidden_pitch<RT>() * 4;
+    return partial > small_rows<T, RT>() ? partial : small_rows<T, RT>();
+}
 template <typename T, int RT, bool WIDE>
 constexpr int many_smem()
 {
-    constexpr int ring = many_stages<T, RT, WIDE>() * many_stage<T, RT, WIDE>(), sums = 2 * kAdapterManyRows * hidden_pitch<RT>() * 4;
-    return ring > sums ? ring : sums;
+    constexpr int ring = kManyStages * many_stage<T, RT, WIDE>(), sums = whole_sums<T, RT>() + kAdapterManyRows * hidden_pitch<RT>() * 4;
+    constexpr int second = small_rows<T, RT>() + kManyAhead * 4 * kAdapterThreads * 16 * own_pieces<T, WIDE>();
+    return ring > sums ? (ring > second ? ring : second) : (sums > second ? sums : second);
 }
 
 // Ranks that a lane has side by side in the second product: 8 of 32 in 16 bits, as one load of 16 bytes, else 4 of 16.
@@ -548,7 +596,7 @@ constexpr int many_near() { return sizeof(T) == 2 && RT % 2 == 0 ? 8 : 4; }
 
 __device__ __forceinline__ void copy_piece(uint32_t dst, const void *src, bool there)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copy_word(uint32_t dst, const void *src, bool there)
 {
@@ -576,18 +624,18 @@ __device__ __forceinline__ void copy_own(uint32_t dst, const T *p, int have)
 }
 // They again, from the pieces at `src`, zeros beyond `have`.
 template <bool WIDE, typename T>
-__device__ __forceinline__ Near<T, 8> own_of(const unsigned char *src, const T *p, int have)
+__device__ __forceinline__ Near<T, 8> own_of(uint32_t src, const T *p, int have)
 {
     constexpr int kApart = 16 * kAdapterThreads;
     Near<T, 8> v;
     uint32_t *w = reinterpret_cast<uint32_t *>(v.w);
-    const uint4 u = *reinterpret_cast<const uint4 *>(src);
+    const uint4 u = dev::lds_v4(src);
     w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
     if constexpr (sizeof(T) == 4) {
-        const uint4 o = *reinterpret_cast<const uint4 *>(src + kApart);
+        const uint4 o = dev::lds_v4(src + kApart);
         w[4] = o.x, w[5] = o.y, w[6] = o.z, w[7] = o.w;
     } else if constexpr (!WIDE) {
-        const uint4 o = *reinterpret_cast<const uint4 *>(src + kApart);
+        const uint4 o = dev::lds_v4(src + kApart);
         const unsigned off = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;
         uint32_t all[8] = {u.x, u.y, u.z, u.w, o.x, o.y, o.z, o.w};
         // Down by whole words, two and one at a time, then by half a word.
@@ -609,9 +657,10 @@ template <typename T, int RT, bool TURNED, bool WIDE>
 __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2 : 1) adapter_many_kernel(const AdapterArgs a)
 {
     constexpr int kRows = kAdapterManyRows, kPitch = hidden_pitch<RT>(), kNear = many_near<T, RT>(), kSteps = 16 * RT / (4 * kNear);
-    constexpr int kStages = many_stages<T, RT, WIDE>(), kStage = many_stage<T, RT, WIDE>();
+    constexpr int kQuads = RT * (int)sizeof(T) / 2;  // of the first operand's registers in the second product
+    constexpr int kStages = kManyStages, kStage = many_stage<T, RT, WIDE>();
     constexpr int kOwn = 16 * kAdapterThreads * own_pieces<T, WIDE>();  // bytes of all threads' elements of one row
-    extern __shared__ __align__(16) float adapter_sums[];  // the ring, and between the products [2][kRows][kPitch] partial and whole sums
+    extern __shared__ __align__(16) float adapter_sums[];  // a ring; [2][kRows][kPitch] partial and whole sums; small rows and a ring
     __shared__ int rows[kRows];
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
@@ -627,92 +676,104 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
     const int wm = warp % 4, ws = warp / 4;  // 32 rows of the tile; a half of each step
     const bool busy = 32 * wm < count;
     bool has[4];
-    int row[4];  // g, g + 8, g + 16 and g + 24 of the warp's
+    int row[4];  // g, g + 8, g + 16 and g + 24 of the warp's; the tile's last in the place of those beyond, which are loaded but not stored
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        has[i] = 32 * wm + 8 * i + g < count;
-        row[i] = has[i] ? rows[32 * wm + 8 * i + g] : 0;
+        const int r = 32 * wm + 8 * i + g;
+        has[i] = r < count;
+        row[i] = rows[has[i] ? r : count - 1];
     }
-    float *whole = adapter_sums + kRows * kPitch;
+    float *whole = adapter_sums + whole_sums<T, RT>() / 4;
     unsigned char *ring = reinterpret_cast<unsigned char *>(adapter_sums);
 
-    // Steps of a product that this CTA takes, and their copies: the weights [a step's 64 of `length`], and from `data`
-    // this thread's elements.
+    // Steps of a product that this CTA takes.
     auto share = [&](int length, int *first, int *stop) {
         const long long steps = (length + kManyStep - 1) / kManyStep;
         *first = (int)(steps * part / parts);
         *stop = (int)(steps * (part + 1) / parts);
     };
-    auto own_column = [&](int step) { return step * kManyStep + 32 * ws + 8 * t; };
-    auto fetch = [&](auto flat, const T *weights, bool pieces, int length, const T *data, long long stride, int step, int first, int stop) {
+    const int own_column = 32 * ws + 8 * t;  // of a step
+    const uint32_t ring_at = dev::smem_u32(ring), my_slot = ring_at + threadIdx.x * 16;
+    // Goes through a product's steps: copies the weights [64 of `length` a step] and this thread's elements of the rows
+    // at `own` (from the first step's on), and calls step(step, stage) when a step's are there for all.
+    auto stream = [&](auto flat, const T *weights, bool pieces, int length, const T *const *own, bool owns, int first, int stop,
+                      auto &&step) {
         constexpr bool kFlat = decltype(flat)::value;
         constexpr int kWRows = weight_rows<T, RT, kFlat>(), kWPitch = weight_pitch<T, RT, kFlat>();
         constexpr int kLong = kFlat ? kManyStep : 16 * RT, kPiece = 16 / (int)sizeof(T), kPieces = kLong / kPiece;
-        if (step < stop) {
-            unsigned char *to = ring + (step - first) % kStages * kStage;
-            if (data) {
-                const int c = own_column(step);
+        constexpr int kAtOnce = kAdapterThreads / kPieces;  // rows of the weights that the threads copy at once
+        const int my_row = (int)threadIdx.x / kPieces, my_piece = (int)threadIdx.x % kPieces * kPiece;
+        const long long row_pitch = kFlat ? length : a.rank;
+        const T *my_weights = weights + my_row * row_pitch + my_piece;
+        const int apart = kAtOnce * (int)row_pitch;
+        const uint32_t my_weight_slot = ring_at + 4 * kOwn + my_row * kWPitch + my_piece * (int)sizeof(T);
+        auto fetch = [&](int j, int stage) {
+            if (j < stop) {
+                if (owns) {
+                    const int have = length - j * kManyStep - own_column;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    copy_own<WIDE, T>(dev::smem_u32(to + i * kOwn + threadIdx.x * 16), data + row[i] * stride + (c < length ? c : 0),
-                                      has[i] ? length - c : 0);
-            }
-            to += 4 * kOwn;
-            if (live && pieces) {
-                for (int i = threadIdx.x; i < kWRows * kPieces; i += kAdapterThreads) {
-                    const int r = i / kPieces, c = i % kPieces * kPiece;
-                    const int rank = kFlat ? r : c, at = step * kManyStep + (kFlat ? c : r);
-                    const bool there = rank < a.rank && at < length;
-                    const T *from = weights + (kFlat ? (long long)rank * length + at : (long long)at * a.rank + rank);
-                    copy_piece(dev::smem_u32(to + r * kWPitch + c * (int)sizeof(T)), there ? from : weights, there);
+                    for (int i = 0; i < 4; ++i)
+                        copy_own<WIDE, T>(my_slot + stage * kStage + i * kOwn, own[i] + (have > 0 ? (j - first) * kManyStep : 0), have);
                 }
-            } else if (live) {
-                for (int i = threadIdx.x; i < kWRows * kLong; i += kAdapterThreads) {
-                    const int r = i / kLong, c = i % kLong;
-                    const int rank = kFlat ? r : c, at = step * kManyStep + (kFlat ? c : r);
-                    T v;
-                    narrowed(0.0f, &v);
-                    if (rank < a.rank && at < length) v = weights[kFlat ? (long long)rank * length + at : (long long)at * a.rank + rank];
-                    reinterpret_cast<T *>(to + r * kWPitch)[c] = v;
+                if (pieces) {
+                    const T *from = my_weights + (kFlat ? (long long)j * kManyStep : (long long)(j * kManyStep) * a.rank);
+#pragma unroll
+                    for (int q = 0; q < (kWRows + kAtOnce - 1) / kAtOnce; ++q) {
+                        const int r = my_row + q * kAtOnce;
+                        const bool there = (kFlat ? r : my_piece) < a.rank && j * kManyStep + (kFlat ? my_piece : r) < length;
+                        if (kWRows % kAtOnce == 0 || r < kWRows)
+                            copy_piece(my_weight_slot + stage * kStage + q * kAtOnce * kWPitch, there ? from + q * apart : weights, there);
+                    }
+                } else {
+                    unsigned char *to = ring + stage * kStage + 4 * kOwn;
+                    for (int i = threadIdx.x; i < kWRows * kLong; i += kAdapterThreads) {
+                        const int r = i / kLong, c = i % kLong;
+                        const int rank = kFlat ? r : c, at = j * kManyStep + (kFlat ? c : r);
+                        T v;
+                        narrowed(0.0f, &v);
+                        if (rank < a.rank && at < length) v = weights[kFlat ? (long long)rank * length + at : (long long)at * a.rank + rank];
+                        reinterpret_cast<T *>(to + r * kWPitch)[c] = v;
+                    }
                 }
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int j = 0; j < kStages - 1; ++j) fetch(first + j, j);
+        int stage = 0;
+        for (int j = first; j < stop; ++j) {
+            // The step's copies are there, for all, and the step before it is read by all.
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncthreads();
+            fetch(j + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+            if (busy) step(j, stage * kStage);
+            stage = stage + 1 == kStages ? 0 : stage + 1;
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto arrived = [&]() {  // a step's copies, for all; and the step before it read by all
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        __syncthreads();
-    };
-    auto own_at = [&](int i, const T *data, long long stride, int length, int step, int first) {
-        const int c = own_column(step);
-        return own_of<WIDE, T>(ring + (step - first) % kStages * kStage + i * kOwn + threadIdx.x * 16,
-                               data + row[i] * stride + (c < length ? c : 0), has[i] ? length - c : 0);
-    };
-    auto weights_at = [&](int step, int first) { return ring + (step - first) % kStages * kStage + 4 * kOwn; };
 
     if (live) {
         const std::integral_constant<bool, !TURNED> flat{};
         constexpr int kWPitch = weight_pitch<T, RT, !TURNED>();
-        const T *w1 = static_cast<const T *>(a.w1) + (long long)adapter * a.rank * a.k, *x = static_cast<const T *>(a.x);
+        const T *w1 = static_cast<const T *>(a.w1) + (long long)adapter * a.rank * a.k;
         float acc[2][2 * RT][4] = {};
         int first, stop;
         share(a.k, &first, &stop);
-        for (int j = 0; j < kStages - 1; ++j) fetch(flat, w1, a.w1_pieces, a.k, x, a.x_stride, first + j, first, stop);
-        for (int step = first; step < stop; ++step) {
-            arrived();
-            fetch(flat, w1, a.w1_pieces, a.k, x, a.x_stride, step + kStages - 1, first, stop);
-            if (!busy) continue;
-            Near<T, 8> own[4];
+        const T *own[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) own[i] = own_at(i, x, a.x_stride, a.k, step, first);
-            const unsigned char *w = weights_at(step, first);
+        for (int i = 0; i < 4; ++i) own[i] = static_cast<const T *>(a.x) + row[i] * a.x_stride + (first * kManyStep + own_column < a.k ? first * kManyStep + own_column : 0);
+        const uint32_t my_weights = ring_at + 4 * kOwn + (TURNED ? own_column * kWPitch + 2 * RT * g * (int)sizeof(T) : g * kWPitch + own_column * (int)sizeof(T));
+        stream(flat, w1, a.w1_pieces, a.k, own, true, first, stop, [&](int step, uint32_t at) {
+            Near<T, 8> v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] = own_of<WIDE, T>(my_slot + at + i * kOwn, own[i] + (step - first) * kManyStep, a.k - step * kManyStep - own_column);
+            const uint32_t w = my_weights + at;
             if constexpr (!TURNED) {
 #pragma unroll
                 for (int j = 0; j < 2 * RT; ++j) {
                     Near<T, 8> col;
-                    from_shared(w + (8 * j + g) * kWPitch + (32 * ws + 8 * t) * (int)sizeof(T), &col);
+                    from_shared(w + 8 * j * kWPitch, &col);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) mma_eight<T>(acc[h][j], own[2 * h], own[2 * h + 1], col);
+                    for (int h = 0; h < 2; ++h) mma_eight<T>(acc[h][j], v[2 * h], v[2 * h + 1], col);
                 }
             } else {
                 constexpr int kC = 2 * RT < 8 ? 2 * RT : 8;
@@ -721,15 +782,15 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
                     Near<T, kC> in[8];
                     Near<T, 8> col[kC];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) from_shared(w + (32 * ws + 8 * t + i) * kWPitch + (2 * RT * g + c) * (int)sizeof(T), &in[i]);
+                    for (int i = 0; i < 8; ++i) from_shared(w + i * kWPitch + c * (int)sizeof(T), &in[i]);
                     turned<T, 8, kC>(in, col);
 #pragma unroll
                     for (int j = 0; j < kC; ++j)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) mma_eight<T>(acc[h][c + j], own[2 * h], own[2 * h + 1], col[j]);
+                        for (int h = 0; h < 2; ++h) mma_eight<T>(acc[h][c + j], v[2 * h], v[2 * h + 1], col[j]);
                 }
             }
-        }
+        });
         __syncthreads();  // the ring is read; what was copied ahead of it, nothing
         // The two halves of the steps: the second's sums beside, where the whole ones will be.
         float *mine = (ws ? whole : adapter_sums) + 32 * wm * kPitch;
@@ -744,9 +805,9 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
                 mine[(16 * h + g + 8) * kPitch + r1] = acc[h][j][3];
             }
         __syncthreads();
-        constexpr int kQuads = 4 * RT;  // of a row
-        for (int i = threadIdx.x; i < count * kQuads; i += kAdapterThreads) {
-            const int offset = i / kQuads * kPitch + i % kQuads * 4;
+        constexpr int kFours = 4 * RT;  // of a row
+        for (int i = threadIdx.x; i < count * kFours; i += kAdapterThreads) {
+            const int offset = i / kFours * kPitch + i % kFours * 4;
             float4 *at = reinterpret_cast<float4 *>(adapter_sums + offset);
             const float4 u = *reinterpret_cast<const float4 *>(whole + offset);
             *at = make_float4(at->x + u.x, at->y + u.y, at->z + u.z, at->w + u.w);
@@ -754,10 +815,10 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
         cluster_arrive();
         cluster_wait();
         const uint32_t sums = dev::smem_u32(adapter_sums);
-        for (int i = threadIdx.x; i < kRows * kQuads; i += kAdapterThreads) {
-            const int offset = i / kQuads * kPitch + i % kQuads * 4;
+        for (int i = threadIdx.x; i < kRows * kFours; i += kAdapterThreads) {
+            const int offset = i / kFours * kPitch + i % kFours * 4;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (i < count * kQuads) {
+            if (i < count * kFours) {
                 v = load_cluster(dev::mapa_cluster(sums + 4 * offset, 0));
                 for (int p = 1; p < parts; ++p) {
                     const float4 u = load_cluster(dev::mapa_cluster(sums + 4 * offset, (uint32_t)p));
@@ -775,92 +836,165 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
             if (r % parts == part) a.hidden[(long long)rows[r] * a.rank + i % a.rank] = live ? whole[r * kPitch + i % a.rank] : 0.0f;
         }
     }
-    // The first operand's rows, as in adapter_products_kernel.
-    Near<T, kNear> h[4][kSteps];
-    float s[4] = {};
+    const int strips = (a.n + 31) / 32;
+    const int first = (int)((long long)strips * part / parts), stop = (int)((long long)strips * (part + 1) / parts);
     if (live) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s[i] = a.scale ? a.scale[adapter] : 1.0f;
-            float v[kSteps][kNear];
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                for (int q = 0; q < kNear; q += 4) {
-                    const float4 u = *reinterpret_cast<const float4 *>(whole + (32 * wm + 8 * i + g) * kPitch + 4 * kNear * k + kNear * t + q);
-                    v[k][q] = u.x, v[k][q + 1] = u.y, v[k][q + 2] = u.z, v[k][q + 3] = u.w;
-                }
-            const float factor = narrow_factor<T, kSteps * kNear>(&v[0][0], &s[i]);
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-                for (int q = 0; q < kNear; q += 2) {
-                    if constexpr (sizeof(T) == 4) {
-                        h[i][k].w[q] = v[k][q];
-                        h[i][k].w[q + 1] = v[k][q + 1];
-                    } else {
-                        h[i][k].w[q / 2] = packed(v[k][q] * factor, v[k][q + 1] * factor, T());
-                    }
-                }
-        }
         cluster_wait();
-        __syncthreads();
-    }
-    if (live || a.base != a.y) {
-        const std::integral_constant<bool, TURNED> flat{};
-        constexpr int kWPitch = weight_pitch<T, RT, TURNED>();
-        const T *w2 = static_cast<const T *>(a.w2) + (live ? (long long)adapter * a.rank * a.n : 0), *base = static_cast<const T *>(a.base);
-        int first, stop;
-        share(a.n, &first, &stop);
-        for (int j = 0; j < kStages - 1; ++j) fetch(flat, w2, a.w2_pieces, a.n, base, a.base_stride, first + j, first, stop);
-        for (int step = first; step < stop; ++step) {
-            arrived();
-            fetch(flat, w2, a.w2_pieces, a.n, base, a.base_stride, step + kStages - 1, first, stop);
-            if (!busy) continue;
-            float acc[2][4][4] = {};
-            if (live) {
-                const unsigned char *w = weights_at(step, first);
-                if constexpr (!TURNED) {
+        // The small rows in the activations' type (as in adapter_products_kernel), as the first operand's registers lie
+        // in a lane: 16 rows by each warp.
+        unsigned char *const small = ring;
+        const char **const base_row = reinterpret_cast<const char **>(small + kRows * 16 * RT * (int)sizeof(T));
+        char **const y_row = reinterpret_cast<char **>(small + kRows * (16 * RT * (int)sizeof(T) + 8));
+        float *const factors = reinterpret_cast<float *>(y_row + kRows);
+        {
+            float v[2][kSteps][kNear];
 #pragma unroll
-                    for (int k = 0; k < kSteps; ++k)
+            for (int i = 0; i < 2; ++i) {
+                const int r = 16 * warp + 8 * i + g;
+                float s = a.scale ? a.scale[adapter] : 1.0f;
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            Near<T, kNear> col;
-                            from_shared(w + (32 * ws + 4 * g + q) * kWPitch + (4 * kNear * k + kNear * t) * (int)sizeof(T), &col);
+                for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                            for (int m = 0; m < 2; ++m) mma_near<T>(acc[m][q], h[2 * m][k], h[2 * m + 1][k], col);
-                        }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < kSteps; ++k) {
-                        Near<T, 4> in[kNear];
-                        Near<T, kNear> col[4];
-#pragma unroll
-                        for (int r = 0; r < kNear; ++r)
-                            from_shared(w + (4 * kNear * k + kNear * t + r) * kWPitch + (32 * ws + 4 * g) * (int)sizeof(T), &in[r]);
-                        turned<T, kNear, 4>(in, col);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int m = 0; m < 2; ++m) mma_near<T>(acc[m][q], h[2 * m][k], h[2 * m + 1][k], col[q]);
+                    for (int q = 0; q < kNear; q += 4) {
+                        const float4 u = *reinterpret_cast<const float4 *>(whole + r * kPitch + 4 * kNear * k + kNear * t + q);
+                        v[i][k][q] = u.x, v[i][k][q + 1] = u.y, v[i][k][q + 2] = u.z, v[i][k][q + 3] = u.w;
                     }
+                const float factor = narrow_factor<T, kSteps * kNear>(&v[i][0][0], &s);
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                    for (int q = 0; q < kNear; ++q) v[i][k][q] *= factor;
+                if (t == 0) {
+                    const long long at = rows[r < count ? r : count - 1];
+                    factors[r] = s;
+                    base_row[r] = static_cast<const char *>(a.base) + at * a.base_stride * (int)sizeof(T);
+                    y_row[r] = static_cast<char *>(a.y) + at * a.y_stride * (int)sizeof(T);
                 }
             }
-            const int n0 = own_column(step), have = a.n - n0;
+            uint4 *const to = reinterpret_cast<uint4 *>(small) + warp * kQuads * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v[8];
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int q = 0; q < kNear; q += 8 / (int)sizeof(T)) {
+                    uint4 u;
+                    if constexpr (sizeof(T) == 4)
+                        u = make_uint4(__float_as_uint(v[0][k][q]), __float_as_uint(v[1][k][q]), __float_as_uint(v[0][k][q + 1]), __float_as_uint(v[1][k][q + 1]));
+                    else
+                        u = make_uint4(packed(v[0][k][q], v[0][k][q + 1], T()), packed(v[1][k][q], v[1][k][q + 1], T()),
+                                       packed(v[0][k][q + 2], v[0][k][q + 3], T()), packed(v[1][k][q + 2], v[1][k][q + 3], T()));
+                    to[(k * kNear + q) / (8 / (int)sizeof(T)) * 32] = u;
+                }
+        }
+        __syncthreads();  // they are there, and the sums read
+        const T *w2 = static_cast<const T *>(a.w2) + (long long)adapter * a.rank * a.n;
+        const bool adds = a.base != nullptr;
+        const int groups = (count + 31) / 32;  // of rows
+        const uint32_t slots = dev::smem_u32(ring + small_rows<T, RT>()) + threadIdx.x * 16;
+        const uint32_t small_at = dev::smem_u32(small) + lane * 16;
+        // As the second operand, the lane's columns of a strip are 8 (g / 2) + g % 2 and every second from there; as the
+        // result, 8t to 8t + 7, two of each instruction's.
+        const unsigned odd = g % 2 ? 0x7632 : 0x5410;
+        constexpr int kRaw = TURNED ? kNear : 4, kRawNear = TURNED ? 8 : kNear;
+        using Raw = Near<T, kRawNear>[kSteps][kRaw];
+        auto weights_of = [&](int strip, Raw &raw) {
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                for (int q = 0; q < kRaw; ++q) {
+                    const int rank = 4 * kNear * k + kNear * t + (TURNED ? q : 0), column = 32 * strip + 8 * (g / 2) + (TURNED ? 0 : g % 2 + 2 * q);
+                    const T *from = w2 + (TURNED ? (long long)rank * a.n + column : (long long)column * a.rank + rank);
+                    const int have = strip >= stop ? 0 : TURNED ? (rank < a.rank ? a.n - column : 0) : (column < a.n ? a.rank - rank : 0);
+                    raw[k][q] = a.w2_wide ? near<true, T, kRawNear>(from, have) : near<false, T, kRawNear>(from, have);
+                }
+        };
+        int next_strip = first + warp, next_group = 0, next_stage = 0;
+        auto fetch = [&]() {
+            if (next_strip < stop && adds) {
+                const int c = 32 * next_strip + 8 * t, have = a.n - c;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    copy_own<WIDE, T>(slots + (next_stage * 4 + i) * kOwn,
+                                      reinterpret_cast<const T *>(base_row[32 * next_group + 8 * i + g] + (have > 0 ? c : 0) * (int)sizeof(T)), have);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            next_stage = next_stage + 1 == kManyAhead ? 0 : next_stage + 1;
+            if (++next_group == groups) {
+                next_group = 0;
+                next_strip += kAdapterThreads / 32;
+            }
+        };
+        for (int i = 0; i < kManyAhead - 1; ++i) fetch();
+        constexpr bool kAhead = !TURNED || RT <= 2;  // the coming strip's weights too, where registers are left
+        Raw raw;
+        if (kAhead) weights_of(first + warp, raw);
+        int stage = 0;
+        for (int strip = first + warp; strip < stop; strip += kAdapterThreads / 32) {
+            if (!kAhead) weights_of(strip, raw);
+            Near<T, kNear> w[kSteps][4];
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    v[q] = acc[i / 2][q][i % 2 * 2] * s[i];
-                    v[4 + q] = acc[i / 2][q][i % 2 * 2 + 1] * s[i];
-                }
-                if (a.base) {
-                    const Near<T, 8> old = own_at(i, base, a.base_stride, a.n, step, first);
+                    if constexpr (!TURNED) {
+                        w[k][q] = raw[k][q];
+                    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] = live ? old.at(q) + v[q] : old.at(q);
+                        for (int r = 0; r < kNear; ++r) w[k][q].w[r] = g % 2 ? raw[k][r].w[2 * q + 1] : raw[k][r].w[2 * q];
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < kNear / 2; ++r) w[k][q].w[r] = __byte_perm(raw[k][2 * r].w[q], raw[k][2 * r + 1].w[q], odd);
+                    }
                 }
-                if (has[i]) store_near<WIDE, T>(static_cast<T *>(a.y) + row[i] * a.y_stride + n0, v, have);
+            if (kAhead) weights_of(strip + kAdapterThreads / 32, raw);
+            const int column = 32 * strip + 8 * t, have = a.n - column;
+            for (int group = 0; group < groups; ++group) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kManyAhead - 2) : "memory");
+                fetch();
+                float acc[2][4][4];
+#pragma unroll
+                for (int j = 0; j < kQuads; ++j)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const uint4 h = dev::lds_v4(small_at + ((2 * group + m) * kQuads + j) * 512);
+                        constexpr int kPairs = kNear * (int)sizeof(T) / 8;  // of a lane's weights of a column
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            mma_quad<T>(acc[m][q], h, w[j / kPairs][q].w[2 * (j % kPairs)], w[j / kPairs][q].w[2 * (j % kPairs) + 1], j == 0);
+                    }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 32 * group + 8 * i + g;
+                    float2 v[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = make_float2(acc[i / 2][q][i % 2 * 2], acc[i / 2][q][i % 2 * 2 + 1]);
+                    const float2 factor = make_float2(factors[r], factors[r]);
+                    if (adds) {
+                        const Near<T, 8> old = own_of<WIDE, T>(slots + (stage * 4 + i) * kOwn,
+                                                               WIDE ? nullptr : reinterpret_cast<const T *>(base_row[r]) + column, have);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[q] = __ffma2_rn(v[q], factor, make_float2(old.at(2 * q), old.at(2 * q + 1)));
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) v[q] = __fmul2_rn(v[q], factor);
+                    }
+                    store_near<WIDE, T>(reinterpret_cast<T *>(y_row[r] + column * (int)sizeof(T)), reinterpret_cast<const float *>(v), r < count ? have : 0);
+                }
+                stage = stage + 1 == kManyAhead ? 0 : stage + 1;
+            }
+        }
+    } else if (a.base != a.y) {
+        // Rows without an adapter: base, or zeros.
+        const int from = 32 * first, to = 32 * stop < a.n ? 32 * stop : a.n;
+        for (int r = warp; r < count; r += kAdapterThreads / 32) {
+            const T *old = static_cast<const T *>(a.base) + rows[r] * a.base_stride;
+            T *y = static_cast<T *>(a.y) + rows[r] * a.y_stride;
+            for (int c = from + 8 * lane; c < to; c += 256) {
+                const int have = to - c < 8 ? to - c : 8;
+                const Near<T, 8> u = near<WIDE, T, 8, false>(old + c, a.base ? have : 0);
+                float v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = u.at(q);
+                store_near<WIDE, T>(y + c, v, have);
             }
         }
     }
