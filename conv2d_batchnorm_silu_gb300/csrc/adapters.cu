@@ -187,17 +187,31 @@ Layout layout_of(const AdapterProblem &p, bool ordered, int k, int n, int sm_cou
 {
     Layout l{};
     l.few = !ordered && p.m <= kFew;
-    // Tiles of 128 rows read an adapter's weights an eighth as often; where an adapter has few rows, on average over all
-    // there are, most of such a tile's warps would have none.
-    l.many = p.m > kFew && p.m >= 24LL * p.adapters;
+    // Tiles of 128 rows read an adapter's weights an eighth as often, which pays the sooner the higher the rank is
+    // (4096x4096, 16 / 128 rows a tile: rank 16 with 1200 rows 22.3 / 21.6 us, with 2400 30.3 / 29.1; rank 64 with 600 rows
+    // 30.9 / 31.8, with 1200 60 / 34); where an adapter has few rows, on average over all there are, most of such a
+    // tile's warps would have none.
+    l.many = p.m > kFew && p.m >= 24LL * p.adapters && (long long)p.m * (adapter_rank_tiles(p.rank) + 1) >= 4096;
     l.tile_rows = l.many ? kAdapterManyRows : kAdapterFewRows;
     const int full = (p.m + l.tile_rows - 1) / l.tile_rows;
     l.tiles = full + (p.adapters + 1 < p.m ? p.adapters + 1 : p.m);
     l.clusters = l.few ? p.m : l.tiles;
-    // As many CTAs a tile as the SMs want, while each has some steps of 32 elements for its warps.
+    // CTAs a tile: what takes the fewest rounds of CTAs for its part of a tile, the fewest of those that do (128 rows of
+    // 64 adapters, 4096x4096: 4 CTAs 9.8 us, 8 12.8; one row: 4 CTAs 7.3, 8 6.1), while each has some steps of 32
+    // elements for its warps.
+    const int ranks = adapter_rank_tiles(p.rank);
+    const long long room = (long long)sm_count * (l.many ? (ranks <= 4 && p.dtype != kF32 ? 2 : 1) : ranks == 1 ? 3 : ranks == 2 ? 2 : 1);
+    const long long about = full + (l.many ? 0 : p.adapters < p.m ? p.adapters : p.m);  // tiles
     const int steps = ((k > n ? k : n) + 31) / 32;
     l.size = 1;
-    while (l.size < 8 && steps >= 16 * l.size && (l.few ? 1 : full) * l.size < 3 * sm_count) l.size *= 2;
+    long long rounds = (about + room - 1) / room;
+    for (int size = 2; size <= 8 && steps >= 8 * size; size *= 2) {
+        const long long these = (about * size + room - 1) / room;
+        if (these * l.size < rounds * size) {
+            rounds = these;
+            l.size = size;
+        }
+    }
     return l;
 }
 
