@@ -35,18 +35,21 @@ struct OrderArgs {
     const int *index;
     int *order, *starts, *tile_count;
     AdapterTile *tiles;
+    AdapterTile *steps;  // nullable: tiles of kTcStepRows rows, and where each adapter's begin
+    int *step_starts;
     int m, adapters, tile_rows;
 };
 
 __global__ void __launch_bounds__(kWindow) adapter_order_kernel(const OrderArgs a)
 {
-    extern __shared__ int order_bins[];  // [5][bins]
+    extern __shared__ int order_bins[];  // [6][bins]
     __shared__ unsigned keys[kWindow];
     __shared__ unsigned long long warp_sums[32];
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
     const int bins = a.adapters + 1, tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    int *total = order_bins, *before = total + bins, *head = before + bins, *base = head + bins, *tile_base = base + bins;
+    int *total = order_bins, *before = total + bins, *head = before + bins, *base = head + bins, *tile_base = base + bins,
+        *step_base = tile_base + bins;
     for (int i = tid; i < bins; i += kWindow) total[i] = before[i] = 0;
     __syncthreads();
     auto of = [&](int i) {
@@ -90,12 +93,14 @@ __global__ void __launch_bounds__(kWindow) adapter_order_kernel(const OrderArgs 
     const bool here = key != 0xffffffffu;
     const int mine = (int)(key >> 10);
     if (here && (tid == 0 || (int)(keys[tid - 1] >> 10) != mine)) head[mine] = tid;
-    // Exclusive sums of rows and of tiles over the adapters before.
+    // Exclusive sums of rows (21 bits), tiles and steps (21 each) over the adapters before.
     const int each = (bins + kWindow - 1) / kWindow;
     auto amount = [&](int b) {
         const unsigned rows = (unsigned)total[b];
-        return (unsigned long long)((rows + a.tile_rows - 1) / a.tile_rows) << 32 | rows;
+        return (unsigned long long)((rows + kTcStepRows - 1) / kTcStepRows) << 42 |
+               (unsigned long long)((rows + a.tile_rows - 1) / a.tile_rows) << 21 | rows;
     };
+    constexpr unsigned kField = (1u << 21) - 1;
     unsigned long long sum = 0;
     for (int b = tid * each; b < (tid + 1) * each && b < bins; ++b) sum += amount(b);
     unsigned long long scan = sum;
@@ -116,14 +121,16 @@ __global__ void __launch_bounds__(kWindow) adapter_order_kernel(const OrderArgs 
     __syncthreads();
     unsigned long long run = scan - sum + (warp ? warp_sums[warp - 1] : 0ull);
     for (int b = tid * each; b < (tid + 1) * each && b < bins; ++b) {
-        base[b] = (int)(unsigned)run;
-        tile_base[b] = (int)(run >> 32);
-        if (blockIdx.x == 0) a.starts[b] = (int)(unsigned)run;
+        base[b] = (int)((unsigned)run & kField);
+        tile_base[b] = (int)((unsigned)(run >> 21) & kField);
+        step_base[b] = (int)(run >> 42);
+        if (blockIdx.x == 0) a.starts[b] = base[b];
+        if (blockIdx.x == 0 && a.steps) a.step_starts[b] = step_base[b];
         run += amount(b);
     }
     if (blockIdx.x == 0 && tid == 0) {
         a.starts[bins] = a.m;
-        *a.tile_count = (int)(warp_sums[31] >> 32);
+        *a.tile_count = (int)((unsigned)(warp_sums[31] >> 21) & kField);
     }
     __syncthreads();
     if (!here) return;
@@ -133,14 +140,18 @@ __global__ void __launch_bounds__(kWindow) adapter_order_kernel(const OrderArgs 
         const int left = total[mine] - rank;
         a.tiles[tile_base[mine] + rank / a.tile_rows] = AdapterTile{mine, at, left < a.tile_rows ? left : a.tile_rows, 0};
     }
+    if (a.steps && rank % kTcStepRows == 0 && mine < a.adapters) {
+        const int left = total[mine] - rank;
+        a.steps[step_base[mine] + rank / kTcStepRows] = AdapterTile{mine, at, left < kTcStepRows ? left : kTcStepRows, 0};
+    }
 }
 
 cudaError_t order_launch(const OrderArgs &a, cudaStream_t stream)
 {
-    const int smem = 5 * 4 * (a.adapters + 1);
+    const int smem = 6 * 4 * (a.adapters + 1);
     static bool allowed[kMaxDevices] = {};
     if (smem > 40 * 1024) {
-        const cudaError_t e = allow_dynamic_smem(adapter_order_kernel, 5 * 4 * (kMostAdapters + 1), allowed);
+        const cudaError_t e = allow_dynamic_smem(adapter_order_kernel, 6 * 4 * (kMostAdapters + 1), allowed);
         if (e != cudaSuccess) return e;
     }
     return launch_overlapped(adapter_order_kernel, dim3((unsigned)((a.m + kWindow - 1) / kWindow)), dim3(kWindow), smem, stream, 1, a);
@@ -162,7 +173,14 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_join_kernel(const Ada
             float v = 0.0f;
             if (first < last) {
                 v = a.partial[(2LL * c0 + 1) * all + i];
-                for (int c = c0 + 1; c <= c1; ++c) v += a.partial[2LL * c * all + i];
+                // Eight loads at once, added in their order.
+                for (int c = c0 + 1; c <= c1; c += 8) {
+                    float u[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) u[j] = c + j <= c1 ? a.partial[2LL * (c + j) * all + i] : 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v += u[j];
+                }
             }
             if (i < of_a)
                 a.da[adapter * of_a + i] = v;
@@ -218,33 +236,45 @@ Layout layout_of(const AdapterProblem &p, bool ordered, int k, int n, int sm_cou
 constexpr long long up16(long long v) { return (v + 15) / 16 * 16; }
 
 struct Workspace {
-    long long starts, order, tiles, dhidden, partial, bytes;
-    int chunks, chunk_rows;
+    long long starts, order, tiles, step_starts, steps, operands, dhidden, partial, bytes;
+    int chunks, chunk_rows, most_steps;
 };
 
-// Chunks of rows for the weights' gradients: enough CTAs for the SMs, 128 rows each at least, and at most 2048, which
-// keeps the runs of additions in the matrix instruction's accumulators short.
-Workspace workspace_of(const AdapterProblem &p, bool gradient, int sm_count)
+// Chunks of `units` rows or steps for the weights' gradients: so many CTAs in all, `least` units each at least, and `most`
+// at most, which also keeps the runs of additions in the matrix instruction's accumulators short.
+void chunks_of(const AdapterProblem &p, int columns, int ctas, long long units, int least, int most, int *chunks, int *chunk_units)
+{
+    const long long strips = (p.k + columns - 1) / columns + (p.n + columns - 1) / columns;
+    long long c = (ctas + strips - 1) / strips;
+    if (c > (units + least - 1) / least) c = (units + least - 1) / least;
+    if (c < (units + most - 1) / most) c = (units + most - 1) / most;
+    if (c < 1) c = 1;
+    *chunk_units = (int)((units + c - 1) / c);
+    *chunks = (int)((units + *chunk_units - 1) / *chunk_units);
+}
+
+// `tc`: with the chunks of adapter_tc_weights_kernel; the bytes are enough for either kernel.
+Workspace workspace_of(const AdapterProblem &p, bool gradient, bool tc, int sm_count)
 {
     Workspace w{};
     const long long rows = p.m;
     w.starts = 16;
     w.order = w.starts + up16(4LL * (p.adapters + 2));
     w.tiles = w.order + up16(4 * rows);
-    w.dhidden = w.tiles + 16LL * ((rows + kAdapterFewRows - 1) / kAdapterFewRows + p.adapters + 1);
-    w.bytes = w.dhidden;
-    if (gradient) {
-        const int columns = adapter_columns(p.rank);
-        const long long strips = (p.k + columns - 1) / columns + (p.n + columns - 1) / columns;
-        long long chunks = (4LL * sm_count + strips - 1) / strips;
-        if (chunks > (rows + 127) / 128) chunks = (rows + 127) / 128;
-        if (chunks < (rows + 2047) / 2048) chunks = (rows + 2047) / 2048;
-        if (chunks < 1) chunks = 1;
-        w.chunk_rows = (int)((rows + chunks - 1) / chunks);
-        if (w.chunk_rows < 1) w.chunk_rows = 1;
-        w.chunks = (int)((rows + w.chunk_rows - 1) / w.chunk_rows);
+    w.step_starts = w.tiles + 16LL * ((rows + kAdapterFewRows - 1) / kAdapterFewRows + p.adapters + 1);
+    w.bytes = w.step_starts;
+    if (gradient && rows > 0) {
+        int chunks[2], chunk_rows[2];
+        w.most_steps = (int)(rows / kTcStepRows + (p.adapters < rows ? p.adapters : rows));
+        chunks_of(p, adapter_columns(p.rank), 3 * sm_count, rows, 64, kAdapterChunkRows, &chunks[0], &chunk_rows[0]);
+        chunks_of(p, 128, 2 * sm_count, w.most_steps, 1, kTcChunkSteps, &chunks[1], &chunk_rows[1]);
+        w.chunks = chunks[tc];
+        w.chunk_rows = chunk_rows[tc];
+        w.steps = w.step_starts + up16(4LL * (p.adapters + 1));
+        w.operands = (w.steps + 16LL * w.most_steps + 127) / 128 * 128;
+        w.dhidden = w.operands + 2LL * w.most_steps * adapter_tc_operand(p.rank);
         w.partial = w.dhidden + up16(4 * rows * p.rank);
-        w.bytes = w.partial + 8LL * w.chunks * p.rank * ((long long)p.k + p.n);
+        w.bytes = w.partial + 8LL * (chunks[0] > chunks[1] ? chunks[0] : chunks[1]) * p.rank * ((long long)p.k + p.n);
     }
     return w;
 }
@@ -282,7 +312,7 @@ OrderArgs order_args(const AdapterProblem &p, const Workspace &w, const Layout &
 long long adapters_workspace_bytes(const AdapterProblem &p, bool gradient, int sm_count)
 {
     if (!gradient && p.m <= kFew) return 0;
-    return workspace_of(p, gradient, sm_count).bytes;
+    return workspace_of(p, gradient, false, sm_count).bytes;
 }
 
 cudaError_t adapters_launch(const AdapterProblem &p, int sm_count, cudaStream_t stream)
@@ -314,7 +344,7 @@ cudaError_t adapters_launch(const AdapterProblem &p, int sm_count, cudaStream_t 
     a.w1_pieces = p.k * size % 16 == 0 && on_boundary(p.a, 0, size);
     a.y_wide = p.n % 8 == 0 && on_boundary(p.y.data, p.y.stride, size) && on_boundary(p.base.data, p.base.stride, size);
     if (!l.few) {
-        const Workspace w = workspace_of(p, false, sm_count);
+        const Workspace w = workspace_of(p, false, false, sm_count);
         const OrderArgs o = order_args(p, w, l, static_cast<char *>(p.workspace));
         const cudaError_t e = order_launch(o, stream);
         if (e != cudaSuccess) return e;
@@ -329,9 +359,16 @@ cudaError_t adapters_grad_launch(const AdapterProblem &p, int sm_count, cudaStre
 {
     const int size = dtype_size(p.dtype);
     const Layout l = layout_of(p, true, p.n, p.k, sm_count);
-    const Workspace w = workspace_of(p, true, sm_count);
+    const bool x_wide = p.k % 8 == 0 && on_boundary(p.x.data, p.x.stride, size), dy_wide = p.n % 8 == 0 && on_boundary(p.dy.data, p.dy.stride, size);
+    const bool tc = p.dtype == kBf16 && x_wide && dy_wide && p.x.stride >= p.k && p.dy.stride >= p.n && adapter_rank_tiles(p.rank) <= 4 &&
+                    p.m >= 1024 && p.m >= 128LL * p.adapters;
+    const Workspace w = workspace_of(p, true, tc, sm_count);
     char *work = static_cast<char *>(p.workspace);
-    const OrderArgs o = order_args(p, w, l, work);
+    OrderArgs o = order_args(p, w, l, work);
+    if (tc) {
+        o.steps = reinterpret_cast<AdapterTile *>(work + w.steps);
+        o.step_starts = reinterpret_cast<int *>(work + w.step_starts);
+    }
     cudaError_t e = order_launch(o, stream);
     if (e != cudaSuccess) return e;
     // dhidden and dx: the two products with dy, B and A.
@@ -374,24 +411,31 @@ cudaError_t adapters_grad_launch(const AdapterProblem &p, int sm_count, cudaStre
     g.scale = p.scale;
     g.order = o.order;
     g.starts = o.starts;
+    g.steps = o.steps;
+    g.step_starts = o.step_starts;
+    g.operands = reinterpret_cast<uint4 *>(work + w.operands);
+    g.most_steps = w.most_steps;
     g.da = p.da;
     g.db = p.db;
     g.partial = reinterpret_cast<float *>(work + w.partial);
+    g.rows = p.m;
     g.k = p.k;
     g.n = p.n;
     g.rank = p.rank;
     g.adapters = p.adapters;
     g.chunks = w.chunks;
     g.chunk_rows = w.chunk_rows;
-    g.x_wide = p.k % 8 == 0 && on_boundary(p.x.data, p.x.stride, size);
-    g.dy_wide = p.n % 8 == 0 && on_boundary(p.dy.data, p.dy.stride, size);
-    switch (p.dtype) {
+    g.x_wide = x_wide;
+    g.dy_wide = dy_wide;
+    if (tc) e = adapter_tc_weights_launch(g, stream);
+    else switch (p.dtype) {
     case kF32: e = adapter_weights_launch<float>(g, stream); break;
     case kBf16: e = adapter_weights_launch<__nv_bfloat16>(g, stream); break;
     default: e = adapter_weights_launch<__half>(g, stream); break;
     }
     if (e != cudaSuccess) return e;
-    const long long blocks = ((long long)p.rank * ((long long)p.k + p.n) + 4 * kAdapterThreads - 1) / (4 * kAdapterThreads);
+    if (tc) g.starts = g.step_starts;
+    const long long blocks = ((long long)p.rank * ((long long)p.k + p.n) + kAdapterThreads - 1) / kAdapterThreads;
     return launch_overlapped(adapter_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096), (unsigned)p.adapters),
                              dim3(kAdapterThreads), 0, stream, 1, g);
 }

@@ -37,18 +37,29 @@ struct AdapterGradArgs {
     const void *x, *dy;
     const float *hidden, *dhidden;  // [m][rank]
     const float *scale;             // nullable
-    const int *order, *starts;      // starts [adapters + 2]
+    const int *order, *starts;      // starts [adapters + 2]: where each adapter's rows begin in the order
+    // adapter_tc_weights_kernel: steps of 64 rows of one adapter, where each adapter's begin, and the steps' second
+    // operands [2][most_steps], hidden's and dhidden's.  The join's starts are then step_starts, its chunks of steps.
+    const AdapterTile *steps;
+    const int *step_starts;
+    uint4 *operands;
+    int most_steps;
     float *da, *db;                 // [adapters][rank][k], [adapters][n][rank]
     float *partial;                 // [2 * chunks][rank * (k + n)]
     long long x_stride, dy_stride;
-    int k, n, rank, adapters;
+    int rows, k, n, rank, adapters;
     int chunks, chunk_rows;
     bool x_wide, dy_wide;
 };
 
 constexpr int kAdapterThreads = 256;
 constexpr int kAdapterFewRows = 16, kAdapterManyRows = 128;  // of a tile
-constexpr int kAdapterColumns = 64;                         // of a weight gradient's CTA, 32 for ranks above 32
+constexpr int kAdapterColumns = 512;                        // of a weight gradient's CTA, half for ranks above 32
+constexpr int kAdapterChunkRows = 1024;                     // of its chunk at most
+
+constexpr int kTcStepRows = 64, kTcChunkSteps = 16;          // of adapter_tc_weights_kernel's steps and chunks
+// Bytes of a step's second operand: three parts of each rank, 64 rows.
+inline long long adapter_tc_operand(int rank) { return 3LL * 16 * (rank <= 16 ? 1 : rank <= 32 ? 2 : 4) * 128; }
 
 inline int adapter_rank_tiles(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 inline int adapter_columns(int rank) { return rank <= 32 ? kAdapterColumns : kAdapterColumns / 2; }
@@ -59,5 +70,8 @@ cudaError_t adapter_products_launch(const AdapterArgs &a, bool transposed, bool 
                                     cudaStream_t stream);
 template <typename T>
 cudaError_t adapter_weights_launch(const AdapterGradArgs &a, cudaStream_t stream);
+
+// On the tensor cores' own memory (tc_adapters.cu): bf16, wide rows at least their width apart, ranks up to 64.
+cudaError_t adapter_tc_weights_launch(const AdapterGradArgs &a, cudaStream_t stream);
 
 }  // namespace cbs

@@ -603,38 +603,43 @@ __device__ __forceinline__ void copy_word(uint32_t dst, const void *src, bool th
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 
-// Eight elements from p, `have` of them there, to their thread's pieces of 16 bytes, kAdapterThreads pieces apart.
-template <bool WIDE, typename T>
+// N elements from p, `have` of them there, to their thread's pieces of 16 bytes, kAdapterThreads pieces apart.
+template <bool WIDE, typename T, int N = 8>
 __device__ __forceinline__ void copy_own(uint32_t dst, const T *p, int have)
 {
-    constexpr int kApart = 16 * kAdapterThreads;
-    if constexpr (WIDE) {
+    constexpr int kApart = 16 * kAdapterThreads, kBytes = N * (int)sizeof(T);
+    if constexpr (WIDE && kBytes == 8) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(p), "r"(have > 0 ? 8 : 0) : "memory");
+    } else if constexpr (WIDE) {
 #pragma unroll
-        for (int i = 0; i < own_pieces<T, true>(); ++i) copy_piece(dst + i * kApart, reinterpret_cast<const char *>(p) + 16 * i, have > 0);
+        for (int i = 0; i < kBytes / 16; ++i) copy_piece(dst + i * kApart, reinterpret_cast<const char *>(p) + 16 * i, have > 0);
     } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) copy_word(dst + i / 4 * kApart + i % 4 * 4, p + (i < have ? i : 0), i < have);
+        for (int i = 0; i < N; ++i) copy_word(dst + i / 4 * kApart + i % 4 * 4, p + (i < have ? i : 0), i < have);
     } else {
         // The aligned pieces that hold some of them.
         const uintptr_t at = reinterpret_cast<uintptr_t>(p), from = at & ~(uintptr_t)15;
-        const int bytes = (int)(at - from) + 2 * (have < 8 ? have : 8);
+        const int bytes = (int)(at - from) + 2 * (have < N ? have : N);
         copy_piece(dst, reinterpret_cast<const void *>(from), have > 0);
         copy_piece(dst + kApart, reinterpret_cast<const void *>(bytes > 16 ? from + 16 : from), have > 0 && bytes > 16);
     }
 }
 // They again, from the pieces at `src`, zeros beyond `have`.
-template <bool WIDE, typename T>
-__device__ __forceinline__ Near<T, 8> own_of(uint32_t src, const T *p, int have)
+template <bool WIDE, typename T, int N = 8>
+__device__ __forceinline__ Near<T, N> own_of(uint32_t src, const T *p, int have)
 {
-    constexpr int kApart = 16 * kAdapterThreads;
-    Near<T, 8> v;
+    constexpr int kApart = 16 * kAdapterThreads, kWords = N * (int)sizeof(T) / 4;
+    Near<T, N> v;
     uint32_t *w = reinterpret_cast<uint32_t *>(v.w);
     const uint4 u = dev::lds_v4(src);
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-    if constexpr (sizeof(T) == 4) {
-        const uint4 o = dev::lds_v4(src + kApart);
-        w[4] = o.x, w[5] = o.y, w[6] = o.z, w[7] = o.w;
-    } else if constexpr (!WIDE) {
+    if constexpr (sizeof(T) == 4 || WIDE) {
+        w[0] = u.x, w[1] = u.y;
+        if constexpr (kWords >= 4) w[2] = u.z, w[3] = u.w;
+        if constexpr (kWords == 8) {
+            const uint4 o = dev::lds_v4(src + kApart);
+            w[4] = o.x, w[5] = o.y, w[6] = o.z, w[7] = o.w;
+        }
+    } else {
         const uint4 o = dev::lds_v4(src + kApart);
         const unsigned off = (unsigned)reinterpret_cast<uintptr_t>(p) & 15u;
         uint32_t all[8] = {u.x, u.y, u.z, u.w, o.x, o.y, o.z, o.w};
@@ -644,7 +649,7 @@ __device__ __forceinline__ Near<T, 8> own_of(uint32_t src, const T *p, int have)
 #pragma unroll
         for (int i = 0; i < 5; ++i) all[i] = off & 4 ? all[i + 1] : all[i];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kWords; ++i) {
             w[i] = __funnelshift_r(all[i], all[i + 1], (off & 2) * 8);
             const int left = have - 2 * i;
             if (left < 2) w[i] = left < 1 ? 0u : w[i] & 0xffffu;
@@ -1003,124 +1008,207 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
 
 // ------------------------------------------------------------------ gradients of the weights
 // Sums over an adapter's rows of outer products, [columns][rank]: a CTA takes a strip of columns of x (for dA) or dy
-// (for dB) and a chunk of the rows in the order by adapter, its warps 16 rows at a time in turn.  A lane loads eight
-// neighbouring columns (four for large ranks) of four rows, and turns them into the first operand; the second, the
-// small rows, comes as fp32 in two parts, so that the sums keep fp32's bits.  An adapter within the chunk is written
-// as it is, one that reaches beyond it into the chunk's two rows of partial sums, which adapter_join_kernel adds up
-// in order.
+// (for dB), 64 a warp (32 for large ranks), and a chunk of the rows in the order by adapter, 16 at a time.  A lane's
+// eight (four) neighbouring columns of four rows come through its own places in a ring of asynchronous copies and are
+// turned into the first operand.  The second, the small rows, is the same for all warps: they make it together for a
+// batch of rows in shared memory, fp32 in three bf16 parts (f16 and f32 activations: two 19-bit ones), so that the sums
+// keep fp32's bits.  An adapter within the chunk is written as it is, one that reaches beyond it into the chunk's two
+// rows of partial sums, which adapter_join_kernel adds up in order.
+template <typename T, int RT>
+struct WeightSizes {
+    static constexpr int kNear = RT <= 2 ? 8 : 4, kWarpColumns = 8 * kNear;
+    static constexpr int kColumns = kWarpColumns * kAdapterThreads / 32;
+    static constexpr int kBatch = RT <= 2 ? 64 : 32;                  // rows
+    static constexpr int kItems = kBatch / 16 * 2 * RT * 32;          // lanes' parts of a batch's second operand
+    static constexpr bool kThree = __is_same(T, __nv_bfloat16);
+    static constexpr int kItemBytes = kThree ? 24 : 32;
+    static constexpr int kBatchBytes = kItems * kItemBytes;
+};
 template <typename T, int RT, bool WIDE>
-__global__ void __launch_bounds__(kAdapterThreads, RT <= 4 ? 2 : 1) adapter_weights_kernel(const AdapterGradArgs a)
+constexpr int weights_pieces()  // of a thread's columns of a row
 {
-    constexpr int kColumns = RT <= 2 ? 64 : 32, kNear = kColumns / 8, kWarps = kAdapterThreads / 32, kRank = 16 * RT;
-    __shared__ float sums[kColumns][kRank + 1];
+    return !WIDE ? 2 : WeightSizes<T, RT>::kNear * (int)sizeof(T) > 16 ? 2 : 1;
+}
+template <typename T, int RT, bool WIDE>
+constexpr int weights_stages() { return 3; }
+// CTAs on an SM: what shared memory holds, where the registers do.
+template <typename T, int RT, bool WIDE>
+constexpr int weights_resident() { return sizeof(T) == 2 && WIDE ? (RT == 1 ? 3 : RT <= 4 ? 2 : 1) : 1; }
+template <typename T, int RT, bool WIDE>
+constexpr int weights_smem()
+{
+    return weights_stages<T, RT, WIDE>() * 4 * kAdapterThreads * 16 * weights_pieces<T, RT, WIDE>() + 2 * WeightSizes<T, RT>::kBatchBytes +
+           kAdapterChunkRows * 12;
+}
+
+template <typename T, int RT, bool WIDE>
+__global__ void __launch_bounds__(kAdapterThreads, weights_resident<T, RT, WIDE>()) adapter_weights_kernel(const AdapterGradArgs a)
+{
+    using S = WeightSizes<T, RT>;
+    constexpr int kNear = S::kNear, kBatchSteps = S::kBatch / 16, kMine = S::kItems / kAdapterThreads;
+    constexpr int kStages = weights_stages<T, RT, WIDE>(), kOwn = kAdapterThreads * 16 * weights_pieces<T, RT, WIDE>();
+    extern __shared__ __align__(16) unsigned char weights_ring[];  // [kStages][4] rows' own pieces; [2] batches; the chunk's rows
     dev::grid_dependency_wait();
     dev::grid_dependents_launch();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const int x_strips = (a.k + kColumns - 1) / kColumns;
+    const int x_strips = (a.k + S::kColumns - 1) / S::kColumns;
     const bool of_x = (int)blockIdx.x < x_strips;
-    const int column0 = ((int)blockIdx.x - (of_x ? 0 : x_strips)) * kColumns, width = of_x ? a.k : a.n;
+    const int width = of_x ? a.k : a.n;
     const T *data = static_cast<const T *>(of_x ? a.x : a.dy);
     const long long stride = of_x ? a.x_stride : a.dy_stride;
     const float *small = of_x ? a.dhidden : a.hidden;
-    const int chunk = blockIdx.y, valid = a.starts[a.adapters];
-    int at = chunk * a.chunk_rows;
-    const int stop = at + a.chunk_rows < valid ? at + a.chunk_rows : valid;
-    const int my_column = column0 + kNear * g, have = width - my_column;
-    while (at < stop) {
+    const int chunk = blockIdx.y, valid = a.starts[a.adapters], chunk_from = chunk * a.chunk_rows;
+    const int stop = chunk_from + a.chunk_rows < valid ? chunk_from + a.chunk_rows : valid;
+    const int column = ((int)blockIdx.x - (of_x ? 0 : x_strips)) * S::kColumns + S::kWarpColumns * warp + kNear * g, have = width - column;
+    unsigned char *const batches = weights_ring + kStages * 4 * kOwn;
+    // The chunk's rows, as the numbers of their first elements.
+    long long *const rows = reinterpret_cast<long long *>(batches + 2 * S::kBatchBytes);
+    int *const row_numbers = reinterpret_cast<int *>(rows + kAdapterChunkRows);
+    for (int i = threadIdx.x; i < stop - chunk_from; i += kAdapterThreads) {
+        const int row = a.order[chunk_from + i];
+        rows[i] = row * stride;
+        row_numbers[i] = row;
+    }
+    __syncthreads();
+    const uint32_t slots = dev::smem_u32(weights_ring) + threadIdx.x * 16;
+    for (int at = chunk_from; at < stop;) {
         // The adapter of position `at`: as many as end at or before it come first.
         int adapter = 0;
         for (int i = 0; i < a.adapters; i += kAdapterThreads)
             adapter += __syncthreads_count(i + (int)threadIdx.x < a.adapters && a.starts[i + threadIdx.x + 1] <= at);
         const int first = a.starts[adapter], last = a.starts[adapter + 1], end = last < stop ? last : stop;
-        float acc[kNear / 2][2 * RT][4] = {};
-        for (int p = at + 16 * warp; p < end; p += 16 * kWarps) {
-            int row[4];
+        const long long *const mine = rows + (at - chunk_from);
+        const int *const numbers = row_numbers + (at - chunk_from);
+        const int count = end - at, steps = (count + 15) / 16;
+        // A batch's second operand: thread's items are lanes' of a step of 16 rows and 8 ranks, four rows each.
+        float held[kMine][4];
+        auto load = [&](int batch) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) row[i] = p + 4 * t + i < end ? a.order[p + 4 * t + i] : -1;
-            Near<T, kNear> in[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                in[i] = near<WIDE, T, kNear>(data + (row[i] < 0 ? 0 : row[i] * stride + my_column), row[i] < 0 ? 0 : have);
-            float h[2 * RT][4];
-#pragma unroll
-            for (int j = 0; j < 2 * RT; ++j)
+            for (int q = 0; q < kMine; ++q) {
+                const int item = q * kAdapterThreads + threadIdx.x, l = item % 32, rank = item / 32 % (2 * RT) * 8 + l / 4;
+                const int from = batch * S::kBatch + item / (64 * RT) * 16 + l % 4 * 4;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    h[j][i] = row[i] >= 0 && 8 * j + g < a.rank ? __ldg(small + (long long)row[i] * a.rank + 8 * j + g) : 0.0f;
-            if constexpr (sizeof(T) == 2 && __is_same(T, __nv_bfloat16)) {
-                Near<T, 4> col[kNear];
-                turned<T, 4, kNear>(in, col);
+                    held[q][i] = rank < a.rank && from + i < count ? __ldg(small + (long long)numbers[from + i] * a.rank + rank) : 0.0f;
+            }
+        };
+        auto keep = [&](int batch) {
+            unsigned char *const to = batches + batch % 2 * S::kBatchBytes;
 #pragma unroll
-                for (int j = 0; j < 2 * RT; ++j) {
-                    uint32_t hi[2], lo[2];
+            for (int q = 0; q < kMine; ++q) {
+                const int item = q * kAdapterThreads + threadIdx.x;
+                if constexpr (S::kThree) {
+                    float v[4] = {held[q][0], held[q][1], held[q][2], held[q][3]};
+#pragma unroll
+                    for (int part = 0; part < 3; ++part) {
+                        uint32_t w[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            w[i] = packed(v[2 * i], v[2 * i + 1], T());
+                            // What is left; of infinities and NaN nothing, as their difference with themselves is NaN.
+                            const float top = __int_as_float(0x7f800000);
+                            v[2 * i] = fabsf(v[2 * i]) < top ? v[2 * i] - __uint_as_float(w[i] << 16) : 0.0f;
+                            v[2 * i + 1] = fabsf(v[2 * i + 1]) < top ? v[2 * i + 1] - __uint_as_float(w[i] & 0xffff0000u) : 0.0f;
+                        }
+                        reinterpret_cast<uint2 *>(to)[part * S::kItems + item] = make_uint2(w[0], w[1]);
+                    }
+                } else {
+                    // 8 rows an instruction.
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float u = h[j][2 * i], v = h[j][2 * i + 1];
-                        hi[i] = packed(u, v, T());
-                        const float most = __int_as_float(0x7f800000);  // of infinities and NaN the first part alone
-                        lo[i] = packed(fabsf(u) < most ? u - __uint_as_float(hi[i] << 16) : 0.0f,
-                                       fabsf(v) < most ? v - __uint_as_float(hi[i] & 0xffff0000u) : 0.0f, T());
-                    }
-#pragma unroll
-                    for (int c = 0; c < kNear / 2; ++c) {
-                        mma16(acc[c][j], col[2 * c].w[0], col[2 * c + 1].w[0], col[2 * c].w[1], col[2 * c + 1].w[1], lo[0], lo[1], T());
-                        mma16(acc[c][j], col[2 * c].w[0], col[2 * c + 1].w[0], col[2 * c].w[1], col[2 * c + 1].w[1], hi[0], hi[1], T());
+                        const Parts b0 = parts_of(held[q][2 * i]), b1 = parts_of(held[q][2 * i + 1]);
+                        reinterpret_cast<uint4 *>(to)[i * S::kItems + item] = make_uint4(b0.hi, b1.hi, b0.lo, b1.lo);
                     }
                 }
-            } else {
-                // f16 and f32 in the 19-bit floats, which hold an f16 exactly.
+            }
+        };
+        const T *const my_data = data + (have > 0 ? column : 0);
+        auto fetch = [&](int step, uint32_t to) {
+            if (step < steps) {
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
+                for (int i = 0; i < 4; ++i) {
+                    const int p = 16 * step + 4 * t + i;
+                    copy_own<WIDE, T, kNear>(to + i * kOwn, my_data + (p < count ? mine[p] : 0), p < count ? have : 0);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int i = 0; i < kStages - 1; ++i) fetch(i, slots + i * 4 * kOwn);
+        int stage = 0;
+        load(0);
+        keep(0);
+        __syncthreads();
+        float acc[kNear / 2][2 * RT][4] = {};
+        for (int batch = 0; batch * kBatchSteps < steps; ++batch) {
+            const bool more = (batch + 1) * kBatchSteps < steps;
+            if (more) load(batch + 1);
+            const int to = (batch + 1) * kBatchSteps < steps ? (batch + 1) * kBatchSteps : steps;
+            uint32_t operand = dev::smem_u32(batches + batch % 2 * S::kBatchBytes) + lane * (S::kThree ? 8 : 16);
+            for (int step = batch * kBatchSteps; step < to; ++step, operand += 2 * RT * 32 * (S::kThree ? 8 : 16)) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+                Near<T, kNear> in[4];
 #pragma unroll
-                    for (int j = 0; j < 2 * RT; ++j) {
-                        const Parts b0 = parts_of(h[j][2 * s]), b1 = parts_of(h[j][2 * s + 1]);
+                for (int i = 0; i < 4; ++i) {
+                    const int p = 16 * step + 4 * t + i;
+                    in[i] = own_of<WIDE, T, kNear>(slots + (stage * 4 + i) * kOwn, WIDE ? nullptr : my_data + (p < count ? mine[p] : 0),
+                                                   p < count ? have : 0);
+                }
+                fetch(step + kStages - 1, slots + (stage == 0 ? kStages - 1 : stage - 1) * 4 * kOwn);
+                stage = stage + 1 == kStages ? 0 : stage + 1;
+                if constexpr (S::kThree) {
+                    Near<T, 4> col[kNear];
+                    turned<T, 4, kNear>(in, col);
 #pragma unroll
-                        for (int c = 0; c < kNear / 2; ++c) {
-                            const float v0 = in[2 * s].at(2 * c), v1 = in[2 * s].at(2 * c + 1), v2 = in[2 * s + 1].at(2 * c),
-                                        v3 = in[2 * s + 1].at(2 * c + 1);
-                            if constexpr (sizeof(T) == 4) {
-                                mma8_parts(acc[c][j], parts_of(v0), parts_of(v1), parts_of(v2), parts_of(v3), b0, b1);
-                            } else {
-                                const uint32_t a0 = __float_as_uint(v0), a1 = __float_as_uint(v1), a2 = __float_as_uint(v2),
-                                               a3 = __float_as_uint(v3);
-                                mma8(acc[c][j], a0, a1, a2, a3, b0.lo, b1.lo);
-                                mma8(acc[c][j], a0, a1, a2, a3, b0.hi, b1.hi);
+                    for (int part = 2; part >= 0; --part)
+#pragma unroll
+                        for (int j = 0; j < 2 * RT; ++j) {
+                            Near<T, 4> b;
+                            from_shared(operand + (part * S::kItems + j * 32) * 8, &b);
+#pragma unroll
+                            for (int c = 0; c < kNear / 2; ++c)
+                                mma16(acc[c][j], col[2 * c].w[0], col[2 * c + 1].w[0], col[2 * c].w[1], col[2 * c + 1].w[1], b.w[0], b.w[1], T());
+                        }
+                } else {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+#pragma unroll
+                        for (int j = 0; j < 2 * RT; ++j) {
+                            const uint4 b = dev::lds_v4(operand + (s * S::kItems + j * 32) * 16);
+#pragma unroll
+                            for (int c = 0; c < kNear / 2; ++c) {
+                                const float v0 = in[2 * s].at(2 * c), v1 = in[2 * s].at(2 * c + 1), v2 = in[2 * s + 1].at(2 * c),
+                                            v3 = in[2 * s + 1].at(2 * c + 1);
+                                if constexpr (sizeof(T) == 4) {
+                                    mma8_parts(acc[c][j], parts_of(v0), parts_of(v1), parts_of(v2), parts_of(v3), Parts{b.x, b.z}, Parts{b.y, b.w});
+                                } else {  // exact
+                                    const uint32_t a0 = __float_as_uint(v0), a1 = __float_as_uint(v1), a2 = __float_as_uint(v2),
+                                                   a3 = __float_as_uint(v3);
+                                    mma8(acc[c][j], a0, a1, a2, a3, b.z, b.w);
+                                    mma8(acc[c][j], a0, a1, a2, a3, b.x, b.y);
+                                }
                             }
                         }
-                    }
+                }
             }
-        }
-        // The warps' sums, in their order.
-        for (int w = 0; w < kWarps; ++w) {
-            if (warp == w) {
-#pragma unroll
-                for (int c = 0; c < kNear / 2; ++c)
-#pragma unroll
-                    for (int j = 0; j < 2 * RT; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float *to = &sums[kNear * g + 2 * c + e / 2][8 * j + 2 * t + e % 2];
-                            *to = w ? *to + acc[c][j][e] : acc[c][j][e];
-                        }
-            }
+            if (more) keep(batch + 1);
             __syncthreads();
         }
         const float s = a.scale ? a.scale[adapter] : 1.0f;
-        const bool whole = first >= chunk * a.chunk_rows && last <= stop;
         float *out = of_x ? a.da + (long long)adapter * a.rank * a.k : a.db + (long long)adapter * a.rank * a.n;
-        if (!whole) {
-            out = a.partial + (2LL * chunk + (first >= chunk * a.chunk_rows)) * a.rank * ((long long)a.k + a.n);
+        if (first < chunk_from || last > stop) {
+            out = a.partial + (2LL * chunk + (first >= chunk_from)) * a.rank * ((long long)a.k + a.n);
             if (!of_x) out += (long long)a.rank * a.k;
         }
-        const int columns = width - column0 < kColumns ? width - column0 : kColumns;
-        if (of_x) {
-            for (int i = threadIdx.x; i < a.rank * kColumns; i += kAdapterThreads)
-                if (i % kColumns < columns) out[(long long)(i / kColumns) * a.k + column0 + i % kColumns] = s * sums[i % kColumns][i / kColumns];
-        } else {
-            for (int i = threadIdx.x; i < columns * a.rank; i += kAdapterThreads)
-                out[(long long)column0 * a.rank + i] = s * sums[i / a.rank][i % a.rank];
-        }
-        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 2 * RT; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int rank = 8 * j + 2 * t + e;
+#pragma unroll
+                for (int i = 0; i < kNear; ++i)
+                    if (rank < a.rank && i < have)
+                        out[of_x ? (long long)rank * a.k + column + i : (long long)(column + i) * a.rank + rank] = s * acc[i / 2][j][i % 2 * 2 + e];
+            }
         at = end;
     }
 }
@@ -1164,14 +1252,22 @@ cudaError_t products_pick(const AdapterArgs &a, bool turned, bool many, int clus
     return turned ? (wide ? pick(yes, yes) : pick(yes, no)) : (wide ? pick(no, yes) : pick(no, no));
 }
 
-template <typename T, int RT>
+template <typename T, int RT, bool WIDE>
 cudaError_t weights_launch(const AdapterGradArgs &a, cudaStream_t stream)
 {
-    const int columns = adapter_columns(a.rank);
-    const dim3 grid((unsigned)((a.k + columns - 1) / columns + (a.n + columns - 1) / columns), (unsigned)a.chunks);
-    return a.x_wide && a.dy_wide
-               ? launch_overlapped(adapter_weights_kernel<T, RT, true>, grid, dim3(kAdapterThreads), 0, stream, 1, a)
-               : launch_overlapped(adapter_weights_kernel<T, RT, false>, grid, dim3(kAdapterThreads), 0, stream, 1, a);
+    using S = WeightSizes<T, RT>;
+    constexpr int kSmem = weights_smem<T, RT, WIDE>();
+    static_assert(S::kColumns == (RT <= 2 ? kAdapterColumns : kAdapterColumns / 2), "as the workspace is laid out");
+    static bool allowed[kMaxDevices] = {};
+    const cudaError_t e = allow_dynamic_smem(adapter_weights_kernel<T, RT, WIDE>, kSmem, allowed);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((a.k + S::kColumns - 1) / S::kColumns + (a.n + S::kColumns - 1) / S::kColumns), (unsigned)a.chunks);
+    return launch_overlapped(adapter_weights_kernel<T, RT, WIDE>, grid, dim3(kAdapterThreads), kSmem, stream, 1, a);
+}
+template <typename T, int RT>
+cudaError_t weights_pick(const AdapterGradArgs &a, cudaStream_t stream)
+{
+    return a.x_wide && a.dy_wide ? weights_launch<T, RT, true>(a, stream) : weights_launch<T, RT, false>(a, stream);
 }
 
 }  // namespace
@@ -1192,10 +1288,10 @@ template <typename T>
 cudaError_t adapter_weights_launch(const AdapterGradArgs &a, cudaStream_t stream)
 {
     switch (adapter_rank_tiles(a.rank)) {
-    case 1: return weights_launch<T, 1>(a, stream);
-    case 2: return weights_launch<T, 2>(a, stream);
-    case 4: return weights_launch<T, 4>(a, stream);
-    default: return weights_launch<T, 8>(a, stream);
+    case 1: return weights_pick<T, 1>(a, stream);
+    case 2: return weights_pick<T, 2>(a, stream);
+    case 4: return weights_pick<T, 4>(a, stream);
+    default: return weights_pick<T, 8>(a, stream);
     }
 }
 

@@ -1034,7 +1034,10 @@ int conv_bn_silu_check(void *stream)
     unsigned int lword = 0;
     e = cbs::linear_read_and_clear_error(static_cast<cudaStream_t>(stream), &lword);
     if (e != cudaSuccess) return cuda_fail(e);
-    if ((gword != 0 || wword != 0 || lword != 0) && word == 0) return CBS_ERR_TIMEOUT;
+    unsigned int aword = 0;
+    e = cbs::adapters_read_and_clear_error(static_cast<cudaStream_t>(stream), &aword);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if ((gword != 0 || wword != 0 || lword != 0 || aword != 0) && word == 0) return CBS_ERR_TIMEOUT;
     if (word == 0) return CBS_OK;
     // A kernel gave up mid-way: stream-K ready flags may be left raised.
     e = cbs::tc_reset_workspaces();

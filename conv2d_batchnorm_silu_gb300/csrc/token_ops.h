@@ -170,6 +170,7 @@ cudaError_t rms_norm_grad_launch(const RmsNormGradProblem &p, int sm_count, cuda
 
 long long adapters_workspace_bytes(const AdapterProblem &p, bool gradient, int sm_count);
 cudaError_t adapters_launch(const AdapterProblem &p, int sm_count, cudaStream_t stream);
+cudaError_t adapters_read_and_clear_error(cudaStream_t stream, unsigned int *out);
 cudaError_t adapters_grad_launch(const AdapterProblem &p, int sm_count, cudaStream_t stream);
 
 constexpr int kAdamWBlock = 256;  // elements that share a scale
