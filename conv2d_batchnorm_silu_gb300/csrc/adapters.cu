@@ -29,7 +29,7 @@ namespace {
 // Each block takes a window of 1024 rows and sorts them by adapter; where an adapter's rows go in all, it finds by
 // counting the whole index itself, so that no block waits for another.  The counts are sums of integers: their order
 // does not matter.  Rows without an adapter come last, as those of an adapter more.
-constexpr int kWindow = 1024;
+constexpr int kWindow = 1024, kFewBins = 96;
 
 struct OrderArgs {
     const int *index;
@@ -42,7 +42,7 @@ struct OrderArgs {
 
 __global__ void __launch_bounds__(kWindow) adapter_order_kernel(const OrderArgs a)
 {
-    extern __shared__ int order_bins[];  // [6][bins]
+    extern __shared__ int order_bins[];  // [6][bins], and for few [32][kFewBins]
     __shared__ unsigned keys[kWindow];
     __shared__ unsigned long long warp_sums[32];
     dev::grid_dependency_wait();
@@ -57,42 +57,74 @@ __global__ void __launch_bounds__(kWindow) adapter_order_kernel(const OrderArgs 
         return v < 0 || v >= a.adapters ? a.adapters : v;
     };
     const int start = (int)blockIdx.x * kWindow;
-    constexpr int kAhead = 4;
-    for (int i0 = 0; i0 < a.m; i0 += kAhead * kWindow) {
-        int v[kAhead];
+    const bool few = bins <= kFewBins;
+    bool here = start + tid < a.m;
+    int mine = here ? of(start + tid) : -1, row = start + tid, local;  // local: rows of the adapter before it in the window
+    if (!few || a.m > kWindow) {
+        constexpr int kAhead = 4;
+        for (int i0 = 0; i0 < a.m; i0 += kAhead * kWindow) {
+            int v[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) v[j] = i0 + j * kWindow + tid < a.m ? of(i0 + j * kWindow + tid) : -1;
+            for (int j = 0; j < kAhead; ++j) v[j] = i0 + j * kWindow + tid < a.m ? of(i0 + j * kWindow + tid) : -1;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const unsigned same = __match_any_sync(0xffffffffu, v[j]);
-            if (v[j] >= 0 && lane == __ffs((int)same) - 1) {
-                atomicAdd(total + v[j], __popc(same));
-                if (i0 + j * kWindow < start) atomicAdd(before + v[j], __popc(same));
+            for (int j = 0; j < kAhead; ++j) {
+                const unsigned same = __match_any_sync(0xffffffffu, v[j]);
+                if (v[j] >= 0 && lane == __ffs((int)same) - 1) {
+                    atomicAdd(total + v[j], __popc(same));
+                    if (i0 + j * kWindow < start) atomicAdd(before + v[j], __popc(same));
+                }
             }
         }
     }
-    // The window's rows by adapter, and among one adapter's in their order.
-    unsigned key = start + tid < a.m ? (unsigned)of(start + tid) << 10 | (unsigned)tid : 0xffffffffu;
-    for (int k = 2; k <= kWindow; k <<= 1)
-        for (int j = k / 2; j > 0; j >>= 1) {
-            unsigned other;
-            if (j >= 32) {
-                __syncthreads();
-                keys[tid] = key;
-                __syncthreads();
-                other = keys[tid ^ j];
-            } else {
-                other = __shfl_xor_sync(0xffffffffu, key, j);
+    if (few) {
+        // Of few adapters: each warp's counts side by side, added up over the warps before.
+        int(*const counts)[kFewBins] = reinterpret_cast<int(*)[kFewBins]>(step_base + bins);
+        for (int b = lane; b < bins; b += 32) counts[warp][b] = 0;
+        __syncwarp();
+        const unsigned same = __match_any_sync(0xffffffffu, mine);
+        local = __popc(same & ((1u << lane) - 1));
+        if (here && local == 0) counts[warp][mine] = __popc(same);
+        __syncthreads();
+        if (tid < bins) {
+            int c[32], sum = 0;
+#pragma unroll
+            for (int w = 0; w < 32; ++w) c[w] = counts[w][tid];
+#pragma unroll
+            for (int w = 0; w < 32; ++w) {
+                counts[w][tid] = sum;
+                sum += c[w];
             }
-            const bool smaller = ((tid & j) == 0) == ((tid & k) == 0);
-            key = (key < other) == smaller ? key : other;
+            if (a.m <= kWindow) total[tid] = sum;  // the window is all there is
         }
-    __syncthreads();
-    keys[tid] = key;
-    __syncthreads();
-    const bool here = key != 0xffffffffu;
-    const int mine = (int)(key >> 10);
-    if (here && (tid == 0 || (int)(keys[tid - 1] >> 10) != mine)) head[mine] = tid;
+        __syncthreads();
+        if (here) local += counts[warp][mine];
+    } else {
+        // The window's rows sorted by adapter, and among one adapter's in their order.
+        unsigned key = here ? (unsigned)mine << 10 | (unsigned)tid : 0xffffffffu;
+        for (int k = 2; k <= kWindow; k <<= 1)
+            for (int j = k / 2; j > 0; j >>= 1) {
+                unsigned other;
+                if (j >= 32) {
+                    __syncthreads();
+                    keys[tid] = key;
+                    __syncthreads();
+                    other = keys[tid ^ j];
+                } else {
+                    other = __shfl_xor_sync(0xffffffffu, key, j);
+                }
+                const bool smaller = ((tid & j) == 0) == ((tid & k) == 0);
+                key = (key < other) == smaller ? key : other;
+            }
+        __syncthreads();
+        keys[tid] = key;
+        __syncthreads();
+        here = key != 0xffffffffu;
+        mine = (int)(key >> 10);
+        row = start + (int)(key & 1023u);
+        if (here && (tid == 0 || (int)(keys[tid - 1] >> 10) != mine)) head[mine] = tid;
+        __syncthreads();
+        local = here ? tid - head[mine] : 0;
+    }
     // Exclusive sums of rows (21 bits), tiles and steps (21 each) over the adapters before.
     const int each = (bins + kWindow - 1) / kWindow;
     auto amount = [&](int b) {
@@ -134,8 +166,8 @@ __global__ void __launch_bounds__(kWindow) adapter_order_kernel(const OrderArgs 
     }
     __syncthreads();
     if (!here) return;
-    const int rank = before[mine] + tid - head[mine], at = base[mine] + rank;
-    a.order[at] = start + (int)(key & 1023u);
+    const int rank = before[mine] + local, at = base[mine] + rank;
+    a.order[at] = row;
     if (rank % a.tile_rows == 0) {
         const int left = total[mine] - rank;
         a.tiles[tile_base[mine] + rank / a.tile_rows] = AdapterTile{mine, at, left < a.tile_rows ? left : a.tile_rows, 0};
@@ -148,7 +180,7 @@ __global__ void __launch_bounds__(kWindow) adapter_order_kernel(const OrderArgs 
 
 cudaError_t order_launch(const OrderArgs &a, cudaStream_t stream)
 {
-    const int smem = 6 * 4 * (a.adapters + 1);
+    const int smem = 6 * 4 * (a.adapters + 1) + (a.adapters < kFewBins ? 32 * kFewBins * 4 : 0);
     static bool allowed[kMaxDevices] = {};
     if (smem > 40 * 1024) {
         const cudaError_t e = allow_dynamic_smem(adapter_order_kernel, 6 * 4 * (kMostAdapters + 1), allowed);
