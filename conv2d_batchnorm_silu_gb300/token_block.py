@@ -12,9 +12,18 @@ The weights are quantised once, by ``quantize_rows`` too: a scale per output cha
 ``TokenBlock.tune_norm`` trains the norm's gamma and beta towards given rows with ``layer_norm`` and
 ``layer_norm_backward``.
 
+``AdaptedProjection`` is what requests with low-rank adapters of their own share on a residual stream,
+
+    total = h + residual,  z = W RMSNorm(total) + bias + s_g B_g A_g RMSNorm(total)
+
+as three calls: ``rms_norm_quantize`` (the total, and its norm as int8 and as it is), ``linear_int8`` with the
+projection that all share, ``linear_adapters`` with each row's adapter, added in place.  ``tune`` trains the adapters
+with ``linear_adapters_backward`` and ``adamw_step``, the projection staying as it is.
+
     python -m conv2d_batchnorm_silu_gb300.token_block [--n 16] [--size 40] [--channels 256] [--hidden 1024]
 
-prints how far the int8 block is from the same block in fp32, its time and the loss of a short tuning.
+prints how far the int8 block is from the same block in fp32, its time and the loss of a short tuning, and the time and
+tuning of a projection with four adapters on the same pixels.
 Needs a GPU.
 """
 from __future__ import annotations
@@ -53,6 +62,38 @@ class TokenBlock:
             _, dgamma, dbeta = capi.layer_norm_backward(off.to(h.dtype), h, self.gamma, stats)
             self.gamma = self.gamma - rate / tokens * dgamma
             self.beta = self.beta - rate / tokens * dbeta
+        return losses
+
+
+class AdaptedProjection:
+    """gamma [c] in fp32, w [n][c] of any float type (quantised here), bias [n] in fp32 or None; a [adapters][rank][c] and
+    b [adapters][n][rank] in fp32, used in h's type; scale [adapters] in fp32 or None."""
+
+    def __init__(self, gamma, w, bias, a, b, scale=None, eps=1e-6):
+        self.gamma, self.bias, self.a, self.b, self.scale, self.eps = gamma, bias, a, b, scale, eps
+        self.w, self.w_scale = capi.quantize_rows(w)
+
+    def __call__(self, h, residual, index, stream=None):
+        """h and residual [..., c], index int32 for each row (outside the adapters: none) -> (z [..., n], total [..., c])."""
+        q, q_scale, total, y = capi.rms_norm_quantize(h, self.gamma, self.eps, residual=residual, return_y=True, stream=stream)
+        z = capi.linear_int8(q, self.w, q_scale, self.w_scale, self.bias, out_dtype=h.dtype, stream=stream)
+        a, b = self.a.to(h.dtype), self.b.to(h.dtype)
+        return capi.linear_adapters(y, index, a, b, self.scale, base=z, y=z, stream=stream), total
+
+    def tune(self, h, residual, index, target, steps=20, lr=1e-2, bits=8):
+        """AdamW steps on the adapters for the mean over rows of |z - target|^2 / 2, with moments of so many bits; the
+        losses."""
+        rows, losses, state = index.numel(), [], capi.adamw_state([self.a, self.b], bits)
+        q, q_scale, _, y = capi.rms_norm_quantize(h, self.gamma, self.eps, residual=residual, return_y=True)
+        shared = capi.linear_int8(q, self.w, q_scale, self.w_scale, self.bias, out_dtype=h.dtype)
+        for step in range(1, steps + 1):
+            a, b = self.a.to(h.dtype), self.b.to(h.dtype)
+            z, hidden = capi.linear_adapters(y, index, a, b, self.scale, base=shared, return_hidden=True)
+            off = z.float() - target
+            losses.append(float(off.square().sum() / (2 * rows)))
+            # The gradient of the sum over rows, so that 16-bit types do not lose errors divided by their number.
+            _, da, db = capi.linear_adapters_backward(off.to(h.dtype), y, index, a, b, self.scale, hidden)
+            capi.adamw_step([self.a, self.b], [da, db], step=step, lr=lr, weight_decay=0.0, grad_scale=1.0 / rows, **state)
         return losses
 
 
@@ -95,6 +136,20 @@ def _main():
     print(f"convolution and block on {n * args.size ** 2} tokens: {start.elapsed_time(stop) * 20:.1f} us")
     losses = block.tune_norm(h, f.layer_norm(h.float(), (c,), 1 + 0.1 * rand(c), 0.1 * rand(c), 1e-5))
     print(f"tuning the norm: loss {losses[0]:.4f} -> {losses[-1]:.6f} in {len(losses)} steps")
+    adapters, rank = 4, 16
+    index = (torch.arange(h.numel() // c, device="cuda") * adapters // (h.numel() // c)).int()
+    shared = AdaptedProjection(gamma, w1, b1, rand(adapters, rank, c) / c ** 0.5, 0.1 * rand(adapters, hidden, rank))
+    wanted = AdaptedProjection(gamma, w1, b1, rand(adapters, rank, c) / c ** 0.5, 0.1 * rand(adapters, hidden, rank))
+    for _ in range(3):
+        shared(h, x, index)
+    start.record()
+    for _ in range(50):
+        shared(h, x, index)
+    stop.record()
+    stop.synchronize()
+    print(f"projection with {adapters} adapters of rank {rank}: {start.elapsed_time(stop) * 20:.1f} us")
+    losses = shared.tune(h, x, index, wanted(h, x, index)[0].float())
+    print(f"tuning the adapters: loss {losses[0]:.4f} -> {losses[-1]:.6f} in {len(losses)} steps")
     capi.check()
 
 
