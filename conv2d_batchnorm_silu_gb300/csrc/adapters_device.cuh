@@ -851,6 +851,7 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
         const char **const base_row = reinterpret_cast<const char **>(small + kRows * 16 * RT * (int)sizeof(T));
         char **const y_row = reinterpret_cast<char **>(small + kRows * (16 * RT * (int)sizeof(T) + 8));
         float *const factors = reinterpret_cast<float *>(y_row + kRows);
+        constexpr bool kFactors = __is_same(T, __half);  // else the small rows take the scale before they are rounded
         {
             float v[2][kSteps][kNear];
 #pragma unroll
@@ -868,7 +869,7 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
 #pragma unroll
                 for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                    for (int q = 0; q < kNear; ++q) v[i][k][q] *= factor;
+                    for (int q = 0; q < kNear; ++q) v[i][k][q] *= kFactors ? factor : s;
                 if (t == 0) {
                     const long long at = rows[r < count ? r : count - 1];
                     factors[r] = s;
@@ -893,6 +894,11 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
         __syncthreads();  // they are there, and the sums read
         const T *w2 = static_cast<const T *>(a.w2) + (long long)adapter * a.rank * a.n;
         const bool adds = a.base != nullptr;
+        if (!adds) {  // what is added is then zeros
+            uint4 *const zeros = reinterpret_cast<uint4 *>(ring + small_rows<T, RT>());
+            for (int i = threadIdx.x; i < kManyAhead * 4 * kOwn / 16; i += kAdapterThreads) zeros[i] = make_uint4(0, 0, 0, 0);
+            __syncthreads();
+        }
         const int groups = (count + 31) / 32;  // of rows
         const uint32_t slots = dev::smem_u32(ring + small_rows<T, RT>()) + threadIdx.x * 16;
         const uint32_t small_at = dev::smem_u32(small) + lane * 16;
@@ -972,15 +978,15 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
                     float2 v[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) v[q] = make_float2(acc[i / 2][q][i % 2 * 2], acc[i / 2][q][i % 2 * 2 + 1]);
-                    const float2 factor = make_float2(factors[r], factors[r]);
-                    if (adds) {
-                        const Near<T, 8> old = own_of<WIDE, T>(slots + (stage * 4 + i) * kOwn,
-                                                               WIDE ? nullptr : reinterpret_cast<const T *>(base_row[r]) + column, have);
+                    const Near<T, 8> old = own_of<WIDE, T>(slots + (stage * 4 + i) * kOwn,
+                                                           WIDE ? nullptr : reinterpret_cast<const T *>(base_row[r]) + column, have);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = __ffma2_rn(v[q], factor, make_float2(old.at(2 * q), old.at(2 * q + 1)));
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) v[q] = __fmul2_rn(v[q], factor);
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 o = make_float2(old.at(2 * q), old.at(2 * q + 1));
+                        if constexpr (kFactors)
+                            v[q] = __ffma2_rn(v[q], make_float2(factors[r], factors[r]), o);
+                        else
+                            v[q] = __fadd2_rn(v[q], o);
                     }
                     store_near<WIDE, T>(reinterpret_cast<T *>(y_row[r] + column * (int)sizeof(T)), reinterpret_cast<const float *>(v), r < count ? have : 0);
                 }
@@ -988,20 +994,30 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
             }
         }
     } else if (a.base != a.y) {
-        // Rows without an adapter: base, or zeros.
+        // Rows without an adapter: base, or zeros; eight loads of a lane in flight, two of each of four rows.
         const int from = 32 * first, to = 32 * stop < a.n ? 32 * stop : a.n;
-        for (int r = warp; r < count; r += kAdapterThreads / 32) {
-            const T *old = static_cast<const T *>(a.base) + rows[r] * a.base_stride;
-            T *y = static_cast<T *>(a.y) + rows[r] * a.y_stride;
-            for (int c = from + 8 * lane; c < to; c += 256) {
-                const int have = to - c < 8 ? to - c : 8;
-                const Near<T, 8> u = near<WIDE, T, 8, false>(old + c, a.base ? have : 0);
-                float v[8];
+        constexpr int kTogether = 4;
+        for (int r0 = kTogether * warp; r0 < count; r0 += kTogether * kAdapterThreads / 32)
+            for (int c0 = from + 8 * lane; c0 < to; c0 += 512) {
+                Near<T, 8> old[kTogether][2];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] = u.at(q);
-                store_near<WIDE, T>(y + c, v, have);
+                for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int c = c0 + 256 * j, have = a.base && r0 + i < count ? to - c : 0;
+                        old[i][j] = near<WIDE, T, 8, false>(static_cast<const T *>(a.base) + rows[r0 + i < count ? r0 + i : 0] * a.base_stride + c, have);
+                    }
+#pragma unroll
+                for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int c = c0 + 256 * j;
+                        float v[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) v[q] = old[i][j].at(q);
+                        store_near<WIDE, T>(static_cast<T *>(a.y) + rows[r0 + i < count ? r0 + i : 0] * a.y_stride + c, v, r0 + i < count ? to - c : 0);
+                    }
             }
-        }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
