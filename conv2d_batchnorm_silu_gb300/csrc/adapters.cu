@@ -392,8 +392,10 @@ cudaError_t adapters_grad_launch(const AdapterProblem &p, int sm_count, cudaStre
     const int size = dtype_size(p.dtype);
     const Layout l = layout_of(p, true, p.n, p.k, sm_count);
     const bool x_wide = p.k % 8 == 0 && on_boundary(p.x.data, p.x.stride, size), dy_wide = p.n % 8 == 0 && on_boundary(p.dy.data, p.dy.stride, size);
-    const bool tc = p.dtype == kBf16 && x_wide && dy_wide && p.x.stride >= p.k && p.dy.stride >= p.n && adapter_rank_tiles(p.rank) <= 4 &&
-                    p.m >= 1024 && p.m >= 128LL * p.adapters;
+    // Where an adapter has few rows on average, most of a step's 64 would be none; a tensor map's rows are less than 2^40
+    // bytes apart.
+    const bool tc = p.dtype == kBf16 && x_wide && dy_wide && p.x.stride >= p.k && p.dy.stride >= p.n && p.x.stride < (1LL << 39) &&
+                    p.dy.stride < (1LL << 39) && adapter_rank_tiles(p.rank) <= 4 && p.m >= 1024 && p.m >= 128LL * p.adapters;
     const Workspace w = workspace_of(p, true, tc, sm_count);
     char *work = static_cast<char *>(p.workspace);
     OrderArgs o = order_args(p, w, l, work);
