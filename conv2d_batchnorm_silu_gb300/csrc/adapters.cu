@@ -250,7 +250,7 @@ Layout layout_of(const AdapterProblem &p, bool ordered, int k, int n, int sm_cou
     // 64 adapters, 4096x4096: 4 CTAs 9.8 us, 8 12.8; one row: 4 CTAs 7.3, 8 6.1), while each has some steps of 32
     // elements for its warps.
     const int ranks = adapter_rank_tiles(p.rank);
-    const long long room = (long long)sm_count * (l.many ? (ranks <= 4 && p.dtype != kF32 ? 2 : 1) : ranks == 1 ? 3 : ranks == 2 ? 2 : 1);
+    const long long room = (long long)sm_count * (l.many ? (ranks <= 4 && p.dtype != kF32 ? 2 : 1) : ranks == 1 ? 3 : ranks == 2 || (ranks == 4 && p.dtype != kF32) ? 2 : 1);
     const long long about = full + (l.many ? 0 : p.adapters < p.m ? p.adapters : p.m);  // tiles
     const int steps = ((k > n ? k : n) + 31) / 32;
     l.size = 1;

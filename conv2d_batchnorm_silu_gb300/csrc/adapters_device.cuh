@@ -313,7 +313,7 @@ constexpr int adapter_smem()
 }
 
 template <typename T, int RT, int WM, bool TURNED, bool WIDE>
-__global__ void __launch_bounds__(kAdapterThreads, RT <= 2 ? 2 : 1) adapter_products_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(kAdapterThreads, RT <= 2 || (RT == 4 && sizeof(T) == 2) ? 2 : 1) adapter_products_kernel(const AdapterArgs a)
 {
     constexpr int kRows = 16 * WM, kWarps = kAdapterThreads / 32, kSplit = kWarps / WM, kPitch = hidden_pitch<RT>();
     extern __shared__ __align__(16) float adapter_sums[];  // [kSplit][kRows][kPitch] partial sums, then [kRows][kPitch] whole ones
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 ? 2 : 1) adapter_prod
         const int steps = (a.k + 31) / 32, from = (int)((long long)steps * part / parts), to = (int)((long long)steps * (part + 1) / parts);
         // This warp's rows may all be beyond the tile's.
         if (16 * wm < count) {
-#pragma unroll 2
+#pragma unroll(RT <= 2 ? 2 : 1)
             for (int s = from + ws; s < to; s += kSplit) {
                 const int k0 = 32 * s + 8 * t, have = a.k - k0;
                 const Near<T, 8> lo = near<WIDE, T, 8>(x_lo + k0, has_lo ? have : 0);
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 ? 2 : 1) adapter_prod
         const T *b_lo = static_cast<const T *>(a.base) + at_lo * a.base_stride, *b_hi = static_cast<const T *>(a.base) + at_hi * a.base_stride;
         T *y_lo = static_cast<T *>(a.y) + at_lo * a.y_stride, *y_hi = static_cast<T *>(a.y) + at_hi * a.y_stride;
         const int steps = (a.n + 31) / 32, from = (int)((long long)steps * part / parts), to = (int)((long long)steps * (part + 1) / parts);
-#pragma unroll 2
+#pragma unroll(RT <= 2 ? 2 : 1)
         for (int s = from + ws; s < to; s += kSplit) {
             // Of 32 columns: as the second operand the lane's are 4g to 4g + 3, as the result 8t to 8t + 7.
             const int n0 = 32 * s + 8 * t, have = a.n - n0;
