@@ -9,6 +9,9 @@
 // odds that keep the mean: to nearest, a change of less than a sixteenth a step (beta2 = 0.999 changes v by a
 // thousandth) would be lost each time.  The odds come from the place and the step alone.  sqrt(v) never becomes 0
 // where it was not: m / (0 + eps) would be a step without bounds.  This step itself uses m and v before the rounding.
+//
+// Measured: 66M fp32 elements with fp32 moments 263 us (7.1 TB/s, memory); 8.3M in 192 bf16 tensors with 8-bit moments
+// 29.5 us (3.4 TB/s), bound by some 80 instructions an element, most of them the dither and the rounding to 8 bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

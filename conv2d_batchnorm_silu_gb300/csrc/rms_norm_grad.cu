@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(32 * kJoinRuns) rms_grad_join_kernel(const Rms
 // As the layer norm's gradient: each thread keeps gamma and the running sums of dy * h for its own columns in
 // registers while x, dy and the gradient past the norm stream by, so that each is read once.  At the end the rows of
 // a block are joined in shared memory, and each block writes one row of partial sums, which rms_grad_join_kernel
-// adds up in order.
+// adds up in order.  bf16 with the join: 16384x4096 with the gradient past the norm 82 us (6.6 TB/s), 25600x256 without it
+// 8.6, of which the join and the launches' ends are a third.
 constexpr int kGradElements = 16;  // of a row per thread
 constexpr int grad_block(int tpr) { return tpr < 256 ? 256 : tpr; }
 // Rounds of the ring: as many as 512 threads' rings find room for in an SM's shared memory.
