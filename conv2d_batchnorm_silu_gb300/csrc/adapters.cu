@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kAdapterThreads) adapter_join_kernel(const Ada
 // ------------------------------------------------------------------ what a call launches
 struct Layout {
     bool few;      // each cluster finds its rows itself
+    bool counted;  // by counting all of them
     bool many;     // tiles of kAdapterManyRows
     int tile_rows, tiles;  // tiles at most
     int clusters, size;
@@ -234,19 +235,29 @@ struct Layout {
 // Rows that one call of adapter_products_kernel's clusters looks at by itself.
 constexpr int kFew = kAdapterThreads;
 
+// Rows whose tiles a CTA finds by counting all of them: an order by adapter first takes a launch more (777x1001x515 f32
+// 11.9 / 9.5 us), and a cluster for each row more clusters than there are tiles, which counts where there are four times
+// as many (4096x4096, rank 16, 256 rows of 4 adapters 9.6 / 8.1 us, of 64 adapters 10.5 / 12.3).
+bool counted(const AdapterProblem &p)
+{
+    return p.m <= kCountedRows && p.adapters < kCountedBins && (long long)p.m * (adapter_rank_tiles(p.rank) + 1) < 4096 &&
+           (p.m > kFew || (p.m > 64 && 4 * (p.m / kAdapterFewRows + p.adapters) < p.m));
+}
+
 Layout layout_of(const AdapterProblem &p, bool ordered, int k, int n, int sm_count)
 {
     Layout l{};
-    l.few = !ordered && p.m <= kFew;
+    l.counted = !ordered && counted(p);
+    l.few = l.counted || (!ordered && p.m <= kFew);
     // Tiles of 128 rows read an adapter's weights an eighth as often, which pays the sooner the higher the rank is
     // (4096x4096, 16 / 128 rows a tile: rank 16 with 1200 rows 22.3 / 21.6 us, with 2400 30.3 / 29.1; rank 64 with 600 rows
     // 30.9 / 31.8, with 1200 60 / 34); where an adapter has few rows, on average over all there are, most of such a
     // tile's warps would have none.
-    l.many = p.m > kFew && p.m >= 24LL * p.adapters && (long long)p.m * (adapter_rank_tiles(p.rank) + 1) >= 4096;
+    l.many = p.m > kFew && !l.few && p.m >= 24LL * p.adapters && (long long)p.m * (adapter_rank_tiles(p.rank) + 1) >= 4096;
     l.tile_rows = l.many ? kAdapterManyRows : kAdapterFewRows;
     const int full = (p.m + l.tile_rows - 1) / l.tile_rows;
     l.tiles = full + (p.adapters + 1 < p.m ? p.adapters + 1 : p.m);
-    l.clusters = l.few ? p.m : l.tiles;
+    l.clusters = l.few && !l.counted ? p.m : l.tiles;
     // CTAs a tile: what takes the fewest rounds of CTAs for its part of a tile, the fewest of those that do (128 rows of
     // 64 adapters, 4096x4096: 4 CTAs 9.8 us, 8 12.8; one row: 4 CTAs 7.3, 8 6.1), while each has some steps of 32
     // elements for its warps.
@@ -344,7 +355,7 @@ OrderArgs order_args(const AdapterProblem &p, const Workspace &w, const Layout &
 
 long long adapters_workspace_bytes(const AdapterProblem &p, bool gradient, int sm_count)
 {
-    if (!gradient && p.m <= kFew) return 0;
+    if (!gradient && (p.m <= kFew || counted(p))) return 0;
     return workspace_of(p, gradient, false, sm_count).bytes;
 }
 
@@ -376,6 +387,7 @@ cudaError_t adapters_launch(const AdapterProblem &p, int sm_count, cudaStream_t 
     a.w2_wide = p.rank % near == 0 && on_boundary(p.b, 0, size);
     a.w1_pieces = p.k * size % 16 == 0 && on_boundary(p.a, 0, size);
     a.y_wide = p.n % 8 == 0 && on_boundary(p.y.data, p.y.stride, size) && on_boundary(p.base.data, p.base.stride, size);
+    a.counted = l.counted;
     if (!l.few) {
         const Workspace w = workspace_of(p, false, false, sm_count);
         const OrderArgs o = order_args(p, w, l, static_cast<char *>(p.workspace));

@@ -28,6 +28,7 @@ struct AdapterArgs {
     const int *tile_count;
     long long x_stride, base_stride, y_stride;
     int m, k, n, rank, adapters;
+    bool counted;           // without an order: tiles found by counting, else by their first rows
     bool x_wide, w1_wide, w2_wide, y_wide;  // rows on the boundaries of wide loads and stores, and as long as they are
     bool w1_pieces;                         // the first weights' rows in whole pieces of 16 bytes
 };
@@ -53,6 +54,7 @@ struct AdapterGradArgs {
 };
 
 constexpr int kAdapterThreads = 256;
+constexpr int kCountedRows = 4 * kAdapterThreads, kCountedBins = 96;  // of tiles found by counting: rows, adapters and one
 constexpr int kAdapterFewRows = 16, kAdapterManyRows = 128;  // of a tile
 constexpr int kAdapterColumns = 512;                        // of a weight gradient's CTA, half for ranks above 32
 constexpr int kAdapterChunkRows = 1024;                     // of its chunk at most

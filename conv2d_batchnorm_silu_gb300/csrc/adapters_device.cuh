@@ -334,6 +334,68 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 || (RT == 4 && sizeof
         adapter = my.adapter;
         count = my.count;
         if ((int)threadIdx.x < count) rows[threadIdx.x] = a.order[my.first + threadIdx.x];
+    } else if (a.counted) {
+        // Up to 1024 rows of few adapters: every CTA counts them all, for each adapter and 32 rows, and finds its tile.
+        __shared__ int counts[32][kCountedBins];
+        __shared__ int totals[kCountedBins];
+        __shared__ int mine[3];  // adapter, first of its rows, rows
+        const int bins = a.adapters + 1;
+        int of[4], before[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = j * kAdapterThreads + (int)threadIdx.x;
+            const int v = i < a.m ? a.index[i] : -1;
+            of[j] = i >= a.m ? -1 : v < 0 || v >= a.adapters ? a.adapters : v;
+        }
+        for (int i = threadIdx.x; i < 32 * kCountedBins; i += kAdapterThreads) counts[i / kCountedBins][i % kCountedBins] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const unsigned same = __match_any_sync(0xffffffffu, of[j]);
+            before[j] = __popc(same & ((1u << lane) - 1));
+            if (of[j] >= 0 && before[j] == 0) counts[j * kWarps + warp][of[j]] = __popc(same);
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < bins) {
+            int c[32], sum = 0;
+#pragma unroll
+            for (int w = 0; w < 32; ++w) c[w] = counts[w][threadIdx.x];
+#pragma unroll
+            for (int w = 0; w < 32; ++w) {
+                counts[w][threadIdx.x] = sum;
+                sum += c[w];
+            }
+            totals[threadIdx.x] = sum;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int left = tile;  // tiles of the adapters from here on that come before this one
+            for (int b0 = 0; b0 < bins; b0 += 32) {
+                const int total = b0 + lane < bins ? totals[b0 + lane] : 0, tiles = (total + kRows - 1) / kRows;
+                int upto = tiles;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += v;
+                }
+                if (left >= 0 && left >= upto - tiles && left < upto) {
+                    mine[0] = b0 + lane;
+                    mine[1] = (left - (upto - tiles)) * kRows;
+                    mine[2] = total;
+                }
+                left -= __shfl_sync(0xffffffffu, upto, 31);
+            }
+            if (lane == 0 && left >= 0) mine[0] = -1;  // one more than there are
+        }
+        __syncthreads();
+        adapter = mine[0];
+        if (adapter < 0) return;
+        const int first = mine[1];
+        count = mine[2] - first < kRows ? mine[2] - first : kRows;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int rank = of[j] == adapter ? counts[j * kWarps + warp][adapter] + before[j] - first : -1;
+            if (rank >= 0 && rank < kRows) rows[rank] = j * kAdapterThreads + (int)threadIdx.x;
+        }
     } else {
         // Few rows: a cluster for each.  Those whose row is the first, or the 17th and so on, of its adapter take it and
         // the next ones of the adapter; the others have nothing to do.
@@ -1254,7 +1316,7 @@ cudaError_t products_launch(const AdapterArgs &a, int clusters, int cluster_size
 {
     constexpr int kSmem = adapter_smem<RT, WM>();
     static bool allowed[kMaxDevices] = {};
-    if (kSmem > 46 * 1024) {
+    if (kSmem > 32 * 1024) {  // the counts take some of the first 48 KB
         const cudaError_t e = allow_dynamic_smem(adapter_products_kernel<T, RT, WM, TURNED, WIDE>, kSmem, allowed);
         if (e != cudaSuccess) return e;
     }

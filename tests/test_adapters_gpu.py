@@ -108,7 +108,8 @@ def check(capi, m, k, n, rank, adapters, dtype, kind, pad=0, offset=0, with_base
 SIZES = [(1, 32, 16, 1, 1), (1, 2048, 1024, 16, 8), (3, 40, 24, 4, 2), (17, 8, 8, 8, 3), (33, 100, 77, 12, 5), (64, 256, 512, 16, 70),
          (255, 64, 96, 16, 1), (256, 96, 128, 32, 3), (257, 128, 64, 16, 2), (300, 136, 264, 64, 4), (400, 128, 128, 128, 3),
          (500, 33, 31, 100, 2), (1500, 72, 40, 16, 2), (2100, 64, 64, 24, 40), (5000, 40, 48, 8, 1), (130, 1, 1, 3, 4),
-         (1024, 16, 32, 48, 300), (1025, 520, 16, 16, 1), (1300, 200, 136, 64, 3), (2500, 264, 128, 32, 2), (1100, 152, 56, 40, 8)]
+         (1024, 16, 32, 48, 300), (1025, 520, 16, 16, 1), (1300, 200, 136, 64, 3), (2500, 264, 128, 32, 2), (1100, 152, 56, 40, 8),
+         (600, 128, 64, 128, 2), (3000, 32, 32, 8, 120), (65, 40, 48, 16, 95), (1000, 64, 64, 16, 94), (640, 48, 40, 4, 30)]
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
