@@ -935,7 +935,7 @@ int conv_bn_silu_adamw_step(const cbs_adamw_tensor *tensors, int count, const cb
     }
     if (v.empty()) return CBS_OK;
     // A parameter given twice would be stepped by two blocks at once.
-    std::sort(written.begin(), written.end());
+    if (!std::is_sorted(written.begin(), written.end())) std::sort(written.begin(), written.end());
     for (size_t i = 1; i < written.size(); ++i)
         if (written[i].first < written[i - 1].second) return CBS_ERR_INVALID_ARG;
     cbs::AdamWScalars s{};

@@ -521,7 +521,7 @@ long long conv_bn_silu_linear_adapters_backward_workspace(long long m, int k, in
  *                  floor(|value| / distance + u) * distance with u in [0, 1) from the mixed bits of
  *                  (element + step * 0x9E3779B9) modulo 2^32, so the same step gives the same bits
  *                  again; where v is not 0 its root is held as 2^-9 of the scale at least.  A block with a
- *                  gradient that is not finite becomes NaN.  Zeros everywhere are the initial state.
+ *                  gradient that is not finite has NaN for its m.  Zeros everywhere are the initial state.
  * No tensor may overlap another; pointers are aligned to their element, and those aligned to 8
  * elements (float32 to 32 bytes) run on wide loads and stores.
  */
