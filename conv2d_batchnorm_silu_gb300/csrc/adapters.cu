@@ -258,22 +258,21 @@ Layout layout_of(const AdapterProblem &p, bool ordered, int k, int n, int sm_cou
     const int full = (p.m + l.tile_rows - 1) / l.tile_rows;
     l.tiles = full + (p.adapters + 1 < p.m ? p.adapters + 1 : p.m);
     l.clusters = l.few && !l.counted ? p.m : l.tiles;
-    // CTAs a tile: what takes the fewest rounds of CTAs for its part of a tile, the fewest of those that do (128 rows of
-    // 64 adapters, 4096x4096: 4 CTAs 9.8 us, 8 12.8; one row: 4 CTAs 7.3, 8 6.1), while each has some steps of 32
-    // elements for its warps.
+    // CTAs a tile, while each has some steps of 32 elements for its warps: of few rows, what takes the fewest rounds of
+    // CTAs for its part of a tile (128 rows of 64 adapters, 4096x4096: 4 CTAs 9.8 us, 8 12.8; one row: 4 CTAs 7.3, 8 6.1);
+    // of many, what leaves the fullest SM, busy from so many CTAs on, the least (32768x64x4096, rank 16: 1 CTA 152 us, 4
+    // 114).  The fewest of those that do.
     const int ranks = adapter_rank_tiles(p.rank);
-    const long long room = (long long)sm_count * (l.many ? (ranks <= 4 && p.dtype != kF32 ? 2 : 1) : ranks == 1 ? 3 : ranks == 2 || (ranks == 4 && p.dtype != kF32) ? 2 : 1);
+    const long long resident = l.many ? (ranks <= 4 && p.dtype != kF32 ? 2 : 1) : ranks == 1 ? 3 : ranks == 2 || (ranks == 4 && p.dtype != kF32) ? 2 : 1;
     const long long about = full + (l.many ? 0 : p.adapters < p.m ? p.adapters : p.m);  // tiles
+    auto rounds_of = [&](int size) {
+        const long long per_sm = (about * size + sm_count - 1) / sm_count;
+        return l.many ? (per_sm > resident ? per_sm : resident) : (about * size + resident * sm_count - 1) / (resident * sm_count);
+    };
     const int steps = ((k > n ? k : n) + 31) / 32;
     l.size = 1;
-    long long rounds = (about + room - 1) / room;
-    for (int size = 2; size <= 8 && steps >= 8 * size; size *= 2) {
-        const long long these = (about * size + room - 1) / room;
-        if (these * l.size < rounds * size) {
-            rounds = these;
-            l.size = size;
-        }
-    }
+    for (int size = 2; size <= 8 && steps >= 8 * size; size *= 2)
+        if (rounds_of(size) * l.size < rounds_of(l.size) * size) l.size = size;
     return l;
 }
 
