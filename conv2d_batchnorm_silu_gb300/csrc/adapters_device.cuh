@@ -511,35 +511,45 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 || (RT == 4 && sizeof
         }
     }
     if (16 * wm < count && (live || a.base != a.y)) {
-        // Rows of the first operand.  16-bit: rounded once more to the activations' type, whose rounding of y it stays
-        // below; f16, whose range the sums may leave, after division by a power of two near the row's largest.
-        Near<T, 4> h_lo[RT], h_hi[RT];
+        // Rows of the first operand.  16-bit: in two parts of the activations' type, f16, whose range the sums may leave,
+        // after division by a power of two near the row's largest.
+        constexpr int kParts = sizeof(T) == 4 ? 1 : 2;
+        Near<T, 4> h_lo[kParts][RT], h_hi[kParts][RT];
         float s_lo = live ? (a.scale ? a.scale[adapter] : 1.0f) : 0.0f, s_hi = s_lo;
         if (live) {
-            float4 v_lo[RT], v_hi[RT];
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                v_lo[i] = *reinterpret_cast<const float4 *>(whole + row_lo * kPitch + 16 * i + 4 * t);
-                v_hi[i] = *reinterpret_cast<const float4 *>(whole + row_hi * kPitch + 16 * i + 4 * t);
-            }
-            if constexpr (sizeof(T) == 4) {
+            auto take = [&](int row, auto &h, float *s) {
+                float v[RT][4];
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
-                    h_lo[i].w[0] = v_lo[i].x, h_lo[i].w[1] = v_lo[i].y, h_lo[i].w[2] = v_lo[i].z, h_lo[i].w[3] = v_lo[i].w;
-                    h_hi[i].w[0] = v_hi[i].x, h_hi[i].w[1] = v_hi[i].y, h_hi[i].w[2] = v_hi[i].z, h_hi[i].w[3] = v_hi[i].w;
+                    const float4 u = *reinterpret_cast<const float4 *>(whole + row * kPitch + 16 * i + 4 * t);
+                    v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
                 }
-            } else {
-                auto narrow = [&](const float4 *v, Near<T, 4> *h, float *s) {
-                    const float factor = narrow_factor<T, 4 * RT>(reinterpret_cast<const float *>(v), s);
+                if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                    for (int i = 0; i < RT; ++i) {
-                        h[i].w[0] = packed(v[i].x * factor, v[i].y * factor, T());
-                        h[i].w[1] = packed(v[i].z * factor, v[i].w * factor, T());
-                    }
-                };
-                narrow(v_lo, h_lo, &s_lo);
-                narrow(v_hi, h_hi, &s_hi);
-            }
+                    for (int i = 0; i < RT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) h[0][i].w[j] = v[i][j];
+                } else {
+                    const float factor = narrow_factor<T, 4 * RT>(&v[0][0], s);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[i][j] *= factor;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int i = 0; i < RT; ++i) {
+                            h[part][i].w[0] = packed(v[i][0], v[i][1], T());
+                            h[part][i].w[1] = packed(v[i][2], v[i][3], T());
+                            // What is left; of infinities and NaN nothing, as their difference with themselves is NaN.
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                v[i][j] = fabsf(v[i][j]) < __int_as_float(0x7f800000) ? v[i][j] - h[part][i].at(j) : 0.0f;
+                        }
+                }
+            };
+            take(row_lo, h_lo, &s_lo);
+            take(row_hi, h_hi, &s_hi);
         }
         const T *w2 = static_cast<const T *>(a.w2) + (live ? (long long)adapter * a.rank * a.n : 0);
         const T *b_lo = static_cast<const T *>(a.base) + at_lo * a.base_stride, *b_hi = static_cast<const T *>(a.base) + at_hi * a.base_stride;
@@ -562,10 +572,12 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 || (RT == 4 && sizeof
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
-                        for (int i = 0; i < RT; ++i)
-                            mma_four<T>(acc[q], h_lo[i], h_hi[i],
-                                        near<WIDE, T, 4>(w2 + (long long)(c0 + q) * a.rank + 16 * i + 4 * t,
-                                                         c0 + q < a.n ? a.rank - 16 * i - 4 * t : 0));
+                        for (int i = 0; i < RT; ++i) {
+                            const Near<T, 4> col = near<WIDE, T, 4>(w2 + (long long)(c0 + q) * a.rank + 16 * i + 4 * t,
+                                                                    c0 + q < a.n ? a.rank - 16 * i - 4 * t : 0);
+#pragma unroll
+                            for (int part = kParts - 1; part >= 0; --part) mma_four<T>(acc[q], h_lo[part][i], h_hi[part][i], col);
+                        }
                 } else {
                     // W2 is [rank][n].
 #pragma unroll
@@ -578,7 +590,9 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 || (RT == 4 && sizeof
                         }
                         turned<T, 4, 4>(in, col);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) mma_four<T>(acc[q], h_lo[i], h_hi[i], col[q]);
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int part = kParts - 1; part >= 0; --part) mma_four<T>(acc[q], h_lo[part][i], h_hi[part][i], col[q]);
                     }
                 }
             }
@@ -913,8 +927,8 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
     const int first = (int)((long long)strips * part / parts), stop = (int)((long long)strips * (part + 1) / parts);
     if (live) {
         cluster_wait();
-        // The small rows in the activations' type (as in adapter_products_kernel), as the first operand's registers lie
-        // in a lane: 16 rows by each warp.
+        // The small rows in the activations' type, whose rounding of y their own stays below (f16 after division by a power
+        // of two near the row's largest), as the first operand's registers lie in a lane: 16 rows by each warp.
         unsigned char *const small = ring;
         const char **const base_row = reinterpret_cast<const char **>(small + kRows * 16 * RT * (int)sizeof(T));
         char **const y_row = reinterpret_cast<char **>(small + kRows * (16 * RT * (int)sizeof(T) + 8));

@@ -474,9 +474,10 @@ long long conv_bn_silu_rms_norm_backward_workspace(long long rows, int c);
  *            zeros without an adapter), or NULL
  *   workspace : device, 16-byte aligned, at least conv_bn_silu_linear_adapters_workspace(...)
  *               bytes; NULL when that is 0
- * Sums in fp32; with 16-bit activations hidden is rounded to their type (f16 with a power of two
- * a row) before the second product, and y once more.  float32 activations are products of
- * two-part 19-bit floats, to some 2^-21 of their terms.
+ * Sums in fp32; with 16-bit activations hidden goes to the second product in two parts of their
+ * type, or, in calls of many rows, rounded to it (f16 with a power of two a row), and y is
+ * rounded once.  float32 activations are products of two-part 19-bit floats, to some 2^-21 of
+ * their terms.
  * m <= 2^20; 1 <= k, n <= 2^22; 1 <= rank <= 128; 1 <= adapters <= 4096.  m == 0 is a no-op.
  * Adapters of lower rank than the others are padded with zeros.
  */
