@@ -477,7 +477,8 @@ long long conv_bn_silu_rms_norm_backward_workspace(long long rows, int c);
  * Sums in fp32; with 16-bit activations hidden goes to the second product in two parts of their
  * type, or, in calls of many rows, rounded to it (f16 with a power of two a row), and y is
  * rounded once.  float32 activations are products of two-part 19-bit floats, to some 2^-21 of
- * their terms.
+ * their terms.  What is computed from a value that is not finite is not finite, but may be NaN
+ * where the formula gives an infinity.
  * m <= 2^20; 1 <= k, n <= 2^22; 1 <= rank <= 128; 1 <= adapters <= 4096.  m == 0 is a no-op.
  * Adapters of lower rank than the others are padded with zeros.
  */
