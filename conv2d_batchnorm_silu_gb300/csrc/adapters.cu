@@ -309,7 +309,9 @@ Workspace workspace_of(const AdapterProblem &p, bool gradient, bool tc, int sm_c
     if (gradient && rows > 0) {
         int chunks[2], chunk_rows[2];
         w.most_steps = (int)(rows / kTcStepRows + (p.adapters < rows ? p.adapters : rows));
-        chunks_of(p, adapter_columns(p.rank), 3 * sm_count, rows, 64, kAdapterChunkRows, &chunks[0], &chunk_rows[0]);
+        // A step of 16 rows at least; of a few rows less, since a CTA takes one adapter after the other (18 rows of 8, in
+        // one chunk 30 us, in five 14).
+        chunks_of(p, adapter_columns(p.rank), 3 * sm_count, rows, rows <= 128 ? 4 : 16, kAdapterChunkRows, &chunks[0], &chunk_rows[0]);
         chunks_of(p, 128, 2 * sm_count, w.most_steps, 1, kTcChunkSteps, &chunks[1], &chunk_rows[1]);
         w.chunks = chunks[tc];
         w.chunk_rows = chunk_rows[tc];
