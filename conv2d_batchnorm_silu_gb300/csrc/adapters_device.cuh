@@ -264,6 +264,11 @@ __device__ __forceinline__ float narrow_factor(const float *v, float *s)
     return __uint_as_float((unsigned)(254 - e) << 23);
 }
 
+// Parts of a hidden row in the second product: 16-bit activations' type holds it in two, to 2^-16 of bf16 and 2^-22 of
+// f16 values.
+template <typename T>
+constexpr int hidden_parts() { return sizeof(T) == 4 ? 1 : 2; }
+
 // N rows of N neighbours -> for each neighbour the N values of its rows, as the second operand wants them.
 template <typename T, int K, int N>
 __device__ __forceinline__ void turned(const Near<T, N> (&rows)[K], Near<T, K> (&out)[N])
@@ -513,7 +518,7 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 || (RT == 4 && sizeof
     if (16 * wm < count && (live || a.base != a.y)) {
         // Rows of the first operand.  16-bit: in two parts of the activations' type, f16, whose range the sums may leave,
         // after division by a power of two near the row's largest.
-        constexpr int kParts = sizeof(T) == 4 ? 1 : 2;
+        constexpr int kParts = hidden_parts<T>();
         Near<T, 4> h_lo[kParts][RT], h_hi[kParts][RT];
         float s_lo = live ? (a.scale ? a.scale[adapter] : 1.0f) : 0.0f, s_hi = s_lo;
         if (live) {
@@ -625,10 +630,10 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 || (RT == 4 && sizeof
 // rows wait in shared memory as the first operand's registers lie, and each warp goes through strips of 32 output
 // columns: it holds the strip's weights in registers and takes 32 rows of base at a time, the coming ones on their way
 // through its threads' own places in the ring, with no barrier.
-// bf16, 8192x4096x16384, rank 64: 127 us with the order (4.9 TB/s; 394 with the kernel above and 64 rows a tile, whose
-// weight loads each touched eight lines; 168 with a barrier a step and conditions in the loop).  The second product alone
-// takes 115 us at any rank up to 64 (4.7 TB/s): some 300 instructions for 32x32 outputs, of which the products are 32,
-// on 16 warps an SM, each waiting for its own before.
+// bf16, 8192x4096x16384, rank 64: 156 us with the order (4.0 TB/s; 394 with the kernel above and 64 rows a tile, whose
+// weight loads each touched eight lines; rank 16: 114), bound by shared memory: the second product reads the small rows'
+// two parts again for each strip, 8 KB for 32x32 outputs of 15 KB in all.  With one part, to 2^-8 of the terms s b h, it
+// took 127, as long as the instructions of the epilogue do.
 constexpr int kManyStep = 64;
 
 // Own elements in the ring: eight on their boundary, or the aligned pieces that they lie in.
@@ -653,10 +658,12 @@ constexpr int weight_bytes()
 template <typename T, int RT, bool WIDE>
 constexpr int many_stage() { return 4 * kAdapterThreads * 16 * own_pieces<T, WIDE>() + weight_bytes<T, RT>(); }
 constexpr int kManyStages = 3, kManyAhead = 4;  // of the first and the second product
-// Bytes of the second product's small rows, in the activations' type, in their places in memory, and what they are
-// multiplied with.
+// Bytes of the second product's small rows, in the parts of the activations' type, then their places in memory, and what
+// they are multiplied with.
 template <typename T, int RT>
-constexpr int small_rows() { return kAdapterManyRows * (16 * RT * (int)sizeof(T) + 8 + 8 + 4); }
+constexpr int small_parts() { return 16 * RT * (int)sizeof(T) * hidden_parts<T>(); }  // of a row
+template <typename T, int RT>
+constexpr int small_rows() { return kAdapterManyRows * (small_parts<T, RT>() + 8 + 8 + 4); }
 // The whole sums, behind the partial ones, which other CTAs read, and behind where the small rows go from them.
 template <typename T, int RT>
 constexpr int whole_sums()
@@ -741,10 +748,11 @@ __device__ __forceinline__ Near<T, N> own_of(uint32_t src, const T *p, int have)
 }
 
 template <typename T, int RT, bool TURNED, bool WIDE>
-__global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2 : 1) adapter_many_kernel(const AdapterArgs a)
+__global__ void __launch_bounds__(kAdapterThreads, WIDE && RT <= 4 && sizeof(T) == 2 ? 2 : 1) adapter_many_kernel(const AdapterArgs a)
 {
     constexpr int kRows = kAdapterManyRows, kPitch = hidden_pitch<RT>(), kNear = many_near<T, RT>(), kSteps = 16 * RT / (4 * kNear);
-    constexpr int kQuads = RT * (int)sizeof(T) / 2;  // of the first operand's registers in the second product
+    constexpr int kQuads = RT * (int)sizeof(T) / 2;  // of the first operand's registers in the second product, of one part
+    constexpr int kParts = hidden_parts<T>();
     constexpr int kStages = kManyStages, kStage = many_stage<T, RT, WIDE>();
     constexpr int kOwn = 16 * kAdapterThreads * own_pieces<T, WIDE>();  // bytes of all threads' elements of one row
     extern __shared__ __align__(16) float adapter_sums[];  // a ring; [2][kRows][kPitch] partial and whole sums; small rows and a ring
@@ -927,13 +935,14 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
     const int first = (int)((long long)strips * part / parts), stop = (int)((long long)strips * (part + 1) / parts);
     if (live) {
         cluster_wait();
-        // The small rows in the activations' type, whose rounding of y their own stays below (f16 after division by a power
-        // of two near the row's largest), as the first operand's registers lie in a lane: 16 rows by each warp.
+        // The small rows in the parts of the activations' type (f16 after division by a power of two near the row's
+        // largest), as the first operand's registers lie in a lane: 16 rows by each warp.  One part alone would leave y off
+        // by 2^-8 (f16 2^-11) of the terms s b h, many times its own rounding where they cancel each other or the base.
         unsigned char *const small = ring;
-        const char **const base_row = reinterpret_cast<const char **>(small + kRows * 16 * RT * (int)sizeof(T));
-        char **const y_row = reinterpret_cast<char **>(small + kRows * (16 * RT * (int)sizeof(T) + 8));
+        const char **const base_row = reinterpret_cast<const char **>(small + kRows * small_parts<T, RT>());
+        char **const y_row = reinterpret_cast<char **>(small + kRows * (small_parts<T, RT>() + 8));
         float *const factors = reinterpret_cast<float *>(y_row + kRows);
-        constexpr bool kFactors = __is_same(T, __half);  // else the small rows take the scale before they are rounded
+        constexpr bool kFactors = __is_same(T, __half);  // else the small rows take the scale before they are split
         {
             float v[2][kSteps][kNear];
 #pragma unroll
@@ -959,19 +968,33 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
                     y_row[r] = static_cast<char *>(a.y) + at * a.y_stride * (int)sizeof(T);
                 }
             }
-            uint4 *const to = reinterpret_cast<uint4 *>(small) + warp * kQuads * 32 + lane;
+            uint4 *const to = reinterpret_cast<uint4 *>(small) + warp * kParts * kQuads * 32 + lane;
 #pragma unroll
             for (int k = 0; k < kSteps; ++k)
 #pragma unroll
-                for (int q = 0; q < kNear; q += 8 / (int)sizeof(T)) {
-                    uint4 u;
-                    if constexpr (sizeof(T) == 4)
-                        u = make_uint4(__float_as_uint(v[0][k][q]), __float_as_uint(v[1][k][q]), __float_as_uint(v[0][k][q + 1]), __float_as_uint(v[1][k][q + 1]));
-                    else
-                        u = make_uint4(packed(v[0][k][q], v[0][k][q + 1], T()), packed(v[1][k][q], v[1][k][q + 1], T()),
-                                       packed(v[0][k][q + 2], v[0][k][q + 3], T()), packed(v[1][k][q + 2], v[1][k][q + 3], T()));
-                    to[(k * kNear + q) / (8 / (int)sizeof(T)) * 32] = u;
-                }
+                for (int q = 0; q < kNear; q += 8 / (int)sizeof(T))
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p) {
+                        uint4 u;
+                        if constexpr (sizeof(T) == 4) {
+                            u = make_uint4(__float_as_uint(v[0][k][q]), __float_as_uint(v[1][k][q]), __float_as_uint(v[0][k][q + 1]), __float_as_uint(v[1][k][q + 1]));
+                        } else {
+                            uint32_t w[2][2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    float *const pair = &v[i][k][q + 2 * h];
+                                    w[i][h] = packed(pair[0], pair[1], T());
+                                    // What is left; of infinities and NaN nothing, as their difference with themselves is NaN.
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j)
+                                        pair[j] = fabsf(pair[j]) < __int_as_float(0x7f800000) ? pair[j] - widened(reinterpret_cast<const T *>(&w[i][h])[j]) : 0.0f;
+                                }
+                            u = make_uint4(w[0][0], w[1][0], w[0][1], w[1][1]);
+                        }
+                        to[(p * kQuads + (k * kNear + q) / (8 / (int)sizeof(T))) * 32] = u;
+                    }
         }
         __syncthreads();  // they are there, and the sums read
         const T *w2 = static_cast<const T *>(a.w2) + (long long)adapter * a.rank * a.n;
@@ -1045,15 +1068,18 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 4 && sizeof(T) == 2 ? 2
                 fetch();
                 float acc[2][4][4];
 #pragma unroll
-                for (int j = 0; j < kQuads; ++j)
+                for (int p = kParts - 1; p >= 0; --p)  // the small parts' sums first
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const uint4 h = dev::lds_v4(small_at + ((2 * group + m) * kQuads + j) * 512);
-                        constexpr int kPairs = kNear * (int)sizeof(T) / 8;  // of a lane's weights of a column
+                    for (int j = 0; j < kQuads; ++j)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            mma_quad<T>(acc[m][q], h, w[j / kPairs][q].w[2 * (j % kPairs)], w[j / kPairs][q].w[2 * (j % kPairs) + 1], j == 0);
-                    }
+                        for (int m = 0; m < 2; ++m) {
+                            const uint4 h = dev::lds_v4(small_at + (((2 * group + m) * kParts + p) * kQuads + j) * 512);
+                            constexpr int kPairs = kNear * (int)sizeof(T) / 8;  // of a lane's weights of a column
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                mma_quad<T>(acc[m][q], h, w[j / kPairs][q].w[2 * (j % kPairs)], w[j / kPairs][q].w[2 * (j % kPairs) + 1],
+                                            j == 0 && p == kParts - 1);
+                        }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = 32 * group + 8 * i + g;

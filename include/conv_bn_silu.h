@@ -475,10 +475,10 @@ long long conv_bn_silu_rms_norm_backward_workspace(long long rows, int c);
  *   workspace : device, 16-byte aligned, at least conv_bn_silu_linear_adapters_workspace(...)
  *               bytes; NULL when that is 0
  * Sums in fp32; with 16-bit activations hidden goes to the second product in two parts of their
- * type, or, in calls of many rows, rounded to it (f16 with a power of two a row), and y is
- * rounded once.  float32 activations are products of two-part 19-bit floats, to some 2^-21 of
- * their terms.  What is computed from a value that is not finite is not finite, but may be NaN
- * where the formula gives an infinity.
+ * type (f16 after a power of two a row), which keep 2^-16 (bf16) or 2^-22 of it, and y is rounded
+ * once.  float32 activations are products of two-part 19-bit floats, to some 2^-21 of their terms.
+ * What is computed from a value that is not finite is not finite, but may be NaN where the formula
+ * gives an infinity, as may what is computed from one within 2^-8 of the largest float32.
  * m <= 2^20; 1 <= k, n <= 2^22; 1 <= rank <= 128; 1 <= adapters <= 4096.  m == 0 is a no-op.
  * Adapters of lower rank than the others are padded with zeros.
  */
