@@ -249,11 +249,12 @@ Layout layout_of(const AdapterProblem &p, bool ordered, int k, int n, int sm_cou
     Layout l{};
     l.counted = !ordered && counted(p);
     l.few = l.counted || (!ordered && p.m <= kFew);
-    // Tiles of 128 rows read an adapter's weights an eighth as often, which pays the sooner the higher the rank is
-    // (4096x4096, 16 / 128 rows a tile: rank 16 with 1200 rows 22.3 / 21.6 us, with 2400 30.3 / 29.1; rank 64 with 600 rows
-    // 30.9 / 31.8, with 1200 60 / 34); where an adapter has few rows, on average over all there are, most of such a
-    // tile's warps would have none.
-    l.many = p.m > kFew && !l.few && p.m >= 24LL * p.adapters && (long long)p.m * (adapter_rank_tiles(p.rank) + 1) >= 4096;
+    // Tiles of 128 rows read an adapter's weights an eighth as often, which pays once the tiles of 16 come to several an SM,
+    // the later the fewer ranks they multiply with (bf16, 4096x4096 of 4 adapters, 16 / 128 rows a tile: rank 16 with 1600
+    // rows 17.3 / 20.5 us, with 1800 28.7 / 22.2; rank 32 with 1100 17.5 / 23.8, with 1366 32.4 / 23.6; rank 64 22.4 / 32.4 and
+    // 43.4 / 32.4; rank 128 34.4 / 48.8 and 86.5 / 48.8); where an adapter has few rows, on average over all there are,
+    // most of such a tile's warps would have none.
+    l.many = p.m >= (adapter_rank_tiles(p.rank) == 1 ? 1700 : 1200) && p.m >= 24LL * p.adapters;
     l.tile_rows = l.many ? kAdapterManyRows : kAdapterFewRows;
     const int full = (p.m + l.tile_rows - 1) / l.tile_rows;
     l.tiles = full + (p.adapters + 1 < p.m ? p.adapters + 1 : p.m);
