@@ -35,6 +35,15 @@ import torch
 from . import capi
 
 
+def _current(stream):
+    """A call's stream (torch.cuda.Stream or a handle; None: the current one) as PyTorch's current one."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        handle = capi._stream_handle(stream)
+        # 0 and 1 are the default stream's; as an ExternalStream, 0 would be one of PyTorch's own.
+        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+    return torch.cuda.stream(stream)
+
+
 class TokenBlock:
     """gamma, beta [c] and b1 [hidden], b2 [c] in fp32; w1 [hidden][c] and w2 [c][hidden] of any float type."""
 
@@ -75,10 +84,11 @@ class AdaptedProjection:
 
     def __call__(self, h, residual, index, stream=None):
         """h and residual [..., c], index int32 for each row (outside the adapters: none) -> (z [..., n], total [..., c])."""
-        q, q_scale, total, y = capi.rms_norm_quantize(h, self.gamma, self.eps, residual=residual, return_y=True, stream=stream)
-        z = capi.linear_int8(q, self.w, q_scale, self.w_scale, self.bias, out_dtype=h.dtype, stream=stream)
-        a, b = self.a.to(h.dtype), self.b.to(h.dtype)
-        return capi.linear_adapters(y, index, a, b, self.scale, base=z, y=z, stream=stream), total
+        with _current(stream):  # PyTorch's casts too, whose memory is then the stream's
+            q, q_scale, total, y = capi.rms_norm_quantize(h, self.gamma, self.eps, residual=residual, return_y=True)
+            z = capi.linear_int8(q, self.w, q_scale, self.w_scale, self.bias, out_dtype=h.dtype)
+            a, b = self.a.to(h.dtype), self.b.to(h.dtype)
+            return capi.linear_adapters(y, index, a, b, self.scale, base=z, y=z), total
 
     def tune(self, h, residual, index, target, steps=20, lr=1e-2, bits=8):
         """AdamW steps on the adapters for the mean over rows of |z - target|^2 / 2, with moments of so many bits; the
