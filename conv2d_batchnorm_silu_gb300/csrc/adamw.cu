@@ -1,7 +1,7 @@
 // adamw.cu -- the AdamW step of many tensors in one launch, with the moments in fp32 or in 8 bits.
 //
 //   g' = grad_scale * g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
-//   p = p (1 - lr decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+//   p = p - (lr decay p + lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps))
 //
 // in fp32, p rounded once to its own type.  In 8 bits m and sqrt(v) are e4m3 values with one scale for each 256 in a
 // row (their largest magnitude / 448): sqrt(v), whose range is half of v's, and a float format, so that small values
@@ -135,7 +135,7 @@ __device__ __forceinline__ float either_most(float a, float b)
 }
 
 struct Rates {
-    float lr, decay_factor, step_size, inv_root_c2, grad_scale;
+    float decay, step_size, inv_root_c2, grad_scale;  // decay: lr * decay
     uint32_t step;
 };
 
@@ -143,7 +143,7 @@ struct Rates {
 __device__ __forceinline__ Rates rates_of(const AdamWScalars &s)
 {
     Rates r;
-    r.lr = s.lr_at ? *s.lr_at : s.lr;
+    const float lr = s.lr_at ? *s.lr_at : s.lr;
     r.grad_scale = s.grad_scale_at ? *s.grad_scale_at : s.grad_scale;
     float c1 = s.c1, root_c2 = s.root_c2;
     r.step = (uint32_t)s.step;
@@ -153,8 +153,8 @@ __device__ __forceinline__ Rates rates_of(const AdamWScalars &s)
         c1 = -expm1f((float)t * s.ln_beta1);
         root_c2 = sqrtf(-expm1f((float)t * s.ln_beta2));
     }
-    r.decay_factor = 1.0f - r.lr * s.decay;
-    r.step_size = r.lr / c1;
+    r.decay = lr * s.decay;
+    r.step_size = lr / c1;
     r.inv_root_c2 = 1.0f / root_c2;
     return r;
 }
@@ -229,9 +229,11 @@ __device__ __forceinline__ void step_block(const Entry &e, long long at, const A
         root[j] = root_of(vj.x), root[j + 1] = root_of(vj.y);
         const float2 under = __ffma2_rn(make_float2(root[j], root[j + 1]), both(r.inv_root_c2), both(s.eps));
         const float2 over = __fmul2_rn(mj, both(r.step_size));
-        const float2 pj = __ffma2_rn(make_float2(p[j], p[j + 1]), both(r.decay_factor),
-                                     make_float2(-__fdividef(over.x, under.x), -__fdividef(over.y, under.y)));
-        p[j] = pj.x, p[j + 1] = pj.y;
+        // What p loses, decay and update, before it is taken away: 1 - lr decay would round the decay itself to multiples of
+        // 2^-24, for each element and step the same way (lr decay = 1e-7: by a fifth).
+        const float2 loss = __ffma2_rn(make_float2(p[j], p[j + 1]), both(r.decay),
+                                       make_float2(__fdividef(over.x, under.x), __fdividef(over.y, under.y)));
+        p[j] -= loss.x, p[j + 1] -= loss.y;
     }
     if constexpr (WIDE) {
         put8(p_at + place(0), p);

@@ -514,7 +514,7 @@ long long conv_bn_silu_linear_adapters_backward_workspace(long long m, int k, in
 /*
  * AdamW step of `count` tensors, each in place:
  *   g' = grad_scale * grad,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2
- *   param = param (1 - lr decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *   param = param - (lr decay param + lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps))
  * in fp32, the parameter rounded once to its type.  Elements of a tensor are adjacent.
  *   state_bits 32: m and v are float32 [n].
  *   state_bits 8 : m and v hold 8-bit floats (e4m3) [n], each times the scale of its block of 256

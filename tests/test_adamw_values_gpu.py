@@ -1,0 +1,60 @@
+"""Values of the AdamW step that its other tests' bounds leave room for, against the 64-bit oracle."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import token_ops as ref
+
+pytestmark = pytest.mark.gpu
+E32 = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def capi():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from conv2d_batchnorm_silu_gb300 import capi
+    return capi
+
+
+def host(t):
+    return t.detach().double().cpu().numpy().reshape(-1)
+
+
+def made(seed, n, size=1.0):
+    return (torch.randn(n, generator=torch.Generator().manual_seed(seed)) * size).cuda()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("on_device", [False, True])
+@pytest.mark.parametrize("lr", [1e-3, 1e-4, 1e-5, 2e-6])
+def test_small_decays_are_kept(capi, lr, on_device, bits):
+    """A fp32 parameter is within half a step of its type, and the roundings of what it loses, of the 64-bit result:
+    a decay of lr * 0.01, some steps of the type or a fraction of one, is neither lost nor rounded by itself."""
+    n, rates = 20000, dict(betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01)
+    p, g = [made(1, n)], [made(2, n, 0.1)]
+    before, state = host(p[0]), capi.adamw_state(p, bits)
+    capi.adamw_step(p, g, step=1, lr=torch.full((1,), lr, device="cuda") if on_device else lr, **rates, **state)
+    zero = np.zeros(n)
+    want, _, _ = ref.adamw(before, host(g[0]), zero, zero, 1, lr, 0.9, 0.999, 1e-8, 0.01)
+    # lr and the products, the moments, the root, the quotient and 1 - beta^step
+    lost = 40 * E32 * (lr * 0.01 * np.abs(before) + lr)
+    half = np.spacing(np.maximum(np.abs(want), np.abs(before)).astype(np.float32)).astype(np.float64) / 2
+    off = host(p[0]) - want
+    assert (np.abs(off) <= half + lost).all()
+    # The roundings of p have no side: of n elements, off by up to half a step each, the mean is within some sigmas.
+    relative = off / np.abs(before) * np.sign(before)
+    assert abs(relative.mean()) <= 6 * (2 * half / np.abs(before)).std() / 12 ** 0.5 / n ** 0.5 + 6 * (half / np.abs(before)).mean() / n ** 0.5 + lost.mean()
+
+
+def test_decay_alone_over_many_steps(capi):
+    """Steps without gradients, so that the decay is all there is: at lr * decay = 1e-5 a step is some 100 steps of
+    the type, each rounded to half of one, 2^-25 to 2^-24 of p; 500 of them leave p within 500 * 2^-24."""
+    p = [made(1, 4096)]
+    before, g, state = host(p[0]), [torch.zeros(4096, device="cuda")], capi.adamw_state(p)
+    for step in range(1, 501):
+        capi.adamw_step(p, g, step=step, lr=1e-3, weight_decay=0.01, **state)
+    want = before * (1 - 1e-5) ** 500
+    ratio = host(p[0]) / want - 1
+    assert np.abs(ratio).max() <= 500 * E32
+    assert abs(ratio.mean()) <= 50 * E32  # the roundings fall on both sides
