@@ -673,8 +673,8 @@ def adamw_step(params, grads, exp_avg, exp_avg_sq, step, lr, betas: tuple[float,
                stream=None) -> None:
     """conv_bn_silu_adamw_step: one AdamW step of every parameter, in place, with the moments that adamw_state made.
 
-    params, grads: lists of dense float32, bf16 or f16 tensors of the same sizes; no parameter twice.  step counts from
-    1.  step, lr and grad_scale (which every gradient is multiplied with) may be CUDA tensors of one element (int64,
+    params, grads: lists of dense float32, bf16 or f16 tensors of the same sizes; nothing that the step writes (params,
+    moments, scales) may be given twice, or be a gradient too.  step counts from 1.  step, lr and grad_scale (which every gradient is multiplied with) may be CUDA tensors of one element (int64,
     float32, float32): they are read when the step runs, so that a captured graph can be replayed with other values.
     """
     ops = _token_ops or _load_token_ops()

@@ -6,7 +6,6 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
-#include <utility>
 #include <vector>
 
 #include "conv_bn_silu.h"
@@ -274,6 +273,45 @@ int rms_norm_call(const void *x, long long x_stride, const void *residual, long 
     if (st != CBS_OK) return st;
     cudaError_t e = cbs::rms_norm_launch(p, sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+}
+
+// Bytes that a call reads or writes: [from, to).
+struct Range {
+    uintptr_t from, to;
+};
+
+// Puts ranges in order; false where two of them overlap.  `joined`: those become one.
+bool put_in_order(std::vector<Range> &r, bool joined)
+{
+    auto before = [](const Range &a, const Range &b) { return a.from < b.from; };
+    if (!std::is_sorted(r.begin(), r.end(), before)) std::sort(r.begin(), r.end(), before);
+    size_t n = 0;
+    for (const Range &x : r) {
+        if (n && x.from < r[n - 1].to && !joined) return false;
+        if (n && x.from <= r[n - 1].to)
+            r[n - 1].to = std::max(r[n - 1].to, x.to);
+        else
+            r[n++] = x;
+    }
+    r.resize(n);
+    return true;
+}
+
+// Of two lists of ranges in order: no byte in both.  What lies before the other's next range is passed over by halves.
+bool apart(const std::vector<Range> &a, const std::vector<Range> &b)
+{
+    auto ends_by = [](const Range &x, uintptr_t at) { return x.to <= at; };
+    auto i = a.begin(), j = b.begin();
+    while (i != a.end() && j != b.end()) {
+        if (i->to <= j->from) {
+            if (++i != a.end() && i->to <= j->from) i = std::lower_bound(i, a.end(), j->from, ends_by);
+        } else if (j->to <= i->from) {
+            if (++j != b.end() && j->to <= i->from) j = std::lower_bound(j, b.end(), i->from, ends_by);
+        } else {
+            return false;
+        }
+    }
+    return true;
 }
 
 bool adapter_sizes_ok(long long m, int k, int n, int rank, int adapters, int dtype)
@@ -913,9 +951,15 @@ int conv_bn_silu_adamw_step(const cbs_adamw_tensor *tensors, int count, const cb
     if (!aligned_to(o.lr_device, 4) || !aligned_to(o.grad_scale_device, 4) || !aligned_to(o.step_device, 8))
         return CBS_ERR_MISALIGNED;
     std::vector<cbs::AdamWTensor> v;
-    std::vector<std::pair<uintptr_t, uintptr_t>> written;  // [from, to) of each parameter
+    // What the step writes, by kind: parameters, moments and their scales; and what it reads beside.
+    std::vector<Range> written[5], read;
     v.reserve((size_t)count);
-    written.reserve((size_t)count);
+    for (int i = 0; i < (eight ? 5 : 3); ++i) written[i].reserve((size_t)count);
+    read.reserve((size_t)count + 3);
+    auto range = [](const void *p, long long bytes) {
+        const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+        return Range{from, from + (uintptr_t)bytes};
+    };
     for (int i = 0; i < count; ++i) {
         const cbs_adamw_tensor &t = tensors[i];
         if (t.n < 0 || t.n > (1LL << 40) || t.param_dtype < CBS_DTYPE_F32 || t.param_dtype > CBS_DTYPE_F16 ||
@@ -928,16 +972,29 @@ int conv_bn_silu_adamw_step(const cbs_adamw_tensor *tensors, int count, const cb
             (!eight && (!aligned_to(t.exp_avg, 4) || !aligned_to(t.exp_avg_sq, 4))) ||
             (eight && (!aligned_to(t.exp_avg_scale, 4) || !aligned_to(t.exp_avg_sq_scale, 4))))
             return CBS_ERR_MISALIGNED;
-        const uintptr_t from = reinterpret_cast<uintptr_t>(t.param);
-        written.emplace_back(from, from + (uintptr_t)t.n * cbs::dtype_size(t.param_dtype));
+        written[0].push_back(range(t.param, t.n * cbs::dtype_size(t.param_dtype)));
+        written[1].push_back(range(t.exp_avg, t.n * (eight ? 1 : 4)));
+        written[2].push_back(range(t.exp_avg_sq, t.n * (eight ? 1 : 4)));
+        if (eight) {
+            const long long scales = 4 * ((t.n + cbs::kAdamWBlock - 1) / cbs::kAdamWBlock);
+            written[3].push_back(range(t.exp_avg_scale, scales));
+            written[4].push_back(range(t.exp_avg_sq_scale, scales));
+        }
+        read.push_back(range(t.grad, t.n * cbs::dtype_size(t.grad_dtype)));
         v.push_back(cbs::AdamWTensor{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale, t.n,
                                      t.param_dtype, t.grad_dtype});
     }
     if (v.empty()) return CBS_OK;
-    // A parameter given twice would be stepped by two blocks at once.
-    if (!std::is_sorted(written.begin(), written.end())) std::sort(written.begin(), written.end());
-    for (size_t i = 1; i < written.size(); ++i)
-        if (written[i].first < written[i - 1].second) return CBS_ERR_INVALID_ARG;
+    if (o.lr_device) read.push_back(range(o.lr_device, 4));
+    if (o.grad_scale_device) read.push_back(range(o.grad_scale_device, 4));
+    if (o.step_device) read.push_back(range(o.step_device, 8));
+    // What two blocks write, or one writes and another reads, has no one result.
+    put_in_order(read, true);
+    for (int i = 0; i < 5; ++i) {
+        if (!put_in_order(written[i], false) || !apart(written[i], read)) return CBS_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (!apart(written[i], written[j])) return CBS_ERR_INVALID_ARG;
+    }
     cbs::AdamWScalars s{};
     s.lr_at = o.lr_device;
     s.grad_scale_at = o.grad_scale_device;

@@ -524,8 +524,10 @@ long long conv_bn_silu_linear_adapters_backward_workspace(long long m, int k, in
  *                  (element + step * 0x9E3779B9) modulo 2^32, so the same step gives the same bits
  *                  again; where v is not 0 its root is held as 2^-9 of the scale at least.  A block with a
  *                  gradient that is not finite has NaN for its m.  Zeros everywhere are the initial state.
- * No tensor may overlap another; pointers are aligned to their element, and those aligned to 8
- * elements (float32 to 32 bytes) run on wide loads and stores.
+ * What the step writes (parameters, moments, scales) may overlap neither another of these nor a
+ * gradient or a number that it reads: CBS_ERR_INVALID_ARG.  Gradients may overlap each other.
+ * Pointers are aligned to their element, and those aligned to 8 elements (float32 to 32 bytes) run
+ * on wide loads and stores.
  */
 typedef struct cbs_adamw_tensor {
     void *param;             /* device, param_dtype [n] */
