@@ -6,6 +6,8 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
+#include <new>
+#include <stdexcept>
 #include <vector>
 
 #include "conv_bn_silu.h"
@@ -20,6 +22,19 @@ int cuda_fail(cudaError_t e)
 {
     t_last_cuda_error = (int)e;
     return CBS_ERR_CUDA;
+}
+
+// A call that allocates on the host: a C caller gets a status, where an exception would end the process.
+template <typename F>
+int without_exceptions(F &&call)
+{
+    try {
+        return call();
+    } catch (const std::bad_alloc &) {
+        return cuda_fail(cudaErrorMemoryAllocation);
+    } catch (const std::length_error &) {
+        return cuda_fail(cudaErrorMemoryAllocation);
+    }
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -416,21 +431,23 @@ int conv_bn_silu_fold(const float *gamma, const float *beta, const float *mean, 
 int conv_bn_silu_fold_batch(const cbs_fold_layer *layers, int n_layers, void *stream)
 {
     if (n_layers < 0 || (n_layers > 0 && !layers)) return CBS_ERR_INVALID_ARG;
-    std::vector<cbs::FoldLayer> v;
-    v.reserve((size_t)n_layers);
-    for (int i = 0; i < n_layers; ++i) {
-        const cbs_fold_layer &L = layers[i];
-        if (L.c_out < 0 || !(L.eps >= 0.0f) || L.eps > 3.0e38f) return CBS_ERR_INVALID_ARG;
-        if (L.c_out == 0) continue;
-        if (!L.gamma || !L.beta || !L.mean || !L.var || !L.scale || !L.bias) return CBS_ERR_INVALID_ARG;
-        if (!aligned16(L.gamma) || !aligned16(L.beta) || !aligned16(L.mean) || !aligned16(L.var) ||
-            !aligned16(L.scale) || !aligned16(L.bias))
-            return CBS_ERR_MISALIGNED;
-        v.push_back(cbs::FoldLayer{L.gamma, L.beta, L.mean, L.var, L.eps, L.c_out, L.scale, L.bias});
-    }
-    if (v.empty()) return CBS_OK;
-    cudaError_t e = cbs::fold_batch_launch(v.data(), (int)v.size(), static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+    return without_exceptions([&]() -> int {
+        std::vector<cbs::FoldLayer> v;
+        v.reserve((size_t)n_layers);
+        for (int i = 0; i < n_layers; ++i) {
+            const cbs_fold_layer &L = layers[i];
+            if (L.c_out < 0 || !(L.eps >= 0.0f) || L.eps > 3.0e38f) return CBS_ERR_INVALID_ARG;
+            if (L.c_out == 0) continue;
+            if (!L.gamma || !L.beta || !L.mean || !L.var || !L.scale || !L.bias) return CBS_ERR_INVALID_ARG;
+            if (!aligned16(L.gamma) || !aligned16(L.beta) || !aligned16(L.mean) || !aligned16(L.var) ||
+                !aligned16(L.scale) || !aligned16(L.bias))
+                return CBS_ERR_MISALIGNED;
+            v.push_back(cbs::FoldLayer{L.gamma, L.beta, L.mean, L.var, L.eps, L.c_out, L.scale, L.bias});
+        }
+        if (v.empty()) return CBS_OK;
+        cudaError_t e = cbs::fold_batch_launch(v.data(), (int)v.size(), static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+    });
 }
 
 int conv_bn_silu_forward_algo(const void *x, const void *w, const float *scale, const float *bias,
@@ -950,72 +967,74 @@ int conv_bn_silu_adamw_step(const cbs_adamw_tensor *tensors, int count, const cb
     if (!o.step_device && o.step < 1) return CBS_ERR_INVALID_ARG;
     if (!aligned_to(o.lr_device, 4) || !aligned_to(o.grad_scale_device, 4) || !aligned_to(o.step_device, 8))
         return CBS_ERR_MISALIGNED;
-    std::vector<cbs::AdamWTensor> v;
-    // What the step writes, by kind: parameters, moments and their scales; and what it reads beside.
-    std::vector<Range> written[5], read;
-    v.reserve((size_t)count);
-    for (int i = 0; i < (eight ? 5 : 3); ++i) written[i].reserve((size_t)count);
-    read.reserve((size_t)count + 3);
-    auto range = [](const void *p, long long bytes) {
-        const uintptr_t from = reinterpret_cast<uintptr_t>(p);
-        return Range{from, from + (uintptr_t)bytes};
-    };
-    for (int i = 0; i < count; ++i) {
-        const cbs_adamw_tensor &t = tensors[i];
-        if (t.n < 0 || t.n > (1LL << 40) || t.param_dtype < CBS_DTYPE_F32 || t.param_dtype > CBS_DTYPE_F16 ||
-            t.grad_dtype < CBS_DTYPE_F32 || t.grad_dtype > CBS_DTYPE_F16)
-            return CBS_ERR_INVALID_ARG;
-        if (t.n == 0) continue;
-        if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq || (eight && (!t.exp_avg_scale || !t.exp_avg_sq_scale)))
-            return CBS_ERR_INVALID_ARG;
-        if (!aligned_to(t.param, cbs::dtype_size(t.param_dtype)) || !aligned_to(t.grad, cbs::dtype_size(t.grad_dtype)) ||
-            (!eight && (!aligned_to(t.exp_avg, 4) || !aligned_to(t.exp_avg_sq, 4))) ||
-            (eight && (!aligned_to(t.exp_avg_scale, 4) || !aligned_to(t.exp_avg_sq_scale, 4))))
-            return CBS_ERR_MISALIGNED;
-        written[0].push_back(range(t.param, t.n * cbs::dtype_size(t.param_dtype)));
-        written[1].push_back(range(t.exp_avg, t.n * (eight ? 1 : 4)));
-        written[2].push_back(range(t.exp_avg_sq, t.n * (eight ? 1 : 4)));
-        if (eight) {
-            const long long scales = 4 * ((t.n + cbs::kAdamWBlock - 1) / cbs::kAdamWBlock);
-            written[3].push_back(range(t.exp_avg_scale, scales));
-            written[4].push_back(range(t.exp_avg_sq_scale, scales));
+    return without_exceptions([&]() -> int {
+        std::vector<cbs::AdamWTensor> v;
+        // What the step writes, by kind: parameters, moments and their scales; and what it reads beside.
+        std::vector<Range> written[5], read;
+        v.reserve((size_t)count);
+        for (int i = 0; i < (eight ? 5 : 3); ++i) written[i].reserve((size_t)count);
+        read.reserve((size_t)count + 3);
+        auto range = [](const void *p, long long bytes) {
+            const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+            return Range{from, from + (uintptr_t)bytes};
+        };
+        for (int i = 0; i < count; ++i) {
+            const cbs_adamw_tensor &t = tensors[i];
+            if (t.n < 0 || t.n > (1LL << 40) || t.param_dtype < CBS_DTYPE_F32 || t.param_dtype > CBS_DTYPE_F16 ||
+                t.grad_dtype < CBS_DTYPE_F32 || t.grad_dtype > CBS_DTYPE_F16)
+                return CBS_ERR_INVALID_ARG;
+            if (t.n == 0) continue;
+            if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq || (eight && (!t.exp_avg_scale || !t.exp_avg_sq_scale)))
+                return CBS_ERR_INVALID_ARG;
+            if (!aligned_to(t.param, cbs::dtype_size(t.param_dtype)) || !aligned_to(t.grad, cbs::dtype_size(t.grad_dtype)) ||
+                (!eight && (!aligned_to(t.exp_avg, 4) || !aligned_to(t.exp_avg_sq, 4))) ||
+                (eight && (!aligned_to(t.exp_avg_scale, 4) || !aligned_to(t.exp_avg_sq_scale, 4))))
+                return CBS_ERR_MISALIGNED;
+            written[0].push_back(range(t.param, t.n * cbs::dtype_size(t.param_dtype)));
+            written[1].push_back(range(t.exp_avg, t.n * (eight ? 1 : 4)));
+            written[2].push_back(range(t.exp_avg_sq, t.n * (eight ? 1 : 4)));
+            if (eight) {
+                const long long scales = 4 * ((t.n + cbs::kAdamWBlock - 1) / cbs::kAdamWBlock);
+                written[3].push_back(range(t.exp_avg_scale, scales));
+                written[4].push_back(range(t.exp_avg_sq_scale, scales));
+            }
+            read.push_back(range(t.grad, t.n * cbs::dtype_size(t.grad_dtype)));
+            v.push_back(cbs::AdamWTensor{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale, t.n,
+                                         t.param_dtype, t.grad_dtype});
         }
-        read.push_back(range(t.grad, t.n * cbs::dtype_size(t.grad_dtype)));
-        v.push_back(cbs::AdamWTensor{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale, t.n,
-                                     t.param_dtype, t.grad_dtype});
-    }
-    if (v.empty()) return CBS_OK;
-    if (o.lr_device) read.push_back(range(o.lr_device, 4));
-    if (o.grad_scale_device) read.push_back(range(o.grad_scale_device, 4));
-    if (o.step_device) read.push_back(range(o.step_device, 8));
-    // What two blocks write, or one writes and another reads, has no one result.
-    put_in_order(read, true);
-    for (int i = 0; i < 5; ++i) {
-        if (!put_in_order(written[i], false) || !apart(written[i], read)) return CBS_ERR_INVALID_ARG;
-        for (int j = 0; j < i; ++j)
-            if (!apart(written[i], written[j])) return CBS_ERR_INVALID_ARG;
-    }
-    cbs::AdamWScalars s{};
-    s.lr_at = o.lr_device;
-    s.grad_scale_at = o.grad_scale_device;
-    s.step_at = o.step_device;
-    s.lr = (float)o.lr;
-    s.grad_scale = (float)o.grad_scale;
-    s.beta1 = (float)o.beta1;
-    s.beta2 = (float)o.beta2;
-    s.rest1 = (float)(1.0 - o.beta1);
-    s.rest2 = (float)(1.0 - o.beta2);
-    s.ln_beta1 = (float)std::log(o.beta1);  // of 0: -infinity, and 1 - beta^t is 1
-    s.ln_beta2 = (float)std::log(o.beta2);
-    if (!o.step_device) {
-        s.step = o.step;
-        s.c1 = (float)-std::expm1((double)o.step * std::log(o.beta1));
-        s.root_c2 = (float)std::sqrt(-std::expm1((double)o.step * std::log(o.beta2)));
-    }
-    s.eps = (float)o.eps;
-    s.decay = (float)o.weight_decay;
-    cudaError_t e = cbs::adamw_launch(v.data(), (int)v.size(), s, eight, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+        if (v.empty()) return CBS_OK;
+        if (o.lr_device) read.push_back(range(o.lr_device, 4));
+        if (o.grad_scale_device) read.push_back(range(o.grad_scale_device, 4));
+        if (o.step_device) read.push_back(range(o.step_device, 8));
+        // What two blocks write, or one writes and another reads, has no one result.
+        put_in_order(read, true);
+        for (int i = 0; i < 5; ++i) {
+            if (!put_in_order(written[i], false) || !apart(written[i], read)) return CBS_ERR_INVALID_ARG;
+            for (int j = 0; j < i; ++j)
+                if (!apart(written[i], written[j])) return CBS_ERR_INVALID_ARG;
+        }
+        cbs::AdamWScalars s{};
+        s.lr_at = o.lr_device;
+        s.grad_scale_at = o.grad_scale_device;
+        s.step_at = o.step_device;
+        s.lr = (float)o.lr;
+        s.grad_scale = (float)o.grad_scale;
+        s.beta1 = (float)o.beta1;
+        s.beta2 = (float)o.beta2;
+        s.rest1 = (float)(1.0 - o.beta1);
+        s.rest2 = (float)(1.0 - o.beta2);
+        s.ln_beta1 = (float)std::log(o.beta1);  // of 0: -infinity, and 1 - beta^t is 1
+        s.ln_beta2 = (float)std::log(o.beta2);
+        if (!o.step_device) {
+            s.step = o.step;
+            s.c1 = (float)-std::expm1((double)o.step * std::log(o.beta1));
+            s.root_c2 = (float)std::sqrt(-std::expm1((double)o.step * std::log(o.beta2)));
+        }
+        s.eps = (float)o.eps;
+        s.decay = (float)o.weight_decay;
+        cudaError_t e = cbs::adamw_launch(v.data(), (int)v.size(), s, eight, static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? CBS_OK : cuda_fail(e);
+    });
 }
 
 long long conv_bn_silu_linear_int8_workspace(long long m, int n, int k)
