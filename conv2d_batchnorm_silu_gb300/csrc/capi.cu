@@ -924,6 +924,7 @@ int conv_bn_silu_linear_adapters_backward(const void *dy, long long dy_stride, c
     if (st != CBS_OK) return st;
     if (!index || !a || !b || !hidden || !workspace || !same_or_apart(base, base_stride, dx, dx_stride, m))
         return CBS_ERR_INVALID_ARG;
+    if (dx == dy || dx == x) return CBS_ERR_INVALID_ARG;  // the weights' gradients read both after dx is written
     if (!aligned_to(index, 4) || !aligned_to(a, size) || !aligned_to(b, size) || !aligned_to(scale, 4) ||
         !aligned_to(hidden, 4) || !aligned16(workspace))
         return CBS_ERR_MISALIGNED;

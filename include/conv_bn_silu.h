@@ -494,7 +494,7 @@ int conv_bn_silu_linear_adapters(const void *x, long long x_stride, const int *i
  *   dy, x, index, a, b, scale : of the forward call
  *   hidden : device, float32 [m][rank], written by the forward call
  *   base   : device, dtype [m][k], or NULL for 0: the gradient that x has from elsewhere.  It may be dx itself
- *   dx     : device, dtype [m][k], written
+ *   dx     : device, dtype [m][k], written; neither dy nor x, which are read again behind it
  *   da, db : device, float32 [adapters][rank][k] and [adapters][n][rank], written (zeros for adapters
  *            without rows)
  * The gradient of base is dy itself.  Sizes as in the forward call; m == 0 leaves da and db zero.
