@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <mutex>
 #include <new>
 #include <stdexcept>
@@ -1031,7 +1032,9 @@ int conv_bn_silu_adamw_step(const cbs_adamw_tensor *tensors, int count, const cb
             s.c1 = (float)-std::expm1((double)o.step * std::log(o.beta1));
             s.root_c2 = (float)std::sqrt(-std::expm1((double)o.step * std::log(o.beta2)));
         }
-        s.eps = (float)o.eps;
+        // Not 0 where it was not, and no subnormal, by which the kernel's quotient of 0 would be NaN; beside a root, 2^-75 at
+        // least, neither shows.
+        s.eps = o.eps > 0.0 ? std::max((float)o.eps, std::numeric_limits<float>::min()) : 0.0f;
         s.decay = (float)o.weight_decay;
         cudaError_t e = cbs::adamw_launch(v.data(), (int)v.size(), s, eight, static_cast<cudaStream_t>(stream));
         return e == cudaSuccess ? CBS_OK : cuda_fail(e);

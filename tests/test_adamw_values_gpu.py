@@ -58,3 +58,15 @@ def test_decay_alone_over_many_steps(capi):
     ratio = host(p[0]) / want - 1
     assert np.abs(ratio).max() <= 500 * E32
     assert abs(ratio.mean()) <= 50 * E32  # the roundings fall on both sides
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("eps", [1e-30, 1e-39, 1e-44, 1e-50, 1e-300])
+def test_the_smallest_eps_keeps_elements_without_gradients(capi, eps, bits):
+    """m = v = 0: the update is 0 / eps, and the decay, of half a step of the type and its own roundings, is all."""
+    p, g = [made(1, 3000)], [torch.zeros(3000, device="cuda")]
+    g[0][1::3] = 0.5
+    before, state = host(p[0]), capi.adamw_state(p, bits)
+    capi.adamw_step(p, g, step=1, lr=1e-3, eps=eps, weight_decay=0.1, **state)
+    want = before * (1 - 1e-4) - 1e-3 * (host(g[0]) > 0)  # the first step's update is the gradient's sign
+    assert (np.abs(host(p[0]) - want) <= E32 * np.abs(want) + 40 * E32 * (1e-4 * np.abs(before) + 1e-3)).all()
