@@ -291,44 +291,58 @@ int rms_norm_call(const void *x, long long x_stride, const void *residual, long 
     return e == cudaSuccess ? CBS_OK : cuda_fail(e);
 }
 
-// Bytes that a call reads or writes: [from, to).
+// Bytes that a call reads or writes, [from, to): ranges in order, those that touch as one.
 struct Range {
     uintptr_t from, to;
 };
-
-// Puts ranges in order; false where two of them overlap.  `joined`: those become one.
-bool put_in_order(std::vector<Range> &r, bool joined)
-{
-    auto before = [](const Range &a, const Range &b) { return a.from < b.from; };
-    if (!std::is_sorted(r.begin(), r.end(), before)) std::sort(r.begin(), r.end(), before);
-    size_t n = 0;
-    for (const Range &x : r) {
-        if (n && x.from < r[n - 1].to && !joined) return false;
-        if (n && x.from <= r[n - 1].to)
-            r[n - 1].to = std::max(r[n - 1].to, x.to);
-        else
-            r[n++] = x;
-    }
-    r.resize(n);
-    return true;
-}
-
-// Of two lists of ranges in order: no byte in both.  What lies before the other's next range is passed over by halves.
-bool apart(const std::vector<Range> &a, const std::vector<Range> &b)
-{
-    auto ends_by = [](const Range &x, uintptr_t at) { return x.to <= at; };
-    auto i = a.begin(), j = b.begin();
-    while (i != a.end() && j != b.end()) {
-        if (i->to <= j->from) {
-            if (++i != a.end() && i->to <= j->from) i = std::lower_bound(i, a.end(), j->from, ends_by);
-        } else if (j->to <= i->from) {
-            if (++j != b.end() && j->to <= i->from) j = std::lower_bound(j, b.end(), i->from, ends_by);
-        } else {
-            return false;
+struct Ranges {
+    std::vector<Range> r;
+    bool ordered = true;
+    void add(const void *p, long long bytes)
+    {
+        const uintptr_t from = reinterpret_cast<uintptr_t>(p), to = from + (uintptr_t)bytes;
+        if (!r.empty() && from == r.back().to) {
+            r.back().to = to;
+            return;
         }
+        ordered = ordered && (r.empty() || from > r.back().to);
+        r.push_back(Range{from, to});
     }
-    return true;
-}
+    // Brings them in order where they did not come so; false where two overlap, which then are one.
+    bool put_in_order()
+    {
+        if (ordered) return true;
+        std::sort(r.begin(), r.end(), [](const Range &a, const Range &b) { return a.from < b.from; });
+        bool apart = true;
+        size_t n = 0;
+        for (const Range &x : r) {
+            if (n && x.from <= r[n - 1].to) {
+                apart = apart && x.from == r[n - 1].to;
+                r[n - 1].to = std::max(r[n - 1].to, x.to);
+            } else {
+                r[n++] = x;
+            }
+        }
+        r.resize(n);
+        return apart;
+    }
+    // No byte in both.  What lies before the other's next range is passed over by halves.
+    bool apart_from(const Ranges &other) const
+    {
+        auto ends_by = [](const Range &x, uintptr_t at) { return x.to <= at; };
+        auto i = r.begin(), i1 = r.end(), j = other.r.begin(), j1 = other.r.end();
+        while (i != i1 && j != j1) {
+            if (i->to <= j->from) {
+                if (++i != i1 && i->to <= j->from) i = std::lower_bound(i, i1, j->from, ends_by);
+            } else if (j->to <= i->from) {
+                if (++j != j1 && j->to <= i->from) j = std::lower_bound(j, j1, i->from, ends_by);
+            } else {
+                return false;
+            }
+        }
+        return true;
+    }
+};
 
 bool adapter_sizes_ok(long long m, int k, int n, int rank, int adapters, int dtype)
 {
@@ -972,14 +986,8 @@ int conv_bn_silu_adamw_step(const cbs_adamw_tensor *tensors, int count, const cb
     return without_exceptions([&]() -> int {
         std::vector<cbs::AdamWTensor> v;
         // What the step writes, by kind: parameters, moments and their scales; and what it reads beside.
-        std::vector<Range> written[5], read;
+        Ranges written[5], read;
         v.reserve((size_t)count);
-        for (int i = 0; i < (eight ? 5 : 3); ++i) written[i].reserve((size_t)count);
-        read.reserve((size_t)count + 3);
-        auto range = [](const void *p, long long bytes) {
-            const uintptr_t from = reinterpret_cast<uintptr_t>(p);
-            return Range{from, from + (uintptr_t)bytes};
-        };
         for (int i = 0; i < count; ++i) {
             const cbs_adamw_tensor &t = tensors[i];
             if (t.n < 0 || t.n > (1LL << 40) || t.param_dtype < CBS_DTYPE_F32 || t.param_dtype > CBS_DTYPE_F16 ||
@@ -992,28 +1000,28 @@ int conv_bn_silu_adamw_step(const cbs_adamw_tensor *tensors, int count, const cb
                 (!eight && (!aligned_to(t.exp_avg, 4) || !aligned_to(t.exp_avg_sq, 4))) ||
                 (eight && (!aligned_to(t.exp_avg_scale, 4) || !aligned_to(t.exp_avg_sq_scale, 4))))
                 return CBS_ERR_MISALIGNED;
-            written[0].push_back(range(t.param, t.n * cbs::dtype_size(t.param_dtype)));
-            written[1].push_back(range(t.exp_avg, t.n * (eight ? 1 : 4)));
-            written[2].push_back(range(t.exp_avg_sq, t.n * (eight ? 1 : 4)));
+            written[0].add(t.param, t.n * cbs::dtype_size(t.param_dtype));
+            written[1].add(t.exp_avg, t.n * (eight ? 1 : 4));
+            written[2].add(t.exp_avg_sq, t.n * (eight ? 1 : 4));
             if (eight) {
                 const long long scales = 4 * ((t.n + cbs::kAdamWBlock - 1) / cbs::kAdamWBlock);
-                written[3].push_back(range(t.exp_avg_scale, scales));
-                written[4].push_back(range(t.exp_avg_sq_scale, scales));
+                written[3].add(t.exp_avg_scale, scales);
+                written[4].add(t.exp_avg_sq_scale, scales);
             }
-            read.push_back(range(t.grad, t.n * cbs::dtype_size(t.grad_dtype)));
+            read.add(t.grad, t.n * cbs::dtype_size(t.grad_dtype));
             v.push_back(cbs::AdamWTensor{t.param, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_scale, t.exp_avg_sq_scale, t.n,
                                          t.param_dtype, t.grad_dtype});
         }
         if (v.empty()) return CBS_OK;
-        if (o.lr_device) read.push_back(range(o.lr_device, 4));
-        if (o.grad_scale_device) read.push_back(range(o.grad_scale_device, 4));
-        if (o.step_device) read.push_back(range(o.step_device, 8));
+        if (o.lr_device) read.add(o.lr_device, 4);
+        if (o.grad_scale_device) read.add(o.grad_scale_device, 4);
+        if (o.step_device) read.add(o.step_device, 8);
         // What two blocks write, or one writes and another reads, has no one result.
-        put_in_order(read, true);
+        read.put_in_order();  // gradients may share memory
         for (int i = 0; i < 5; ++i) {
-            if (!put_in_order(written[i], false) || !apart(written[i], read)) return CBS_ERR_INVALID_ARG;
+            if (!written[i].put_in_order() || !written[i].apart_from(read)) return CBS_ERR_INVALID_ARG;
             for (int j = 0; j < i; ++j)
-                if (!apart(written[i], written[j])) return CBS_ERR_INVALID_ARG;
+                if (!written[i].apart_from(written[j])) return CBS_ERR_INVALID_ARG;
         }
         cbs::AdamWScalars s{};
         s.lr_at = o.lr_device;
