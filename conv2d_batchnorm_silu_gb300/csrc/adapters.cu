@@ -297,7 +297,14 @@ void chunks_of(const AdapterProblem &p, int columns, int ctas, long long units, 
     *chunks = (int)((units + *chunk_units - 1) / *chunk_units);
 }
 
-// `tc`: with the chunks of adapter_tc_weights_kernel; the bytes are enough for either kernel.
+// Sizes that adapter_tc_weights_kernel takes, if type and boundaries allow it: where an adapter has few rows on average,
+// most of a step's 64 would be none.
+bool tc_sizes(const AdapterProblem &p)
+{
+    return p.k % 8 == 0 && p.n % 8 == 0 && adapter_rank_tiles(p.rank) <= 4 && p.m >= 1024 && p.m >= 128LL * p.adapters;
+}
+
+// `tc`: with the chunks of adapter_tc_weights_kernel; the bytes are enough for any kernel that the sizes allow.
 Workspace workspace_of(const AdapterProblem &p, bool gradient, bool tc, int sm_count)
 {
     Workspace w{};
@@ -313,12 +320,14 @@ Workspace workspace_of(const AdapterProblem &p, bool gradient, bool tc, int sm_c
         // A step of 16 rows at least; of a few rows less, since a CTA takes one adapter after the other (18 rows of 8, in
         // one chunk 30 us, in five 14).
         chunks_of(p, adapter_columns(p.rank), 3 * sm_count, rows, rows <= 128 ? 4 : 16, kAdapterChunkRows, &chunks[0], &chunk_rows[0]);
-        chunks_of(p, 128, 2 * sm_count, w.most_steps, 1, kTcChunkSteps, &chunks[1], &chunk_rows[1]);
+        const bool steps = tc_sizes(p);
+        chunks[1] = chunk_rows[1] = 0;
+        if (steps) chunks_of(p, 128, 2 * sm_count, w.most_steps, 1, kTcChunkSteps, &chunks[1], &chunk_rows[1]);
         w.chunks = chunks[tc];
         w.chunk_rows = chunk_rows[tc];
         w.steps = w.step_starts + up16(4LL * (p.adapters + 1));
-        w.operands = (w.steps + 16LL * w.most_steps + 127) / 128 * 128;
-        w.dhidden = w.operands + 2LL * w.most_steps * adapter_tc_operand(p.rank);
+        w.operands = (w.steps + (steps ? 16LL * w.most_steps : 0) + 127) / 128 * 128;
+        w.dhidden = w.operands + (steps ? 2LL * w.most_steps * adapter_tc_operand(p.rank) : 0);
         w.partial = w.dhidden + up16(4 * rows * p.rank);
         w.bytes = w.partial + 8LL * (chunks[0] > chunks[1] ? chunks[0] : chunks[1]) * p.rank * ((long long)p.k + p.n);
     }
@@ -407,10 +416,9 @@ cudaError_t adapters_grad_launch(const AdapterProblem &p, int sm_count, cudaStre
     const int size = dtype_size(p.dtype);
     const Layout l = layout_of(p, true, p.n, p.k, sm_count);
     const bool x_wide = p.k % 8 == 0 && on_boundary(p.x.data, p.x.stride, size), dy_wide = p.n % 8 == 0 && on_boundary(p.dy.data, p.dy.stride, size);
-    // Where an adapter has few rows on average, most of a step's 64 would be none; a tensor map's rows are less than 2^40
-    // bytes apart.
-    const bool tc = p.dtype == kBf16 && x_wide && dy_wide && p.x.stride >= p.k && p.dy.stride >= p.n && p.x.stride < (1LL << 39) &&
-                    p.dy.stride < (1LL << 39) && adapter_rank_tiles(p.rank) <= 4 && p.m >= 1024 && p.m >= 128LL * p.adapters;
+    // A tensor map's rows are less than 2^40 bytes apart.
+    const bool tc = p.dtype == kBf16 && tc_sizes(p) && x_wide && dy_wide && p.x.stride >= p.k && p.dy.stride >= p.n &&
+                    p.x.stride < (1LL << 39) && p.dy.stride < (1LL << 39);
     const Workspace w = workspace_of(p, true, tc, sm_count);
     char *work = static_cast<char *>(p.workspace);
     OrderArgs o = order_args(p, w, l, work);
