@@ -317,9 +317,11 @@ Workspace workspace_of(const AdapterProblem &p, bool gradient, bool tc, int sm_c
     if (gradient && rows > 0) {
         int chunks[2], chunk_rows[2];
         w.most_steps = (int)(rows / kTcStepRows + (p.adapters < rows ? p.adapters : rows));
-        // A step of 16 rows at least; of a few rows less, since a CTA takes one adapter after the other (18 rows of 8, in
-        // one chunk 30 us, in five 14).
-        chunks_of(p, adapter_columns(p.rank), 3 * sm_count, rows, rows <= 128 ? 4 : 16, kAdapterChunkRows, &chunks[0], &chunk_rows[0]);
+        // A step of 16 rows at least, or as many as an adapter has on average, since a CTA takes one adapter after the other.
+        // (bf16, rank 12 to 16, k and n 4096, least 4 rows / 16 / that many: 18 rows of 64 adapters 89 / 114 / 61 us, 200 of 64
+        // 116 / 159 / 114, 64 of 8 42 / 36 / 38; f32, 160 of 8 49 / 38 / 38, 200 of 32 81 / 72 / 81.)
+        const long long each = (rows + p.adapters - 1) / p.adapters;
+        chunks_of(p, adapter_columns(p.rank), 3 * sm_count, rows, each < 16 ? (int)each : 16, kAdapterChunkRows, &chunks[0], &chunk_rows[0]);
         const bool steps = tc_sizes(p);
         chunks[1] = chunk_rows[1] = 0;
         if (steps) chunks_of(p, 128, 2 * sm_count, w.most_steps, 1, kTcChunkSteps, &chunks[1], &chunk_rows[1]);
