@@ -6,9 +6,15 @@
 // in fp32, p rounded once to its own type.  In 8 bits m and sqrt(v) are e4m3 values with one scale for each 256 in a
 // row (their largest magnitude / 448): sqrt(v), whose range is half of v's, and a float format, so that small values
 // beside a large one keep their relative precision.  They are rounded to one of the two values around them with the
-// odds that keep the mean: to nearest, a change of less than a sixteenth a step (beta2 = 0.999 changes v by a
+// odds that keep the value's mean: to nearest, a change of less than a sixteenth a step (beta2 = 0.999 changes v by a
 // thousandth) would be lost each time.  The odds come from the place and the step alone.  sqrt(v) never becomes 0
 // where it was not: m / (0 + eps) would be a step without bounds.  This step itself uses m and v before the rounding.
+//
+// What that costs: with d the distance of the values around a root r, a step of steady gradients changes the root by
+// |c| = (1 - beta2) / 2 r |g^2 / v - 1|, 0.48 (1 - beta2) r on average over normal ones, and its rounding adds |c| d to the
+// variance.  v, its square, grows by as much, until it lies above the gradients' own by 0.48 d / r, of which the root's
+// variance is half: d / r is a sixteenth to an eighth, so roots spread by 12 to 17 % and v is 3 to 6 % too large, for any
+// beta2 near 1 (a restatement over 8000 steps: 16.6 and 5.3).
 //
 // Measured: 66M fp32 elements with fp32 moments 263 us (7.1 TB/s, memory); 8.3M in 192 bf16 tensors with 8-bit moments
 // 28.5 us (3.5 TB/s), bound by some 80 instructions an element, most of them the dither and the rounding to 8 bits, and by

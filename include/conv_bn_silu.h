@@ -522,7 +522,10 @@ long long conv_bn_silu_linear_adapters_backward_workspace(long long m, int k, in
  *                  (2^-100 at least) / 448.  A value goes to one of the two around it: to
  *                  floor(|value| / distance + u) * distance with u in [0, 1) from the mixed bits of
  *                  (element + step * 0x9E3779B9) modulo 2^32, so the same step gives the same bits
- *                  again; where v is not 0 its root is held as 2^-9 of the scale at least.  A block with a
+ *                  again; where v is not 0 its root is held as 2^-9 of the scale at least.  The odds keep the
+ *                  mean of a value that is rounded, not of v over many steps: under steady gradients
+ *                  the held roots spread by 12 to 17 % of themselves, and v is 3 to 6 % larger than
+ *                  in 32 bits (where beta2 = 0.999 leaves roots a spread of 1.6 %).  A block with a
  *                  gradient that is not finite has NaN for its m.  Zeros everywhere are the initial state.
  * What the step writes (parameters, moments, scales) may overlap neither another of these nor a
  * gradient or a number that it reads: CBS_ERR_INVALID_ARG.  Gradients may overlap each other.
