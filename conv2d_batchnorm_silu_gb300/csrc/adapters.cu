@@ -29,7 +29,8 @@ namespace {
 // Each block takes a window of 1024 rows and sorts them by adapter; where an adapter's rows go in all, it finds by
 // counting the whole index itself, so that no block waits for another.  The counts are sums of integers: their order
 // does not matter.  Rows without an adapter come last, as those of an adapter more.  777 rows 4.8 us, 8192 6.3 (cold),
-// by its barriers and trips to memory.
+// by its barriers and trips to memory.  Every block counts every row, so that many rows cost their square: 65536 24 us,
+// 262144 154 (of 1189 with the products of 4096x4096, rank 16), 2^20 2065 (of 6016).
 constexpr int kWindow = 1024, kFewBins = 96;
 
 struct OrderArgs {

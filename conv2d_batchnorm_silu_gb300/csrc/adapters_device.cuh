@@ -631,9 +631,10 @@ __global__ void __launch_bounds__(kAdapterThreads, RT <= 2 || (RT == 4 && sizeof
 // columns: it holds the strip's weights in registers and takes 32 rows of base at a time, the coming ones on their way
 // through its threads' own places in the ring, with no barrier.
 // bf16, 8192x4096x16384, rank 64: 156 us with the order (4.0 TB/s; 394 with the kernel above and 64 rows a tile, whose
-// weight loads each touched eight lines; rank 16: 114), bound by shared memory: the second product reads the small rows'
-// two parts again for each strip, 8 KB for 32x32 outputs of 15 KB in all.  With one part, to 2^-8 of the terms s b h, it
-// took 127, as long as the instructions of the epilogue do.
+// weight loads each touched eight lines; rank 16: 114, rank 128 245).  Some 340 instructions for 32x32 outputs, of which 64
+// are products, and 15 KB through shared memory, 8 of them the small rows' two parts again for each strip, on 16 warps an
+// SM: the tensor pipe is busy for 51 % of the time and L1 for 72, in turns rather than together.  (One part, which left y
+// off by up to 2^-8 of the terms s b h: 127.)
 constexpr int kManyStep = 64;
 
 // Own elements in the ring: eight on their boundary, or the aligned pieces that they lie in.
