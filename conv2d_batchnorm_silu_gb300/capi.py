@@ -639,7 +639,8 @@ def linear_adapters_backward(dy: torch.Tensor, x: torch.Tensor, index: torch.Ten
                              scale: torch.Tensor | None, hidden: torch.Tensor, base: torch.Tensor | None = None,
                              dx: torch.Tensor | None = None, stream=None):
     """conv_bn_silu_linear_adapters_backward: (dx, da, db) from dy, the forward call's arguments and the hidden rows it
-    returned.  base: the gradient that x has from elsewhere, added to dx (it may be dx); dx is like x; da and db are fp32
+    returned.  base: the gradient that x has from elsewhere, added to dx (it may be dx); dx is like x, and neither x nor dy,
+    which are read again after it is written; da and db are fp32
     like a and b, zeros for adapters without rows.  The gradient of the forward call's base is dy itself."""
     ops = _token_ops or _load_token_ops()
     out = ops.linear_adapters_backward(dy, x, index, a, b, scale, hidden, base, dx,
