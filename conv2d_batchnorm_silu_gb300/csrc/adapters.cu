@@ -238,7 +238,9 @@ constexpr int kFew = kAdapterThreads;
 
 // Rows whose tiles a CTA finds by counting all of them: an order by adapter first takes a launch more (777x1001x515 f32
 // 11.9 / 9.5 us), and a cluster for each row more clusters than there are tiles, which counts where there are four times
-// as many (4096x4096, rank 16, 256 rows of 4 adapters 9.6 / 8.1 us, of 64 adapters 10.5 / 12.3).
+// as many (4096x4096, rank 16, 256 rows of 4 adapters 9.6 / 8.1 us, of 64 adapters 10.5 / 12.3).  From 820 rows of rank 64
+// and 456 of 128 on neither is the faster throughout, and rows are ordered (ordered / counted: rank 128, 1000 rows of 4
+// adapters 33.8 / 31.5 us, of 64 97 / 106).
 bool counted(const AdapterProblem &p)
 {
     return p.m <= kCountedRows && p.adapters < kCountedBins && (long long)p.m * (adapter_rank_tiles(p.rank) + 1) < 4096 &&
@@ -262,8 +264,9 @@ Layout layout_of(const AdapterProblem &p, bool ordered, int k, int n, int sm_cou
     l.clusters = l.few && !l.counted ? p.m : l.tiles;
     // CTAs a tile, while each has some steps of 32 elements for its warps: of few rows, what takes the fewest rounds of
     // CTAs for its part of a tile (128 rows of 64 adapters, 4096x4096: 4 CTAs 9.8 us, 8 12.8; one row: 4 CTAs 7.3, 8 6.1);
-    // of many, what leaves the fullest SM, busy from so many CTAs on, the least (32768x64x4096, rank 16: 1 CTA 152 us, 4
-    // 114).  The fewest of those that do.
+    // of many, what leaves the fullest SM, busy from so many CTAs on, the least (1 / 2 / 4 / 8 CTAs: 8192x4096x16384 of rank 64
+    // 311 / 170 / 156 / 193 us, 8192x4096x4096 of rank 16 76 / 51 / 46 / 57; it misses by a tenth where little is left to
+    // share: 32768x64x4096 121 / 114 / 127 / 167).  The fewest of those that do.
     const int ranks = adapter_rank_tiles(p.rank);
     const long long resident = l.many ? (ranks <= 4 && p.dtype != kF32 ? 2 : 1) : ranks == 1 ? 3 : ranks == 2 || (ranks == 4 && p.dtype != kF32) ? 2 : 1;
     const long long about = full + (l.many ? 0 : p.adapters < p.m ? p.adapters : p.m);  // tiles
